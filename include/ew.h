@@ -24,7 +24,18 @@
  *   ew_gather_stride  out[i] = in[(stride * i) mod n]
  *                     CUDA-MODE lecture notes, §3.2 non-coalesced version (stride 2).
  *
- * Arithmetic (bit-exact, no tolerance):
+ * Row operators (rows of a matrix, one at a time: the memory-bound steps around a
+ * language model's matrix products; see "row operators" below):
+ *
+ *   ew_embed          out[t,:] = scale * table[tokens[t],:], and ew_embed_grad
+ *   ew_rmsnorm        root-mean-square norm with the residual's addition,
+ *                     ew_rmsnorm_quant (8-bit output with scales), ew_rmsnorm_grad
+ *   ew_logprob        log probabilities of given tokens, entropy and top
+ *                     alternatives, and ew_logprob_grad
+ *   ew_distill        distillation from a teacher's top logits: ew_distill,
+ *                     ew_distill_grad, and both in one call, ew_distill_step
+ *
+ * Arithmetic of the elementwise operators (bit-exact, no tolerance):
  *   f32 add      IEEE binary32 addition, round to nearest even; subnormals kept.
  *   f16/bf16 add the exact sum rounded once to the format, nearest even.  This
  *                equals "binary32 add, then one rounding" (binary32 carries more
@@ -230,6 +241,85 @@ EW_API ew_status ew_copy(ew_dtype dtype, const void *in, void *out, int64_t n, e
  * (same DRAM sectors, an eighth of the load instructions). */
 EW_API ew_status ew_gather_stride(ew_dtype dtype, const void *in, void *out, int64_t n,
                            int64_t stride, ew_stream_t stream);
+
+/* ---- row operators ---------------------------------------------------- */
+/*
+ * These work on matrices of `rows` rows of `cols` elements.  Element (i, j) of
+ * a matrix is at base[i * stride + j]; a stride counts elements and is at least
+ * cols.  Vectors (tokens, per-row results) are contiguous.  What holds for all
+ * calls above holds here too (pointers, streams, errors, threads), with these
+ * additions:
+ *
+ *   Types      dtype is EW_F32, EW_F16 or EW_BF16.  Sums, statistics and
+ *              per-row results are binary32; an output of a narrower type is
+ *              rounded to it once, nearest even.
+ *   Sizes      rows == 0 returns EW_OK and launches nothing (ew_embed_grad and
+ *              ew_rmsnorm_grad still write what they owe: a zero gradient).
+ *              rows, cols and table_rows are at most 2^31 - 2^16, cols at
+ *              least 1; offsets are formed in 64 bits.
+ *   Alignment  any pointer aligned to its element.  16-byte accesses are used
+ *              where bases and strides allow.
+ *   Aliasing   outputs overlap no input and no other output, but for the
+ *              in-place forms that a call names.  Matrices that interleave
+ *              with one common stride and share no element do not overlap.
+ *   Workspace  calls that need one take device memory of at least the size
+ *              that their _workspace function returns, aligned to 256 bytes;
+ *              its contents are undefined before and after.  A smaller size is
+ *              EW_ERR_INVALID_VALUE.
+ *   Launches   a call enqueues at most three kernels; none waits on the host.
+ *              Results do not depend on the order in which blocks run: the
+ *              same call gives the same bits each time.
+ */
+
+/* 8-bit output types of ew_rmsnorm_quant. */
+typedef enum {
+    EW_Q_E4M3 = 0, /* 4 exponent and 3 mantissa bits, largest value 448 */
+    EW_Q_I8 = 1    /* two's complement integers in [-127, 127] */
+} ew_qtype;
+
+/* Root-mean-square norm with the residual's addition:
+ *     h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
+ * residual may be NULL (h = x).  weight: cols elements of type wtype (dtype or
+ * EW_F32), or NULL for ones.  h_out (dtype) and rstd_out (binary32, rows) may
+ * be NULL where they are not wanted; the backward call needs both.   The norm is
+ * taken of the binary32 sum; only what is stored in h_out is rounded.  y may be
+ * x or residual, and h_out may be x or residual (the same base and stride),
+ * but y is not h_out.  eps >= 0.  NaN and infinity go through the formula: a
+ * NaN makes its whole row NaN; an infinity (rstd = 0) gives NaN at its place
+ * and 0 elsewhere. */
+EW_API ew_status ew_rmsnorm(ew_dtype dtype, const void *x, int64_t x_stride, const void *residual,
+                            int64_t residual_stride, ew_dtype wtype, const void *weight, float eps, void *y,
+                            int64_t y_stride, void *h_out, int64_t h_stride, float *rstd_out, int64_t rows,
+                            int64_t cols, ew_stream_t stream);
+
+/* The same norm with an 8-bit output q (rows x cols, one byte an element) and
+ * its binary32 scales, so that q * scale stands for y:
+ *     scale = max(largest |y| of the group, 2^-100) / (448 or 127)
+ *     q     = y * ((448 or 127) / that largest |y|), saturated, rounded to nearest even
+ * group: 32, 64, 128 or 256 columns, the last group of a row being shorter
+ * where it does not divide cols, or 0 for the whole row.  scales: rows x
+ * ceil(cols / group) (rows x 1), its own stride.  A NaN in a group makes its
+ * scale NaN. */
+EW_API ew_status ew_rmsnorm_quant(ew_dtype dtype, const void *x, int64_t x_stride, const void *residual,
+                                  int64_t residual_stride, ew_dtype wtype, const void *weight, float eps,
+                                  ew_qtype qtype, int64_t group, void *q, int64_t q_stride, float *scales,
+                                  int64_t scales_stride, void *h_out, int64_t h_stride, float *rstd_out,
+                                  int64_t rows, int64_t cols, ew_stream_t stream);
+
+/* Backward of ew_rmsnorm, from the h and rstd that it wrote:
+ *     n = h * rstd,  g = dy * weight
+ *     dx = rstd * (g - n * mean(g * n)) + dh      (also the residual's gradient)
+ *     dweight = sum over rows of dy * n           (binary32)
+ * dh, the gradient that reaches h by the residual stream, may be NULL.  weight
+ * may be NULL (ones).  dweight may be NULL.  dx may be dy or dh (the same base
+ * and stride).  rows == 0 writes a zero dweight. */
+EW_API ew_status ew_rmsnorm_grad(ew_dtype dtype, const void *dy, int64_t dy_stride, const void *h,
+                                 int64_t h_stride, ew_dtype wtype, const void *weight, const float *rstd,
+                                 const void *dh, int64_t dh_stride, void *dx, int64_t dx_stride, float *dweight,
+                                 int64_t rows, int64_t cols, void *workspace, int64_t workspace_bytes,
+                                 ew_stream_t stream);
+/* Bytes of workspace (-1: sizes out of range); 0 columns of dweight need none. */
+EW_API int64_t ew_rmsnorm_grad_workspace(int64_t rows, int64_t cols);
 
 /* ---- variant selection and introspection ------------------------------ */
 

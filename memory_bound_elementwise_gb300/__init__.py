@@ -15,6 +15,12 @@ Tensor entry points (same names as the C ABI)::
     ew_copy(x, out)                 out = x
     ew_gather_stride(x, out, s)     out[i] = x[(s*i) mod n]
 
+Row operators (matrices, one row at a time; ``rows.py``)::
+
+    ew_rmsnorm(x, w, residual)      (y, h, rstd): h = x + residual, y = h / rms(h) * w
+    ew_rmsnorm_quant(...)           (q, scales, h, rstd): the same with an 8-bit output
+    ew_rmsnorm_grad(dy, h, w, rstd) (dx, dweight)
+
 Tensors must be contiguous CUDA tensors of dtype float32, float16 or bfloat16
 (int32 for ew_select_even_odd, ew_copy and ew_gather_stride) on the current
 device; calls are enqueued on ``stream`` (default: torch's
@@ -49,7 +55,18 @@ EXPORTS = ("ew_add", "ew_saxpy", "ew_relu", "ew_add_relu", "ew_saxpy_relu", "ew_
            "ew_get_programmatic_launch",
            "ew_get_path", "ew_set_schedule", "ew_get_schedule", "ew_set_pointer_check",
            "ew_plan_query", "ew_last_launch", "ew_gather_plan_query", "ew_status_string", "ew_last_cuda_error",
-           "ew_device_error", "ew_selftest_bounded_wait", "ew_version")
+           "ew_device_error", "ew_selftest_bounded_wait", "ew_version",
+           "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad", "ew_rmsnorm_grad_workspace")
+
+# Row operators (rows.py), loaded with torch at their first use.
+_ROW_OPERATORS = ("ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad")
+# Their C arguments: i enum, l int64, f float, p pointer.
+_ROW_SIGNATURES = {
+    "ew_rmsnorm": "iplplipfplplpllp",
+    "ew_rmsnorm_quant": "iplplipfilplplplpllp",
+    "ew_rmsnorm_grad": "iplplippplplpllplp",
+    "ew_rmsnorm_grad_workspace": "ll",
+}
 
 
 class EwError(RuntimeError):
@@ -125,8 +142,27 @@ def lib():
     L.ew_device_error.argtypes = [vp, ctypes.POINTER(i32)]
     L.ew_version.argtypes = []
     L.ew_version.restype = ctypes.c_int
+    _declare_rows(L)
     _lib = L
     return _lib
+
+
+def _declare_rows(L):
+    i32, i64, f32, vp = ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+    letters = {"i": i32, "l": i64, "f": f32, "p": vp}
+    for name, args in _ROW_SIGNATURES.items():
+        fn = getattr(L, name)
+        fn.argtypes = [letters[c] for c in args]
+        fn.restype = i64 if name.endswith("_workspace") else i32
+
+
+def __getattr__(name):
+    if name in _ROW_OPERATORS:
+        from . import rows
+        for op in _ROW_OPERATORS:
+            globals()[op] = getattr(rows, op)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
 
 
 def status_string(status):
@@ -323,4 +359,4 @@ __all__ = ["ew_add", "ew_saxpy", "ew_relu", "ew_add_relu", "ew_saxpy_relu", "ew_
            "ew_gather_stride", "set_path",
            "get_path", "set_schedule", "get_schedule", "set_programmatic_launch",
            "get_programmatic_launch", "set_pointer_check", "plan_query",
-           "last_launch", "device_error", "selftest_bounded_wait", "lib", "EwError", "EXPORTS"]
+           "last_launch", "device_error", "selftest_bounded_wait", "lib", "EwError", "EXPORTS", *_ROW_OPERATORS]

@@ -26,6 +26,7 @@
 
 #include "ew.h"
 #include "ew_internal.h"
+#include "ew_rows.h"
 
 using namespace ew;
 
@@ -737,6 +738,23 @@ ew_launch_record record_of(const GatherLaunch &gl) {
 
 bool ew::programmatic_launch() { return g_programmatic.load(std::memory_order_relaxed) != 0; }
 
+// What the row operators (ew_rows_api.cu) share with the calls below.
+ew_status ew::report_cuda(cudaError_t e) { return cuda_fail(e); }
+ew_launch_record &ew::launch_record() { return t_last; }
+ew_status ew::check_pointers(const void *const *p, int np) {
+    if (!pointer_check_enabled()) return EW_OK;
+    for (int k = 0; k < np; ++k) {
+        if (p[k] == nullptr) continue;
+        const ew_status st = check_device_pointers(p + k, 1);
+        if (st != EW_OK) return st;
+    }
+    return EW_OK;
+}
+cudaError_t ew::current_sms(int *sms) {
+    int dev = 0;
+    return device_info(&dev, sms);
+}
+
 // ---------------------------------------------------------------- C ABI
 
 extern "C" {
@@ -950,6 +968,6 @@ ew_status ew_selftest_bounded_wait(int64_t limit_ns, ew_stream_t s) {
     return EW_OK;
 }
 
-int ew_version(void) { return 600; }
+int ew_version(void) { return 700; }
 
 }  // extern "C"

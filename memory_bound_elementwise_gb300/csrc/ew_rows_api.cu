@@ -1,0 +1,198 @@
+// ew_rows_api.cu -- the row operators' part of the C ABI declared in
+// include/ew.h: argument validation and dispatch.  As for the elementwise
+// calls, every argument error is found on the host before any CUDA call.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "ew_rows.h"
+
+using namespace ew;
+
+namespace {
+
+constexpr int64_t kMaxSize = (int64_t(1) << 31) - (int64_t(1) << 16);  // rows, columns, table rows
+
+bool float_type(int dt) { return dt == EW_F32 || dt == EW_F16 || dt == EW_BF16; }
+int bytes_of(ew_dtype dt) { return dt == EW_F32 ? 4 : 2; }
+bool size_ok(int64_t v, int64_t least) { return v >= least && v <= kMaxSize; }
+
+// A matrix operand: rows x cols elements of `e` bytes, `stride` elements apart.
+struct Operand {
+    const void *p;
+    int64_t rows, cols, stride;
+    int e;
+    bool wanted = true;  // an optional operand may be null
+};
+Operand vec(const void *p, int64_t n, int e, bool wanted = true) { return {p, 1, n, n, e, wanted}; }
+
+ew_status check_operand(const Operand &m) {
+    if (m.p == nullptr) return m.wanted && m.rows > 0 && m.cols > 0 ? EW_ERR_NULL_POINTER : EW_OK;
+    if (reinterpret_cast<uintptr_t>(m.p) % m.e != 0) return EW_ERR_INVALID_VALUE;
+    if (m.stride < m.cols || m.stride > INT64_MAX / 8 / std::max<int64_t>(m.rows, 1)) return EW_ERR_INVALID_VALUE;
+    return EW_OK;
+}
+
+// Whether two matrices share a byte.  Matrices with one stride may interleave:
+// then their rows are compared modulo the stride.
+bool share_bytes(const Operand &a, const Operand &b) {
+    if (a.p == nullptr || b.p == nullptr || a.rows == 0 || b.rows == 0) return false;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    const uint64_t ra = static_cast<uint64_t>(a.cols) * a.e, rb = static_cast<uint64_t>(b.cols) * b.e;
+    const uint64_t sa = static_cast<uint64_t>(a.stride) * a.e, sb = static_cast<uint64_t>(b.stride) * b.e;
+    const uint64_t la = (a.rows - 1) * sa + ra, lb = (b.rows - 1) * sb + rb;
+    if (pa >= pb + lb || pb >= pa + la) return false;
+    if (sa != sb || (a.rows == 1 && b.rows == 1)) return true;
+    const uint64_t d = pa <= pb ? (pb - pa) % sa : sa - (pa - pb) % sa;  // b's rows start d bytes into a's
+    return d % sa == 0 || d < ra || d + rb > sa;
+}
+bool same_place(const Operand &a, const Operand &b) {
+    return a.p == b.p && a.e == b.e && a.cols == b.cols && (a.rows <= 1 || a.stride == b.stride);
+}
+
+// Overlap rules: an output shares bytes with no other operand, but that output
+// `in_place[k]` may be input k itself.
+ew_status check_overlap(const Operand *in, int ni, const Operand *out, int no, const bool (*in_place)[2] = nullptr) {
+    for (int o = 0; o < no; ++o) {
+        for (int i = 0; i < ni; ++i) {
+            const bool allowed = in_place != nullptr && i < 2 && in_place[o][i] && same_place(in[i], out[o]);
+            if (!allowed && share_bytes(in[i], out[o])) return EW_ERR_OVERLAP;
+        }
+        for (int q = o + 1; q < no; ++q)
+            if (share_bytes(out[o], out[q])) return EW_ERR_OVERLAP;
+    }
+    return EW_OK;
+}
+
+ew_status check_all(const Operand *in, int ni, const Operand *out, int no, const bool (*in_place)[2] = nullptr) {
+    const void *p[16];
+    int np = 0;
+    for (int i = 0; i < ni; ++i) {
+        const ew_status st = check_operand(in[i]);
+        if (st != EW_OK) return st;
+        p[np++] = in[i].rows > 0 ? in[i].p : nullptr;
+    }
+    for (int o = 0; o < no; ++o) {
+        const ew_status st = check_operand(out[o]);
+        if (st != EW_OK) return st;
+        p[np++] = out[o].rows > 0 ? out[o].p : nullptr;
+    }
+    const ew_status st = check_overlap(in, ni, out, no, in_place);
+    return st != EW_OK ? st : check_pointers(p, np);
+}
+
+void record(const LaunchInfo &info, int launches) {
+    ew_launch_record &r = launch_record();
+    r.launches = launches;
+    r.path = info.vec_bytes >= 32 ? EW_PATH_V256 : info.vec_bytes == 16 ? EW_PATH_V128 : EW_PATH_SCALAR;
+    r.vec_bytes = info.vec_bytes;
+    r.grid = info.grid;
+    r.block = info.block;
+    r.smem = info.smem;
+    r.schedule = EW_SCHED_ONESHOT;
+}
+
+ew_status norm_call(ew_dtype dt, const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                    ew_dtype wtype, const void *weight, float eps, bool quant, ew_qtype qtype, int64_t group,
+                    void *out, int64_t out_stride, float *scales, int64_t scales_stride, void *h_out,
+                    int64_t h_stride, float *rstd_out, int64_t rows, int64_t cols, cudaStream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || (weight != nullptr && wtype != dt && wtype != EW_F32)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!size_ok(rows, 0) || !size_ok(cols, 1) || !(eps >= 0.0f) || std::isinf(eps)) return EW_ERR_INVALID_VALUE;
+    if (quant) {
+        if (qtype != EW_Q_E4M3 && qtype != EW_Q_I8) return EW_ERR_UNSUPPORTED_DTYPE;
+        if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256) return EW_ERR_INVALID_VALUE;
+    }
+    if (rows == 0) return EW_OK;
+    const int e = bytes_of(dt);
+    const int64_t groups = !quant ? 0 : group == 0 ? 1 : (cols + group - 1) / group;
+    const Operand in[3] = {{x, rows, cols, x_stride, e},
+                           {residual, rows, cols, residual_stride, e, false},
+                           vec(weight, cols, wtype == EW_F32 ? 4 : e, false)};
+    const Operand outs[4] = {{out, rows, cols, out_stride, quant ? 1 : e},
+                             {h_out, rows, cols, h_stride, e, false},
+                             vec(rstd_out, rows, 4, false),
+                             {scales, rows, groups, scales_stride, 4, quant}};
+    const bool in_place[4][2] = {{!quant, !quant}, {true, true}, {false, false}, {false, false}};
+    const ew_status st = check_all(in, 3, outs, quant ? 4 : 3, in_place);
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    const NormArgs a{x, residual, weight, out, h_out, rstd_out, scales, x_stride, residual_stride, out_stride,
+                     h_stride, scales_stride, rows, static_cast<int32_t>(cols), static_cast<int32_t>(group), eps,
+                     weight != nullptr && wtype == EW_F32, quant && qtype == EW_Q_I8};
+    LaunchInfo info;
+    ce = (dt == EW_F32 ? norm_f32 : dt == EW_F16 ? norm_f16 : norm_bf16)(quant, a, sms, s, &info);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, 1);
+    return EW_OK;
+}
+
+// Rows of partial sums that the norm's backward may use: one for each row up to
+// 1280, which is more than its blocks.
+constexpr int64_t kNormPartials = 1280;
+
+}  // namespace
+
+extern "C" {
+
+ew_status ew_rmsnorm(ew_dtype dt, const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                     ew_dtype wtype, const void *weight, float eps, void *y, int64_t y_stride, void *h_out,
+                     int64_t h_stride, float *rstd_out, int64_t rows, int64_t cols, ew_stream_t s) {
+    return norm_call(dt, x, x_stride, residual, residual_stride, wtype, weight, eps, false, EW_Q_E4M3, 0, y, y_stride,
+                     nullptr, 0, h_out, h_stride, rstd_out, rows, cols, reinterpret_cast<cudaStream_t>(s));
+}
+
+ew_status ew_rmsnorm_quant(ew_dtype dt, const void *x, int64_t x_stride, const void *residual,
+                           int64_t residual_stride, ew_dtype wtype, const void *weight, float eps, ew_qtype qtype,
+                           int64_t group, void *q, int64_t q_stride, float *scales, int64_t scales_stride,
+                           void *h_out, int64_t h_stride, float *rstd_out, int64_t rows, int64_t cols,
+                           ew_stream_t s) {
+    return norm_call(dt, x, x_stride, residual, residual_stride, wtype, weight, eps, true, qtype, group, q, q_stride,
+                     scales, scales_stride, h_out, h_stride, rstd_out, rows, cols, reinterpret_cast<cudaStream_t>(s));
+}
+
+int64_t ew_rmsnorm_grad_workspace(int64_t rows, int64_t cols) {
+    if (!size_ok(rows, 0) || !size_ok(cols, 1)) return -1;
+    return std::min(rows, kNormPartials) * cols * 4;
+}
+
+ew_status ew_rmsnorm_grad(ew_dtype dt, const void *dy, int64_t dy_stride, const void *h, int64_t h_stride,
+                          ew_dtype wtype, const void *weight, const float *rstd, const void *dh, int64_t dh_stride,
+                          void *dx, int64_t dx_stride, float *dweight, int64_t rows, int64_t cols, void *workspace,
+                          int64_t workspace_bytes, ew_stream_t stream) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || (weight != nullptr && wtype != dt && wtype != EW_F32)) return EW_ERR_UNSUPPORTED_DTYPE;
+    const int64_t need = ew_rmsnorm_grad_workspace(rows, cols);
+    if (need < 0 || (dweight != nullptr && workspace_bytes < need)) return EW_ERR_INVALID_VALUE;
+    if (rows == 0 && dweight == nullptr) return EW_OK;
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return EW_ERR_INVALID_VALUE;
+    const int e = bytes_of(dt);
+    const Operand in[5] = {{dy, rows, cols, dy_stride, e},
+                           {dh, rows, cols, dh_stride, e, false},
+                           {h, rows, cols, h_stride, e},
+                           vec(weight, cols, wtype == EW_F32 ? 4 : e, false),
+                           vec(rstd, rows, 4)};
+    const Operand out[3] = {{dx, rows, cols, dx_stride, e},
+                            vec(dweight, cols, 4, false),
+                            vec(workspace, need / 4, 4, dweight != nullptr && need > 0)};
+    const bool in_place[3][2] = {{true, true}, {false, false}, {false, false}};
+    const ew_status st = check_all(in, 5, out, dweight != nullptr ? 3 : 2, in_place);
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    const NormGradArgs a{dy, h, weight, dh, rstd, dx, dweight, static_cast<float *>(workspace), dy_stride, h_stride,
+                         dh_stride, dx_stride, rows, static_cast<int32_t>(cols),
+                         weight != nullptr && wtype == EW_F32};
+    LaunchInfo info;
+    int launches = 0;
+    ce = (dt == EW_F32 ? norm_grad_f32 : dt == EW_F16 ? norm_grad_f16 : norm_grad_bf16)(
+        a, std::min(rows, kNormPartials), sms, reinterpret_cast<cudaStream_t>(stream), &info, &launches);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, launches);
+    return EW_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,211 @@
+"""Row operators: torch entry points over the C ABI (include/ew.h, "row operators").
+
+Matrices are CUDA tensors whose last dimension is contiguous.  Two-dimensional
+ones may have any row stride; others are contiguous and count as rows of their
+last dimension.  Outputs that are not given are allocated; calls are enqueued
+on ``stream`` (default: torch's current stream) and do not synchronise.  What is
+allocated belongs to that stream.  Arguments that do not fit raise ``ValueError``
+or ``TypeError`` here, or ``EwError`` with the library's status.
+"""
+import contextlib
+
+import torch
+
+_F32, _F16, _BF16 = 0, 1, 2
+_CODES = {torch.float32: _F32, torch.float16: _F16, torch.bfloat16: _BF16}
+_QTYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
+_fns = {}
+
+
+def _call(name, *args):
+    fn = _fns.get(name)
+    if fn is None:
+        from . import lib
+        fn = _fns[name] = getattr(lib(), name)
+    status = fn(*args)
+    if status != 0:
+        from . import check
+        check(status, name)
+
+
+def _bytes(name, *args):
+    """A workspace function's answer."""
+    fn = _fns.get(name)
+    if fn is None:
+        from . import lib
+        fn = _fns[name] = getattr(lib(), name)
+    n = fn(*args)
+    if n < 0:
+        raise ValueError("%s: sizes out of range" % name)
+    return n
+
+
+def _code(t, what):
+    c = _CODES.get(t.dtype)
+    if c is None:
+        raise TypeError("%s: unsupported dtype %s (float32, float16, bfloat16)" % (what, t.dtype))
+    return c
+
+
+def _matrix(t, what, device):
+    """(rows, cols, stride) of a tensor as a matrix of its last dimension."""
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (what, device))
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        stride, inner = t.stride()
+        if rows <= 1 and stride < cols:
+            stride = cols  # the stride of a single row says nothing
+        if (inner == 1 or cols == 1) and (stride >= cols or rows <= 1):
+            return rows, cols, stride
+    elif len(shape) >= 1 and t.is_contiguous():
+        cols = shape[-1]
+        return (t.numel() // cols if cols else 0), cols, cols
+    raise ValueError("%s: a matrix needs a contiguous last dimension and rows that do not overlap" % what)
+
+
+def _like(t, what, rows, cols, dtype, device):
+    """The row stride of a tensor that has to be rows x cols of dtype."""
+    r, c, stride = _matrix(t, what, device)
+    if r != rows or c != cols or t.dtype != dtype:
+        raise ValueError("%s: expected %d x %d of %s, got %s of %s" % (what, rows, cols, dtype, tuple(t.shape), t.dtype))
+    return stride
+
+
+def _vector(t, what, n, dtype, device):
+    if t.device != device or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: expected %d contiguous elements of %s on %s" % (what, n, dtype, device))
+    return t.data_ptr()
+
+
+def _cuda_device(t, what):
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % what)
+    device = t.device
+    if device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on the current device" % what)
+    return device
+
+
+def _raw_stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+_here = contextlib.nullcontext()
+
+
+def _allocating(stream):
+    """Allocations inside belong to the stream that the call runs on."""
+    return _here if stream is None else torch.cuda.stream(stream)
+
+
+def _weight(weight, cols, dtype, code, device):
+    """(type code, pointer) of a norm's weight."""
+    if weight is None:
+        return code, None
+    if weight.dtype != dtype and weight.dtype != torch.float32:
+        raise TypeError("weight: %s or float32, got %s" % (dtype, weight.dtype))
+    return _CODES[weight.dtype], _vector(weight, "weight", cols, weight.dtype, device)
+
+
+def _norm_inputs(x, weight, residual, h, rstd):
+    """What both norm calls take: checked and with the outputs h and rstd allocated."""
+    device = _cuda_device(x, "x")
+    code = _code(x, "x")
+    dtype = x.dtype
+    rows, cols, x_stride = _matrix(x, "x", device)
+    wcode, wptr = _weight(weight, cols, dtype, code, device)
+    r_ptr, r_stride, h_ptr, h_stride = None, 0, None, 0
+    if residual is not None:
+        r_ptr, r_stride = residual.data_ptr(), _like(residual, "residual", rows, cols, dtype, device)
+        if h is None:
+            h = torch.empty(x.shape, dtype=dtype, device=device)
+            h_ptr, h_stride = h.data_ptr(), cols
+    if h is None:
+        h = x  # without a residual h is x: nothing to write
+    elif h_ptr is None:
+        h_ptr, h_stride = h.data_ptr(), _like(h, "h", rows, cols, dtype, device)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+        rstd_ptr = rstd.data_ptr()
+    else:
+        rstd_ptr = _vector(rstd, "rstd", rows, torch.float32, device)
+    head = (code, x.data_ptr(), x_stride, r_ptr, r_stride, wcode, wptr)
+    return device, dtype, rows, cols, h, rstd, head, (h_ptr, h_stride, rstd_ptr, rows, cols)
+
+
+def ew_rmsnorm(x, weight, residual=None, eps=1e-6, y=None, h=None, rstd=None, stream=None):
+    """y = h / sqrt(mean(h^2) + eps) * weight with h = x + residual; returns (y, h, rstd).
+
+    ``weight`` has x's dtype or float32 (None: ones).  Without a residual h is
+    x.  ``rstd`` (float32, one a row) and ``h`` are what ew_rmsnorm_grad takes.
+    y may be x or residual, h may be x or residual, for in place."""
+    with _allocating(stream):
+        device, dtype, rows, cols, h, rstd, head, tail = _norm_inputs(x, weight, residual, h, rstd)
+        if y is None:
+            y = torch.empty(x.shape, dtype=dtype, device=device)
+            y_stride = cols
+        else:
+            y_stride = _like(y, "y", rows, cols, dtype, device)
+    _call("ew_rmsnorm", *head, eps, y.data_ptr(), y_stride, *tail, _raw_stream(stream, device))
+    return y, h, rstd
+
+
+def ew_rmsnorm_quant(x, weight, residual=None, eps=1e-6, group=0, q=None, scales=None, h=None, rstd=None,
+                     dtype=torch.float8_e4m3fn, stream=None):
+    """The norm with an 8-bit output: returns (q, scales, h, rstd), q * scale standing for y.
+
+    ``dtype`` is torch.float8_e4m3fn or torch.int8; ``group`` is 32, 64, 128 or
+    256 columns a scale, or 0 for one scale a row; scales: float32, rows x groups."""
+    if q is not None:
+        dtype = q.dtype
+    if dtype not in _QTYPES:
+        raise TypeError("dtype: float8_e4m3fn or int8, got %s" % dtype)
+    with _allocating(stream):
+        device, _, rows, cols, h, rstd, head, tail = _norm_inputs(x, weight, residual, h, rstd)
+        groups = -(-cols // group) if group > 0 else 1
+        if q is None:
+            q = torch.empty(x.shape, dtype=dtype, device=device)
+            q_stride = cols
+        else:
+            q_stride = _like(q, "q", rows, cols, dtype, device)
+        if scales is None:
+            scales = torch.empty((rows, groups), dtype=torch.float32, device=device)
+            s_stride = groups
+        else:
+            s_stride = _like(scales, "scales", rows, groups, torch.float32, device)
+    _call("ew_rmsnorm_quant", *head, eps, _QTYPES[dtype], group, q.data_ptr(), q_stride, scales.data_ptr(), s_stride,
+          *tail, _raw_stream(stream, device))
+    return q, scales, h, rstd
+
+
+def ew_rmsnorm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, stream=None):
+    """Gradients of ew_rmsnorm: returns (dx, dweight), dx for x and for the residual alike.
+
+    ``h`` and ``rstd`` come from the forward call; ``dh`` is the gradient that
+    reaches h by the residual stream.  dweight is float32.  dx may be dy or dh."""
+    device = _cuda_device(dy, "dy")
+    code, dtype = _code(dy, "dy"), dy.dtype
+    rows, cols, dy_stride = _matrix(dy, "dy", device)
+    h_stride = _like(h, "h", rows, cols, dtype, device)
+    wcode, wptr = _weight(weight, cols, dtype, code, device)
+    r_ptr = _vector(rstd, "rstd", rows, torch.float32, device)
+    dh_ptr, dh_stride = (None, 0) if dh is None else (dh.data_ptr(), _like(dh, "dh", rows, cols, dtype, device))
+    with _allocating(stream):
+        if dx is None:
+            dx = torch.empty(dy.shape, dtype=dtype, device=device)
+            dx_stride = cols
+        else:
+            dx_stride = _like(dx, "dx", rows, cols, dtype, device)
+        if dweight is None:
+            dweight = torch.empty(cols, dtype=torch.float32, device=device)
+            dw_ptr = dweight.data_ptr()
+        else:
+            dw_ptr = _vector(dweight, "dweight", cols, torch.float32, device)
+        need = _bytes("ew_rmsnorm_grad_workspace", rows, cols)
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+    _call("ew_rmsnorm_grad", code, dy.data_ptr(), dy_stride, h.data_ptr(), h_stride, wcode, wptr, r_ptr, dh_ptr,
+          dh_stride, dx.data_ptr(), dx_stride, dw_ptr, rows, cols, work.data_ptr(), need, _raw_stream(stream, device))
+    return dx, dweight

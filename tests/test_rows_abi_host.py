@@ -1,0 +1,79 @@
+"""The row operators' C ABI on the host: refusals, sizes and overlap rules.
+
+Every call here is rejected, or has nothing to do, before any CUDA call."""
+import os
+
+import pytest
+
+import memory_bound_elementwise_gb300 as ew
+
+pytestmark = pytest.mark.skipif(not os.path.exists(ew.LIB_PATH), reason="libew.so not built")
+
+OK, INVALID, NULLP, DTYPE, OVERLAP = 0, 1, 2, 3, 4
+P = 0x10000000  # fake addresses, never dereferenced
+MB = 1 << 20
+BIG = (1 << 31) - (1 << 16)
+
+
+def norm(dt=2, x=P, xs=64, r=None, rs=0, wt=2, w=None, eps=1e-6, y=P + MB, ys=64, h=None, hs=0, rstd=None, rows=4,
+         cols=64):
+    return ew.lib().ew_rmsnorm(dt, x, xs, r, rs, wt, w, eps, y, ys, h, hs, rstd, rows, cols, None)
+
+
+def quant(dt=2, x=P, xs=64, qt=0, group=32, q=P + MB, qs=64, s=P + 2 * MB, ss=2, rows=4, cols=64, eps=1e-6):
+    return ew.lib().ew_rmsnorm_quant(dt, x, xs, None, 0, 2, None, eps, qt, group, q, qs, s, ss, None, 0, None, rows, cols,
+                                     None)
+
+
+def norm_grad(dt=2, dy=P, h=P + MB, rstd=P + 2 * MB, dh=None, dx=P + 3 * MB, dw=P + 4 * MB, rows=4, cols=64,
+              work=P + 5 * MB, size=MB, s=64):
+    return ew.lib().ew_rmsnorm_grad(dt, dy, s, h, s, 2, None, rstd, dh, s, dx, s, dw, rows, cols, work, size, None)
+
+
+def test_norm_refusals():
+    assert norm(dt=3) == DTYPE and norm(dt=-1) == DTYPE and norm(w=P + 2 * MB, wt=1) == DTYPE
+    assert norm(rows=0, x=None, y=None) == OK and ew.last_launch()["launches"] == 0
+    assert norm(rows=-1) == INVALID and norm(cols=0) == INVALID and norm(rows=BIG + 1) == INVALID
+    assert norm(cols=BIG + 1, xs=BIG + 1, ys=BIG + 1) == INVALID
+    assert norm(x=None) == NULLP and norm(y=None) == NULLP
+    assert norm(x=P + 1) == INVALID and norm(y=P + MB + 1) == INVALID and norm(rstd=P + 2 * MB + 2) == INVALID
+    assert norm(xs=63) == INVALID and norm(ys=10) == INVALID and norm(r=P + 2 * MB, rs=1) == INVALID
+    assert norm(xs=1 << 62) == INVALID
+    assert norm(eps=-1e-9) == INVALID and norm(eps=float("nan")) == INVALID and norm(eps=float("inf")) == INVALID
+
+
+def test_norm_overlap():
+    row = 64 * 2
+    assert norm(y=P + row) == OVERLAP                      # the next row of x
+    assert norm(y=P + 2) == OVERLAP
+    assert norm(y=P, ys=128) == OVERLAP                    # the same base at another stride
+    assert norm(h=P + MB, hs=64) == OVERLAP                # y and h the same
+    assert norm(w=P + MB + 8) == OVERLAP
+    assert norm(rstd=P + MB) == OVERLAP
+    # two matrices side by side in rows of 128 elements share nothing; shifted by one element they do
+    assert norm(xs=128, y=P + row - 2, ys=128) == OVERLAP
+    assert norm(xs=128, y=P + row + 2, ys=128) == OVERLAP  # y's row ends in x's next row
+    assert norm(xs=128, x=P + row, y=P + 2, ys=128) == OVERLAP
+
+
+def test_quant_refusals():
+    assert quant(dt=3) == DTYPE and quant(qt=2) == DTYPE
+    assert quant(group=31) == INVALID and quant(group=-32) == INVALID and quant(group=512) == INVALID
+    assert quant(s=None) == NULLP and quant(q=None) == NULLP
+    assert quant(ss=1) == INVALID and quant(s=P + 2 * MB + 1) == INVALID and quant(qs=63) == INVALID
+    assert quant(q=P) == OVERLAP and quant(s=P + MB) == OVERLAP  # no in-place form, scales inside q
+    assert quant(rows=0) == OK
+
+
+def test_norm_grad_refusals():
+    assert norm_grad(dt=3) == DTYPE
+    assert norm_grad(rows=-1) == INVALID and norm_grad(cols=0) == INVALID
+    assert norm_grad(dy=None) == NULLP and norm_grad(h=None) == NULLP and norm_grad(rstd=None) == NULLP
+    assert norm_grad(dx=None) == NULLP and norm_grad(work=None) == NULLP
+    need = ew.lib().ew_rmsnorm_grad_workspace(4, 64)
+    assert need == 4 * 64 * 4 and norm_grad(size=need - 1) == INVALID
+    assert norm_grad(work=P + 5 * MB + 128) == INVALID
+    assert norm_grad(dx=P + MB) == OVERLAP and norm_grad(dx=P + 2) == OVERLAP and norm_grad(work=P) == OVERLAP
+    assert norm_grad(rows=0, dw=None) == OK
+    assert ew.lib().ew_rmsnorm_grad_workspace(-1, 64) == -1 and ew.lib().ew_rmsnorm_grad_workspace(4, BIG + 1) == -1
+    assert ew.last_launch()["launches"] == 0
