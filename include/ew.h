@@ -271,11 +271,36 @@ EW_API ew_status ew_gather_stride(ew_dtype dtype, const void *in, void *out, int
  *              same call gives the same bits each time.
  */
 
+/* Width of token ids. */
+typedef enum { EW_INDEX_I32 = 0, EW_INDEX_I64 = 1 } ew_index;
+
 /* 8-bit output types of ew_rmsnorm_quant. */
 typedef enum {
     EW_Q_E4M3 = 0, /* 4 exponent and 3 mantissa bits, largest value 448 */
     EW_Q_I8 = 1    /* two's complement integers in [-127, 127] */
 } ew_qtype;
+
+/* out[t,:] = scale * table[tokens[t],:] for t in [0, rows), the product rounded
+ * once.  table: table_rows x cols.  A token outside [0, table_rows) gives a row
+ * of zeros.  out may not overlap the table. */
+EW_API ew_status ew_embed(ew_dtype dtype, ew_index itype, const void *table, int64_t table_rows,
+                          int64_t table_stride, const void *tokens, float scale, void *out, int64_t out_stride,
+                          int64_t rows, int64_t cols, ew_stream_t stream);
+
+/* Gradient of ew_embed with respect to the table:
+ *     dtable[v,:] = scale * sum over t with tokens[t] == v of dout[t,:]
+ * Tokens outside [0, table_rows) add nothing.  dtable: table_rows x cols of
+ * type gtype, which is dtype or EW_F32.  accumulate 0: the whole table is
+ * written, zeros where no token points.  accumulate 1: the sums are added to
+ * what dtable holds, and rows that no token names are not touched.  The tokens
+ * are sorted on the device (stable) and each row's terms are added in
+ * binary32 in an order that depends on the tokens alone. */
+EW_API ew_status ew_embed_grad(ew_dtype dtype, ew_index itype, const void *dout, int64_t dout_stride,
+                               const void *tokens, float scale, ew_dtype gtype, void *dtable, int64_t table_rows,
+                               int64_t table_stride, int64_t rows, int64_t cols, int accumulate, void *workspace,
+                               int64_t workspace_bytes, ew_stream_t stream);
+/* Bytes of workspace (-1: sizes out of range). */
+EW_API int64_t ew_embed_grad_workspace(int64_t table_rows, int64_t rows, int64_t cols);
 
 /* Root-mean-square norm with the residual's addition:
  *     h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight

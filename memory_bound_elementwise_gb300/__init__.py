@@ -17,6 +17,8 @@ Tensor entry points (same names as the C ABI)::
 
 Row operators (matrices, one row at a time; ``rows.py``)::
 
+    ew_embed(table, tokens)         out[t] = scale * table[tokens[t]]
+    ew_embed_grad(dout, tokens, n)  the n x cols table's gradient, by sorted tokens
     ew_rmsnorm(x, w, residual)      (y, h, rstd): h = x + residual, y = h / rms(h) * w
     ew_rmsnorm_quant(...)           (q, scales, h, rstd): the same with an 8-bit output
     ew_rmsnorm_grad(dy, h, w, rstd) (dx, dweight)
@@ -56,12 +58,15 @@ EXPORTS = ("ew_add", "ew_saxpy", "ew_relu", "ew_add_relu", "ew_saxpy_relu", "ew_
            "ew_get_path", "ew_set_schedule", "ew_get_schedule", "ew_set_pointer_check",
            "ew_plan_query", "ew_last_launch", "ew_gather_plan_query", "ew_status_string", "ew_last_cuda_error",
            "ew_device_error", "ew_selftest_bounded_wait", "ew_version",
-           "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad", "ew_rmsnorm_grad_workspace")
+           "ew_embed", "ew_embed_grad", "ew_embed_grad_workspace", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad", "ew_rmsnorm_grad_workspace")
 
 # Row operators (rows.py), loaded with torch at their first use.
-_ROW_OPERATORS = ("ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad")
+_ROW_OPERATORS = ("ew_embed", "ew_embed_grad", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad")
 # Their C arguments: i enum, l int64, f float, p pointer.
 _ROW_SIGNATURES = {
+    "ew_embed": "iipllpfplllp",
+    "ew_embed_grad": "iiplpfiplllliplp",
+    "ew_embed_grad_workspace": "lll",
     "ew_rmsnorm": "iplplipfplplpllp",
     "ew_rmsnorm_quant": "iplplipfilplplplpllp",
     "ew_rmsnorm_grad": "iplplippplplpllplp",

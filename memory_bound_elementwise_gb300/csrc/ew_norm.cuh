@@ -387,11 +387,6 @@ inline int tiles_per_thread(int tiles, int warps, int most) {
     return 0;
 }
 
-// 16-byte accesses (32-byte ones for binary32): the base and the stride of a
-// matrix are multiples of 8 elements.  Null matrices allow anything.
-template <int DT> bool wide_rows(const void *p, int64_t stride) {
-    return reinterpret_cast<uintptr_t>(p) % (8 * ElemOf<DT>::kBytes) == 0 && (p == nullptr || stride % 8 == 0);
-}
 template <int DT> bool wide_weight(const void *w, bool f32) {
     return reinterpret_cast<uintptr_t>(w) % (f32 || DT == DT_F32 ? 32 : 16) == 0;
 }

@@ -185,4 +185,10 @@ template <int DT> __device__ __forceinline__ void *row_of(void *base, int64_t ro
     return static_cast<char *>(base) + row * stride * ElemOf<DT>::kBytes;
 }
 
+// 16-byte accesses (32-byte ones for binary32): the base and the stride of a
+// matrix are multiples of 8 elements.  Null matrices allow anything.
+template <int DT> inline bool wide_rows(const void *p, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % (8 * ElemOf<DT>::kBytes) == 0 && (p == nullptr || stride % 8 == 0);
+}
+
 }  // namespace ew

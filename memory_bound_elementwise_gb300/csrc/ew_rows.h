@@ -91,4 +91,34 @@ cudaError_t norm_grad_f16(const NormGradArgs &a, int64_t most_writers, int sms, 
 cudaError_t norm_grad_bf16(const NormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
                            int *launches);
 
+// ---------------------------------------------------------------- embedding
+
+struct EmbedArgs {
+    const void *table, *tokens;
+    void *out;
+    int64_t table_rows, table_stride, out_stride, rows;
+    int32_t cols;
+    int32_t i64;  // tokens are 64-bit integers
+    float scale;
+};
+cudaError_t launch_embed(int dtype, const EmbedArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
+
+struct EmbedGradArgs {
+    const void *dout, *tokens;
+    void *dtable;
+    int64_t dout_stride, table_rows, table_stride, rows;
+    int32_t cols;
+    int32_t i64;
+    int32_t accumulate;
+    float scale;
+    // workspace
+    uint2 *items0, *items1;  // (token, position) between passes of the sort
+    uint32_t *keys, *order;  // sorted tokens (table_rows: none) and their positions
+    uint32_t *present;       // a bit for each table row that a token names; null with accumulate
+    float *partial;          // sums of the runs that cross chunks
+};
+int64_t embed_partial_bytes(int64_t rows, int64_t cols);
+cudaError_t launch_embed_grad(int dtype, int gtype, const EmbedGradArgs &a, cudaStream_t s, LaunchInfo *info,
+                              int *launches);
+
 }  // namespace ew

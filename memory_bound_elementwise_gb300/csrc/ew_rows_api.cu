@@ -129,6 +129,28 @@ ew_status norm_call(ew_dtype dt, const void *x, int64_t x_stride, const void *re
     return EW_OK;
 }
 
+// Workspace of the embedding's gradient, each part at a multiple of 256 bytes.
+struct EmbedWork {
+    int64_t items0, items1, keys, order, present, partial, bytes;
+};
+EmbedWork embed_work(int64_t table_rows, int64_t rows, int64_t cols) {
+    int64_t at = 0;
+    auto take = [&at](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    EmbedWork w;
+    w.items0 = take(rows * 8);
+    w.items1 = take(rows * 8);
+    w.keys = take(rows * 4);
+    w.order = take(rows * 4);
+    w.present = take((table_rows + 31) / 32 * 4);
+    w.partial = take(embed_partial_bytes(rows, cols));
+    w.bytes = at;
+    return w;
+}
+
 // Rows of partial sums that the norm's backward may use: one for each row up to
 // 1280, which is more than its blocks.
 constexpr int64_t kNormPartials = 1280;
@@ -136,6 +158,68 @@ constexpr int64_t kNormPartials = 1280;
 }  // namespace
 
 extern "C" {
+
+ew_status ew_embed(ew_dtype dt, ew_index itype, const void *table, int64_t table_rows, int64_t table_stride,
+                   const void *tokens, float scale, void *out, int64_t out_stride, int64_t rows, int64_t cols,
+                   ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || (itype != EW_INDEX_I32 && itype != EW_INDEX_I64)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!size_ok(rows, 0) || !size_ok(cols, 1) || !size_ok(table_rows, 0)) return EW_ERR_INVALID_VALUE;
+    if (rows == 0) return EW_OK;
+    const int e = bytes_of(dt);
+    const Operand in[2] = {{table, table_rows, cols, table_stride, e}, vec(tokens, rows, itype == EW_INDEX_I64 ? 8 : 4)};
+    const Operand outs[1] = {{out, rows, cols, out_stride, e}};
+    const ew_status st = check_all(in, 2, outs, 1);
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    const EmbedArgs a{table, tokens, out, table_rows, table_stride, out_stride, rows, static_cast<int32_t>(cols),
+                      itype == EW_INDEX_I64, scale};
+    LaunchInfo info;
+    ce = launch_embed(dt, a, sms, reinterpret_cast<cudaStream_t>(s), &info);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, 1);
+    return EW_OK;
+}
+
+int64_t ew_embed_grad_workspace(int64_t table_rows, int64_t rows, int64_t cols) {
+    if (!size_ok(table_rows, 0) || !size_ok(rows, 0) || !size_ok(cols, 1)) return -1;
+    return embed_work(table_rows, rows, cols).bytes;
+}
+
+ew_status ew_embed_grad(ew_dtype dt, ew_index itype, const void *dout, int64_t dout_stride, const void *tokens,
+                        float scale, ew_dtype gtype, void *dtable, int64_t table_rows, int64_t table_stride,
+                        int64_t rows, int64_t cols, int accumulate, void *workspace, int64_t workspace_bytes,
+                        ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || (gtype != dt && gtype != EW_F32) || (itype != EW_INDEX_I32 && itype != EW_INDEX_I64))
+        return EW_ERR_UNSUPPORTED_DTYPE;
+    const int64_t need = ew_embed_grad_workspace(table_rows, rows, cols);
+    if (need < 0 || workspace_bytes < need || (accumulate != 0 && accumulate != 1) ||
+        reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return EW_ERR_INVALID_VALUE;
+    if (table_rows == 0 || (rows == 0 && accumulate)) return EW_OK;
+    const Operand in[2] = {{dout, rows, cols, dout_stride, bytes_of(dt)},
+                           vec(tokens, rows, itype == EW_INDEX_I64 ? 8 : 4)};
+    const Operand out[2] = {{dtable, table_rows, cols, table_stride, bytes_of(gtype)}, vec(workspace, need, 1)};
+    const ew_status st = check_all(in, 2, out, 2);
+    if (st != EW_OK) return st;
+    const EmbedWork w = embed_work(table_rows, rows, cols);
+    char *base = static_cast<char *>(workspace);
+    const EmbedGradArgs a{dout, tokens, dtable, dout_stride, table_rows, table_stride, rows, static_cast<int32_t>(cols),
+                          itype == EW_INDEX_I64, accumulate, scale, reinterpret_cast<uint2 *>(base + w.items0),
+                          reinterpret_cast<uint2 *>(base + w.items1), reinterpret_cast<uint32_t *>(base + w.keys),
+                          reinterpret_cast<uint32_t *>(base + w.order),
+                          accumulate ? nullptr : reinterpret_cast<uint32_t *>(base + w.present),
+                          reinterpret_cast<float *>(base + w.partial)};
+    LaunchInfo info;
+    int launches = 0;
+    const cudaError_t ce = launch_embed_grad(dt, gtype, a, reinterpret_cast<cudaStream_t>(s), &info, &launches);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, launches);
+    return EW_OK;
+}
 
 ew_status ew_rmsnorm(ew_dtype dt, const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
                      ew_dtype wtype, const void *weight, float eps, void *y, int64_t y_stride, void *h_out,

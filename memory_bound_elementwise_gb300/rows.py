@@ -13,6 +13,7 @@ import torch
 
 _F32, _F16, _BF16 = 0, 1, 2
 _CODES = {torch.float32: _F32, torch.float16: _F16, torch.bfloat16: _BF16}
+_INDEX = {torch.int32: 0, torch.int64: 1}
 _QTYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
 
 _fns = {}
@@ -99,6 +100,62 @@ _here = contextlib.nullcontext()
 def _allocating(stream):
     """Allocations inside belong to the stream that the call runs on."""
     return _here if stream is None else torch.cuda.stream(stream)
+
+
+def _tokens(t, what, n, device):
+    """(type code, pointer) of n token ids."""
+    code = _INDEX.get(t.dtype)
+    if code is None:
+        raise TypeError("%s: int32 or int64, got %s" % (what, t.dtype))
+    return code, _vector(t, what, n, t.dtype, device)
+
+
+def ew_embed(table, tokens, out=None, scale=1.0, stream=None):
+    """out[t] = scale * table[tokens[t]]; returns out, of tokens' shape by the table's columns.
+
+    A token outside the table gives a row of zeros."""
+    device = _cuda_device(table, "table")
+    code = _code(table, "table")
+    table_rows, cols, stride = _matrix(table, "table", device)
+    rows = tokens.numel()
+    icode, iptr = _tokens(tokens, "tokens", rows, device)
+    if out is None:
+        with _allocating(stream):
+            out = torch.empty((*tokens.shape, cols), dtype=table.dtype, device=device)
+        out_stride = cols
+    else:
+        out_stride = _like(out, "out", rows, cols, table.dtype, device)
+    _call("ew_embed", code, icode, table.data_ptr(), table_rows, stride, iptr, scale, out.data_ptr(), out_stride, rows,
+          cols, _raw_stream(stream, device))
+    return out
+
+
+def ew_embed_grad(dout, tokens, table_rows, dtable=None, scale=1.0, accumulate=False, stream=None):
+    """Gradient of ew_embed for a table of ``table_rows`` rows; returns dtable.
+
+    dtable has dout's dtype or float32; it is written whole, or with
+    ``accumulate`` the gradient is added to what it holds.  The same tokens and
+    values give the same bits each time."""
+    device = _cuda_device(dout, "dout")
+    code = _code(dout, "dout")
+    rows, cols, stride = _matrix(dout, "dout", device)
+    icode, iptr = _tokens(tokens, "tokens", rows, device)
+    if dtable is None and accumulate:
+        raise ValueError("accumulate needs a dtable to add to")
+    if dtable is not None and dtable.dtype != dout.dtype and dtable.dtype != torch.float32:
+        raise TypeError("dtable: %s or float32, got %s" % (dout.dtype, dtable.dtype))
+    with _allocating(stream):
+        if dtable is None:
+            dtable = torch.empty((table_rows, cols), dtype=dout.dtype, device=device)
+            table_stride = cols
+        else:
+            table_stride = _like(dtable, "dtable", table_rows, cols, dtable.dtype, device)
+        need = _bytes("ew_embed_grad_workspace", table_rows, rows, cols)
+        work = torch.empty(need, dtype=torch.uint8, device=device)
+    _call("ew_embed_grad", code, icode, dout.data_ptr(), stride, iptr, scale, _CODES[dtable.dtype], dtable.data_ptr(),
+          table_rows, table_stride, rows, cols, 1 if accumulate else 0, work.data_ptr(), need,
+          _raw_stream(stream, device))
+    return dtable
 
 
 def _weight(weight, cols, dtype, code, device):

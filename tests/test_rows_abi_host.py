@@ -77,3 +77,34 @@ def test_norm_grad_refusals():
     assert norm_grad(rows=0, dw=None) == OK
     assert ew.lib().ew_rmsnorm_grad_workspace(-1, 64) == -1 and ew.lib().ew_rmsnorm_grad_workspace(4, BIG + 1) == -1
     assert ew.last_launch()["launches"] == 0
+
+
+def embed(dt=2, it=1, table=P, n=100, ts=64, tokens=P + MB, out=P + 2 * MB, os_=64, rows=4, cols=64):
+    return ew.lib().ew_embed(dt, it, table, n, ts, tokens, 1.0, out, os_, rows, cols, None)
+
+
+def embed_grad(dt=2, it=1, dout=P, ds=64, tokens=P + MB, gt=0, dtable=P + 2 * MB, n=100, ts=64, rows=4, cols=64, acc=0,
+               work=P + 8 * MB, size=8 * MB):
+    return ew.lib().ew_embed_grad(dt, it, dout, ds, tokens, 1.0, gt, dtable, n, ts, rows, cols, acc, work, size, None)
+
+
+def test_embed_refusals():
+    assert embed(dt=3) == DTYPE and embed(it=2) == DTYPE and embed(it=-1) == DTYPE
+    assert embed(rows=0, tokens=None, out=None) == OK
+    assert embed(rows=-1) == INVALID and embed(cols=0) == INVALID and embed(n=-1) == INVALID and embed(n=BIG + 1) == INVALID
+    assert embed(table=None) == NULLP and embed(tokens=None) == NULLP and embed(out=None) == NULLP
+    assert embed(tokens=P + MB + 4) == INVALID and embed(ts=63) == INVALID and embed(out=P + 1) == INVALID
+    assert embed(out=P) == OVERLAP and embed(out=P + MB) == OVERLAP
+
+
+def test_embed_grad_refusals():
+    assert embed_grad(dt=3) == DTYPE and embed_grad(gt=1) == DTYPE and embed_grad(it=5) == DTYPE
+    assert embed_grad(acc=2) == INVALID and embed_grad(size=100) == INVALID and embed_grad(work=P + 8 * MB + 8) == INVALID
+    assert embed_grad(rows=-1) == INVALID and embed_grad(cols=BIG + 1) == INVALID and embed_grad(ds=1) == INVALID
+    assert embed_grad(dout=None) == NULLP and embed_grad(tokens=None) == NULLP and embed_grad(dtable=None) == NULLP
+    assert embed_grad(work=None) == NULLP
+    assert embed_grad(dtable=P) == OVERLAP and embed_grad(work=P) == OVERLAP
+    assert embed_grad(n=0) == OK and embed_grad(rows=0, acc=1) == OK
+    assert ew.lib().ew_embed_grad_workspace(100, -1, 64) == -1
+    assert ew.lib().ew_embed_grad_workspace(0, 0, 1) == 0
+    assert ew.last_launch()["launches"] == 0
