@@ -346,6 +346,62 @@ EW_API ew_status ew_rmsnorm_grad(ew_dtype dtype, const void *dy, int64_t dy_stri
 /* Bytes of workspace (-1: sizes out of range); 0 columns of dweight need none. */
 EW_API int64_t ew_rmsnorm_grad_workspace(int64_t rows, int64_t cols);
 
+/* Log probabilities of given tokens, with entropy and top alternatives.  Per row,
+ * with p = softmax(scale * logits):
+ *     lse      = log(sum exp(scale * logits))
+ *     logp     = log p[tokens[row]]
+ *     entropy  = -sum p log p
+ *     top_ids, top_logp: the `top` (0 to 64) largest logits' columns and log p,
+ *                largest first, equal ones by the lower column
+ * logp, entropy and lse may each be NULL; tokens may be with logp.  A token
+ * outside [0, cols) has logp 0.  0 < scale <= 2^20.  Logits of -inf are masked: p = 0, and
+ * they are no alternatives; where fewer than `top` are left, ids are -1 with
+ * top_logp -inf.  The type's lowest value is a value like others: a row of
+ * nothing else is uniform.  A row of -inf alone has lse and logp -inf and
+ * entropy 0.  A row with a NaN or +inf has NaN in all results and ids of -1. */
+EW_API ew_status ew_logprob(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride, const void *tokens,
+                            float scale, int64_t top, float *logp, float *entropy, float *lse, float *top_logp,
+                            int32_t *top_ids, int64_t rows, int64_t cols, ew_stream_t stream);
+
+/* Gradient of ew_logprob with respect to the logits, from its lse and entropy:
+ *     dlogits = scale * (dlogp (1_token - p) - dentropy p (log p + entropy))
+ * dlogp and dentropy: binary32, one a row, either may be NULL (tokens and
+ * entropy are then not read).  Rows without a token have no dlogp term, rows of -inf
+ * alone a zero gradient.  dlogits may be logits (the same base and stride). */
+EW_API ew_status ew_logprob_grad(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride,
+                                 const void *tokens, const float *lse, const float *entropy, const float *dlogp,
+                                 const float *dentropy, float scale, void *dlogits, int64_t dstride, int64_t rows,
+                                 int64_t cols, ew_stream_t stream);
+
+/* Distillation from a teacher's top logits.  ids, teacher: rows x k (k at most
+ * 1024) columns and the teacher's logits there, of type ttype (dtype or
+ * EW_F32).  Per row, q = softmax(scale * teacher) over the k entries and
+ * p = softmax(scale * logits) over the whole row:
+ *     loss    = sum over entries of q (log q - log p[id])
+ *     dlogits = dloss * scale * (p - q at its columns)
+ *     lse     = log(sum exp(scale * logits))
+ * scale is 1 / temperature, 0 < scale <= 2^20.  Entries with an id outside [0, cols) or a value
+ * of -inf do not count; a row without any has loss 0 and gradient 0.  Entries
+ * of one row with the same id stay terms of their own in the loss and add up
+ * in the gradient.  Masked logits have p = 0; a teacher's
+ * entry there makes the loss infinite.
+ * ew_distill computes loss and lse, ew_distill_grad dlogits from a given lse,
+ * ew_distill_step all of it in one pass over the rows where dloss (binary32,
+ * one a row) is known beforehand.  dlogits may be logits (the same base and
+ * stride). */
+EW_API ew_status ew_distill(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride, const void *ids,
+                            int64_t ids_stride, ew_dtype ttype, const void *teacher, int64_t teacher_stride,
+                            int64_t k, float scale, float *loss, float *lse, int64_t rows, int64_t cols,
+                            ew_stream_t stream);
+EW_API ew_status ew_distill_grad(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride, const void *ids,
+                                 int64_t ids_stride, ew_dtype ttype, const void *teacher, int64_t teacher_stride,
+                                 int64_t k, float scale, const float *lse, const float *dloss, void *dlogits,
+                                 int64_t dstride, int64_t rows, int64_t cols, ew_stream_t stream);
+EW_API ew_status ew_distill_step(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride, const void *ids,
+                                 int64_t ids_stride, ew_dtype ttype, const void *teacher, int64_t teacher_stride,
+                                 int64_t k, float scale, const float *dloss, float *loss, float *lse, void *dlogits,
+                                 int64_t dstride, int64_t rows, int64_t cols, ew_stream_t stream);
+
 /* ---- variant selection and introspection ------------------------------ */
 
 /* Select the kernel variant for later calls in this process (EW_PATH_AUTO

@@ -22,6 +22,9 @@ Row operators (matrices, one row at a time; ``rows.py``)::
     ew_rmsnorm(x, w, residual)      (y, h, rstd): h = x + residual, y = h / rms(h) * w
     ew_rmsnorm_quant(...)           (q, scales, h, rstd): the same with an 8-bit output
     ew_rmsnorm_grad(dy, h, w, rstd) (dx, dweight)
+    ew_logprob(logits, tokens, top) log probabilities, entropy, lse and top alternatives
+    ew_logprob_grad(...)            their gradient
+    ew_distill(logits, ids, teacher)(loss, lse); ew_distill_grad, ew_distill_step
 
 Tensors must be contiguous CUDA tensors of dtype float32, float16 or bfloat16
 (int32 for ew_select_even_odd, ew_copy and ew_gather_stride) on the current
@@ -58,10 +61,12 @@ EXPORTS = ("ew_add", "ew_saxpy", "ew_relu", "ew_add_relu", "ew_saxpy_relu", "ew_
            "ew_get_path", "ew_set_schedule", "ew_get_schedule", "ew_set_pointer_check",
            "ew_plan_query", "ew_last_launch", "ew_gather_plan_query", "ew_status_string", "ew_last_cuda_error",
            "ew_device_error", "ew_selftest_bounded_wait", "ew_version",
-           "ew_embed", "ew_embed_grad", "ew_embed_grad_workspace", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad", "ew_rmsnorm_grad_workspace")
+           "ew_embed", "ew_embed_grad", "ew_embed_grad_workspace", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad", "ew_rmsnorm_grad_workspace",
+           "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
 
 # Row operators (rows.py), loaded with torch at their first use.
-_ROW_OPERATORS = ("ew_embed", "ew_embed_grad", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad")
+_ROW_OPERATORS = ("ew_embed", "ew_embed_grad", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad",
+                  "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
 # Their C arguments: i enum, l int64, f float, p pointer.
 _ROW_SIGNATURES = {
     "ew_embed": "iipllpfplllp",
@@ -71,6 +76,11 @@ _ROW_SIGNATURES = {
     "ew_rmsnorm_quant": "iplplipfilplplplpllp",
     "ew_rmsnorm_grad": "iplplippplplpllplp",
     "ew_rmsnorm_grad_workspace": "ll",
+    "ew_logprob": "iiplpflpppppllp",
+    "ew_logprob_grad": "iiplpppppfplllp",
+    "ew_distill": "iiplplipllfppllp",
+    "ew_distill_grad": "iiplplipllfppplllp",
+    "ew_distill_step": "iiplplipllfpppplllp",
 }
 
 

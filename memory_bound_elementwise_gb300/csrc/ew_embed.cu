@@ -20,10 +20,6 @@
 namespace ew {
 namespace {
 
-__device__ __forceinline__ int64_t token_at(const void *tokens, bool i64, int64_t t) {
-    return i64 ? static_cast<const int64_t *>(tokens)[t] : static_cast<const int32_t *>(tokens)[t];
-}
-
 // ---------------------------------------------------------------- lookup
 
 // A warp takes U consecutive (row, tile of 256 columns) items.
@@ -101,22 +97,6 @@ constexpr int kSortBlocks = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 10;
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t load_of_block(const uint32_t *mine, uint32_t rank) {
-    uint32_t at, v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-        : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
-}
 
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradArgs a, int passes, int bits) {
     enter_grid();

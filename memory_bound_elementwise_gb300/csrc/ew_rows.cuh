@@ -168,13 +168,42 @@ __device__ __forceinline__ float block_sum(float v, int warps, float *part) {
     __syncthreads();
     return warp_sum(lane < warps ? part[lane] : 0.0f);
 }
-__device__ __forceinline__ float block_max_nan(float v, int warps, float *part) {
+__device__ __forceinline__ float block_max_nan(float v, int warps, float *part, float least = 0.0f) {
     v = lanes_max_nan(v, 32);
     if (warps == 1) return v;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (lane == 0) part[warp] = v;
     __syncthreads();
-    return lanes_max_nan(lane < warps ? part[lane] : 0.0f, 32);
+    return lanes_max_nan(lane < warps ? part[lane] : least, 32);
+}
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t load_of_block(const uint32_t *mine, uint32_t rank) {
+    uint32_t at, v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// The address of a shared variable of this block as block `rank` of the cluster has it.
+template <typename T> __device__ __forceinline__ const T *in_block(const T *mine, uint32_t rank) {
+    uint64_t at;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(at) : "l"(reinterpret_cast<uint64_t>(mine)), "r"(rank));
+    return reinterpret_cast<const T *>(at);
+}
+
+__device__ __forceinline__ int64_t token_at(const void *tokens, bool i64, int64_t t) {
+    return i64 ? static_cast<const int64_t *>(tokens)[t] : static_cast<const int32_t *>(tokens)[t];
 }
 
 // base + row * stride elements, in 64 bits

@@ -121,4 +121,46 @@ int64_t embed_partial_bytes(int64_t rows, int64_t cols);
 cudaError_t launch_embed_grad(int dtype, int gtype, const EmbedGradArgs &a, cudaStream_t s, LaunchInfo *info,
                               int *launches);
 
+// ---------------------------------------------------------------- logits
+
+constexpr int kMostTop = 64;        // alternatives a row
+constexpr int kMostTeacher = 1024;  // teacher entries a row
+
+struct LogprobArgs {
+    const void *logits, *tokens;
+    float *logp, *entropy, *lse;  // null where not wanted
+    float *top_logp;
+    int32_t *top_ids;
+    int64_t stride, rows;
+    int32_t cols, i64, top;
+    float scale;
+};
+struct LogprobGradArgs {
+    const void *logits, *tokens;
+    const float *lse, *entropy, *dlogp, *dentropy;
+    void *dlogits;
+    int64_t stride, dstride, rows;
+    int32_t cols, i64;
+    float scale;
+};
+struct DistillArgs {
+    const void *logits, *ids, *teacher;
+    const float *dloss;
+    float *loss, *lse;  // lse: an input of the gradient alone
+    void *dlogits;
+    int64_t stride, ids_stride, teacher_stride, dstride, rows;
+    int32_t cols, i64, teacher_f32, k;
+    float scale;
+};
+// sums: the loss and lse are computed; grad: dlogits is.
+cudaError_t logprob_f32(const LogprobArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t logprob_grad_f32(const LogprobGradArgs &a, cudaStream_t s, LaunchInfo *info);
+cudaError_t distill_f32(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t logprob_f16(const LogprobArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t logprob_grad_f16(const LogprobGradArgs &a, cudaStream_t s, LaunchInfo *info);
+cudaError_t distill_f16(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t logprob_bf16(const LogprobArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t logprob_grad_bf16(const LogprobGradArgs &a, cudaStream_t s, LaunchInfo *info);
+cudaError_t distill_bf16(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info);
+
 }  // namespace ew

@@ -151,6 +151,46 @@ EmbedWork embed_work(int64_t table_rows, int64_t rows, int64_t cols) {
     return w;
 }
 
+bool index_type(int t) { return t == EW_INDEX_I32 || t == EW_INDEX_I64; }
+int index_bytes(ew_index t) { return t == EW_INDEX_I64 ? 8 : 4; }
+// What multiplies logits: positive, and far from where binary32 ends.
+bool scale_ok(float scale) { return scale > 0.0f && scale <= 1048576.0f; }
+
+// The three distillation calls: sums (loss and lse) and grad (dlogits).
+ew_status distill_call(bool sums, bool grad, ew_dtype dt, ew_index itype, const void *logits, int64_t stride,
+                       const void *ids, int64_t ids_stride, ew_dtype ttype, const void *teacher,
+                       int64_t teacher_stride, int64_t k, float scale, const float *dloss, float *loss, float *lse,
+                       void *dlogits, int64_t dstride, int64_t rows, int64_t cols, cudaStream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || (ttype != dt && ttype != EW_F32) || !index_type(itype)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!size_ok(rows, 0) || !size_ok(cols, 1) || k < 1 || k > kMostTeacher || !scale_ok(scale))
+        return EW_ERR_INVALID_VALUE;
+    if (rows == 0) return EW_OK;
+    const int e = bytes_of(dt);
+    const Operand in[5] = {{logits, rows, cols, stride, e},
+                           {ids, rows, k, ids_stride, index_bytes(itype)},
+                           {teacher, rows, k, teacher_stride, bytes_of(ttype)},
+                           vec(dloss, grad ? rows : 0, 4),
+                           vec(sums ? nullptr : lse, rows, 4, !sums)};
+    const Operand out[3] = {{dlogits, grad ? rows : 0, cols, grad ? dstride : cols, e},
+                            vec(sums ? loss : nullptr, rows, 4, sums),
+                            vec(sums ? lse : nullptr, rows, 4, sums)};
+    const bool in_place[3][2] = {{true, false}, {false, false}, {false, false}};
+    const ew_status st = check_all(in, 5, out, 3, in_place);
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    const DistillArgs a{logits, ids, teacher, dloss, loss, lse, dlogits, stride, ids_stride, teacher_stride, dstride,
+                        rows, static_cast<int32_t>(cols), itype == EW_INDEX_I64, ttype == EW_F32,
+                        static_cast<int32_t>(k), scale};
+    LaunchInfo info;
+    ce = (dt == EW_F32 ? distill_f32 : dt == EW_F16 ? distill_f16 : distill_bf16)(a, sums, grad, sms, s, &info);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, 1);
+    return EW_OK;
+}
+
 // Rows of partial sums that the norm's backward may use: one for each row up to
 // 1280, which is more than its blocks.
 constexpr int64_t kNormPartials = 1280;
@@ -163,11 +203,11 @@ ew_status ew_embed(ew_dtype dt, ew_index itype, const void *table, int64_t table
                    const void *tokens, float scale, void *out, int64_t out_stride, int64_t rows, int64_t cols,
                    ew_stream_t s) {
     launch_record() = ew_launch_record{};
-    if (!float_type(dt) || (itype != EW_INDEX_I32 && itype != EW_INDEX_I64)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!float_type(dt) || !index_type(itype)) return EW_ERR_UNSUPPORTED_DTYPE;
     if (!size_ok(rows, 0) || !size_ok(cols, 1) || !size_ok(table_rows, 0)) return EW_ERR_INVALID_VALUE;
     if (rows == 0) return EW_OK;
     const int e = bytes_of(dt);
-    const Operand in[2] = {{table, table_rows, cols, table_stride, e}, vec(tokens, rows, itype == EW_INDEX_I64 ? 8 : 4)};
+    const Operand in[2] = {{table, table_rows, cols, table_stride, e}, vec(tokens, rows, index_bytes(itype))};
     const Operand outs[1] = {{out, rows, cols, out_stride, e}};
     const ew_status st = check_all(in, 2, outs, 1);
     if (st != EW_OK) return st;
@@ -193,7 +233,7 @@ ew_status ew_embed_grad(ew_dtype dt, ew_index itype, const void *dout, int64_t d
                         int64_t rows, int64_t cols, int accumulate, void *workspace, int64_t workspace_bytes,
                         ew_stream_t s) {
     launch_record() = ew_launch_record{};
-    if (!float_type(dt) || (gtype != dt && gtype != EW_F32) || (itype != EW_INDEX_I32 && itype != EW_INDEX_I64))
+    if (!float_type(dt) || (gtype != dt && gtype != EW_F32) || !index_type(itype))
         return EW_ERR_UNSUPPORTED_DTYPE;
     const int64_t need = ew_embed_grad_workspace(table_rows, rows, cols);
     if (need < 0 || workspace_bytes < need || (accumulate != 0 && accumulate != 1) ||
@@ -201,7 +241,7 @@ ew_status ew_embed_grad(ew_dtype dt, ew_index itype, const void *dout, int64_t d
         return EW_ERR_INVALID_VALUE;
     if (table_rows == 0 || (rows == 0 && accumulate)) return EW_OK;
     const Operand in[2] = {{dout, rows, cols, dout_stride, bytes_of(dt)},
-                           vec(tokens, rows, itype == EW_INDEX_I64 ? 8 : 4)};
+                           vec(tokens, rows, index_bytes(itype))};
     const Operand out[2] = {{dtable, table_rows, cols, table_stride, bytes_of(gtype)}, vec(workspace, need, 1)};
     const ew_status st = check_all(in, 2, out, 2);
     if (st != EW_OK) return st;
@@ -277,6 +317,85 @@ ew_status ew_rmsnorm_grad(ew_dtype dt, const void *dy, int64_t dy_stride, const 
     if (ce != cudaSuccess) return report_cuda(ce);
     record(info, launches);
     return EW_OK;
+}
+
+ew_status ew_logprob(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *tokens, float scale,
+                     int64_t top, float *logp, float *entropy, float *lse, float *top_logp, int32_t *top_ids,
+                     int64_t rows, int64_t cols, ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || !index_type(itype)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!size_ok(rows, 0) || !size_ok(cols, 1) || top < 0 || top > kMostTop || !scale_ok(scale))
+        return EW_ERR_INVALID_VALUE;
+    if (rows == 0) return EW_OK;
+    const Operand in[2] = {{logits, rows, cols, stride, bytes_of(dt)},
+                           vec(tokens, rows, index_bytes(itype), logp != nullptr)};
+    const Operand out[5] = {vec(logp, rows, 4, false), vec(entropy, rows, 4, false), vec(lse, rows, 4, false),
+                            vec(top_logp, rows * top, 4), vec(top_ids, rows * top, 4)};
+    const ew_status st = check_all(in, 2, out, top > 0 ? 5 : 3);
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    const LogprobArgs a{logits, tokens, logp, entropy, lse, top_logp, top_ids, stride, rows,
+                        static_cast<int32_t>(cols), itype == EW_INDEX_I64, static_cast<int32_t>(top), scale};
+    LaunchInfo info;
+    ce = (dt == EW_F32 ? logprob_f32 : dt == EW_F16 ? logprob_f16 : logprob_bf16)(
+        a, sms, reinterpret_cast<cudaStream_t>(s), &info);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, 1);
+    return EW_OK;
+}
+
+ew_status ew_logprob_grad(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *tokens,
+                          const float *lse, const float *entropy, const float *dlogp, const float *dentropy,
+                          float scale, void *dlogits, int64_t dstride, int64_t rows, int64_t cols, ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || !index_type(itype)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!size_ok(rows, 0) || !size_ok(cols, 1) || !scale_ok(scale)) return EW_ERR_INVALID_VALUE;
+    if (rows == 0) return EW_OK;
+    const int e = bytes_of(dt);
+    const Operand in[6] = {{logits, rows, cols, stride, e},
+                           vec(tokens, rows, index_bytes(itype), dlogp != nullptr),
+                           vec(lse, rows, 4),
+                           vec(entropy, rows, 4, dentropy != nullptr),
+                           vec(dlogp, rows, 4, false),
+                           vec(dentropy, rows, 4, false)};
+    const Operand out[1] = {{dlogits, rows, cols, dstride, e}};
+    const bool in_place[1][2] = {{true, false}};
+    const ew_status st = check_all(in, 6, out, 1, in_place);
+    if (st != EW_OK) return st;
+    const LogprobGradArgs a{logits, tokens, lse, entropy, dlogp, dentropy, dlogits, stride, dstride, rows,
+                            static_cast<int32_t>(cols), itype == EW_INDEX_I64, scale};
+    LaunchInfo info;
+    const cudaError_t ce = (dt == EW_F32 ? logprob_grad_f32 : dt == EW_F16 ? logprob_grad_f16 : logprob_grad_bf16)(
+        a, reinterpret_cast<cudaStream_t>(s), &info);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, 1);
+    return EW_OK;
+}
+
+ew_status ew_distill(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *ids,
+                     int64_t ids_stride, ew_dtype ttype, const void *teacher, int64_t teacher_stride, int64_t k,
+                     float scale, float *loss, float *lse, int64_t rows, int64_t cols, ew_stream_t s) {
+    return distill_call(true, false, dt, itype, logits, stride, ids, ids_stride, ttype, teacher, teacher_stride, k,
+                        scale, nullptr, loss, lse, nullptr, 0, rows, cols, reinterpret_cast<cudaStream_t>(s));
+}
+
+ew_status ew_distill_grad(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *ids,
+                          int64_t ids_stride, ew_dtype ttype, const void *teacher, int64_t teacher_stride, int64_t k,
+                          float scale, const float *lse, const float *dloss, void *dlogits, int64_t dstride,
+                          int64_t rows, int64_t cols, ew_stream_t s) {
+    return distill_call(false, true, dt, itype, logits, stride, ids, ids_stride, ttype, teacher, teacher_stride, k,
+                        scale, dloss, nullptr, const_cast<float *>(lse), dlogits, dstride, rows, cols,
+                        reinterpret_cast<cudaStream_t>(s));
+}
+
+ew_status ew_distill_step(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *ids,
+                          int64_t ids_stride, ew_dtype ttype, const void *teacher, int64_t teacher_stride, int64_t k,
+                          float scale, const float *dloss, float *loss, float *lse, void *dlogits, int64_t dstride,
+                          int64_t rows, int64_t cols, ew_stream_t s) {
+    return distill_call(true, true, dt, itype, logits, stride, ids, ids_stride, ttype, teacher, teacher_stride, k,
+                        scale, dloss, loss, lse, dlogits, dstride, rows, cols, reinterpret_cast<cudaStream_t>(s));
 }
 
 }  // extern "C"

@@ -7,6 +7,7 @@ on ``stream`` (default: torch's current stream) and do not synchronise.  What is
 allocated belongs to that stream.  Arguments that do not fit raise ``ValueError``
 or ``TypeError`` here, or ``EwError`` with the library's status.
 """
+import collections
 import contextlib
 
 import torch
@@ -266,3 +267,115 @@ def ew_rmsnorm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, stream=
     _call("ew_rmsnorm_grad", code, dy.data_ptr(), dy_stride, h.data_ptr(), h_stride, wcode, wptr, r_ptr, dh_ptr,
           dh_stride, dx.data_ptr(), dx_stride, dw_ptr, rows, cols, work.data_ptr(), need, _raw_stream(stream, device))
     return dx, dweight
+
+
+Logprobs = collections.namedtuple("Logprobs", "logp entropy lse top_logp top_ids")
+
+
+def ew_logprob(logits, tokens, top=0, scale=1.0, stream=None):
+    """Log probabilities under softmax(scale * logits), one row a token.
+
+    Returns Logprobs(logp, entropy, lse, top_logp, top_ids): float32, one a row,
+    and the ``top`` (at most 64) largest logits' log probabilities and int32
+    columns, largest first, equal ones by the lower column.  A token outside
+    the row (such as -1) has logp 0.  ``tokens`` may be None: then logp is None."""
+    device = _cuda_device(logits, "logits")
+    code = _code(logits, "logits")
+    rows, cols, stride = _matrix(logits, "logits", device)
+    icode, iptr = (0, None) if tokens is None else _tokens(tokens, "tokens", rows, device)
+    with _allocating(stream):
+        each = torch.empty((3, rows), dtype=torch.float32, device=device)
+        top_logp = torch.empty((rows, top), dtype=torch.float32, device=device)
+        top_ids = torch.empty((rows, top), dtype=torch.int32, device=device)
+    at, step = each.data_ptr(), 4 * rows
+    _call("ew_logprob", code, icode, logits.data_ptr(), stride, iptr, scale, top, at if iptr else None, at + step,
+          at + 2 * step, top_logp.data_ptr(), top_ids.data_ptr(), rows, cols, _raw_stream(stream, device))
+    logp, entropy, lse = each.unbind(0)
+    return Logprobs(None if tokens is None else logp, entropy, lse, top_logp, top_ids)
+
+
+def ew_logprob_grad(logits, tokens, lse, entropy, dlogp, dentropy=None, scale=1.0, dlogits=None, stream=None):
+    """Gradient with respect to the logits of ew_logprob's logp (times dlogp) and entropy (times dentropy); returns
+    dlogits, which may be logits.  dlogp or dentropy may be None."""
+    device = _cuda_device(logits, "logits")
+    code, dtype = _code(logits, "logits"), logits.dtype
+    rows, cols, stride = _matrix(logits, "logits", device)
+    icode, iptr, dlogp_ptr = 0, None, None
+    if dlogp is not None:
+        icode, iptr = _tokens(tokens, "tokens", rows, device)
+        dlogp_ptr = _vector(dlogp, "dlogp", rows, torch.float32, device)
+    lse_ptr = _vector(lse, "lse", rows, torch.float32, device)
+    ent_ptr, dent_ptr = None, None
+    if dentropy is not None:
+        ent_ptr = _vector(entropy, "entropy", rows, torch.float32, device)
+        dent_ptr = _vector(dentropy, "dentropy", rows, torch.float32, device)
+    dlogits, dstride = _gradient_of(logits, dlogits, rows, cols, dtype, device, stream)
+    _call("ew_logprob_grad", code, icode, logits.data_ptr(), stride, iptr, lse_ptr, ent_ptr, dlogp_ptr, dent_ptr, scale,
+          dlogits.data_ptr(), dstride, rows, cols, _raw_stream(stream, device))
+    return dlogits
+
+
+def _gradient_of(logits, dlogits, rows, cols, dtype, device, stream):
+    if dlogits is not None:
+        return dlogits, _like(dlogits, "dlogits", rows, cols, dtype, device)
+    with _allocating(stream):
+        return torch.empty(logits.shape, dtype=dtype, device=device), cols
+
+
+def _distill_inputs(logits, ids, teacher):
+    device = _cuda_device(logits, "logits")
+    code = _code(logits, "logits")
+    rows, cols, stride = _matrix(logits, "logits", device)
+    icode = _INDEX.get(ids.dtype)
+    if icode is None:
+        raise TypeError("ids: int32 or int64, got %s" % ids.dtype)
+    if teacher.dtype != logits.dtype and teacher.dtype != torch.float32:
+        raise TypeError("teacher: %s or float32, got %s" % (logits.dtype, teacher.dtype))
+    n, k, ids_stride = _matrix(ids, "ids", device)
+    if n != rows:
+        raise ValueError("ids: expected %d rows, got %d" % (rows, n))
+    teacher_stride = _like(teacher, "teacher", rows, k, teacher.dtype, device)
+    head = (code, icode, logits.data_ptr(), stride, ids.data_ptr(), ids_stride, _CODES[teacher.dtype],
+            teacher.data_ptr(), teacher_stride, k)
+    return device, rows, cols, head
+
+
+def ew_distill(logits, ids, teacher, scale=1.0, stream=None):
+    """Distillation from a teacher's top logits: returns (loss, lse), float32, one a row.
+
+    ``ids`` (int32 or int64) and ``teacher`` are rows x k: columns of the logits
+    and the teacher's logits there; an id of -1 does not count.  The loss is the
+    divergence of softmax(scale * logits) from softmax(scale * teacher) over the
+    k entries; scale is 1 / temperature."""
+    device, rows, cols, head = _distill_inputs(logits, ids, teacher)
+    with _allocating(stream):
+        each = torch.empty((2, rows), dtype=torch.float32, device=device)
+    at = each.data_ptr()
+    _call("ew_distill", *head, scale, at, at + 4 * rows, rows, cols, _raw_stream(stream, device))
+    return each.unbind(0)
+
+
+def ew_distill_grad(logits, ids, teacher, lse, dloss, scale=1.0, dlogits=None, stream=None):
+    """Gradient of ew_distill's loss (times dloss, float32, one a row) with respect to the logits, from its lse;
+    returns dlogits, which may be logits."""
+    device, rows, cols, head = _distill_inputs(logits, ids, teacher)
+    lse_ptr = _vector(lse, "lse", rows, torch.float32, device)
+    dloss_ptr = _vector(dloss, "dloss", rows, torch.float32, device)
+    dlogits, dstride = _gradient_of(logits, dlogits, rows, cols, logits.dtype, device, stream)
+    _call("ew_distill_grad", *head, scale, lse_ptr, dloss_ptr, dlogits.data_ptr(), dstride, rows, cols,
+          _raw_stream(stream, device))
+    return dlogits
+
+
+def ew_distill_step(logits, ids, teacher, dloss, scale=1.0, dlogits=None, stream=None):
+    """ew_distill and ew_distill_grad in one call, where dloss is known beforehand; returns (loss, lse, dlogits)."""
+    device, rows, cols, head = _distill_inputs(logits, ids, teacher)
+    dloss_ptr = _vector(dloss, "dloss", rows, torch.float32, device)
+    dlogits, dstride = _gradient_of(logits, dlogits, rows, cols, logits.dtype, device, stream)
+    with _allocating(stream):
+        each = torch.empty((2, rows), dtype=torch.float32, device=device)
+    at = each.data_ptr()
+    _call("ew_distill_step", *head, scale, dloss_ptr, at, at + 4 * rows, dlogits.data_ptr(), dstride, rows, cols,
+          _raw_stream(stream, device))
+    loss, lse = each.unbind(0)
+    return loss, lse, dlogits

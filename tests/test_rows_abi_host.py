@@ -108,3 +108,55 @@ def test_embed_grad_refusals():
     assert ew.lib().ew_embed_grad_workspace(100, -1, 64) == -1
     assert ew.lib().ew_embed_grad_workspace(0, 0, 1) == 0
     assert ew.last_launch()["launches"] == 0
+
+
+def logprob(dt=2, it=1, x=P, s=64, tok=P + MB, scale=1.0, top=0, lp=P + 2 * MB, ent=None, lse=None, tl=P + 3 * MB,
+            ti=P + 4 * MB, rows=4, cols=64):
+    return ew.lib().ew_logprob(dt, it, x, s, tok, scale, top, lp, ent, lse, tl, ti, rows, cols, None)
+
+
+def logprob_grad(dt=2, it=1, x=P, s=64, tok=P + MB, lse=P + 2 * MB, ent=P + 3 * MB, dlp=P + 4 * MB, dent=P + 5 * MB,
+                 scale=1.0, d=P + 6 * MB, ds=64, rows=4, cols=64):
+    return ew.lib().ew_logprob_grad(dt, it, x, s, tok, lse, ent, dlp, dent, scale, d, ds, rows, cols, None)
+
+
+def distill_step(dt=2, it=1, x=P, s=64, ids=P + MB, ids_s=8, tt=2, t=P + 2 * MB, ts=8, k=8, scale=1.0, dloss=P + 3 * MB,
+                 loss=P + 4 * MB, lse=P + 5 * MB, d=P + 6 * MB, ds=64, rows=4, cols=64):
+    return ew.lib().ew_distill_step(dt, it, x, s, ids, ids_s, tt, t, ts, k, scale, dloss, loss, lse, d, ds, rows, cols,
+                                    None)
+
+
+def test_logprob_refusals():
+    assert logprob(dt=3) == DTYPE and logprob(it=2) == DTYPE
+    assert logprob(rows=-1) == INVALID and logprob(cols=0) == INVALID and logprob(s=63) == INVALID
+    assert logprob(top=-1) == INVALID and logprob(top=65) == INVALID
+    for scale in (0.0, -1.0, float("nan"), float("inf"), 2.0 ** 21):
+        assert logprob(scale=scale) == INVALID and logprob_grad(scale=scale) == INVALID
+        assert distill_step(scale=scale) == INVALID
+    assert logprob(x=None) == NULLP and logprob(tok=None) == NULLP and logprob(top=3, ti=None) == NULLP
+    assert logprob(tok=P + MB + 4) == INVALID and logprob(lp=P + 2) == INVALID
+    assert logprob(lp=P) == OVERLAP and logprob(ent=P + 2 * MB) == OVERLAP and logprob(top=2, tl=P + 4 * MB) == OVERLAP
+    assert logprob(rows=0, x=None) == OK
+
+
+def test_logprob_grad_refusals():
+    assert logprob_grad(dt=-1) == DTYPE and logprob_grad(it=9) == DTYPE
+    assert logprob_grad(tok=None) == NULLP and logprob_grad(ent=None) == NULLP and logprob_grad(lse=None) == NULLP
+    assert logprob_grad(d=None) == NULLP and logprob_grad(ds=10) == INVALID and logprob_grad(d=P + 1) == INVALID
+    assert logprob_grad(d=P + 2) == OVERLAP and logprob_grad(d=P, ds=128) == OVERLAP and logprob_grad(d=P + MB) == OVERLAP
+    assert logprob_grad(rows=0) == OK
+
+
+def test_distill_refusals():
+    assert distill_step(dt=3) == DTYPE and distill_step(tt=1) == DTYPE and distill_step(it=-1) == DTYPE
+    assert distill_step(k=0) == INVALID and distill_step(k=1025, ids_s=1025, ts=1025) == INVALID
+    assert distill_step(ids_s=7) == INVALID and distill_step(ts=7) == INVALID and distill_step(rows=BIG + 1) == INVALID
+    for name in ("x", "ids", "t", "dloss", "loss", "lse", "d"):
+        assert distill_step(**{name: None}) == NULLP, name
+    assert distill_step(d=P + MB) == OVERLAP and distill_step(loss=P) == OVERLAP and distill_step(lse=P + 4 * MB) == OVERLAP
+    assert distill_step(rows=0) == OK
+    L = ew.lib()
+    assert L.ew_distill(2, 1, P, 64, P + MB, 8, 2, P + 2 * MB, 8, 8, 1.0, None, P + 5 * MB, 4, 64, None) == NULLP
+    assert L.ew_distill_grad(2, 1, P, 64, P + MB, 8, 2, P + 2 * MB, 8, 8, 1.0, None, P + 3 * MB, P + 6 * MB, 64, 4, 64,
+                             None) == NULLP
+    assert ew.last_launch()["launches"] == 0
