@@ -50,13 +50,13 @@ template <int DT, bool VEC, int U> __global__ void __launch_bounds__(256) embed_
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (first + u >= items) break;
-        float f[8];
+        float2 f[4];
         unpack8<DT>(r[u], f);
         const int64_t v = token_at(a.tokens, a.i64, rows[u]);
         // a row of no token is zeros whatever the scale is
         const bool given = v >= 0 && v < a.table_rows;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = given ? f[j] * a.scale : 0.0f;
+        for (int j = 0; j < 4; ++j) f[j] = given ? mul2(f[j], both(a.scale)) : both(0.0f);
         store_tile<DT, VEC>(row_of<DT>(a.out, rows[u], a.out_stride), bases[u], a.cols, lane, pack8<DT>(f));
     }
 }
@@ -194,16 +194,16 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradArgs 
 constexpr int kChunk = 32;  // sorted positions a warp takes, one to a lane
 
 template <int GT, bool VEC>
-__device__ __forceinline__ void write_sum(const EmbedGradArgs &a, uint32_t v, int base, int lane, const float (&sum)[8]) {
+__device__ __forceinline__ void write_sum(const EmbedGradArgs &a, uint32_t v, int base, int lane, const float2 (&sum)[4]) {
     void *row = row_of<GT>(a.dtable, v, a.table_stride);
-    float f[8];
+    float2 f[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = sum[j] * a.scale;
+    for (int j = 0; j < 4; ++j) f[j] = mul2(sum[j], both(a.scale));
     if (a.accumulate) {
-        float old[8];
+        float2 old[4];
         unpack8<GT>(load_tile<GT, VEC>(row, base, a.cols, lane), old);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] += old[j];
+        for (int j = 0; j < 4; ++j) f[j] = add2(f[j], old[j]);
     }
     store_tile<GT, VEC>(row, base, a.cols, lane, pack8<GT>(f));
 }
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a, int64_t
     const int count = __popc(__ballot_sync(kAllLanes, key != nowhere));  // positions without a token come last
     if (count == 0) return;
 
-    float sum[8] = {};
+    float2 sum[4] = {};
     uint32_t current = __shfl_sync(kAllLanes, key, 0);
     bool from_before = chunk > 0 && key_before == current;
     auto put = [&](bool goes_on) {
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a, int64_t
             write_sum<GT, VEC>(a, current, base, lane, sum);
         } else {
             float4 *p = partial_at(a, chunk, from_before ? 0 : 1, tile, lane);
-            p[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-            p[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+            p[0] = make_float4(sum[0].x, sum[0].y, sum[1].x, sum[1].y);
+            p[1] = make_float4(sum[2].x, sum[2].y, sum[3].x, sum[3].y);
         }
     };
     constexpr int U = 8;  // rows in flight
@@ -281,12 +281,12 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a, int64_t
                 current = k;
                 from_before = false;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+                for (int j = 0; j < 4; ++j) sum[j] = both(0.0f);
             }
-            float f[8];
+            float2 f[4];
             unpack8<DT>(r[u], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += f[j];
+            for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], f[j]);
         }
     }
     put(count == kChunk && key_after == current);
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a, int64_t
 // slot 1 and the slots 0 of the chunks after it, its 8 warps every eighth.
 template <int GT, bool VEC> __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
     enter_grid();
-    __shared__ float part[8][32][9];
+    __shared__ float2 part[8][4][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tile = blockIdx.y, base = tile * kTileCols;
     const int64_t chunk = blockIdx.x, chunks = (a.rows + kChunk - 1) / kChunk;
@@ -313,24 +313,26 @@ template <int GT, bool VEC> __global__ void __launch_bounds__(256) embed_join_ke
         reach += in == kAllLanes ? 32 : __ffs(~in) - 1;
         if (in != kAllLanes) break;
     }
-    float sum[8] = {};
+    float2 sum[4] = {};
     auto add = [&](int64_t c, int slot) {
         const float4 *p = partial_at(a, c, slot, tile, lane);
         const float4 x = p[0], y = p[1];
-        sum[0] += x.x; sum[1] += x.y; sum[2] += x.z; sum[3] += x.w;
-        sum[4] += y.x; sum[5] += y.y; sum[6] += y.z; sum[7] += y.w;
+        sum[0] = add2(sum[0], make_float2(x.x, x.y));
+        sum[1] = add2(sum[1], make_float2(x.z, x.w));
+        sum[2] = add2(sum[2], make_float2(y.x, y.y));
+        sum[3] = add2(sum[3], make_float2(y.z, y.w));
     };
     if (warp == 0) add(chunk, 1);
 #pragma unroll 4
     for (int64_t k = warp; k < reach; k += 8) add(chunk + 1 + k, 0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[warp][lane][j] = sum[j];
+    for (int j = 0; j < 4; ++j) part[warp][j][lane] = sum[j];
     __syncthreads();
     if (warp != 0) return;
 #pragma unroll
     for (int w = 1; w < 8; ++w)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += part[w][lane][j];
+        for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], part[w][j][lane]);
     write_sum<GT, VEC>(a, v, base, lane, sum);
 }
 

@@ -17,92 +17,104 @@
 namespace ew {
 namespace {
 
+constexpr int kGradWarps = 16;  // most warps that hold a row in the backward
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100: a scale is never zero
 
-__device__ __forceinline__ uint32_t quant_pair(float hi, float lo, bool i8) {
+__device__ __forceinline__ uint32_t quant_pair(float2 v, bool i8) {
     if (i8) {
         int32_t a, b;
-        asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(a) : "f"(lo));
-        asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(b) : "f"(hi));
+        asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(a) : "f"(v.x));
+        asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(b) : "f"(v.y));
         return (a & 0xff) | ((b & 0xff) << 8);
     }
     uint16_t d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(v.y), "f"(v.x));
     return d;
 }
 
 // Scale of a group whose largest absolute value is amax, and the factor that
-// takes y to q.  One division a group instead of one an element: the product
-// is within a rounding of y / scale.
-__device__ __forceinline__ float quant_factor(float amax, float qmax, float *scale) {
+// takes y to q.  Products with reciprocals: within two roundings of the
+// quotients, which moves a q only where y / scale all but ties.
+__device__ __forceinline__ float quant_factor(float amax, bool i8, float *scale) {
     amax = max_nan(amax, kAmaxFloor);
-    *scale = amax / qmax;
-    return qmax / amax;
+    *scale = amax * (i8 ? 1.0f / 127.0f : 1.0f / 448.0f);
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(amax));
+    return r * (i8 ? 127.0f : 448.0f);
 }
 
 // Quantises the lane's 8 values of y of one tile and stores them, with the
 // group's scales.  Every lane of the warp takes part.
 template <bool VEC>
-__device__ __forceinline__ void quant_tile(const float (&y)[8], const NormArgs &a, int64_t row, int base, int lane,
+__device__ __forceinline__ void quant_tile(const float2 (&y)[4], const NormArgs &a, int64_t row, int base, int lane,
                                            float row_factor) {
-    const float qmax = a.i8 ? 127.0f : 448.0f;
     uint8_t *q = static_cast<uint8_t *>(a.out) + row * a.out_stride;
-    float f[8];
-    if (a.group == 0) {
+    const int shift = a.group_shift;  // log2 of the group, 0: the row
+    const bool i8 = a.i8;
+    const int c0 = tile_col<VEC>(base, lane, 0);
+    if constexpr (VEC) {
+        float factor = row_factor;
+        if (shift != 0) {
+            float m = largest_of(y);
+            m = max_nan(m, __shfl_xor_sync(kAllLanes, m, 1));
+            m = max_nan(m, __shfl_xor_sync(kAllLanes, m, 2));
+            if (shift > 5) m = max_nan(m, __shfl_xor_sync(kAllLanes, m, 4));
+            if (shift > 6) m = max_nan(m, __shfl_xor_sync(kAllLanes, m, 8));
+            if (shift > 7) m = max_nan(m, __shfl_xor_sync(kAllLanes, m, 16));
+            float scale;
+            factor = quant_factor(m, i8, &scale);
+            if ((lane << 3 & ((1 << shift) - 1)) == 0 && c0 < a.cols)
+                a.scales[row * a.scales_stride + (c0 >> shift)] = scale;
+        }
+        const float2 f = both(factor);
+        const uint32_t q0 = quant_pair(mul2(y[0], f), i8), q1 = quant_pair(mul2(y[1], f), i8);
+        const uint32_t q2 = quant_pair(mul2(y[2], f), i8), q3 = quant_pair(mul2(y[3], f), i8);
+        Vec<8> v;
+        v.w[0] = q0 | (q1 << 16);
+        v.w[1] = q2 | (q3 << 16);
+        if (c0 + 8 <= a.cols) {
+            st<8>(q + c0, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j < a.cols) q[c0 + j] = static_cast<uint8_t>(v.w[j / 4] >> (8 * (j & 3)));
+        }
+    } else {
+        // step j of the tile is columns base + 32 j .. + 31; a group is 1, 2, 4 or 8 steps
+        float v[8], f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = y[j].x;
+            v[2 * j + 1] = y[j].y;
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = row_factor;
-    } else {
-        float *scales = a.scales + row * a.scales_stride;
-        if (VEC) {
-            float m = 0.0f;
+        if (shift != 0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(y[j]));
-            const int lanes = a.group / 8;
-            m = lanes_max_nan(m, lanes);
-            float scale;
-            const float factor = quant_factor(m, qmax, &scale);
-            const int c0 = base + lane * 8;
-            if (lane % lanes == 0 && c0 < a.cols) scales[c0 / a.group] = scale;
+            for (int j = 0; j < 8; ++j) f[j] = lanes_max_nan(fabsf(v[j]), 32);
+            // butterflies over the steps of a group: every step has its group's largest value
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = factor;
-        } else {
-            const int per = a.group / 32;  // steps of 32 columns a group
-            float m[8];
+            for (int d = 1; d < 8; d <<= 1) {
+                if ((32 << 1) * d > (1 << shift)) break;
+                float g[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m[j] = lanes_max_nan(fabsf(y[j]), 32);
-            for (int d = 1; d < per; d <<= 1) {
+                for (int j = 0; j < 8; ++j) g[j] = max_nan(f[j], f[j ^ d]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (((j & d) == 0)) {
-                        const float v = max_nan(m[j], m[(j + d) & 7]);
-                        m[j] = v;
-                    }
-                }
+                for (int j = 0; j < 8; ++j) f[j] = g[j];
             }
-            // after log2(per) rounds the first step of each group holds its largest value
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float first = m[0];
-#pragma unroll
-                for (int k = 1; k < 8; ++k) first = (j / per) * per == k ? m[k] : first;
                 float scale;
-                f[j] = quant_factor(first, qmax, &scale);
+                f[j] = quant_factor(f[j], i8, &scale);
                 const int c = base + j * 32;
-                if (lane == 0 && j % per == 0 && c < a.cols) scales[c / a.group] = scale;
+                if (lane == 0 && (c & ((1 << shift) - 1)) == 0 && c < a.cols)
+                    a.scales[row * a.scales_stride + (c >> shift)] = scale;
             }
         }
-    }
-    const int c0 = tile_col<VEC>(base, lane, 0);
-    if (VEC && c0 + 8 <= a.cols) {
-        Vec<8> v;
-        v.w[0] = quant_pair(y[1] * f[1], y[0] * f[0], a.i8) | (quant_pair(y[3] * f[3], y[2] * f[2], a.i8) << 16);
-        v.w[1] = quant_pair(y[5] * f[5], y[4] * f[4], a.i8) | (quant_pair(y[7] * f[7], y[6] * f[6], a.i8) << 16);
-        st<8>(q + c0, v);
-    } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = tile_col<VEC>(base, lane, j);
-            if (c < a.cols) q[c] = static_cast<uint8_t>(quant_pair(0.0f, y[j] * f[j], a.i8));
+            const int c = c0 + j * 32;
+            if (c < a.cols) q[c] = static_cast<uint8_t>(quant_pair(both(v[j] * f[j]), i8));
         }
     }
 }
@@ -123,41 +135,32 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024) norm_kernel(NormArgs a) {
     const void *res = a.residual ? row_of<DT>(a.residual, row, a.residual_stride) : nullptr;
     void *h = a.h ? row_of<DT>(a.h, row, a.h_stride) : nullptr;
     const int tiles = (a.cols + kTileCols - 1) / kTileCols;
-    const float qmax = a.i8 ? 127.0f : 448.0f;
 
-    auto sum_of = [&](int base, float (&f)[8]) {
-        unpack8<DT>(load_tile<DT, VEC>(x, base, a.cols, lane), f);
-        if (res) {
-            float g[8];
-            unpack8<DT>(load_tile<DT, VEC>(res, base, a.cols, lane), g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] += g[j];
-        }
-    };
-    auto scaled = [&](int base, float r, const float (&f)[8], float (&y)[8]) {
+    auto scaled = [&](int base, float r, const float2 (&f)[4], float2 (&y)[4]) {
         load_weight<DT, VEC>(a.weight, a.weight_f32, base, a.cols, lane, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= f[j] * r;
+        for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], mul2(f[j], both(r)));
     };
-    auto put = [&](int base, const float (&y)[8], float row_factor) {
+    auto put = [&](int base, const float2 (&y)[4], float row_factor) {
         if constexpr (QUANT) quant_tile<VEC>(y, a, row, base, lane, row_factor);
         else store_tile<DT, VEC>(row_of<DT>(a.out, row, a.out_stride), base, a.cols, lane, pack8<DT>(y));
     };
-    auto rstd_of = [&](float ss) {
-        const float r = __frsqrt_rn(ss / static_cast<float>(a.cols) + a.eps);
+    auto rstd_of = [&](float2 ss) {
+        const float r = __frsqrt_rn(block_sum(ss.x + ss.y, warps, part[0]) / static_cast<float>(a.cols) + a.eps);
         if (threadIdx.x == 0 && a.rstd) a.rstd[row] = r;
         return r;
     };
     auto row_scale = [&](float amax) {
         float scale;
-        const float factor = quant_factor(amax, qmax, &scale);
+        const float factor = quant_factor(block_max_nan(amax, warps, part[1]), a.i8, &scale);
         if (threadIdx.x == 0) a.scales[row * a.scales_stride] = scale;
         return factor;
     };
 
-    float ss = 0.0f;
+    float2 ss = both(0.0f);
+    float amax = 0.0f, factor = 0.0f;
     if constexpr (HELD) {
-        float f[KT][8];
+        float2 f[KT][4];
         Raw8<DT> rx[KT], rr[KT];
 #pragma unroll
         for (int k = 0; k < KT; ++k) rx[k] = load_tile<DT, VEC>(x, (warp + k * warps) * kTileCols, a.cols, lane);
@@ -169,58 +172,65 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024) norm_kernel(NormArgs a) {
         for (int k = 0; k < KT; ++k) {
             unpack8<DT>(rx[k], f[k]);
             if (res) {
-                float g[8];
+                float2 g[4];
                 unpack8<DT>(rr[k], g);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[k][j] += g[j];
+                for (int j = 0; j < 4; ++j) f[k][j] = add2(f[k][j], g[j]);
             }
             if (h) store_tile<DT, VEC>(h, (warp + k * warps) * kTileCols, a.cols, lane, pack8<DT>(f[k]));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(f[k][j], f[k][j], ss);
+            for (int j = 0; j < 4; ++j) ss = fma2(f[k][j], f[k][j], ss);
         }
-        const float r = rstd_of(block_sum(ss, warps, part[0]));
-        float amax = 0.0f, factor = 0.0f;
+        const float r = rstd_of(ss);
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            float y[8];
-            scaled((warp + k * warps) * kTileCols, r, f[k], y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[k][j] = y[j];
-        }
-        if (QUANT && a.group == 0) {
-#pragma unroll
-            for (int k = 0; k < KT; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(f[k][j]));
-            factor = row_scale(block_max_nan(amax, warps, part[1]));
-        }
-#pragma unroll
-        for (int k = 0; k < KT; ++k) {
+            float2 y[4];
             const int base = (warp + k * warps) * kTileCols;
-            if (base < a.cols) put(base, f[k], factor);
+            scaled(base, r, f[k], y);
+            if (QUANT && a.group_shift == 0) {
+                amax = max_nan(amax, largest_of(y));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[k][j] = y[j];
+            } else if (base < a.cols) {
+                put(base, y, 0.0f);
+            }
+        }
+        if (QUANT && a.group_shift == 0) {
+            factor = row_scale(amax);
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                const int base = (warp + k * warps) * kTileCols;
+                if (base < a.cols) put(base, f[k], factor);
+            }
         }
     } else {
+        auto sum_of = [&](int base, float2 (&f)[4]) {
+            unpack8<DT>(load_tile<DT, VEC>(x, base, a.cols, lane), f);
+            if (res) {
+                float2 g[4];
+                unpack8<DT>(load_tile<DT, VEC>(res, base, a.cols, lane), g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
+            }
+        };
         for (int t = warp; t < tiles; t += warps) {
-            float f[8];
+            float2 f[4];
             sum_of(t * kTileCols, f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
+            for (int j = 0; j < 4; ++j) ss = fma2(f[j], f[j], ss);
         }
-        const float r = rstd_of(block_sum(ss, warps, part[0]));
-        float factor = 0.0f;
-        if (QUANT && a.group == 0) {
-            float amax = 0.0f;
+        const float r = rstd_of(ss);
+        if (QUANT && a.group_shift == 0) {
             for (int t = warp; t < tiles; t += warps) {
-                float f[8], y[8];
+                float2 f[4], y[4];
                 sum_of(t * kTileCols, f);
                 scaled(t * kTileCols, r, f, y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(y[j]));
+                amax = max_nan(amax, largest_of(y));
             }
-            factor = row_scale(block_max_nan(amax, warps, part[1]));
+            factor = row_scale(amax);
         }
         for (int t = warp; t < tiles; t += warps) {
-            float f[8], y[8];
+            float2 f[4], y[4];
             sum_of(t * kTileCols, f);
             if (h) store_tile<DT, VEC>(h, t * kTileCols, a.cols, lane, pack8<DT>(f));
             scaled(t * kTileCols, r, f, y);
@@ -233,23 +243,35 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024) norm_kernel(NormArgs a) {
 // dx = r * (g - n * c) + dh.  Blocks walk over rows (row, row + writers, ..)
 // and keep their columns' sums of dy * n in registers; each writes them once,
 // to its own row of `partial`, and dweight_kernel adds those rows in order.
-template <int DT, bool VEC, int KT>
-__global__ void __launch_bounds__(512) norm_grad_kernel(NormGradArgs a) {
+//
+// AHEAD, for rows that 8 warps hold: a row's loads are issued while the row
+// before is worked on, and the weights stay in registers.  With two blocks of
+// 256 threads and 4096 bf16 columns an SM has about 96 KiB in flight.  Wider
+// rows have no registers left for either.
+template <int DT, bool VEC, int KT, bool AHEAD>
+__global__ void __launch_bounds__(AHEAD ? 256 : 512, AHEAD && KT * ElemOf<DT>::kBytes <= 4 ? 2 : 1)
+    norm_grad_kernel(NormGradArgs a) {
     enter_grid();
     __shared__ float part[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t writer = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     const int64_t writers = static_cast<int64_t>(gridDim.x) * blockDim.y;
-    float dw[KT][8];
+    float2 dw[KT][4], held[AHEAD ? KT : 1][4];
+    auto weight = [&](int k, float2 (&w)[4]) {
+        load_weight<DT, VEC>(a.weight, a.weight_f32, (warp + k * warps) * kTileCols, a.cols, lane, w);
+    };
 #pragma unroll
-    for (int k = 0; k < KT; ++k)
+    for (int k = 0; k < KT; ++k) {
+        if constexpr (AHEAD) weight(k, held[k]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[k][j] = 0.0f;
-    int turn = 0;
-    for (int64_t row = writer; row < a.rows; row += writers, turn ^= 1) {
+        for (int j = 0; j < 4; ++j) dw[k][j] = both(0.0f);
+    }
+    const float per_col = 1.0f / static_cast<float>(a.cols);
+    Raw8<DT> rdy[KT], rh[KT], rdh[KT];
+    float r = 0.0f;
+    auto fetch = [&](int64_t row) {
         const void *dy = row_of<DT>(a.dy, row, a.dy_stride), *h = row_of<DT>(a.h, row, a.h_stride);
-        const float r = a.rstd[row];
-        Raw8<DT> rdy[KT], rh[KT], rdh[KT];
+        r = a.rstd[row];
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             rdy[k] = load_tile<DT, VEC>(dy, (warp + k * warps) * kTileCols, a.cols, lane);
@@ -260,38 +282,54 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
             for (int k = 0; k < KT; ++k) rdh[k] = load_tile<DT, VEC>(dh, (warp + k * warps) * kTileCols, a.cols, lane);
         }
-        // dy and n of a tile, and its weights, read again from L1 rather than held
-        auto products = [&](int k, float (&g)[8], float (&n)[8]) {
-            float w[8];
-            load_weight<DT, VEC>(a.weight, a.weight_f32, (warp + k * warps) * kTileCols, a.cols, lane, w);
-            unpack8<DT>(rdy[k], g);
-            unpack8<DT>(rh[k], n);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) n[j] *= r;
-            return [&, w](int j) { return w[j]; };
-        };
-        float c = 0.0f;
+    };
+    int turn = 0;
+    if (AHEAD && writer < a.rows) fetch(writer);
+    for (int64_t row = writer; row < a.rows; row += writers, turn ^= 1) {
+        Raw8<DT> cdy[KT], ch[KT], cdh[KT];
+        if constexpr (!AHEAD) fetch(row);
+        const float cr = r;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            float g[8], n[8];
-            auto w = products(k, g, n);
+            cdy[k] = rdy[k];
+            ch[k] = rh[k];
+            cdh[k] = rdh[k];
+        }
+        if (AHEAD && row + writers < a.rows) fetch(row + writers);
+        float2 c2 = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dw[k][j] = fmaf(g[j], n[j], dw[k][j]);
-                c = fmaf(g[j] * w(j), n[j], c);
+        for (int k = 0; k < KT; ++k) {
+            float2 g[4], n[4], w[4];
+            if constexpr (!AHEAD) weight(k, w);
+            unpack8<DT>(cdy[k], g);
+            unpack8<DT>(ch[k], n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (AHEAD) w[j] = held[k][j];
+                n[j] = mul2(n[j], both(cr));
+                dw[k][j] = fma2(g[j], n[j], dw[k][j]);
+                c2 = fma2(mul2(g[j], w[j]), n[j], c2);
             }
         }
-        c = block_sum(c, warps, part[turn]) / static_cast<float>(a.cols);
+        const float c = block_sum(c2.x + c2.y, warps, part[turn]) * per_col;
+        const float2 minus_c = both(-c), r2 = both(cr);
         void *dx = row_of<DT>(a.dx, row, a.dx_stride);
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            float g[8], n[8], d[8];
-            auto w = products(k, g, n);
-            if (a.dh) unpack8<DT>(rdh[k], d);
+            float2 g[4], n[4], w[4], d[4];
+            if constexpr (!AHEAD) weight(k, w);
+            unpack8<DT>(cdy[k], g);
+            unpack8<DT>(ch[k], n);
+            if (a.dh) {
+                unpack8<DT>(cdh[k], d);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float v = fmaf(-c, n[j], g[j] * w(j));
-                d[j] = a.dh ? fmaf(r, v, d[j]) : r * v;
+                for (int j = 0; j < 4; ++j) d[j] = both(0.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (AHEAD) w[j] = held[k][j];
+                d[j] = fma2(r2, fma2(minus_c, mul2(n[j], r2), mul2(g[j], w[j])), d[j]);
             }
             store_tile<DT, VEC>(dx, (warp + k * warps) * kTileCols, a.cols, lane, pack8<DT>(d));
         }
@@ -299,12 +337,20 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormGradArgs a) {
     if (a.dweight == nullptr) return;
     float *out = a.partial + writer * a.cols;
 #pragma unroll
-    for (int k = 0; k < KT; ++k)
+    for (int k = 0; k < KT; ++k) {
+        const int base = (warp + k * warps) * kTileCols, c0 = tile_col<VEC>(base, lane, 0);
+        if (VEC && c0 + 8 <= a.cols && a.cols % 4 == 0) {
+            float4 *p = reinterpret_cast<float4 *>(out + c0);
+            p[0] = make_float4(dw[k][0].x, dw[k][0].y, dw[k][1].x, dw[k][1].y);
+            p[1] = make_float4(dw[k][2].x, dw[k][2].y, dw[k][3].x, dw[k][3].y);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int col = tile_col<VEC>((warp + k * warps) * kTileCols, lane, j);
-            if (col < a.cols) out[col] = dw[k][j];
+            for (int j = 0; j < 8; ++j) {
+                const int col = tile_col<VEC>(base, lane, j);
+                if (col < a.cols) out[col] = (j & 1) ? dw[k][j / 2].y : dw[k][j / 2].x;
+            }
         }
+    }
 }
 
 // Rows too wide to hold: the row's two passes read it twice.  dweight has its
@@ -318,34 +364,31 @@ __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(NormGradArgs a) {
     const int tiles = (a.cols + kTileCols - 1) / kTileCols;
     const void *dy = row_of<DT>(a.dy, row, a.dy_stride), *h = row_of<DT>(a.h, row, a.h_stride);
     const float r = a.rstd[row];
-    auto products = [&](int base, float (&g)[8], float (&n)[8]) {
-        float w[8];
+    auto products = [&](int base, float2 (&g)[4], float2 (&n)[4]) {
+        float2 w[4];
         load_weight<DT, VEC>(a.weight, a.weight_f32, base, a.cols, lane, w);
         unpack8<DT>(load_tile<DT, VEC>(dy, base, a.cols, lane), g);
         unpack8<DT>(load_tile<DT, VEC>(h, base, a.cols, lane), n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            n[j] *= r;
-            g[j] *= w[j];
+        for (int j = 0; j < 4; ++j) {
+            n[j] = mul2(n[j], both(r));
+            g[j] = mul2(g[j], w[j]);
         }
     };
-    float c = 0.0f, g[8], n[8];
+    float2 c2 = both(0.0f), g[4], n[4];
     for (int t = warp; t < tiles; t += warps) {
         products(t * kTileCols, g, n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c = fmaf(g[j], n[j], c);
+        for (int j = 0; j < 4; ++j) c2 = fma2(g[j], n[j], c2);
     }
-    c = block_sum(c, warps, part) / static_cast<float>(a.cols);
+    const float c = block_sum(c2.x + c2.y, warps, part) / static_cast<float>(a.cols);
     void *dx = row_of<DT>(a.dx, row, a.dx_stride);
     for (int t = warp; t < tiles; t += warps) {
         products(t * kTileCols, g, n);
-        float d[8];
+        float2 d[4] = {};
         if (a.dh) unpack8<DT>(load_tile<DT, VEC>(row_of<DT>(a.dh, row, a.dh_stride), t * kTileCols, a.cols, lane), d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float v = fmaf(-c, n[j], g[j]);
-            d[j] = a.dh ? fmaf(r, v, d[j]) : r * v;
-        }
+        for (int j = 0; j < 4; ++j) d[j] = fma2(both(r), fma2(both(-c), n[j], g[j]), d[j]);
         store_tile<DT, VEC>(dx, t * kTileCols, a.cols, lane, pack8<DT>(d));
     }
 }
@@ -358,20 +401,20 @@ __global__ void __launch_bounds__(256) norm_dweight_wide_kernel(NormGradArgs a) 
     const int lane = threadIdx.x & 31;
     const int base = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kTileCols;
     if (base >= a.cols) return;
-    float dw[8] = {};
+    float2 dw[4] = {};
     for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-        float g[8], n[8];
+        float2 g[4], n[4];
         const float r = a.rstd[row];
         unpack8<DT>(load_tile<DT, VEC>(row_of<DT>(a.dy, row, a.dy_stride), base, a.cols, lane), g);
         unpack8<DT>(load_tile<DT, VEC>(row_of<DT>(a.h, row, a.h_stride), base, a.cols, lane), n);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[j] = fmaf(g[j], n[j] * r, dw[j]);
+        for (int j = 0; j < 4; ++j) dw[j] = fma2(g[j], mul2(n[j], both(r)), dw[j]);
     }
     float *out = a.partial + static_cast<int64_t>(blockIdx.y) * a.cols;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int col = tile_col<VEC>(base, lane, j);
-        if (col < a.cols) out[col] = dw[j];
+        if (col < a.cols) out[col] = (j & 1) ? dw[j / 2].y : dw[j / 2].x;
     }
 }
 
@@ -429,23 +472,28 @@ template <int DT, bool VEC>
 cudaError_t norm_grad_launch(const NormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
                              int *launches) {
     const int tiles = (a.cols + kTileCols - 1) / kTileCols;
-    const int kt = tiles_per_thread(tiles, kHeldWarps, DT == DT_F32 ? 2 : 4);
+    constexpr int most = DT == DT_F32 ? 2 : 4;
+    int kt = tiles_per_thread(tiles, 8, most);
+    const bool ahead = kt != 0;
+    if (!ahead) kt = tiles_per_thread(tiles, kGradWarps, most);
     info->vec_bytes = VEC ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
     int64_t writers = 0;
     cudaError_t e = cudaSuccess;
     if (a.rows > 0 && kt != 0) {
         const int warps = (tiles + kt - 1) / kt;
         const int per_block = warps == 1 && a.rows >= 4 * static_cast<int64_t>(sms) ? 4 : 1;
-        const int resident = std::max(1, 16 / (warps * per_block));  // blocks that 512 threads of an SM make
+        const int resident = std::max(1, 16 / (warps * per_block));  // blocks that make 512 threads an SM
         const int64_t grid = std::min<int64_t>({(a.rows + per_block - 1) / per_block,
                                                 static_cast<int64_t>(sms) * resident, most_writers / per_block});
         writers = grid * per_block;
         const dim3 block(32 * warps, per_block);
         info->grid = static_cast<int>(grid);
         info->block = 32 * warps * per_block;
-        e = kt == 1   ? launch_rows(norm_grad_kernel<DT, VEC, 1>, dim3(grid), block, 0, 1, s, a)
-            : kt == 2 ? launch_rows(norm_grad_kernel<DT, VEC, 2>, dim3(grid), block, 0, 1, s, a)
-                      : launch_rows(norm_grad_kernel<DT, VEC, 4>, dim3(grid), block, 0, 1, s, a);
+        auto kernel = norm_grad_kernel<DT, VEC, 1, true>;
+        if (kt == 2) kernel = ahead ? norm_grad_kernel<DT, VEC, 2, true> : norm_grad_kernel<DT, VEC, 2, false>;
+        if constexpr (most == 4)
+            if (kt == 4) kernel = ahead ? norm_grad_kernel<DT, VEC, 4, true> : norm_grad_kernel<DT, VEC, 4, false>;
+        e = launch_rows(kernel, dim3(grid), block, 0, 1, s, a);
         ++*launches;
     } else if (a.rows > 0) {
         if (a.dweight) {

@@ -31,24 +31,67 @@ template <int DT> __device__ __forceinline__ typename ElemOf<DT>::type f32_to_el
     else return f32_to_bf16(f);
 }
 
+// Two binary32 values in one instruction each (the sm_100 family's f32x2 forms).
+__device__ __forceinline__ uint64_t pair_bits(float2 a) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a.x), "f"(a.y));
+    return d;
+}
+__device__ __forceinline__ float2 pair_of(uint64_t d) {
+    float2 a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(d));
+    return a;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// The two 16-bit elements of a word, and back, rounded.
+template <int DT> __device__ __forceinline__ float2 widen(uint32_t w) {
+    if constexpr (DT == DT_F16)
+        return make_float2(f16_to_f32(static_cast<uint16_t>(w)), f16_to_f32(static_cast<uint16_t>(w >> 16)));
+    else
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <int DT> __device__ __forceinline__ uint32_t narrow(float2 a) {
+    if constexpr (DT == DT_F16) return f32x2_to_f16x2(a.y, a.x);
+    else return f32x2_to_bf16x2(a.y, a.x);
+}
+
 // 8 elements as they lie in memory (16-bit elements two to a word).
 template <int DT> struct Raw8 { uint32_t w[ElemOf<DT>::kWords]; };
 
-template <int DT> __device__ __forceinline__ void unpack8(const Raw8<DT> &r, float (&f)[8]) {
+// The same as 4 pairs.
+template <int DT> __device__ __forceinline__ void unpack8(const Raw8<DT> &r, float2 (&f)[4]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if constexpr (DT == DT_F32) f[j] = __uint_as_float(r.w[j]);
-        else if constexpr (DT == DT_F16) f[j] = f16_to_f32(static_cast<uint16_t>(r.w[j / 2] >> (16 * (j & 1))));
-        else f[j] = __uint_as_float((j & 1) ? (r.w[j / 2] & 0xffff0000u) : (r.w[j / 2] << 16));
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == DT_F32) f[j] = make_float2(__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1]));
+        else f[j] = widen<DT>(r.w[j]);
     }
 }
-template <int DT> __device__ __forceinline__ Raw8<DT> pack8(const float (&f)[8]) {
+template <int DT> __device__ __forceinline__ Raw8<DT> pack8(const float2 (&f)[4]) {
     Raw8<DT> r;
 #pragma unroll
-    for (int j = 0; j < ElemOf<DT>::kWords; ++j) {
-        if constexpr (DT == DT_F32) r.w[j] = __float_as_uint(f[j]);
-        else if constexpr (DT == DT_F16) r.w[j] = f32x2_to_f16x2(f[2 * j + 1], f[2 * j]);
-        else r.w[j] = f32x2_to_bf16x2(f[2 * j + 1], f[2 * j]);
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == DT_F32) {
+            r.w[2 * j] = __float_as_uint(f[j].x);
+            r.w[2 * j + 1] = __float_as_uint(f[j].y);
+        } else {
+            r.w[j] = narrow<DT>(f[j]);
+        }
     }
     return r;
 }
@@ -107,34 +150,41 @@ __device__ __forceinline__ void store_tile(void *row, int base, int cols, int la
 
 // The same 8 columns of a vector that every row reads again (cached in L1), in
 // binary32; its type is the matrix's or binary32, one for the whole launch.
-// Null stands for ones.
+// Null stands for ones; columns from `cols` on are zero.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load_weight(const void *w, bool f32, int base, int cols, int lane, float (&f)[8]) {
+__device__ __forceinline__ void load_weight(const void *w, bool f32, int base, int cols, int lane, float2 (&f)[4]) {
     const int c0 = tile_col<VEC>(base, lane, 0);
     if (w == nullptr) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = 1.0f;
+        for (int j = 0; j < 4; ++j) f[j] = both(1.0f);
     } else if (VEC && c0 + 8 <= cols) {
         if (DT == DT_F32 || f32) {
             const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + c0);
             const float4 a = q[0], b = q[1];
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+            f[0] = make_float2(a.x, a.y);
+            f[1] = make_float2(a.z, a.w);
+            f[2] = make_float2(b.x, b.y);
+            f[3] = make_float2(b.z, b.w);
         } else if constexpr (DT != DT_F32) {
             const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + c0);
-            const Raw8<DT> r = {{a.x, a.y, a.z, a.w}};
-            unpack8<DT>(r, f);
+            f[0] = widen<DT>(a.x);
+            f[1] = widen<DT>(a.y);
+            f[2] = widen<DT>(a.z);
+            f[3] = widen<DT>(a.w);
         }
     } else {
+        float e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = tile_col<VEC>(base, lane, j);
-            f[j] = 0.0f;
+            e[j] = 0.0f;
             if (c < cols) {
-                if (DT == DT_F32 || f32) f[j] = static_cast<const float *>(w)[c];
-                else f[j] = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(w)[c]);
+                if (DT == DT_F32 || f32) e[j] = static_cast<const float *>(w)[c];
+                else e[j] = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(w)[c]);
             }
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = make_float2(e[2 * j], e[2 * j + 1]);
     }
 }
 
@@ -150,6 +200,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float largest_of(const float2 (&y)[4]) {  // by absolute value
+    const float m = max_nan(fabsf(y[0].x), fabsf(y[0].y), fabsf(y[1].x));
+    const float n = max_nan(fabsf(y[1].y), fabsf(y[2].x), fabsf(y[2].y));
+    return max_nan(max_nan(m, fabsf(y[3].x), fabsf(y[3].y)), n);
 }
 // Largest over the `width` lanes (a power of two) around this one.
 __device__ __forceinline__ float lanes_max_nan(float v, int width) {

@@ -63,7 +63,7 @@ struct NormArgs {
     int64_t x_stride, residual_stride, out_stride, h_stride, scales_stride;
     int64_t rows;
     int32_t cols;
-    int32_t group;    // columns a scale; 0: the row
+    int32_t group_shift;  // log2 of the columns a scale; 0: the row
     float eps;
     int32_t weight_f32;
     int32_t i8;       // 8-bit forms: int8 instead of e4m3
