@@ -20,37 +20,39 @@ namespace {
 constexpr int kGradWarps = 16;  // most warps that hold a row in the backward
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100: a scale is never zero
 
-__device__ __forceinline__ uint32_t quant_pair(float2 v, bool i8) {
-    if (i8) {
+enum Quant : int { kPlain = 0, kE4m3 = 1, kI8 = 2 };  // what a norm kernel writes
+
+template <int QUANT> __device__ __forceinline__ uint32_t quant_pair(float2 v) {
+    if constexpr (QUANT == kI8) {
         int32_t a, b;
         asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(a) : "f"(v.x));
         asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(b) : "f"(v.y));
         return (a & 0xff) | ((b & 0xff) << 8);
+    } else {
+        uint16_t d;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(v.y), "f"(v.x));
+        return d;
     }
-    uint16_t d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(v.y), "f"(v.x));
-    return d;
 }
 
 // Scale of a group whose largest absolute value is amax, and the factor that
 // takes y to q.  Products with reciprocals: within two roundings of the
 // quotients, which moves a q only where y / scale all but ties.
-__device__ __forceinline__ float quant_factor(float amax, bool i8, float *scale) {
+template <int QUANT> __device__ __forceinline__ float quant_factor(float amax, float *scale) {
     amax = max_nan(amax, kAmaxFloor);
-    *scale = amax * (i8 ? 1.0f / 127.0f : 1.0f / 448.0f);
+    *scale = amax * (QUANT == kI8 ? 1.0f / 127.0f : 1.0f / 448.0f);
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(amax));
-    return r * (i8 ? 127.0f : 448.0f);
+    return r * (QUANT == kI8 ? 127.0f : 448.0f);
 }
 
 // Quantises the lane's 8 values of y of one tile and stores them, with the
 // group's scales.  Every lane of the warp takes part.
-template <bool VEC>
+template <int QUANT, bool VEC>
 __device__ __forceinline__ void quant_tile(const float2 (&y)[4], const NormArgs &a, int64_t row, int base, int lane,
                                            float row_factor) {
     uint8_t *q = static_cast<uint8_t *>(a.out) + row * a.out_stride;
     const int shift = a.group_shift;  // log2 of the group, 0: the row
-    const bool i8 = a.i8;
     const int c0 = tile_col<VEC>(base, lane, 0);
     if constexpr (VEC) {
         float factor = row_factor;
@@ -62,13 +64,13 @@ __device__ __forceinline__ void quant_tile(const float2 (&y)[4], const NormArgs 
             if (shift > 6) m = max_nan(m, __shfl_xor_sync(kAllLanes, m, 8));
             if (shift > 7) m = max_nan(m, __shfl_xor_sync(kAllLanes, m, 16));
             float scale;
-            factor = quant_factor(m, i8, &scale);
+            factor = quant_factor<QUANT>(m, &scale);
             if ((lane << 3 & ((1 << shift) - 1)) == 0 && c0 < a.cols)
                 a.scales[row * a.scales_stride + (c0 >> shift)] = scale;
         }
         const float2 f = both(factor);
-        const uint32_t q0 = quant_pair(mul2(y[0], f), i8), q1 = quant_pair(mul2(y[1], f), i8);
-        const uint32_t q2 = quant_pair(mul2(y[2], f), i8), q3 = quant_pair(mul2(y[3], f), i8);
+        const uint32_t q0 = quant_pair<QUANT>(mul2(y[0], f)), q1 = quant_pair<QUANT>(mul2(y[1], f));
+        const uint32_t q2 = quant_pair<QUANT>(mul2(y[2], f)), q3 = quant_pair<QUANT>(mul2(y[3], f));
         Vec<8> v;
         v.w[0] = q0 | (q1 << 16);
         v.w[1] = q2 | (q3 << 16);
@@ -105,7 +107,7 @@ __device__ __forceinline__ void quant_tile(const float2 (&y)[4], const NormArgs 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 float scale;
-                f[j] = quant_factor(f[j], i8, &scale);
+                f[j] = quant_factor<QUANT>(f[j], &scale);
                 const int c = base + j * 32;
                 if (lane == 0 && (c & ((1 << shift) - 1)) == 0 && c < a.cols)
                     a.scales[row * a.scales_stride + (c >> shift)] = scale;
@@ -114,7 +116,7 @@ __device__ __forceinline__ void quant_tile(const float2 (&y)[4], const NormArgs 
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = c0 + j * 32;
-            if (c < a.cols) q[c] = static_cast<uint8_t>(quant_pair(both(v[j] * f[j]), i8));
+            if (c < a.cols) q[c] = static_cast<uint8_t>(quant_pair<QUANT>(both(v[j] * f[j])));
         }
     }
 }
@@ -124,8 +126,9 @@ __device__ __forceinline__ void quant_tile(const float2 (&y)[4], const NormArgs 
 // warps x KT tiles cover the row, which stays in registers.  Otherwise (rows
 // beyond 16 warps x 4 tiles) the passes read the row again, each thread its
 // own elements, and h is written by the last pass, so in-place forms hold.
-template <int DT, bool VEC, int KT, bool QUANT, bool HELD>
-__global__ void __launch_bounds__(HELD ? 512 : 1024) norm_kernel(NormArgs a) {
+template <int DT, bool VEC, int KT, int QUANT, bool HELD>
+__global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && VEC && KT * ElemOf<DT>::kBytes <= 8 ? 2 : 1)
+    norm_kernel(NormArgs a) {
     enter_grid();
     __shared__ float part[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -142,17 +145,17 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024) norm_kernel(NormArgs a) {
         for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], mul2(f[j], both(r)));
     };
     auto put = [&](int base, const float2 (&y)[4], float row_factor) {
-        if constexpr (QUANT) quant_tile<VEC>(y, a, row, base, lane, row_factor);
+        if constexpr (QUANT != kPlain) quant_tile<QUANT, VEC>(y, a, row, base, lane, row_factor);
         else store_tile<DT, VEC>(row_of<DT>(a.out, row, a.out_stride), base, a.cols, lane, pack8<DT>(y));
     };
     auto rstd_of = [&](float2 ss) {
-        const float r = __frsqrt_rn(block_sum(ss.x + ss.y, warps, part[0]) / static_cast<float>(a.cols) + a.eps);
+        const float r = rsqrtf(fmaf(block_sum(ss.x + ss.y, warps, part[0]), a.per_col, a.eps));
         if (threadIdx.x == 0 && a.rstd) a.rstd[row] = r;
         return r;
     };
     auto row_scale = [&](float amax) {
         float scale;
-        const float factor = quant_factor(block_max_nan(amax, warps, part[1]), a.i8, &scale);
+        const float factor = quant_factor<QUANT>(block_max_nan(amax, warps, part[1]), &scale);
         if (threadIdx.x == 0) a.scales[row * a.scales_stride] = scale;
         return factor;
     };
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024) norm_kernel(NormArgs a) {
             float2 y[4];
             const int base = (warp + k * warps) * kTileCols;
             scaled(base, r, f[k], y);
-            if (QUANT && a.group_shift == 0) {
+            if (QUANT != kPlain && a.group_shift == 0) {
                 amax = max_nan(amax, largest_of(y));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[k][j] = y[j];
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024) norm_kernel(NormArgs a) {
                 put(base, y, 0.0f);
             }
         }
-        if (QUANT && a.group_shift == 0) {
+        if (QUANT != kPlain && a.group_shift == 0) {
             factor = row_scale(amax);
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024) norm_kernel(NormArgs a) {
             for (int j = 0; j < 4; ++j) ss = fma2(f[j], f[j], ss);
         }
         const float r = rstd_of(ss);
-        if (QUANT && a.group_shift == 0) {
+        if (QUANT != kPlain && a.group_shift == 0) {
             for (int t = warp; t < tiles; t += warps) {
                 float2 f[4], y[4];
                 sum_of(t * kTileCols, f);
@@ -434,13 +437,18 @@ template <int DT> bool wide_weight(const void *w, bool f32) {
     return reinterpret_cast<uintptr_t>(w) % (f32 || DT == DT_F32 ? 32 : 16) == 0;
 }
 
-template <int DT, bool VEC, bool QUANT>
+template <int DT, bool VEC, int QUANT>
 cudaError_t norm_launch(const NormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
     const int tiles = (a.cols + kTileCols - 1) / kTileCols;
-    // One tile a thread where rows are few (the row's latency counts), up to
-    // four where they are many.
+    // Few rows: as few tiles a thread as 16 warps allow, for the row's latency.
+    // Many: two tiles a thread, and four for 16-bit rows past 2048 columns,
+    // where blocks are small enough that four of them share an SM and cover
+    // one another's waits.  e4m3 of 2^26 bf16 at 8192 columns: 4 tiles 79 us,
+    // 2 tiles 88 us; at 1024: 77 and 75 us, 1 tile 92 us.  binary32 at 4096:
+    // 4, 2 and 1 tiles 126, 125 and 123 us.
     const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
-    const int kt = tiles_per_thread(tiles, many ? std::min(kHeldWarps, std::max(1, (tiles + 1) / 2)) : kHeldWarps, 4);
+    int kt = tiles_per_thread(tiles, kHeldWarps, 4);
+    if (many && kt != 0) kt = std::max(kt, tiles == 1 ? 1 : DT != DT_F32 && tiles > 8 ? 4 : 2);
     int warps = 32, per_block = 1;
     if (kt != 0) {
         warps = (tiles + kt - 1) / kt;
@@ -464,8 +472,9 @@ template <int DT> cudaError_t norm_dispatch(bool quant, const NormArgs &a, int s
                                 : wide_rows<DT>(a.out, a.out_stride);
     const bool vec = out_wide && wide_rows<DT>(a.x, a.x_stride) && wide_rows<DT>(a.residual, a.residual_stride) &&
                      wide_rows<DT>(a.h, a.h_stride) && wide_weight<DT>(a.weight, a.weight_f32);
-    if (quant) return vec ? norm_launch<DT, true, true>(a, sms, s, info) : norm_launch<DT, false, true>(a, sms, s, info);
-    return vec ? norm_launch<DT, true, false>(a, sms, s, info) : norm_launch<DT, false, false>(a, sms, s, info);
+    if (!quant) return vec ? norm_launch<DT, true, kPlain>(a, sms, s, info) : norm_launch<DT, false, kPlain>(a, sms, s, info);
+    if (a.i8) return vec ? norm_launch<DT, true, kI8>(a, sms, s, info) : norm_launch<DT, false, kI8>(a, sms, s, info);
+    return vec ? norm_launch<DT, true, kE4m3>(a, sms, s, info) : norm_launch<DT, false, kE4m3>(a, sms, s, info);
 }
 
 template <int DT, bool VEC>

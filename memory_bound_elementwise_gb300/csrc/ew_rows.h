@@ -64,7 +64,7 @@ struct NormArgs {
     int64_t rows;
     int32_t cols;
     int32_t group_shift;  // log2 of the columns a scale; 0: the row
-    float eps;
+    float eps, per_col;   // per_col: 1 / cols
     int32_t weight_f32;
     int32_t i8;       // 8-bit forms: int8 instead of e4m3
 };

@@ -121,6 +121,7 @@ ew_status norm_call(ew_dtype dt, const void *x, int64_t x_stride, const void *re
     if (ce != cudaSuccess) return report_cuda(ce);
     const NormArgs a{x, residual, weight, out, h_out, rstd_out, scales, x_stride, residual_stride, out_stride,
                      h_stride, scales_stride, rows, static_cast<int32_t>(cols), group == 0 ? 0 : __builtin_ctzll(group), eps,
+                     1.0f / static_cast<float>(cols),
                      weight != nullptr && wtype == EW_F32, quant && qtype == EW_Q_I8};
     LaunchInfo info;
     ce = (dt == EW_F32 ? norm_f32 : dt == EW_F16 ? norm_f16 : norm_bf16)(quant, a, sms, s, &info);
