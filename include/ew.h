@@ -354,7 +354,7 @@ EW_API int64_t ew_rmsnorm_grad_workspace(int64_t rows, int64_t cols);
  *     top_ids, top_logp: the `top` (0 to 64) largest logits' columns and log p,
  *                largest first, equal ones by the lower column
  * logp, entropy and lse may each be NULL; tokens may be with logp.  A token
- * outside [0, cols) has logp 0.  0 < scale <= 2^20.  Logits of -inf are masked: p = 0, and
+ * outside [0, cols) has logp 0.  2^-20 <= scale <= 2^20.  Logits of -inf are masked: p = 0, and
  * they are no alternatives; where fewer than `top` are left, ids are -1 with
  * top_logp -inf.  The type's lowest value is a value like others: a row of
  * nothing else is uniform.  A row of -inf alone has lse and logp -inf and
@@ -380,7 +380,7 @@ EW_API ew_status ew_logprob_grad(ew_dtype dtype, ew_index itype, const void *log
  *     loss    = sum over entries of q (log q - log p[id])
  *     dlogits = dloss * scale * (p - q at its columns)
  *     lse     = log(sum exp(scale * logits))
- * scale is 1 / temperature, 0 < scale <= 2^20.  Entries with an id outside [0, cols) or a value
+ * scale is 1 / temperature, 2^-20 <= scale <= 2^20.  Entries with an id outside [0, cols) or a value
  * of -inf do not count; a row without any has loss 0 and gradient 0.  Entries
  * of one row with the same id stay terms of their own in the loss and add up
  * in the gradient.  Masked logits have p = 0; a teacher's

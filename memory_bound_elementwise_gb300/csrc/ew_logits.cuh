@@ -12,6 +12,11 @@
 // type's lowest value) finite: they add 2^-huge = 0 to both sums.  A row for
 // which this does not hold a sum (only masked elements, NaN, infinities,
 // values past +-1e6 / scale) is summed again by careful_row().
+//
+// What bounds these kernels is the rate at which instructions issue as much as
+// memory: a bf16 element arrives in 1/8 ns an SM, in which four schedulers
+// issue about 7 instructions for 32 of them.  So maxima and the bound by kLeast
+// work on packed pairs, and products and sums on pairs of binary32.
 #pragma once
 
 #include <algorithm>
@@ -23,10 +28,15 @@
 namespace ew {
 namespace {
 
-constexpr int kThreads = 512;
+// Four blocks of 256 threads share an SM, each thread with 8 chunks of 16 bytes
+// in flight: 128 KiB an SM when all of them wait, and blocks small enough that
+// some load while others reduce.
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kFlight = 4;             // 16-byte chunks a thread has in flight
-constexpr float kLeast = -1e30f;
+constexpr int kFlight = 8;
+constexpr int kResident = 4;
+constexpr int kTurn = kFlight * kThreads;  // chunks that a block takes at a time
+constexpr float kLeast = -1e12f;
 constexpr float kLeastExponent = -1048576.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -44,11 +54,57 @@ template <int DT> struct Chunk {  // 16 bytes of a row
 };
 template <int DT> __device__ __forceinline__ void unpack(const Chunk<DT> &r, float (&f)[Chunk<DT>::kElems]) {
 #pragma unroll
-    for (int j = 0; j < Chunk<DT>::kElems; ++j) {
-        if constexpr (DT == DT_F32) f[j] = __uint_as_float(r.w[j]);
-        else if constexpr (DT == DT_F16) f[j] = f16_to_f32(static_cast<uint16_t>(r.w[j / 2] >> (16 * (j & 1))));
-        else f[j] = __uint_as_float((j & 1) ? (r.w[j / 2] & 0xffff0000u) : (r.w[j / 2] << 16));
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (DT == DT_F32) {
+            f[j] = __uint_as_float(r.w[j]);
+        } else {
+            const float2 p = widen<DT>(r.w[j]);
+            f[2 * j] = p.x;
+            f[2 * j + 1] = p.y;
+        }
     }
+}
+// A word of masked elements.
+template <int DT> __device__ __forceinline__ uint32_t masked_word() {
+    return DT == DT_F32 ? 0xff800000u : DT == DT_F16 ? 0xfc00fc00u : 0xff80ff80u;
+}
+template <int DT> __device__ __forceinline__ Chunk<DT> masked_chunk() {
+    return Chunk<DT>{{masked_word<DT>(), masked_word<DT>(), masked_word<DT>(), masked_word<DT>()}};
+}
+// Largest of two words, element by element, NaN kept.
+template <int DT> __device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (DT == DT_F32) asm("max.NaN.f32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else if constexpr (DT == DT_F16) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <int DT> __device__ __forceinline__ float max_of_word(uint32_t w) {
+    if constexpr (DT == DT_F32) return __uint_as_float(w);
+    else {
+        const float2 p = widen<DT>(w);
+        return max_nan(p.x, p.y);
+    }
+}
+// The pair of elements in words w (and v for binary32), at least kLeast each.
+// bfloat16: the bound is applied to the packed pair, as -1e12 rounded to it.
+template <int DT> __device__ __forceinline__ float2 bounded(uint32_t w, uint32_t v) {
+    if constexpr (DT == DT_F32) {
+        return make_float2(fmaxf(__uint_as_float(w), kLeast), fmaxf(__uint_as_float(v), kLeast));
+    } else if constexpr (DT == DT_F16) {
+        const float2 p = widen<DT>(w);
+        return make_float2(fmaxf(p.x, kLeast), fmaxf(p.y, kLeast));
+    } else {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0xd369d369u));
+        return widen<DT>(d);
+    }
+}
+// Pair j of a chunk: 4 pairs of 16-bit elements, 2 of binary32.
+template <int DT> struct Pairs { static constexpr int kCount = DT == DT_F32 ? 2 : 4; };
+template <int DT> __device__ __forceinline__ float2 bounded_pair(const Chunk<DT> &r, int j) {
+    if constexpr (DT == DT_F32) return bounded<DT>(r.w[2 * j], r.w[2 * j + 1]);
+    else return bounded<DT>(r.w[j], 0u);
 }
 
 // A block's share of a row: whole 16-byte chunks from element `head` on, and
@@ -113,20 +169,49 @@ __device__ __forceinline__ Sums merged(Sums a, Sums b) {
     move_to(b, c);
     return {c, a.s + b.s, a.u + b.u, max_nan(a.top, b.top)};
 }
-template <int N> __device__ __forceinline__ void add_elements(Sums &v, const float (&x)[N], float a) {
-    float top = x[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) top = max_nan(top, x[j]);
-    v.top = max_nan(v.top, top);
-    const float c = fmaxf(ceilf(top * a), kLeastExponent);
+// One element.
+__device__ __forceinline__ void add_element(Sums &v, float x, float a) {
+    v.top = max_nan(v.top, x);
+    const float c = fmaxf(ceilf(x * a), kLeastExponent);
     if (c > v.c) move_to(v, c);
+    const float t = fmaf(fmaxf(x, kLeast), a, -v.c), e = ex2(t);
+    v.s += e;
+    v.u = fmaf(e, t, v.u);
+}
+// A thread's chunks; sums in two lanes of a pair each.  Returns the largest element.
+struct PairSums {
+    float c;
+    float2 s, u;
+    uint32_t top;  // a word of largest elements
+};
+template <int DT, bool ENTROPY>
+__device__ __forceinline__ float add_chunks(PairSums &v, const Chunk<DT> (&r)[kFlight], float a) {
+    uint32_t m = max_words<DT>(r[0].w[0], r[0].w[1]);
+    m = max_words<DT>(m, max_words<DT>(r[0].w[2], r[0].w[3]));
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        const float t = fmaf(fmaxf(x[j], kLeast), a, -v.c);
-        const float e = ex2(t);
-        v.s += e;
-        v.u = fmaf(e, t, v.u);
+    for (int k = 1; k < kFlight; ++k)
+        m = max_words<DT>(m, max_words<DT>(max_words<DT>(r[k].w[0], r[k].w[1]), max_words<DT>(r[k].w[2], r[k].w[3])));
+    v.top = max_words<DT>(v.top, m);
+    const float top = max_of_word<DT>(m);
+    const float c = fmaxf(ceilf(top * a), kLeastExponent);
+    if (c > v.c) {
+        const float d = v.c - c, f = ex2(d);
+        if (ENTROPY) v.u = mul2(both(f), fma2(v.s, both(d), v.u));
+        v.s = mul2(both(f), v.s);
+        v.c = c;
     }
+    const float2 scale = both(a), shift = both(-v.c);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+#pragma unroll
+        for (int j = 0; j < Pairs<DT>::kCount; ++j) {
+            const float2 t = fma2(bounded_pair<DT>(r[k], j), scale, shift);
+            const float2 e = make_float2(ex2(t.x), ex2(t.y));
+            v.s = add2(v.s, e);
+            if (ENTROPY) v.u = fma2(e, t, v.u);
+        }
+    }
+    return top;
 }
 __device__ __forceinline__ Sums warp_sums(Sums v) {
 #pragma unroll
@@ -144,6 +229,12 @@ __device__ __forceinline__ Sums block_sums(Sums v, Sums *part) {
     if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     return warp_sums(lane < kWarps ? part[lane] : no_sums());
+}
+
+// The sums of all blocks of the cluster, to every thread: lane b reads block b's.
+__device__ __forceinline__ Sums cluster_sums(const Sums *mine, int blocks) {
+    const int lane = threadIdx.x & 31;
+    return warp_sums(lane < blocks ? *in_block(mine, lane) : no_sums());
 }
 
 // What a row's elements are compared with: log p(x) = ln2 (a x - c) - log_s,
@@ -210,7 +301,7 @@ __device__ __forceinline__ RowSum finish_row(const Sums &v, const void *row, int
 // finds the k-th value by bisection instead.
 
 constexpr int kCandidates = 2048;
-constexpr int kGroups = kThreads / 4;
+constexpr int kGroups = 128;  // of two lanes each
 
 struct Candidate {
     float x;
@@ -221,7 +312,7 @@ __device__ __forceinline__ bool before(const Candidate &a, const Candidate &b) {
 }
 
 struct TopShared {
-    float group[kGroups];
+    alignas(16) float group[kGroups];
     float bound;
     int count;
     Candidate list[kCandidates];
@@ -233,6 +324,19 @@ __device__ __forceinline__ void collect(TopShared &t, float x, int id) {
     if (at < kCandidates) t.list[at] = {x, id};
 }
 
+// The elements of a chunk that reach the bound.  Out of line: it is rarely
+// run, and 8 copies of it in the loop would crowd the instruction cache.
+template <int DT>
+__device__ __noinline__ void collect_chunk(TopShared &t, uint4 w, int col, float bound) {
+    constexpr int V = Chunk<DT>::kElems;
+    const Chunk<DT> r = {{w.x, w.y, w.z, w.w}};
+    float f[V];
+    unpack<DT>(r, f);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (f[j] >= bound && f[j] > kNegInf) collect(t, f[j], col + j);
+}
+
 // The k best of n entries into best[0 .. k): the rank of an entry is the
 // number of entries before it.
 __device__ __forceinline__ void rank_list(const Candidate *list, int n, int k, Candidate *best) {
@@ -240,6 +344,7 @@ __device__ __forceinline__ void rank_list(const Candidate *list, int n, int k, C
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const Candidate mine = list[i];
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) rank += before(list[j], mine) ? 1 : 0;
         if (rank < k) best[rank] = mine;
     }
@@ -247,16 +352,21 @@ __device__ __forceinline__ void rank_list(const Candidate *list, int n, int k, C
 
 // Bound from the largest element that each thread has seen.
 __device__ __forceinline__ void find_bound(TopShared &t, float mine, int k) {
+    static_assert(kGroups * 2 == kThreads && kGroups >= kMostTop, "a group to two lanes, and a k-th largest group");
     mine = fmaxf(mine, __shfl_xor_sync(kAllLanes, mine, 1));
-    mine = fmaxf(mine, __shfl_xor_sync(kAllLanes, mine, 2));
-    if ((threadIdx.x & 3) == 0) t.group[threadIdx.x >> 2] = mine;
+    if ((threadIdx.x & 1) == 0) t.group[threadIdx.x >> 1] = mine;
     if (threadIdx.x == 0) t.count = 0;
     __syncthreads();
     if (threadIdx.x < kGroups) {
         const float v = t.group[threadIdx.x];
         int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < kGroups; ++j) rank += t.group[j] > v || (t.group[j] == v && j < static_cast<int>(threadIdx.x));
+#pragma unroll 4
+        for (int j = 0; j < kGroups; j += 4) {
+            const float4 g = *reinterpret_cast<const float4 *>(t.group + j);
+            const int me = threadIdx.x;
+            rank += (g.x > v || (g.x == v && j < me)) + (g.y > v || (g.y == v && j + 1 < me)) +
+                    (g.z > v || (g.z == v && j + 2 < me)) + (g.w > v || (g.w == v && j + 3 < me));
+        }
         if (rank == k - 1) t.bound = v;
     }
     __syncthreads();
@@ -343,78 +453,57 @@ template <int DT> __device__ __noinline__ void exact_top(TopShared &t, const Sha
 
 // ---------------------------------------------------------------- the pass over a row
 
-// Sums of the block's share of a row and, where k > 0, its k best elements in
-// t.best, sorted.
-template <int DT, bool TOP>
-__device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShared *t, int k, Sums *part) {
-    constexpr int V = Chunk<DT>::kElems;
-    Sums v = no_sums();
-    Chunk<DT> r[kFlight];
+// The thread's chunks of the turn that begins at its chunk c0; those past the share are masked.
+template <int DT>
+__device__ __forceinline__ void load_turn(const Share<DT> &sh, int c0, Chunk<DT> (&r)[kFlight]) {
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+        r[u] = c0 + u * kThreads < sh.end ? sh.chunk(c0 + u * kThreads) : masked_chunk<DT>();
+}
+
+// A thread's sums over the block's share of a row; with TOP, the elements
+// that may be among the k best are in t's list when the block next synchronises.
+// r comes with the first turn loaded and is left with the last one: the whole
+// share where that is one turn.
+template <int DT, bool ENTROPY, bool TOP>
+__device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShared *t, int k, Chunk<DT> (&r)[kFlight]) {
+    PairSums v = {kLeastExponent, both(0.0f), both(0.0f), masked_word<DT>()};
+    const bool single = static_cast<int>(threadIdx.x) < sh.singles;
+    const float one = single ? sh.at(sh.single(threadIdx.x)) : kNegInf;
     float bound = kNegInf;
-    auto take = [&](int c0) {  // up to kFlight chunks of this thread from c0 on
-        float top = kNegInf;
+    for (int c0 = sh.first + static_cast<int>(threadIdx.x);;) {
+        const float top = add_chunks<DT, ENTROPY>(v, r, a);
+        if constexpr (TOP) {
+            if (c0 < sh.first + kTurn) {  // the first turn, for all threads
+                find_bound(*t, fmaxf(top, one), k);
+                bound = t->bound;
+                if (one >= bound && one > kNegInf) collect(*t, one, sh.single(threadIdx.x));
+            }
+            if (top >= bound && top > kNegInf) {
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u)
-            if (c0 + u * kThreads < sh.end) r[u] = sh.chunk(c0 + u * kThreads);
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            if (c0 + u * kThreads < sh.end) {
-                float f[V];
-                unpack<DT>(r[u], f);
-                const float seen = v.top;
-                v.top = kNegInf;
-                add_elements(v, f, a);
-                top = fmaxf(top, v.top);
-                v.top = max_nan(v.top, seen);
+                for (int u = 0; u < kFlight; ++u) {
+                    // few of the chunks that get here hold a candidate
+                    const uint32_t m = max_words<DT>(max_words<DT>(r[u].w[0], r[u].w[1]), max_words<DT>(r[u].w[2], r[u].w[3]));
+                    if (max_of_word<DT>(m) >= bound)
+                        collect_chunk<DT>(*t, make_uint4(r[u].w[0], r[u].w[1], r[u].w[2], r[u].w[3]),
+                                          sh.column(c0 + u * kThreads, 0), bound);
+                }
             }
         }
-        return top;
-    };
-    auto offer = [&](int c0, float top) {  // those that reach the bound become candidates
-        if (!(top >= bound)) return;
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            if (c0 + u * kThreads < sh.end) {
-                float f[V];
-                unpack<DT>(r[u], f);
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (f[j] >= bound && f[j] > kNegInf) collect(*t, f[j], sh.column(c0 + u * kThreads, j));
-            }
-        }
-    };
-    int c0 = sh.first + threadIdx.x;
-    float top = take(c0);
-    float one = kNegInf;
-    if (static_cast<int>(threadIdx.x) < sh.singles) {
-        one = sh.at(sh.single(threadIdx.x));
-        const float f[1] = {one};
-        add_elements(v, f, a);
+        c0 += kTurn;
+        if (c0 - static_cast<int>(threadIdx.x) >= sh.end) break;
+        load_turn<DT>(sh, c0, r);
     }
-    if constexpr (TOP) {
-        find_bound(*t, fmaxf(top, one), k);
-        bound = t->bound;
-        offer(c0, top);
-        if (one >= bound && one > kNegInf) collect(*t, one, sh.single(threadIdx.x));
-    }
-    for (c0 += kFlight * kThreads; c0 < sh.end; c0 += kFlight * kThreads) {
-        top = take(c0);
-        if constexpr (TOP) offer(c0, top);
-    }
-    v = block_sums(v, part);  // and every candidate is in the list
-    if constexpr (TOP) {
-        if (t->count > kCandidates) exact_top<DT>(*t, sh, k);
-        rank_list(t->list, t->count, k, t->best);
-        __syncthreads();
-    }
-    return v;
+    Sums sums = {v.c, v.s.x + v.s.y, v.u.x + v.u.y, max_of_word<DT>(v.top)};
+    if (single) add_element(sums, one, a);
+    return sums;
 }
 
 // ---------------------------------------------------------------- log probabilities
 
 // A row to a cluster of `blocks` blocks (one block: no cluster); the first
 // puts the parts together.
-template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads) logprob_kernel(LogprobArgs a, int blocks) {
+template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads, kResident) logprob_kernel(LogprobArgs a, int blocks) {
     enter_grid();
     __shared__ Sums part[kWarps];
     __shared__ Sums mine;
@@ -427,25 +516,25 @@ template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads) logprob_
     const void *logits = row_of<DT>(a.logits, row, a.stride);
     const Share<DT> sh(logits, a.cols, block, blocks);
     const float ax = a.scale * kLog2e;
-    Sums v = pass_over<DT, TOP>(sh, ax, t, a.top, part);
+    Chunk<DT> r_chunks[kFlight];
+    load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), r_chunks);
+    Sums v = block_sums(pass_over<DT, true, TOP>(sh, ax, t, a.top, r_chunks), part);  // and every candidate is in the list
+    if constexpr (TOP) {
+        if (t->count > kCandidates) exact_top<DT>(*t, sh, a.top);
+        rank_list(t->list, t->count, a.top, t->best);
+        __syncthreads();
+    }
     if (blocks > 1) {
         if (threadIdx.x == 0) mine = v;
+        if (TOP && threadIdx.x == 0) t->count = 0;
         cluster_sync();
         if (block == 0) {
-            for (int b = 1; b < blocks; ++b) v = merged(v, *in_block(&mine, b));
+            v = cluster_sums(&mine, blocks);
             if constexpr (TOP) {
-                for (int i = threadIdx.x; i < blocks * a.top; i += kThreads)
-                    t->list[i] = in_block(t->best, i / a.top)[i % a.top];
-                __syncthreads();
-                // entries that are not there (-inf, -1) rank behind all others; drop them
-                if (threadIdx.x == 0) t->count = 0;
-                __syncthreads();
-                Candidate keep[2];
-                int n = 0;
-                for (int i = threadIdx.x; i < blocks * a.top; i += kThreads) keep[n++] = t->list[i];
-                __syncthreads();
-                for (int i = 0; i < n; ++i)
-                    if (keep[i].id >= 0) collect(*t, keep[i].x, keep[i].id);
+                for (int i = threadIdx.x; i < blocks * a.top; i += kThreads) {
+                    const Candidate c = in_block(t->best, i / a.top)[i % a.top];
+                    if (c.id >= 0) collect(*t, c.x, c.id);
+                }
                 __syncthreads();
                 rank_list(t->list, t->count, a.top, t->best);
             }
@@ -453,6 +542,7 @@ template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads) logprob_
         cluster_sync();  // no block leaves while its shared memory is read
         if (block != 0) return;
     }
+    if (TOP) __syncthreads();  // best is written
     const RowSum r = finish_row<DT>(v, logits, a.cols, ax, fpart);
     if (threadIdx.x == 0) {
         const bool empty = r.careful && r.top == kNegInf;
@@ -485,86 +575,114 @@ __device__ __forceinline__ float p_of(const Weights &w, float x, float a) {
     if (w.careful) return w.weight * ex2(fmaxf((x - w.top) * a, -200.0f));
     return w.weight * ex2(fmaf(fmaxf(x, kLeast), a, -w.c));
 }
-// p = 0 whatever x is.
-__device__ __forceinline__ Weights no_weights() { return {0.0f, 0.0f, -kNegInf, true}; }
 // From a saved lse: c is lse * log2(e) rounded to an integer, weight 2^ of what
 // is left, formed with the two parts of log2(e).
 __device__ __forceinline__ Weights weights_of(float lse, float scale) {
     const float c = rintf(lse * kLog2e);
     const float left = fmaf(lse, kLog2e, -c) + lse * 1.9259629911266175e-8f;
     if (fabsf(lse) < 1e6f) return {c, ex2(-left), 0.0f, false};
-    if (lse == kNegInf) return no_weights();  // an empty row
     return {0.0f, lse == lse ? 1.0f : lse, lse / scale, true};  // huge values; NaN stays NaN
 }
 
-// d(x) = g p(x), or with entropy g p(x) - dH p(x) (log p(x) + H), into dlogits.
+// A row's gradient but for single places: d(x) = p(x) (g - dent (log p(x) + H)).
+// With e = 2^t, t = a x - c, and log p = ln2 t + (ln2 c - lse):
+//     d = e (A + B t),  A = weight (g - dent (H + ln2 c - lse)),  B = -weight dent ln2.
+// Without an entropy term (lse and H 0 there) d = e A.
 struct RowGrad {
     Weights w;
-    float g, dent, lse, entropy;
+    float g, dent, lse, entropy, A, B;
 };
+__device__ __forceinline__ RowGrad row_grad(const Weights &w, float g, float dent, float lse, float entropy) {
+    const float offset = fmaf(w.c, kLn2, w.c * -1.9046543e-9f) - lse;  // ln2 in two parts
+    return {w, g, dent, lse, entropy, w.weight * fmaf(-dent, entropy + offset, g), w.weight * -dent * kLn2};
+}
 template <bool ENTROPY> __device__ __forceinline__ float grad_of(const RowGrad &r, float x, float a, float scale) {
-    const float p = p_of(r.w, x, a);
-    if constexpr (ENTROPY) {
+    if (r.w.careful) {
+        const float p = p_of(r.w, x, a);
+        if constexpr (!ENTROPY) return p * r.g;
         const float logp = fmaf(fmaxf(x, kLeast), scale, -r.lse);
         return p * fmaf(-r.dent, p > 0.0f ? logp + r.entropy : 0.0f, r.g);
-    } else {
-        return p * r.g;
     }
-}
-
-// Writes the gradient of the block's share.  The output row may start at
-// another offset from 16 bytes than the input's: then element by element.
-template <int DT, bool ENTROPY>
-__device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, const RowGrad &r, float a, float scale) {
-    using T = typename ElemOf<DT>::type;
-    constexpr int V = Chunk<DT>::kElems;
-    T *out = static_cast<T *>(out_row);
-    const bool alike = (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(sh.row)) % 16 == 0;
-    auto put_one = [&](int col, float x) {
-        const T d = f32_to_elem<DT>(grad_of<ENTROPY>(r, x, a, scale));
-        if constexpr (DT == DT_F32) { Vec<4> v; v.w[0] = d; st<4>(out + col, v); }
-        else { Vec<2> v; v.h = d; st<2>(out + col, v); }
-    };
-    for (int c0 = sh.first + static_cast<int>(threadIdx.x); c0 < sh.end; c0 += kFlight * kThreads) {
-        Chunk<DT> raw[kFlight];
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u)
-            if (c0 + u * kThreads < sh.end) raw[u] = sh.chunk(c0 + u * kThreads);
-#pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            if (c0 + u * kThreads >= sh.end) break;
-            float f[V];
-            unpack<DT>(raw[u], f);
-            if (alike) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) f[j] = grad_of<ENTROPY>(r, f[j], a, scale);
-                Vec<16> o;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (DT == DT_F32) o.w[j] = __float_as_uint(f[j]);
-                    else if constexpr (DT == DT_F16) o.w[j] = f32x2_to_f16x2(f[2 * j + 1], f[2 * j]);
-                    else o.w[j] = f32x2_to_bf16x2(f[2 * j + 1], f[2 * j]);
-                }
-                st<16>(out + sh.column(c0 + u * kThreads, 0), o);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) put_one(sh.column(c0 + u * kThreads, j), f[j]);
-            }
-        }
-    }
-    if (static_cast<int>(threadIdx.x) < sh.singles) {
-        const int col = sh.single(threadIdx.x);
-        put_one(col, sh.at(col));
-    }
+    const float t = fmaf(fmaxf(x, kLeast), a, -r.w.c);
+    return ex2(t) * (ENTROPY ? fmaf(r.B, t, r.A) : r.A);
 }
 template <int DT> __device__ __forceinline__ void store_one(void *row, int col, float x) {
     using T = typename ElemOf<DT>::type;
     static_cast<T *>(row)[col] = f32_to_elem<DT>(x);
 }
 
+// Rows whose p is formed the careful way, and rows whose output starts at
+// another offset from 16 bytes than the input: element by element.
+template <int DT, bool ENTROPY>
+__device__ __noinline__ void write_grad_slowly(const Share<DT> &sh, void *out, const RowGrad &r, float a, float scale) {
+    constexpr int V = Chunk<DT>::kElems;
+    for (int c = sh.first * V + static_cast<int>(threadIdx.x); c < sh.end * V; c += kThreads)
+        store_one<DT>(out, sh.head + c, grad_of<ENTROPY>(r, sh.at(sh.head + c), a, scale));
+    if (static_cast<int>(threadIdx.x) < sh.singles) {
+        const int col = sh.single(threadIdx.x);
+        store_one<DT>(out, col, grad_of<ENTROPY>(r, sh.at(col), a, scale));
+    }
+}
+
+// Zeros for the block's share, whatever the logits are.
+template <int DT> __device__ __forceinline__ void write_zeros(void *out_row, int cols, int block, int blocks) {
+    const Share<DT> sh(out_row, cols, block, blocks);
+    typename ElemOf<DT>::type *out = static_cast<typename ElemOf<DT>::type *>(out_row);
+    const Vec<16> zero = {};
+    for (int c = sh.first + static_cast<int>(threadIdx.x); c < sh.end; c += kThreads) st<16>(out + sh.column(c, 0), zero);
+    if (static_cast<int>(threadIdx.x) < sh.singles) store_one<DT>(out, sh.single(threadIdx.x), 0.0f);
+}
+
+// Writes the gradient of the block's share, which is read again, or, HELD, is one
+// turn that r still holds.  REVERSE takes the turns from the end: what the pass
+// for the sums read last is the likeliest to be still in L2.
+template <int DT, bool ENTROPY, bool REVERSE, bool HELD>
+__device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, const RowGrad &g, float a, float scale,
+                                           Chunk<DT> (&r)[kFlight]) {
+    using T = typename ElemOf<DT>::type;
+    T *out = static_cast<T *>(out_row);
+    const bool alike = (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(sh.row)) % 16 == 0;
+    if (g.w.careful || !alike) {
+        write_grad_slowly<DT, ENTROPY>(sh, out_row, g, a, scale);
+        return;
+    }
+    const float2 slope = both(a), shift = both(-g.w.c), A2 = both(g.A), B2 = both(g.B);
+    const int turns = HELD ? 1 : (sh.end - sh.first + kTurn - 1) / kTurn;
+    for (int turn = 0; turn < turns; ++turn) {
+        const int c0 = sh.first + (REVERSE ? turns - 1 - turn : turn) * kTurn + static_cast<int>(threadIdx.x);
+        if constexpr (!HELD) {
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                if (c0 + u * kThreads < sh.end) r[u] = sh.chunk(c0 + u * kThreads);
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            if (c0 + u * kThreads >= sh.end) break;
+            Vec<16> o;
+#pragma unroll
+            for (int j = 0; j < Pairs<DT>::kCount; ++j) {
+                const float2 t = fma2(bounded_pair<DT>(r[u], j), slope, shift);
+                float2 d = make_float2(ex2(t.x), ex2(t.y));
+                d = mul2(d, ENTROPY ? fma2(B2, t, A2) : A2);
+                if constexpr (DT == DT_F32) {
+                    o.w[2 * j] = __float_as_uint(d.x);
+                    o.w[2 * j + 1] = __float_as_uint(d.y);
+                } else {
+                    o.w[j] = narrow<DT>(d);
+                }
+            }
+            st<16>(out + sh.column(c0 + u * kThreads, 0), o);
+        }
+    }
+    if (static_cast<int>(threadIdx.x) < sh.singles) {
+        const int col = sh.single(threadIdx.x);
+        store_one<DT>(out, col, grad_of<ENTROPY>(g, sh.at(col), a, scale));
+    }
+}
+
 // dlogits = scale (dlogp (1_token - p) - dentropy p (log p + H)).
 template <int DT, bool ENTROPY>
-__global__ void __launch_bounds__(kThreads) logprob_grad_kernel(LogprobGradArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(LogprobGradArgs a, int blocks) {
     enter_grid();
     const int block = static_cast<int>(blockIdx.x % blocks);
     const int64_t row = blockIdx.x / blocks;
@@ -574,22 +692,22 @@ __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(LogprobGradArgs 
     int64_t token = a.dlogp ? token_at(a.tokens, a.i64, row) : -1;
     if (token >= a.cols) token = -1;
     const float dlogp = token >= 0 ? a.dlogp[row] : 0.0f;
-    RowGrad r;
-    r.lse = a.lse[row];
-    r.w = weights_of(r.lse, a.scale);
-    const bool empty = r.lse == kNegInf;  // nothing depends on the logits of an empty row
-    r.g = -a.scale * dlogp;
-    r.dent = ENTROPY && !empty ? a.scale * a.dentropy[row] : 0.0f;
-    r.entropy = ENTROPY && !empty ? a.entropy[row] : 0.0f;
-    if (empty) r.lse = 0.0f;
+    const float lse = a.lse[row];
+    if (lse == kNegInf) {  // nothing depends on the logits of an empty row
+        write_zeros<DT>(out, a.cols, block, blocks);
+        return;
+    }
+    const RowGrad r = row_grad(weights_of(lse, a.scale), -a.scale * dlogp, ENTROPY ? a.scale * a.dentropy[row] : 0.0f,
+                               ENTROPY ? lse : 0.0f, ENTROPY ? a.entropy[row] : 0.0f);
     const bool here = token >= 0 && sh.holds(static_cast<int>(token));
     const float x = here ? sh.at(static_cast<int>(token)) : 0.0f;  // read before it may be overwritten
     if (here) __syncthreads();                                     // uniform: all threads have the same token
-    write_grad<DT, ENTROPY>(sh, out, r, ax, a.scale);
+    Chunk<DT> chunks[kFlight];
+    write_grad<DT, ENTROPY, false, false>(sh, out, r, ax, a.scale, chunks);
     if (!here) return;
     __syncthreads();
     if (threadIdx.x == 0)
-        store_one<DT>(out, static_cast<int>(token), empty ? 0.0f : grad_of<ENTROPY>(r, x, ax, a.scale) + a.scale * dlogp);
+        store_one<DT>(out, static_cast<int>(token), grad_of<ENTROPY>(r, x, ax, a.scale) + a.scale * dlogp);
 }
 
 // ---------------------------------------------------------------- distillation
@@ -598,30 +716,56 @@ __global__ void __launch_bounds__(kThreads) logprob_grad_kernel(LogprobGradArgs 
 // row, both of values times `scale`:
 //     loss = sum q_i (log q_i - log p(id_i)),   dlogits = dloss scale (p - q).
 // Entries with an id outside the row or a value of -inf do not count; a row
-// without any has loss 0 and gradient 0.  The row is read for the sums and
-// again for the gradient, the second time mostly from L2.
+// without any has loss 0 and gradient 0.  HELD: a block's share is one turn and
+// stays in registers between the sums and the gradient; longer shares are read
+// twice, the second time from L2.
 
 struct Teacher {
     int id[kMostTeacher];
-    float q[kMostTeacher];
+    float t[kMostTeacher];  // scaled value
     float x[kMostTeacher];  // the student's logit there
 };
 
-template <int DT, bool SUMS, bool GRAD>
-__global__ void __launch_bounds__(kThreads) distill_kernel(DistillArgs a, int blocks) {
+// Largest value and the sum of e^(value - largest), and two of them together.
+struct Softmax {
+    float top, sum;
+};
+__device__ __forceinline__ Softmax merged(Softmax a, Softmax b) {
+    const float top = max_nan(a.top, b.top);
+    // equal ones, both of them -inf among these, keep their sum
+    const float fa = a.top == top ? 1.0f : expf(a.top - top), fb = b.top == top ? 1.0f : expf(b.top - top);
+    return {top, fmaf(a.sum, fa, b.sum * fb)};
+}
+__device__ __forceinline__ Softmax warp_softmax(Softmax v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const Softmax o = {__shfl_xor_sync(kAllLanes, v.top, d), __shfl_xor_sync(kAllLanes, v.sum, d)};
+        // a fixed order of the two makes both lanes' bits the same
+        v = (threadIdx.x & d) ? merged(o, v) : merged(v, o);
+    }
+    return v;
+}
+
+template <int DT, bool SUMS, bool GRAD, bool HELD>
+__global__ void __launch_bounds__(kThreads, kResident) distill_kernel(DistillArgs a, int blocks) {
     enter_grid();
     __shared__ Sums part[kWarps];
+    __shared__ Softmax tpart[kWarps];
     __shared__ Sums mine;
     __shared__ float fpart[2][32];
     __shared__ Teacher th;
     const int block = static_cast<int>(blockIdx.x % blocks);
     const int64_t row = blockIdx.x / blocks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const void *logits = row_of<DT>(a.logits, row, a.stride);
     const Share<DT> sh(logits, a.cols, block, blocks);
     const float ax = a.scale * kLog2e;
 
-    // the teacher's entries and its softmax; every block has them all
-    float largest = kNegInf;
+    Chunk<DT> chunks[kFlight];  // on their way while the teacher's entries are
+    if constexpr (SUMS) load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), chunks);
+
+    // the teacher's entries; every block has them all
+    Softmax q = {kNegInf, 0.0f};
     for (int i = threadIdx.x; i < a.k; i += kThreads) {
         const int64_t id = token_at(a.ids, a.i64, row * a.ids_stride + i);
         const int64_t at = row * a.teacher_stride + i;
@@ -629,94 +773,99 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(DistillArgs a, int bl
         if (DT == DT_F32 || a.teacher_f32) v = static_cast<const float *>(a.teacher)[at];
         else v = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(a.teacher)[at]);
         const bool given = id >= 0 && id < a.cols && v != kNegInf;
-        th.id[i] = given ? static_cast<int>(id) : -1;
-        th.q[i] = v * a.scale;
-        // the loss needs them all, the gradient those that this block writes
+        // the loss needs all the student's logits there, the gradient those that this block writes
         const bool read = given && ((SUMS && block == 0) || sh.holds(static_cast<int>(id)));
+        v *= a.scale;
+        th.id[i] = given ? static_cast<int>(id) : -1;
+        th.t[i] = v;
         th.x[i] = read ? sh.at(static_cast<int>(id)) : 0.0f;
-        if (given) largest = max_nan(largest, th.q[i]);
+        if (given) q = merged(q, Softmax{v, 1.0f});
+    }
+    Sums v = no_sums();
+    if constexpr (SUMS) v = warp_sums(pass_over<DT, false, false>(sh, ax, nullptr, 0, chunks));
+    q = warp_softmax(q);
+    if (lane == 0) {
+        part[warp] = v;
+        tpart[warp] = q;
     }
     __syncthreads();
-    largest = block_max_nan(largest, kWarps, fpart[0], kNegInf);
-    const bool any = largest != kNegInf;
-    float sum = 0.0f;
-    for (int i = threadIdx.x; i < a.k; i += kThreads) {
-        th.q[i] = th.id[i] >= 0 ? th.q[i] - largest : kNegInf;
-        sum += th.id[i] >= 0 ? expf(th.q[i]) : 0.0f;
-    }
-    sum = block_sum(sum, kWarps, fpart[1]);
-    const float log_sum = logf(sum);
+    q = warp_softmax(lane < kWarps ? tpart[lane] : Softmax{kNegInf, 0.0f});
+    const bool any = q.top != kNegInf;
+    const float log_sum = logf(q.sum);
+    auto log_q = [&](int i) { return th.t[i] - q.top - log_sum; };
 
-    Sums v = no_sums();
-    RowSum r;
     Weights w;
+    RowSum r;
     if constexpr (SUMS) {
-        v = pass_over<DT, false>(sh, ax, nullptr, 0, part);
+        v = warp_sums(lane < kWarps ? part[lane] : no_sums());
         if (blocks > 1) {
             if (threadIdx.x == 0) mine = v;
             cluster_sync();
-            Sums all = *in_block(&mine, 0);
-            for (int b = 1; b < blocks; ++b) all = merged(all, *in_block(&mine, b));
-            v = all;
-            cluster_sync();
+            v = cluster_sums(&mine, blocks);
+            cluster_arrive();  // the wait is further down: mine has been read
         }
         r = finish_row<DT>(v, logits, a.cols, ax, fpart[0]);
-        const bool empty = r.careful && r.top == kNegInf;
         w = {r.c, r.inv_s, r.top, r.careful};
-        if (block == 0) {
-            // in order of the entries, added by the block's fixed tree
-            float loss = 0.0f;
-            for (int i = threadIdx.x; i < a.k; i += kThreads) {
-                const float logq = th.q[i] - log_sum, q = th.id[i] >= 0 ? expf(logq) : 0.0f;
-                const float logp = empty ? kNegInf : logp_of(r, th.x[i], ax, a.scale);
-                if (q != 0.0f) loss += q * (logq - logp);
-            }
-            __syncthreads();
-            loss = block_sum(loss, kWarps, fpart[1]);
-            if (threadIdx.x == 0) {
-                if (a.loss) a.loss[row] = any ? loss : 0.0f;
-                if (a.lse) a.lse[row] = empty ? kNegInf : lse_of(r, a.scale);
-            }
-        }
     } else {
         w = weights_of(a.lse[row], a.scale);
     }
     if constexpr (GRAD) {
-        const float g = any ? a.dloss[row] * a.scale : 0.0f;
+        const RowGrad rg = row_grad(w, any ? a.dloss[row] * a.scale : 0.0f, 0.0f, 0.0f, 0.0f);
         void *out = row_of<DT>(a.dlogits, row, a.dstride);
-        RowGrad rg = {w, g, 0.0f, 0.0f, 0.0f};
-        if (!any) rg.w = no_weights();
-        // careful rows may be read again by another block: all have to be done before any writes in place
+        // a careful row has been read whole by every block: all are done with it before any writes in place
         if (SUMS && w.careful) {
-            if (blocks > 1) cluster_sync();
-            else __syncthreads();
+            if (blocks > 1) {
+                cluster_wait();
+                cluster_arrive();
+                cluster_wait();
+                cluster_arrive();
+            } else {
+                __syncthreads();
+            }
         }
-        write_grad<DT, false>(sh, out, rg, ax, a.scale);
-        if (!any) return;
+        if (any) write_grad<DT, false, true, HELD>(sh, out, rg, ax, a.scale, chunks);
+        else write_zeros<DT>(out, a.cols, block, blocks);
         __syncthreads();
         // entries of one id add up; the first of them writes
-        for (int i = threadIdx.x; i < a.k; i += kThreads) {
+        for (int i = threadIdx.x; any && i < a.k; i += kThreads) {
             const int id = th.id[i];
             if (id < 0 || !sh.holds(id)) continue;
             bool first = true;
-            float q = 0.0f;
+            float qs = 0.0f;
             for (int j = 0; j < a.k; ++j) {
                 if (th.id[j] != id) continue;
                 if (j < i) { first = false; break; }
-                q += expf(th.q[j] - log_sum);
+                qs += expf(log_q(j));
             }
-            if (first) store_one<DT>(out, id, g * (p_of(w, th.x[i], ax) - q));
+            if (first) store_one<DT>(out, id, rg.g * (p_of(w, th.x[i], ax) - qs));
         }
+    }
+    if constexpr (SUMS) {
+        if (block == 0) {
+            const bool empty = r.careful && r.top == kNegInf;
+            float loss = 0.0f;
+            for (int i = threadIdx.x; i < a.k; i += kThreads) {
+                const float logq = log_q(i), qi = th.id[i] >= 0 ? expf(logq) : 0.0f;
+                const float logp = empty ? kNegInf : logp_of(r, th.x[i], ax, a.scale);
+                if (qi != 0.0f) loss += qi * (logq - logp);
+            }
+            loss = block_sum(loss, kWarps, fpart[1]);
+            if (threadIdx.x == 0) {
+                a.loss[row] = any ? loss : 0.0f;
+                a.lse[row] = empty ? kNegInf : lse_of(r, a.scale);
+            }
+        }
+        if (blocks > 1) cluster_wait();
     }
 }
 
 // ---------------------------------------------------------------- launches
 
-// Blocks a row: one where the rows alone fill the device twice, up to a
-// cluster of 8 where they are few, each with at least 4096 elements.
+// Blocks a row: one where the rows alone fill the device, up to a cluster of 8
+// where they are few, each with a turn's worth of 2048 elements at least.
 inline int blocks_per_row(int64_t rows, int cols, int sms) {
     int blocks = 1;
-    while (blocks < 8 && rows * blocks < 2 * static_cast<int64_t>(sms) && cols / (2 * blocks) >= 4096) blocks *= 2;
+    while (blocks < 8 && rows * blocks < kResident * static_cast<int64_t>(sms) && cols / (2 * blocks) >= 4096) blocks *= 2;
     return blocks;
 }
 inline void describe(LaunchInfo *info, int64_t grid) {
@@ -743,12 +892,16 @@ template <int DT> cudaError_t logprob_grad_launch(const LogprobGradArgs &a, cuda
 template <int DT>
 cudaError_t distill_launch(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info) {
     const int blocks = blocks_per_row(a.rows, a.cols, sms);
+    // Rows are not split further to be held: 2048 rows of 65536 bf16 in clusters
+    // of 4 that hold them take 190 us, in one block that reads them twice 105 us.
+    const bool held = a.cols / Chunk<DT>::kElems <= static_cast<int64_t>(kTurn) * blocks;
     const int64_t grid = a.rows * blocks;
     describe(info, grid);
     const dim3 g(grid), b(kThreads);
-    if (!sums) return launch_rows(distill_kernel<DT, false, true>, g, b, 0, blocks, s, a, blocks);
-    return grad ? launch_rows(distill_kernel<DT, true, true>, g, b, 0, blocks, s, a, blocks)
-                : launch_rows(distill_kernel<DT, true, false>, g, b, 0, blocks, s, a, blocks);
+    if (!sums) return launch_rows(distill_kernel<DT, false, true, false>, g, b, 0, blocks, s, a, blocks);
+    if (!grad) return launch_rows(distill_kernel<DT, true, false, false>, g, b, 0, blocks, s, a, blocks);
+    return held ? launch_rows(distill_kernel<DT, true, true, true>, g, b, 0, blocks, s, a, blocks)
+                : launch_rows(distill_kernel<DT, true, true, false>, g, b, 0, blocks, s, a, blocks);
 }
 
 }  // namespace

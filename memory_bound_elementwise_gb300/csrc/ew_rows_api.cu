@@ -155,7 +155,7 @@ EmbedWork embed_work(int64_t table_rows, int64_t rows, int64_t cols) {
 bool index_type(int t) { return t == EW_INDEX_I32 || t == EW_INDEX_I64; }
 int index_bytes(ew_index t) { return t == EW_INDEX_I64 ? 8 : 4; }
 // What multiplies logits: positive, and far from where binary32 ends.
-bool scale_ok(float scale) { return scale > 0.0f && scale <= 1048576.0f; }
+bool scale_ok(float scale) { return scale >= 1.0f / 1048576.0f && scale <= 1048576.0f; }
 
 // The three distillation calls: sums (loss and lse) and grad (dlogits).
 ew_status distill_call(bool sums, bool grad, ew_dtype dt, ew_index itype, const void *logits, int64_t stride,

@@ -385,7 +385,7 @@ def test_repeats_bit_for_bit_and_in_a_graph():
 def test_refusals():
     x, tokens = torch.zeros(4, 64, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
     each = torch.zeros(4, device="cuda")
-    for bad in (0.0, -1.0, math.nan, math.inf, 2.0 ** 21):
+    for bad in (0.0, -1.0, math.nan, math.inf, 2.0 ** 21, 2.0 ** -21):
         with pytest.raises(ew.EwError, match="INVALID"):
             ew.ew_logprob(x, tokens, scale=bad)
     with pytest.raises(ew.EwError, match="INVALID"):
