@@ -100,12 +100,28 @@ template <int DT> __device__ __forceinline__ float2 bounded(uint32_t w, uint32_t
         return widen<DT>(d);
     }
 }
-// Pair j of a chunk: 4 pairs of 16-bit elements, 2 of binary32.
+// Pair j of a chunk: 4 pairs of 16-bit elements, 2 of binary32.  Unbounded
+// masked elements have t = -inf and 2^t = 0; only a product with t needs the
+// bound.
 template <int DT> struct Pairs { static constexpr int kCount = DT == DT_F32 ? 2 : 4; };
-template <int DT> __device__ __forceinline__ float2 bounded_pair(const Chunk<DT> &r, int j) {
-    if constexpr (DT == DT_F32) return bounded<DT>(r.w[2 * j], r.w[2 * j + 1]);
-    else return bounded<DT>(r.w[j], 0u);
+template <int DT, bool BOUNDED> __device__ __forceinline__ float2 pair_at(const Chunk<DT> &r, int j) {
+    if constexpr (DT == DT_F32) {
+        if constexpr (BOUNDED) return bounded<DT>(r.w[2 * j], r.w[2 * j + 1]);
+        else return make_float2(__uint_as_float(r.w[2 * j]), __uint_as_float(r.w[2 * j + 1]));
+    } else {
+        if constexpr (BOUNDED) return bounded<DT>(r.w[j], 0u);
+        else return widen<DT>(r.w[j]);
+    }
 }
+
+// How a launch splits its rows: 2^shift blocks a row, a cluster of them where
+// they work together, each with `each` chunks (the last with the rest).
+struct Split {
+    int shift, each;
+    __host__ __device__ __forceinline__ int blocks() const { return 1 << shift; }
+};
+// The whole row to one block.
+__device__ __forceinline__ Split unsplit() { return {0, INT32_MAX}; }
 
 // A block's share of a row: whole 16-byte chunks from element `head` on, and
 // the single elements before the first (block 0) and after the last chunk
@@ -118,17 +134,18 @@ template <int DT> struct Share {
     int first, end;        // chunks of this block
     int singles, tail0;    // single elements: [0, n_head) and [tail0, cols)
     int n_head;
-    __device__ __forceinline__ Share(const void *p, int cols_, int block, int blocks) {
+    __device__ __forceinline__ Share(const void *p, int cols_, int block, Split split) {
         row = static_cast<const T *>(p);
         cols = cols_;
         const int past = static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16) / ElemOf<DT>::kBytes;
         head = min((V - past) % V, cols);
         const int chunks = (cols - head) / V;
-        first = static_cast<int>(static_cast<int64_t>(chunks) * block / blocks);
-        end = static_cast<int>(static_cast<int64_t>(chunks) * (block + 1) / blocks);
+        // each * blocks may be past 2^31 only where each is at least chunks
+        first = block == 0 ? 0 : min(static_cast<int>(min(static_cast<int64_t>(block) * split.each, int64_t(INT32_MAX))), chunks);
+        end = split.each >= chunks - first ? chunks : first + split.each;
         n_head = block == 0 ? head : 0;
         tail0 = head + chunks * V;
-        singles = n_head + (block == blocks - 1 ? cols - tail0 : 0);
+        singles = n_head + (block == split.blocks() - 1 ? cols - tail0 : 0);
     }
     __device__ __forceinline__ int column(int chunk, int j) const { return head + chunk * V + j; }
     // the column of single element k < singles
@@ -162,13 +179,6 @@ __device__ __forceinline__ void move_to(Sums &v, float c) {
     v.s *= f;
     v.c = c;
 }
-// Both sums at the larger exponent; symmetric, so that a butterfly gives every lane the same bits.
-__device__ __forceinline__ Sums merged(Sums a, Sums b) {
-    const float c = fmaxf(a.c, b.c);
-    move_to(a, c);
-    move_to(b, c);
-    return {c, a.s + b.s, a.u + b.u, max_nan(a.top, b.top)};
-}
 // One element.
 __device__ __forceinline__ void add_element(Sums &v, float x, float a) {
     v.top = max_nan(v.top, x);
@@ -184,12 +194,12 @@ struct PairSums {
     float2 s, u;
     uint32_t top;  // a word of largest elements
 };
-template <int DT, bool ENTROPY>
-__device__ __forceinline__ float add_chunks(PairSums &v, const Chunk<DT> (&r)[kFlight], float a) {
+template <int DT, bool ENTROPY, int N>
+__device__ __forceinline__ float add_chunks(PairSums &v, const Chunk<DT> (&r)[N], float a) {
     uint32_t m = max_words<DT>(r[0].w[0], r[0].w[1]);
     m = max_words<DT>(m, max_words<DT>(r[0].w[2], r[0].w[3]));
 #pragma unroll
-    for (int k = 1; k < kFlight; ++k)
+    for (int k = 1; k < N; ++k)
         m = max_words<DT>(m, max_words<DT>(max_words<DT>(r[k].w[0], r[k].w[1]), max_words<DT>(r[k].w[2], r[k].w[3])));
     v.top = max_words<DT>(v.top, m);
     const float top = max_of_word<DT>(m);
@@ -202,10 +212,10 @@ __device__ __forceinline__ float add_chunks(PairSums &v, const Chunk<DT> (&r)[kF
     }
     const float2 scale = both(a), shift = both(-v.c);
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
+    for (int k = 0; k < N; ++k) {
 #pragma unroll
         for (int j = 0; j < Pairs<DT>::kCount; ++j) {
-            const float2 t = fma2(bounded_pair<DT>(r[k], j), scale, shift);
+            const float2 t = fma2(pair_at<DT, ENTROPY>(r[k], j), scale, shift);
             const float2 e = make_float2(ex2(t.x), ex2(t.y));
             v.s = add2(v.s, e);
             if (ENTROPY) v.u = fma2(e, t, v.u);
@@ -213,28 +223,41 @@ __device__ __forceinline__ float add_chunks(PairSums &v, const Chunk<DT> (&r)[kF
     }
     return top;
 }
-__device__ __forceinline__ Sums warp_sums(Sums v) {
+// The sums of the first LANES lanes together (all others' are no_sums()), to
+// all lanes: the largest exponent first, then plain sums.  Every lane adds the
+// same pairs, so all get the same bits.
+template <int LANES> __device__ __forceinline__ Sums warp_sums(Sums v) {
+    float c = v.c;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const Sums o = {__shfl_xor_sync(kAllLanes, v.c, d), __shfl_xor_sync(kAllLanes, v.s, d),
-                        __shfl_xor_sync(kAllLanes, v.u, d), __shfl_xor_sync(kAllLanes, v.top, d)};
-        v = merged(v, o);
+    for (int d = LANES / 2; d > 0; d >>= 1) {
+        c = fmaxf(c, __shfl_xor_sync(kAllLanes, c, d));
+        v.top = max_nan(v.top, __shfl_xor_sync(kAllLanes, v.top, d));
+    }
+    if (LANES < 32) {
+        c = __shfl_sync(kAllLanes, c, 0);
+        v.top = __shfl_sync(kAllLanes, v.top, 0);
+    }
+    move_to(v, c);
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1) {
+        v.s += __shfl_xor_sync(kAllLanes, v.s, d);
+        v.u += __shfl_xor_sync(kAllLanes, v.u, d);
+    }
+    if (LANES < 32) {
+        v.s = __shfl_sync(kAllLanes, v.s, 0);
+        v.u = __shfl_sync(kAllLanes, v.u, 0);
     }
     return v;
 }
-// Sums of the block, to all its threads.
-__device__ __forceinline__ Sums block_sums(Sums v, Sums *part) {
-    v = warp_sums(v);
+// Sums of the block, to all its threads, from the warps' in `part`.
+__device__ __forceinline__ Sums sums_of_warps(const Sums *part) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return warp_sums(lane < kWarps ? part[lane] : no_sums());
+    return warp_sums<kWarps>(lane < kWarps ? part[lane] : no_sums());
 }
-
 // The sums of all blocks of the cluster, to every thread: lane b reads block b's.
 __device__ __forceinline__ Sums cluster_sums(const Sums *mine, int blocks) {
     const int lane = threadIdx.x & 31;
-    return warp_sums(lane < blocks ? *in_block(mine, lane) : no_sums());
+    return warp_sums<8>(lane < blocks ? *in_block(mine, lane) : no_sums());
 }
 
 // What a row's elements are compared with: log p(x) = ln2 (a x - c) - log_s,
@@ -266,7 +289,7 @@ __device__ __forceinline__ float entropy_of(const RowSum &r) {
 template <int DT> __device__ __noinline__ RowSum careful_row(const void *row, int cols, float a, float top, float *part) {
     RowSum r = {0.0f, 0.0f, 0.0f, 0.0f, top, true};
     if (top == kNegInf) return r;
-    const Share<DT> all(row, cols, 0, 1);
+    const Share<DT> all(row, cols, 0, unsplit());
     float s = 0.0f, u = 0.0f;
     for (int k = threadIdx.x; k < cols; k += kThreads) {
         const float t = fmaxf((all.at(k) - top) * a, -200.0f);
@@ -453,6 +476,13 @@ template <int DT> __device__ __noinline__ void exact_top(TopShared &t, const Sha
 
 // ---------------------------------------------------------------- the pass over a row
 
+// A thread's sums out of its pairs, and one of the single elements.
+template <int DT> __device__ __forceinline__ Sums finished(const PairSums &v, bool single, float one, float a) {
+    Sums sums = {v.c, v.s.x + v.s.y, v.u.x + v.u.y, max_of_word<DT>(v.top)};
+    if (single) add_element(sums, one, a);
+    return sums;
+}
+
 // The thread's chunks of the turn that begins at its chunk c0; those past the share are masked.
 template <int DT>
 __device__ __forceinline__ void load_turn(const Share<DT> &sh, int c0, Chunk<DT> (&r)[kFlight]) {
@@ -494,16 +524,14 @@ __device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShare
         if (c0 - static_cast<int>(threadIdx.x) >= sh.end) break;
         load_turn<DT>(sh, c0, r);
     }
-    Sums sums = {v.c, v.s.x + v.s.y, v.u.x + v.u.y, max_of_word<DT>(v.top)};
-    if (single) add_element(sums, one, a);
-    return sums;
+    return finished<DT>(v, single, one, a);
 }
 
 // ---------------------------------------------------------------- log probabilities
 
 // A row to a cluster of `blocks` blocks (one block: no cluster); the first
 // puts the parts together.
-template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads, kResident) logprob_kernel(LogprobArgs a, int blocks) {
+template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads, kResident) logprob_kernel(LogprobArgs a, Split split) {
     enter_grid();
     __shared__ Sums part[kWarps];
     __shared__ Sums mine;
@@ -511,14 +539,17 @@ template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads, kResiden
     __shared__ typename std::conditional<TOP, TopShared, int>::type top_store;
     TopShared *t = nullptr;
     if constexpr (TOP) t = &top_store;
-    const int block = static_cast<int>(blockIdx.x % blocks);
-    const int64_t row = blockIdx.x / blocks;
+    const int blocks = split.blocks(), block = blockIdx.x & (blocks - 1);
+    const int64_t row = blockIdx.x >> split.shift;
     const void *logits = row_of<DT>(a.logits, row, a.stride);
-    const Share<DT> sh(logits, a.cols, block, blocks);
+    const Share<DT> sh(logits, a.cols, block, split);
     const float ax = a.scale * kLog2e;
     Chunk<DT> r_chunks[kFlight];
     load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), r_chunks);
-    Sums v = block_sums(pass_over<DT, true, TOP>(sh, ax, t, a.top, r_chunks), part);  // and every candidate is in the list
+    Sums v = warp_sums<32>(pass_over<DT, true, TOP>(sh, ax, t, a.top, r_chunks));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();  // every candidate is in the list too
+    v = sums_of_warps(part);
     if constexpr (TOP) {
         if (t->count > kCandidates) exact_top<DT>(*t, sh, a.top);
         rank_list(t->list, t->count, a.top, t->best);
@@ -625,53 +656,59 @@ __device__ __noinline__ void write_grad_slowly(const Share<DT> &sh, void *out, c
 }
 
 // Zeros for the block's share, whatever the logits are.
-template <int DT> __device__ __forceinline__ void write_zeros(void *out_row, int cols, int block, int blocks) {
-    const Share<DT> sh(out_row, cols, block, blocks);
+template <int DT> __device__ __forceinline__ void write_zeros(void *out_row, int cols, int block, Split split) {
+    const Share<DT> sh(out_row, cols, block, split);
     typename ElemOf<DT>::type *out = static_cast<typename ElemOf<DT>::type *>(out_row);
     const Vec<16> zero = {};
     for (int c = sh.first + static_cast<int>(threadIdx.x); c < sh.end; c += kThreads) st<16>(out + sh.column(c, 0), zero);
     if (static_cast<int>(threadIdx.x) < sh.singles) store_one<DT>(out, sh.single(threadIdx.x), 0.0f);
 }
 
-// Writes the gradient of the block's share, which is read again, or, HELD, is one
-// turn that r still holds.  REVERSE takes the turns from the end: what the pass
-// for the sums read last is the likeliest to be still in L2.
-template <int DT, bool ENTROPY, bool REVERSE, bool HELD>
-__device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, const RowGrad &g, float a, float scale,
-                                           Chunk<DT> (&r)[kFlight]) {
+// The gradient of a chunk, by the formula above.
+template <int DT, bool ENTROPY> struct ChunkGrad {
+    float2 slope, shift, A, B;
+    __device__ __forceinline__ ChunkGrad(const RowGrad &g, float a)
+        : slope(both(a)), shift(both(-g.w.c)), A(both(g.A)), B(both(g.B)) {}
+    __device__ __forceinline__ Vec<16> operator()(const Chunk<DT> &r) const {
+        Vec<16> o;
+#pragma unroll
+        for (int j = 0; j < Pairs<DT>::kCount; ++j) {
+            const float2 t = fma2(pair_at<DT, ENTROPY>(r, j), slope, shift);
+            float2 d = make_float2(ex2(t.x), ex2(t.y));
+            d = mul2(d, ENTROPY ? fma2(B, t, A) : A);
+            if constexpr (DT == DT_F32) {
+                o.w[2 * j] = __float_as_uint(d.x);
+                o.w[2 * j + 1] = __float_as_uint(d.y);
+            } else {
+                o.w[j] = narrow<DT>(d);
+            }
+        }
+        return o;
+    }
+};
+template <int DT> __device__ __forceinline__ bool starts_alike(const void *out, const Share<DT> &sh) {
+    return (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(sh.row)) % 16 == 0;
+}
+
+// Writes the gradient of the block's share, which it reads (again).
+template <int DT, bool ENTROPY>
+__device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, const RowGrad &g, float a, float scale) {
     using T = typename ElemOf<DT>::type;
     T *out = static_cast<T *>(out_row);
-    const bool alike = (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(sh.row)) % 16 == 0;
-    if (g.w.careful || !alike) {
+    if (g.w.careful || !starts_alike(out, sh)) {
         write_grad_slowly<DT, ENTROPY>(sh, out_row, g, a, scale);
         return;
     }
-    const float2 slope = both(a), shift = both(-g.w.c), A2 = both(g.A), B2 = both(g.B);
-    const int turns = HELD ? 1 : (sh.end - sh.first + kTurn - 1) / kTurn;
-    for (int turn = 0; turn < turns; ++turn) {
-        const int c0 = sh.first + (REVERSE ? turns - 1 - turn : turn) * kTurn + static_cast<int>(threadIdx.x);
-        if constexpr (!HELD) {
+    const ChunkGrad<DT, ENTROPY> grad(g, a);
+    for (int c0 = sh.first + static_cast<int>(threadIdx.x); c0 < sh.end; c0 += kTurn) {
+        Chunk<DT> r[kFlight];
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u)
-                if (c0 + u * kThreads < sh.end) r[u] = sh.chunk(c0 + u * kThreads);
-        }
+        for (int u = 0; u < kFlight; ++u)
+            if (c0 + u * kThreads < sh.end) r[u] = sh.chunk(c0 + u * kThreads);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             if (c0 + u * kThreads >= sh.end) break;
-            Vec<16> o;
-#pragma unroll
-            for (int j = 0; j < Pairs<DT>::kCount; ++j) {
-                const float2 t = fma2(bounded_pair<DT>(r[u], j), slope, shift);
-                float2 d = make_float2(ex2(t.x), ex2(t.y));
-                d = mul2(d, ENTROPY ? fma2(B2, t, A2) : A2);
-                if constexpr (DT == DT_F32) {
-                    o.w[2 * j] = __float_as_uint(d.x);
-                    o.w[2 * j + 1] = __float_as_uint(d.y);
-                } else {
-                    o.w[j] = narrow<DT>(d);
-                }
-            }
-            st<16>(out + sh.column(c0 + u * kThreads, 0), o);
+            st<16>(out + sh.column(c0 + u * kThreads, 0), grad(r[u]));
         }
     }
     if (static_cast<int>(threadIdx.x) < sh.singles) {
@@ -680,13 +717,97 @@ __device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, c
     }
 }
 
+// ---------------------------------------------------------------- a share held in shared memory
+//
+// Up to kHeldTurns * 4 chunks a thread (64 KiB a block) are copied to shared
+// memory at once, asynchronously, and stay there between the sums and the
+// gradient: the row crosses DRAM once.  Each thread copies and reads its own
+// chunks only, so it waits for its own copies and needs no barrier; the copies
+// are in kHeldTurns groups, and the sums of the first are formed while the
+// others are on their way.
+
+constexpr int kHeldTurns = 4;
+constexpr int kHeldFlight = 4;
+constexpr int kHeldChunks = kHeldTurns * kHeldFlight * kThreads;
+
+template <int DT> __device__ __forceinline__ void copy_share(const Share<DT> &sh, uint4 *held) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(held));
+#pragma unroll
+    for (int g = 0; g < kHeldTurns; ++g) {
+#pragma unroll
+        for (int u = 0; u < kHeldFlight; ++u) {
+            const int at = (g * kHeldFlight + u) * kThreads + static_cast<int>(threadIdx.x);
+            if (sh.first + at < sh.end)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                             :: "r"(to + 16u * at), "l"(sh.row + sh.column(sh.first + at, 0)) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+}
+template <int LEFT> __device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
+}
+// The thread's chunks of group g.
+template <int DT>
+__device__ __forceinline__ void held_chunks(const Share<DT> &sh, const uint4 *held, int g, Chunk<DT> (&r)[kHeldFlight]) {
+#pragma unroll
+    for (int u = 0; u < kHeldFlight; ++u) {
+        const int at = (g * kHeldFlight + u) * kThreads + static_cast<int>(threadIdx.x);
+        r[u] = masked_chunk<DT>();
+        if (sh.first + at < sh.end) {
+            const uint4 w = held[at];
+            r[u] = Chunk<DT>{{w.x, w.y, w.z, w.w}};
+        }
+    }
+}
+template <int DT> __device__ __forceinline__ Sums sums_of_held(const Share<DT> &sh, const uint4 *held, float a) {
+    PairSums v = {kLeastExponent, both(0.0f), both(0.0f), masked_word<DT>()};
+    const bool single = static_cast<int>(threadIdx.x) < sh.singles;
+    const float one = single ? sh.at(sh.single(threadIdx.x)) : kNegInf;
+    Chunk<DT> r[kHeldFlight];
+    static_assert(kHeldTurns == 4, "one wait for each group below");
+    copies_left<3>();
+    held_chunks<DT>(sh, held, 0, r);
+    add_chunks<DT, false>(v, r, a);
+    copies_left<2>();
+    held_chunks<DT>(sh, held, 1, r);
+    add_chunks<DT, false>(v, r, a);
+    copies_left<1>();
+    held_chunks<DT>(sh, held, 2, r);
+    add_chunks<DT, false>(v, r, a);
+    copies_left<0>();
+    held_chunks<DT>(sh, held, 3, r);
+    add_chunks<DT, false>(v, r, a);
+    return finished<DT>(v, single, one, a);
+}
+template <int DT>
+__device__ __forceinline__ void write_grad_of_held(const Share<DT> &sh, const uint4 *held, void *out_row, const RowGrad &g,
+                                                   float a, float scale) {
+    using T = typename ElemOf<DT>::type;
+    T *out = static_cast<T *>(out_row);
+    if (g.w.careful || !starts_alike(out, sh)) {
+        write_grad_slowly<DT, false>(sh, out_row, g, a, scale);
+        return;
+    }
+    const ChunkGrad<DT, false> grad(g, a);
+#pragma unroll 4
+    for (int c = sh.first + static_cast<int>(threadIdx.x); c < sh.end; c += kThreads) {
+        const uint4 w = held[c - sh.first];
+        st<16>(out + sh.column(c, 0), grad(Chunk<DT>{{w.x, w.y, w.z, w.w}}));
+    }
+    if (static_cast<int>(threadIdx.x) < sh.singles) {
+        const int col = sh.single(threadIdx.x);
+        store_one<DT>(out, col, grad_of<false>(g, sh.at(col), a, scale));
+    }
+}
+
 // dlogits = scale (dlogp (1_token - p) - dentropy p (log p + H)).
 template <int DT, bool ENTROPY>
-__global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(LogprobGradArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(LogprobGradArgs a, Split split) {
     enter_grid();
-    const int block = static_cast<int>(blockIdx.x % blocks);
-    const int64_t row = blockIdx.x / blocks;
-    const Share<DT> sh(row_of<DT>(a.logits, row, a.stride), a.cols, block, blocks);
+    const int blocks = split.blocks(), block = blockIdx.x & (blocks - 1);
+    const int64_t row = blockIdx.x >> split.shift;
+    const Share<DT> sh(row_of<DT>(a.logits, row, a.stride), a.cols, block, split);
     void *out = row_of<DT>(a.dlogits, row, a.dstride);
     const float ax = a.scale * kLog2e;
     int64_t token = a.dlogp ? token_at(a.tokens, a.i64, row) : -1;
@@ -694,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(Logpr
     const float dlogp = token >= 0 ? a.dlogp[row] : 0.0f;
     const float lse = a.lse[row];
     if (lse == kNegInf) {  // nothing depends on the logits of an empty row
-        write_zeros<DT>(out, a.cols, block, blocks);
+        write_zeros<DT>(out, a.cols, block, split);
         return;
     }
     const RowGrad r = row_grad(weights_of(lse, a.scale), -a.scale * dlogp, ENTROPY ? a.scale * a.dentropy[row] : 0.0f,
@@ -702,8 +823,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(Logpr
     const bool here = token >= 0 && sh.holds(static_cast<int>(token));
     const float x = here ? sh.at(static_cast<int>(token)) : 0.0f;  // read before it may be overwritten
     if (here) __syncthreads();                                     // uniform: all threads have the same token
-    Chunk<DT> chunks[kFlight];
-    write_grad<DT, ENTROPY, false, false>(sh, out, r, ax, a.scale, chunks);
+    write_grad<DT, ENTROPY>(sh, out, r, ax, a.scale);
     if (!here) return;
     __syncthreads();
     if (threadIdx.x == 0)
@@ -716,56 +836,39 @@ __global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(Logpr
 // row, both of values times `scale`:
 //     loss = sum q_i (log q_i - log p(id_i)),   dlogits = dloss scale (p - q).
 // Entries with an id outside the row or a value of -inf do not count; a row
-// without any has loss 0 and gradient 0.  HELD: a block's share is one turn and
-// stays in registers between the sums and the gradient; longer shares are read
-// twice, the second time from L2.
+// without any has loss 0 and gradient 0.  HELD: each block's share of the row
+// stays in shared memory; rows beyond 8 blocks' 512 KiB are read twice.
 
+// Dynamic shared memory: the held share, then per teacher's entry the student's
+// column, the scaled value and the student's logit.
 struct Teacher {
-    int id[kMostTeacher];
-    float t[kMostTeacher];  // scaled value
-    float x[kMostTeacher];  // the student's logit there
+    int *id;
+    float *t, *x;
+    __device__ __forceinline__ Teacher(void *at, int k) : id(static_cast<int *>(at)), t(static_cast<float *>(at) + k),
+                                                          x(static_cast<float *>(at) + 2 * k) {}
 };
-
-// Largest value and the sum of e^(value - largest), and two of them together.
-struct Softmax {
-    float top, sum;
-};
-__device__ __forceinline__ Softmax merged(Softmax a, Softmax b) {
-    const float top = max_nan(a.top, b.top);
-    // equal ones, both of them -inf among these, keep their sum
-    const float fa = a.top == top ? 1.0f : expf(a.top - top), fb = b.top == top ? 1.0f : expf(b.top - top);
-    return {top, fmaf(a.sum, fa, b.sum * fb)};
-}
-__device__ __forceinline__ Softmax warp_softmax(Softmax v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        const Softmax o = {__shfl_xor_sync(kAllLanes, v.top, d), __shfl_xor_sync(kAllLanes, v.sum, d)};
-        // a fixed order of the two makes both lanes' bits the same
-        v = (threadIdx.x & d) ? merged(o, v) : merged(v, o);
-    }
-    return v;
-}
 
 template <int DT, bool SUMS, bool GRAD, bool HELD>
-__global__ void __launch_bounds__(kThreads, kResident) distill_kernel(DistillArgs a, int blocks) {
+__global__ void __launch_bounds__(kThreads, HELD ? 3 : kResident) distill_kernel(DistillArgs a, Split split) {
     enter_grid();
+    extern __shared__ uint4 held[];
     __shared__ Sums part[kWarps];
-    __shared__ Softmax tpart[kWarps];
     __shared__ Sums mine;
     __shared__ float fpart[2][32];
-    __shared__ Teacher th;
-    const int block = static_cast<int>(blockIdx.x % blocks);
-    const int64_t row = blockIdx.x / blocks;
+    const Teacher th(held + (HELD ? split.each : 0), a.k);
+    const int blocks = split.blocks(), block = blockIdx.x & (blocks - 1);
+    const int64_t row = blockIdx.x >> split.shift;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const void *logits = row_of<DT>(a.logits, row, a.stride);
-    const Share<DT> sh(logits, a.cols, block, blocks);
+    const Share<DT> sh(logits, a.cols, block, split);
     const float ax = a.scale * kLog2e;
 
-    Chunk<DT> chunks[kFlight];  // on their way while the teacher's entries are
-    if constexpr (SUMS) load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), chunks);
+    Chunk<DT> first_turn[kFlight];  // on its way, as the held share is, while the teacher's entries are
+    if constexpr (HELD) copy_share<DT>(sh, held);
+    else if constexpr (SUMS) load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), first_turn);
 
-    // the teacher's entries; every block has them all
-    Softmax q = {kNegInf, 0.0f};
+    // The teacher's entries; every block has them all.  Of the student's logits
+    // the loss (block 0) needs all, the gradient those that this block writes.
     for (int i = threadIdx.x; i < a.k; i += kThreads) {
         const int64_t id = token_at(a.ids, a.i64, row * a.ids_stride + i);
         const int64_t at = row * a.teacher_stride + i;
@@ -773,31 +876,29 @@ __global__ void __launch_bounds__(kThreads, kResident) distill_kernel(DistillArg
         if (DT == DT_F32 || a.teacher_f32) v = static_cast<const float *>(a.teacher)[at];
         else v = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(a.teacher)[at]);
         const bool given = id >= 0 && id < a.cols && v != kNegInf;
-        // the loss needs all the student's logits there, the gradient those that this block writes
         const bool read = given && ((SUMS && block == 0) || sh.holds(static_cast<int>(id)));
-        v *= a.scale;
         th.id[i] = given ? static_cast<int>(id) : -1;
-        th.t[i] = v;
+        th.t[i] = given ? v * a.scale : kNegInf;
         th.x[i] = read ? sh.at(static_cast<int>(id)) : 0.0f;
-        if (given) q = merged(q, Softmax{v, 1.0f});
     }
     Sums v = no_sums();
-    if constexpr (SUMS) v = warp_sums(pass_over<DT, false, false>(sh, ax, nullptr, 0, chunks));
-    q = warp_softmax(q);
-    if (lane == 0) {
-        part[warp] = v;
-        tpart[warp] = q;
-    }
+    if constexpr (HELD) v = warp_sums<32>(sums_of_held<DT>(sh, held, ax));
+    else if constexpr (SUMS) v = warp_sums<32>(pass_over<DT, false, false>(sh, ax, nullptr, 0, first_turn));
+    if (lane == 0) part[warp] = v;
     __syncthreads();
-    q = warp_softmax(lane < kWarps ? tpart[lane] : Softmax{kNegInf, 0.0f});
-    const bool any = q.top != kNegInf;
-    const float log_sum = logf(q.sum);
-    auto log_q = [&](int i) { return th.t[i] - q.top - log_sum; };
+    // its softmax, by each warp for itself
+    float teacher_top = kNegInf, teacher_sum = 0.0f;
+    for (int i = lane; i < a.k; i += 32) teacher_top = max_nan(teacher_top, th.t[i]);
+    teacher_top = lanes_max_nan(teacher_top, 32);
+    const bool any = teacher_top != kNegInf;
+    for (int i = lane; any && i < a.k; i += 32) teacher_sum += expf(th.t[i] - teacher_top);
+    const float teacher_log_sum = logf(warp_sum(teacher_sum));
+    auto log_q = [&](int i) { return th.t[i] - teacher_top - teacher_log_sum; };
 
     Weights w;
     RowSum r;
     if constexpr (SUMS) {
-        v = warp_sums(lane < kWarps ? part[lane] : no_sums());
+        v = sums_of_warps(part);
         if (blocks > 1) {
             if (threadIdx.x == 0) mine = v;
             cluster_sync();
@@ -823,20 +924,19 @@ __global__ void __launch_bounds__(kThreads, kResident) distill_kernel(DistillArg
                 __syncthreads();
             }
         }
-        if (any) write_grad<DT, false, true, HELD>(sh, out, rg, ax, a.scale, chunks);
-        else write_zeros<DT>(out, a.cols, block, blocks);
+        if (!any) write_zeros<DT>(out, a.cols, block, split);
+        else if constexpr (HELD) write_grad_of_held<DT>(sh, held, out, rg, ax, a.scale);
+        else write_grad<DT, false>(sh, out, rg, ax, a.scale);
         __syncthreads();
         // entries of one id add up; the first of them writes
         for (int i = threadIdx.x; any && i < a.k; i += kThreads) {
             const int id = th.id[i];
             if (id < 0 || !sh.holds(id)) continue;
             bool first = true;
-            float qs = 0.0f;
-            for (int j = 0; j < a.k; ++j) {
-                if (th.id[j] != id) continue;
-                if (j < i) { first = false; break; }
-                qs += expf(log_q(j));
-            }
+            for (int j = 0; j < i; ++j) first = first && th.id[j] != id;
+            float qs = expf(log_q(i));
+            for (int j = i + 1; j < a.k; ++j)
+                if (th.id[j] == id) qs += expf(log_q(j));
             if (first) store_one<DT>(out, id, rg.g * (p_of(w, th.x[i], ax) - qs));
         }
     }
@@ -863,10 +963,14 @@ __global__ void __launch_bounds__(kThreads, kResident) distill_kernel(DistillArg
 
 // Blocks a row: one where the rows alone fill the device, up to a cluster of 8
 // where they are few, each with a turn's worth of 2048 elements at least.
-inline int blocks_per_row(int64_t rows, int cols, int sms) {
-    int blocks = 1;
-    while (blocks < 8 && rows * blocks < kResident * static_cast<int64_t>(sms) && cols / (2 * blocks) >= 4096) blocks *= 2;
-    return blocks;
+inline int split_shift(int64_t rows, int cols, int sms) {
+    int shift = 0;
+    while (shift < 3 && (rows << shift) < kResident * static_cast<int64_t>(sms) && (cols >> (shift + 1)) >= 4096) ++shift;
+    return shift;
+}
+template <int DT> Split split_of(int cols, int shift) {
+    const int chunks = cols / Chunk<DT>::kElems;
+    return {shift, (chunks >> shift) + ((chunks & ((1 << shift) - 1)) != 0)};
 }
 inline void describe(LaunchInfo *info, int64_t grid) {
     info->grid = static_cast<int>(grid);
@@ -875,33 +979,41 @@ inline void describe(LaunchInfo *info, int64_t grid) {
 }
 
 template <int DT> cudaError_t logprob_launch(const LogprobArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
-    const int blocks = blocks_per_row(a.rows, a.cols, sms);
-    const int64_t grid = a.rows * blocks;
+    const Split split = split_of<DT>(a.cols, split_shift(a.rows, a.cols, sms));
+    const int64_t grid = a.rows << split.shift;
     describe(info, grid);
-    return a.top > 0 ? launch_rows(logprob_kernel<DT, true>, dim3(grid), dim3(kThreads), 0, blocks, s, a, blocks)
-                     : launch_rows(logprob_kernel<DT, false>, dim3(grid), dim3(kThreads), 0, blocks, s, a, blocks);
+    auto kernel = a.top > 0 ? logprob_kernel<DT, true> : logprob_kernel<DT, false>;
+    return launch_rows(kernel, dim3(grid), dim3(kThreads), 0, split.blocks(), s, a, split);
 }
 template <int DT> cudaError_t logprob_grad_launch(const LogprobGradArgs &a, cudaStream_t s, LaunchInfo *info) {
-    // no sums: blocks of about 16384 elements, no cluster
-    const int blocks = std::max<int>(1, std::min<int64_t>(a.cols / 16384, INT32_MAX / a.rows));
-    const int64_t grid = a.rows * blocks;
+    // no sums: blocks of 16384 to 32768 elements, no cluster
+    int shift = 0;
+    while ((a.cols >> (shift + 1)) >= 16384 && a.rows << (shift + 1) <= INT32_MAX) ++shift;
+    const Split split = split_of<DT>(a.cols, shift);
+    const int64_t grid = a.rows << shift;
     describe(info, grid);
-    return a.dentropy ? launch_rows(logprob_grad_kernel<DT, true>, dim3(grid), dim3(kThreads), 0, 1, s, a, blocks)
-                      : launch_rows(logprob_grad_kernel<DT, false>, dim3(grid), dim3(kThreads), 0, 1, s, a, blocks);
+    auto kernel = a.dentropy ? logprob_grad_kernel<DT, true> : logprob_grad_kernel<DT, false>;
+    return launch_rows(kernel, dim3(grid), dim3(kThreads), 0, 1, s, a, split);
 }
 template <int DT>
 cudaError_t distill_launch(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info) {
-    const int blocks = blocks_per_row(a.rows, a.cols, sms);
-    // Rows are not split further to be held: 2048 rows of 65536 bf16 in clusters
-    // of 4 that hold them take 190 us, in one block that reads them twice 105 us.
-    const bool held = a.cols / Chunk<DT>::kElems <= static_cast<int64_t>(kTurn) * blocks;
-    const int64_t grid = a.rows * blocks;
+    // The loss alone splits and sums its rows as loss and gradient in one call
+    // do, so both give the same bits.
+    int shift = split_shift(a.rows, a.cols, sms);
+    const int chunks = a.cols / Chunk<DT>::kElems;
+    const bool held = sums && chunks <= 8 * kHeldChunks && a.rows << 3 <= INT32_MAX;
+    while (held && chunks > kHeldChunks << shift) ++shift;
+    const Split split = split_of<DT>(a.cols, shift);
+    const int64_t grid = a.rows << shift;
     describe(info, grid);
-    const dim3 g(grid), b(kThreads);
-    if (!sums) return launch_rows(distill_kernel<DT, false, true, false>, g, b, 0, blocks, s, a, blocks);
-    if (!grad) return launch_rows(distill_kernel<DT, true, false, false>, g, b, 0, blocks, s, a, blocks);
-    return held ? launch_rows(distill_kernel<DT, true, true, true>, g, b, 0, blocks, s, a, blocks)
-                : launch_rows(distill_kernel<DT, true, true, false>, g, b, 0, blocks, s, a, blocks);
+    const size_t smem = static_cast<size_t>(held ? split.each : 0) * 16 + static_cast<size_t>(a.k) * 12;
+    info->smem = static_cast<int>(smem);
+    auto kernel = distill_kernel<DT, false, true, false>;
+    if (sums && !grad) kernel = held ? distill_kernel<DT, true, false, true> : distill_kernel<DT, true, false, false>;
+    if (sums && grad) kernel = held ? distill_kernel<DT, true, true, true> : distill_kernel<DT, true, true, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kHeldChunks * 16 + kMostTeacher * 12);
+    return e != cudaSuccess ? e : launch_rows(kernel, dim3(grid), dim3(kThreads), smem, split.blocks(), s, a, split);
 }
 
 }  // namespace
