@@ -24,7 +24,8 @@ OBJ_DIR = os.path.join(OUT_DIR, "obj")
 SOURCES = ["ew_api.cu", "ew_kernels_f32.cu", "ew_kernels_f16.cu", "ew_kernels_bf16.cu", "ew_tma.cu",
            "ew_gather_fixed.cu", "ew_gather_fixed_wide.cu", "ew_rows_api.cu", "ew_rows.cu", "ew_embed.cu",
            "ew_norm_f32.cu", "ew_norm_f16.cu", "ew_norm_bf16.cu",
-           "ew_logits_f32.cu", "ew_logits_f16.cu", "ew_logits_bf16.cu"]
+           "ew_logits_f32.cu", "ew_logits_f16.cu", "ew_logits_bf16.cu",
+           "ew_distill_f32.cu", "ew_distill_f16.cu", "ew_distill_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-fmad=false",

@@ -1,0 +1,463 @@
+// ew_distill.cuh -- distillation from a teacher's top logits, loss and gradient.
+// Compiled once per element type.
+//
+// q = softmax of the teacher's values at its ids, p = softmax of the student's
+// row, both of values times `scale`:
+//     loss = sum q_i (log q_i - log p(id_i)),   dlogits = dloss scale (p - q).
+// Entries with an id outside the row or a value of -inf do not count; a row
+// without any has loss 0 and gradient 0.
+//
+// The gradient needs the row's sums, so a row is worked over twice.  At the
+// floor it crosses DRAM once: distill_stream_kernel keeps it in shared memory
+// in between.  distill_kernel reads it again, for rows too short to be worth
+// a block of their own, rows too long, and the gradient from a given lse.
+#pragma once
+
+#include "ew_logits.cuh"
+
+namespace ew {
+namespace {
+
+// What a block has of a row's teacher: for each entry the student's column
+// (-1: does not count), the scaled value (-inf) and the student's logit.
+struct Teacher {
+    int *id;
+    float *t, *x;
+    __device__ __forceinline__ Teacher(void *at, int k) : id(static_cast<int *>(at)), t(static_cast<float *>(at) + k),
+                                                          x(static_cast<float *>(at) + 2 * k) {}
+};
+struct TeacherEntry {
+    int id;
+    float t;
+};
+// An entry as it lies in memory; what it says is worked out when it is needed,
+// so that reading it ahead does not wait for it.
+template <int DT> struct RawEntry {
+    int64_t id;
+    uint32_t value;
+    __device__ __forceinline__ void read(const DistillArgs &a, int64_t row, int i) {
+        id = token_at(a.ids, a.i64, row * a.ids_stride + i);
+        const int64_t at = row * a.teacher_stride + i;
+        if (DT == DT_F32 || a.teacher_f32) value = static_cast<const uint32_t *>(a.teacher)[at];
+        else value = static_cast<const typename ElemOf<DT>::type *>(a.teacher)[at];
+    }
+    __device__ __forceinline__ TeacherEntry entry(const DistillArgs &a) const {
+        float v;
+        if (DT == DT_F32 || a.teacher_f32) v = __uint_as_float(value);
+        else v = elem_to_f32<DT>(static_cast<typename ElemOf<DT>::type>(value));
+        const bool given = id >= 0 && id < a.cols && v != kNegInf;
+        return {given ? static_cast<int>(id) : -1, given ? v * a.scale : kNegInf};
+    }
+};
+
+// The softmax of the teacher's k values, by each warp that needs it for itself.
+// An entry counts where `any` is true.
+struct TeacherSum {
+    float top, log_sum;
+    __device__ __forceinline__ float log_q(float t) const { return t - top - log_sum; }
+};
+__device__ __forceinline__ TeacherSum teacher_sum(const float *t, int k) {
+    const int lane = threadIdx.x & 31;
+    float top = kNegInf, sum = 0.0f;
+    for (int i = lane; i < k; i += 32) top = max_nan(top, t[i]);
+    top = lanes_max_nan(top, 32);
+    for (int i = lane; i < k; i += 32) sum += t[i] == kNegInf ? 0.0f : expf(t[i] - top);
+    return {top, logf(warp_sum(sum))};
+}
+// Called by one warp: the row's loss, to all its lanes.
+__device__ __forceinline__ float loss_of(const Teacher &th, int k, const RowSum &r, float a, float scale) {
+    const TeacherSum q = teacher_sum(th.t, k);
+    const bool empty = r.careful && r.top == kNegInf;
+    float loss = 0.0f;
+    for (int i = threadIdx.x & 31; i < k; i += 32) {
+        const float logq = q.log_q(th.t[i]), qi = th.id[i] >= 0 ? expf(logq) : 0.0f;
+        const float logp = empty ? kNegInf : logp_of(r, th.x[i], a, scale);
+        if (qi != 0.0f) loss += qi * (logq - logp);
+    }
+    return warp_sum(loss);
+}
+// The teacher's columns of the block's share, by the block's last threads
+// (its first warp has the loss to do).  Entries of one id add up; the first of
+// them writes.
+template <int DT>
+__device__ __forceinline__ void write_teacher_columns(const Share<DT> &sh, void *out, const Teacher &th, int k,
+                                                      const RowGrad &g, float a) {
+    const int me = static_cast<int>(blockDim.x - 1 - threadIdx.x);
+    if ((me & ~31) >= k) return;  // no entry for this warp
+    const TeacherSum q = teacher_sum(th.t, k);
+    for (int i = me; i < k; i += blockDim.x) {
+        const int id = th.id[i];
+        if (id < 0 || !sh.holds(id)) continue;
+        int alike = 0, earlier = 0;
+#pragma unroll 8
+        for (int j = 0; j < k; ++j) {
+            const int same = th.id[j] == id;
+            alike += same;
+            earlier += same && j < i;
+        }
+        if (earlier) continue;
+        float qs = expf(q.log_q(th.t[i]));
+        for (int j = i + 1; alike > 1 && j < k; ++j)
+            if (th.id[j] == id) qs += expf(q.log_q(th.t[j]));
+        store_one<DT>(out, id, g.g * (p_of(g.w, th.x[i], a) - qs));
+    }
+}
+
+// ---------------------------------------------------------------- rows read twice
+
+template <int DT, bool SUMS, bool GRAD>
+__global__ void __launch_bounds__(kThreads, kResident) distill_kernel(DistillArgs a, Split split) {
+    enter_grid();
+    extern __shared__ uint4 dynamic[];
+    __shared__ Sums part[kWarps];
+    __shared__ Sums mine;
+    __shared__ float fpart[32];
+    const Teacher th(dynamic, a.k);
+    const int blocks = split.blocks(), block = blockIdx.x & (blocks - 1);
+    const int64_t row = blockIdx.x >> split.shift;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const void *logits = row_of<DT>(a.logits, row, a.stride);
+    const Share<DT> sh(logits, a.cols, block, split);
+    const float ax = a.scale * kLog2e;
+
+    Chunk<DT> first_turn[kFlight];  // on its way while the teacher's entries are
+    if constexpr (SUMS) load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), first_turn);
+    // Every block has all entries; of the student's logits the loss (block 0)
+    // needs all, the gradient those that this block writes.
+    bool mine_counts = false;
+    for (int i = threadIdx.x; i < a.k; i += kThreads) {
+        RawEntry<DT> raw;
+        raw.read(a, row, i);
+        const TeacherEntry e = raw.entry(a);
+        const bool read = e.id >= 0 && ((SUMS && block == 0) || sh.holds(e.id));
+        th.id[i] = e.id;
+        th.t[i] = e.t;
+        th.x[i] = read ? sh.at(e.id) : 0.0f;
+        mine_counts = mine_counts || e.id >= 0;
+    }
+    Sums v = no_sums();
+    if constexpr (SUMS) v = warp_sums<32, false>(pass_over<DT, false, false>(sh, ax, nullptr, 0, first_turn));
+    if (lane == 0) part[warp] = v;
+    const bool any = __syncthreads_or(mine_counts);
+
+    Weights w;
+    RowSum r;
+    if constexpr (SUMS) {
+        v = sums_of_warps<kWarps, false>(part);
+        if (blocks > 1) {
+            if (threadIdx.x == 0) mine = v;
+            cluster_sync();
+            v = cluster_sums<false>(&mine, blocks);
+            cluster_arrive();  // the wait is further down: mine has been read
+        }
+        r = finish_row<DT>(v, logits, a.cols, ax, fpart);
+        w = {r.c, r.inv_s, r.top, r.careful};
+        if (block == 0 && warp == 0) {
+            const float loss = loss_of(th, a.k, r, ax, a.scale);
+            if (lane == 0) {
+                a.loss[row] = any ? loss : 0.0f;
+                a.lse[row] = r.careful && r.top == kNegInf ? kNegInf : lse_of(r, a.scale);
+            }
+        }
+    } else {
+        w = weights_of(a.lse[row], a.scale);
+    }
+    if constexpr (GRAD) {
+        const RowGrad rg = row_grad(w, any ? a.dloss[row] * a.scale : 0.0f, 0.0f, 0.0f, 0.0f);
+        void *out = row_of<DT>(a.dlogits, row, a.dstride);
+        // a careful row has been read whole by every block: all are done with it before any writes in place
+        if (SUMS && w.careful) {
+            if (blocks > 1) {
+                cluster_wait();
+                cluster_sync();
+                cluster_arrive();
+            } else {
+                __syncthreads();
+            }
+        }
+        if (any) {
+            write_grad<DT, false>(sh, out, rg, ax, a.scale);
+            __syncthreads();
+            write_teacher_columns<DT>(sh, out, th, a.k, rg, ax);
+        } else {
+            write_zeros<DT>(out, a.cols, block, split);
+        }
+    }
+    if (SUMS && blocks > 1) cluster_wait();
+}
+
+// ---------------------------------------------------------------- rows held in shared memory
+//
+// One block of 512 threads an SM (or a cluster of up to 8 for a row) walks over
+// rows.  Its share of a row is `groups` groups of 4 chunks a thread (32 KiB);
+// a ring of kRing groups is filled by asynchronous copies in the order of the
+// stream of groups, row after row, and a group's place is filled again as
+// soon as the gradient (or, for the loss alone, the sum) has used it.  So
+// kRing - groups groups of rows to come are on their way at any time, through
+// the reductions too.  Each thread copies and reads its own chunks only: it
+// waits for its own copies and needs no barrier for them.
+//
+// A row has one barrier, between its sums and its gradient.  Between two of
+// them a thread writes one row's gradient and sums the next row, while single
+// warps do what is left of the row before: its loss, and the teacher's columns,
+// whose gradient has to come after all others' stores.  The next row's teacher
+// is read ahead into registers.
+
+constexpr int kStreamThreads = 512;
+constexpr int kStreamWarps = kStreamThreads / 32;
+constexpr int kGroup = 4;
+constexpr int kGroupChunks = kGroup * kStreamThreads;
+constexpr int kRing = 6;
+
+template <int LEFT> __device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
+}
+
+template <int DT, bool GRAD>
+__global__ void __launch_bounds__(kStreamThreads, 1) distill_stream_kernel(DistillArgs a, Split split, int groups) {
+    using T = typename ElemOf<DT>::type;
+    enter_grid();
+    extern __shared__ uint4 dynamic[];
+    __shared__ Sums part[2][kStreamWarps];
+    __shared__ Sums mine[2];
+    __shared__ float fpart[32];
+    uint4 *ring = dynamic + threadIdx.x;
+    const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    char *teachers = reinterpret_cast<char *>(dynamic + kRing * kGroupChunks);
+    const int blocks = split.blocks(), block = blockIdx.x & (blocks - 1);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t step = gridDim.x >> split.shift, first_row = blockIdx.x >> split.shift;
+    const float ax = a.scale * kLog2e;
+    // this thread's entry of a teacher: not the first warps', which have the losses to do
+    const int entry = static_cast<int>(threadIdx.x + kStreamThreads / 2) % kStreamThreads;
+
+    auto share_of = [&](int64_t row) {
+        return Share<DT>(row_of<DT>(a.logits, row, a.stride), a.cols, block, split);
+    };
+    // the next group of the stream into the ring; past the last row an empty one, so that the count holds
+    int64_t copy_row = first_row;
+    int copy_group = 0, copy_place = 0, copy_count = 0;  // chunks of this thread's row from its next one on
+    const T *copy_from = nullptr;
+    auto start_copies = [&] {
+        copy_count = 0;
+        if (copy_row < a.rows) {
+            const Share<DT> sh = share_of(copy_row);
+            copy_from = sh.row + sh.column(sh.first + static_cast<int>(threadIdx.x), 0);
+            copy_count = sh.end - sh.first - static_cast<int>(threadIdx.x);
+        }
+    };
+    auto copy_next = [&] {
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+            if (u * kStreamThreads < copy_count)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                             :: "r"(ring_at + (copy_place * kGroup + u) * kStreamThreads * 16),
+                                "l"(copy_from + u * kStreamThreads * Chunk<DT>::kElems) : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        copy_from += kGroupChunks * Chunk<DT>::kElems;
+        copy_count -= kGroupChunks;
+        if (++copy_group == groups) {
+            copy_group = 0;
+            copy_row += step;
+            start_copies();
+        }
+        if (++copy_place == kRing) copy_place = 0;
+    };
+    start_copies();
+    auto held = [&](int place, int u) {
+        const uint4 w = ring[(place * kGroup + u) * kStreamThreads];
+        return Chunk<DT>{{w.x, w.y, w.z, w.w}};
+    };
+#pragma unroll 1
+    for (int q = 0; q < kRing; ++q) copy_next();
+    RawEntry<DT> next = {};
+    if (entry < a.k && first_row < a.rows) next.read(a, first_row, entry);
+
+    int place0 = 0;           // the ring's place of the row's first group
+    int turn = 0, third = 0;  // the row's number modulo 2 and 3
+    auto teacher_of = [&](int third) { return Teacher(teachers + third * a.k * 12, a.k); };
+    // what is left to do of the row before, after the barrier that all its stores precede
+    bool left = false;
+    RowGrad left_grad = {};
+    auto finish_left = [&](int64_t row, int third) {
+        if (GRAD && left)
+            write_teacher_columns<DT>(share_of(row), row_of<DT>(a.dlogits, row, a.dstride), teacher_of(third), a.k, left_grad, ax);
+    };
+
+    for (int64_t row = first_row; row < a.rows; row += step) {
+        const void *logits = row_of<DT>(a.logits, row, a.stride);
+        const Share<DT> sh = share_of(row);
+        const Teacher th = teacher_of(third);
+        // every block has all entries; of the student's logits the loss (block 0)
+        // needs all, the gradient those that this block writes
+        const TeacherEntry e = entry < a.k ? next.entry(a) : TeacherEntry{-1, kNegInf};
+        float x = 0.0f;
+        if (e.id >= 0 && (block == 0 || (GRAD && sh.holds(e.id)))) x = sh.at(e.id);
+        const bool single = static_cast<int>(threadIdx.x) < sh.singles;
+        const float one = single ? sh.at(sh.single(threadIdx.x)) : kNegInf;
+        if (entry < a.k && row + step < a.rows) next.read(a, row + step, entry);
+        const float dloss = GRAD ? a.dloss[row] : 0.0f;
+
+        PairSums pairs = {kLeastExponent, both(0.0f), both(0.0f)};
+        auto add_group = [&](int g) {
+            int place = place0 + g;
+            if (place >= kRing) place -= kRing;
+            Chunk<DT> r[kGroup];
+            const int c0 = sh.first + g * kGroupChunks;
+            if (c0 + kGroupChunks <= sh.end) {
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) r[u] = held(place, u);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u)
+                    r[u] = c0 + u * kStreamThreads + static_cast<int>(threadIdx.x) < sh.end ? held(place, u) : masked_chunk<DT>();
+            }
+            add_chunks<DT, false>(pairs, r, ax);
+            if (!GRAD) copy_next();
+        };
+        // Group g of the row is complete when only the groups after it are left:
+        // kRing - 1 - g have been asked for since, or, with one more for each
+        // group that the loss alone has used, kRing - 1.
+        static_assert(kRing == 6, "one wait for each group below");
+        copies_left<5>();
+        add_group(0);
+        if (groups > 1) { copies_left<GRAD ? 4 : 5>(); add_group(1); }
+        if (groups > 2) { copies_left<GRAD ? 3 : 5>(); add_group(2); }
+        if (groups > 3) { copies_left<GRAD ? 2 : 5>(); add_group(3); }
+        if (groups > 4) { copies_left<GRAD ? 1 : 5>(); add_group(4); }
+        if (groups > 5) { copies_left<GRAD ? 0 : 5>(); add_group(5); }
+
+        Sums v = warp_sums<32, false>(finished<DT>(pairs, single, one, ax));
+        if (lane == 0) part[turn][warp] = v;
+        if (entry < a.k) {
+            th.id[entry] = e.id;
+            th.t[entry] = e.t;
+            th.x[entry] = x;
+        }
+        const bool any = __syncthreads_or(e.id >= 0);
+        v = sums_of_warps<kStreamWarps, false>(part[turn]);
+        if (blocks > 1) {
+            if (threadIdx.x == 0) mine[turn] = v;
+            cluster_sync();  // the next row's keeps mine[turn] from being written before all have read it
+            v = cluster_sums<false>(&mine[turn], blocks);
+        }
+        const RowSum r = finish_row<DT>(v, logits, a.cols, ax, fpart);
+        // a careful row has been read whole by every block: all are done with it before any writes in place
+        if (r.careful && blocks > 1) cluster_sync();
+        if (row != first_row) finish_left(row - step, third == 0 ? 2 : third - 1);
+        if (block == 0 && warp == 0) {
+            const float loss = loss_of(th, a.k, r, ax, a.scale);
+            if (lane == 0) {
+                a.loss[row] = any ? loss : 0.0f;
+                a.lse[row] = r.careful && r.top == kNegInf ? kNegInf : lse_of(r, a.scale);
+            }
+        }
+        if constexpr (GRAD) {
+            T *out = static_cast<T *>(row_of<DT>(a.dlogits, row, a.dstride));
+            const RowGrad rg = row_grad({r.c, r.inv_s, r.top, r.careful}, any ? dloss * a.scale : 0.0f, 0.0f, 0.0f, 0.0f);
+            const bool fast = any && !r.careful, alike = starts_alike(out, sh);
+            const ChunkGrad<DT, false> grad(rg, ax);
+#pragma unroll 1
+            for (int g = 0; g < groups; ++g) {
+                int place = place0 + g;
+                if (place >= kRing) place -= kRing;
+                if (fast) {
+                    const int c0 = sh.first + g * kGroupChunks + static_cast<int>(threadIdx.x);
+                    T *to = out + sh.column(c0, 0);
+                    if (sh.first + (g + 1) * kGroupChunks <= sh.end) {
+#pragma unroll
+                        for (int u = 0; u < kGroup; ++u) store_chunk<DT>(to + u * kStreamThreads * Chunk<DT>::kElems, grad(held(place, u)), alike);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < kGroup; ++u)
+                            if (c0 + u * kStreamThreads < sh.end) store_chunk<DT>(to + u * kStreamThreads * Chunk<DT>::kElems, grad(held(place, u)), alike);
+                    }
+                }
+                copy_next();  // into this group's place
+            }
+            if (fast) {
+                if (single) store_one<DT>(out, sh.single(threadIdx.x), grad_of<false>(rg, one, ax, a.scale));
+            } else if (any) {
+                write_grad_slowly<DT, false>(sh, out, rg, ax, a.scale);
+            } else {
+                write_zeros<DT>(out, a.cols, block, split);
+            }
+            left = any;
+            left_grad = rg;
+        }
+        place0 += groups;
+        if (place0 >= kRing) place0 -= kRing;
+        turn ^= 1;
+        third = third == 2 ? 0 : third + 1;
+    }
+    copies_left<0>();
+    __syncthreads();
+    const int64_t last_row = first_row + (a.rows - 1 - first_row) / step * step;
+    if (first_row < a.rows) finish_left(last_row, third == 0 ? 2 : third - 1);
+    if (blocks > 1) cluster_sync();  // no block leaves while its sums are read
+}
+
+// ---------------------------------------------------------------- launches
+
+// Rows that are worked on at once: one an SM, or as many clusters of a row's
+// blocks as fit the device (a cluster lies within one of its partitions).
+template <typename Kernel> cudaError_t rows_at_once(Kernel kernel, int shift, size_t smem, int sms, int *rows) {
+    if (shift == 0) {
+        *rows = sms;
+        return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms >> shift << shift);
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 1u << shift;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(rows, kernel, &cfg);
+}
+
+template <int DT>
+cudaError_t distill_launch(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info) {
+    // The loss alone splits and sums its rows as loss and gradient in one call
+    // do, so both give the same bits.
+    const int chunks = a.cols / Chunk<DT>::kElems;
+    auto groups_of = [&](int shift) { return std::max(1, (split_of<DT>(a.cols, shift).each + kGroupChunks - 1) / kGroupChunks); };
+    int shift = 0;
+    if (sums && chunks >= kTurn && a.k <= kStreamThreads) {
+        // at most 4 groups, so that 2 are on their way; then more blocks a row while SMs are left
+        while (shift < 3 && groups_of(shift) > 4) ++shift;
+        while (shift < 3 && a.rows << (shift + 1) <= sms && a.cols >> (shift + 1) >= 4096) ++shift;
+        const int groups = groups_of(shift);
+        if (groups <= kRing) {
+            const Split split = split_of<DT>(a.cols, shift);
+            const size_t smem = static_cast<size_t>(kRing) * kGroupChunks * 16 + static_cast<size_t>(a.k) * 36;
+            auto kernel = grad ? distill_stream_kernel<DT, true> : distill_stream_kernel<DT, false>;
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 kRing * kGroupChunks * 16 + kStreamThreads * 36);
+            int at_once = 0;
+            if (e == cudaSuccess) e = rows_at_once(kernel, shift, smem, sms, &at_once);
+            if (e != cudaSuccess) return e;
+            const int64_t grid = std::min<int64_t>(a.rows, std::max(1, at_once)) << shift;
+            info->grid = static_cast<int>(grid);
+            info->block = kStreamThreads;
+            info->vec_bytes = 16;
+            info->smem = static_cast<int>(smem);
+            return launch_rows(kernel, dim3(grid), dim3(kStreamThreads), smem, split.blocks(), s, a, split, groups);
+        }
+    }
+    shift = split_shift(a.rows, a.cols, sms);
+    const Split split = split_of<DT>(a.cols, shift);
+    const int64_t grid = a.rows << shift;
+    describe(info, grid);
+    const size_t smem = static_cast<size_t>(a.k) * 12;
+    info->smem = static_cast<int>(smem);
+    auto kernel = distill_kernel<DT, false, true>;
+    if (sums) kernel = grad ? distill_kernel<DT, true, true> : distill_kernel<DT, true, false>;
+    return launch_rows(kernel, dim3(grid), dim3(kThreads), smem, split.blocks(), s, a, split);
+}
+
+}  // namespace
+}  // namespace ew

@@ -1,6 +1,7 @@
 // ew_logits.cuh -- operators on rows of logits: log probabilities of given
-// tokens with entropy and top alternatives, distillation from a teacher's top
-// logits, and their gradients.  Compiled once per element type.
+// tokens with entropy and top alternatives, and their gradient; and what
+// distillation (ew_distill.cuh) shares with them.  Compiled once per element
+// type.
 //
 // With a = scale * log2(e), a row is summed as
 //     s = sum 2^(a x - c),   u = sum 2^(a x - c) (a x - c),
@@ -167,10 +168,9 @@ template <int DT> struct Share {
 // ---------------------------------------------------------------- sums
 
 struct Sums {
-    float c, s, u;
-    float top;  // largest element, NaN kept
+    float c, s, u;  // u where the entropy is wanted
 };
-__device__ __forceinline__ Sums no_sums() { return {kLeastExponent, 0.0f, 0.0f, kNegInf}; }
+__device__ __forceinline__ Sums no_sums() { return {kLeastExponent, 0.0f, 0.0f}; }
 
 __device__ __forceinline__ void move_to(Sums &v, float c) {
     const float d = v.c - c;  // an integer <= 0
@@ -181,18 +181,16 @@ __device__ __forceinline__ void move_to(Sums &v, float c) {
 }
 // One element.
 __device__ __forceinline__ void add_element(Sums &v, float x, float a) {
-    v.top = max_nan(v.top, x);
     const float c = fmaxf(ceilf(x * a), kLeastExponent);
     if (c > v.c) move_to(v, c);
-    const float t = fmaf(fmaxf(x, kLeast), a, -v.c), e = ex2(t);
+    const float t = x < kLeast ? kLeast * a - v.c : fmaf(x, a, -v.c), e = ex2(t);  // NaN stays
     v.s += e;
     v.u = fmaf(e, t, v.u);
 }
-// A thread's chunks; sums in two lanes of a pair each.  Returns the largest element.
+// A thread's chunks; sums in two lanes of a pair each.  Returns the largest element, or NaN.
 struct PairSums {
     float c;
     float2 s, u;
-    uint32_t top;  // a word of largest elements
 };
 template <int DT, bool ENTROPY, int N>
 __device__ __forceinline__ float add_chunks(PairSums &v, const Chunk<DT> (&r)[N], float a) {
@@ -201,9 +199,9 @@ __device__ __forceinline__ float add_chunks(PairSums &v, const Chunk<DT> (&r)[N]
 #pragma unroll
     for (int k = 1; k < N; ++k)
         m = max_words<DT>(m, max_words<DT>(max_words<DT>(r[k].w[0], r[k].w[1]), max_words<DT>(r[k].w[2], r[k].w[3])));
-    v.top = max_words<DT>(v.top, m);
     const float top = max_of_word<DT>(m);
     const float c = fmaxf(ceilf(top * a), kLeastExponent);
+    if (ENTROPY && top != top) v.s = both(top);  // the bound of the pairs below would lose a NaN
     if (c > v.c) {
         const float d = v.c - c, f = ex2(d);
         if (ENTROPY) v.u = mul2(both(f), fma2(v.s, both(d), v.u));
@@ -226,38 +224,32 @@ __device__ __forceinline__ float add_chunks(PairSums &v, const Chunk<DT> (&r)[N]
 // The sums of the first LANES lanes together (all others' are no_sums()), to
 // all lanes: the largest exponent first, then plain sums.  Every lane adds the
 // same pairs, so all get the same bits.
-template <int LANES> __device__ __forceinline__ Sums warp_sums(Sums v) {
+template <int LANES, bool ENTROPY> __device__ __forceinline__ Sums warp_sums(Sums v) {
     float c = v.c;
 #pragma unroll
-    for (int d = LANES / 2; d > 0; d >>= 1) {
-        c = fmaxf(c, __shfl_xor_sync(kAllLanes, c, d));
-        v.top = max_nan(v.top, __shfl_xor_sync(kAllLanes, v.top, d));
-    }
-    if (LANES < 32) {
-        c = __shfl_sync(kAllLanes, c, 0);
-        v.top = __shfl_sync(kAllLanes, v.top, 0);
-    }
+    for (int d = LANES / 2; d > 0; d >>= 1) c = fmaxf(c, __shfl_xor_sync(kAllLanes, c, d));
+    if (LANES < 32) c = __shfl_sync(kAllLanes, c, 0);
     move_to(v, c);
 #pragma unroll
     for (int d = LANES / 2; d > 0; d >>= 1) {
         v.s += __shfl_xor_sync(kAllLanes, v.s, d);
-        v.u += __shfl_xor_sync(kAllLanes, v.u, d);
+        if (ENTROPY) v.u += __shfl_xor_sync(kAllLanes, v.u, d);
     }
     if (LANES < 32) {
         v.s = __shfl_sync(kAllLanes, v.s, 0);
-        v.u = __shfl_sync(kAllLanes, v.u, 0);
+        if (ENTROPY) v.u = __shfl_sync(kAllLanes, v.u, 0);
     }
     return v;
 }
-// Sums of the block, to all its threads, from the warps' in `part`.
-__device__ __forceinline__ Sums sums_of_warps(const Sums *part) {
+// Sums of the block, to all its threads, from its WARPS warps' in `part`.
+template <int WARPS, bool ENTROPY> __device__ __forceinline__ Sums sums_of_warps(const Sums *part) {
     const int lane = threadIdx.x & 31;
-    return warp_sums<kWarps>(lane < kWarps ? part[lane] : no_sums());
+    return warp_sums<WARPS, ENTROPY>(lane < WARPS ? part[lane] : no_sums());
 }
 // The sums of all blocks of the cluster, to every thread: lane b reads block b's.
-__device__ __forceinline__ Sums cluster_sums(const Sums *mine, int blocks) {
+template <bool ENTROPY> __device__ __forceinline__ Sums cluster_sums(const Sums *mine, int blocks) {
     const int lane = threadIdx.x & 31;
-    return warp_sums<8>(lane < blocks ? *in_block(mine, lane) : no_sums());
+    return warp_sums<8, ENTROPY>(lane < blocks ? *in_block(mine, lane) : no_sums());
 }
 
 // What a row's elements are compared with: log p(x) = ln2 (a x - c) - log_s,
@@ -286,12 +278,16 @@ __device__ __forceinline__ float entropy_of(const RowSum &r) {
 // shortcuts above: rows of masked elements alone, of NaN or infinity, or of
 // huge values.  An empty row (no element above -inf) has lse -inf, entropy 0;
 // NaN or +inf make everything NaN.  Every thread of the block takes part.
-template <int DT> __device__ __noinline__ RowSum careful_row(const void *row, int cols, float a, float top, float *part) {
+template <int DT> __device__ __noinline__ RowSum careful_row(const void *row, int cols, float a, float *part) {
+    const Share<DT> all(row, cols, 0, unsplit());
+    const int warps = blockDim.x >> 5;
+    float top = kNegInf, s = 0.0f, u = 0.0f;
+    for (int k = threadIdx.x; k < cols; k += blockDim.x) top = max_nan(top, all.at(k));
+    __syncthreads();
+    top = block_max_nan(top, warps, part, kNegInf);
     RowSum r = {0.0f, 0.0f, 0.0f, 0.0f, top, true};
     if (top == kNegInf) return r;
-    const Share<DT> all(row, cols, 0, unsplit());
-    float s = 0.0f, u = 0.0f;
-    for (int k = threadIdx.x; k < cols; k += kThreads) {
+    for (int k = threadIdx.x; k < cols; k += blockDim.x) {
         const float t = fmaxf((all.at(k) - top) * a, -200.0f);
         const float e = ex2(t);
         s += e;
@@ -299,19 +295,23 @@ template <int DT> __device__ __noinline__ RowSum careful_row(const void *row, in
     }
     if (!(top < -kNegInf)) s = top - top;  // NaN
     __syncthreads();
-    s = block_sum(s, kWarps, part);
+    s = block_sum(s, warps, part);
     __syncthreads();
-    u = block_sum(u, kWarps, part);
+    u = block_sum(u, warps, part);
     r.log_s = logf(s);
     r.inv_s = 1.0f / s;
     r.u_over_s = u / s;
     return r;
 }
+// A sum that is 0, infinite or NaN says that the shortcuts do not hold for the
+// row: an infinity has c infinite and so a NaN, too.
 template <int DT>
 __device__ __forceinline__ RowSum finish_row(const Sums &v, const void *row, int cols, float a, float *part) {
-    if (v.s > 0.0f && v.s < 1e37f && fabsf(v.u) < 1e37f && v.top < -kNegInf)
-        return {v.c, logf(v.s), 1.0f / v.s, v.u / v.s, v.top, false};
-    return careful_row<DT>(row, cols, a, v.top, part);
+    if (v.s > 0.0f && v.s < 1e37f && fabsf(v.u) < 1e37f) {
+        const float inv_s = 1.0f / v.s;
+        return {v.c, logf(v.s), inv_s, v.u * inv_s, 0.0f, false};
+    }
+    return careful_row<DT>(row, cols, a, part);
 }
 
 // ---------------------------------------------------------------- top alternatives
@@ -478,7 +478,7 @@ template <int DT> __device__ __noinline__ void exact_top(TopShared &t, const Sha
 
 // A thread's sums out of its pairs, and one of the single elements.
 template <int DT> __device__ __forceinline__ Sums finished(const PairSums &v, bool single, float one, float a) {
-    Sums sums = {v.c, v.s.x + v.s.y, v.u.x + v.u.y, max_of_word<DT>(v.top)};
+    Sums sums = {v.c, v.s.x + v.s.y, v.u.x + v.u.y};
     if (single) add_element(sums, one, a);
     return sums;
 }
@@ -497,7 +497,7 @@ __device__ __forceinline__ void load_turn(const Share<DT> &sh, int c0, Chunk<DT>
 // share where that is one turn.
 template <int DT, bool ENTROPY, bool TOP>
 __device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShared *t, int k, Chunk<DT> (&r)[kFlight]) {
-    PairSums v = {kLeastExponent, both(0.0f), both(0.0f), masked_word<DT>()};
+    PairSums v = {kLeastExponent, both(0.0f), both(0.0f)};
     const bool single = static_cast<int>(threadIdx.x) < sh.singles;
     const float one = single ? sh.at(sh.single(threadIdx.x)) : kNegInf;
     float bound = kNegInf;
@@ -546,10 +546,10 @@ template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads, kResiden
     const float ax = a.scale * kLog2e;
     Chunk<DT> r_chunks[kFlight];
     load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), r_chunks);
-    Sums v = warp_sums<32>(pass_over<DT, true, TOP>(sh, ax, t, a.top, r_chunks));
+    Sums v = warp_sums<32, true>(pass_over<DT, true, TOP>(sh, ax, t, a.top, r_chunks));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();  // every candidate is in the list too
-    v = sums_of_warps(part);
+    v = sums_of_warps<kWarps, true>(part);
     if constexpr (TOP) {
         if (t->count > kCandidates) exact_top<DT>(*t, sh, a.top);
         rank_list(t->list, t->count, a.top, t->best);
@@ -560,7 +560,7 @@ template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads, kResiden
         if (TOP && threadIdx.x == 0) t->count = 0;
         cluster_sync();
         if (block == 0) {
-            v = cluster_sums(&mine, blocks);
+            v = cluster_sums<true>(&mine, blocks);
             if constexpr (TOP) {
                 for (int i = threadIdx.x; i < blocks * a.top; i += kThreads) {
                     const Candidate c = in_block(t->best, i / a.top)[i % a.top];
@@ -642,12 +642,11 @@ template <int DT> __device__ __forceinline__ void store_one(void *row, int col, 
     static_cast<T *>(row)[col] = f32_to_elem<DT>(x);
 }
 
-// Rows whose p is formed the careful way, and rows whose output starts at
-// another offset from 16 bytes than the input: element by element.
+// Rows whose p is formed the careful way.
 template <int DT, bool ENTROPY>
 __device__ __noinline__ void write_grad_slowly(const Share<DT> &sh, void *out, const RowGrad &r, float a, float scale) {
     constexpr int V = Chunk<DT>::kElems;
-    for (int c = sh.first * V + static_cast<int>(threadIdx.x); c < sh.end * V; c += kThreads)
+    for (int c = sh.first * V + static_cast<int>(threadIdx.x); c < sh.end * V; c += blockDim.x)
         store_one<DT>(out, sh.head + c, grad_of<ENTROPY>(r, sh.at(sh.head + c), a, scale));
     if (static_cast<int>(threadIdx.x) < sh.singles) {
         const int col = sh.single(threadIdx.x);
@@ -660,7 +659,7 @@ template <int DT> __device__ __forceinline__ void write_zeros(void *out_row, int
     const Share<DT> sh(out_row, cols, block, split);
     typename ElemOf<DT>::type *out = static_cast<typename ElemOf<DT>::type *>(out_row);
     const Vec<16> zero = {};
-    for (int c = sh.first + static_cast<int>(threadIdx.x); c < sh.end; c += kThreads) st<16>(out + sh.column(c, 0), zero);
+    for (int c = sh.first + static_cast<int>(threadIdx.x); c < sh.end; c += blockDim.x) st<16>(out + sh.column(c, 0), zero);
     if (static_cast<int>(threadIdx.x) < sh.singles) store_one<DT>(out, sh.single(threadIdx.x), 0.0f);
 }
 
@@ -689,13 +688,32 @@ template <int DT, bool ENTROPY> struct ChunkGrad {
 template <int DT> __device__ __forceinline__ bool starts_alike(const void *out, const Share<DT> &sh) {
     return (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(sh.row)) % 16 == 0;
 }
+// Stores a chunk's gradient; element by element where the output row starts at
+// another offset from 16 bytes than the input's (alike is false).
+template <int DT>
+__device__ __forceinline__ void store_chunk(typename ElemOf<DT>::type *to, const Vec<16> &d, bool alike) {
+    if (alike) {
+        st<16>(to, d);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == DT_F32) {
+                to[j] = d.w[j];
+            } else {
+                to[2 * j] = static_cast<uint16_t>(d.w[j]);
+                to[2 * j + 1] = static_cast<uint16_t>(d.w[j] >> 16);
+            }
+        }
+    }
+}
 
 // Writes the gradient of the block's share, which it reads (again).
 template <int DT, bool ENTROPY>
 __device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, const RowGrad &g, float a, float scale) {
     using T = typename ElemOf<DT>::type;
     T *out = static_cast<T *>(out_row);
-    if (g.w.careful || !starts_alike(out, sh)) {
+    const bool alike = starts_alike(out, sh);
+    if (g.w.careful) {
         write_grad_slowly<DT, ENTROPY>(sh, out_row, g, a, scale);
         return;
     }
@@ -708,96 +726,12 @@ __device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, c
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
             if (c0 + u * kThreads >= sh.end) break;
-            st<16>(out + sh.column(c0 + u * kThreads, 0), grad(r[u]));
+            store_chunk<DT>(out + sh.column(c0 + u * kThreads, 0), grad(r[u]), alike);
         }
     }
     if (static_cast<int>(threadIdx.x) < sh.singles) {
         const int col = sh.single(threadIdx.x);
         store_one<DT>(out, col, grad_of<ENTROPY>(g, sh.at(col), a, scale));
-    }
-}
-
-// ---------------------------------------------------------------- a share held in shared memory
-//
-// Up to kHeldTurns * 4 chunks a thread (64 KiB a block) are copied to shared
-// memory at once, asynchronously, and stay there between the sums and the
-// gradient: the row crosses DRAM once.  Each thread copies and reads its own
-// chunks only, so it waits for its own copies and needs no barrier; the copies
-// are in kHeldTurns groups, and the sums of the first are formed while the
-// others are on their way.
-
-constexpr int kHeldTurns = 4;
-constexpr int kHeldFlight = 4;
-constexpr int kHeldChunks = kHeldTurns * kHeldFlight * kThreads;
-
-template <int DT> __device__ __forceinline__ void copy_share(const Share<DT> &sh, uint4 *held) {
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(held));
-#pragma unroll
-    for (int g = 0; g < kHeldTurns; ++g) {
-#pragma unroll
-        for (int u = 0; u < kHeldFlight; ++u) {
-            const int at = (g * kHeldFlight + u) * kThreads + static_cast<int>(threadIdx.x);
-            if (sh.first + at < sh.end)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                             :: "r"(to + 16u * at), "l"(sh.row + sh.column(sh.first + at, 0)) : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-}
-template <int LEFT> __device__ __forceinline__ void copies_left() {
-    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
-}
-// The thread's chunks of group g.
-template <int DT>
-__device__ __forceinline__ void held_chunks(const Share<DT> &sh, const uint4 *held, int g, Chunk<DT> (&r)[kHeldFlight]) {
-#pragma unroll
-    for (int u = 0; u < kHeldFlight; ++u) {
-        const int at = (g * kHeldFlight + u) * kThreads + static_cast<int>(threadIdx.x);
-        r[u] = masked_chunk<DT>();
-        if (sh.first + at < sh.end) {
-            const uint4 w = held[at];
-            r[u] = Chunk<DT>{{w.x, w.y, w.z, w.w}};
-        }
-    }
-}
-template <int DT> __device__ __forceinline__ Sums sums_of_held(const Share<DT> &sh, const uint4 *held, float a) {
-    PairSums v = {kLeastExponent, both(0.0f), both(0.0f), masked_word<DT>()};
-    const bool single = static_cast<int>(threadIdx.x) < sh.singles;
-    const float one = single ? sh.at(sh.single(threadIdx.x)) : kNegInf;
-    Chunk<DT> r[kHeldFlight];
-    static_assert(kHeldTurns == 4, "one wait for each group below");
-    copies_left<3>();
-    held_chunks<DT>(sh, held, 0, r);
-    add_chunks<DT, false>(v, r, a);
-    copies_left<2>();
-    held_chunks<DT>(sh, held, 1, r);
-    add_chunks<DT, false>(v, r, a);
-    copies_left<1>();
-    held_chunks<DT>(sh, held, 2, r);
-    add_chunks<DT, false>(v, r, a);
-    copies_left<0>();
-    held_chunks<DT>(sh, held, 3, r);
-    add_chunks<DT, false>(v, r, a);
-    return finished<DT>(v, single, one, a);
-}
-template <int DT>
-__device__ __forceinline__ void write_grad_of_held(const Share<DT> &sh, const uint4 *held, void *out_row, const RowGrad &g,
-                                                   float a, float scale) {
-    using T = typename ElemOf<DT>::type;
-    T *out = static_cast<T *>(out_row);
-    if (g.w.careful || !starts_alike(out, sh)) {
-        write_grad_slowly<DT, false>(sh, out_row, g, a, scale);
-        return;
-    }
-    const ChunkGrad<DT, false> grad(g, a);
-#pragma unroll 4
-    for (int c = sh.first + static_cast<int>(threadIdx.x); c < sh.end; c += kThreads) {
-        const uint4 w = held[c - sh.first];
-        st<16>(out + sh.column(c, 0), grad(Chunk<DT>{{w.x, w.y, w.z, w.w}}));
-    }
-    if (static_cast<int>(threadIdx.x) < sh.singles) {
-        const int col = sh.single(threadIdx.x);
-        store_one<DT>(out, col, grad_of<false>(g, sh.at(col), a, scale));
     }
 }
 
@@ -828,135 +762,6 @@ __global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(Logpr
     __syncthreads();
     if (threadIdx.x == 0)
         store_one<DT>(out, static_cast<int>(token), grad_of<ENTROPY>(r, x, ax, a.scale) + a.scale * dlogp);
-}
-
-// ---------------------------------------------------------------- distillation
-//
-// q = softmax of the teacher's values at its ids, p = softmax of the student's
-// row, both of values times `scale`:
-//     loss = sum q_i (log q_i - log p(id_i)),   dlogits = dloss scale (p - q).
-// Entries with an id outside the row or a value of -inf do not count; a row
-// without any has loss 0 and gradient 0.  HELD: each block's share of the row
-// stays in shared memory; rows beyond 8 blocks' 512 KiB are read twice.
-
-// Dynamic shared memory: the held share, then per teacher's entry the student's
-// column, the scaled value and the student's logit.
-struct Teacher {
-    int *id;
-    float *t, *x;
-    __device__ __forceinline__ Teacher(void *at, int k) : id(static_cast<int *>(at)), t(static_cast<float *>(at) + k),
-                                                          x(static_cast<float *>(at) + 2 * k) {}
-};
-
-template <int DT, bool SUMS, bool GRAD, bool HELD>
-__global__ void __launch_bounds__(kThreads, HELD ? 3 : kResident) distill_kernel(DistillArgs a, Split split) {
-    enter_grid();
-    extern __shared__ uint4 held[];
-    __shared__ Sums part[kWarps];
-    __shared__ Sums mine;
-    __shared__ float fpart[2][32];
-    const Teacher th(held + (HELD ? split.each : 0), a.k);
-    const int blocks = split.blocks(), block = blockIdx.x & (blocks - 1);
-    const int64_t row = blockIdx.x >> split.shift;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const void *logits = row_of<DT>(a.logits, row, a.stride);
-    const Share<DT> sh(logits, a.cols, block, split);
-    const float ax = a.scale * kLog2e;
-
-    Chunk<DT> first_turn[kFlight];  // on its way, as the held share is, while the teacher's entries are
-    if constexpr (HELD) copy_share<DT>(sh, held);
-    else if constexpr (SUMS) load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), first_turn);
-
-    // The teacher's entries; every block has them all.  Of the student's logits
-    // the loss (block 0) needs all, the gradient those that this block writes.
-    for (int i = threadIdx.x; i < a.k; i += kThreads) {
-        const int64_t id = token_at(a.ids, a.i64, row * a.ids_stride + i);
-        const int64_t at = row * a.teacher_stride + i;
-        float v;
-        if (DT == DT_F32 || a.teacher_f32) v = static_cast<const float *>(a.teacher)[at];
-        else v = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(a.teacher)[at]);
-        const bool given = id >= 0 && id < a.cols && v != kNegInf;
-        const bool read = given && ((SUMS && block == 0) || sh.holds(static_cast<int>(id)));
-        th.id[i] = given ? static_cast<int>(id) : -1;
-        th.t[i] = given ? v * a.scale : kNegInf;
-        th.x[i] = read ? sh.at(static_cast<int>(id)) : 0.0f;
-    }
-    Sums v = no_sums();
-    if constexpr (HELD) v = warp_sums<32>(sums_of_held<DT>(sh, held, ax));
-    else if constexpr (SUMS) v = warp_sums<32>(pass_over<DT, false, false>(sh, ax, nullptr, 0, first_turn));
-    if (lane == 0) part[warp] = v;
-    __syncthreads();
-    // its softmax, by each warp for itself
-    float teacher_top = kNegInf, teacher_sum = 0.0f;
-    for (int i = lane; i < a.k; i += 32) teacher_top = max_nan(teacher_top, th.t[i]);
-    teacher_top = lanes_max_nan(teacher_top, 32);
-    const bool any = teacher_top != kNegInf;
-    for (int i = lane; any && i < a.k; i += 32) teacher_sum += expf(th.t[i] - teacher_top);
-    const float teacher_log_sum = logf(warp_sum(teacher_sum));
-    auto log_q = [&](int i) { return th.t[i] - teacher_top - teacher_log_sum; };
-
-    Weights w;
-    RowSum r;
-    if constexpr (SUMS) {
-        v = sums_of_warps(part);
-        if (blocks > 1) {
-            if (threadIdx.x == 0) mine = v;
-            cluster_sync();
-            v = cluster_sums(&mine, blocks);
-            cluster_arrive();  // the wait is further down: mine has been read
-        }
-        r = finish_row<DT>(v, logits, a.cols, ax, fpart[0]);
-        w = {r.c, r.inv_s, r.top, r.careful};
-    } else {
-        w = weights_of(a.lse[row], a.scale);
-    }
-    if constexpr (GRAD) {
-        const RowGrad rg = row_grad(w, any ? a.dloss[row] * a.scale : 0.0f, 0.0f, 0.0f, 0.0f);
-        void *out = row_of<DT>(a.dlogits, row, a.dstride);
-        // a careful row has been read whole by every block: all are done with it before any writes in place
-        if (SUMS && w.careful) {
-            if (blocks > 1) {
-                cluster_wait();
-                cluster_arrive();
-                cluster_wait();
-                cluster_arrive();
-            } else {
-                __syncthreads();
-            }
-        }
-        if (!any) write_zeros<DT>(out, a.cols, block, split);
-        else if constexpr (HELD) write_grad_of_held<DT>(sh, held, out, rg, ax, a.scale);
-        else write_grad<DT, false>(sh, out, rg, ax, a.scale);
-        __syncthreads();
-        // entries of one id add up; the first of them writes
-        for (int i = threadIdx.x; any && i < a.k; i += kThreads) {
-            const int id = th.id[i];
-            if (id < 0 || !sh.holds(id)) continue;
-            bool first = true;
-            for (int j = 0; j < i; ++j) first = first && th.id[j] != id;
-            float qs = expf(log_q(i));
-            for (int j = i + 1; j < a.k; ++j)
-                if (th.id[j] == id) qs += expf(log_q(j));
-            if (first) store_one<DT>(out, id, rg.g * (p_of(w, th.x[i], ax) - qs));
-        }
-    }
-    if constexpr (SUMS) {
-        if (block == 0) {
-            const bool empty = r.careful && r.top == kNegInf;
-            float loss = 0.0f;
-            for (int i = threadIdx.x; i < a.k; i += kThreads) {
-                const float logq = log_q(i), qi = th.id[i] >= 0 ? expf(logq) : 0.0f;
-                const float logp = empty ? kNegInf : logp_of(r, th.x[i], ax, a.scale);
-                if (qi != 0.0f) loss += qi * (logq - logp);
-            }
-            loss = block_sum(loss, kWarps, fpart[1]);
-            if (threadIdx.x == 0) {
-                a.loss[row] = any ? loss : 0.0f;
-                a.lse[row] = empty ? kNegInf : lse_of(r, a.scale);
-            }
-        }
-        if (blocks > 1) cluster_wait();
-    }
 }
 
 // ---------------------------------------------------------------- launches
@@ -995,26 +800,5 @@ template <int DT> cudaError_t logprob_grad_launch(const LogprobGradArgs &a, cuda
     auto kernel = a.dentropy ? logprob_grad_kernel<DT, true> : logprob_grad_kernel<DT, false>;
     return launch_rows(kernel, dim3(grid), dim3(kThreads), 0, 1, s, a, split);
 }
-template <int DT>
-cudaError_t distill_launch(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info) {
-    // The loss alone splits and sums its rows as loss and gradient in one call
-    // do, so both give the same bits.
-    int shift = split_shift(a.rows, a.cols, sms);
-    const int chunks = a.cols / Chunk<DT>::kElems;
-    const bool held = sums && chunks <= 8 * kHeldChunks && a.rows << 3 <= INT32_MAX;
-    while (held && chunks > kHeldChunks << shift) ++shift;
-    const Split split = split_of<DT>(a.cols, shift);
-    const int64_t grid = a.rows << shift;
-    describe(info, grid);
-    const size_t smem = static_cast<size_t>(held ? split.each : 0) * 16 + static_cast<size_t>(a.k) * 12;
-    info->smem = static_cast<int>(smem);
-    auto kernel = distill_kernel<DT, false, true, false>;
-    if (sums && !grad) kernel = held ? distill_kernel<DT, true, false, true> : distill_kernel<DT, true, false, false>;
-    if (sums && grad) kernel = held ? distill_kernel<DT, true, true, true> : distill_kernel<DT, true, true, false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kHeldChunks * 16 + kMostTeacher * 12);
-    return e != cudaSuccess ? e : launch_rows(kernel, dim3(grid), dim3(kThreads), smem, split.blocks(), s, a, split);
-}
-
 }  // namespace
 }  // namespace ew

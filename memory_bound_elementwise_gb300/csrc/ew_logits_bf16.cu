@@ -9,8 +9,5 @@ cudaError_t logprob_bf16(const LogprobArgs &a, int sms, cudaStream_t s, LaunchIn
 cudaError_t logprob_grad_bf16(const LogprobGradArgs &a, cudaStream_t s, LaunchInfo *info) {
     return logprob_grad_launch<DT_BF16>(a, s, info);
 }
-cudaError_t distill_bf16(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info) {
-    return distill_launch<DT_BF16>(a, sums, grad, sms, s, info);
-}
 
 }  // namespace ew

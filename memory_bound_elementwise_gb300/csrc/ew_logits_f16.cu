@@ -9,8 +9,5 @@ cudaError_t logprob_f16(const LogprobArgs &a, int sms, cudaStream_t s, LaunchInf
 cudaError_t logprob_grad_f16(const LogprobGradArgs &a, cudaStream_t s, LaunchInfo *info) {
     return logprob_grad_launch<DT_F16>(a, s, info);
 }
-cudaError_t distill_f16(const DistillArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info) {
-    return distill_launch<DT_F16>(a, sums, grad, sms, s, info);
-}
 
 }  // namespace ew
