@@ -1,4 +1,5 @@
-"""Build ``libew.so`` (the C ABI of include/ew.h) in-tree with nvcc for sm_103a.
+"""Build ``libew.so`` (the C ABI of include/ew.h) in-tree with nvcc for sm_103a,
+and beside it the row operators' torch binding.
 
 The translation units are compiled in parallel, then linked into
 ``memory_bound_elementwise_gb300/_lib/libew.so`` with the CUDA runtime linked
@@ -8,10 +9,12 @@ contraction of separate multiplies and adds, IEEE division and square root
 """
 import concurrent.futures as cf
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libew.so")
 OBJ_DIR = os.path.join(OUT_DIR, "obj")
+BINDING_SOURCE = os.path.join(CSRC, "ew_torch.cpp")
+BINDING = os.path.join(OUT_DIR, "_ew_torch.so")  # CPython extension over torch's C++ headers
 
 SOURCES = ["ew_api.cu", "ew_kernels_f32.cu", "ew_kernels_f16.cu", "ew_kernels_bf16.cu", "ew_tma.cu",
            "ew_gather_fixed.cu", "ew_gather_fixed_wide.cu", "ew_rows_api.cu", "ew_rows.cu", "ew_embed.cu",
@@ -63,19 +68,59 @@ def source_digest():
     return _kernel_digest()
 
 
+def _torch_dir():
+    """The installed torch's folder, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found")
+    return list(spec.submodule_search_locations)[0]
+
+
 def _inputs_digest():
-    """Build stamp: the kernel sources and flags plus the public header."""
+    """Build stamp: the kernel sources and flags, the public header, the binding and what it is built for."""
     h = hashlib.sha256(_kernel_digest().encode())
-    with open(os.path.join(INCLUDE, "ew.h"), "rb") as f:
-        h.update(f.read())
+    for path in (os.path.join(INCLUDE, "ew.h"), BINDING_SOURCE, os.path.join(_torch_dir(), "version.py")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    h.update(sys.version.encode())
     return h.hexdigest()
 
 
+def _build_binding():
+    """Compiles the torch binding; it is linked against libew.so and the installed torch."""
+    torch_dir = _torch_dir()
+    include, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cuda_include = [d for d in [os.path.join(cuda, "include")] +
+                    [os.path.join(cuda, "targets", t, "include") for t in ("x86_64-linux", "sbsa-linux")]
+                    if os.path.exists(os.path.join(d, "cuda_runtime_api.h"))][:1]
+    obj = os.path.join(OBJ_DIR, "ew_torch.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", include, "-isystem",
+           os.path.join(include, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-D_GLIBCXX_USE_CXX11_ABI=1", "-c", BINDING_SOURCE, "-o", obj]
+    for d in cuda_include:
+        cmd += ["-isystem", d]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for ew_torch.cpp:\n%s" % r.stdout)
+    return obj, lib
+
+
+def _link_binding(obj, torch_lib):
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-shared", "-o", tmp, obj, LIB, "-L", torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link of the torch binding failed:\n%s" % r.stdout)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libew.so unless an up-to-date build exists."""
+    """Compile and link libew.so and the torch binding unless an up-to-date build exists."""
     stamp = os.path.join(OUT_DIR, "build.sha256")
     digest = _inputs_digest() + ("|" + " ".join(extra_flags) if extra_flags else "")
-    if (not force and os.path.exists(LIB) and os.path.exists(stamp)
+    if (not force and os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(stamp)
             and open(stamp).read().strip() == digest):
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -91,18 +136,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError("nvcc failed for %s:\n%s" % (src, r.stdout))
         return obj, r.stdout
 
-    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_build_binding)  # the longest: first
         results = list(ex.map(compile_one, SOURCES))
+        binding = binding.result()
     if verbose:
         for _, log in results:
             sys.stdout.write(log)
     objs = [o for o, _ in results]
     tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+    cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xlinker", "-soname=libew.so"]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s" % r.stdout)
     os.replace(tmp, LIB)
+    _link_binding(*binding)
     with open(stamp, "w") as f:
         f.write(digest)
     return LIB

@@ -400,12 +400,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1) distill_stream_kernel(Disti
 // ---------------------------------------------------------------- launches
 
 // Rows that are worked on at once: one an SM, or as many clusters of a row's
-// blocks as fit the device (a cluster lies within one of its partitions).
-template <typename Kernel> cudaError_t rows_at_once(Kernel kernel, int shift, size_t smem, int sms, int *rows) {
-    if (shift == 0) {
-        *rows = sms;
-        return cudaSuccess;
-    }
+// blocks as fit the device (a cluster lies within one of its partitions); asked
+// once for each kernel and size of cluster, on the first device that calls.
+template <typename Kernel> cudaError_t rows_at_once(Kernel kernel, int shift, int smem, int sms, int *rows) {
+    *rows = sms;
+    if (shift == 0) return cudaSuccess;
+    static std::atomic<int> known[4];  // of this kernel type: loss, and loss with gradient, have the same block and memory
+    if ((*rows = known[shift].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sms >> shift << shift);
     cfg.blockDim = dim3(kStreamThreads);
@@ -416,7 +417,9 @@ template <typename Kernel> cudaError_t rows_at_once(Kernel kernel, int shift, si
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(rows, kernel, &cfg);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(rows, kernel, &cfg);
+    if (e == cudaSuccess) known[shift].store(*rows = std::max(1, *rows), std::memory_order_relaxed);
+    return e;
 }
 
 template <int DT>
@@ -435,12 +438,14 @@ cudaError_t distill_launch(const DistillArgs &a, bool sums, bool grad, int sms, 
             const Split split = split_of<DT>(a.cols, shift);
             const size_t smem = static_cast<size_t>(kRing) * kGroupChunks * 16 + static_cast<size_t>(a.k) * 36;
             auto kernel = grad ? distill_stream_kernel<DT, true> : distill_stream_kernel<DT, false>;
-            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 kRing * kGroupChunks * 16 + kStreamThreads * 36);
+            // the most that any call needs; one block an SM in any case
+            constexpr int kMostSmem = kRing * kGroupChunks * 16 + kStreamThreads * 36;
+            static std::atomic<uint64_t> allowed[2];
             int at_once = 0;
-            if (e == cudaSuccess) e = rows_at_once(kernel, shift, smem, sms, &at_once);
+            cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), kMostSmem, &allowed[grad]);
+            if (e == cudaSuccess) e = rows_at_once(kernel, shift, kMostSmem, sms, &at_once);
             if (e != cudaSuccess) return e;
-            const int64_t grid = std::min<int64_t>(a.rows, std::max(1, at_once)) << shift;
+            const int64_t grid = std::min<int64_t>(a.rows, at_once) << shift;
             info->grid = static_cast<int>(grid);
             info->block = kStreamThreads;
             info->vec_bytes = 16;

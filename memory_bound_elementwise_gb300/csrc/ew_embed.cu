@@ -381,8 +381,8 @@ cudaError_t launch_embed_grad(int dtype, int gtype, const EmbedGradArgs &a, cuda
     const int passes = std::max(1, (width + kDigitBits - 1) / kDigitBits);
     const int bits = std::max(1, (width + passes - 1) / passes);
     const size_t smem = size_t(kSortWarps) * 4 << bits;
-    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (kSortWarps * 4) << kDigitBits);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(embed_sort_kernel), (kSortWarps * 4) << kDigitBits, &allowed);
     if (e == cudaSuccess)
         e = launch_rows(embed_sort_kernel, dim3(kSortBlocks), dim3(kSortThreads), smem, kSortBlocks, s, a, passes, bits);
     if (e != cudaSuccess) return e;

@@ -2,6 +2,7 @@
 // (ew_rows_api.cu) and their kernels.  Not installed.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -45,6 +46,19 @@ cudaError_t launch_rows(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t 
     }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess) (void)cudaGetLastError();  // the failure is returned; do not leave it pending too
+    return e;
+}
+
+// Lets a kernel use up to `bytes` of dynamic shared memory: once per kernel and
+// device, of which `done` keeps a bit each (devices past 63 are asked every time).
+inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_t> *done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
     return e;
 }
 
