@@ -6,7 +6,7 @@
 //
 // Both move memory and compute next to nothing.  The gradient sorts the
 // positions by token (stable), so that each table row's terms lie in one run,
-// in the order of their positions.  Warps take 32 sorted positions by 256
+// in the order of their positions.  Warps take 32 (or 8) sorted positions by 256
 // columns each and add run by run in binary32; a run that ends within the
 // chunk goes straight to its table row, one that crosses a chunk's edge leaves
 // a partial sum, and embed_join_kernel adds those in order.  The split depends
@@ -90,27 +90,85 @@ template <int DT> cudaError_t embed_dispatch(const EmbedArgs &a, int sms, cudaSt
 // memory, turns the counts into places by a prefix over (digit, block, warp),
 // the other blocks' totals read from their shared memory, and moves the items;
 // lanes with equal digits are ranked by a match.  Passes are separated by
-// cluster barriers.  Digits have at most 10 bits, so tables of less than 2^20
-// rows take two passes.
+// cluster barriers, which order the blocks' global stores too.  Digits have at
+// most 10 bits, so tables of less than 2^20 rows take two passes.
+//
+// The other SMs meanwhile write zeros: the grid's further blocks clear the
+// first `blind` rows of the table, which at the end of the sort need not be
+// looked at again (a row that a token names is written once more, by its sum).
 
 constexpr int kSortBlocks = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 10;
 
+constexpr int kKept = 4;  // items a lane keeps between counting and moving them
+
+template <int GT, bool VEC>
+__device__ __forceinline__ void clear_row(void *row, int cols, int lane) {
+    Raw8<GT> zero;
+#pragma unroll
+    for (int k = 0; k < ElemOf<GT>::kWords; ++k) zero.w[k] = 0u;
+#pragma unroll 4
+    for (int base = 0; base < cols; base += kTileCols) store_tile<GT, VEC>(row, base, cols, lane, zero);
+}
+
+// Inclusive prefix sum over the block's threads; `scan` has a slot a warp.
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *scan) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t u = __shfl_up_sync(kAllLanes, v, d);
+        v += lane >= d ? u : 0u;
+    }
+    if (lane == 31) scan[warp] = v;
+    __syncthreads();
+    uint32_t before = lane < warp ? scan[lane] : 0u;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(kAllLanes, before, d);
+    return v + before;
+}
+
+// The lanes of `active` whose digit is this lane's: a ballot for each bit.  (A
+// match instruction takes about 64 cycles of the SM for 32 different digits,
+// ten ballots a quarter of that.)
+__device__ __forceinline__ unsigned lanes_alike(uint32_t digit, int bits, unsigned active) {
+    unsigned same = active;
+#pragma unroll 2
+    for (int b = 0; b < bits; ++b) {
+        const bool one = digit >> b & 1;
+        const unsigned ones = __ballot_sync(kAllLanes, one);
+        same &= one ? ones : ~ones;
+    }
+    return same;
+}
+
+template <int GT, bool VEC> __device__ __forceinline__ void clear_blind(const EmbedGradArgs &a, int sort_blocks) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t v = (static_cast<int64_t>(blockIdx.x) - sort_blocks) * kSortWarps + warp; v < a.blind;
+         v += static_cast<int64_t>(gridDim.x - sort_blocks) * kSortWarps)
+        clear_row<GT, VEC>(row_of<GT>(a.dtable, v, a.table_stride), a.cols, lane);
+}
+
+template <int GT, bool VEC>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradArgs a, int passes, int bits) {
     enter_grid();
     extern __shared__ uint32_t count[];  // [warp][digit]
-    __shared__ uint32_t total[1 << kDigitBits];
+    __shared__ uint32_t total[1 << kDigitBits], first_place[1 << kDigitBits];
     __shared__ uint32_t scan[kSortWarps];
-    const uint32_t rank = cluster_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x >= kSortBlocks) {
+        clear_blind<GT, VEC>(a, kSortBlocks);
+        return;
+    }
+    const uint32_t rank = blockIdx.x;
     const int bins = 1 << bits;
     uint32_t *mine = count + warp * bins;
     // this warp's consecutive part of the positions
     const int64_t parts = kSortBlocks * kSortWarps, part = rank * kSortWarps + warp;
     const int64_t each = ((a.rows + parts - 1) / parts + 31) / 32 * 32;
     const int64_t begin = min(part * each, a.rows), end = min(begin + each, a.rows);
+    const bool keep = each <= 32 * kKept;
     const uint32_t nowhere = static_cast<uint32_t>(a.table_rows);  // the key of positions without a token
     if (a.present != nullptr) {
         const int64_t words = (a.table_rows + 31) / 32;
@@ -125,87 +183,108 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradArgs 
             const int64_t v = token_at(a.tokens, a.i64, t);
             return make_uint2(v >= 0 && v < a.table_rows ? static_cast<uint32_t>(v) : nowhere, static_cast<uint32_t>(t));
         };
+        auto digit_of = [&](uint2 it) { return (it.x >> shift) & (bins - 1); };
+        uint2 kept[kKept];
+        if (keep) {
+#pragma unroll
+            for (int k = 0; k < kKept; ++k)
+                if (begin + k * 32 + lane < end) kept[k] = item(begin + k * 32 + lane);
+        }
         for (int k = threadIdx.x; k < kSortWarps * bins; k += kSortThreads) count[k] = 0u;
         __syncthreads();
-        for (int64_t t = begin + lane; t < end; t += 32) atomicAdd(mine + ((item(t).x >> shift) & (bins - 1)), 1u);
+        if (keep) {
+#pragma unroll
+            for (int k = 0; k < kKept; ++k)
+                if (begin + k * 32 + lane < end) atomicAdd(mine + digit_of(kept[k]), 1u);
+        } else {
+            for (int64_t t = begin + lane; t < end; t += 32) atomicAdd(mine + digit_of(item(t)), 1u);
+        }
         __syncthreads();
         if (static_cast<int>(threadIdx.x) < bins) {  // counts become places within the block's digit
-            uint32_t sum = 0;
+            uint32_t c[kSortWarps], sum = 0;
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) c[w] = count[w * bins + threadIdx.x];
+#pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t c = count[w * bins + threadIdx.x];
                 count[w * bins + threadIdx.x] = sum;
-                sum += c;
+                sum += c[w];
             }
             total[threadIdx.x] = sum;
         }
         cluster_sync();
         uint32_t all = 0, lower = 0;
         if (static_cast<int>(threadIdx.x) < bins) {
+            uint32_t c[kSortBlocks];
+#pragma unroll
+            for (uint32_t b = 0; b < kSortBlocks; ++b) c[b] = *in_block(total + threadIdx.x, b);
 #pragma unroll
             for (uint32_t b = 0; b < kSortBlocks; ++b) {
-                const uint32_t c = load_of_block(total + threadIdx.x, b);
-                all += c;
-                lower += b < rank ? c : 0u;
+                all += c[b];
+                lower += b < rank ? c[b] : 0u;
             }
         }
-        uint32_t before = all;  // inclusive prefix over the digits of a warp, then of the block
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t v = __shfl_up_sync(kAllLanes, before, d);
-            before += lane >= d ? v : 0u;
-        }
-        if (lane == 31) scan[warp] = before;
+        const uint32_t upto = block_prefix(all, scan);
+        if (static_cast<int>(threadIdx.x) < bins) first_place[threadIdx.x] = upto - all + lower;
         __syncthreads();
-        uint32_t warps_before = lane < warp ? scan[lane] : 0u;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) warps_before += __shfl_xor_sync(kAllLanes, warps_before, d);
-        const uint32_t base = before - all + warps_before + lower;
-        if (static_cast<int>(threadIdx.x) < bins)
-            for (int w = 0; w < kSortWarps; ++w) count[w * bins + threadIdx.x] += base;
-        __syncthreads();
-        for (int64_t t0 = begin; t0 < end; t0 += 32) {
-            const bool valid = t0 + lane < end;
+        auto move = [&](uint2 it, bool valid) {  // the valid lanes' items, in the order of their lanes
             const unsigned active = __ballot_sync(kAllLanes, valid);
+            const uint32_t digit = digit_of(it);
+            const unsigned same = lanes_alike(digit, bits, active);
+            const uint32_t in_digit = mine[digit];
+            __syncwarp();
             if (valid) {
-                const uint2 it = item(t0 + lane);
-                const uint32_t digit = (it.x >> shift) & (bins - 1);
-                const unsigned same = __match_any_sync(active, digit);
-                const uint32_t place = mine[digit] + __popc(same & ((1u << lane) - 1u));
-                __syncwarp(active);
-                if (lane == __ffs(same) - 1) mine[digit] += __popc(same);
-                __syncwarp(active);
+                if (lane == __ffs(same) - 1) mine[digit] = in_digit + __popc(same);
+                const uint32_t place = first_place[digit] + in_digit + __popc(same & ((1u << lane) - 1u));
                 if (pass + 1 < passes) {
                     dst[place] = it;
                 } else {
                     a.keys[place] = it.x;
                     a.order[place] = it.y;
                 }
-                if (pass == 0 && a.present != nullptr && it.x != nowhere)
-                    atomicOr(a.present + (it.x >> 5), 1u << (it.x & 31));
+                if (pass == 0 && a.present != nullptr && it.x != nowhere) atomicOr(a.present + (it.x >> 5), 1u << (it.x & 31));
+            }
+            __syncwarp();
+        };
+        if (keep) {
+#pragma unroll
+            for (int k = 0; k < kKept; ++k)
+                if (begin + k * 32 < end) move(kept[k], begin + k * 32 + lane < end);
+        } else {
+            for (int64_t t0 = begin; t0 < end; t0 += 32) {
+                const bool valid = t0 + lane < end;
+                move(valid ? item(t0 + lane) : make_uint2(0u, 0u), valid);
             }
         }
-        __threadfence();
         cluster_sync();  // the next pass reads what all blocks moved, and reuses `total`
     }
 }
 
 // ---------------------------------------------------------------- sums
 
-constexpr int kChunk = 32;  // sorted positions a warp takes, one to a lane
+// Sorted positions a warp takes, one to a lane: 32, or 8 where that leaves few
+// warps (a warp takes its positions a few at a time, each time waiting for
+// memory; more chunks cut more runs).  Gradient of 32003 x 1000 binary32 from
+// 5003 tokens: 8 a warp 31 us, 32 a warp 37 us.
+inline int chunk_of(int64_t rows, int64_t cols) {
+    return rows <= 16384 && (rows + 31) / 32 * ((cols + kTileCols - 1) / kTileCols) < 4096 ? 8 : 32;
+}
 
+// The table's row of a sum, or what the sum is added to.
 template <int GT, bool VEC>
-__device__ __forceinline__ void write_sum(const EmbedGradArgs &a, uint32_t v, int base, int lane, const float2 (&sum)[4]) {
-    void *row = row_of<GT>(a.dtable, v, a.table_stride);
-    float2 f[4];
+__device__ __forceinline__ void write_sum(const EmbedGradArgs &a, uint32_t v, int base, int lane, const float2 (&sum)[4],
+                                          const Raw8<GT> &old) {
+    float2 f[4], o[4];
+    unpack8<GT>(old, o);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = mul2(sum[j], both(a.scale));
-    if (a.accumulate) {
-        float2 old[4];
-        unpack8<GT>(load_tile<GT, VEC>(row, base, a.cols, lane), old);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = add2(f[j], old[j]);
+    for (int j = 0; j < 4; ++j) {
+        f[j] = mul2(sum[j], both(a.scale));
+        if (a.accumulate) f[j] = add2(f[j], o[j]);
     }
-    store_tile<GT, VEC>(row, base, a.cols, lane, pack8<GT>(f));
+    store_tile<GT, VEC>(row_of<GT>(a.dtable, v, a.table_stride), base, a.cols, lane, pack8<GT>(f));
+}
+template <int GT, bool VEC>
+__device__ __forceinline__ Raw8<GT> old_row(const EmbedGradArgs &a, uint32_t v, int base, int lane) {
+    return load_tile<GT, VEC>(row_of<GT>(a.dtable, v, a.table_stride), base, a.cols, lane);
 }
 
 // Partial sums: for each chunk its first run where that began before the chunk
@@ -216,105 +295,118 @@ __device__ __forceinline__ float4 *partial_at(const EmbedGradArgs &a, int64_t ch
     return reinterpret_cast<float4 *>(a.partial) + (((chunk * 2 + slot) * tiles + tile) * 32 + lane) * 2;
 }
 
-template <int DT, int GT, bool VEC>
-__global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a, int64_t sum_blocks) {
+// Blocks of two kinds, the sums spread evenly among the others: 8 warps that
+// each add a chunk's tile, and 8 warps that write the zeros of 32 table rows.
+template <int DT, int GT, bool VEC, bool ACCUMULATE>
+__global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a, uint32_t sum_blocks, uint32_t every) {
     enter_grid();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tiles = (a.cols + kTileCols - 1) / kTileCols;
-    if (static_cast<int64_t>(blockIdx.x) >= sum_blocks) {  // rows that no token names become zero
-        const int64_t w = (static_cast<int64_t>(blockIdx.x) - sum_blocks) * 8 + warp;
+    const uint32_t turn = blockIdx.x / every;
+    if (blockIdx.x % every != 0 || turn >= sum_blocks) {  // rows that no token names become zero
+        const int64_t w = a.blind / 32 + (blockIdx.x - min(turn + 1, sum_blocks));
         if (w * 32 >= a.table_rows) return;
-        uint32_t absent = ~a.present[w];
-        if (a.table_rows - w * 32 < 32) absent &= (1u << (a.table_rows - w * 32)) - 1u;
-        Raw8<GT> zero;
-#pragma unroll
-        for (int k = 0; k < ElemOf<GT>::kWords; ++k) zero.w[k] = 0u;
-        while (absent) {
-            const int64_t v = w * 32 + __ffs(absent) - 1;
-            absent &= absent - 1;
-            void *row = row_of<GT>(a.dtable, v, a.table_stride);
-#pragma unroll 4
-            for (int t = 0; t < tiles; ++t) store_tile<GT, VEC>(row, t * kTileCols, a.cols, lane, zero);
-        }
+        const uint32_t present = a.present[w];
+#pragma unroll 1
+        for (int k = warp; k < 32; k += 8)
+            if (!((present >> k) & 1) && w * 32 + k < a.table_rows)
+                clear_row<GT, VEC>(row_of<GT>(a.dtable, w * 32 + k, a.table_stride), a.cols, lane);
         return;
     }
-    const int64_t chunks = (a.rows + kChunk - 1) / kChunk;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+    const int size = a.chunk;
+    const int64_t chunks = (a.rows + size - 1) / size;
+    const int64_t item = static_cast<int64_t>(turn) * 8 + warp;
     const int64_t chunk = item / tiles;
     const int tile = static_cast<int>(item - chunk * tiles), base = tile * kTileCols;
     if (chunk >= chunks) return;
     const uint32_t nowhere = static_cast<uint32_t>(a.table_rows);
-    const int64_t at = chunk * kChunk + lane;
-    const uint32_t key = at < a.rows ? a.keys[at] : nowhere;
-    const uint32_t pos = at < a.rows ? a.order[at] : 0u;
-    const uint32_t key_before = chunk > 0 ? a.keys[chunk * kChunk - 1] : nowhere;
-    const uint32_t key_after = (chunk + 1) * kChunk < a.rows ? a.keys[(chunk + 1) * kChunk] : nowhere;
+    const int64_t at = chunk * size + lane;
+    const bool mine = lane < size && at < a.rows;
+    const uint32_t key = mine ? a.keys[at] : nowhere;
+    const uint32_t pos = mine ? a.order[at] : 0u;
+    const uint32_t key_before = chunk > 0 ? a.keys[chunk * size - 1] : nowhere;
+    const uint32_t key_after = (chunk + 1) * size < a.rows ? a.keys[(chunk + 1) * size] : nowhere;
     const int count = __popc(__ballot_sync(kAllLanes, key != nowhere));  // positions without a token come last
     if (count == 0) return;
+    // where a run ends: the next key is another (last lane: the next chunk's first)
+    uint32_t key_next = __shfl_down_sync(kAllLanes, key, 1);
+    if (lane == size - 1) key_next = key_after;
+    const unsigned ends = __ballot_sync(kAllLanes, lane < count && (key_next != key || lane == count - 1));
+    const bool goes_on = count == size && key_after == __shfl_sync(kAllLanes, key, size - 1);
 
     float2 sum[4] = {};
-    uint32_t current = __shfl_sync(kAllLanes, key, 0);
-    bool from_before = chunk > 0 && key_before == current;
-    auto put = [&](bool goes_on) {
-        if (!from_before && !goes_on) {
-            write_sum<GT, VEC>(a, current, base, lane, sum);
-        } else {
-            float4 *p = partial_at(a, chunk, from_before ? 0 : 1, tile, lane);
-            p[0] = make_float4(sum[0].x, sum[0].y, sum[1].x, sum[1].y);
-            p[1] = make_float4(sum[2].x, sum[2].y, sum[3].x, sum[3].y);
-        }
-    };
-    constexpr int U = 8;  // rows in flight
+    bool from_before = chunk > 0 && key_before == __shfl_sync(kAllLanes, key, 0);
+    constexpr int U = ACCUMULATE ? 4 : 8;  // rows in flight, with accumulate each with the row it is added to
     for (int i0 = 0; i0 < count; i0 += U) {
         Raw8<DT> r[U];
+        Raw8<GT> old[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t t = __shfl_sync(kAllLanes, pos, i0 + u);
-            if (i0 + u < count) r[u] = load_tile<DT, VEC>(row_of<DT>(a.dout, t, a.dout_stride), base, a.cols, lane);
+            const uint32_t t = __shfl_sync(kAllLanes, pos, i0 + u), k = __shfl_sync(kAllLanes, key, i0 + u);
+            if (i0 + u < count) {
+                r[u] = load_tile<DT, VEC>(row_of<DT>(a.dout, t, a.dout_stride), base, a.cols, lane);
+                if (ACCUMULATE && (ends >> (i0 + u) & 1)) old[u] = old_row<GT, VEC>(a, k, base, lane);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t k = __shfl_sync(kAllLanes, key, i0 + u);
             if (i0 + u >= count) break;
-            if (k != current) {
-                put(false);
-                current = k;
-                from_before = false;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sum[j] = both(0.0f);
-            }
             float2 f[4];
             unpack8<DT>(r[u], f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], f[j]);
+            if (!(ends >> (i0 + u) & 1)) continue;
+            const bool crosses = from_before || (goes_on && i0 + u == count - 1);
+            if (!crosses) {
+                write_sum<GT, VEC>(a, k, base, lane, sum, old[u]);
+            } else {
+                float4 *p = partial_at(a, chunk, from_before ? 0 : 1, tile, lane);
+                p[0] = make_float4(sum[0].x, sum[0].y, sum[1].x, sum[1].y);
+                p[1] = make_float4(sum[2].x, sum[2].y, sum[3].x, sum[3].y);
+            }
+            from_before = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] = both(0.0f);
         }
     }
-    put(count == kChunk && key_after == current);
 }
 
-// Runs that cross chunks: the block of the chunk where a run begins adds its
-// slot 1 and the slots 0 of the chunks after it, its 8 warps every eighth.
+// Runs that cross chunks: the warp of the chunk where a run begins adds its slot
+// 1 and the slots 0 of the chunks after it; runs of more than kLongRun chunks
+// are added by the whole block, each warp every eighth chunk.
+constexpr int kLongRun = 16;
+
 template <int GT, bool VEC> __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
     enter_grid();
     __shared__ float2 part[8][4][32];
+    __shared__ int64_t reaches[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tile = blockIdx.y, base = tile * kTileCols;
-    const int64_t chunk = blockIdx.x, chunks = (a.rows + kChunk - 1) / kChunk;
-    const int64_t last = chunk * kChunk + kChunk - 1;
-    if (last + 1 >= a.rows) return;
-    const uint32_t v = a.keys[last];
-    if (v == static_cast<uint32_t>(a.table_rows) || a.keys[last + 1] != v) return;  // no run goes on from here
-    if (chunk > 0 && a.keys[chunk * kChunk - 1] == v) return;                       // or it began earlier
-    // chunks after this one that the run reaches: heads[chunk + 1 .. chunk + reach] == v
-    int64_t reach = 0;
-    while (true) {
-        const int64_t c = chunk + 1 + reach + lane;
-        const unsigned in = __ballot_sync(kAllLanes, c < chunks && a.keys[c * kChunk] == v);
-        reach += in == kAllLanes ? 32 : __ffs(~in) - 1;
-        if (in != kAllLanes) break;
+    const int size = a.chunk;
+    const int64_t chunk = static_cast<int64_t>(blockIdx.x) * 8 + warp, chunks = (a.rows + size - 1) / size;
+    const int64_t last = chunk * size + size - 1;
+    const uint32_t nowhere = static_cast<uint32_t>(a.table_rows);
+    uint32_t v = nowhere, after = nowhere, ahead = nowhere;
+    if (last + 1 < a.rows) {
+        v = a.keys[last];
+        after = a.keys[last + 1];
+        ahead = chunk > 0 ? a.keys[last - size] : nowhere;
     }
-    float2 sum[4] = {};
-    auto add = [&](int64_t c, int slot) {
+    int64_t reach = 0;  // chunks after this one that a run reaches which begins here
+    if (v != nowhere && after == v && ahead != v) {
+        // the chunks' first keys rise, so those equal to v come first: 32 probes at a time
+        int64_t lo = chunk + 1, hi = chunks;
+        while (lo < hi) {
+            const int64_t step = (hi - lo + 31) / 32, probe = lo + lane * step;
+            const int found = __popc(__ballot_sync(kAllLanes, probe < hi && a.keys[probe * size] == v));
+            hi = min(hi, lo + found * step);
+            if (found > 0) lo += (found - 1) * step + 1;
+        }
+        reach = lo - (chunk + 1);
+    }
+    if (lane == 0) reaches[warp] = reach;
+    auto add = [&](float2 (&sum)[4], int64_t c, int slot) {
         const float4 *p = partial_at(a, c, slot, tile, lane);
         const float4 x = p[0], y = p[1];
         sum[0] = add2(sum[0], make_float2(x.x, x.y));
@@ -322,44 +414,95 @@ template <int GT, bool VEC> __global__ void __launch_bounds__(256) embed_join_ke
         sum[2] = add2(sum[2], make_float2(y.x, y.y));
         sum[3] = add2(sum[3], make_float2(y.z, y.w));
     };
-    if (warp == 0) add(chunk, 1);
-#pragma unroll 4
-    for (int64_t k = warp; k < reach; k += 8) add(chunk + 1 + k, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) part[warp][j][lane] = sum[j];
+    if (reach > 0 && reach <= kLongRun) {
+        float2 sum[4] = {};
+        Raw8<GT> old = {};
+        if (a.accumulate) old = old_row<GT, VEC>(a, v, base, lane);
+        add(sum, chunk, 1);
+#pragma unroll 8
+        for (int64_t k = 0; k < reach; ++k) add(sum, chunk + 1 + k, 0);
+        write_sum<GT, VEC>(a, v, base, lane, sum, old);
+    }
     __syncthreads();
-    if (warp != 0) return;
+#pragma unroll 1
+    for (int w = 0; w < 8; ++w) {
+        const int64_t far = reaches[w];
+        if (far <= kLongRun) continue;
+        const int64_t from = static_cast<int64_t>(blockIdx.x) * 8 + w;
+        float2 sum[4] = {};
+        if (warp == 0) add(sum, from, 1);
+#pragma unroll 8
+        for (int64_t k = warp; k < far; k += 8) add(sum, from + 1 + k, 0);
 #pragma unroll
-    for (int w = 1; w < 8; ++w)
+        for (int j = 0; j < 4; ++j) part[warp][j][lane] = sum[j];
+        __syncthreads();
+        if (warp == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], part[w][j][lane]);
-    write_sum<GT, VEC>(a, v, base, lane, sum);
+            for (int k = 1; k < 8; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] = add2(sum[j], part[k][j][lane]);
+            const uint32_t far_v = a.keys[from * size + size - 1];
+            Raw8<GT> old = {};
+            if (a.accumulate) old = old_row<GT, VEC>(a, far_v, base, lane);
+            write_sum<GT, VEC>(a, far_v, base, lane, sum, old);
+        }
+        __syncthreads();
+    }
 }
 
 template <int DT, int GT, bool VEC>
-cudaError_t embed_grad_launch(const EmbedGradArgs &a, cudaStream_t s, LaunchInfo *info, int *launches) {
-    const int64_t tiles = (a.cols + kTileCols - 1) / kTileCols, chunks = (a.rows + kChunk - 1) / kChunk;
+cudaError_t embed_grad_launch(EmbedGradArgs a, int sms, cudaStream_t s, LaunchInfo *info, int *launches) {
+    int width = 0;  // bits of a key: 0 .. table_rows
+    while (width < 32 && (static_cast<uint64_t>(a.table_rows) >> width) != 0) ++width;
+    const int passes = std::max(1, (width + kDigitBits - 1) / kDigitBits);
+    const int bits = std::max(1, (width + passes - 1) / passes);
+    const size_t smem = size_t(kSortWarps) * 4 << bits;
+    static std::atomic<uint64_t> allowed{0};
+    auto sort = embed_sort_kernel<GT, VEC>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(sort), (kSortWarps * 4) << kDigitBits, &allowed);
+    if (e != cudaSuccess) return e;
+    // Rows to clear meanwhile: what 6 TB/s write in the sort's time, about 9 us
+    // and 0.4 ns a position; whole words of the bitmap.
+    a.chunk = chunk_of(a.rows, a.cols);
+    a.blind = 0;
+    int64_t clear_blocks = 0;
+    if (!a.accumulate) {
+        const double bytes = (9e-6 + 0.4e-9 * static_cast<double>(a.rows)) * 6e12;
+        const double rows = bytes / (static_cast<double>(a.cols) * ElemOf<GT>::kBytes);
+        a.blind = rows >= static_cast<double>(a.table_rows) ? (a.table_rows + 31) / 32 * 32 : static_cast<int64_t>(rows) / 32 * 32;
+        a.blind = std::min(a.blind, a.table_rows);
+        // up to two blocks of 1024 threads an SM, in whole clusters
+        clear_blocks = std::min<int64_t>((a.blind + kSortWarps - 1) / kSortWarps, 2 * sms);
+        clear_blocks = (clear_blocks + kSortBlocks - 1) / kSortBlocks * kSortBlocks;
+    }
+    e = launch_rows(sort, dim3(kSortBlocks + clear_blocks), dim3(kSortThreads), smem, kSortBlocks, s, a, passes, bits);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    info->smem = static_cast<int>(smem);
+
+    const int64_t tiles = (a.cols + kTileCols - 1) / kTileCols, chunks = (a.rows + a.chunk - 1) / a.chunk;
     const int64_t sums = (chunks * tiles + 7) / 8;
-    const int64_t fills = a.accumulate ? 0 : (a.table_rows + 255) / 256;
+    const int64_t fills = a.accumulate ? 0 : (a.table_rows + 31) / 32 - a.blind / 32;
     if (sums + fills > INT32_MAX || tiles > 65535) return cudaErrorInvalidConfiguration;
     info->vec_bytes = VEC ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
     info->grid = static_cast<int>(sums + fills);
     info->block = 256;
-    cudaError_t e = cudaSuccess;
     if (sums + fills > 0) {
-        e = launch_rows(embed_sum_kernel<DT, GT, VEC>, dim3(sums + fills), dim3(256), 0, 1, s, a, sums);
+        const uint32_t every = sums > 0 ? static_cast<uint32_t>((sums + fills) / sums) : 1;
+        auto sum = a.accumulate ? embed_sum_kernel<DT, GT, VEC, true> : embed_sum_kernel<DT, GT, VEC, false>;
+        e = launch_rows(sum, dim3(sums + fills), dim3(256), 0, 1, s, a, static_cast<uint32_t>(sums), every);
         ++*launches;
     }
     if (e != cudaSuccess || chunks < 2) return e;
     ++*launches;
-    return launch_rows(embed_join_kernel<GT, VEC>, dim3(chunks, tiles), dim3(256), 0, 1, s, a);
+    return launch_rows(embed_join_kernel<GT, VEC>, dim3((chunks + 7) / 8, tiles), dim3(256), 0, 1, s, a);
 }
 
 template <int DT, int GT>
-cudaError_t embed_grad_dispatch(const EmbedGradArgs &a, cudaStream_t s, LaunchInfo *info, int *launches) {
+cudaError_t embed_grad_dispatch(const EmbedGradArgs &a, int sms, cudaStream_t s, LaunchInfo *info, int *launches) {
     return wide_rows<DT>(a.dout, a.dout_stride) && wide_rows<GT>(a.dtable, a.table_stride)
-               ? embed_grad_launch<DT, GT, true>(a, s, info, launches)
-               : embed_grad_launch<DT, GT, false>(a, s, info, launches);
+               ? embed_grad_launch<DT, GT, true>(a, sms, s, info, launches)
+               : embed_grad_launch<DT, GT, false>(a, sms, s, info, launches);
 }
 
 }  // namespace
@@ -371,29 +514,18 @@ cudaError_t launch_embed(int dtype, const EmbedArgs &a, int sms, cudaStream_t s,
 }
 
 int64_t embed_partial_bytes(int64_t rows, int64_t cols) {
-    return (rows + kChunk - 1) / kChunk * 2 * ((cols + kTileCols - 1) / kTileCols) * kTileCols * 4;
+    const int size = chunk_of(rows, cols);
+    return (rows + size - 1) / size * 2 * ((cols + kTileCols - 1) / kTileCols) * kTileCols * 4;
 }
 
-cudaError_t launch_embed_grad(int dtype, int gtype, const EmbedGradArgs &a, cudaStream_t s, LaunchInfo *info,
+cudaError_t launch_embed_grad(int dtype, int gtype, const EmbedGradArgs &a, int sms, cudaStream_t s, LaunchInfo *info,
                               int *launches) {
-    int width = 0;  // bits of a key: 0 .. table_rows
-    while (width < 32 && (static_cast<uint64_t>(a.table_rows) >> width) != 0) ++width;
-    const int passes = std::max(1, (width + kDigitBits - 1) / kDigitBits);
-    const int bits = std::max(1, (width + passes - 1) / passes);
-    const size_t smem = size_t(kSortWarps) * 4 << bits;
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(embed_sort_kernel), (kSortWarps * 4) << kDigitBits, &allowed);
-    if (e == cudaSuccess)
-        e = launch_rows(embed_sort_kernel, dim3(kSortBlocks), dim3(kSortThreads), smem, kSortBlocks, s, a, passes, bits);
-    if (e != cudaSuccess) return e;
-    ++*launches;
-    info->smem = static_cast<int>(smem);
-    if (dtype == DT_F32) return embed_grad_dispatch<DT_F32, DT_F32>(a, s, info, launches);
+    if (dtype == DT_F32) return embed_grad_dispatch<DT_F32, DT_F32>(a, sms, s, info, launches);
     if (dtype == DT_F16)
-        return gtype == DT_F32 ? embed_grad_dispatch<DT_F16, DT_F32>(a, s, info, launches)
-                               : embed_grad_dispatch<DT_F16, DT_F16>(a, s, info, launches);
-    return gtype == DT_F32 ? embed_grad_dispatch<DT_BF16, DT_F32>(a, s, info, launches)
-                           : embed_grad_dispatch<DT_BF16, DT_BF16>(a, s, info, launches);
+        return gtype == DT_F32 ? embed_grad_dispatch<DT_F16, DT_F32>(a, sms, s, info, launches)
+                               : embed_grad_dispatch<DT_F16, DT_F16>(a, sms, s, info, launches);
+    return gtype == DT_F32 ? embed_grad_dispatch<DT_BF16, DT_F32>(a, sms, s, info, launches)
+                           : embed_grad_dispatch<DT_BF16, DT_BF16>(a, sms, s, info, launches);
 }
 
 }  // namespace ew

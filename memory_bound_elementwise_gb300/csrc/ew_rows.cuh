@@ -239,24 +239,11 @@ __device__ __forceinline__ float block_max_nan(float v, int warps, float *part, 
 
 // ---------------------------------------------------------------- clusters
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-__device__ __forceinline__ uint32_t load_of_block(const uint32_t *mine, uint32_t rank) {
-    uint32_t at, v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-        : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
-}
-
 // The address of a shared variable of this block as block `rank` of the cluster has it.
 template <typename T> __device__ __forceinline__ const T *in_block(const T *mine, uint32_t rank) {
     uint64_t at;

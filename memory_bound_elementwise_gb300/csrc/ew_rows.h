@@ -130,10 +130,13 @@ struct EmbedGradArgs {
     uint32_t *keys, *order;  // sorted tokens (table_rows: none) and their positions
     uint32_t *present;       // a bit for each table row that a token names; null with accumulate
     float *partial;          // sums of the runs that cross chunks
+    // set by the launch
+    int64_t blind;           // rows that are cleared beside the sort
+    int32_t chunk;           // sorted positions a warp adds
 };
 int64_t embed_partial_bytes(int64_t rows, int64_t cols);
-cudaError_t launch_embed_grad(int dtype, int gtype, const EmbedGradArgs &a, cudaStream_t s, LaunchInfo *info,
-                              int *launches);
+cudaError_t launch_embed_grad(int dtype, int gtype, const EmbedGradArgs &a, int sms, cudaStream_t s,
+                              LaunchInfo *info, int *launches);
 
 // ---------------------------------------------------------------- logits
 

@@ -253,10 +253,12 @@ ew_status ew_embed_grad(ew_dtype dt, ew_index itype, const void *dout, int64_t d
                           reinterpret_cast<uint2 *>(base + w.items1), reinterpret_cast<uint32_t *>(base + w.keys),
                           reinterpret_cast<uint32_t *>(base + w.order),
                           accumulate ? nullptr : reinterpret_cast<uint32_t *>(base + w.present),
-                          reinterpret_cast<float *>(base + w.partial)};
+                          reinterpret_cast<float *>(base + w.partial), 0, 0};
     LaunchInfo info;
-    int launches = 0;
-    const cudaError_t ce = launch_embed_grad(dt, gtype, a, reinterpret_cast<cudaStream_t>(s), &info, &launches);
+    int launches = 0, sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    ce = launch_embed_grad(dt, gtype, a, sms, reinterpret_cast<cudaStream_t>(s), &info, &launches);
     if (ce != cudaSuccess) return report_cuda(ce);
     record(info, launches);
     return EW_OK;
