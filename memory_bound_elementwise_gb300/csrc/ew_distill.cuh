@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kThreads, kResident) distill_kernel(DistillArg
         mine_counts = mine_counts || e.id >= 0;
     }
     Sums v = no_sums();
-    if constexpr (SUMS) v = warp_sums<32, false>(pass_over<DT, false, false>(sh, ax, nullptr, 0, first_turn));
+    float largest;
+    if constexpr (SUMS) v = warp_sums<32, false>(pass_over<DT, false, false>(sh, ax, nullptr, 0, first_turn, largest));
     if (lane == 0) part[warp] = v;
     const bool any = __syncthreads_or(mine_counts);
 

@@ -316,17 +316,24 @@ __device__ __forceinline__ RowSum finish_row(const Sums &v, const void *row, int
 
 // ---------------------------------------------------------------- top alternatives
 //
-// The largest `k` elements, equal ones by index.  The first elements that the
-// block reads give a bound: of 128 groups of lanes, the k-th largest group
-// maximum; at least k elements reach it.  Elements that reach it are collected
-// while the row streams past (a few hundred of a row in no particular order)
-// and ranked at the end.  Where more than kCandidates are collected, exact_top
-// finds the k-th value by bisection instead.
+// The largest `k` elements, equal ones by index.  Any k-th largest of disjoint
+// groups' maxima is a bound that at least k elements reach, and not many more:
+// of 32 groups, about 31 elements for k = 20.  The first turn gives a bound for
+// the rest of the row, the first two and four turns better ones; elements that
+// reach it are collected while the row streams past (a hundred or so of a row
+// in no particular order).  At the end the groups' maxima over the whole row
+// give the last bound, and the few that reach it are ranked.  Where more than
+// kCandidates are collected, exact_top finds the k-th value by bisection
+// instead.
 
 constexpr int kCandidates = 2048;
-constexpr int kGroups = 128;  // of two lanes each
+constexpr int kFew = 512;
+constexpr int kManyGroups = 128;    // of two lanes each, for k past kFewGroupsTop
+constexpr int kFewGroups = 32;      // of eight
+constexpr int kFewGroupsTop = 24;
+constexpr int kBounds = 4;          // times that a bound is found
 
-struct Candidate {
+struct alignas(8) Candidate {
     float x;
     int id;
 };
@@ -334,12 +341,13 @@ __device__ __forceinline__ bool before(const Candidate &a, const Candidate &b) {
     return a.x > b.x || (a.x == b.x && a.id < b.id);
 }
 
-struct TopShared {
-    alignas(16) float group[kGroups];
-    float bound;
-    int count;
-    Candidate list[kCandidates];
-    Candidate best[kMostTop];  // ids of -1 at the end where there are fewer
+struct TopShared {  // every array at a multiple of 16 bytes
+    alignas(16) float group[kManyGroups];
+    alignas(16) Candidate list[kCandidates];
+    alignas(16) Candidate few[kFew];
+    alignas(16) Candidate best[kMostTop];  // ids of -1 at the end where there are fewer
+    alignas(16) float bound;
+    int count, few_count;
 };
 
 __device__ __forceinline__ void collect(TopShared &t, float x, int id) {
@@ -373,26 +381,62 @@ __device__ __forceinline__ void rank_list(const Candidate *list, int n, int k, C
     }
 }
 
-// Bound from the largest element that each thread has seen.
-__device__ __forceinline__ void find_bound(TopShared &t, float mine, int k) {
-    static_assert(kGroups * 2 == kThreads && kGroups >= kMostTop, "a group to two lanes, and a k-th largest group");
+// The bound that the largest elements which the threads have seen give.  Every
+// thread of the block takes part; what else was written to shared memory is
+// visible after it.  The calls of a kernel use different slots: a warp may be in
+// the next while another still reads for the last.
+__device__ __forceinline__ float find_bound(TopShared &t, float mine, int k, int slot) {
+    static_assert(kManyGroups * 2 == kThreads && kFewGroups * 8 == kThreads && kManyGroups >= kMostTop &&
+                      kFewGroups >= kFewGroupsTop && kBounds * kFewGroups <= kManyGroups, "groups of lanes, and a k-th largest of them");
+    const int lane = threadIdx.x & 31;
     mine = fmaxf(mine, __shfl_xor_sync(kAllLanes, mine, 1));
-    if ((threadIdx.x & 1) == 0) t.group[threadIdx.x >> 1] = mine;
-    if (threadIdx.x == 0) t.count = 0;
+    if (k <= kFewGroupsTop) {
+        mine = fmaxf(mine, __shfl_xor_sync(kAllLanes, mine, 2));
+        mine = fmaxf(mine, __shfl_xor_sync(kAllLanes, mine, 4));
+        if ((lane & 7) == 0) t.group[slot * kFewGroups + (threadIdx.x >> 3)] = mine;
+        __syncthreads();
+        float v = t.group[slot * kFewGroups + lane];  // each warp sorts them, the largest first
+#pragma unroll
+        for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+            for (int d = size / 2; d > 0; d /= 2) {
+                const float o = __shfl_xor_sync(kAllLanes, v, d);
+                v = ((lane & d) == 0) == ((lane & size) == 0) ? fmaxf(v, o) : fminf(v, o);
+            }
+        return __shfl_sync(kAllLanes, v, k - 1);
+    }
+    if ((lane & 1) == 0) t.group[threadIdx.x >> 1] = mine;
     __syncthreads();
-    if (threadIdx.x < kGroups) {
+    if (threadIdx.x < kManyGroups) {
         const float v = t.group[threadIdx.x];
+        const int me = threadIdx.x;
         int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < kGroups; j += 4) {
+        for (int j = 0; j < kManyGroups; j += 4) {
             const float4 g = *reinterpret_cast<const float4 *>(t.group + j);
-            const int me = threadIdx.x;
             rank += (g.x > v || (g.x == v && j < me)) + (g.y > v || (g.y == v && j + 1 < me)) +
                     (g.z > v || (g.z == v && j + 2 < me)) + (g.w > v || (g.w == v && j + 3 < me));
         }
         if (rank == k - 1) t.bound = v;
     }
     __syncthreads();
+    return t.bound;
+}
+
+// The k best of the list's entries that reach the bound, into best.
+__device__ __forceinline__ void rank_few(TopShared &t, float bound, int k) {
+    const int n = t.count;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const Candidate c = t.list[i];
+        if (c.x >= bound) {
+            const int at = atomicAdd(&t.few_count, 1);
+            if (at < kFew) t.few[at] = c;
+        }
+    }
+    __syncthreads();
+    const int few = t.few_count;
+    if (few <= kFew) rank_list(t.few, few, k, t.best);
+    else rank_list(t.list, n, k, t.best);
 }
 
 // Order of binary32 values as unsigned integers (-0 and +0 the same).
@@ -402,7 +446,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 
 // The exact k best of the block's share, however many elements tie.
-template <int DT> __device__ __noinline__ void exact_top(TopShared &t, const Share<DT> &sh, int k) {
+template <int DT> __device__ __noinline__ void exact_top(TopShared &t, const Share<DT> &sh, int k, float bound) {
     constexpr int V = Chunk<DT>::kElems;
     auto count_from = [&](uint32_t least) {  // elements of the share from `least` on
         int n = 0;
@@ -424,9 +468,9 @@ template <int DT> __device__ __noinline__ void exact_top(TopShared &t, const Sha
         __syncthreads();
         return t.count;
     };
-    // the k-th largest value: the largest `least` that k elements reach.  The
-    // collected elements say that k reach the bound; often no more lie above.
-    uint32_t lo = order_of(t.bound), hi = 0xffffffffu;
+    // the k-th largest value: the largest `least` that k elements reach, which
+    // the bound is known to be; often no more than that lie above it
+    uint32_t lo = order_of(bound), hi = 0xffffffffu;
     for (uint32_t probe = lo + 1; lo < hi; probe = lo + (hi - lo) / 2 + 1) {
         if (count_from(probe) >= k) lo = probe;
         else hi = probe - 1;
@@ -493,21 +537,24 @@ __device__ __forceinline__ void load_turn(const Share<DT> &sh, int c0, Chunk<DT>
 
 // A thread's sums over the block's share of a row; with TOP, the elements
 // that may be among the k best are in t's list when the block next synchronises.
-// r comes with the first turn loaded and is left with the last one: the whole
-// share where that is one turn.
+// r comes with the first turn loaded; largest is the thread's largest element.
 template <int DT, bool ENTROPY, bool TOP>
-__device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShared *t, int k, Chunk<DT> (&r)[kFlight]) {
+__device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShared *t, int k, Chunk<DT> (&r)[kFlight],
+                                          float &largest) {
     PairSums v = {kLeastExponent, both(0.0f), both(0.0f)};
     const bool single = static_cast<int>(threadIdx.x) < sh.singles;
     const float one = single ? sh.at(sh.single(threadIdx.x)) : kNegInf;
+    largest = one;
     float bound = kNegInf;
-    for (int c0 = sh.first + static_cast<int>(threadIdx.x);;) {
+    int c0 = sh.first + static_cast<int>(threadIdx.x);
+    for (int turn = 0;; ++turn) {
         const float top = add_chunks<DT, ENTROPY>(v, r, a);
         if constexpr (TOP) {
-            if (c0 < sh.first + kTurn) {  // the first turn, for all threads
-                find_bound(*t, fmaxf(top, one), k);
-                bound = t->bound;
-                if (one >= bound && one > kNegInf) collect(*t, one, sh.single(threadIdx.x));
+            largest = fmaxf(largest, top);
+            if (turn == 0 && threadIdx.x == 0) t->count = t->few_count = 0;
+            if (turn == 0 || turn == 1 || turn == 3) {
+                bound = find_bound(*t, largest, k, (turn + 1) / 2);
+                if (turn == 0 && one >= bound && one > kNegInf) collect(*t, one, sh.single(threadIdx.x));
             }
             if (top >= bound && top > kNegInf) {
 #pragma unroll
@@ -546,25 +593,45 @@ template <int DT, bool TOP> __global__ void __launch_bounds__(kThreads, kResiden
     const float ax = a.scale * kLog2e;
     Chunk<DT> r_chunks[kFlight];
     load_turn<DT>(sh, sh.first + static_cast<int>(threadIdx.x), r_chunks);
-    Sums v = warp_sums<32, true>(pass_over<DT, true, TOP>(sh, ax, t, a.top, r_chunks));
+    float largest;
+    Sums v = warp_sums<32, true>(pass_over<DT, true, TOP>(sh, ax, t, a.top, r_chunks, largest));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();  // every candidate is in the list too
+    float bound = kNegInf;
+    if constexpr (TOP) bound = find_bound(*t, largest, a.top, kBounds - 1);  // with a barrier: every candidate is in the list
+    else __syncthreads();
     v = sums_of_warps<kWarps, true>(part);
     if constexpr (TOP) {
-        if (t->count > kCandidates) exact_top<DT>(*t, sh, a.top);
-        rank_list(t->list, t->count, a.top, t->best);
-        __syncthreads();
+        if (t->count > kCandidates) exact_top<DT>(*t, sh, a.top, bound);
+        rank_few(*t, bound, a.top);
     }
     if (blocks > 1) {
         if (threadIdx.x == 0) mine = v;
-        if (TOP && threadIdx.x == 0) t->count = 0;
+        if constexpr (TOP) {
+            __syncthreads();
+            if (threadIdx.x == 0) t->count = 0;
+        }
         cluster_sync();
         if (block == 0) {
             v = cluster_sums<true>(&mine, blocks);
             if constexpr (TOP) {
+                // Of every block's best ceil(k / blocks) are at least k, all of which reach the least of them; and
+                // every block's k-th best is reached by k.
+                const int lane = threadIdx.x & 31, each = (a.top + blocks - 1) / blocks;
+                float low = -kNegInf, high = kNegInf;
+                if (lane < blocks) {
+                    const Candidate *its = in_block(t->best, lane);
+                    low = its[each - 1].x;
+                    high = its[a.top - 1].x;
+                }
+#pragma unroll
+                for (int d = 4; d > 0; d >>= 1) {
+                    low = fminf(low, __shfl_xor_sync(kAllLanes, low, d));
+                    high = fmaxf(high, __shfl_xor_sync(kAllLanes, high, d));
+                }
+                bound = fmaxf(__shfl_sync(kAllLanes, low, 0), __shfl_sync(kAllLanes, high, 0));
                 for (int i = threadIdx.x; i < blocks * a.top; i += kThreads) {
                     const Candidate c = in_block(t->best, i / a.top)[i % a.top];
-                    if (c.id >= 0) collect(*t, c.x, c.id);
+                    if (c.id >= 0 && c.x >= bound) collect(*t, c.x, c.id);
                 }
                 __syncthreads();
                 rank_list(t->list, t->count, a.top, t->best);
