@@ -711,9 +711,10 @@ template <int DT> __device__ __forceinline__ void store_one(void *row, int col, 
 
 // Rows whose p is formed the careful way.
 template <int DT, bool ENTROPY>
-__device__ __noinline__ void write_grad_slowly(const Share<DT> &sh, void *out, const RowGrad &r, float a, float scale) {
+__device__ __noinline__ void write_grad_slowly(const Share<DT> &sh, void *out, const RowGrad &r, float a, float scale,
+                                               int threads = kThreads) {
     constexpr int V = Chunk<DT>::kElems;
-    for (int c = sh.first * V + static_cast<int>(threadIdx.x); c < sh.end * V; c += blockDim.x)
+    for (int c = sh.first * V + static_cast<int>(threadIdx.x); c < sh.end * V; c += threads)
         store_one<DT>(out, sh.head + c, grad_of<ENTROPY>(r, sh.at(sh.head + c), a, scale));
     if (static_cast<int>(threadIdx.x) < sh.singles) {
         const int col = sh.single(threadIdx.x);
@@ -722,11 +723,12 @@ __device__ __noinline__ void write_grad_slowly(const Share<DT> &sh, void *out, c
 }
 
 // Zeros for the block's share, whatever the logits are.
-template <int DT> __device__ __forceinline__ void write_zeros(void *out_row, int cols, int block, Split split) {
+template <int DT> __device__ __forceinline__ void write_zeros(void *out_row, int cols, int block, Split split,
+                                                               int threads = kThreads) {
     const Share<DT> sh(out_row, cols, block, split);
     typename ElemOf<DT>::type *out = static_cast<typename ElemOf<DT>::type *>(out_row);
     const Vec<16> zero = {};
-    for (int c = sh.first + static_cast<int>(threadIdx.x); c < sh.end; c += blockDim.x) st<16>(out + sh.column(c, 0), zero);
+    for (int c = sh.first + static_cast<int>(threadIdx.x); c < sh.end; c += threads) st<16>(out + sh.column(c, 0), zero);
     if (static_cast<int>(threadIdx.x) < sh.singles) store_one<DT>(out, sh.single(threadIdx.x), 0.0f);
 }
 
