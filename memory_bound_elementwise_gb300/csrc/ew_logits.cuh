@@ -528,17 +528,17 @@ template <int DT> __device__ __forceinline__ Sums finished(const PairSums &v, bo
 }
 
 // The thread's chunks of the turn that begins at its chunk c0; those past the share are masked.
-template <int DT>
+template <int DT, int THREADS = kThreads>
 __device__ __forceinline__ void load_turn(const Share<DT> &sh, int c0, Chunk<DT> (&r)[kFlight]) {
 #pragma unroll
     for (int u = 0; u < kFlight; ++u)
-        r[u] = c0 + u * kThreads < sh.end ? sh.chunk(c0 + u * kThreads) : masked_chunk<DT>();
+        r[u] = c0 + u * THREADS < sh.end ? sh.chunk(c0 + u * THREADS) : masked_chunk<DT>();
 }
 
 // A thread's sums over the block's share of a row; with TOP, the elements
 // that may be among the k best are in t's list when the block next synchronises.
 // r comes with the first turn loaded; largest is the thread's largest element.
-template <int DT, bool ENTROPY, bool TOP>
+template <int DT, bool ENTROPY, bool TOP, int THREADS = kThreads>
 __device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShared *t, int k, Chunk<DT> (&r)[kFlight],
                                           float &largest) {
     PairSums v = {kLeastExponent, both(0.0f), both(0.0f)};
@@ -550,6 +550,7 @@ __device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShare
     for (int turn = 0;; ++turn) {
         const float top = add_chunks<DT, ENTROPY>(v, r, a);
         if constexpr (TOP) {
+            static_assert(THREADS == kThreads, "the groups of the bounds");
             largest = fmaxf(largest, top);
             if (turn == 0 && threadIdx.x == 0) t->count = t->few_count = 0;
             if (turn == 0 || turn == 1 || turn == 3) {
@@ -567,9 +568,9 @@ __device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShare
                 }
             }
         }
-        c0 += kTurn;
+        c0 += kFlight * THREADS;
         if (c0 - static_cast<int>(threadIdx.x) >= sh.end) break;
-        load_turn<DT>(sh, c0, r);
+        load_turn<DT, THREADS>(sh, c0, r);
     }
     return finished<DT>(v, single, one, a);
 }
@@ -754,48 +755,71 @@ template <int DT, bool ENTROPY> struct ChunkGrad {
         return o;
     }
 };
-template <int DT> __device__ __forceinline__ bool starts_alike(const void *out, const Share<DT> &sh) {
-    return (reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(sh.row)) % 16 == 0;
+// Bytes that an output row lies past the input row's place between multiples
+// of 16 bytes: chunks of both are 16-byte aligned where it is 0.
+template <int DT> __device__ __forceinline__ int bytes_apart(const void *out, const Share<DT> &sh) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(sh.row)) % 16);
 }
-// Stores a chunk's gradient; element by element where the output row starts at
-// another offset from 16 bytes than the input's (alike is false).
+// Stores a chunk's gradient.  Where the rows lie apart, a warp that stores 32
+// chunks in a row (`whole`, the same in all its lanes) shifts them by `apart`
+// bytes: a lane stores the end of the chunk of the lane before and the start of
+// its own to the aligned 16 bytes that they share, and the first and the last
+// lane the two ends left over, element by element.  Where a warp has fewer
+// chunks it stores elements.  50605 f16 columns, 2 bytes apart, took 200 us with
+// elements alone.
 template <int DT>
-__device__ __forceinline__ void store_chunk(typename ElemOf<DT>::type *to, const Vec<16> &d, bool alike) {
-    if (alike) {
+__device__ __forceinline__ void store_chunk(typename ElemOf<DT>::type *to, const Vec<16> &d, int apart, bool whole) {
+    constexpr int B = ElemOf<DT>::kBytes;
+    if (apart == 0) {
         st<16>(to, d);
-    } else {
+        return;
+    }
+    int first = 0, last = 16;  // bytes that go as elements
+    if (whole) {
+        const int lane = threadIdx.x & 31, from = 16 - apart;
+        uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == DT_F32) {
-                to[j] = d.w[j];
-            } else {
-                to[2 * j] = static_cast<uint16_t>(d.w[j]);
-                to[2 * j + 1] = static_cast<uint16_t>(d.w[j] >> 16);
-            }
+            w[j] = __shfl_up_sync(kAllLanes, d.w[j], 1);
+            w[j + 4] = d.w[j];
         }
+#pragma unroll
+        for (int j = 0; j < 6; ++j) w[j] = from & 8 ? w[j + 2] : w[j];
+#pragma unroll
+        for (int j = 0; j < 5; ++j) w[j] = from & 4 ? w[j + 1] : w[j];
+        Vec<16> o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.w[j] = __funnelshift_r(w[j], w[j + 1], (from & 3) * 8);
+        if (lane != 0) st<16>(reinterpret_cast<char *>(to) - apart, o);
+        first = lane == 31 ? from : 0;
+        last = lane == 0 ? from : lane == 31 ? 16 : 0;
     }
+#pragma unroll
+    for (int j = 0; j < 16 / B; ++j)
+        if (j * B >= first && j * B < last) to[j] = static_cast<typename ElemOf<DT>::type>(d.w[j * B / 4] >> (j * B % 4 * 8));
 }
 
 // Writes the gradient of the block's share, which it reads (again).
-template <int DT, bool ENTROPY>
+template <int DT, bool ENTROPY, int THREADS = kThreads>
 __device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, const RowGrad &g, float a, float scale) {
     using T = typename ElemOf<DT>::type;
     T *out = static_cast<T *>(out_row);
-    const bool alike = starts_alike(out, sh);
+    const int apart = bytes_apart(out, sh), last_lane = 31 - static_cast<int>(threadIdx.x & 31);
     if (g.w.careful) {
-        write_grad_slowly<DT, ENTROPY>(sh, out_row, g, a, scale);
+        write_grad_slowly<DT, ENTROPY>(sh, out_row, g, a, scale, THREADS);
         return;
     }
     const ChunkGrad<DT, ENTROPY> grad(g, a);
-    for (int c0 = sh.first + static_cast<int>(threadIdx.x); c0 < sh.end; c0 += kTurn) {
+    for (int c0 = sh.first + static_cast<int>(threadIdx.x); c0 < sh.end; c0 += kFlight * THREADS) {
         Chunk<DT> r[kFlight];
 #pragma unroll
         for (int u = 0; u < kFlight; ++u)
-            if (c0 + u * kThreads < sh.end) r[u] = sh.chunk(c0 + u * kThreads);
+            if (c0 + u * THREADS < sh.end) r[u] = sh.chunk(c0 + u * THREADS);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            if (c0 + u * kThreads >= sh.end) break;
-            store_chunk<DT>(out + sh.column(c0 + u * kThreads, 0), grad(r[u]), alike);
+            const int c = c0 + u * THREADS;
+            if (c >= sh.end) break;
+            store_chunk<DT>(out + sh.column(c, 0), grad(r[u]), apart, c + last_lane < sh.end);
         }
     }
     if (static_cast<int>(threadIdx.x) < sh.singles) {
