@@ -104,13 +104,19 @@ constexpr int kDigitBits = 10;
 
 constexpr int kKept = 4;  // items a lane keeps between counting and moving them
 
-template <int GT, bool VEC>
-__device__ __forceinline__ void clear_row(void *row, int cols, int lane) {
-    Raw8<GT> zero;
-#pragma unroll
-    for (int k = 0; k < ElemOf<GT>::kWords; ++k) zero.w[k] = 0u;
+// One row of zeros, by a warp: whole runs of 8 elements wherever the row starts,
+// and the elements before the first and after the last of them.
+template <int GT> __device__ __forceinline__ void clear_row(void *row, int cols, int lane) {
+    using T = typename ElemOf<GT>::type;
+    constexpr int B = ElemOf<GT>::kBytes;
+    T *p = static_cast<T *>(row);
+    const int past = static_cast<int>(reinterpret_cast<uintptr_t>(row) % (8 * B)) / B;
+    const int head = min((8 - past) % 8, cols), runs = (cols - head) / 8;
+    const Vec<8 * B> zero = {};
 #pragma unroll 4
-    for (int base = 0; base < cols; base += kTileCols) store_tile<GT, VEC>(row, base, cols, lane, zero);
+    for (int k = lane; k < runs; k += 32) st<8 * B>(p + head + k * 8, zero);
+    if (lane < head) p[lane] = 0;
+    if (head + runs * 8 + lane < cols) p[head + runs * 8 + lane] = 0;
 }
 
 // Inclusive prefix sum over the block's threads; `scan` has a slot a warp.
@@ -143,14 +149,14 @@ __device__ __forceinline__ unsigned lanes_alike(uint32_t digit, int bits, unsign
     return same;
 }
 
-template <int GT, bool VEC> __device__ __forceinline__ void clear_blind(const EmbedGradArgs &a, int sort_blocks) {
+template <int GT> __device__ __forceinline__ void clear_blind(const EmbedGradArgs &a, int sort_blocks) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t v = (static_cast<int64_t>(blockIdx.x) - sort_blocks) * kSortWarps + warp; v < a.blind;
          v += static_cast<int64_t>(gridDim.x - sort_blocks) * kSortWarps)
-        clear_row<GT, VEC>(row_of<GT>(a.dtable, v, a.table_stride), a.cols, lane);
+        clear_row<GT>(row_of<GT>(a.dtable, v, a.table_stride), a.cols, lane);
 }
 
-template <int GT, bool VEC>
+template <int GT>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradArgs a, int passes, int bits) {
     enter_grid();
     extern __shared__ uint32_t count[];  // [warp][digit]
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradArgs 
     __shared__ uint32_t scan[kSortWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= kSortBlocks) {
-        clear_blind<GT, VEC>(a, kSortBlocks);
+        clear_blind<GT>(a, kSortBlocks);
         return;
     }
     const uint32_t rank = blockIdx.x;
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a, uint32_
 #pragma unroll 1
         for (int k = warp; k < 32; k += 8)
             if (!((present >> k) & 1) && w * 32 + k < a.table_rows)
-                clear_row<GT, VEC>(row_of<GT>(a.dtable, w * 32 + k, a.table_stride), a.cols, lane);
+                clear_row<GT>(row_of<GT>(a.dtable, w * 32 + k, a.table_stride), a.cols, lane);
         return;
     }
     const int size = a.chunk;
@@ -458,7 +464,7 @@ cudaError_t embed_grad_launch(EmbedGradArgs a, int sms, cudaStream_t s, LaunchIn
     const int bits = std::max(1, (width + passes - 1) / passes);
     const size_t smem = size_t(kSortWarps) * 4 << bits;
     static std::atomic<uint64_t> allowed{0};
-    auto sort = embed_sort_kernel<GT, VEC>;
+    auto sort = embed_sort_kernel<GT>;
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(sort), (kSortWarps * 4) << kDigitBits, &allowed);
     if (e != cudaSuccess) return e;
     // Rows to clear meanwhile: what 6 TB/s write in the sort's time, about 9 us
