@@ -247,11 +247,11 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && VEC && KT * ElemOf<
 // and keep their columns' sums of dy * n in registers; each writes them once,
 // to its own row of `partial`, and dweight_kernel adds those rows in order.
 //
-// AHEAD, for rows that 8 warps hold: a row's loads are issued while the row
-// before is worked on, and the weights stay in registers.  With two blocks of
-// 256 threads and 4096 bf16 columns an SM has about 96 KiB in flight.  Wider
-// rows have no registers left for either.
-template <int DT, bool VEC, int KT, bool AHEAD>
+// This kernel takes rows that start anywhere, element by element.  AHEAD, for
+// rows that 8 warps hold: a row's loads are issued while the row before is
+// worked on, and the weights stay in registers; wider rows have no registers
+// left for either.
+template <int DT, int KT, bool AHEAD>
 __global__ void __launch_bounds__(AHEAD ? 256 : 512, AHEAD && KT * ElemOf<DT>::kBytes <= 4 ? 2 : 1)
     norm_grad_kernel(NormGradArgs a) {
     enter_grid();
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(AHEAD ? 256 : 512, AHEAD && KT * ElemOf<DT>::k
     const int64_t writers = static_cast<int64_t>(gridDim.x) * blockDim.y;
     float2 dw[KT][4], held[AHEAD ? KT : 1][4];
     auto weight = [&](int k, float2 (&w)[4]) {
-        load_weight<DT, VEC>(a.weight, a.weight_f32, (warp + k * warps) * kTileCols, a.cols, lane, w);
+        load_weight<DT, false>(a.weight, a.weight_f32, (warp + k * warps) * kTileCols, a.cols, lane, w);
     };
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
@@ -277,13 +277,13 @@ __global__ void __launch_bounds__(AHEAD ? 256 : 512, AHEAD && KT * ElemOf<DT>::k
         r = a.rstd[row];
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            rdy[k] = load_tile<DT, VEC>(dy, (warp + k * warps) * kTileCols, a.cols, lane);
-            rh[k] = load_tile<DT, VEC>(h, (warp + k * warps) * kTileCols, a.cols, lane);
+            rdy[k] = load_tile<DT, false>(dy, (warp + k * warps) * kTileCols, a.cols, lane);
+            rh[k] = load_tile<DT, false>(h, (warp + k * warps) * kTileCols, a.cols, lane);
         }
         if (a.dh) {
             const void *dh = row_of<DT>(a.dh, row, a.dh_stride);
 #pragma unroll
-            for (int k = 0; k < KT; ++k) rdh[k] = load_tile<DT, VEC>(dh, (warp + k * warps) * kTileCols, a.cols, lane);
+            for (int k = 0; k < KT; ++k) rdh[k] = load_tile<DT, false>(dh, (warp + k * warps) * kTileCols, a.cols, lane);
         }
     };
     int turn = 0;
@@ -334,23 +334,180 @@ __global__ void __launch_bounds__(AHEAD ? 256 : 512, AHEAD && KT * ElemOf<DT>::k
                 if constexpr (AHEAD) w[j] = held[k][j];
                 d[j] = fma2(r2, fma2(minus_c, mul2(n[j], r2), mul2(g[j], w[j])), d[j]);
             }
-            store_tile<DT, VEC>(dx, (warp + k * warps) * kTileCols, a.cols, lane, pack8<DT>(d));
+            store_tile<DT, false>(dx, (warp + k * warps) * kTileCols, a.cols, lane, pack8<DT>(d));
         }
     }
     if (a.dweight == nullptr) return;
     float *out = a.partial + writer * a.cols;
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
-        const int base = (warp + k * warps) * kTileCols, c0 = tile_col<VEC>(base, lane, 0);
-        if (VEC && c0 + 8 <= a.cols && a.cols % 4 == 0) {
-            float4 *p = reinterpret_cast<float4 *>(out + c0);
-            p[0] = make_float4(dw[k][0].x, dw[k][0].y, dw[k][1].x, dw[k][1].y);
-            p[1] = make_float4(dw[k][2].x, dw[k][2].y, dw[k][3].x, dw[k][3].y);
-        } else {
+        const int base = (warp + k * warps) * kTileCols;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int col = tile_col<false>(base, lane, j);
+            if (col < a.cols) out[col] = (j & 1) ? dw[k][j / 2].y : dw[k][j / 2].x;
+        }
+    }
+}
+
+// The same for rows that start at multiples of 8 elements, their loads as
+// asynchronous copies into a ring of `depth` rows in shared memory: rows on
+// their way take no registers, so that an SM has two to four rows of each block
+// in flight whatever their width.  Each thread copies and reads its own elements
+// alone, waits for its own copies and needs no barrier for them.  The bound is
+// memory: 12000 rows of 5056 bf16 take 81 us (floor 72; with the rows ahead held
+// in registers, 156), of 12288 bf16 175 us (174), of 4096 binary32 120 us (116).
+template <int LEFT> __device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
+}
+template <int DT, int KT> __global__ void __launch_bounds__(512, 1) norm_grad_ring_kernel(NormGradArgs a, int depth) {
+    enter_grid();
+    // P pieces of 16 bytes hold a lane's 8 elements: of binary32 the two are 128
+    // columns apart, so that a copy of the warp takes whole sectors
+    constexpr int B = ElemOf<DT>::kBytes, P = B / 2, E = 16 / B;
+    extern __shared__ uint4 ring[];                   // [row][dy, h, dh][tile][piece][thread]
+    __shared__ float part[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int threads = blockDim.x * blockDim.y, slot_size = 3 * KT * P * threads;
+    uint4 *const mine = ring + threadIdx.y * blockDim.x + threadIdx.x;
+    const int64_t writer = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t writers = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    auto col = [&](int k, int piece) { return (warp + k * warps) * kTileCols + piece * 128 + lane * E; };
+    auto place = [&](int slot, int matrix, int k, int piece) {
+        return mine + slot * slot_size + ((matrix * KT + k) * P + piece) * threads;
+    };
+    float2 dw[KT][4], w[KT][4];
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        if constexpr (DT == DT_F32) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int col = tile_col<VEC>(base, lane, j);
-                if (col < a.cols) out[col] = (j & 1) ? dw[k][j / 2].y : dw[k][j / 2].x;
+                const int c = col(k, j / 4) + j % 4;
+                const float v = a.weight == nullptr ? 1.0f : c < a.cols ? static_cast<const float *>(a.weight)[c] : 0.0f;
+                (j & 1 ? w[k][j / 2].y : w[k][j / 2].x) = v;
+            }
+        } else {
+            load_weight<DT, true>(a.weight, a.weight_f32, (warp + k * warps) * kTileCols, a.cols, lane, w[k]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[k][j] = both(0.0f);
+    }
+    // pieces past the row stay zero: nothing is copied there
+    for (int slot = 0; slot < depth; ++slot)
+#pragma unroll
+        for (int matrix = 0; matrix < 3; ++matrix)
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int piece = 0; piece < P; ++piece)
+                    if (col(k, piece) >= a.cols || (matrix == 2 && a.dh == nullptr))
+                        *place(slot, matrix, k, piece) = make_uint4(0u, 0u, 0u, 0u);
+    auto copy = [&](const void *row, int slot, int matrix) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int piece = 0; piece < P; ++piece) {
+                const int c = col(k, piece);
+                if (c < a.cols) {
+                    const int bytes = min(16, (a.cols - c) * B);  // zeros after them
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                                 :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(place(slot, matrix, k, piece)))),
+                                    "l"(static_cast<const char *>(row) + static_cast<int64_t>(c) * B), "r"(bytes) : "memory");
+                }
+            }
+    };
+    auto start = [&](int64_t row, int slot) {
+        if (row < a.rows) {
+            copy(row_of<DT>(a.dy, row, a.dy_stride), slot, 0);
+            copy(row_of<DT>(a.h, row, a.h_stride), slot, 1);
+            if (a.dh) copy(row_of<DT>(a.dh, row, a.dh_stride), slot, 2);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto held = [&](int slot, int matrix, int k, float2 (&f)[4]) {
+        Raw8<DT> r;
+#pragma unroll
+        for (int piece = 0; piece < P; ++piece) {
+            const uint4 v = *place(slot, matrix, k, piece);
+            r.w[piece * 4] = v.x;
+            r.w[piece * 4 + 1] = v.y;
+            r.w[piece * 4 + 2] = v.z;
+            r.w[piece * 4 + 3] = v.w;
+        }
+        unpack8<DT>(r, f);
+    };
+    const float per_col = 1.0f / static_cast<float>(a.cols);
+#pragma unroll 1
+    for (int q = 0; q < depth; ++q) start(writer + q * writers, q);
+    float next_r = writer < a.rows ? a.rstd[writer] : 0.0f;
+    int turn = 0, slot = 0;
+#pragma unroll 1
+    for (int64_t row = writer; row < a.rows; row += writers, turn ^= 1) {
+        if (depth == 2) copies_left<1>();
+        else if (depth == 3) copies_left<2>();
+        else copies_left<3>();
+        const float r = next_r;
+        if (row + writers < a.rows) next_r = a.rstd[row + writers];
+        float2 c2 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            float2 g[4], n[4];
+            held(slot, 0, k, g);
+            held(slot, 1, k, n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                n[j] = mul2(n[j], both(r));
+                dw[k][j] = fma2(g[j], n[j], dw[k][j]);
+                c2 = fma2(mul2(g[j], w[k][j]), n[j], c2);
+            }
+        }
+        const float c = block_sum(c2.x + c2.y, warps, part[turn]) * per_col;
+        const float2 minus_c = both(-c), r2 = both(r);
+        void *dx = row_of<DT>(a.dx, row, a.dx_stride);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            float2 g[4], n[4], d[4];
+            held(slot, 0, k, g);
+            held(slot, 1, k, n);
+            held(slot, 2, k, d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] = fma2(r2, fma2(minus_c, mul2(n[j], r2), mul2(g[j], w[k][j])), d[j]);
+            const Raw8<DT> o = pack8<DT>(d);
+#pragma unroll
+            for (int piece = 0; piece < P; ++piece) {
+                const int c = col(k, piece);
+                typename ElemOf<DT>::type *to = static_cast<typename ElemOf<DT>::type *>(dx) + c;
+                if (c + E <= a.cols) {
+                    Vec<16> v;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v.w[i] = o.w[piece * 4 + i];
+                    st<16>(to, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        if (c + j < a.cols)
+                            to[j] = static_cast<typename ElemOf<DT>::type>(o.w[piece * 4 + j * B / 4] >> (j * B % 4 * 8));
+                }
+            }
+        }
+        start(row + depth * writers, slot);
+        if (++slot == depth) slot = 0;
+    }
+    copies_left<0>();
+    if (a.dweight == nullptr) return;
+    float *out = a.partial + writer * a.cols;
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            const int c = col(k, P == 2 ? j / 2 : 0) + (P == 2 ? 0 : 2 * j);
+            if (c + 4 <= a.cols && a.cols % 4 == 0) {
+                *reinterpret_cast<float4 *>(out + c) = make_float4(dw[k][j].x, dw[k][j].y, dw[k][j + 1].x, dw[k][j + 1].y);
+            } else {
+                const float f[4] = {dw[k][j].x, dw[k][j].y, dw[k][j + 1].x, dw[k][j + 1].y};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < a.cols) out[c + i] = f[i];
             }
         }
     }
@@ -477,6 +634,10 @@ template <int DT> cudaError_t norm_dispatch(bool quant, const NormArgs &a, int s
     return vec ? norm_launch<DT, true, kE4m3>(a, sms, s, info) : norm_launch<DT, false, kE4m3>(a, sms, s, info);
 }
 
+// Of an SM's shared memory.  A row of the 16 warps that an SM holds (512 threads
+// of up to 128 registers) takes up to 96 KiB, so at least two fit.
+constexpr int kRingBytes = 200 * 1024;
+
 template <int DT, bool VEC>
 cudaError_t norm_grad_launch(const NormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
                              int *launches) {
@@ -484,6 +645,8 @@ cudaError_t norm_grad_launch(const NormGradArgs &a, int64_t most_writers, int sm
     constexpr int most = DT == DT_F32 ? 2 : 4;
     int kt = tiles_per_thread(tiles, 8, most);
     const bool ahead = kt != 0;
+    // 12000 rows of 1984 bf16: 41 us with one tile a thread, 37 us with two; of 1000: 25 and 27 us.
+    if (VEC && DT != DT_F32 && kt == 1 && tiles > 6 && a.rows >= 4 * static_cast<int64_t>(sms)) kt = 2;
     if (!ahead) kt = tiles_per_thread(tiles, kGradWarps, most);
     info->vec_bytes = VEC ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
     int64_t writers = 0;
@@ -498,11 +661,24 @@ cudaError_t norm_grad_launch(const NormGradArgs &a, int64_t most_writers, int sm
         const dim3 block(32 * warps, per_block);
         info->grid = static_cast<int>(grid);
         info->block = 32 * warps * per_block;
-        auto kernel = norm_grad_kernel<DT, VEC, 1, true>;
-        if (kt == 2) kernel = ahead ? norm_grad_kernel<DT, VEC, 2, true> : norm_grad_kernel<DT, VEC, 2, false>;
-        if constexpr (most == 4)
-            if (kt == 4) kernel = ahead ? norm_grad_kernel<DT, VEC, 4, true> : norm_grad_kernel<DT, VEC, 4, false>;
-        e = launch_rows(kernel, dim3(grid), block, 0, 1, s, a);
+        if constexpr (VEC) {
+            auto kernel = kt == 1 ? norm_grad_ring_kernel<DT, 1> : norm_grad_ring_kernel<DT, 2>;
+            if constexpr (most == 4)
+                if (kt == 4) kernel = norm_grad_ring_kernel<DT, 4>;
+            const int row_bytes = 3 * kt * info->block * 8 * ElemOf<DT>::kBytes;  // of a row of each of the block's writers
+            const int depth = std::max(2, std::min(4, kRingBytes / (resident * row_bytes)));
+            static std::atomic<uint64_t> allowed[3];
+            e = allow_smem(reinterpret_cast<const void *>(kernel), kRingBytes, &allowed[kt / 2]);
+            if (e != cudaSuccess) return e;
+            info->smem = depth * row_bytes;
+            e = launch_rows(kernel, dim3(grid), block, depth * row_bytes, 1, s, a, depth);
+        } else {
+            auto kernel = norm_grad_kernel<DT, 1, true>;
+            if (kt == 2) kernel = ahead ? norm_grad_kernel<DT, 2, true> : norm_grad_kernel<DT, 2, false>;
+            if constexpr (most == 4)
+                if (kt == 4) kernel = ahead ? norm_grad_kernel<DT, 4, true> : norm_grad_kernel<DT, 4, false>;
+            e = launch_rows(kernel, dim3(grid), block, 0, 1, s, a);
+        }
         ++*launches;
     } else if (a.rows > 0) {
         if (a.dweight) {
