@@ -47,13 +47,16 @@ def nvcc():
     raise RuntimeError("nvcc not found")
 
 
-def _kernel_digest():
-    """SHA-256 over the CUDA sources (kernels and dispatch) and the compiler
-    flags, independent of where the repository sits on disk.  Profiler figures
-    are tied to it."""
+ROW_OPERATORS = ("ew_rows", "ew_embed", "ew_norm", "ew_logits", "ew_distill")  # what their sources' names begin with
+
+
+def _kernel_digest(skip=()):
+    """SHA-256 over the CUDA sources (kernels and dispatch) but for those whose
+    names begin with one of `skip`, and the compiler flags, independent of where
+    the repository sits on disk."""
     h = hashlib.sha256()
     files = [os.path.join(CSRC, name) for name in sorted(os.listdir(CSRC))
-             if name.endswith((".cu", ".cuh", ".h"))]
+             if name.endswith((".cu", ".cuh", ".h")) and not name.startswith(skip)]
     for path in files:
         h.update(os.path.relpath(path, ROOT).encode())
         with open(path, "rb") as f:
@@ -64,8 +67,9 @@ def _kernel_digest():
 
 
 def source_digest():
-    """SHA-256 over the kernel sources and flags (what profiler figures were taken on)."""
-    return _kernel_digest()
+    """SHA-256 over the sources and flags of the elementwise kernels: what the
+    profiler's figures that bench.py reports were taken on."""
+    return _kernel_digest(ROW_OPERATORS)
 
 
 def _torch_dir():
