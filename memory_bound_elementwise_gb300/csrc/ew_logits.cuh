@@ -864,16 +864,22 @@ __global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(Logpr
 
 // ---------------------------------------------------------------- launches
 
-// Blocks a row: one where the rows alone fill the device, up to a cluster of 8
-// where they are few, each with a turn's worth of 2048 elements at least, and no
-// more than fit at a time: clusters of 4 and 8 do not fill every SM of a
-// partition of the device, so a tenth is left.  65536 bf16 columns with the 5
-// best: 134 rows by 4 blocks 11 us, by 8 (two waves) 20 us; 340 rows by 1 block 19
-// us, by 2 23 us; 76 rows by 8, which all but fill the device, 16 us.
+// Blocks a row: one where the rows alone fill the device or have up to 16384
+// elements, up to a cluster of 8 where they are few; each with 4096 elements at
+// least while SMs are idle, and with 16384 after that.  Splitting costs two cluster
+// barriers and the joining of the parts: with the 5 best, 152 rows of 16384 bf16
+// take 5.9 us whole and 8.2 us by 2 blocks, 5 rows of 32768 7.5 us by 8 blocks and
+// 8.3 us by 2.  And no more blocks than fit at a time: clusters of 4 and 8 do not
+// fill every SM of a partition of the device, so a tenth is left.  Of 65536
+// elements, 134 rows by 4 blocks 11 us, by 8 (two waves) 20 us; 340 rows by 1 block
+// 19 us, by 2 23 us; 76 rows by 8, which all but fill the device, 16 us.
 inline int split_shift(int64_t rows, int cols, int sms) {
     const int64_t fit = kResident * static_cast<int64_t>(sms);
     int shift = 0;
-    while (shift < 3 && (rows << (shift + 1)) <= (shift == 0 ? fit : fit * 9 / 10) && (cols >> (shift + 1)) >= 4096) ++shift;
+    if (cols <= 16384) return 0;
+    while (shift < 3 && (rows << (shift + 1)) <= (shift == 0 ? fit : fit * 9 / 10) &&
+           (cols >> (shift + 1)) >= (rows << shift >= sms ? 16384 : 4096))
+        ++shift;
     return shift;
 }
 template <int DT> Split split_of(int cols, int shift) {
