@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) disti
     }
     if (a.k + static_cast<int>(threadIdx.x) < Teacher::padded(a.k)) th.id[a.k + threadIdx.x] = -1;
     Sums v = no_sums();
-    float largest;
-    if constexpr (SUMS) v = warp_sums<32, false>(pass_over<DT, false, false, THREADS>(sh, ax, nullptr, 0, first_turn, largest));
+    float largest, bound;
+    if constexpr (SUMS) v = warp_sums<32, false>(pass_over<DT, false, false, THREADS>(sh, ax, nullptr, 0, first_turn, largest, bound));
     if (lane == 0) part[warp] = v;
     const bool any = __syncthreads_or(mine_counts);
 

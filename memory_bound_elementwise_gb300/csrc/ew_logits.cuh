@@ -332,6 +332,7 @@ constexpr int kManyGroups = 128;    // of two lanes each, for k past kFewGroupsT
 constexpr int kFewGroups = 32;      // of eight
 constexpr int kFewGroupsTop = 24;
 constexpr int kBounds = 4;          // times that a bound is found
+constexpr int kRankedAtOnce = 128;  // candidates that are compared with each other without a bound
 
 struct alignas(8) Candidate {
     float x;
@@ -540,15 +541,16 @@ __device__ __forceinline__ void load_turn(const Share<DT> &sh, int c0, Chunk<DT>
 
 // A thread's sums over the block's share of a row; with TOP, the elements
 // that may be among the k best are in t's list when the block next synchronises.
-// r comes with the first turn loaded; largest is the thread's largest element.
+// r comes with the first turn loaded; largest is the thread's largest element,
+// bound the last one found.
 template <int DT, bool ENTROPY, bool TOP, int THREADS = kThreads>
 __device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShared *t, int k, Chunk<DT> (&r)[kFlight],
-                                          float &largest) {
+                                          float &largest, float &bound) {
     PairSums v = {kLeastExponent, both(0.0f), both(0.0f)};
     const bool single = static_cast<int>(threadIdx.x) < sh.singles;
     const float one = single ? sh.at(sh.single(threadIdx.x)) : kNegInf;
     largest = one;
-    float bound = kNegInf;
+    bound = kNegInf;
     int c0 = sh.first + static_cast<int>(threadIdx.x);
     for (int turn = 0;; ++turn) {
         const float top = add_chunks<DT, ENTROPY>(v, r, a);
@@ -603,16 +605,30 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) logpr
     if (threadIdx.x == 0 && a.logp && block == 0) token = token_at(a.tokens, a.i64, row);
     const bool given = token >= 0 && token < a.cols;
     if (given) chosen = sh.row[token];
-    float largest;
-    Sums v = warp_sums<32, true>(pass_over<DT, true, TOP, THREADS>(sh, ax, t, a.top, r_chunks, largest));
+    float largest, bound;
+    Sums v = warp_sums<32, true>(pass_over<DT, true, TOP, THREADS>(sh, ax, t, a.top, r_chunks, largest, bound));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    float bound = kNegInf;
-    if constexpr (TOP) bound = find_bound<THREADS>(*t, largest, a.top, kBounds - 1);  // with a barrier: every candidate is in the list
+    // After a single turn the bound is of the whole share already, and all candidates reach it.
+    const bool once = sh.end - sh.first <= kFlight * THREADS;
+    if (TOP && !once) bound = find_bound<THREADS>(*t, largest, a.top, kBounds - 1);
     else __syncthreads();
+    // every candidate is in the list now
     v = sums_of_warps<THREADS / 32, true>(part);
     if constexpr (TOP) {
-        if (t->count > kCandidates) exact_top<DT>(*t, sh, a.top, bound);
-        rank_few<THREADS>(*t, bound, a.top);
+        const int n = t->count;
+        bool all_reach = once;
+        if (n > kCandidates) {
+            exact_top<DT>(*t, sh, a.top, bound);
+        } else if (bound == kNegInf && n > kRankedAtOnce) {
+            // fewer groups than k have an element (a short row, or one masked but for a short part): the same
+            // bound over the list, spread over all threads
+            float most = kNegInf;
+            for (int i = threadIdx.x; i < n; i += THREADS) most = fmaxf(most, t->list[i].x);
+            bound = find_bound<THREADS>(*t, most, a.top, 0);
+            all_reach = false;
+        }
+        if (all_reach) rank_list<THREADS>(t->list, t->count, a.top, t->best);
+        else rank_few<THREADS>(*t, bound, a.top);
     }
     if (blocks > 1) {
         if (threadIdx.x == 0) mine = v;
@@ -893,9 +909,10 @@ inline void describe(LaunchInfo *info, int64_t grid) {
 }
 
 template <int DT> cudaError_t logprob_launch(const LogprobArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
-    // Many short rows: blocks of 64 threads, sixteen to an SM.  2000 rows of 1773
-    // bf16 with the 5 best: 11 us, with 256 threads a row 21 us.
-    if (a.rows > 4 * sms && a.cols <= kNarrow * kFlight * Chunk<DT>::kElems && a.top <= kFewGroupsTop) {
+    // Many short rows: blocks of 64 threads, sixteen to an SM.  600 rows of 2000
+    // bf16 with the 5 best: 5.3 us, with 256 threads a row 6.9; 300 rows: the
+    // same; 5 rows: 4.5 and 4.2.
+    if (a.rows > 2 * sms && a.cols <= kNarrow * kFlight * Chunk<DT>::kElems && a.top <= kFewGroupsTop) {
         info->grid = static_cast<int>(a.rows);
         info->block = kNarrow;
         info->vec_bytes = 16;

@@ -83,3 +83,15 @@ def test_distill(dtype, cols, pad, offset, k):
                                                   (200, 16384, 0, 0)])
 def test_norm_grad(dtype, rows, cols, pad, offset):
     norm.test_backward(dtype, rows, cols, pad, offset)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [3, 700])
+@pytest.mark.parametrize("cols,left", [(300, 300), (1000, 1000), (1500, 1500), (2000, 130), (9000, 700), (70000, 1400), (70000, 150)])
+def test_top_where_few_threads_have_an_element(dtype, rows, cols, left):
+    """Short rows, and rows masked but for a short part: more than 128 elements left, in fewer groups of threads than k."""
+    rows = min(rows, 3 if cols > 9000 else rows)
+    x = torch.full((rows, cols), -math.inf, device="cuda", dtype=TORCH[dtype])
+    x[:, cols - left:] = randn((rows, left), 51, TORCH[dtype], 2.0)
+    for top in (20, 24, 64):
+        logits.check_top(ew.ew_logprob(x, None, top=top), x, logits.Want(x, 1.0), top)
