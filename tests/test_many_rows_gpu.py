@@ -1,10 +1,12 @@
-"""Row operators on more rows than the device holds at a time: the block sizes and rings that are chosen then."""
+"""Row operators where another kernel, block size or ring is chosen: more rows than the device holds at a time, the
+sizes on both sides of a choice."""
 import math
 
 import pytest
 import torch
 
 import memory_bound_elementwise_gb300 as ew
+from tests import test_embed_gpu as embed
 from tests import test_logits_gpu as logits
 from tests import test_norm_gpu as norm
 from tests.rows_util import EPS32, TINY, TORCH, UNIT, Guarded, assert_within, randn
@@ -95,3 +97,16 @@ def test_top_where_few_threads_have_an_element(dtype, rows, cols, left):
     x[:, cols - left:] = randn((rows, left), 51, TORCH[dtype], 2.0)
     for top in (20, 24, 64):
         logits.check_top(ew.ew_logprob(x, None, top=top), x, logits.Want(x, 1.0), top)
+
+
+@pytest.mark.parametrize("n", [2, 65, 511, 512, 513, 2049])
+@pytest.mark.parametrize("how", ["uniform", "same", "falling"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embed_grad_on_both_sides_of_the_sorts(n, how, accumulate):
+    embed.grad_case(n, 600, 40, how, "bf16", "f32", accumulate=accumulate)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols,pad,offset", [(1, 0, 0), (7, 0, 0), (1981, 0, 0), (33, 2, 5)])
+def test_zero_rows_that_start_anywhere(dtype, cols, pad, offset):
+    embed.grad_case(3, 5000, cols, "uniform", dtype, dtype, pad, offset)
