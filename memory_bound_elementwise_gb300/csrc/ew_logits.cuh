@@ -582,7 +582,9 @@ __device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShare
 // ---------------------------------------------------------------- log probabilities
 
 // A row to a cluster of `blocks` blocks (one block: no cluster); the first
-// puts the parts together.
+// puts the parts together.  2048 rows of 131072 bf16 with the 5 best take 101 us
+// (5.3 TB/s, floor 79), as much for the instructions as for memory; 5 rows with
+// the 20 best 11 us, all latency (3.3 us without alternatives).
 template <int DT, bool TOP, int THREADS>
 __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) logprob_kernel(LogprobArgs a, Split split) {
     enter_grid();
@@ -786,8 +788,8 @@ template <int DT> __device__ __forceinline__ int bytes_apart(const void *out, co
 // bytes: a lane stores the end of the chunk of the lane before and the start of
 // its own to the aligned 16 bytes that they share, and the first and the last
 // lane the two ends left over, element by element.  Where a warp has fewer
-// chunks it stores elements.  50605 f16 columns, 2 bytes apart, took 200 us with
-// elements alone.
+// chunks it stores elements.  1565 rows of 50605 f16, 2 bytes apart, take 69 us
+// (floor 47); with elements alone 200.
 template <int DT>
 __device__ __forceinline__ void store_chunk(typename ElemOf<DT>::type *to, const Vec<16> &d, int apart, bool whole) {
     constexpr int B = ElemOf<DT>::kBytes;
@@ -849,7 +851,8 @@ __device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, c
     }
 }
 
-// dlogits = scale (dlogp (1_token - p) - dentropy p (log p + H)).
+// dlogits = scale (dlogp (1_token - p) - dentropy p (log p + H)).  The bound is
+// memory: 1500 rows of 50001 f16 take 48 us (6.2 TB/s, floor 44).
 template <int DT, bool ENTROPY>
 __global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(LogprobGradArgs a, Split split) {
     enter_grid();

