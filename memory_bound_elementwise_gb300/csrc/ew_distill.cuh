@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) disti
             v = cluster_sums<false>(&mine, blocks);
             cluster_arrive();  // the wait is further down: mine has been read
         }
-        r = finish_row<DT>(v, logits, a.cols, ax, fpart);
+        r = finish_row<DT, false>(v, logits, a.cols, ax, fpart);
         w = {r.c, r.inv_s, r.top, r.careful};
         if (block == 0 && warp == 0) {
             TeacherSum q;
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(THREADS + Stream<THREADS>::kHelpers, Stream<TH
             if (groups > 4) { copies_left<GRAD ? 1 : 5>(); add_group(4); }
             if (groups > 5) { copies_left<GRAD ? 0 : 5>(); add_group(5); }
 
-            Sums v = warp_sums<32, false>(finished<DT>(pairs, single, one, ax));
+            Sums v = warp_sums<32, false>(finished<DT, false>(pairs, single, one, ax));
             if (lane == 0) part[turn][warp] = v;
             const bool any = __syncthreads_or(0);
             v = row_sums(turn);

@@ -168,24 +168,24 @@ template <int DT> struct Share {
 // ---------------------------------------------------------------- sums
 
 struct Sums {
-    float c, s, u;  // u where the entropy is wanted
+    float c, s, u;  // u where the entropy is wanted, else 0
 };
 __device__ __forceinline__ Sums no_sums() { return {kLeastExponent, 0.0f, 0.0f}; }
 
-__device__ __forceinline__ void move_to(Sums &v, float c) {
+template <bool ENTROPY> __device__ __forceinline__ void move_to(Sums &v, float c) {
     const float d = v.c - c;  // an integer <= 0
     const float f = ex2(d);
-    v.u = f * fmaf(v.s, d, v.u);
+    if (ENTROPY) v.u = f * fmaf(v.s, d, v.u);
     v.s *= f;
     v.c = c;
 }
 // One element.
-__device__ __forceinline__ void add_element(Sums &v, float x, float a) {
+template <bool ENTROPY> __device__ __forceinline__ void add_element(Sums &v, float x, float a) {
     const float c = fmaxf(ceilf(x * a), kLeastExponent);
-    if (c > v.c) move_to(v, c);
+    if (c > v.c) move_to<ENTROPY>(v, c);
     const float t = x < kLeast ? kLeast * a - v.c : fmaf(x, a, -v.c), e = ex2(t);  // NaN stays
     v.s += e;
-    v.u = fmaf(e, t, v.u);
+    if (ENTROPY) v.u = fmaf(e, t, v.u);
 }
 // A thread's chunks; sums in two lanes of a pair each.  Returns the largest element, or NaN.
 struct PairSums {
@@ -229,7 +229,7 @@ template <int LANES, bool ENTROPY> __device__ __forceinline__ Sums warp_sums(Sum
 #pragma unroll
     for (int d = LANES / 2; d > 0; d >>= 1) c = fmaxf(c, __shfl_xor_sync(kAllLanes, c, d));
     if (LANES < 32) c = __shfl_sync(kAllLanes, c, 0);
-    move_to(v, c);
+    move_to<ENTROPY>(v, c);
 #pragma unroll
     for (int d = LANES / 2; d > 0; d >>= 1) {
         v.s += __shfl_xor_sync(kAllLanes, v.s, d);
@@ -304,12 +304,14 @@ template <int DT> __device__ __noinline__ RowSum careful_row(const void *row, in
     return r;
 }
 // A sum that is 0, infinite or NaN says that the shortcuts do not hold for the
-// row: an infinity has c infinite and so a NaN, too.
-template <int DT>
+// row: an infinity has c infinite and so a NaN, too.  The branch holds barriers,
+// so it goes by sums that every thread of the block has the same bits of: u only
+// where warp_sums() added it up.
+template <int DT, bool ENTROPY>
 __device__ __forceinline__ RowSum finish_row(const Sums &v, const void *row, int cols, float a, float *part) {
-    if (v.s > 0.0f && v.s < 1e37f && fabsf(v.u) < 1e37f) {
+    if (v.s > 0.0f && v.s < 1e37f && (!ENTROPY || fabsf(v.u) < 1e37f)) {
         const float inv_s = 1.0f / v.s;
-        return {v.c, logf(v.s), inv_s, v.u * inv_s, 0.0f, false};
+        return {v.c, logf(v.s), inv_s, ENTROPY ? v.u * inv_s : 0.0f, 0.0f, false};
     }
     return careful_row<DT>(row, cols, a, part);
 }
@@ -525,9 +527,10 @@ template <int DT> __device__ __noinline__ void exact_top(TopShared &t, const Sha
 // ---------------------------------------------------------------- the pass over a row
 
 // A thread's sums out of its pairs, and one of the single elements.
-template <int DT> __device__ __forceinline__ Sums finished(const PairSums &v, bool single, float one, float a) {
-    Sums sums = {v.c, v.s.x + v.s.y, v.u.x + v.u.y};
-    if (single) add_element(sums, one, a);
+template <int DT, bool ENTROPY>
+__device__ __forceinline__ Sums finished(const PairSums &v, bool single, float one, float a) {
+    Sums sums = {v.c, v.s.x + v.s.y, ENTROPY ? v.u.x + v.u.y : 0.0f};
+    if (single) add_element<ENTROPY>(sums, one, a);
     return sums;
 }
 
@@ -576,7 +579,7 @@ __device__ __forceinline__ Sums pass_over(const Share<DT> &sh, float a, TopShare
         if (c0 - static_cast<int>(threadIdx.x) >= sh.end) break;
         load_turn<DT, THREADS>(sh, c0, r);
     }
-    return finished<DT>(v, single, one, a);
+    return finished<DT, ENTROPY>(v, single, one, a);
 }
 
 // ---------------------------------------------------------------- log probabilities
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) logpr
         if (block != 0) return;
     }
     if (TOP) __syncthreads();  // best is written
-    const RowSum r = finish_row<DT>(v, logits, a.cols, ax, fpart);
+    const RowSum r = finish_row<DT, true>(v, logits, a.cols, ax, fpart);
     if (threadIdx.x == 0) {
         const bool empty = r.careful && r.top == kNegInf;
         if (a.lse) a.lse[row] = empty ? kNegInf : lse_of(r, a.scale);
