@@ -367,7 +367,10 @@ EW_API ew_status ew_logprob(ew_dtype dtype, ew_index itype, const void *logits, 
  *     dlogits = scale * (dlogp (1_token - p) - dentropy p (log p + entropy))
  * dlogp and dentropy: binary32, one a row, either may be NULL (tokens and
  * entropy are then not read).  Rows without a token have no dlogp term, rows of -inf
- * alone a zero gradient.  dlogits may be logits (the same base and stride). */
+ * alone a zero gradient.  p comes from lse, whose rounding to binary32 makes it off by
+ * up to |lse| 2^-22 of itself; a row whose |lse| is 4096 or more is summed again, to
+ * the same precision as a row near 0.  dlogits may be logits (the same base and
+ * stride). */
 EW_API ew_status ew_logprob_grad(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride,
                                  const void *tokens, const float *lse, const float *entropy, const float *dlogp,
                                  const float *dentropy, float scale, void *dlogits, int64_t dstride, int64_t rows,
@@ -385,7 +388,8 @@ EW_API ew_status ew_logprob_grad(ew_dtype dtype, ew_index itype, const void *log
  * of one row with the same id stay terms of their own in the loss and add up
  * in the gradient.  Masked logits have p = 0; a teacher's
  * entry there makes the loss infinite.
- * ew_distill computes loss and lse, ew_distill_grad dlogits from a given lse,
+ * ew_distill computes loss and lse, ew_distill_grad dlogits from its lse (with the
+ * precision that ew_logprob_grad states),
  * ew_distill_step all of it in one pass over the rows where dloss (binary32,
  * one a row) is known beforehand.  dlogits may be logits (the same base and
  * stride). */

@@ -226,7 +226,15 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) disti
             }
         }
     } else {
-        w = weights_of(a.lse[row], a.scale);
+        // every block of the row decides alike
+        const float lse = a.lse[row];
+        if (!any || lse_holds(lse)) {
+            w = weights_of(lse);
+        } else {
+            const RowSum again = careful_row<DT>(logits, a.cols, ax, fpart);
+            if (blocks > 1) cluster_sync();  // all have read the row before any writes in place
+            w = {0.0f, again.inv_s, again.top, true};
+        }
     }
     if constexpr (GRAD) {
         const RowGrad rg = row_grad(w, any ? a.dloss[row] * a.scale : 0.0f, 0.0f, 0.0f, 0.0f);

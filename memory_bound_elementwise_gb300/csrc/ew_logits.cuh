@@ -700,19 +700,25 @@ __device__ __forceinline__ float p_of(const Weights &w, float x, float a) {
     if (w.careful) return w.weight * ex2(fmaxf((x - w.top) * a, -200.0f));
     return w.weight * ex2(fmaf(fmaxf(x, kLeast), a, -w.c));
 }
-// From a saved lse: c is lse * log2(e) rounded to an integer, weight 2^ of what
-// is left, formed with the two parts of log2(e).
-__device__ __forceinline__ Weights weights_of(float lse, float scale) {
+// A saved lse, rounded to binary32, keeps a row's normalisation to half of its
+// own last place, which at 4096 makes p off by up to 2.4e-4 of itself, at 5e5 by 1.5e-2, and
+// from about 1e7 on the log of the number of elements that share the row is lost.
+// Rows from kMostLse on are summed again (careful_row).
+constexpr float kMostLse = 4096.0f;
+__device__ __forceinline__ bool lse_holds(float lse) { return fabsf(lse) < kMostLse || lse != lse; }
+// From a saved lse that holds: c is lse * log2(e) rounded to an integer, weight 2^ of
+// what is left, formed with the two parts of log2(e).
+__device__ __forceinline__ Weights weights_of(float lse) {
     const float c = rintf(lse * kLog2e);
     const float left = fmaf(lse, kLog2e, -c) + lse * 1.9259629911266175e-8f;
-    if (fabsf(lse) < 1e6f) return {c, ex2(-left), 0.0f, false};
-    return {0.0f, lse == lse ? 1.0f : lse, lse / scale, true};  // huge values; NaN stays NaN
+    if (lse == lse) return {c, ex2(-left), 0.0f, false};
+    return {0.0f, lse, 0.0f, true};  // NaN everywhere
 }
 
 // A row's gradient but for single places: d(x) = p(x) (g - dent (log p(x) + H)).
 // With e = 2^t, t = a x - c, and log p = ln2 t + (ln2 c - lse):
 //     d = e (A + B t),  A = weight (g - dent (H + ln2 c - lse)),  B = -weight dent ln2.
-// Without an entropy term (lse and H 0 there) d = e A.
+// Without an entropy term (lse and H 0 there) d = e A.  Careful: lse is relative to top.
 struct RowGrad {
     Weights w;
     float g, dent, lse, entropy, A, B;
@@ -725,7 +731,7 @@ template <bool ENTROPY> __device__ __forceinline__ float grad_of(const RowGrad &
     if (r.w.careful) {
         const float p = p_of(r.w, x, a);
         if constexpr (!ENTROPY) return p * r.g;
-        const float logp = fmaf(fmaxf(x, kLeast), scale, -r.lse);
+        const float logp = fmaf(x - r.w.top, scale, -r.lse);
         return p * fmaf(-r.dent, p > 0.0f ? logp + r.entropy : 0.0f, r.g);
     }
     const float t = fmaf(fmaxf(x, kLeast), a, -r.w.c);
@@ -854,26 +860,18 @@ __device__ __forceinline__ void write_grad(const Share<DT> &sh, void *out_row, c
     }
 }
 
-// dlogits = scale (dlogp (1_token - p) - dentropy p (log p + H)).  The bound is
-// memory: 1500 rows of 50001 f16 take 48 us (6.2 TB/s, floor 44).
+// The block's share of dlogits = scale (dlogp (1_token - p) - dentropy p (log p + H)).
+// lse: the row's, in careful form relative to its largest element.
 template <int DT, bool ENTROPY>
-__global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(LogprobGradArgs a, Split split) {
-    enter_grid();
-    const int blocks = split.blocks(), block = blockIdx.x & (blocks - 1);
-    const int64_t row = blockIdx.x >> split.shift;
+__device__ __forceinline__ void write_logprob_grad(const LogprobGradArgs &a, const Split split, int64_t row, int block,
+                                                   const Weights &w, float lse, int64_t token) {
     const Share<DT> sh(row_of<DT>(a.logits, row, a.stride), a.cols, block, split);
     void *out = row_of<DT>(a.dlogits, row, a.dstride);
     const float ax = a.scale * kLog2e;
-    int64_t token = a.dlogp ? token_at(a.tokens, a.i64, row) : -1;
     if (token >= a.cols) token = -1;
     const float dlogp = token >= 0 ? a.dlogp[row] : 0.0f;
-    const float lse = a.lse[row];
-    if (lse == kNegInf) {  // nothing depends on the logits of an empty row
-        write_zeros<DT>(out, a.cols, block, split);
-        return;
-    }
-    const RowGrad r = row_grad(weights_of(lse, a.scale), -a.scale * dlogp, ENTROPY ? a.scale * a.dentropy[row] : 0.0f,
-                               ENTROPY ? lse : 0.0f, ENTROPY ? a.entropy[row] : 0.0f);
+    const RowGrad r = row_grad(w, -a.scale * dlogp, ENTROPY ? a.scale * a.dentropy[row] : 0.0f, ENTROPY ? lse : 0.0f,
+                               ENTROPY ? a.entropy[row] : 0.0f);
     const bool here = token >= 0 && sh.holds(static_cast<int>(token));
     const float x = here ? sh.at(static_cast<int>(token)) : 0.0f;  // read before it may be overwritten
     if (here) __syncthreads();                                     // uniform: all threads have the same token
@@ -882,6 +880,36 @@ __global__ void __launch_bounds__(kThreads, kResident) logprob_grad_kernel(Logpr
     __syncthreads();
     if (threadIdx.x == 0)
         store_one<DT>(out, static_cast<int>(token), grad_of<ENTROPY>(r, x, ax, a.scale) + a.scale * dlogp);
+}
+
+// Rows whose lse does not hold.  Out of line, all of it, so that nothing is kept
+// in registers for it.
+template <int DT, bool ENTROPY>
+__device__ __noinline__ void resummed_grad(const LogprobGradArgs &a, Split split, int64_t row, int block, int64_t token,
+                                           float *part) {
+    const RowSum sum = careful_row<DT>(row_of<DT>(a.logits, row, a.stride), a.cols, a.scale * kLog2e, part);
+    // in place: all blocks have read the row before any writes to it
+    if (split.shift > 0 && a.dlogits == a.logits) cluster_sync();
+    if (sum.top == kNegInf) write_zeros<DT>(row_of<DT>(a.dlogits, row, a.dstride), a.cols, block, split);
+    else write_logprob_grad<DT, ENTROPY>(a, split, row, block, {0.0f, sum.inv_s, sum.top, true}, sum.log_s, token);
+}
+
+// The bound is memory: 1500 rows of 50001 f16 take 48 us (6.2 TB/s, floor 44).
+template <int DT, bool ENTROPY>
+__global__ void __launch_bounds__(kThreads, kResident)
+    logprob_grad_kernel(const __grid_constant__ LogprobGradArgs a, Split split) {
+    enter_grid();
+    __shared__ float part[32];
+    const int block = blockIdx.x & (split.blocks() - 1);
+    const int64_t row = blockIdx.x >> split.shift;
+    const int64_t token = a.dlogp ? token_at(a.tokens, a.i64, row) : -1;
+    const float lse = a.lse[row];
+    if (lse == kNegInf && a.scale <= 1.0f)  // an empty row: nothing depends on its logits
+        write_zeros<DT>(row_of<DT>(a.dlogits, row, a.dstride), a.cols, block, split);
+    else if (lse_holds(lse))
+        write_logprob_grad<DT, ENTROPY>(a, split, row, block, weights_of(lse), lse, token);
+    else  // past a scale of 1 the lse of a row of the type's lowest values may be -inf, too
+        resummed_grad<DT, ENTROPY>(a, split, row, block, token, part);
 }
 
 // ---------------------------------------------------------------- launches
@@ -932,14 +960,16 @@ template <int DT> cudaError_t logprob_launch(const LogprobArgs &a, int sms, cuda
     return launch_rows(kernel, dim3(grid), dim3(kThreads), 0, split.blocks(), s, a, split);
 }
 template <int DT> cudaError_t logprob_grad_launch(const LogprobGradArgs &a, cudaStream_t s, LaunchInfo *info) {
-    // no sums: blocks of 16384 to 32768 elements, no cluster
+    // blocks of 16384 to 32768 elements; in place a cluster of up to 8 a row, for the
+    // rows that are summed again before any block writes
+    const bool in_place = a.dlogits == a.logits;
     int shift = 0;
-    while ((a.cols >> (shift + 1)) >= 16384 && a.rows << (shift + 1) <= INT32_MAX) ++shift;
+    while ((a.cols >> (shift + 1)) >= 16384 && a.rows << (shift + 1) <= INT32_MAX && !(in_place && shift == 3)) ++shift;
     const Split split = split_of<DT>(a.cols, shift);
     const int64_t grid = a.rows << shift;
     describe(info, grid);
     auto kernel = a.dentropy ? logprob_grad_kernel<DT, true> : logprob_grad_kernel<DT, false>;
-    return launch_rows(kernel, dim3(grid), dim3(kThreads), 0, 1, s, a, split);
+    return launch_rows(kernel, dim3(grid), dim3(kThreads), 0, in_place ? split.blocks() : 1, s, a, split);
 }
 }  // namespace
 }  // namespace ew

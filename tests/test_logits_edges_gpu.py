@@ -1,9 +1,11 @@
 """Rows of logits at the edges of binary32, through every kernel that a call may take."""
+import math
+
 import pytest
 import torch
 
 import memory_bound_elementwise_gb300 as ew
-from tests.rows_util import EPS32, TORCH, UNIT, assert_within, generator, randn
+from tests.rows_util import EPS32, TINY, TORCH, UNIT, assert_within, generator, randn
 from tests.test_logits_gpu import Want
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +69,111 @@ def test_ordinary_rows_beside_them():
     want = Want(x[rest], 1.0)
     _, lse = ew.ew_distill(x, ids, t)
     assert_within(lse[rest], want.lse, want.bound + 2 * EPS32 * want.lse.abs(), "lse")
+
+
+def far_rows(dtype, cols):
+    """Rows whose lse is far from 0 or has no room for the logarithm of their number, and ordinary ones."""
+    kind = TORCH[dtype]
+    lowest, largest, far = torch.finfo(kind).min, torch.finfo(kind).max, 5e4 if dtype == "f16" else 5e5
+    x = randn((12, cols), 41, kind)
+    x[0] = lowest
+    x[1] = -math.inf
+    x[1, 0], x[1, cols - 1] = lowest, lowest
+    x[2] = largest
+    x[3] = far
+    x[4] = randn((cols,), 42, torch.float32, 3.0) + 6000.0
+    x[5] = randn((cols,), 43) * 8000.0
+    x[6] = randn((cols,), 44, torch.float32, 3.0) + far / 5
+    x[8] = randn((cols,), 45) - 20000.0
+    x[8, ::3] = -math.inf
+    x[9] = -math.inf
+    x[10] = randn((cols,), 46) + 3000.0
+    x[11, cols // 2] = largest / 8
+    return x
+
+
+class FarWant:
+    """A row's softmax in 64 bits, relative to its largest element, and how far p may be off in parts of itself: the
+    exponents up to 100 (beyond, p is below 2^-126) by three roundings, cols / 256 terms a thread and a tree; from a
+    given lse below 4096, four roundings of its size more (lse itself, log2 e, ln 2 and the product)."""
+
+    def __init__(self, x, scale, from_lse):
+        z = x.double() * scale
+        self.empty = torch.isneginf(z).all(1)
+        top = torch.where(self.empty, 0.0, z.amax(1))
+        away = z - top[:, None]
+        log_s = torch.where(self.empty, 0.0, torch.logsumexp(torch.where(self.empty[:, None], 0.0, away), 1))
+        self.logp = torch.where(self.empty[:, None], -math.inf, away - log_s[:, None])
+        self.p = self.logp.exp()
+        self.entropy = torch.special.entr(self.p).sum(1)
+        self.lse = top + log_s
+        spread = torch.where(torch.isfinite(away), -away, 0.0).clamp(max=100.0)
+        self.e = EPS32 * (x.shape[1] / 256 + 64 + 6 * spread.amax(1))
+        self.e_entropy = self.e * (3 + (self.p * spread).sum(1))
+        if from_lse:
+            self.e = self.e + torch.where(self.lse.abs() < 4096 * 1.001, 4 * EPS32 * self.lse.abs(), 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("times,cols", [(1, 100), (1, 4099), (1, 70001), (1, 300000), (30, 70001), (60, 1000)])
+@pytest.mark.parametrize("scale", [1.0, 2.0])
+def test_logprob_gradient_far_from_zero(dtype, times, cols, scale):
+    x = far_rows(dtype, cols).repeat(times, 1)
+    rows = x.shape[0]
+    tokens = torch.randint(0, cols, (rows,), generator=generator(47), device="cuda")
+    tokens[1], tokens[8], tokens[11] = cols - 1, 1, cols // 2
+    a, b = randn((rows,), 48), randn((rows,), 49)
+    f = ew.ew_logprob(x, tokens, scale=scale)
+    want = FarWant(x, scale, True)
+    one = torch.zeros_like(want.p).scatter_(1, tokens[:, None], 1.0)
+    away = torch.where(want.p > 0, want.logp + want.entropy[:, None], 0.0)
+    for dent in (None, b):
+        h = 0.0 if dent is None else b.double()[:, None]
+        d = scale * (a.double()[:, None] * (one - want.p) - h * want.p * away)
+        d = torch.where(want.empty[:, None], 0.0, d)
+        size = scale * want.p * (a.double().abs()[:, None] + abs(h) * (away.abs() + 1))
+        bound = (UNIT[dtype] * d.abs() + want.e[:, None] * size + scale * abs(h) * want.p * want.e_entropy[:, None]
+                 + 4 * EPS32 * scale * a.double().abs()[:, None] * one
+                 + scale * 2.0 ** -125 * (a.double().abs()[:, None] + 100 * abs(h)) + TINY[dtype])
+        got = ew.ew_logprob_grad(x, tokens, f.lse, f.entropy, a, dent, scale=scale)
+        assert_within(got, d, bound, "dlogits")
+        apart = torch.empty(rows * cols + 1, dtype=x.dtype, device="cuda")[1:].view(rows, cols)
+        assert torch.equal(ew.ew_logprob_grad(x, tokens, f.lse, f.entropy, a, dent, scale=scale, dlogits=apart), got)
+        place = x.clone()
+        ew.ew_logprob_grad(place, tokens, f.lse, f.entropy, a, dent, scale=scale, dlogits=place)
+        assert torch.equal(place, got)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("times,cols,k", [(1, 100, 3), (1, 4099, 300), (1, 70001, 3), (1, 70001, 300), (30, 70001, 100),
+                                          (60, 1000, 3)])
+def test_distillation_gradient_far_from_zero(dtype, times, cols, k):
+    """From a given lse, and from the sums of the same call: both within the bounds of the same values."""
+    x = far_rows(dtype, cols).repeat(times, 1)
+    rows, k, scale = x.shape[0], min(k, cols), 0.5
+    ids = (torch.arange(rows, device="cuda")[:, None] + torch.arange(k, device="cuda") * (cols // k)) % cols
+    ids[7, :] = -1
+    t = randn((rows, k), 51)
+    dloss = randn((rows,), 52)
+    q = torch.softmax(t.double() * scale, 1)
+    q[7] = 0.0
+    g = dloss.double()[:, None] * scale
+    e_q = EPS32 * (k + 32 + 4 * t.double().abs().amax(1, keepdim=True))
+    for fused in (False, True):
+        want = FarWant(x, scale, not fused)
+        dense = torch.zeros_like(want.p).scatter_(1, ids.clamp(min=0), q)
+        some = torch.ones_like(q[:, :1])
+        some[7] = 0.0
+        d = g * (want.p * some - dense)
+        bound = (UNIT[dtype] * d.abs() + g.abs() * (want.p * want.e[:, None] + dense * e_q + 2.0 ** -125) + TINY[dtype])
+        place = x.clone()
+        if fused:
+            _, _, got = ew.ew_distill_step(x, ids, t, dloss, scale=scale)
+            ew.ew_distill_step(place, ids, t, dloss, scale=scale, dlogits=place)
+        else:
+            _, lse = ew.ew_distill(x, ids, t, scale=scale)
+            got = ew.ew_distill_grad(x, ids, t, lse, dloss, scale=scale)
+            ew.ew_distill_grad(place, ids, t, lse, dloss, scale=scale, dlogits=place)
+        assert_within(got, d, bound, "step" if fused else "from lse")
+        assert torch.equal(place, got)
+        assert not got[7].any()
