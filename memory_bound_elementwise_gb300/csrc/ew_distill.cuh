@@ -81,7 +81,9 @@ __device__ __forceinline__ TeacherSum teacher_sum(const float *t, int k) {
 // softmax with it.  With e_i = exp(t_i - top) the loss is
 //     sum e_i (t_i - top - log p_i) / sum e_i - log sum e_i,
 // two sums that do not wait for one another: in the rows held in shared memory
-// this is the longest chain between two barriers.
+// this is the longest chain between two barriers.  The first is kept in parts of
+// kLossPart, so that terms near the end of binary32 do not overflow it together.
+constexpr float kLossPart = 1.0f / (2 * kMostTeacher);  // a power of two
 __device__ __forceinline__ float loss_of(const Teacher &th, int k, const RowSum &r, float a, float scale, TeacherSum &q) {
     const bool empty = r.careful && r.top == kNegInf;
     const float top = teacher_top(th.t, k);
@@ -94,11 +96,11 @@ __device__ __forceinline__ float loss_of(const Teacher &th, int k, const RowSum 
             const float w = t == kNegInf ? 0.0f : expf(t - top);
             const float logp = empty ? kNegInf : logp_of(r, x, a, scale);
             sum += w;
-            if (w != 0.0f) loss += w * (t - top - logp);
+            if (w != 0.0f) loss += w * kLossPart * (t - top - logp);
         }
     sum = warp_sum(sum);
     q = {top, logf(sum)};
-    return warp_sum(loss) / sum - q.log_sum;
+    return warp_sum(loss) / sum / kLossPart - q.log_sum;
 }
 // Whether any two entries have the same id: a table of at least 4k ids, open
 // addressing.  Entries of one id add up to one column; a teacher's top values

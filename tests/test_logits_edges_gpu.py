@@ -177,3 +177,15 @@ def test_distillation_gradient_far_from_zero(dtype, times, cols, k):
         assert_within(got, d, bound, "step" if fused else "from lse")
         assert torch.equal(place, got)
         assert not got[7].any()
+
+
+@pytest.mark.parametrize("rows,cols,k", [(2, 100, 100), (3, 5000, 64), (200, 1000, 64), (2, 70001, 1024)])
+def test_loss_of_many_terms_near_the_end_of_binary32(rows, cols, k):
+    """k equal terms of 1.5e38: their weighted mean is finite, their sum is not."""
+    x = torch.zeros(rows, cols, device="cuda")
+    x[:, cols - 1] = 1.5e38
+    ids = torch.arange(k, device="cuda").repeat(rows, 1)
+    ids[ids == cols - 1] = -1
+    loss, _ = ew.ew_distill(x, ids, torch.zeros(rows, k, device="cuda"))
+    want = torch.full((rows,), 1.5e38, dtype=torch.float64, device="cuda")
+    assert_within(loss, want, (k + 40) * EPS32 * want, "loss")
