@@ -189,3 +189,93 @@ def test_loss_of_many_terms_near_the_end_of_binary32(rows, cols, k):
     loss, _ = ew.ew_distill(x, ids, torch.zeros(rows, k, device="cuda"))
     want = torch.full((rows,), 1.5e38, dtype=torch.float64, device="cuda")
     assert_within(loss, want, (k + 40) * EPS32 * want, "loss")
+
+
+# What distill_launch chooses: rows, columns and entries, and the threads of the block that it launches for
+# step and loss (bf16 and f16; f32 at half the columns).  64 and 256: the row is read twice; 160, 320, 640: it is held
+# in shared memory by 128, 256 or 512 streaming threads.
+ROUTES = [(360, 1000, 3, 64), (360, 14000, 300, 64), (12, 100, 3, 256), (12, 4098, 300, 256), (12, 70002, 300, 256),
+          (360, 50002, 300, 256), (360, 14002, 3, 160), (360, 14002, 60, 160), (360, 24002, 100, 320), (12, 10002, 3, 320),
+          (360, 50002, 3, 640), (360, 50002, 250, 640), (12, 70002, 3, 640), (12, 70002, 100, 640), (24, 270000, 64, 640)]
+
+
+def special_rows(dtype, times, cols):
+    lowest, largest = torch.finfo(TORCH[dtype]).min, torch.finfo(TORCH[dtype]).max
+    x = randn((12, cols), 61, TORCH[dtype])
+    x[0] = -math.inf
+    x[1] = lowest
+    x[2] = -math.inf
+    x[2, cols // 2] = 2.5
+    x[3, cols // 3] = math.nan
+    x[4, cols - 1] = math.inf
+    x[5] = lowest
+    x[5, 1], x[5, cols - 2] = 1.0, 2.0
+    x[6] = -math.inf
+    x[6, 0], x[6, cols - 1] = lowest, lowest
+    x[7] = largest
+    x[8, 0] = largest
+    x[10] = -math.inf
+    x[10, 3] = lowest
+    return x.repeat(times, 1)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,cols,k,block", ROUTES)
+def test_distillation_of_special_rows_by_every_kernel(dtype, rows, cols, k, block):
+    cols, scale = cols // 2 if dtype == "f32" else cols, 0.5
+    x = special_rows(dtype, rows // 12, cols)
+    k = min(k, cols)
+    g = generator(62)
+    # among the ids the columns that special rows have left; some rows without a teacher
+    ids = (torch.randint(0, cols, (rows, 1), generator=g, device="cuda") + torch.arange(k, device="cuda") * (cols // k)) % cols
+    ids[2::12], ids[6::12, 1], ids[10::12] = cols // 2, cols - 1, 3  # one id k times in rows 2 and 10
+    ids[9::24] = -1
+    t, dloss = randn((rows, k), 63, TORCH[dtype]), randn((rows,), 64)
+    broken = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    broken[3::12] = broken[4::12] = True
+    want = FarWant(torch.where(broken[:, None], 0.0, x), scale, False)
+    given = (ids >= 0)
+    some = given[:, :1]
+    logq = torch.where(given, torch.log_softmax(t.double() * scale, 1), 0.0)
+    q = torch.where(given, logq.exp(), 0.0)
+    at = ids.clamp(min=0)
+    logp = want.logp.gather(1, at)
+    want_loss = torch.where(q > 0, q * (logq - logp), 0.0).sum(1)
+    e_q = EPS32 * (k + 32 + 4 * t.double().abs().amax(1))
+    size = (q * (logq.abs() + torch.where(torch.isfinite(logp), logp, 0.0).abs())).sum(1)
+    loss_bound = want.e + e_q + (e_q + 8 * EPS32) * size
+    want_lse = torch.where(want.empty, -math.inf, want.lse)
+    lse_bound = want.e + 4 * EPS32 * want.lse.abs()
+    gain = dloss.double()[:, None] * scale
+    dense = torch.zeros_like(want.p).scatter_add_(1, at, q)
+    want_d = gain * (want.p * some - dense)
+    d_bound = (UNIT[dtype] * want_d.abs() + gain.abs() * (want.p * want.e[:, None] + dense * e_q[:, None] + 2.0 ** -125)
+               + TINY[dtype])
+    lse_d_bound = d_bound + gain.abs() * want.p * torch.where(want.lse.abs() < 4100, 4 * EPS32 * want.lse.abs(), 0.0)[:, None]
+    nan = torch.full_like(want_loss, math.nan)
+    want_loss, want_lse = torch.where(broken & some[:, 0], nan, want_loss), torch.where(broken, nan, want_lse)
+    want_d = torch.where((broken & some[:, 0])[:, None], math.nan, want_d)
+
+    place = x.clone()
+    loss, lse, d = ew.ew_distill_step(x, ids, t, dloss, scale=scale)
+    assert ew.last_launch()["block"] == block
+    assert_within(lse, want_lse, lse_bound, "lse")
+    assert_within(loss, want_loss, loss_bound, "loss")
+    assert_within(d, want_d, d_bound, "dlogits")
+    ew.ew_distill_step(place, ids, t, dloss, scale=scale, dlogits=place)
+    assert same_bits(place, d)
+    apart = torch.empty(rows * cols + 1, dtype=x.dtype, device="cuda")[1:].view(rows, cols)
+    ew.ew_distill_step(x, ids, t, dloss, scale=scale, dlogits=apart)
+    assert same_bits(apart, d)
+    loss2, lse2 = ew.ew_distill(x, ids, t, scale=scale)
+    assert ew.last_launch()["block"] == block and same_bits(loss, loss2) and same_bits(lse, lse2)
+    d2 = ew.ew_distill_grad(x, ids, t, lse, dloss, scale=scale)
+    assert_within(d2, want_d, lse_d_bound, "dlogits from lse")
+    place = x.clone()
+    ew.ew_distill_grad(place, ids, t, lse, dloss, scale=scale, dlogits=place)
+    assert same_bits(place, d2)
+
+
+def same_bits(a, b):
+    """Equal, NaN with NaN."""
+    return torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(torch.nan_to_num(a, nan=0.0), torch.nan_to_num(b, nan=0.0))
