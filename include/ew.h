@@ -294,7 +294,8 @@ EW_API ew_status ew_embed(ew_dtype dtype, ew_index itype, const void *table, int
  * written, zeros where no token points.  accumulate 1: the sums are added to
  * what dtable holds, and rows that no token names are not touched.  The tokens
  * are sorted on the device (stable) and each row's terms are added in
- * binary32 in an order that depends on the tokens alone. */
+ * binary32 in an order that depends on the tokens alone.  rows x cols is at most
+ * 2^46. */
 EW_API ew_status ew_embed_grad(ew_dtype dtype, ew_index itype, const void *dout, int64_t dout_stride,
                                const void *tokens, float scale, ew_dtype gtype, void *dtable, int64_t table_rows,
                                int64_t table_stride, int64_t rows, int64_t cols, int accumulate, void *workspace,

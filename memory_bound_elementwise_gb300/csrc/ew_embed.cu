@@ -435,14 +435,15 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(EmbedGradArgs a, uint32_
 // are added by the whole block, each warp every eighth chunk.
 constexpr int kLongRun = 16;
 
-template <int GT, bool VEC> __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a) {
+// Block blockIdx.x takes eight chunks of tile blockIdx.x / strips.
+template <int GT, bool VEC> __global__ void __launch_bounds__(256) embed_join_kernel(EmbedGradArgs a, uint32_t strips) {
     enter_grid();
     __shared__ float2 part[8][4][32];
     __shared__ int64_t reaches[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tile = blockIdx.y, base = tile * kTileCols;
+    const int tile = static_cast<int>(blockIdx.x / strips), base = tile * kTileCols;
     const int size = a.chunk;
-    const int64_t chunk = static_cast<int64_t>(blockIdx.x) * 8 + warp, chunks = (a.rows + size - 1) / size;
+    const int64_t first = static_cast<int64_t>(blockIdx.x % strips) * 8, chunk = first + warp, chunks = (a.rows + size - 1) / size;
     const int64_t last = chunk * size + size - 1;
     const uint32_t nowhere = static_cast<uint32_t>(a.table_rows);
     uint32_t v = nowhere, after = nowhere, ahead = nowhere;
@@ -486,7 +487,7 @@ template <int GT, bool VEC> __global__ void __launch_bounds__(256) embed_join_ke
     for (int w = 0; w < 8; ++w) {
         const int64_t far = reaches[w];
         if (far <= kLongRun) continue;
-        const int64_t from = static_cast<int64_t>(blockIdx.x) * 8 + w;
+        const int64_t from = first + w;
         float2 sum[4] = {};
         if (warp == 0) add(sum, from, 1);
 #pragma unroll 8
@@ -548,7 +549,6 @@ cudaError_t embed_grad_launch(EmbedGradArgs a, int sms, cudaStream_t s, LaunchIn
     const int64_t tiles = (a.cols + kTileCols - 1) / kTileCols, chunks = (a.rows + a.chunk - 1) / a.chunk;
     const int64_t sums = (chunks * tiles + 7) / 8;
     const int64_t fills = a.accumulate ? 0 : (a.table_rows + 31) / 32 - a.blind / 32;
-    if (sums + fills > INT32_MAX || tiles > 65535) return cudaErrorInvalidConfiguration;
     info->vec_bytes = VEC ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
     info->grid = static_cast<int>(sums + fills);
     info->block = 256;
@@ -560,7 +560,8 @@ cudaError_t embed_grad_launch(EmbedGradArgs a, int sms, cudaStream_t s, LaunchIn
     }
     if (e != cudaSuccess || chunks < 2) return e;
     ++*launches;
-    return launch_rows(embed_join_kernel<GT, VEC>, dim3((chunks + 7) / 8, tiles), dim3(256), 0, 1, s, a);
+    const int64_t strips = (chunks + 7) / 8;
+    return launch_rows(embed_join_kernel<GT, VEC>, dim3(strips * tiles), dim3(256), 0, 1, s, a, static_cast<uint32_t>(strips));
 }
 
 template <int DT, int GT>

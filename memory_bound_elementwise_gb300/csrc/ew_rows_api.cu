@@ -130,6 +130,10 @@ ew_status norm_call(ew_dtype dt, const void *x, int64_t x_stride, const void *re
     return EW_OK;
 }
 
+// Elements whose rows the embedding's gradient sorts and adds: blocks of 32 positions
+// by 256 columns, eight of them to a block, stay below 2^31.
+constexpr int64_t kMostSummed = int64_t(1) << 46;
+
 // Workspace of the embedding's gradient, each part at a multiple of 256 bytes.
 struct EmbedWork {
     int64_t items0, items1, keys, order, present, partial, bytes;
@@ -226,6 +230,7 @@ ew_status ew_embed(ew_dtype dt, ew_index itype, const void *table, int64_t table
 
 int64_t ew_embed_grad_workspace(int64_t table_rows, int64_t rows, int64_t cols) {
     if (!size_ok(table_rows, 0) || !size_ok(rows, 0) || !size_ok(cols, 1)) return -1;
+    if (rows > 0 && cols > kMostSummed / rows) return -1;
     return embed_work(table_rows, rows, cols).bytes;
 }
 
