@@ -271,19 +271,21 @@ struct NormCall {
     float eps;
     float *rstd_p;
     Output h, rstd;
-    NormCall(PyObject *const *a, PyObject *h_given, PyObject *rstd_given)
+    // `y_given`: an output that may be x
+    NormCall(PyObject *const *a, PyObject *y_given, PyObject *h_given, PyObject *rstd_given)
         : x(tensor(a[0], "x")), d(device_of(x, "x")), code(code_of(x, "x")), type(x.scalar_type()), m(matrix(x, "x", d)),
           w(weight_of(a[1], m.cols, code, type, d)), eps(static_cast<float>(number(a[3]))) {
         if (a[2] != Py_None) residual = matrix_like(tensor(a[2], "residual"), "residual", m.rows, m.cols, type, d);
-        // without a residual h is x: nothing to write
-        if (a[2] == Py_None && h_given == Py_None) h.give(a[0]);
+        // without a residual h is x: nothing to write, unless y takes its place
+        const bool over = y_given != Py_None && m.p != nullptr && tensor(y_given, "y").data_ptr() == m.p;
+        if (a[2] == Py_None && h_given == Py_None && !over) h.give(a[0]);
         else hm = h.matrix(h_given, "h", x.sizes(), m.rows, m.cols, type, d);
         rstd_p = rstd.floats(rstd_given, "rstd", m.rows, d);
     }
 };
 
 PyObject *rmsnorm(PyObject *const *a) {  // x, weight, residual, eps, y, h, rstd
-    NormCall c(a, a[5], a[6]);
+    NormCall c(a, a[4], a[5], a[6]);
     Output y;
     const Matrix o = y.matrix(a[4], "y", c.x.sizes(), c.m.rows, c.m.cols, c.type, c.d);
     check_status(ew_rmsnorm(c.code, c.m.p, c.m.stride, c.residual.p, c.residual.stride, c.w.type, c.w.p, c.eps, o.p, o.stride,
@@ -293,7 +295,7 @@ PyObject *rmsnorm(PyObject *const *a) {  // x, weight, residual, eps, y, h, rstd
 }
 
 PyObject *rmsnorm_quant(PyObject *const *a) {  // x, weight, residual, eps, group, q, scales, h, rstd, int8
-    NormCall c(a, a[7], a[8]);
+    NormCall c(a, Py_None, a[7], a[8]);
     const int64_t group = integer(a[4]);
     const bool i8 = a[9] == Py_True;
     // a group that the library refuses gets any size here

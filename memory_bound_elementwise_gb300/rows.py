@@ -71,8 +71,9 @@ def ew_rmsnorm(x, weight, residual=None, eps=1e-6, y=None, h=None, rstd=None, st
     """y = h / sqrt(mean(h^2) + eps) * weight with h = x + residual; returns (y, h, rstd).
 
     ``weight`` has x's dtype or float32 (None: ones).  Without a residual h is
-    x.  ``rstd`` (float32, one a row) and ``h`` are what ew_rmsnorm_grad takes.
-    y may be x or residual, h may be x or residual, for in place."""
+    x, or, where y is x, a copy of it.  ``rstd`` (float32, one a row) and ``h`` are
+    what ew_rmsnorm_grad takes.  y may be x or residual, h may be x or residual,
+    for in place."""
     if stream is not None:
         return _on(stream, ew_rmsnorm, x, weight, residual, eps, y, h, rstd)
     return _C.rmsnorm(x, weight, residual, eps, y, h, rstd)

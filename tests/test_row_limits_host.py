@@ -1,7 +1,11 @@
 """Limits of the row operators that need no GPU."""
+import os
+
 import pytest
 
 import memory_bound_elementwise_gb300 as ew
+
+pytestmark = pytest.mark.skipif(not os.path.exists(ew.LIB_PATH), reason="libew.so not built")
 
 MOST = 2 ** 31 - 2 ** 16
 
