@@ -173,11 +173,23 @@ def _declare_rows(L):
 
 def __getattr__(name):
     if name in _ROW_OPERATORS:
-        from . import rows
+        try:
+            from . import rows
+        except (ImportError, OSError, RuntimeError):  # no torch, or nothing built
+            return _raising(name)
         for op in _ROW_OPERATORS:
             globals()[op] = getattr(rows, op)
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))
+
+
+def _raising(name):
+    """Stands for a row operator that cannot be loaded: calling it says why, importing it does not."""
+    def call(*args, **kwargs):
+        from . import rows
+        return getattr(rows, name)(*args, **kwargs)
+    call.__name__ = call.__qualname__ = name
+    return call
 
 
 def status_string(status):
