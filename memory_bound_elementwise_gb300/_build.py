@@ -73,26 +73,34 @@ def source_digest():
 
 
 def _torch_dir():
-    """The installed torch's folder, found without importing it."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch not found")
-    return list(spec.submodule_search_locations)[0]
+    """The installed torch's folder, found without importing it; None where there is none."""
+    try:
+        spec = importlib.util.find_spec("torch")
+    except (ImportError, ValueError):
+        spec = None
+    return list(spec.submodule_search_locations)[0] if spec is not None and spec.submodule_search_locations else None
 
 
-def _inputs_digest():
-    """Build stamp: the kernel sources and flags, the public header, the binding and what it is built for."""
-    h = hashlib.sha256(_kernel_digest().encode())
-    for path in (os.path.join(INCLUDE, "ew.h"), BINDING_SOURCE, os.path.join(_torch_dir(), "version.py")):
+def _digest_of(start, paths):
+    h = hashlib.sha256(start.encode())
+    for path in paths:
         with open(path, "rb") as f:
             h.update(f.read())
-    h.update(sys.version.encode())
     return h.hexdigest()
 
 
-def _build_binding():
+def _inputs_digest():
+    """Build stamp of the library: the kernel sources and flags, and the public header."""
+    return _digest_of(_kernel_digest(), [os.path.join(INCLUDE, "ew.h")])
+
+
+def _binding_digest(torch_dir):
+    """Build stamp of the binding: its source, the header, and what it is built for."""
+    return _digest_of(sys.version, [os.path.join(INCLUDE, "ew.h"), BINDING_SOURCE, os.path.join(torch_dir, "version.py")])
+
+
+def _build_binding(torch_dir):
     """Compiles the torch binding; it is linked against libew.so and the installed torch."""
-    torch_dir = _torch_dir()
     include, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cuda_include = [d for d in [os.path.join(cuda, "include")] +
@@ -120,15 +128,30 @@ def _link_binding(obj, torch_lib):
     os.replace(tmp, BINDING)
 
 
+def _up_to_date(product, stamp, digest):
+    return os.path.exists(product) and os.path.exists(stamp) and open(stamp).read().strip() == digest
+
+
+def _write(path, text):
+    with open(path, "w") as f:
+        f.write(text)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libew.so and the torch binding unless an up-to-date build exists."""
-    stamp = os.path.join(OUT_DIR, "build.sha256")
+    """Compile and link libew.so and the torch binding unless up-to-date builds exist.
+
+    The library needs nvcc alone.  Without torch there is no binding."""
+    stamp, binding_stamp = os.path.join(OUT_DIR, "build.sha256"), os.path.join(OUT_DIR, "binding.sha256")
     digest = _inputs_digest() + ("|" + " ".join(extra_flags) if extra_flags else "")
-    if (not force and os.path.exists(LIB) and os.path.exists(BINDING) and os.path.exists(stamp)
-            and open(stamp).read().strip() == digest):
+    torch_dir = _torch_dir()
+    with_lib = force or not _up_to_date(LIB, stamp, digest)
+    with_binding = torch_dir is not None and (force or not _up_to_date(BINDING, binding_stamp, _binding_digest(torch_dir)))
+    if torch_dir is None:
+        sys.stderr.write("torch not found: the row operators' torch binding is not built\n")
+    if not with_lib and not with_binding:
         return LIB
     os.makedirs(OBJ_DIR, exist_ok=True)
-    exe = nvcc()
+    exe = nvcc() if with_lib else None
 
     def compile_one(src):
         obj = os.path.join(OBJ_DIR, src.replace(".cu", ".o"))
@@ -141,22 +164,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj, r.stdout
 
     with cf.ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_build_binding)  # the longest: first
-        results = list(ex.map(compile_one, SOURCES))
-        binding = binding.result()
-    if verbose:
-        for _, log in results:
-            sys.stdout.write(log)
-    objs = [o for o, _ in results]
-    tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [exe, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-Xlinker", "-soname=libew.so"]
-    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s" % r.stdout)
-    os.replace(tmp, LIB)
-    _link_binding(*binding)
-    with open(stamp, "w") as f:
-        f.write(digest)
+        binding = ex.submit(_build_binding, torch_dir) if with_binding else None  # the longest: first
+        if with_lib:
+            results = list(ex.map(compile_one, SOURCES))
+            if verbose:
+                for _, log in results:
+                    sys.stdout.write(log)
+            tmp = LIB + ".tmp.%d" % os.getpid()
+            cmd = [exe, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-cudart", "static", "-Xlinker", "-soname=libew.so"]
+            r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+            if r.returncode != 0:
+                raise RuntimeError("link failed:\n%s" % r.stdout)
+            os.replace(tmp, LIB)
+            _write(stamp, digest)
+        if with_binding:
+            _link_binding(*binding.result())
+            _write(binding_stamp, _binding_digest(torch_dir))
     return LIB
 
 
