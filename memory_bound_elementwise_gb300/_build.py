@@ -120,8 +120,9 @@ def _build_binding(torch_dir):
 
 def _link_binding(obj, torch_lib):
     tmp = BINDING + ".tmp.%d" % os.getpid()
-    cmd = ["g++", "-shared", "-o", tmp, obj, LIB, "-L", torch_lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
-           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+    # by name: the library has no soname, and by path its place would be written down
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if r.returncode != 0:
         raise RuntimeError("link of the torch binding failed:\n%s" % r.stdout)
@@ -171,7 +172,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 for _, log in results:
                     sys.stdout.write(log)
             tmp = LIB + ".tmp.%d" % os.getpid()
-            cmd = [exe, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-cudart", "static", "-Xlinker", "-soname=libew.so"]
+            cmd = [exe, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-cudart", "static"]
             r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
             if r.returncode != 0:
                 raise RuntimeError("link failed:\n%s" % r.stdout)
