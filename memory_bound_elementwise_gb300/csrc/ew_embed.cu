@@ -319,12 +319,24 @@ template <int GT> __global__ void __launch_bounds__(kSortThreads) embed_sort_few
 
 // ---------------------------------------------------------------- sums
 
-// Sorted positions a warp takes, one to a lane: 32, or 8 where that leaves few
-// warps (a warp takes its positions a few at a time, each time waiting for
-// memory; more chunks cut more runs).  Gradient of 32003 x 1000 binary32 from
-// 5003 tokens: 8 a warp 31 us, 32 a warp 37 us.
+// Sorted positions a warp takes, one to a lane: 32, or 8 where 32 leave fewer than
+// kFewWarps warps, about 13 for each of the device's SMs, and positions are few.  A
+// warp takes its positions some at a time, each time waiting for memory; more chunks
+// cut more runs, which count the more the more positions share a table.  Whole
+// gradients of 32000 rows in us, with 8 and with 32 a warp, and the warps of the latter
+// (of 2000 rows, 40000 x 64 bf16: 45.7 and 42.8):
+//     positions x columns         bf16          binary32      warps
+//     2000 x 64                18.5   23.7     18.2   22.5       63
+//     20000 x 64               26.7   32.3     27.0   30.4      625
+//     40000 x 64               41.6   44.7     42.5   39.3     1250
+//     10000 x 1000             30.5   36.4     41.1   41.7     1252
+//     16384 x 1000             36.0   36.3     50.4   46.7     2048
+//     20000 x 1000             39.9   38.9     56.4   52.6     2500
+//     16384 x 2048             52.6   46.9     88.1   79.2     4096
+// The workspace's size goes by it, so it asks no device.
+constexpr int64_t kFewWarps = 2048, kFewPositions = 32768;
 inline int chunk_of(int64_t rows, int64_t cols) {
-    return rows <= 16384 && (rows + 31) / 32 * ((cols + kTileCols - 1) / kTileCols) < 4096 ? 8 : 32;
+    return rows <= kFewPositions && (rows + 31) / 32 * ((cols + kTileCols - 1) / kTileCols) < kFewWarps ? 8 : 32;
 }
 
 // The table's row of a sum, or what the sum is added to.
@@ -514,6 +526,8 @@ cudaError_t embed_grad_launch(EmbedGradArgs a, int sms, cudaStream_t s, LaunchIn
     const bool few = a.rows <= kFew;
     // Rows to clear meanwhile: what 6 TB/s write in the sort's time, 3 us of few
     // positions, otherwise about 9 us and 0.4 ns a position; whole words of the bitmap.
+    // The blocks beside the sort write 4.2 to 4.5 TB/s and end after it; with the rows
+    // that 4.4 TB/s write, calls took 9 % less to 7 % more time.
     a.chunk = chunk_of(a.rows, a.cols);
     a.blind = 0;
     int64_t clear_blocks = 0;

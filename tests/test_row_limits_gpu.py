@@ -19,3 +19,16 @@ def test_embedding_gradient_of_many_columns(rows, accumulate):
     for v in range(5):
         want = (dout[tokens == v].float().sum(0) + (7.0 if accumulate else 0.0)).half()
         assert torch.equal(got[v], want)
+
+
+@pytest.mark.parametrize("rows,cols", [(20000, 64), (20000, 300), (32768, 40), (32769, 40), (16384, 1024), (16353, 1001)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_gradient_on_both_sides_of_the_chunks_rule(rows, cols, accumulate):
+    """Chunks of 8 and of 32 positions; sums of small integers are exact in binary32."""
+    g = generator(72)
+    tokens = (torch.rand(rows, generator=g, device="cuda") ** 4 * 700).long() - 1  # long runs and short ones, some absent
+    dout = torch.randint(-4, 5, (rows, cols), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    given = torch.full((800, cols), 3.0, device="cuda")
+    got = ew.ew_embed_grad(dout, tokens, 800, dtable=given, scale=0.5, accumulate=accumulate)
+    want = torch.zeros(801, cols, dtype=torch.float64, device="cuda").index_add_(0, tokens % 801, dout.double())[:800] * 0.5
+    assert torch.equal(got.double(), want + (3.0 if accumulate else 0.0))
