@@ -70,8 +70,8 @@
  *              and saxpy_relu with x == y, relu, copy).  Any other overlap of an output's byte
  *              range with an input's is EW_ERR_OVERLAP.  ew_gather_stride
  *              accepts no overlap at all.
- *   Streams    every call enqueues at most one kernel on `stream` (NULL = the
- *              legacy default stream) on the calling thread's current device and
+ *   Streams    every call enqueues at most one kernel (row operators: at most
+ *              three) on `stream` (NULL = the legacy default stream) on the calling thread's current device and
  *              returns without synchronising.  Kernels are launched with
  *              programmatic dependent launch unless ew_set_programmatic_launch(0)
  *              (see there).  Device faults surface at the caller's next
@@ -307,7 +307,8 @@ EW_API int64_t ew_embed_grad_workspace(int64_t table_rows, int64_t rows, int64_t
  *     h = x + residual,  rstd = 1 / sqrt(mean(h^2) + eps),  y = h * rstd * weight
  * residual may be NULL (h = x).  weight: cols elements of type wtype (dtype or
  * EW_F32), or NULL for ones.  h_out (dtype) and rstd_out (binary32, rows) may
- * be NULL where they are not wanted; the backward call needs both.   The norm is
+ * be NULL where they are not wanted; the backward call needs both (h is x where there
+ * is no residual, unless y has taken its place).  The norm is
  * taken of the binary32 sum; only what is stored in h_out is rounded.  y may be
  * x or residual, and h_out may be x or residual (the same base and stride),
  * but y is not h_out.  eps >= 0.  NaN and infinity go through the formula: a
@@ -461,7 +462,8 @@ EW_API ew_status ew_plan_query(ew_dtype dtype, const void *const *ptrs, int32_t 
 
 /* What the most recent operator call on this thread launched. */
 typedef struct {
-    int32_t launches;  /* kernels enqueued by the call (0 or 1) */
+    int32_t launches;  /* kernels enqueued by the call (0 or 1; row operators 0 to 3, of which
+                          what follows describes the largest) */
     int32_t path;      /* ew_path that ran */
     int32_t vec_bytes;
     int32_t grid;      /* blocks */

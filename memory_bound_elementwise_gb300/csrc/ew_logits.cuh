@@ -707,7 +707,8 @@ __device__ __forceinline__ float p_of(const Weights &w, float x, float a) {
 constexpr float kMostLse = 4096.0f;
 __device__ __forceinline__ bool lse_holds(float lse) { return fabsf(lse) < kMostLse || lse != lse; }
 // From a saved lse that holds: c is lse * log2(e) rounded to an integer, weight 2^ of
-// what is left, formed with the two parts of log2(e).
+// what is left, formed with the two parts of log2(e) (Cody and Waite's reduction: a
+// constant as the binary32 next to it and what that leaves).
 __device__ __forceinline__ Weights weights_of(float lse) {
     const float c = rintf(lse * kLog2e);
     const float left = fmaf(lse, kLog2e, -c) + lse * 1.9259629911266175e-8f;
@@ -724,7 +725,7 @@ struct RowGrad {
     float g, dent, lse, entropy, A, B;
 };
 __device__ __forceinline__ RowGrad row_grad(const Weights &w, float g, float dent, float lse, float entropy) {
-    const float offset = fmaf(w.c, kLn2, w.c * -1.9046543e-9f) - lse;  // ln2 in two parts
+    const float offset = fmaf(w.c, kLn2, w.c * -1.9046543e-9f) - lse;  // ln2 in two parts, after Cody and Waite
     return {w, g, dent, lse, entropy, w.weight * fmaf(-dent, entropy + offset, g), w.weight * -dent * kLn2};
 }
 template <bool ENTROPY> __device__ __forceinline__ float grad_of(const RowGrad &r, float x, float a, float scale) {
@@ -943,7 +944,8 @@ inline void describe(LaunchInfo *info, int64_t grid) {
 }
 
 template <int DT> cudaError_t logprob_launch(const LogprobArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
-    // Many short rows: blocks of 64 threads, sixteen to an SM.  600 rows of 2000
+    // Many short rows: blocks of 64 threads, sixteen to an SM, or ten with
+    // alternatives, whose lists take 21 KiB of shared memory each.  600 rows of 2000
     // bf16 with the 5 best: 5.3 us, with 256 threads a row 6.9; 300 rows: the
     // same; 5 rows: 4.5 and 4.2.
     if (a.rows > 2 * sms && a.cols <= kNarrow * kFlight * Chunk<DT>::kElems && a.top <= kFewGroupsTop) {

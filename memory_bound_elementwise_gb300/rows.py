@@ -7,6 +7,11 @@ on ``stream`` (default: torch's current stream) and do not synchronise.  What is
 allocated belongs to that stream.  Arguments that do not fit raise ``ValueError``
 or ``TypeError``, and ``EwError`` carries the library's status.
 
+Gradients are calls of their own (``ew_*_grad``, ``ew_distill_step``): autograd does
+not see these functions.  Results require no gradient whatever the inputs do, and
+writing to a given output leaves its version counter as it is.  To use them in a
+graph, wrap forward and backward calls in a ``torch.autograd.Function``.
+
 The checks, allocations and calls are in the compiled binding
 (csrc/ew_torch.cpp), built beside libew.so.
 """
@@ -122,7 +127,8 @@ def ew_logprob(logits, tokens, top=0, scale=1.0, stream=None):
 
 def ew_logprob_grad(logits, tokens, lse, entropy, dlogp, dentropy=None, scale=1.0, dlogits=None, stream=None):
     """Gradient with respect to the logits of ew_logprob's logp (times dlogp) and entropy (times dentropy); returns
-    dlogits, which may be logits.  dlogp or dentropy may be None."""
+    dlogits, which may be logits.  dlogp or dentropy may be None.  Rows whose lse is 4096 or more in size are
+    summed again, as float32 does not hold their normalisation."""
     if stream is not None:
         return _on(stream, ew_logprob_grad, logits, tokens, lse, entropy, dlogp, dentropy, scale, dlogits)
     return _C.logprob_grad(logits, tokens, lse, entropy, dlogp, dentropy, scale, dlogits)
