@@ -541,7 +541,6 @@ cudaError_t embed_grad_launch(EmbedGradArgs a, int sms, cudaStream_t s, LaunchIn
         clear_blocks = (clear_blocks + kSortBlocks - 1) / kSortBlocks * kSortBlocks;
     }
     cudaError_t e = cudaSuccess;
-    info->smem = 0;
     if (few) {
         e = launch_rows(embed_sort_few_kernel<GT>, dim3(1 + clear_blocks), dim3(kSortThreads), 0, 1, s, a);
     } else {
@@ -555,7 +554,6 @@ cudaError_t embed_grad_launch(EmbedGradArgs a, int sms, cudaStream_t s, LaunchIn
         e = allow_smem(reinterpret_cast<const void *>(sort), (kSortWarps * 4) << kDigitBits, &allowed);
         if (e != cudaSuccess) return e;
         e = launch_rows(sort, dim3(kSortBlocks + clear_blocks), dim3(kSortThreads), smem, kSortBlocks, s, a, passes, bits);
-        info->smem = static_cast<int>(smem);
     }
     if (e != cudaSuccess) return e;
     ++*launches;

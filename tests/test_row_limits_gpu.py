@@ -32,3 +32,12 @@ def test_embedding_gradient_on_both_sides_of_the_chunks_rule(rows, cols, accumul
     got = ew.ew_embed_grad(dout, tokens, 800, dtable=given, scale=0.5, accumulate=accumulate)
     want = torch.zeros(801, cols, dtype=torch.float64, device="cuda").index_add_(0, tokens % 801, dout.double())[:800] * 0.5
     assert torch.equal(got.double(), want + (3.0 if accumulate else 0.0))
+
+
+@pytest.mark.parametrize("rows,launches", [(0, 2), (5, 2), (2000, 3)])
+def test_launch_record_of_the_embedding_gradient(rows, launches):
+    """The record's grid, block and shared memory are of one kernel, the sums' (which also clears the last, partial
+    word of 32 rows)."""
+    ew.ew_embed_grad(torch.zeros(rows, 64, device="cuda"), torch.zeros(rows, dtype=torch.int32, device="cuda"), 500)
+    r = ew.last_launch()
+    assert (r["launches"], r["block"], r["smem"]) == (launches, 256, 0)
