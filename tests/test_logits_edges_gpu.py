@@ -279,3 +279,22 @@ def test_distillation_of_special_rows_by_every_kernel(dtype, rows, cols, k, bloc
 def same_bits(a, b):
     """Equal, NaN with NaN."""
     return torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(torch.nan_to_num(a, nan=0.0), torch.nan_to_num(b, nan=0.0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("times,cols", [(1, 100), (1, 4099), (1, 70001), (30, 1000), (30, 40001)])
+@pytest.mark.parametrize("top", [20, 25, 64])
+def test_alternatives_of_special_rows(dtype, times, cols, top):
+    """Ties, few elements, NaN and infinities, with the bounds of few and of many groups."""
+    x = special_rows(dtype, times, cols)
+    got = ew.ew_logprob(x, None, top=top, scale=0.5)
+    broken = torch.isnan(x).any(1) | torch.isposinf(x).any(1)
+    clean = torch.where(broken[:, None], 0.0, x.double())
+    best, ids = torch.sort(clean, dim=1, descending=True, stable=True)
+    best, ids = best[:, :top], ids[:, :top]
+    missing = torch.isneginf(best) | broken[:, None]
+    assert torch.equal(got.top_ids.long(), torch.where(missing, -1, ids))
+    want = FarWant(clean, 0.5, False)
+    logp = torch.where(torch.isneginf(best), -math.inf, want.logp.gather(1, ids))
+    size = torch.where(torch.isfinite(logp), logp.abs(), 0.0)
+    assert_within(got.top_logp, torch.where(broken[:, None], math.nan, logp), want.e[:, None] + 6 * EPS32 * size, "top")
