@@ -389,7 +389,7 @@ EW_API ew_status ew_logprob_grad(ew_dtype dtype, ew_index itype, const void *log
  * of -inf do not count; a row without any has loss 0 and gradient 0.  Entries
  * of one row with the same id stay terms of their own in the loss and add up
  * in the gradient.  Masked logits have p = 0; a teacher's
- * entry there makes the loss infinite.
+ * entry there makes the loss infinite, as does one whose log p is past binary32.
  * ew_distill computes loss and lse, ew_distill_grad dlogits from its lse (with the
  * precision that ew_logprob_grad states),
  * ew_distill_step all of it in one pass over the rows where dloss (binary32,
