@@ -30,6 +30,7 @@
  *   ew_embed          out[t,:] = scale * table[tokens[t],:], and ew_embed_grad
  *   ew_rmsnorm        root-mean-square norm with the residual's addition,
  *                     ew_rmsnorm_quant (8-bit output with scales), ew_rmsnorm_grad
+ *   ew_layernorm      layer norm with the residual's addition, and ew_layernorm_grad
  *   ew_logprob        log probabilities of given tokens, entropy and top
  *                     alternatives, and ew_logprob_grad
  *   ew_distill        distillation from a teacher's top logits: ew_distill,
@@ -347,6 +348,40 @@ EW_API ew_status ew_rmsnorm_grad(ew_dtype dtype, const void *dy, int64_t dy_stri
                                  ew_stream_t stream);
 /* Bytes of workspace (-1: sizes out of range); 0 columns of dweight need none. */
 EW_API int64_t ew_rmsnorm_grad_workspace(int64_t rows, int64_t cols);
+
+/* Layer norm with the residual's addition:
+ *     h = x + residual,  mean = mean(h),  rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ *     y = (h - mean) * rstd * weight + bias
+ * residual may be NULL (h = x).  weight and bias: cols elements of type wtype
+ * (dtype or EW_F32) each, NULL for ones and for zeros.  h_out (dtype), mean_out and
+ * rstd_out (binary32, rows) may be NULL where they are not wanted; the backward call
+ * needs all three (h is x where there is no residual, unless y has taken its place).
+ * The norm is taken of the binary32 sum; only what is stored in h_out is rounded.
+ * y is formed from differences to the row's first element, so a mean far from zero
+ * costs it nothing; mean_out is rounded.  y may be x or residual, and h_out may be x
+ * or residual (the same base and stride), but y is not h_out.  eps >= 0.  A NaN or
+ * an infinity makes y's whole row and rstd NaN.  Where the variance is past binary32
+ * rstd is 0; where it and eps are 0 rstd is infinite and y NaN. */
+EW_API ew_status ew_layernorm(ew_dtype dtype, const void *x, int64_t x_stride, const void *residual,
+                              int64_t residual_stride, ew_dtype wtype, const void *weight, const void *bias, float eps,
+                              void *y, int64_t y_stride, void *h_out, int64_t h_stride, float *mean_out,
+                              float *rstd_out, int64_t rows, int64_t cols, ew_stream_t stream);
+
+/* Backward of ew_layernorm, from the h, mean and rstd that it wrote:
+ *     n = (h - mean) * rstd,  g = dy * weight
+ *     dx = rstd * (g - mean(g) - n * mean(g * n)) + dh    (also the residual's gradient)
+ *     dweight = sum over rows of dy * n,  dbias = sum over rows of dy    (binary32)
+ * dh, the gradient that reaches h by the residual stream, may be NULL.  weight may be
+ * NULL (ones).  dweight and dbias may each be NULL; where both are, no workspace is
+ * needed.  dx may be dy or dh (the same base and stride).  rows == 0 writes zeros to
+ * dweight and dbias. */
+EW_API ew_status ew_layernorm_grad(ew_dtype dtype, const void *dy, int64_t dy_stride, const void *h, int64_t h_stride,
+                                   ew_dtype wtype, const void *weight, const float *mean, const float *rstd,
+                                   const void *dh, int64_t dh_stride, void *dx, int64_t dx_stride, float *dweight,
+                                   float *dbias, int64_t rows, int64_t cols, void *workspace, int64_t workspace_bytes,
+                                   ew_stream_t stream);
+/* Bytes of workspace (-1: sizes out of range). */
+EW_API int64_t ew_layernorm_grad_workspace(int64_t rows, int64_t cols);
 
 /* Log probabilities of given tokens, with entropy and top alternatives.  Per row,
  * with p = softmax(scale * logits):

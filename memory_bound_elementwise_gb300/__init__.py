@@ -22,6 +22,8 @@ Row operators (matrices, one row at a time; ``rows.py``)::
     ew_rmsnorm(x, w, residual)      (y, h, rstd): h = x + residual, y = h / rms(h) * w
     ew_rmsnorm_quant(...)           (q, scales, h, rstd): the same with an 8-bit output
     ew_rmsnorm_grad(dy, h, w, rstd) (dx, dweight)
+    ew_layernorm(x, w, b, residual) (y, h, mean, rstd): h = x + residual, y = (h - mean) * rstd * w + b
+    ew_layernorm_grad(dy, h, w, mean, rstd) (dx, dweight, dbias)
     ew_logprob(logits, tokens, top) log probabilities, entropy, lse and top alternatives
     ew_logprob_grad(...)            their gradient
     ew_distill(logits, ids, teacher)(loss, lse); ew_distill_grad, ew_distill_step
@@ -62,11 +64,12 @@ EXPORTS = ("ew_add", "ew_saxpy", "ew_relu", "ew_add_relu", "ew_saxpy_relu", "ew_
            "ew_plan_query", "ew_last_launch", "ew_gather_plan_query", "ew_status_string", "ew_last_cuda_error",
            "ew_device_error", "ew_selftest_bounded_wait", "ew_version",
            "ew_embed", "ew_embed_grad", "ew_embed_grad_workspace", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad", "ew_rmsnorm_grad_workspace",
+           "ew_layernorm", "ew_layernorm_grad", "ew_layernorm_grad_workspace",
            "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
 
 # Row operators (rows.py), loaded with torch at their first use.
 _ROW_OPERATORS = ("ew_embed", "ew_embed_grad", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad",
-                  "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
+                  "ew_layernorm", "ew_layernorm_grad", "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
 # Their C arguments: i enum, l int64, f float, p pointer.
 _ROW_SIGNATURES = {
     "ew_embed": "iipllpfplllp",
@@ -76,6 +79,9 @@ _ROW_SIGNATURES = {
     "ew_rmsnorm_quant": "iplplipfilplplplpllp",
     "ew_rmsnorm_grad": "iplplippplplpllplp",
     "ew_rmsnorm_grad_workspace": "ll",
+    "ew_layernorm": "iplplippfplplppllp",
+    "ew_layernorm_grad": "iplplipppplplppllplp",
+    "ew_layernorm_grad_workspace": "ll",
     "ew_logprob": "iiplpflpppppllp",
     "ew_logprob_grad": "iiplpppppfplllp",
     "ew_distill": "iiplplipllfppllp",

@@ -300,10 +300,6 @@ template <int T> struct Stream {  // T streaming threads
     static constexpr int kMostSmem = kRing * kGroupChunks * 16 + 3 * kMostEntries * 12 + 2 * 4 * kMostEntries * 4;
 };
 
-template <int LEFT> __device__ __forceinline__ void copies_left() {
-    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
-}
-
 template <int DT, bool GRAD, int THREADS>
 __global__ void __launch_bounds__(THREADS + Stream<THREADS>::kHelpers, Stream<THREADS>::kBlocks)
     distill_stream_kernel(DistillArgs a, Split split, int groups) {

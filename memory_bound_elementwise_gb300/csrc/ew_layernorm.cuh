@@ -1,0 +1,569 @@
+// ew_layernorm.cuh -- layer norm with the residual's addition, and its backward.
+// Compiled once per element type.
+//
+//   h = x + residual,  m = mean(h),  r = 1 / sqrt(mean((h - m)^2) + eps),  y = (h - m) r w + b
+//
+// Both directions move their matrices once and are bounded by memory.  Rows may
+// start anywhere: where all matrices of a call have their rows at the same place
+// between multiples of 8 elements, a row is taken in runs of 8 that start at such
+// a multiple, `past` elements before the row, and the runs at its two ends are
+// moved element by element (RUNS).  Other matrices are moved an element at a time.
+//
+// The mean of a row far from zero is subtracted in two steps: first the row's
+// first element, an exact difference where the row's elements are within a factor
+// of two of each other, then the mean of what is left.  So y does not lose what
+// the rounding of m to binary32 would cost it.
+#pragma once
+
+#include <algorithm>
+
+#include "ew_rows.cuh"
+#include "ew_rows.h"
+
+namespace ew {
+namespace {
+
+// ---------------------------------------------------------------- runs of 8 elements
+
+// Elements of a row's first run that lie before the row.
+template <int DT> __host__ __device__ __forceinline__ int past_of(const void *row) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(row) % (8 * ElemOf<DT>::kBytes)) / ElemOf<DT>::kBytes;
+}
+// Column of element j of this lane in tile `tile` of a row.
+template <bool RUNS> __device__ __forceinline__ int col_of(int tile, int past, int lane, int j) {
+    return RUNS ? tile * kTileCols - past + lane * 8 + j : tile * kTileCols + j * 32 + lane;
+}
+// The lane's 8 elements; columns outside the row are zero.
+template <int DT, bool RUNS> __device__ __forceinline__ Raw8<DT> load_run(const void *row, int tile, int past, int cols, int lane) {
+    if constexpr (!RUNS) {
+        return load_tile<DT, false>(row, tile * kTileCols, cols, lane);
+    } else {
+        using T = typename ElemOf<DT>::type;
+        const T *p = static_cast<const T *>(row);
+        const int c0 = col_of<true>(tile, past, lane, 0);
+        Raw8<DT> r;
+        if (c0 >= 0 && c0 + 8 <= cols) {
+            const Vec<8 * ElemOf<DT>::kBytes> v = ld<8 * ElemOf<DT>::kBytes>(p + c0);
+#pragma unroll
+            for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = v.w[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j >= 0 && c0 + j < cols) {
+                    if constexpr (DT == DT_F32) r.w[j] = ld<4>(p + c0 + j).w[0];
+                    else r.w[j / 2] |= static_cast<uint32_t>(ld<2>(p + c0 + j).h) << (16 * (j & 1));
+                }
+        }
+        return r;
+    }
+}
+template <int DT, bool RUNS>
+__device__ __forceinline__ void store_run(void *row, int tile, int past, int cols, int lane, const Raw8<DT> &r) {
+    if constexpr (!RUNS) {
+        store_tile<DT, false>(row, tile * kTileCols, cols, lane, r);
+    } else {
+        using T = typename ElemOf<DT>::type;
+        T *p = static_cast<T *>(row);
+        const int c0 = col_of<true>(tile, past, lane, 0);
+        if (c0 >= 0 && c0 + 8 <= cols) {
+            Vec<8 * ElemOf<DT>::kBytes> v;
+#pragma unroll
+            for (int k = 0; k < ElemOf<DT>::kWords; ++k) v.w[k] = r.w[k];
+            st<8 * ElemOf<DT>::kBytes>(p + c0, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j >= 0 && c0 + j < cols) p[c0 + j] = static_cast<T>(r.w[j * ElemOf<DT>::kBytes / 4] >> (j * ElemOf<DT>::kBytes % 4 * 8));
+        }
+    }
+}
+// The columns of a vector, in binary32; null stands for `other`, columns
+// outside for zero.  A run of it starts anywhere: it is cut out of the 16-byte
+// pieces around it, which lie within the vector but at its ends.
+template <int DT, bool RUNS>
+__device__ __forceinline__ void load_columns(const void *w, bool f32, float other, int tile, int past, int cols, int lane,
+                                             float2 (&f)[4]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = both(other);
+        return;
+    }
+    const bool wide = DT == DT_F32 || f32;
+    const int c0 = col_of<RUNS>(tile, past, lane, 0);
+    const char *at = static_cast<const char *>(w) + static_cast<int64_t>(c0) * (wide ? 4 : 2);
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);  // the same for all lanes of a run
+    const int room = shift == 0 ? 0 : 8;
+    if (RUNS && c0 >= room && c0 + 8 + room <= cols) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(at - shift);
+        const uint4 a = q[0];
+        uint4 b = make_uint4(0u, 0u, 0u, 0u), c = b;
+        if (wide || shift) b = q[1];
+        if (wide && shift) c = q[2];
+        uint32_t v[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+        if (shift & 8) {
+#pragma unroll
+            for (int j = 0; j < 10; ++j) v[j] = v[j + 2];
+        }
+        if (shift & 4) {
+#pragma unroll
+            for (int j = 0; j < 9; ++j) v[j] = v[j + 1];
+        }
+        if (wide) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+        } else if constexpr (DT != DT_F32) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = widen<DT>(__funnelshift_r(v[j], v[j + 1], (shift & 3) * 8));
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int col = col_of<RUNS>(tile, past, lane, j);
+        float e = 0.0f;
+        if (col >= 0 && col < cols) {
+            if (wide) e = static_cast<const float *>(w)[col];
+            else e = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(w)[col]);
+        }
+        (j & 1 ? f[j / 2].y : f[j / 2].x) = e;
+    }
+}
+// Zeros in columns outside the row.
+template <bool RUNS> __device__ __forceinline__ void clip_columns(int tile, int past, int cols, int lane, float2 (&f)[4]) {
+    const int first = tile * kTileCols - (RUNS ? past : 0);
+    if (first >= 0 && first + kTileCols <= cols) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int a = col_of<RUNS>(tile, past, lane, 2 * j), b = col_of<RUNS>(tile, past, lane, 2 * j + 1);
+        if (a < 0 || a >= cols) f[j].x = 0.0f;
+        if (b < 0 || b >= cols) f[j].y = 0.0f;
+    }
+}
+// Columns of the row in tile `tile`.
+__device__ __forceinline__ int columns_in(int tile, int past, int cols) {
+    const int first = max(tile * kTileCols - past, 0), end = min(static_cast<int64_t>(tile + 1) * kTileCols - past, static_cast<int64_t>(cols));
+    return max(end - first, 0);
+}
+
+// Two sums over a block of `warps` warps at once; `part` as in block_sum.
+__device__ __forceinline__ float2 warp_sum2(float2 v) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        v = add2(v, make_float2(__shfl_xor_sync(kAllLanes, v.x, d), __shfl_xor_sync(kAllLanes, v.y, d)));
+    return v;
+}
+__device__ __forceinline__ float2 block_sum2(float2 v, int warps, float2 *part) {
+    v = warp_sum2(v);
+    if (warps == 1) return v;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) part[warp] = v;
+    __syncthreads();
+    return warp_sum2(lane < warps ? part[lane] : both(0.0f));
+}
+
+// ---------------------------------------------------------------- forward
+
+// One row to a block of `warps` warps, tile t of the row to warp t mod warps;
+// with one warp a row, blockDim.y rows to a block.  HELD: the warps x KT tiles
+// cover the row, which stays in registers.  Each warp takes the mean of its own
+// columns and the squares around that; the parts are joined by
+//     sum (v - m)^2 = sum over warps of (squares + n (mean - m)^2),
+// so that both statistics cost one barrier and no cancellation.  Otherwise the
+// passes read the row again.  Nothing is written before all threads have read
+// the row's first element: h and y may take x's place.
+template <int DT, bool RUNS, int KT, bool HELD>
+__global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && RUNS && KT * ElemOf<DT>::kBytes <= 8 ? 2 : 1)
+    layernorm_kernel(LayerNormArgs a) {
+    enter_grid();
+    __shared__ float2 part[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (row >= a.rows) return;  // whole warps: blockDim.y > 1 only with one warp a row
+    const void *x = row_of<DT>(a.x, row, a.x_stride);
+    const void *res = a.residual ? row_of<DT>(a.residual, row, a.residual_stride) : nullptr;
+    void *h = a.h ? row_of<DT>(a.h, row, a.h_stride) : nullptr;
+    void *out = row_of<DT>(a.y, row, a.y_stride);
+    const int past = RUNS ? past_of<DT>(x) : 0;
+    const float per_col = a.per_col;
+    auto first_of = [](const void *p) {
+        if constexpr (DT == DT_F32) return __uint_as_float(ld<4>(p).w[0]);
+        else return elem_to_f32<DT>(ld<2>(p).h);
+    };
+    auto sum_of = [&](int tile, float2 (&f)[4]) {
+        unpack8<DT>(load_run<DT, RUNS>(x, tile, past, a.cols, lane), f);
+        if (res) {
+            float2 g[4];
+            unpack8<DT>(load_run<DT, RUNS>(res, tile, past, a.cols, lane), g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
+        }
+    };
+    // y of one tile from h, the first element `at` and the mean beyond it
+    auto put = [&](int tile, const float2 (&f)[4], float at, float mean, float r) {
+        float2 w[4], b[4], y[4];
+        load_columns<DT, RUNS>(a.weight, a.weight_f32, 1.0f, tile, past, a.cols, lane, w);
+        load_columns<DT, RUNS>(a.bias, a.weight_f32, 0.0f, tile, past, a.cols, lane, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            y[j] = fma2(mul2(add2(add2(f[j], both(-at)), both(-mean)), both(r)), w[j], b[j]);
+        store_run<DT, RUNS>(out, tile, past, a.cols, lane, pack8<DT>(y));
+    };
+    auto statistics = [&](float at, float mean, float squares) {
+        const float r = rsqrtf(fmaf(squares, per_col, a.eps));
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = at + mean;
+            if (a.rstd) a.rstd[row] = r;
+        }
+        return r;
+    };
+
+    if constexpr (HELD) {
+        float2 f[KT][4];
+        Raw8<DT> rx[KT], rr[KT];
+#pragma unroll
+        for (int k = 0; k < KT; ++k) rx[k] = load_run<DT, RUNS>(x, warp + k * warps, past, a.cols, lane);
+        if (res) {
+#pragma unroll
+            for (int k = 0; k < KT; ++k) rr[k] = load_run<DT, RUNS>(res, warp + k * warps, past, a.cols, lane);
+        }
+        float at = first_of(x);
+        if (res) at += first_of(res);
+        float2 s2 = both(0.0f);
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            unpack8<DT>(rx[k], f[k]);
+            if (res) {
+                float2 g[4];
+                unpack8<DT>(rr[k], g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[k][j] = add2(f[k][j], g[j]);
+            }
+            float2 d[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] = add2(f[k][j], both(-at));
+            clip_columns<RUNS>(warp + k * warps, past, a.cols, lane, d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
+            n += columns_in(warp + k * warps, past, a.cols);
+        }
+        float mean = warp_sum(s2.x + s2.y) / static_cast<float>(max(n, 1));
+        float2 q2 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            float2 d[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] = add2(add2(f[k][j], both(-at)), both(-mean));
+            clip_columns<RUNS>(warp + k * warps, past, a.cols, lane, d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
+        }
+        float squares = warp_sum(q2.x + q2.y);
+        if (warps > 1) {
+            if (lane == 0) part[warp] = make_float2(mean, squares);
+            __syncthreads();
+            const float2 v = lane < warps ? part[lane] : both(0.0f);
+            int m = 0;
+#pragma unroll
+            for (int k = 0; k < KT; ++k) m += lane < warps ? columns_in(lane + k * warps, past, a.cols) : 0;
+            const float count = static_cast<float>(m);
+            mean = warp_sum(m > 0 ? count * v.x : 0.0f) * per_col;
+            const float off = v.x - mean;
+            squares = warp_sum(m > 0 ? fmaf(count * off, off, v.y) : 0.0f);
+        }
+        const float r = statistics(at, mean, squares);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            const int tile = warp + k * warps;
+            if (tile * kTileCols - past >= a.cols) continue;
+            if (h) store_run<DT, RUNS>(h, tile, past, a.cols, lane, pack8<DT>(f[k]));
+            put(tile, f[k], at, mean, r);
+        }
+    } else {
+        __shared__ float sums[2][32];
+        const int tiles = (a.cols + past + kTileCols - 1) / kTileCols;
+        float at = first_of(x);
+        if (res) at += first_of(res);
+        float2 s2 = both(0.0f), q2 = both(0.0f), f[4];
+        for (int t = warp; t < tiles; t += warps) {
+            sum_of(t, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = add2(f[j], both(-at));
+            clip_columns<RUNS>(t, past, a.cols, lane, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s2 = add2(s2, f[j]);
+        }
+        const float mean = block_sum(s2.x + s2.y, warps, sums[0]) * per_col;
+        for (int t = warp; t < tiles; t += warps) {
+            sum_of(t, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = add2(add2(f[j], both(-at)), both(-mean));
+            clip_columns<RUNS>(t, past, a.cols, lane, f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q2 = fma2(f[j], f[j], q2);
+        }
+        const float r = statistics(at, mean, block_sum(q2.x + q2.y, warps, sums[1]));
+        for (int t = warp; t < tiles; t += warps) {
+            sum_of(t, f);
+            if (h) store_run<DT, RUNS>(h, t, past, a.cols, lane, pack8<DT>(f));
+            put(t, f, at, mean, r);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- backward
+//
+// With n = (h - m) r and g = dy w:  dx = r (g - mean(g) - n mean(g n)) + dh.
+// Blocks walk over rows (row, row + writers, ..) and keep their columns' sums of
+// dy n and dy in registers; each writes them once, to its own row of `partial`,
+// and column_sums_kernel adds those rows in order.
+
+// Matrices whose rows lie apart, element by element.
+template <int DT, int KT> __global__ void __launch_bounds__(512) layernorm_grad_kernel(LayerNormGradArgs a) {
+    enter_grid();
+    __shared__ float2 part[2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t writer = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t writers = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    float2 dw[KT][4], db[KT][4];
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[k][j] = db[k][j] = both(0.0f);
+    const float per_col = 1.0f / static_cast<float>(a.cols);
+    int turn = 0;
+    for (int64_t row = writer; row < a.rows; row += writers, turn ^= 1) {
+        const void *dy = row_of<DT>(a.dy, row, a.dy_stride), *h = row_of<DT>(a.h, row, a.h_stride);
+        const float2 m = both(-a.mean[row]), r = both(a.rstd[row]);
+        Raw8<DT> cdy[KT], ch[KT];
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            cdy[k] = load_run<DT, false>(dy, warp + k * warps, 0, a.cols, lane);
+            ch[k] = load_run<DT, false>(h, warp + k * warps, 0, a.cols, lane);
+        }
+        float2 c1 = both(0.0f), c2 = both(0.0f);
+        auto products = [&](int k, float2 (&g)[4], float2 (&n)[4], bool add) {
+            float2 w[4];
+            load_columns<DT, false>(a.weight, a.weight_f32, 1.0f, warp + k * warps, 0, a.cols, lane, w);
+            unpack8<DT>(cdy[k], g);
+            unpack8<DT>(ch[k], n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n[j] = mul2(add2(n[j], m), r);
+            clip_columns<false>(warp + k * warps, 0, a.cols, lane, n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (add) {
+                    dw[k][j] = fma2(g[j], n[j], dw[k][j]);
+                    db[k][j] = add2(g[j], db[k][j]);
+                }
+                g[j] = mul2(g[j], w[j]);
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            float2 g[4], n[4];
+            products(k, g, n, true);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                c1 = add2(c1, g[j]);
+                c2 = fma2(g[j], n[j], c2);
+            }
+        }
+        const float2 c = block_sum2(make_float2(c1.x + c1.y, c2.x + c2.y), warps, part[turn]);
+        const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * per_col);
+        void *dx = row_of<DT>(a.dx, row, a.dx_stride);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            float2 g[4], n[4], d[4];
+            products(k, g, n, false);
+            if (a.dh) {
+                unpack8<DT>(load_run<DT, false>(row_of<DT>(a.dh, row, a.dh_stride), warp + k * warps, 0, a.cols, lane), d);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] = both(0.0f);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] = fma2(r, fma2(m2, n[j], add2(g[j], m1)), d[j]);
+            store_run<DT, false>(dx, warp + k * warps, 0, a.cols, lane, pack8<DT>(d));
+        }
+    }
+    if (a.partial == nullptr) return;
+    float *out = a.partial + writer * a.cols, *out_b = a.partial + (writers + writer) * a.cols;
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int col = col_of<false>(warp + k * warps, 0, lane, j);
+            if (col < a.cols) {
+                out[col] = (j & 1) ? dw[k][j / 2].y : dw[k][j / 2].x;
+                out_b[col] = (j & 1) ? db[k][j / 2].y : db[k][j / 2].x;
+            }
+        }
+}
+
+// Rows too wide to hold are read twice, after layernorm_columns_kernel has taken
+// the columns' sums (dx may be dy).
+template <int DT, bool RUNS> __global__ void __launch_bounds__(1024) layernorm_grad_wide_kernel(LayerNormGradArgs a) {
+    enter_grid();
+    __shared__ float2 part[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t row = blockIdx.x;
+    const void *dy = row_of<DT>(a.dy, row, a.dy_stride), *h = row_of<DT>(a.h, row, a.h_stride);
+    const int past = RUNS ? past_of<DT>(dy) : 0, tiles = (a.cols + past + kTileCols - 1) / kTileCols;
+    const float2 m = both(-a.mean[row]), r = both(a.rstd[row]);
+    auto products = [&](int tile, float2 (&g)[4], float2 (&n)[4]) {
+        float2 w[4];
+        load_columns<DT, RUNS>(a.weight, a.weight_f32, 1.0f, tile, past, a.cols, lane, w);
+        unpack8<DT>(load_run<DT, RUNS>(dy, tile, past, a.cols, lane), g);
+        unpack8<DT>(load_run<DT, RUNS>(h, tile, past, a.cols, lane), n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            n[j] = mul2(add2(n[j], m), r);
+            g[j] = mul2(g[j], w[j]);
+        }
+        clip_columns<RUNS>(tile, past, a.cols, lane, n);
+    };
+    float2 c1 = both(0.0f), c2 = both(0.0f), g[4], n[4];
+    for (int t = warp; t < tiles; t += warps) {
+        products(t, g, n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c1 = add2(c1, g[j]);
+            c2 = fma2(g[j], n[j], c2);
+        }
+    }
+    const float2 c = block_sum2(make_float2(c1.x + c1.y, c2.x + c2.y), warps, part);
+    const float per_col = 1.0f / static_cast<float>(a.cols);
+    const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * per_col);
+    void *dx = row_of<DT>(a.dx, row, a.dx_stride);
+    for (int t = warp; t < tiles; t += warps) {
+        products(t, g, n);
+        float2 d[4] = {};
+        if (a.dh) unpack8<DT>(load_run<DT, RUNS>(row_of<DT>(a.dh, row, a.dh_stride), t, past, a.cols, lane), d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = fma2(r, fma2(m2, n[j], add2(g[j], m1)), d[j]);
+        store_run<DT, RUNS>(dx, t, past, a.cols, lane, pack8<DT>(d));
+    }
+}
+
+// dweight and dbias of wide rows: one warp takes a tile of columns over the rows
+// blockIdx.y, blockIdx.y + gridDim.y, ..
+template <int DT, bool VEC> __global__ void __launch_bounds__(256) layernorm_columns_kernel(LayerNormGradArgs a) {
+    enter_grid();
+    const int lane = threadIdx.x & 31;
+    const int base = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kTileCols;
+    if (base >= a.cols) return;
+    float2 dw[4] = {}, db[4] = {};
+    for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+        float2 g[4], n[4];
+        const float2 m = both(-a.mean[row]), r = both(a.rstd[row]);
+        unpack8<DT>(load_tile<DT, VEC>(row_of<DT>(a.dy, row, a.dy_stride), base, a.cols, lane), g);
+        unpack8<DT>(load_tile<DT, VEC>(row_of<DT>(a.h, row, a.h_stride), base, a.cols, lane), n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            dw[j] = fma2(g[j], mul2(add2(n[j], m), r), dw[j]);
+            db[j] = add2(g[j], db[j]);
+        }
+    }
+    float *out = a.partial + static_cast<int64_t>(blockIdx.y) * a.cols;
+    float *out_b = out + static_cast<int64_t>(gridDim.y) * a.cols;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int col = tile_col<VEC>(base, lane, j);
+        if (col < a.cols) {
+            out[col] = (j & 1) ? dw[j / 2].y : dw[j / 2].x;
+            out_b[col] = (j & 1) ? db[j / 2].y : db[j / 2].x;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+constexpr int kLayerNormWarps = 16;  // that hold a row
+
+// Whether two matrices have their rows at the same place between multiples of 8 elements.
+template <int DT> bool same_runs(const void *p, int64_t stride, const void *q, int64_t other) {
+    return q == nullptr || (past_of<DT>(p) == past_of<DT>(q) && (stride - other) % 8 == 0);
+}
+
+template <int DT, bool RUNS>
+cudaError_t layernorm_launch(const LayerNormArgs &a, bool aligned, int sms, cudaStream_t s, LaunchInfo *info) {
+    const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (RUNS && !aligned ? 7 : 0) + kTileCols - 1) / kTileCols);
+    const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
+    int kt = tiles_per_thread(tiles, kLayerNormWarps, 4);
+    if (many && kt != 0) kt = std::max(kt, tiles == 1 ? 1 : DT != DT_F32 && tiles > 8 ? 4 : 2);
+    int warps = 32, per_block = 1;
+    if (kt != 0) {
+        warps = (tiles + kt - 1) / kt;
+        if (warps == 1 && many) per_block = 8;
+    }
+    const int64_t grid = (a.rows + per_block - 1) / per_block;
+    const dim3 block(32 * warps, per_block);
+    info->grid = static_cast<int>(grid);
+    info->block = 32 * warps * per_block;
+    info->vec_bytes = RUNS ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
+    switch (kt) {
+        case 1: return launch_rows(layernorm_kernel<DT, RUNS, 1, true>, dim3(grid), block, 0, 1, s, a);
+        case 2: return launch_rows(layernorm_kernel<DT, RUNS, 2, true>, dim3(grid), block, 0, 1, s, a);
+        case 4: return launch_rows(layernorm_kernel<DT, RUNS, 4, true>, dim3(grid), block, 0, 1, s, a);
+        default: return launch_rows(layernorm_kernel<DT, RUNS, 1, false>, dim3(grid), block, 0, 1, s, a);
+    }
+}
+
+template <int DT> cudaError_t layernorm_dispatch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
+    const bool runs = same_runs<DT>(a.x, a.x_stride, a.residual, a.residual_stride) &&
+                      same_runs<DT>(a.x, a.x_stride, a.y, a.y_stride) && same_runs<DT>(a.x, a.x_stride, a.h, a.h_stride);
+    return runs ? layernorm_launch<DT, true>(a, wide_rows<DT>(a.x, a.x_stride), sms, s, info)
+                : layernorm_launch<DT, false>(a, false, sms, s, info);
+}
+
+template <int DT>
+cudaError_t layernorm_grad_dispatch(const LayerNormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
+                                    int *launches) {
+    const bool runs = same_runs<DT>(a.dy, a.dy_stride, a.h, a.h_stride) &&
+                      same_runs<DT>(a.dy, a.dy_stride, a.dh, a.dh_stride) && same_runs<DT>(a.dy, a.dy_stride, a.dx, a.dx_stride);
+    const bool aligned = runs && wide_rows<DT>(a.dy, a.dy_stride);
+    const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + kTileCols - 1) / kTileCols);
+    const int kt = tiles_per_thread(tiles, kLayerNormWarps, DT == DT_F32 ? 2 : 4);
+    const bool sums = a.dweight != nullptr || a.dbias != nullptr;
+    int64_t writers = 0;
+    cudaError_t e = cudaSuccess;
+    info->vec_bytes = ElemOf<DT>::kBytes;
+    if (a.rows > 0 && kt != 0) {
+        const int warps = (tiles + kt - 1) / kt;
+        const int per_block = warps == 1 && a.rows >= 4 * static_cast<int64_t>(sms) ? 4 : 1;
+        const int resident = std::max(1, 16 / (warps * per_block));  // blocks that make 512 threads an SM
+        const int64_t grid = std::min<int64_t>({(a.rows + per_block - 1) / per_block,
+                                                static_cast<int64_t>(sms) * resident, most_writers / per_block});
+        writers = grid * per_block;
+        info->grid = static_cast<int>(grid);
+        info->block = 32 * warps * per_block;
+        auto kernel = kt == 1 ? layernorm_grad_kernel<DT, 1> : layernorm_grad_kernel<DT, 2>;
+        if constexpr (DT != DT_F32)
+            if (kt == 4) kernel = layernorm_grad_kernel<DT, 4>;
+        e = launch_rows(kernel, dim3(grid), dim3(32 * warps, per_block), 0, 1, s, a);
+        ++*launches;
+    } else if (a.rows > 0) {
+        if (sums) {
+            const bool vec = aligned && wide_rows<DT>(a.h, a.h_stride);
+            writers = std::min<int64_t>({a.rows, most_writers, std::max(1, 8 * sms * 8 / tiles)});
+            e = launch_rows(vec ? layernorm_columns_kernel<DT, true> : layernorm_columns_kernel<DT, false>,
+                            dim3((tiles + 7) / 8, static_cast<unsigned>(writers)), dim3(256), 0, 1, s, a);
+            ++*launches;
+        }
+        if (e == cudaSuccess)
+            e = launch_rows(runs ? layernorm_grad_wide_kernel<DT, true> : layernorm_grad_wide_kernel<DT, false>,
+                            dim3(static_cast<unsigned>(a.rows)), dim3(1024), 0, 1, s, a);
+        ++*launches;
+        info->grid = static_cast<int>(a.rows);
+        info->block = 1024;
+    }
+    if (e != cudaSuccess || !sums) return e;
+    ++*launches;
+    return launch_column_sums(a.partial, writers, a.cols, a.dweight, s, true, a.dbias);
+}
+
+}  // namespace
+}  // namespace ew

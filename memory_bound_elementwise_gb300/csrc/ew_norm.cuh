@@ -362,9 +362,6 @@ __global__ void __launch_bounds__(AHEAD ? 256 : 512, AHEAD && KT * ElemOf<DT>::k
 // alone, waits for its own copies and needs no barrier for them.  The bound is
 // memory: 12000 rows of 5056 bf16 take 81 us (floor 72; with the rows ahead held
 // in registers, 156), of 12288 bf16 175 us (174), of 4096 binary32 120 us (116).
-template <int LEFT> __device__ __forceinline__ void copies_left() {
-    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
-}
 template <int DT, int KT> __global__ void __launch_bounds__(512, 1) norm_grad_ring_kernel(NormGradArgs a, int depth) {
     enter_grid();
     // P pieces of 16 bytes hold a lane's 8 elements: of binary32 the two are 128
@@ -587,18 +584,6 @@ __global__ void __launch_bounds__(256) norm_dweight_wide_kernel(NormGradArgs a) 
 // ---------------------------------------------------------------- launches
 
 constexpr int kHeldWarps = 16;
-
-// Smallest number of tiles a thread (1, 2 or 4) with which `warps` warps hold a
-// row of `tiles` tiles; 0 where none does.
-inline int tiles_per_thread(int tiles, int warps, int most) {
-    for (int kt = 1; kt <= most; kt *= 2)
-        if ((tiles + kt - 1) / kt <= warps) return kt;
-    return 0;
-}
-
-template <int DT> bool wide_weight(const void *w, bool f32) {
-    return reinterpret_cast<uintptr_t>(w) % (f32 || DT == DT_F32 ? 32 : 16) == 0;
-}
 
 template <int DT, bool VEC, int QUANT>
 cudaError_t norm_launch(const NormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {

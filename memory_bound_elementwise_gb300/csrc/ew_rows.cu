@@ -9,8 +9,15 @@ namespace {
 // 32nd row, then the 32 sums are added in order.  A block takes 32 columns, so
 // a warp reads whole lines; the rows come from L2, where the kernel before
 // left them, and what counts is how many loads are under way at once.
-__global__ void __launch_bounds__(1024) column_sums_kernel(const float *rows, int64_t n, int32_t cols, float *out) {
+// The second row of blocks adds the n rows after the first n, into out2.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float *rows, int64_t n, int32_t cols, float *out,
+                                                           float *out2) {
     enter_grid();
+    if (blockIdx.y > 0) {
+        rows += n * cols;
+        out = out2;
+    }
+    if (out == nullptr) return;
     __shared__ float part[32][33];
     const int lane = threadIdx.x & 31, strip = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
@@ -39,8 +46,9 @@ __global__ void __launch_bounds__(1024) column_sums_kernel(const float *rows, in
 
 }  // namespace
 
-cudaError_t launch_column_sums(const float *rows, int64_t n, int32_t cols, float *out, cudaStream_t s) {
-    return launch_rows(column_sums_kernel, dim3((cols + 31) / 32), dim3(1024), 0, 1, s, rows, n, cols, out);
+cudaError_t launch_column_sums(const float *rows, int64_t n, int32_t cols, float *out, cudaStream_t s, bool two,
+                               float *out2) {
+    return launch_rows(column_sums_kernel, dim3((cols + 31) / 32, two ? 2 : 1), dim3(1024), 0, 1, s, rows, n, cols, out, out2);
 }
 
 }  // namespace ew

@@ -255,6 +255,11 @@ __device__ __forceinline__ int64_t token_at(const void *tokens, bool i64, int64_
     return i64 ? static_cast<const int64_t *>(tokens)[t] : static_cast<const int32_t *>(tokens)[t];
 }
 
+// Waits until at most LEFT of this thread's latest groups of asynchronous copies are under way.
+template <int LEFT> __device__ __forceinline__ void copies_left() {
+    asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
+}
+
 // base + row * stride elements, in 64 bits
 template <int DT> __device__ __forceinline__ const void *row_of(const void *base, int64_t row, int64_t stride) {
     return static_cast<const char *>(base) + row * stride * ElemOf<DT>::kBytes;
@@ -267,6 +272,17 @@ template <int DT> __device__ __forceinline__ void *row_of(void *base, int64_t ro
 // matrix are multiples of 8 elements.  Null matrices allow anything.
 template <int DT> inline bool wide_rows(const void *p, int64_t stride) {
     return reinterpret_cast<uintptr_t>(p) % (8 * ElemOf<DT>::kBytes) == 0 && (p == nullptr || stride % 8 == 0);
+}
+template <int DT> inline bool wide_weight(const void *w, bool f32) {
+    return reinterpret_cast<uintptr_t>(w) % (f32 || DT == DT_F32 ? 32 : 16) == 0;
+}
+
+// Smallest number of tiles a thread (1, 2 or 4) with which `warps` warps hold a
+// row of `tiles` tiles; 0 where none does.
+inline int tiles_per_thread(int tiles, int warps, int most) {
+    for (int kt = 1; kt <= most; kt *= 2)
+        if ((tiles + kt - 1) / kt <= warps) return kt;
+    return 0;
 }
 
 }  // namespace ew

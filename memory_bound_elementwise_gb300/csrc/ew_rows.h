@@ -63,8 +63,10 @@ inline cudaError_t allow_smem(const void *kernel, int bytes, std::atomic<uint64_
 }
 
 // Adds `n` rows of `cols` binary32 values in order into out[cols] (zeros where
-// n is 0).
-cudaError_t launch_column_sums(const float *rows, int64_t n, int32_t cols, float *out, cudaStream_t s);
+// n is 0); with `two`, the n rows after those into out2[cols] in the same launch.
+// Null outputs are left out.
+cudaError_t launch_column_sums(const float *rows, int64_t n, int32_t cols, float *out, cudaStream_t s, bool two = false,
+                               float *out2 = nullptr);
 
 // ---------------------------------------------------------------- norm
 
@@ -104,6 +106,39 @@ cudaError_t norm_grad_f16(const NormGradArgs &a, int64_t most_writers, int sms, 
                           int *launches);
 cudaError_t norm_grad_bf16(const NormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
                            int *launches);
+
+struct LayerNormArgs {
+    const void *x, *residual, *weight, *bias;
+    void *y, *h;          // h null where not wanted
+    float *mean, *rstd;   // null where not wanted
+    int64_t x_stride, residual_stride, y_stride, h_stride;
+    int64_t rows;
+    int32_t cols;
+    float eps, per_col;   // per_col: 1 / cols
+    int32_t weight_f32;   // the weight's and the bias's type
+};
+cudaError_t layernorm_f32(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t layernorm_f16(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t layernorm_bf16(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
+
+struct LayerNormGradArgs {
+    const void *dy, *h, *weight, *dh;
+    const float *mean, *rstd;
+    void *dx;
+    float *dweight, *dbias;  // null where not wanted
+    float *partial;          // workspace: each writer's sums of dweight, then each writer's of dbias
+    int64_t dy_stride, h_stride, dh_stride, dx_stride;
+    int64_t rows;
+    int32_t cols;
+    int32_t weight_f32;
+};
+// most_writers: twice as many rows of cols fit the workspace.
+cudaError_t layernorm_grad_f32(const LayerNormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
+                               int *launches);
+cudaError_t layernorm_grad_f16(const LayerNormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
+                               int *launches);
+cudaError_t layernorm_grad_bf16(const LayerNormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
+                                int *launches);
 
 // ---------------------------------------------------------------- embedding
 

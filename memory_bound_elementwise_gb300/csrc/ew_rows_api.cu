@@ -327,6 +327,86 @@ ew_status ew_rmsnorm_grad(ew_dtype dt, const void *dy, int64_t dy_stride, const 
     return EW_OK;
 }
 
+ew_status ew_layernorm(ew_dtype dt, const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                       ew_dtype wtype, const void *weight, const void *bias, float eps, void *y, int64_t y_stride,
+                       void *h_out, int64_t h_stride, float *mean_out, float *rstd_out, int64_t rows, int64_t cols,
+                       ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || ((weight != nullptr || bias != nullptr) && wtype != dt && wtype != EW_F32))
+        return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!size_ok(rows, 0) || !size_ok(cols, 1) || !(eps >= 0.0f) || std::isinf(eps)) return EW_ERR_INVALID_VALUE;
+    if (rows == 0) return EW_OK;
+    const int e = bytes_of(dt), we = wtype == EW_F32 ? 4 : e;
+    const Operand in[4] = {{x, rows, cols, x_stride, e},
+                           {residual, rows, cols, residual_stride, e, false},
+                           vec(weight, cols, we, false),
+                           vec(bias, cols, we, false)};
+    const Operand out[4] = {{y, rows, cols, y_stride, e},
+                            {h_out, rows, cols, h_stride, e, false},
+                            vec(mean_out, rows, 4, false),
+                            vec(rstd_out, rows, 4, false)};
+    const bool in_place[4][2] = {{true, true}, {true, true}, {false, false}, {false, false}};
+    const ew_status st = check_all(in, 4, out, 4, in_place);
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    const LayerNormArgs a{x, residual, weight, bias, y, h_out, mean_out, rstd_out, x_stride, residual_stride, y_stride,
+                          h_stride, rows, static_cast<int32_t>(cols), eps, 1.0f / static_cast<float>(cols),
+                          wtype == EW_F32};
+    LaunchInfo info;
+    ce = (dt == EW_F32 ? layernorm_f32 : dt == EW_F16 ? layernorm_f16 : layernorm_bf16)(
+        a, sms, reinterpret_cast<cudaStream_t>(s), &info);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, 1);
+    return EW_OK;
+}
+
+int64_t ew_layernorm_grad_workspace(int64_t rows, int64_t cols) {
+    if (!size_ok(rows, 0) || !size_ok(cols, 1)) return -1;
+    return std::min(rows, kNormPartials) * cols * 8;
+}
+
+ew_status ew_layernorm_grad(ew_dtype dt, const void *dy, int64_t dy_stride, const void *h, int64_t h_stride, ew_dtype wtype,
+                            const void *weight, const float *mean, const float *rstd, const void *dh, int64_t dh_stride,
+                            void *dx, int64_t dx_stride, float *dweight, float *dbias, int64_t rows, int64_t cols,
+                            void *workspace, int64_t workspace_bytes, ew_stream_t stream) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || (weight != nullptr && wtype != dt && wtype != EW_F32)) return EW_ERR_UNSUPPORTED_DTYPE;
+    const bool sums = dweight != nullptr || dbias != nullptr;
+    const int64_t need = ew_layernorm_grad_workspace(rows, cols);
+    if (need < 0 || (sums && workspace_bytes < need)) return EW_ERR_INVALID_VALUE;
+    if (rows == 0 && !sums) return EW_OK;
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return EW_ERR_INVALID_VALUE;
+    const int e = bytes_of(dt);
+    const Operand in[6] = {{dy, rows, cols, dy_stride, e},
+                           {dh, rows, cols, dh_stride, e, false},
+                           {h, rows, cols, h_stride, e},
+                           vec(weight, cols, wtype == EW_F32 ? 4 : e, false),
+                           vec(mean, rows, 4),
+                           vec(rstd, rows, 4)};
+    const Operand out[4] = {{dx, rows, cols, dx_stride, e},
+                            vec(dweight, cols, 4, false),
+                            vec(dbias, cols, 4, false),
+                            vec(sums ? workspace : nullptr, need / 4, 4, sums && need > 0)};
+    const bool in_place[4][2] = {{true, true}, {false, false}, {false, false}, {false, false}};
+    const ew_status st = check_all(in, 6, out, 4, in_place);
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    const LayerNormGradArgs a{dy, h, weight, dh, mean, rstd, dx, dweight, dbias, sums ? static_cast<float *>(workspace) : nullptr,
+                              dy_stride, h_stride, dh_stride, dx_stride, rows, static_cast<int32_t>(cols),
+                              weight != nullptr && wtype == EW_F32};
+    LaunchInfo info;
+    int launches = 0;
+    ce = (dt == EW_F32 ? layernorm_grad_f32 : dt == EW_F16 ? layernorm_grad_f16 : layernorm_grad_bf16)(
+        a, std::min(rows, kNormPartials), sms, reinterpret_cast<cudaStream_t>(stream), &info, &launches);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, launches);
+    return EW_OK;
+}
+
 ew_status ew_logprob(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *tokens, float scale,
                      int64_t top, float *logp, float *entropy, float *lse, float *top_logp, int32_t *top_ids,
                      int64_t rows, int64_t cols, ew_stream_t s) {

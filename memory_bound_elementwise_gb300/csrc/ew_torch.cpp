@@ -252,15 +252,15 @@ struct Weight {
     ew_dtype type;
     const void *p;
 };
-Weight weight_of(PyObject *o, int64_t cols, ew_dtype code, at::ScalarType type, Device d) {
+Weight weight_of(PyObject *o, int64_t cols, ew_dtype code, at::ScalarType type, Device d, const char *what = "weight") {
     if (o == Py_None) return {code, nullptr};
-    const Tensor &w = tensor(o, "weight");
+    const Tensor &w = tensor(o, what);
     if (w.scalar_type() != type && w.scalar_type() != at::kFloat)
-        REFUSE(PyExc_TypeError, "weight: %s or float32, got %s", c10::toString(type), c10::toString(w.scalar_type()));
-    return {w.scalar_type() == type ? code : EW_F32, vector(w, "weight", cols, w.scalar_type(), d)};
+        REFUSE(PyExc_TypeError, "%s: %s or float32, got %s", what, c10::toString(type), c10::toString(w.scalar_type()));
+    return {w.scalar_type() == type ? code : EW_F32, vector(w, what, cols, w.scalar_type(), d)};
 }
 
-// What both norm calls take (x, weight, residual, eps), and their outputs h and rstd.
+// What the norm calls take (x, weight, residual, eps), and their outputs h and rstd.
 struct NormCall {
     const Tensor &x;
     Device d;
@@ -328,6 +328,40 @@ PyObject *rmsnorm_grad(PyObject *const *a) {  // dy, h, weight, rstd, dh, dx, dw
                                  m.rows, m.cols, work.p(), work.bytes, d.stream()),
                  "ew_rmsnorm_grad");
     return tuple_of(dx, dweight);
+}
+
+PyObject *layernorm(PyObject *const *a) {  // x, weight, residual, eps, bias, y, h, mean, rstd
+    NormCall c(a, a[5], a[6], a[8]);
+    const Weight b = weight_of(a[4], c.m.cols, c.code, c.type, c.d, "bias");
+    if (c.w.p != nullptr && b.p != nullptr && c.w.type != b.type) REFUSE(PyExc_TypeError, "weight and bias: one dtype");
+    Output y, mean;
+    const Matrix o = y.matrix(a[5], "y", c.x.sizes(), c.m.rows, c.m.cols, c.type, c.d);
+    float *mean_p = mean.floats(a[7], "mean", c.m.rows, c.d);
+    check_status(ew_layernorm(c.code, c.m.p, c.m.stride, c.residual.p, c.residual.stride, c.w.p != nullptr ? c.w.type : b.type,
+                              c.w.p, b.p, c.eps, o.p, o.stride, c.hm.p, c.hm.stride, mean_p, c.rstd_p, c.m.rows, c.m.cols,
+                              c.d.stream()),
+                 "ew_layernorm");
+    return tuple_of(y, c.h, mean, c.rstd);
+}
+
+PyObject *layernorm_grad(PyObject *const *a) {  // dy, h, weight, mean, rstd, dh, dx, dweight, dbias
+    const Tensor &dy = tensor(a[0], "dy");
+    const Device d = device_of(dy, "dy");
+    const ew_dtype code = code_of(dy, "dy");
+    const at::ScalarType type = dy.scalar_type();
+    const Matrix m = matrix(dy, "dy", d), h = matrix_like(tensor(a[1], "h"), "h", m.rows, m.cols, type, d);
+    const Weight w = weight_of(a[2], m.cols, code, type, d);
+    const float *mean = floats(a[3], "mean", m.rows, d), *rstd = floats(a[4], "rstd", m.rows, d);
+    Matrix dh{nullptr, 0, 0, 0};
+    if (a[5] != Py_None) dh = matrix_like(tensor(a[5], "dh"), "dh", m.rows, m.cols, type, d);
+    const Workspace work(ew_layernorm_grad_workspace(m.rows, m.cols), "ew_layernorm_grad", d);
+    Output dx, dweight, dbias;
+    const Matrix o = dx.matrix(a[6], "dx", dy.sizes(), m.rows, m.cols, type, d);
+    float *dw = dweight.floats(a[7], "dweight", m.cols, d), *db = dbias.floats(a[8], "dbias", m.cols, d);
+    check_status(ew_layernorm_grad(code, m.p, m.stride, h.p, h.stride, w.type, w.p, mean, rstd, dh.p, dh.stride, o.p, o.stride,
+                                   dw, db, m.rows, m.cols, work.p(), work.bytes, d.stream()),
+                 "ew_layernorm_grad");
+    return tuple_of(dx, dweight, dbias);
 }
 
 // ---------------------------------------------------------------- logits
@@ -473,7 +507,7 @@ PyObject *set_check(PyObject *, PyObject *fn) {
 
 PyMethodDef g_methods[] = {
     ENTRY(embed, 4), ENTRY(embed_grad, 6), ENTRY(rmsnorm, 7), ENTRY(rmsnorm_quant, 10), ENTRY(rmsnorm_grad, 7),
-    ENTRY(logprob, 4), ENTRY(logprob_grad, 8), ENTRY(distill, 4), ENTRY(distill_grad, 7), ENTRY(distill_step, 6),
+    ENTRY(layernorm, 9), ENTRY(layernorm_grad, 9), ENTRY(logprob, 4), ENTRY(logprob_grad, 8), ENTRY(distill, 4), ENTRY(distill_grad, 7), ENTRY(distill_step, 6),
     {"set_check", set_check, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ew_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

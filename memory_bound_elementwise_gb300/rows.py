@@ -108,6 +108,28 @@ def ew_rmsnorm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, stream=
     return _C.rmsnorm_grad(dy, h, weight, rstd, dh, dx, dweight)
 
 
+def ew_layernorm(x, weight, bias=None, residual=None, eps=1e-5, y=None, h=None, mean=None, rstd=None, stream=None):
+    """y = (h - mean(h)) / sqrt(var(h) + eps) * weight + bias with h = x + residual; returns (y, h, mean, rstd).
+
+    ``weight`` and ``bias`` have x's dtype or float32, both the same (None: ones, zeros).  Without
+    a residual h is x, or, where y is x, a copy of it.  ``mean`` and ``rstd`` (float32, one a row)
+    and ``h`` are what ew_layernorm_grad takes.  y may be x or residual, h may be x or residual,
+    for in place."""
+    if stream is not None:
+        return _on(stream, ew_layernorm, x, weight, bias, residual, eps, y, h, mean, rstd)
+    return _C.layernorm(x, weight, residual, eps, bias, y, h, mean, rstd)
+
+
+def ew_layernorm_grad(dy, h, weight, mean, rstd, dh=None, dx=None, dweight=None, dbias=None, stream=None):
+    """Gradients of ew_layernorm: returns (dx, dweight, dbias), dx for x and for the residual alike.
+
+    ``h``, ``mean`` and ``rstd`` come from the forward call; ``dh`` is the gradient that reaches h
+    by the residual stream.  dweight and dbias are float32.  dx may be dy or dh."""
+    if stream is not None:
+        return _on(stream, ew_layernorm_grad, dy, h, weight, mean, rstd, dh, dx, dweight, dbias)
+    return _C.layernorm_grad(dy, h, weight, mean, rstd, dh, dx, dweight, dbias)
+
+
 # ---------------------------------------------------------------- logits
 
 Logprobs = collections.namedtuple("Logprobs", "logp entropy lse top_logp top_ids")

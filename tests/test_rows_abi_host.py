@@ -160,3 +160,41 @@ def test_distill_refusals():
     assert L.ew_distill_grad(2, 1, P, 64, P + MB, 8, 2, P + 2 * MB, 8, 8, 1.0, None, P + 3 * MB, P + 6 * MB, 64, 4, 64,
                              None) == NULLP
     assert ew.last_launch()["launches"] == 0
+
+
+def layernorm(dt=2, x=P, xs=64, r=None, rs=0, wt=2, w=None, b=None, eps=1e-5, y=P + MB, ys=64, h=None, hs=0, mean=None,
+              rstd=None, rows=4, cols=64):
+    return ew.lib().ew_layernorm(dt, x, xs, r, rs, wt, w, b, eps, y, ys, h, hs, mean, rstd, rows, cols, None)
+
+
+def layernorm_grad(dt=2, dy=P, h=P + MB, mean=P + 2 * MB, rstd=P + 3 * MB, dh=None, dx=P + 4 * MB, dw=P + 5 * MB,
+                   db=P + 6 * MB, rows=4, cols=64, work=P + 7 * MB, size=MB, s=64, wt=2, w=None):
+    return ew.lib().ew_layernorm_grad(dt, dy, s, h, s, wt, w, mean, rstd, dh, s, dx, s, dw, db, rows, cols, work, size, None)
+
+
+def test_layernorm_refusals():
+    assert layernorm(dt=3) == DTYPE and layernorm(w=P + 2 * MB, wt=1) == DTYPE and layernorm(b=P + 2 * MB, wt=1) == DTYPE
+    assert layernorm(rows=0, x=None, y=None) == OK and ew.last_launch()["launches"] == 0
+    assert layernorm(rows=-1) == INVALID and layernorm(cols=0) == INVALID and layernorm(rows=BIG + 1) == INVALID
+    assert layernorm(x=None) == NULLP and layernorm(y=None) == NULLP
+    assert layernorm(x=P + 1) == INVALID and layernorm(mean=P + 2 * MB + 2) == INVALID and layernorm(b=P + 1) == INVALID
+    assert layernorm(xs=63) == INVALID and layernorm(ys=10) == INVALID and layernorm(r=P + 2 * MB, rs=1) == INVALID
+    for eps in (-1e-9, float("nan"), float("inf")):
+        assert layernorm(eps=eps) == INVALID
+    assert layernorm(y=P + 2) == OVERLAP and layernorm(y=P, ys=128) == OVERLAP and layernorm(h=P + MB, hs=64) == OVERLAP
+    assert layernorm(b=P + MB + 8) == OVERLAP and layernorm(mean=P + MB) == OVERLAP
+    assert layernorm(mean=P + 2 * MB, rstd=P + 2 * MB) == OVERLAP
+
+
+def test_layernorm_grad_refusals():
+    assert layernorm_grad(dt=3) == DTYPE and layernorm_grad(w=P + 8 * MB, wt=1) == DTYPE
+    assert layernorm_grad(rows=-1) == INVALID and layernorm_grad(cols=0) == INVALID
+    for name in ("dy", "h", "mean", "rstd", "dx", "work"):
+        assert layernorm_grad(**{name: None}) == NULLP, name
+    need = ew.lib().ew_layernorm_grad_workspace(4, 64)
+    assert need == 4 * 64 * 8 and layernorm_grad(size=need - 1) == INVALID and layernorm_grad(work=P + 7 * MB + 128) == INVALID
+    assert layernorm_grad(dx=P + MB) == OVERLAP and layernorm_grad(dx=P + 2) == OVERLAP and layernorm_grad(work=P) == OVERLAP
+    assert layernorm_grad(db=P + 5 * MB) == OVERLAP and layernorm_grad(db=P + 7 * MB + 64) == OVERLAP
+    assert layernorm_grad(rows=0, dw=None, db=None) == OK
+    assert ew.lib().ew_layernorm_grad_workspace(-1, 64) == -1 and ew.lib().ew_layernorm_grad_workspace(4, BIG + 1) == -1
+    assert ew.last_launch()["launches"] == 0
