@@ -31,6 +31,9 @@
  *   ew_rmsnorm        root-mean-square norm with the residual's addition,
  *                     ew_rmsnorm_quant (8-bit output with scales), ew_rmsnorm_grad
  *   ew_layernorm      layer norm with the residual's addition, and ew_layernorm_grad
+ *   ew_expert_sort    tokens sorted by expert, ew_expert_dispatch (their rows in that
+ *                     order), ew_expert_combine (weighted, back to the tokens) and
+ *                     ew_expert_combine_grad
  *   ew_logprob        log probabilities of given tokens, entropy and top
  *                     alternatives, and ew_logprob_grad
  *   ew_distill        distillation from a teacher's top logits: ew_distill,
@@ -382,6 +385,63 @@ EW_API ew_status ew_layernorm_grad(ew_dtype dtype, const void *dy, int64_t dy_st
                                    ew_stream_t stream);
 /* Bytes of workspace (-1: sizes out of range). */
 EW_API int64_t ew_layernorm_grad_workspace(int64_t rows, int64_t cols);
+
+/* ---- tokens by expert.  Each of `rows` tokens names k (1 to 64) experts of n_experts
+ * (1 to 1024); slot t * k + j stands for expert j of token t.  rows * k is at most
+ * 2^31 - 2^16.  The rows sorted by expert are the slots' rows, each expert's in the
+ * slots' order and beginning at a multiple of `align` (1 to 65536), as a product with
+ * whole tiles takes them. */
+
+/* Rows that suffice for any choice of experts: rows * k, and align - 1 more for each
+ * expert that may have a slot, rounded down to a multiple of align.  -1: sizes out of
+ * range, or more than 2^31 - 2^16 rows. */
+EW_API int64_t ew_expert_capacity(int64_t rows, int64_t k, int64_t n_experts, int64_t align);
+
+/* Sorts the slots by expert (stable).  experts: rows x k of type itype, its own
+ * stride; an id outside [0, n_experts) is a slot of no expert, and two slots of one
+ * token may name the same one.
+ *     positions[slot]  the slot's row among the sorted ones, -1 of no expert (rows x k)
+ *     offsets[e]       the first row of expert e; offsets[n_experts] the end of the last
+ *     counts[e]        slots of expert e: its rows from offsets[e] on; further ones, up
+ *                      to offsets[e + 1], are of no slot
+ *     slots[row]       the slot of a row, -1 of none (capacity of them)
+ * capacity is at least ew_expert_capacity's.  rows == 0 writes what belongs to no slot. */
+EW_API ew_status ew_expert_sort(ew_index itype, const void *experts, int64_t experts_stride, int64_t n_experts,
+                                int64_t align, int32_t *positions, int32_t *offsets, int32_t *counts, int32_t *slots,
+                                int64_t capacity, int64_t rows, int64_t k, void *workspace, int64_t workspace_bytes,
+                                ew_stream_t stream);
+/* Bytes of workspace, 0 for few slots (-1: sizes out of range). */
+EW_API int64_t ew_expert_sort_workspace(int64_t rows, int64_t k, int64_t n_experts);
+
+/* out[positions[t,j],:] = x[t,:], bit for bit, and zeros in the rows whose slot is
+ * negative.  out: capacity x cols.  Positions outside [0, capacity) are left out.  Its
+ * gradient is ew_expert_combine without weights and residual.  Where positions and
+ * slots do not belong together, rows that both name or that neither names hold
+ * nothing in particular; this holds for ew_expert_combine_grad, too. */
+EW_API ew_status ew_expert_dispatch(ew_dtype dtype, const void *x, int64_t x_stride, const int32_t *positions,
+                                    const int32_t *slots, void *out, int64_t out_stride, int64_t capacity, int64_t rows,
+                                    int64_t k, int64_t cols, ew_stream_t stream);
+
+/* out[t,:] = residual[t,:] + sum over j of weights[t,j] * y[positions[t,j],:], the sum
+ * in binary32, in the order of j.  y: capacity x cols.  weights: rows x k of type wtype
+ * (dtype or EW_F32), contiguous, or NULL for ones.  residual may be NULL (zeros); out
+ * may be residual (the same base and stride).  Positions outside [0, capacity) add
+ * nothing, whatever their weight is. */
+EW_API ew_status ew_expert_combine(ew_dtype dtype, const void *y, int64_t y_stride, int64_t capacity,
+                                   const int32_t *positions, ew_dtype wtype, const void *weights, const void *residual,
+                                   int64_t residual_stride, void *out, int64_t out_stride, int64_t rows, int64_t k,
+                                   int64_t cols, ew_stream_t stream);
+
+/* Gradients of ew_expert_combine (its residual's is dout itself):
+ *     dy[positions[t,j],:] = weights[t,j] * dout[t,:], zeros in the rows whose slot is negative
+ *     dweights[t,j] = sum over columns of dout[t,:] * y[positions[t,j],:]    (binary32, rows x k)
+ * Slots without a row have dweights 0.  weights may be NULL (ones); dweights may be
+ * NULL, and then y too. */
+EW_API ew_status ew_expert_combine_grad(ew_dtype dtype, const void *dout, int64_t dout_stride, const void *y,
+                                        int64_t y_stride, int64_t capacity, const int32_t *positions,
+                                        const int32_t *slots, ew_dtype wtype, const void *weights, void *dy,
+                                        int64_t dy_stride, float *dweights, int64_t rows, int64_t k, int64_t cols,
+                                        ew_stream_t stream);
 
 /* Log probabilities of given tokens, with entropy and top alternatives.  Per row,
  * with p = softmax(scale * logits):

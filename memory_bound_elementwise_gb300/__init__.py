@@ -24,6 +24,9 @@ Row operators (matrices, one row at a time; ``rows.py``)::
     ew_rmsnorm_grad(dy, h, w, rstd) (dx, dweight)
     ew_layernorm(x, w, b, residual) (y, h, mean, rstd): h = x + residual, y = (h - mean) * rstd * w + b
     ew_layernorm_grad(dy, h, w, mean, rstd) (dx, dweight, dbias)
+    ew_expert_sort(experts, n)      ExpertPlan: tokens sorted by expert
+    ew_expert_dispatch(x, plan)     the tokens' rows in that order
+    ew_expert_combine(y, plan, w, residual)  back to the tokens, weighted; ew_expert_combine_grad
     ew_logprob(logits, tokens, top) log probabilities, entropy, lse and top alternatives
     ew_logprob_grad(...)            their gradient
     ew_distill(logits, ids, teacher)(loss, lse); ew_distill_grad, ew_distill_step
@@ -34,6 +37,7 @@ device; calls are enqueued on ``stream`` (default: torch's
 current stream) and do not synchronise.  ``lib()`` exposes the raw ctypes
 handle with the exact C signatures.
 """
+import collections
 import ctypes
 import os
 
@@ -65,11 +69,14 @@ EXPORTS = ("ew_add", "ew_saxpy", "ew_relu", "ew_add_relu", "ew_saxpy_relu", "ew_
            "ew_device_error", "ew_selftest_bounded_wait", "ew_version",
            "ew_embed", "ew_embed_grad", "ew_embed_grad_workspace", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad", "ew_rmsnorm_grad_workspace",
            "ew_layernorm", "ew_layernorm_grad", "ew_layernorm_grad_workspace",
+           "ew_expert_capacity", "ew_expert_sort", "ew_expert_sort_workspace", "ew_expert_dispatch", "ew_expert_combine",
+           "ew_expert_combine_grad",
            "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
 
 # Row operators (rows.py), loaded with torch at their first use.
 _ROW_OPERATORS = ("ew_embed", "ew_embed_grad", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad",
-                  "ew_layernorm", "ew_layernorm_grad", "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
+                  "ew_layernorm", "ew_layernorm_grad", "ew_expert_sort", "ew_expert_dispatch", "ew_expert_combine",
+                  "ew_expert_combine_grad", "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
 # Their C arguments: i enum, l int64, f float, p pointer.
 _ROW_SIGNATURES = {
     "ew_embed": "iipllpfplllp",
@@ -82,12 +89,21 @@ _ROW_SIGNATURES = {
     "ew_layernorm": "iplplippfplplppllp",
     "ew_layernorm_grad": "iplplipppplplppllplp",
     "ew_layernorm_grad_workspace": "ll",
+    "ew_expert_capacity": "llll",
+    "ew_expert_sort": "iplllpppplllplp",
+    "ew_expert_sort_workspace": "lll",
+    "ew_expert_dispatch": "iplppplllllp",
+    "ew_expert_combine": "ipllpipplplllp",
+    "ew_expert_combine_grad": "iplpllppipplplllp",
     "ew_logprob": "iiplpflpppppllp",
     "ew_logprob_grad": "iiplpppppfplllp",
     "ew_distill": "iiplplipllfppllp",
     "ew_distill_grad": "iiplplipllfppplllp",
     "ew_distill_step": "iiplplipllfpppplllp",
 }
+
+# What ew_expert_sort returns and the other ew_expert_* functions take.
+ExpertPlan = collections.namedtuple("ExpertPlan", "positions offsets counts slots")
 
 
 class EwError(RuntimeError):
@@ -174,7 +190,7 @@ def _declare_rows(L):
     for name, args in _ROW_SIGNATURES.items():
         fn = getattr(L, name)
         fn.argtypes = [letters[c] for c in args]
-        fn.restype = i64 if name.endswith("_workspace") else i32
+        fn.restype = i64 if name.endswith(("_workspace", "_capacity")) else i32
 
 
 def __getattr__(name):
@@ -392,4 +408,4 @@ __all__ = ["ew_add", "ew_saxpy", "ew_relu", "ew_add_relu", "ew_saxpy_relu", "ew_
            "ew_gather_stride", "set_path",
            "get_path", "set_schedule", "get_schedule", "set_programmatic_launch",
            "get_programmatic_launch", "set_pointer_check", "plan_query",
-           "last_launch", "device_error", "selftest_bounded_wait", "lib", "EwError", "EXPORTS", *_ROW_OPERATORS]
+           "last_launch", "device_error", "selftest_bounded_wait", "lib", "EwError", "EXPORTS", "ExpertPlan", *_ROW_OPERATORS]

@@ -27,7 +27,7 @@ BINDING_SOURCE = os.path.join(CSRC, "ew_torch.cpp")
 BINDING = os.path.join(OUT_DIR, "_ew_torch.so")  # CPython extension over torch's C++ headers
 
 SOURCES = ["ew_api.cu", "ew_kernels_f32.cu", "ew_kernels_f16.cu", "ew_kernels_bf16.cu", "ew_tma.cu",
-           "ew_gather_fixed.cu", "ew_gather_fixed_wide.cu", "ew_rows_api.cu", "ew_rows.cu", "ew_embed.cu",
+           "ew_gather_fixed.cu", "ew_gather_fixed_wide.cu", "ew_rows_api.cu", "ew_rows.cu", "ew_embed.cu", "ew_expert.cu",
            "ew_norm_f32.cu", "ew_norm_f16.cu", "ew_norm_bf16.cu",
            "ew_layernorm_f32.cu", "ew_layernorm_f16.cu", "ew_layernorm_bf16.cu",
            "ew_logits_f32.cu", "ew_logits_f16.cu", "ew_logits_bf16.cu",
@@ -48,7 +48,7 @@ def nvcc():
     raise RuntimeError("nvcc not found")
 
 
-ROW_OPERATORS = ("ew_rows", "ew_embed", "ew_norm", "ew_layernorm", "ew_logits", "ew_distill")  # what their sources' names begin with
+ROW_OPERATORS = ("ew_rows", "ew_embed", "ew_norm", "ew_layernorm", "ew_expert", "ew_logits", "ew_distill")  # what their sources' names begin with
 
 
 def _kernel_digest(skip=()):

@@ -108,51 +108,6 @@ constexpr int kDigitBits = 10;
 
 constexpr int kKept = 4;  // items a lane keeps between counting and moving them
 
-// One row of zeros, by a warp: whole runs of 8 elements wherever the row starts,
-// and the elements before the first and after the last of them.
-template <int GT> __device__ __forceinline__ void clear_row(void *row, int cols, int lane) {
-    using T = typename ElemOf<GT>::type;
-    constexpr int B = ElemOf<GT>::kBytes;
-    T *p = static_cast<T *>(row);
-    const int past = static_cast<int>(reinterpret_cast<uintptr_t>(row) % (8 * B)) / B;
-    const int head = min((8 - past) % 8, cols), runs = (cols - head) / 8;
-    const Vec<8 * B> zero = {};
-#pragma unroll 4
-    for (int k = lane; k < runs; k += 32) st<8 * B>(p + head + k * 8, zero);
-    if (lane < head) p[lane] = 0;
-    if (head + runs * 8 + lane < cols) p[head + runs * 8 + lane] = 0;
-}
-
-// Inclusive prefix sum over the block's threads; `scan` has a slot a warp.
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *scan) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t u = __shfl_up_sync(kAllLanes, v, d);
-        v += lane >= d ? u : 0u;
-    }
-    if (lane == 31) scan[warp] = v;
-    __syncthreads();
-    uint32_t before = lane < warp ? scan[lane] : 0u;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(kAllLanes, before, d);
-    return v + before;
-}
-
-// The lanes of `active` whose digit is this lane's: a ballot for each bit.  (A
-// match instruction takes about 64 cycles of the SM for 32 different digits,
-// ten ballots a quarter of that.)
-__device__ __forceinline__ unsigned lanes_alike(uint32_t digit, int bits, unsigned active) {
-    unsigned same = active;
-#pragma unroll 2
-    for (int b = 0; b < bits; ++b) {
-        const bool one = digit >> b & 1;
-        const unsigned ones = __ballot_sync(kAllLanes, one);
-        same &= one ? ones : ~ones;
-    }
-    return same;
-}
-
 template <int GT> __device__ __forceinline__ void clear_blind(const EmbedGradArgs &a, int sort_blocks) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int64_t v = (static_cast<int64_t>(blockIdx.x) - sort_blocks) * kSortWarps + warp; v < a.blind;

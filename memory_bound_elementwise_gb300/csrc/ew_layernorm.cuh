@@ -23,111 +23,32 @@
 namespace ew {
 namespace {
 
-// ---------------------------------------------------------------- runs of 8 elements
+// ---------------------------------------------------------------- columns
 
-// Elements of a row's first run that lie before the row.
-template <int DT> __host__ __device__ __forceinline__ int past_of(const void *row) {
-    return static_cast<int>(reinterpret_cast<uintptr_t>(row) % (8 * ElemOf<DT>::kBytes)) / ElemOf<DT>::kBytes;
-}
-// Column of element j of this lane in tile `tile` of a row.
-template <bool RUNS> __device__ __forceinline__ int col_of(int tile, int past, int lane, int j) {
-    return RUNS ? tile * kTileCols - past + lane * 8 + j : tile * kTileCols + j * 32 + lane;
-}
-// The lane's 8 elements; columns outside the row are zero.
-template <int DT, bool RUNS> __device__ __forceinline__ Raw8<DT> load_run(const void *row, int tile, int past, int cols, int lane) {
-    if constexpr (!RUNS) {
-        return load_tile<DT, false>(row, tile * kTileCols, cols, lane);
-    } else {
-        using T = typename ElemOf<DT>::type;
-        const T *p = static_cast<const T *>(row);
-        const int c0 = col_of<true>(tile, past, lane, 0);
-        Raw8<DT> r;
-        if (c0 >= 0 && c0 + 8 <= cols) {
-            const Vec<8 * ElemOf<DT>::kBytes> v = ld<8 * ElemOf<DT>::kBytes>(p + c0);
-#pragma unroll
-            for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = v.w[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = 0u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j >= 0 && c0 + j < cols) {
-                    if constexpr (DT == DT_F32) r.w[j] = ld<4>(p + c0 + j).w[0];
-                    else r.w[j / 2] |= static_cast<uint32_t>(ld<2>(p + c0 + j).h) << (16 * (j & 1));
-                }
-        }
-        return r;
-    }
-}
-template <int DT, bool RUNS>
-__device__ __forceinline__ void store_run(void *row, int tile, int past, int cols, int lane, const Raw8<DT> &r) {
-    if constexpr (!RUNS) {
-        store_tile<DT, false>(row, tile * kTileCols, cols, lane, r);
-    } else {
-        using T = typename ElemOf<DT>::type;
-        T *p = static_cast<T *>(row);
-        const int c0 = col_of<true>(tile, past, lane, 0);
-        if (c0 >= 0 && c0 + 8 <= cols) {
-            Vec<8 * ElemOf<DT>::kBytes> v;
-#pragma unroll
-            for (int k = 0; k < ElemOf<DT>::kWords; ++k) v.w[k] = r.w[k];
-            st<8 * ElemOf<DT>::kBytes>(p + c0, v);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j >= 0 && c0 + j < cols) p[c0 + j] = static_cast<T>(r.w[j * ElemOf<DT>::kBytes / 4] >> (j * ElemOf<DT>::kBytes % 4 * 8));
-        }
-    }
-}
 // The columns of a vector, in binary32; null stands for `other`, columns
-// outside for zero.  A run of it starts anywhere: it is cut out of the 16-byte
-// pieces around it, which lie within the vector but at its ends.
+// outside for zero.  A run of it starts anywhere.
 template <int DT, bool RUNS>
 __device__ __forceinline__ void load_columns(const void *w, bool f32, float other, int tile, int past, int cols, int lane,
                                              float2 (&f)[4]) {
+    const int c0 = col_of<RUNS>(tile, past, lane, 0);
     if (w == nullptr) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = both(other);
-        return;
-    }
-    const bool wide = DT == DT_F32 || f32;
-    const int c0 = col_of<RUNS>(tile, past, lane, 0);
-    const char *at = static_cast<const char *>(w) + static_cast<int64_t>(c0) * (wide ? 4 : 2);
-    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);  // the same for all lanes of a run
-    const int room = shift == 0 ? 0 : 8;
-    if (RUNS && c0 >= room && c0 + 8 + room <= cols) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(at - shift);
-        const uint4 a = q[0];
-        uint4 b = make_uint4(0u, 0u, 0u, 0u), c = b;
-        if (wide || shift) b = q[1];
-        if (wide && shift) c = q[2];
-        uint32_t v[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
-        if (shift & 8) {
+    } else if (RUNS && (DT == DT_F32 || f32)) {
+        unpack8<DT_F32>(load_at<DT_F32>(w, c0, cols), f);
+    } else if (RUNS) {
+        unpack8<DT>(load_at<DT>(w, c0, cols), f);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 10; ++j) v[j] = v[j + 2];
+        for (int j = 0; j < 8; ++j) {
+            const int col = col_of<false>(tile, past, lane, j);
+            float e = 0.0f;
+            if (col < cols) {
+                if (DT == DT_F32 || f32) e = static_cast<const float *>(w)[col];
+                else e = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(w)[col]);
+            }
+            (j & 1 ? f[j / 2].y : f[j / 2].x) = e;
         }
-        if (shift & 4) {
-#pragma unroll
-            for (int j = 0; j < 9; ++j) v[j] = v[j + 1];
-        }
-        if (wide) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-        } else if constexpr (DT != DT_F32) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = widen<DT>(__funnelshift_r(v[j], v[j + 1], (shift & 3) * 8));
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int col = col_of<RUNS>(tile, past, lane, j);
-        float e = 0.0f;
-        if (col >= 0 && col < cols) {
-            if (wide) e = static_cast<const float *>(w)[col];
-            else e = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(w)[col]);
-        }
-        (j & 1 ? f[j / 2].y : f[j / 2].x) = e;
     }
 }
 // Zeros in columns outside the row.

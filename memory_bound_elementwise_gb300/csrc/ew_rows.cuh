@@ -268,6 +268,160 @@ template <int DT> __device__ __forceinline__ void *row_of(void *base, int64_t ro
     return static_cast<char *>(base) + row * stride * ElemOf<DT>::kBytes;
 }
 
+// ---------------------------------------------------------------- runs of 8 elements
+//
+// Rows that start anywhere, in runs of 8 elements that start at multiples of 8
+// in memory: the first begins `past` elements before the row, and what is
+// outside the row is neither read nor written.
+
+// Elements of a row's first run that lie before the row.
+template <int DT> __host__ __device__ __forceinline__ int past_of(const void *row) {
+    return static_cast<int>(reinterpret_cast<uintptr_t>(row) % (8 * ElemOf<DT>::kBytes)) / ElemOf<DT>::kBytes;
+}
+// Column of element j of this lane in tile `tile` of a row.
+template <bool RUNS> __device__ __forceinline__ int col_of(int tile, int past, int lane, int j) {
+    return RUNS ? tile * kTileCols - past + lane * 8 + j : tile * kTileCols + j * 32 + lane;
+}
+// The lane's 8 elements; columns outside the row are zero.
+template <int DT, bool RUNS> __device__ __forceinline__ Raw8<DT> load_run(const void *row, int tile, int past, int cols, int lane) {
+    if constexpr (!RUNS) {
+        return load_tile<DT, false>(row, tile * kTileCols, cols, lane);
+    } else {
+        using T = typename ElemOf<DT>::type;
+        const T *p = static_cast<const T *>(row);
+        const int c0 = col_of<true>(tile, past, lane, 0);
+        Raw8<DT> r;
+        if (c0 >= 0 && c0 + 8 <= cols) {
+            const Vec<8 * ElemOf<DT>::kBytes> v = ld<8 * ElemOf<DT>::kBytes>(p + c0);
+#pragma unroll
+            for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = v.w[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j >= 0 && c0 + j < cols) {
+                    if constexpr (DT == DT_F32) r.w[j] = ld<4>(p + c0 + j).w[0];
+                    else r.w[j / 2] |= static_cast<uint32_t>(ld<2>(p + c0 + j).h) << (16 * (j & 1));
+                }
+        }
+        return r;
+    }
+}
+template <int DT, bool RUNS>
+__device__ __forceinline__ void store_run(void *row, int tile, int past, int cols, int lane, const Raw8<DT> &r) {
+    if constexpr (!RUNS) {
+        store_tile<DT, false>(row, tile * kTileCols, cols, lane, r);
+    } else {
+        using T = typename ElemOf<DT>::type;
+        T *p = static_cast<T *>(row);
+        const int c0 = col_of<true>(tile, past, lane, 0);
+        if (c0 >= 0 && c0 + 8 <= cols) {
+            Vec<8 * ElemOf<DT>::kBytes> v;
+#pragma unroll
+            for (int k = 0; k < ElemOf<DT>::kWords; ++k) v.w[k] = r.w[k];
+            st<8 * ElemOf<DT>::kBytes>(p + c0, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c0 + j >= 0 && c0 + j < cols) p[c0 + j] = static_cast<T>(r.w[j * ElemOf<DT>::kBytes / 4] >> (j * ElemOf<DT>::kBytes % 4 * 8));
+        }
+    }
+}
+
+// The 8 elements from column c0 on, wherever they start; columns outside the row
+// are zero.  They are cut out of the 16-byte pieces around them, which lie
+// within the row but at its ends; the lanes of a warp, which take runs of one
+// row, all cut at the same place.
+template <int DT> __device__ __forceinline__ Raw8<DT> load_at(const void *row, int c0, int cols) {
+    constexpr int B = ElemOf<DT>::kBytes, W = ElemOf<DT>::kWords;
+    using T = typename ElemOf<DT>::type;
+    const char *at = static_cast<const char *>(row) + static_cast<int64_t>(c0) * B;
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
+    const int room = shift == 0 ? 0 : 16 / B;
+    Raw8<DT> r;
+    if (c0 >= room && c0 + 8 + room <= cols) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(at - shift);
+        uint32_t v[W + 4];
+#pragma unroll
+        for (int k = 0; k < W / 4; ++k) {
+            const uint4 a = q[k];
+            v[4 * k] = a.x, v[4 * k + 1] = a.y, v[4 * k + 2] = a.z, v[4 * k + 3] = a.w;
+        }
+        if (shift != 0) {
+            const uint4 a = q[W / 4];
+            v[W] = a.x, v[W + 1] = a.y, v[W + 2] = a.z, v[W + 3] = a.w;
+#pragma unroll
+            for (int j = 0; j < W + 2; ++j) v[j] = shift & 8 ? v[j + 2] : v[j];
+#pragma unroll
+            for (int j = 0; j < W + 1; ++j) v[j] = shift & 4 ? v[j + 1] : v[j];
+            if constexpr (B == 2) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[j] = __funnelshift_r(v[j], v[j + 1], (shift & 3) * 8);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) r.w[j] = v[j];
+    } else {
+        const T *p = static_cast<const T *>(row);
+#pragma unroll
+        for (int k = 0; k < W; ++k) r.w[k] = 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c0 + j >= 0 && c0 + j < cols) r.w[j * B / 4] |= static_cast<uint32_t>(p[c0 + j]) << (j * B % 4 * 8);
+    }
+    return r;
+}
+
+// One row of zeros, by a warp: whole runs of 8 elements wherever the row starts,
+// and the elements before the first and after the last of them.
+template <int GT> __device__ __forceinline__ void clear_row(void *row, int cols, int lane) {
+    using T = typename ElemOf<GT>::type;
+    constexpr int B = ElemOf<GT>::kBytes;
+    T *p = static_cast<T *>(row);
+    const int past = static_cast<int>(reinterpret_cast<uintptr_t>(row) % (8 * B)) / B;
+    const int head = min((8 - past) % 8, cols), runs = (cols - head) / 8;
+    const Vec<8 * B> zero = {};
+#pragma unroll 4
+    for (int k = lane; k < runs; k += 32) st<8 * B>(p + head + k * 8, zero);
+    if (lane < head) p[lane] = 0;
+    if (head + runs * 8 + lane < cols) p[head + runs * 8 + lane] = 0;
+}
+
+// ---------------------------------------------------------------- sorts
+
+// Inclusive prefix sum over the block's threads; `scan` has a slot a warp.
+__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t *scan) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t u = __shfl_up_sync(kAllLanes, v, d);
+        v += lane >= d ? u : 0u;
+    }
+    if (lane == 31) scan[warp] = v;
+    __syncthreads();
+    uint32_t before = lane < warp ? scan[lane] : 0u;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) before += __shfl_xor_sync(kAllLanes, before, d);
+    return v + before;
+}
+
+// The lanes of `active` whose digit is this lane's: a ballot for each bit.  (A
+// match instruction takes about 64 cycles of the SM for 32 different digits,
+// ten ballots a quarter of that.)
+__device__ __forceinline__ unsigned lanes_alike(uint32_t digit, int bits, unsigned active) {
+    unsigned same = active;
+#pragma unroll 2
+    for (int b = 0; b < bits; ++b) {
+        const bool one = digit >> b & 1;
+        const unsigned ones = __ballot_sync(kAllLanes, one);
+        same &= one ? ones : ~ones;
+    }
+    return same;
+}
+
+// ---------------------------------------------------------------- host
+
 // 16-byte accesses (32-byte ones for binary32): the base and the stride of a
 // matrix are multiples of 8 elements.  Null matrices allow anything.
 template <int DT> inline bool wide_rows(const void *p, int64_t stride) {

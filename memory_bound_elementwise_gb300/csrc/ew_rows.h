@@ -173,6 +173,36 @@ int64_t embed_partial_bytes(int64_t rows, int64_t cols);
 cudaError_t launch_embed_grad(int dtype, int gtype, const EmbedGradArgs &a, int sms, cudaStream_t s,
                               LaunchInfo *info, int *launches);
 
+// ---------------------------------------------------------------- experts
+
+constexpr int kMostExperts = 1024;
+constexpr int kMostChoices = 64;  // experts a token
+
+struct ExpertSortArgs {
+    const void *experts;  // rows x k
+    int32_t *positions, *offsets, *counts, *slots;
+    uint32_t *partial;    // workspace: the blocks' counts
+    int64_t stride, rows, capacity;
+    int32_t k, n_experts, align, i64;
+};
+int64_t expert_sort_bytes(int64_t slots, int n_experts);
+cudaError_t launch_expert_sort(const ExpertSortArgs &a, cudaStream_t s, LaunchInfo *info, int *launches);
+
+// Dispatch: x by tokens, out by sorted rows.  Combine: x by sorted rows, residual
+// and out by tokens.  Combine's gradient: x is combine's (null where dweights is),
+// residual its output's gradient, out x's.
+struct ExpertRowsArgs {
+    const void *x, *residual, *weights;
+    const int32_t *positions, *slots;
+    void *out;
+    float *dweights;
+    int64_t x_stride, residual_stride, out_stride;
+    int64_t rows, sorted;  // tokens, and sorted rows
+    int32_t cols, k, wtype;
+};
+enum ExpertRows : int { EXPERT_DISPATCH = 0, EXPERT_COMBINE = 1, EXPERT_COMBINE_GRAD = 2 };
+cudaError_t launch_expert_rows(int what, int dtype, const ExpertRowsArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
+
 // ---------------------------------------------------------------- logits
 
 constexpr int kMostTop = 64;        // alternatives a row

@@ -196,6 +196,50 @@ ew_status distill_call(bool sums, bool grad, ew_dtype dt, ew_index itype, const 
     return EW_OK;
 }
 
+// Slots of tokens by expert: rows x k in range.
+bool slots_ok(int64_t rows, int64_t k) {
+    return size_ok(rows, 0) && k >= 1 && k <= kMostChoices && rows <= kMaxSize / k;
+}
+bool experts_ok(int64_t n_experts) { return n_experts >= 1 && n_experts <= kMostExperts; }
+constexpr int64_t kMostAlign = 65536;
+
+// The three calls that move rows between tokens (by_token) and sorted rows (by_expert).
+ew_status expert_rows_call(int what, ew_dtype dt, const Operand &by_token, const Operand &by_expert, const Operand &residual,
+                           const int32_t *positions, const int32_t *slots, ew_dtype wtype, const void *weights,
+                           float *dweights, const Operand &dy, int64_t rows, int64_t k, cudaStream_t s) {
+    const int64_t sorted = by_expert.rows, cols = by_expert.cols;
+    const bool combine = what == EXPERT_COMBINE, grad = what == EXPERT_COMBINE_GRAD;
+    const int64_t zeroed = combine ? 0 : sorted;  // rows that may be cleared
+    if (rows == 0 && zeroed == 0) return EW_OK;
+    const Operand place = vec(positions, rows * k, 4), slot = vec(slots, zeroed, 4);
+    const Operand weight = vec(weights, rows * k, wtype == EW_F32 ? 4 : bytes_of(dt), false);
+    ew_status st;
+    if (what == EXPERT_DISPATCH) {
+        const Operand in[3] = {by_token, place, slot}, out[1] = {by_expert};
+        st = check_all(in, 3, out, 1);
+    } else if (combine) {
+        const Operand in[4] = {residual, by_expert, place, weight}, out[1] = {by_token};
+        const bool in_place[1][2] = {{true, false}};
+        st = check_all(in, 4, out, 1, in_place);
+    } else {
+        const Operand in[5] = {by_token, by_expert, place, slot, weight}, out[2] = {dy, vec(dweights, rows * k, 4, false)};
+        st = check_all(in, 5, out, 2);
+    }
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    const Operand &from = what == EXPERT_DISPATCH ? by_token : by_expert, &add = grad ? by_token : residual;
+    const Operand &to = what == EXPERT_DISPATCH ? by_expert : combine ? by_token : dy;
+    const ExpertRowsArgs a{from.p, add.p, weights, positions, slots, const_cast<void *>(to.p), dweights, from.stride,
+                           add.stride, to.stride, rows, sorted, static_cast<int32_t>(cols), static_cast<int32_t>(k), wtype};
+    LaunchInfo info;
+    ce = launch_expert_rows(what, dt, a, sms, s, &info);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, 1);
+    return EW_OK;
+}
+
 // Rows of partial sums that the norm's backward may use: one for each row up to
 // 1280, which is more than its blocks.
 constexpr int64_t kNormPartials = 1280;
@@ -405,6 +449,80 @@ ew_status ew_layernorm_grad(ew_dtype dt, const void *dy, int64_t dy_stride, cons
     if (ce != cudaSuccess) return report_cuda(ce);
     record(info, launches);
     return EW_OK;
+}
+
+int64_t ew_expert_capacity(int64_t rows, int64_t k, int64_t n_experts, int64_t align) {
+    if (!slots_ok(rows, k) || !experts_ok(n_experts) || align < 1 || align > kMostAlign) return -1;
+    const int64_t slots = rows * k, most = (slots + std::min(n_experts, slots) * (align - 1)) / align * align;
+    return most <= kMaxSize ? most : -1;
+}
+
+int64_t ew_expert_sort_workspace(int64_t rows, int64_t k, int64_t n_experts) {
+    if (!slots_ok(rows, k) || !experts_ok(n_experts)) return -1;
+    return expert_sort_bytes(rows * k, static_cast<int>(n_experts));
+}
+
+ew_status ew_expert_sort(ew_index itype, const void *experts, int64_t experts_stride, int64_t n_experts, int64_t align,
+                         int32_t *positions, int32_t *offsets, int32_t *counts, int32_t *slots, int64_t capacity,
+                         int64_t rows, int64_t k, void *workspace, int64_t workspace_bytes, ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!index_type(itype)) return EW_ERR_UNSUPPORTED_DTYPE;
+    const int64_t least = ew_expert_capacity(rows, k, n_experts, align), need = ew_expert_sort_workspace(rows, k, n_experts);
+    if (least < 0 || capacity < least || capacity > kMaxSize || need < 0 || workspace_bytes < need ||
+        (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 256 != 0))
+        return EW_ERR_INVALID_VALUE;
+    const Operand in[1] = {{experts, rows, k, experts_stride, index_bytes(itype)}};
+    const Operand out[5] = {vec(positions, rows * k, 4), vec(offsets, n_experts + 1, 4), vec(counts, n_experts, 4),
+                            vec(slots, capacity, 4), vec(need > 0 ? workspace : nullptr, need / 4, 4)};
+    const ew_status st = check_all(in, 1, out, 5);
+    if (st != EW_OK) return st;
+    const ExpertSortArgs a{experts, positions, offsets, counts, slots, static_cast<uint32_t *>(workspace), experts_stride,
+                           rows, capacity, static_cast<int32_t>(k), static_cast<int32_t>(n_experts),
+                           static_cast<int32_t>(align), itype == EW_INDEX_I64};
+    LaunchInfo info;
+    int launches = 0;
+    const cudaError_t ce = launch_expert_sort(a, reinterpret_cast<cudaStream_t>(s), &info, &launches);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, launches);
+    return EW_OK;
+}
+
+ew_status ew_expert_dispatch(ew_dtype dt, const void *x, int64_t x_stride, const int32_t *positions, const int32_t *slots,
+                             void *out, int64_t out_stride, int64_t capacity, int64_t rows, int64_t k, int64_t cols,
+                             ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!slots_ok(rows, k) || !size_ok(cols, 1) || !size_ok(capacity, 0)) return EW_ERR_INVALID_VALUE;
+    const int e = bytes_of(dt);
+    return expert_rows_call(EXPERT_DISPATCH, dt, {x, rows, cols, x_stride, e}, {out, capacity, cols, out_stride, e}, Operand{},
+                            positions, slots, dt, nullptr, nullptr, Operand{}, rows, k, reinterpret_cast<cudaStream_t>(s));
+}
+
+ew_status ew_expert_combine(ew_dtype dt, const void *y, int64_t y_stride, int64_t capacity, const int32_t *positions,
+                            ew_dtype wtype, const void *weights, const void *residual, int64_t residual_stride, void *out,
+                            int64_t out_stride, int64_t rows, int64_t k, int64_t cols, ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || (weights != nullptr && wtype != dt && wtype != EW_F32)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!slots_ok(rows, k) || !size_ok(cols, 1) || !size_ok(capacity, 0)) return EW_ERR_INVALID_VALUE;
+    const int e = bytes_of(dt);
+    return expert_rows_call(EXPERT_COMBINE, dt, {out, rows, cols, out_stride, e}, {y, capacity, cols, y_stride, e},
+                            {residual, rows, cols, residual_stride, e, false}, positions, nullptr, wtype, weights, nullptr,
+                            Operand{}, rows, k, reinterpret_cast<cudaStream_t>(s));
+}
+
+ew_status ew_expert_combine_grad(ew_dtype dt, const void *dout, int64_t dout_stride, const void *y, int64_t y_stride,
+                                 int64_t capacity, const int32_t *positions, const int32_t *slots, ew_dtype wtype,
+                                 const void *weights, void *dy, int64_t dy_stride, float *dweights, int64_t rows,
+                                 int64_t k, int64_t cols, ew_stream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || (weights != nullptr && wtype != dt && wtype != EW_F32)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!slots_ok(rows, k) || !size_ok(cols, 1) || !size_ok(capacity, 0)) return EW_ERR_INVALID_VALUE;
+    const int e = bytes_of(dt);
+    const Operand read{dweights != nullptr ? y : nullptr, capacity, cols, dweights != nullptr ? y_stride : cols, e,
+                       dweights != nullptr};
+    return expert_rows_call(EXPERT_COMBINE_GRAD, dt, {dout, rows, cols, dout_stride, e}, read, Operand{}, positions, slots,
+                            wtype, weights, dweights, {dy, capacity, cols, dy_stride, e}, rows, k,
+                            reinterpret_cast<cudaStream_t>(s));
 }
 
 ew_status ew_logprob(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *tokens, float scale,

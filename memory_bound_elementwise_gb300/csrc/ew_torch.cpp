@@ -364,6 +364,108 @@ PyObject *layernorm_grad(PyObject *const *a) {  // dy, h, weight, mean, rstd, dh
     return tuple_of(dx, dweight, dbias);
 }
 
+// ---------------------------------------------------------------- experts
+
+PyObject *expert_sort(PyObject *const *a) {  // experts, n_experts, align
+    const Tensor &experts = tensor(a[0], "experts");
+    const Device d = device_of(experts, "experts");
+    const ew_index type = index_of(experts, "experts");
+    const Matrix m = matrix(experts, "experts", d);
+    const int64_t n_experts = integer(a[1]), align = integer(a[2]);
+    const int64_t capacity = ew_expert_capacity(m.rows, m.cols, n_experts, align);
+    const int64_t need = ew_expert_sort_workspace(m.rows, m.cols, n_experts);
+    if (capacity < 0 || need < 0) check_status(EW_ERR_INVALID_VALUE, "ew_expert_sort");
+    const Workspace work(need, "ew_expert_sort", d);
+    Output positions, offsets, counts, slots;
+    auto make = [&](Output &o, at::IntArrayRef sizes) { return static_cast<int32_t *>(o.make(sizes, at::kInt, d)); };
+    int32_t *p = make(positions, {m.rows, m.cols}), *o = make(offsets, {n_experts + 1}), *c = make(counts, {n_experts});
+    int32_t *s = make(slots, {capacity});
+    check_status(ew_expert_sort(type, m.p, m.stride, n_experts, align, p, o, c, s, capacity, m.rows, m.cols, work.p(),
+                                work.bytes, d.stream()),
+                 "ew_expert_sort");
+    return tuple_of(positions, offsets, counts, slots);
+}
+
+// What the calls take of a sort: positions (rows x k) and slots.
+struct Plan {
+    const int32_t *positions, *slots;
+    int64_t rows, k, capacity;
+    Plan(PyObject *o, Device d) {
+        if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 4) REFUSE(PyExc_TypeError, "plan: what ew_expert_sort returns");
+        const Tensor &p = tensor(PyTuple_GET_ITEM(o, 0), "positions"), &s = tensor(PyTuple_GET_ITEM(o, 3), "slots");
+        if (p.dim() != 2) REFUSE(PyExc_ValueError, "positions: expected tokens x experts");
+        rows = p.size(0);
+        k = p.size(1);
+        capacity = s.numel();
+        positions = static_cast<const int32_t *>(vector(p, "positions", rows * k, at::kInt, d));
+        slots = static_cast<const int32_t *>(vector(s, "slots", capacity, at::kInt, d));
+    }
+};
+Weight weights_of(PyObject *o, const Plan &plan, ew_dtype code, at::ScalarType type, Device d) {
+    return weight_of(o, plan.rows * plan.k, code, type, d, "weights");
+}
+
+PyObject *expert_dispatch(PyObject *const *a) {  // x, plan, out
+    const Tensor &x = tensor(a[0], "x");
+    const Device d = device_of(x, "x");
+    const ew_dtype code = code_of(x, "x");
+    const Matrix m = matrix(x, "x", d);
+    const Plan plan(a[1], d);
+    if (m.rows != plan.rows)
+        REFUSE(PyExc_ValueError, "x: expected %lld rows, got %lld", static_cast<long long>(plan.rows), static_cast<long long>(m.rows));
+    Output out;
+    const Matrix o = out.matrix(a[2], "out", {plan.capacity, m.cols}, plan.capacity, m.cols, x.scalar_type(), d);
+    check_status(ew_expert_dispatch(code, m.p, m.stride, plan.positions, plan.slots, o.p, o.stride, plan.capacity, plan.rows,
+                                    plan.k, m.cols, d.stream()),
+                 "ew_expert_dispatch");
+    return out.take();
+}
+
+PyObject *expert_combine(PyObject *const *a) {  // y, plan, weights, residual, out
+    const Tensor &y = tensor(a[0], "y");
+    const Device d = device_of(y, "y");
+    const ew_dtype code = code_of(y, "y");
+    const at::ScalarType type = y.scalar_type();
+    const Plan plan(a[1], d);
+    const Matrix m = matrix(y, "y", d);
+    if (m.rows != plan.capacity)
+        REFUSE(PyExc_ValueError, "y: expected %lld rows, got %lld", static_cast<long long>(plan.capacity), static_cast<long long>(m.rows));
+    const Weight w = weights_of(a[2], plan, code, type, d);
+    Matrix residual{nullptr, 0, 0, 0};
+    if (a[3] != Py_None) residual = matrix_like(tensor(a[3], "residual"), "residual", plan.rows, m.cols, type, d);
+    Output out;
+    const Matrix o = out.matrix(a[4], "out", {plan.rows, m.cols}, plan.rows, m.cols, type, d);
+    check_status(ew_expert_combine(code, m.p, m.stride, plan.capacity, plan.positions, w.type, w.p, residual.p, residual.stride,
+                                   o.p, o.stride, plan.rows, plan.k, m.cols, d.stream()),
+                 "ew_expert_combine");
+    return out.take();
+}
+
+PyObject *expert_combine_grad(PyObject *const *a) {  // dout, y, plan, weights, dy, dweights
+    const Tensor &dout = tensor(a[0], "dout");
+    const Device d = device_of(dout, "dout");
+    const ew_dtype code = code_of(dout, "dout");
+    const at::ScalarType type = dout.scalar_type();
+    const Plan plan(a[2], d);
+    const Matrix m = matrix(dout, "dout", d);
+    if (m.rows != plan.rows)
+        REFUSE(PyExc_ValueError, "dout: expected %lld rows, got %lld", static_cast<long long>(plan.rows), static_cast<long long>(m.rows));
+    const Matrix y = matrix_like(tensor(a[1], "y"), "y", plan.capacity, m.cols, type, d);
+    const Weight w = weights_of(a[3], plan, code, type, d);
+    Output dy, dweights;
+    const Matrix o = dy.matrix(a[4], "dy", {plan.capacity, m.cols}, plan.capacity, m.cols, type, d);
+    float *dw;
+    if (a[5] != Py_None) {
+        dw = dweights.floats(a[5], "dweights", plan.rows * plan.k, d);
+    } else {
+        dw = static_cast<float *>(dweights.make({plan.rows, plan.k}, at::kFloat, d));
+    }
+    check_status(ew_expert_combine_grad(code, m.p, m.stride, y.p, y.stride, plan.capacity, plan.positions, plan.slots, w.type,
+                                        w.p, o.p, o.stride, dw, plan.rows, plan.k, m.cols, d.stream()),
+                 "ew_expert_combine_grad");
+    return tuple_of(dy, dweights);
+}
+
 // ---------------------------------------------------------------- logits
 
 PyObject *logprob(PyObject *const *a) {  // logits, tokens, top, scale
@@ -507,7 +609,8 @@ PyObject *set_check(PyObject *, PyObject *fn) {
 
 PyMethodDef g_methods[] = {
     ENTRY(embed, 4), ENTRY(embed_grad, 6), ENTRY(rmsnorm, 7), ENTRY(rmsnorm_quant, 10), ENTRY(rmsnorm_grad, 7),
-    ENTRY(layernorm, 9), ENTRY(layernorm_grad, 9), ENTRY(logprob, 4), ENTRY(logprob_grad, 8), ENTRY(distill, 4), ENTRY(distill_grad, 7), ENTRY(distill_step, 6),
+    ENTRY(layernorm, 9), ENTRY(layernorm_grad, 9), ENTRY(expert_sort, 3), ENTRY(expert_dispatch, 3),
+    ENTRY(expert_combine, 5), ENTRY(expert_combine_grad, 6), ENTRY(logprob, 4), ENTRY(logprob_grad, 8), ENTRY(distill, 4), ENTRY(distill_grad, 7), ENTRY(distill_step, 6),
     {"set_check", set_check, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ew_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

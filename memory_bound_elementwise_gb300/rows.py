@@ -22,7 +22,7 @@ import os
 
 import torch
 
-from . import LIB_PATH, check, lib
+from . import ExpertPlan, LIB_PATH, check, lib
 
 
 def _load():
@@ -128,6 +128,49 @@ def ew_layernorm_grad(dy, h, weight, mean, rstd, dh=None, dx=None, dweight=None,
     if stream is not None:
         return _on(stream, ew_layernorm_grad, dy, h, weight, mean, rstd, dh, dx, dweight, dbias)
     return _C.layernorm_grad(dy, h, weight, mean, rstd, dh, dx, dweight, dbias)
+
+
+# ---------------------------------------------------------------- experts
+
+def ew_expert_sort(experts, n_experts, align=1, stream=None):
+    """Sorts tokens by expert; ``experts`` (int32 or int64) is tokens x k, k at most 64, of ``n_experts`` (at most 1024).
+
+    Returns ExpertPlan(positions, offsets, counts, slots), int32: the row of each token's experts
+    among the sorted rows (-1 where the id is outside [0, n_experts)), the first row of each expert
+    and the end of the last, the experts' counts, and for each sorted row token * k + j, or -1 where
+    it stands for none.  Each expert's rows begin at a multiple of ``align`` and keep the tokens'
+    order.  There are as many sorted rows as any choice of experts may need, whatever this one does."""
+    if stream is not None:
+        return _on(stream, ew_expert_sort, experts, n_experts, align)
+    return ExpertPlan._make(_C.expert_sort(experts, n_experts, align))
+
+
+def ew_expert_dispatch(x, plan, out=None, stream=None):
+    """The rows of x sorted by expert: out[plan.positions[t, j]] = x[t]; returns out.
+
+    Rows that stand for no token are zeros.  The gradient is ``ew_expert_combine(dout, plan)``."""
+    if stream is not None:
+        return _on(stream, ew_expert_dispatch, x, plan, out)
+    return _C.expert_dispatch(x, plan, out)
+
+
+def ew_expert_combine(y, plan, weights=None, residual=None, out=None, stream=None):
+    """out[t] = residual[t] + sum over j of weights[t, j] * y[plan.positions[t, j]]; returns out.
+
+    ``weights`` has y's dtype or float32 (None: ones).  Without a residual the sum begins at zero;
+    out may be residual."""
+    if stream is not None:
+        return _on(stream, ew_expert_combine, y, plan, weights, residual, out)
+    return _C.expert_combine(y, plan, weights, residual, out)
+
+
+def ew_expert_combine_grad(dout, y, plan, weights=None, dy=None, dweights=None, stream=None):
+    """Gradients of ew_expert_combine: returns (dy, dweights); the residual's is dout itself.
+
+    Rows of dy that stand for no token are zeros; dweights is float32, tokens x k."""
+    if stream is not None:
+        return _on(stream, ew_expert_combine_grad, dout, y, plan, weights, dy, dweights)
+    return _C.expert_combine_grad(dout, y, plan, weights, dy, dweights)
 
 
 # ---------------------------------------------------------------- logits

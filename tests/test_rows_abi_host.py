@@ -198,3 +198,79 @@ def test_layernorm_grad_refusals():
     assert layernorm_grad(rows=0, dw=None, db=None) == OK
     assert ew.lib().ew_layernorm_grad_workspace(-1, 64) == -1 and ew.lib().ew_layernorm_grad_workspace(4, BIG + 1) == -1
     assert ew.last_launch()["launches"] == 0
+
+
+def expert_sort(it=0, e=P, es=2, n=8, align=1, pos=P + MB, off=P + 2 * MB, cnt=P + 3 * MB, slots=P + 4 * MB, cap=8, rows=4, k=2,
+                work=None, size=0):
+    return ew.lib().ew_expert_sort(it, e, es, n, align, pos, off, cnt, slots, cap, rows, k, work, size, None)
+
+
+def dispatch(dt=2, x=P, xs=64, pos=P + MB, slots=P + 2 * MB, out=P + 3 * MB, os_=64, cap=8, rows=4, k=2, cols=64):
+    return ew.lib().ew_expert_dispatch(dt, x, xs, pos, slots, out, os_, cap, rows, k, cols, None)
+
+
+def combine(dt=2, y=P, ys=64, cap=8, pos=P + MB, wt=0, w=P + 2 * MB, r=P + 3 * MB, rs=64, out=P + 4 * MB, os_=64, rows=4, k=2,
+            cols=64):
+    return ew.lib().ew_expert_combine(dt, y, ys, cap, pos, wt, w, r, rs, out, os_, rows, k, cols, None)
+
+
+def combine_grad(dt=2, dout=P, ds=64, y=P + MB, ys=64, cap=8, pos=P + 2 * MB, slots=P + 3 * MB, wt=0, w=P + 4 * MB,
+                 dy=P + 5 * MB, dys=64, dw=P + 6 * MB, rows=4, k=2, cols=64):
+    return ew.lib().ew_expert_combine_grad(dt, dout, ds, y, ys, cap, pos, slots, wt, w, dy, dys, dw, rows, k, cols, None)
+
+
+def test_expert_capacity():
+    cap = ew.lib().ew_expert_capacity
+    assert cap(4, 2, 8, 1) == 8 and cap(0, 2, 8, 16) == 0
+    assert cap(1, 8, 256, 128) == 8 * 128          # eight experts of one slot each
+    assert cap(100, 1, 3, 8) == (100 + 3 * 7) // 8 * 8
+    for bad in ((-1, 2, 8, 1), (4, 0, 8, 1), (4, 65, 8, 1), (4, 2, 0, 1), (4, 2, 1025, 1), (4, 2, 8, 0), (4, 2, 8, 65537),
+                (BIG // 2 + 1, 2, 8, 1), (BIG // 2, 2, 8, 2), (BIG + 1, 1, 8, 1)):
+        assert cap(*bad) == -1, bad
+    # whatever the choices are, the rows suffice: the fullest case by brute force
+    for rows, n, align in ((5, 3, 4), (7, 2, 3), (2, 6, 5)):
+        most = max(sum(-(-c // align) * align for c in split) for split in splits(rows, n))
+        assert cap(rows, 1, n, align) >= most and cap(rows, 1, n, align) - most < align
+
+
+def splits(total, parts):
+    if parts == 1:
+        yield (total,)
+        return
+    for first in range(total + 1):
+        for rest in splits(total - first, parts - 1):
+            yield (first, *rest)
+
+
+def test_expert_sort_refusals():
+    assert expert_sort(it=2) == DTYPE and expert_sort(k=65) == INVALID and expert_sort(n=1025) == INVALID
+    assert expert_sort(cap=7) == INVALID and expert_sort(cap=BIG + 1) == INVALID and expert_sort(align=2) == INVALID
+    assert expert_sort(es=1) == INVALID and expert_sort(e=P + 2) == INVALID and expert_sort(rows=-1) == INVALID
+    for name in ("e", "pos", "off", "cnt", "slots"):
+        assert expert_sort(**{name: None}) == NULLP, name
+    assert expert_sort(pos=P) == OVERLAP and expert_sort(cnt=P + 2 * MB + 32) == OVERLAP
+    need = ew.lib().ew_expert_sort_workspace
+    assert need(4, 2, 8) == 0 and need(-1, 2, 8) == -1 and need(4, 2, 1025) == -1
+    big = need(100000, 2, 8)
+    assert big > 0
+    args = dict(rows=100000, cap=200000, n=8, e=P, pos=P + 8 * MB, slots=P + 16 * MB, off=P + 32 * MB, cnt=P + 33 * MB)
+    assert expert_sort(**args, size=big - 1, work=P + 40 * MB) == INVALID and expert_sort(**args, size=big) == NULLP
+    assert expert_sort(**args, size=big, work=P + 40 * MB + 64) == INVALID and expert_sort(**args, size=big, work=P + 33 * MB) == OVERLAP
+    assert ew.last_launch()["launches"] == 0
+
+
+def test_expert_rows_refusals():
+    for call, names in ((dispatch, ("x", "pos", "slots", "out")), (combine, ("y", "pos", "out")),
+                        (combine_grad, ("dout", "y", "pos", "slots", "dy"))):
+        assert call(dt=3) == DTYPE and call(k=0) == INVALID and call(k=65) == INVALID and call(cols=0) == INVALID
+        assert call(rows=-1) == INVALID and call(cap=-1) == INVALID and call(cap=BIG + 1) == INVALID
+        for name in names:
+            assert call(**{name: None}) == NULLP, (call.__name__, name)
+        assert call(pos=P + MB // 2 + 2) == INVALID
+    assert dispatch(rows=0, cap=0) == OK and combine(rows=0) == OK and combine_grad(rows=0, cap=0) == OK
+    assert combine(wt=1) == DTYPE and combine_grad(wt=1) == DTYPE
+    assert dispatch(xs=63) == INVALID and combine(rs=63) == INVALID and combine_grad(dys=63) == INVALID
+    assert dispatch(out=P) == OVERLAP and combine(out=P) == OVERLAP and combine(out=P + 3 * MB, os_=128) == OVERLAP
+    assert combine_grad(dy=P + MB) == OVERLAP and combine_grad(dy=P) == OVERLAP and combine_grad(dw=P + 4 * MB) == OVERLAP
+    assert combine_grad(dw=None, y=None, dy=P) == OVERLAP
+    assert ew.last_launch()["launches"] == 0
