@@ -503,6 +503,40 @@ EW_API ew_status ew_distill_step(ew_dtype dtype, ew_index itype, const void *log
                                  int64_t k, float scale, const float *dloss, float *loss, float *lse, void *dlogits,
                                  int64_t dstride, int64_t rows, int64_t cols, ew_stream_t stream);
 
+/* The clipped policy loss with a divergence term, and its gradient.  Per row with a
+ * token in [0, cols), its log probability under softmax(scale * logits) being logp:
+ *     ratio   = exp(logp - old_logp), or 1 where old_logp is NULL
+ *     gain    = min(ratio * advantage, clip(ratio, 1 - clip_low, 1 + clip_high) * advantage)
+ *     apart   = ref_logp - logp
+ *     loss    = -gain + kl * (exp(apart) - apart - 1)
+ *     slope   = -(ratio * advantage where the minimum is that, else 0) + kl * (1 - exp(apart))
+ *     dlogits = dloss * slope * scale * (1_token - p)
+ * advantage, old_logp, ref_logp, dloss: binary32, one a row.  ref_logp may be NULL; with
+ * it NULL or kl 0 the terms with apart are left out.  0 <= clip_low <= 1, clip_high >= 0
+ * (infinity: not clipped above), 0 <= kl < infinity, 2^-20 <= scale <= 2^20.  An
+ * advantage of 0 has gain and slope 0, a dloss of 0 gradient 0.  A row without a token has loss, logp and lse 0
+ * and gradient 0, and its logits are not read.  Masked logits have p = 0; a token
+ * there has logp -inf, and with kl an infinite loss.  A row of -inf alone has lse
+ * and logp -inf and gradient 0, a row with NaN or +inf NaN in all its results.
+ * ew_policy computes loss, logp and lse (the last two may be NULL), ew_policy_grad
+ * dlogits from its logp and lse (with the precision that ew_logprob_grad states),
+ * ew_policy_step all of it in one pass over the rows where dloss is known
+ * beforehand.  dlogits may be logits (the same base and stride). */
+EW_API ew_status ew_policy(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride, const void *tokens,
+                           const float *advantage, const float *old_logp, const float *ref_logp, float clip_low,
+                           float clip_high, float kl, float scale, float *loss, float *logp, float *lse, int64_t rows,
+                           int64_t cols, ew_stream_t stream);
+EW_API ew_status ew_policy_grad(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride, const void *tokens,
+                                const float *advantage, const float *old_logp, const float *ref_logp, float clip_low,
+                                float clip_high, float kl, float scale, const float *logp, const float *lse,
+                                const float *dloss, void *dlogits, int64_t dstride, int64_t rows, int64_t cols,
+                                ew_stream_t stream);
+EW_API ew_status ew_policy_step(ew_dtype dtype, ew_index itype, const void *logits, int64_t stride, const void *tokens,
+                                const float *advantage, const float *old_logp, const float *ref_logp, float clip_low,
+                                float clip_high, float kl, float scale, const float *dloss, float *loss, float *logp,
+                                float *lse, void *dlogits, int64_t dstride, int64_t rows, int64_t cols,
+                                ew_stream_t stream);
+
 /* ---- variant selection and introspection ------------------------------ */
 
 /* Select the kernel variant for later calls in this process (EW_PATH_AUTO

@@ -30,6 +30,7 @@ Row operators (matrices, one row at a time; ``rows.py``)::
     ew_logprob(logits, tokens, top) log probabilities, entropy, lse and top alternatives
     ew_logprob_grad(...)            their gradient
     ew_distill(logits, ids, teacher)(loss, lse); ew_distill_grad, ew_distill_step
+    ew_policy(logits, tokens, advantage, ...)  (loss, logp, lse); ew_policy_grad, ew_policy_step
 
 Tensors must be contiguous CUDA tensors of dtype float32, float16 or bfloat16
 (int32 for ew_select_even_odd, ew_copy and ew_gather_stride) on the current
@@ -71,12 +72,14 @@ EXPORTS = ("ew_add", "ew_saxpy", "ew_relu", "ew_add_relu", "ew_saxpy_relu", "ew_
            "ew_layernorm", "ew_layernorm_grad", "ew_layernorm_grad_workspace",
            "ew_expert_capacity", "ew_expert_sort", "ew_expert_sort_workspace", "ew_expert_dispatch", "ew_expert_combine",
            "ew_expert_combine_grad",
-           "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
+           "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step",
+           "ew_policy", "ew_policy_grad", "ew_policy_step")
 
 # Row operators (rows.py), loaded with torch at their first use.
 _ROW_OPERATORS = ("ew_embed", "ew_embed_grad", "ew_rmsnorm", "ew_rmsnorm_quant", "ew_rmsnorm_grad",
                   "ew_layernorm", "ew_layernorm_grad", "ew_expert_sort", "ew_expert_dispatch", "ew_expert_combine",
-                  "ew_expert_combine_grad", "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step")
+                  "ew_expert_combine_grad", "ew_logprob", "ew_logprob_grad", "ew_distill", "ew_distill_grad", "ew_distill_step",
+                  "ew_policy", "ew_policy_grad", "ew_policy_step")
 # Their C arguments: i enum, l int64, f float, p pointer.
 _ROW_SIGNATURES = {
     "ew_embed": "iipllpfplllp",
@@ -100,6 +103,9 @@ _ROW_SIGNATURES = {
     "ew_distill": "iiplplipllfppllp",
     "ew_distill_grad": "iiplplipllfppplllp",
     "ew_distill_step": "iiplplipllfpppplllp",
+    "ew_policy": "iiplppppffffpppllp",
+    "ew_policy_grad": "iiplppppffffpppplllp",
+    "ew_policy_step": "iiplppppffffppppplllp",
 }
 
 # What ew_expert_sort returns and the other ew_expert_* functions take.

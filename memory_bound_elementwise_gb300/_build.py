@@ -31,7 +31,8 @@ SOURCES = ["ew_api.cu", "ew_kernels_f32.cu", "ew_kernels_f16.cu", "ew_kernels_bf
            "ew_norm_f32.cu", "ew_norm_f16.cu", "ew_norm_bf16.cu",
            "ew_layernorm_f32.cu", "ew_layernorm_f16.cu", "ew_layernorm_bf16.cu",
            "ew_logits_f32.cu", "ew_logits_f16.cu", "ew_logits_bf16.cu",
-           "ew_distill_f32.cu", "ew_distill_f16.cu", "ew_distill_bf16.cu"]
+           "ew_distill_f32.cu", "ew_distill_f16.cu", "ew_distill_bf16.cu",
+           "ew_policy_f32.cu", "ew_policy_f16.cu", "ew_policy_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "-ftz=false", "-prec-div=true", "-prec-sqrt=true", "-fmad=false",
@@ -48,7 +49,8 @@ def nvcc():
     raise RuntimeError("nvcc not found")
 
 
-ROW_OPERATORS = ("ew_rows", "ew_embed", "ew_norm", "ew_layernorm", "ew_expert", "ew_logits", "ew_distill")  # what their sources' names begin with
+ROW_OPERATORS = ("ew_rows", "ew_embed", "ew_norm", "ew_layernorm", "ew_expert", "ew_logits", "ew_distill",
+                 "ew_policy")  # what their sources' names begin with
 
 
 def _kernel_digest(skip=()):

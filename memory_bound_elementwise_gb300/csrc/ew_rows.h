@@ -234,6 +234,21 @@ struct DistillArgs {
     int32_t cols, i64, teacher_f32, k;
     float scale;
 };
+struct PolicyArgs {
+    const void *logits, *tokens;
+    const float *advantage, *old_logp, *ref_logp;  // the last two null where not given
+    const float *logp, *lse;                       // inputs of the gradient alone
+    const float *dloss;
+    float *loss, *logp_out, *lse_out;              // the last two null where not wanted
+    void *dlogits;
+    int64_t stride, dstride, rows;
+    int32_t cols, i64;
+    float least, most;  // of the ratio, where it is clipped
+    float kl, scale;
+};
+cudaError_t policy_f32(const PolicyArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t policy_f16(const PolicyArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info);
+cudaError_t policy_bf16(const PolicyArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info);
 // sums: the loss and lse are computed; grad: dlogits is.
 cudaError_t logprob_f32(const LogprobArgs &a, int sms, cudaStream_t s, LaunchInfo *info);
 cudaError_t logprob_grad_f32(const LogprobGradArgs &a, cudaStream_t s, LaunchInfo *info);

@@ -196,6 +196,47 @@ ew_status distill_call(bool sums, bool grad, ew_dtype dt, ew_index itype, const 
     return EW_OK;
 }
 
+// The three calls of the policy loss: sums (loss, logp and lse) and grad (dlogits).
+ew_status policy_call(bool sums, bool grad, ew_dtype dt, ew_index itype, PolicyArgs a, int64_t cols, float clip_low,
+                      float clip_high, cudaStream_t s) {
+    launch_record() = ew_launch_record{};
+    if (!float_type(dt) || !index_type(itype)) return EW_ERR_UNSUPPORTED_DTYPE;
+    if (!size_ok(a.rows, 0) || !size_ok(cols, 1) || !scale_ok(a.scale) || !(clip_low >= 0.0f && clip_low <= 1.0f) ||
+        !(clip_high >= 0.0f) || !(a.kl >= 0.0f) || std::isinf(a.kl))
+        return EW_ERR_INVALID_VALUE;
+    if (a.rows == 0) return EW_OK;
+    const int64_t rows = a.rows;
+    const int e = bytes_of(dt);
+    const Operand in[8] = {{a.logits, rows, cols, a.stride, e},
+                           vec(a.tokens, rows, index_bytes(itype)),
+                           vec(a.advantage, rows, 4),
+                           vec(a.old_logp, rows, 4, false),
+                           vec(a.ref_logp, rows, 4, false),
+                           vec(a.logp, rows, 4, !sums),
+                           vec(a.lse, rows, 4, !sums),
+                           vec(a.dloss, rows, 4, grad)};
+    const Operand out[4] = {{a.dlogits, grad ? rows : 0, cols, grad ? a.dstride : cols, e},
+                            vec(a.loss, rows, 4, sums),
+                            vec(a.logp_out, rows, 4, false),
+                            vec(a.lse_out, rows, 4, false)};
+    const bool in_place[4][2] = {{true, false}, {false, false}, {false, false}, {false, false}};
+    const ew_status st = check_all(in, 8, out, 4, in_place);
+    if (st != EW_OK) return st;
+    int sms = 0;
+    cudaError_t ce = current_sms(&sms);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    a.cols = static_cast<int32_t>(cols);
+    a.i64 = itype == EW_INDEX_I64;
+    a.least = 1.0f - clip_low;
+    a.most = 1.0f + clip_high;
+    if (a.kl == 0.0f) a.ref_logp = nullptr;  // no term: nothing is multiplied by 0
+    LaunchInfo info;
+    ce = (dt == EW_F32 ? policy_f32 : dt == EW_F16 ? policy_f16 : policy_bf16)(a, sums, grad, sms, s, &info);
+    if (ce != cudaSuccess) return report_cuda(ce);
+    record(info, 1);
+    return EW_OK;
+}
+
 // Slots of tokens by expert: rows x k in range.
 bool slots_ok(int64_t rows, int64_t k) {
     return size_ok(rows, 0) && k >= 1 && k <= kMostChoices && rows <= kMaxSize / k;
@@ -602,6 +643,32 @@ ew_status ew_distill_step(ew_dtype dt, ew_index itype, const void *logits, int64
                           int64_t rows, int64_t cols, ew_stream_t s) {
     return distill_call(true, true, dt, itype, logits, stride, ids, ids_stride, ttype, teacher, teacher_stride, k,
                         scale, dloss, loss, lse, dlogits, dstride, rows, cols, reinterpret_cast<cudaStream_t>(s));
+}
+
+ew_status ew_policy(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *tokens,
+                    const float *advantage, const float *old_logp, const float *ref_logp, float clip_low, float clip_high,
+                    float kl, float scale, float *loss, float *logp, float *lse, int64_t rows, int64_t cols, ew_stream_t s) {
+    const PolicyArgs a{logits, tokens, advantage, old_logp, ref_logp, nullptr, nullptr, nullptr, loss, logp, lse, nullptr,
+                       stride, 0, rows, 0, 0, 0.0f, 0.0f, kl, scale};
+    return policy_call(true, false, dt, itype, a, cols, clip_low, clip_high, reinterpret_cast<cudaStream_t>(s));
+}
+
+ew_status ew_policy_grad(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *tokens,
+                         const float *advantage, const float *old_logp, const float *ref_logp, float clip_low,
+                         float clip_high, float kl, float scale, const float *logp, const float *lse, const float *dloss,
+                         void *dlogits, int64_t dstride, int64_t rows, int64_t cols, ew_stream_t s) {
+    const PolicyArgs a{logits, tokens, advantage, old_logp, ref_logp, logp, lse, dloss, nullptr, nullptr, nullptr, dlogits,
+                       stride, dstride, rows, 0, 0, 0.0f, 0.0f, kl, scale};
+    return policy_call(false, true, dt, itype, a, cols, clip_low, clip_high, reinterpret_cast<cudaStream_t>(s));
+}
+
+ew_status ew_policy_step(ew_dtype dt, ew_index itype, const void *logits, int64_t stride, const void *tokens,
+                         const float *advantage, const float *old_logp, const float *ref_logp, float clip_low,
+                         float clip_high, float kl, float scale, const float *dloss, float *loss, float *logp, float *lse,
+                         void *dlogits, int64_t dstride, int64_t rows, int64_t cols, ew_stream_t s) {
+    const PolicyArgs a{logits, tokens, advantage, old_logp, ref_logp, nullptr, nullptr, dloss, loss, logp, lse, dlogits,
+                       stride, dstride, rows, 0, 0, 0.0f, 0.0f, kl, scale};
+    return policy_call(true, true, dt, itype, a, cols, clip_low, clip_high, reinterpret_cast<cudaStream_t>(s));
 }
 
 }  // extern "C"

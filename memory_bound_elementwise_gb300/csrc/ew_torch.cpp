@@ -579,6 +579,64 @@ PyObject *distill_step(PyObject *const *a) {  // logits, ids, teacher, dloss, sc
     return tuple_of(loss, lse, out);
 }
 
+// What the three calls of the policy loss take: logits, tokens, advantage, old_logp, ref_logp, clip_low, clip_high, kl, scale.
+struct PolicyCall {
+    const Tensor &logits;
+    Device d;
+    ew_dtype code;
+    Matrix m;
+    Ids tokens;
+    const float *advantage, *old_logp = nullptr, *ref_logp = nullptr;
+    float clip_low, clip_high, kl, scale;
+    explicit PolicyCall(PyObject *const *a)
+        : logits(tensor(a[0], "logits")), d(device_of(logits, "logits")), code(code_of(logits, "logits")),
+          m(matrix(logits, "logits", d)), tokens(ids_of(a[1], "tokens", m.rows, d)),
+          advantage(floats(a[2], "advantage", m.rows, d)), clip_low(static_cast<float>(number(a[5]))),
+          clip_high(static_cast<float>(number(a[6]))), kl(static_cast<float>(number(a[7]))),
+          scale(static_cast<float>(number(a[8]))) {
+        if (a[3] != Py_None) old_logp = floats(a[3], "old_logp", m.rows, d);
+        if (a[4] != Py_None) ref_logp = floats(a[4], "ref_logp", m.rows, d);
+    }
+};
+
+PyObject *policy(PyObject *const *a) {  // what PolicyCall takes
+    const PolicyCall c(a);
+    Output loss, logp, lse;
+    float *loss_p = loss.floats(Py_None, "loss", c.m.rows, c.d), *logp_p = logp.floats(Py_None, "logp", c.m.rows, c.d);
+    float *lse_p = lse.floats(Py_None, "lse", c.m.rows, c.d);
+    check_status(ew_policy(c.code, c.tokens.type, c.m.p, c.m.stride, c.tokens.p, c.advantage, c.old_logp, c.ref_logp, c.clip_low,
+                           c.clip_high, c.kl, c.scale, loss_p, logp_p, lse_p, c.m.rows, c.m.cols, c.d.stream()),
+                 "ew_policy");
+    return tuple_of(loss, logp, lse);
+}
+
+PyObject *policy_grad(PyObject *const *a) {  // what PolicyCall takes, logp, lse, dloss, dlogits
+    const PolicyCall c(a);
+    const float *logp = floats(a[9], "logp", c.m.rows, c.d), *lse = floats(a[10], "lse", c.m.rows, c.d);
+    const float *dloss = floats(a[11], "dloss", c.m.rows, c.d);
+    Output out;
+    const Matrix o = out.matrix(a[12], "dlogits", c.logits.sizes(), c.m.rows, c.m.cols, c.logits.scalar_type(), c.d);
+    check_status(ew_policy_grad(c.code, c.tokens.type, c.m.p, c.m.stride, c.tokens.p, c.advantage, c.old_logp, c.ref_logp,
+                                c.clip_low, c.clip_high, c.kl, c.scale, logp, lse, dloss, o.p, o.stride, c.m.rows, c.m.cols,
+                                c.d.stream()),
+                 "ew_policy_grad");
+    return out.take();
+}
+
+PyObject *policy_step(PyObject *const *a) {  // what PolicyCall takes, dloss, dlogits
+    const PolicyCall c(a);
+    const float *dloss = floats(a[9], "dloss", c.m.rows, c.d);
+    Output loss, logp, lse, out;
+    const Matrix o = out.matrix(a[10], "dlogits", c.logits.sizes(), c.m.rows, c.m.cols, c.logits.scalar_type(), c.d);
+    float *loss_p = loss.floats(Py_None, "loss", c.m.rows, c.d), *logp_p = logp.floats(Py_None, "logp", c.m.rows, c.d);
+    float *lse_p = lse.floats(Py_None, "lse", c.m.rows, c.d);
+    check_status(ew_policy_step(c.code, c.tokens.type, c.m.p, c.m.stride, c.tokens.p, c.advantage, c.old_logp, c.ref_logp,
+                                c.clip_low, c.clip_high, c.kl, c.scale, dloss, loss_p, logp_p, lse_p, o.p, o.stride, c.m.rows,
+                                c.m.cols, c.d.stream()),
+                 "ew_policy_step");
+    return tuple_of(loss, logp, lse, out);
+}
+
 // ---------------------------------------------------------------- module
 
 // A function of N positional arguments; C++ exceptions become Python's.
@@ -611,6 +669,7 @@ PyMethodDef g_methods[] = {
     ENTRY(embed, 4), ENTRY(embed_grad, 6), ENTRY(rmsnorm, 7), ENTRY(rmsnorm_quant, 10), ENTRY(rmsnorm_grad, 7),
     ENTRY(layernorm, 9), ENTRY(layernorm_grad, 9), ENTRY(expert_sort, 3), ENTRY(expert_dispatch, 3),
     ENTRY(expert_combine, 5), ENTRY(expert_combine_grad, 6), ENTRY(logprob, 4), ENTRY(logprob_grad, 8), ENTRY(distill, 4), ENTRY(distill_grad, 7), ENTRY(distill_step, 6),
+    ENTRY(policy, 9), ENTRY(policy_grad, 13), ENTRY(policy_step, 11),
     {"set_check", set_check, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ew_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

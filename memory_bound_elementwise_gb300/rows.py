@@ -224,3 +224,37 @@ def ew_distill_step(logits, ids, teacher, dloss, scale=1.0, dlogits=None, stream
     if stream is not None:
         return _on(stream, ew_distill_step, logits, ids, teacher, dloss, scale, dlogits)
     return _C.distill_step(logits, ids, teacher, dloss, scale, dlogits)
+
+
+def ew_policy(logits, tokens, advantage, old_logp=None, ref_logp=None, clip_low=0.2, clip_high=0.2, kl=0.0, scale=1.0,
+              stream=None):
+    """The clipped policy loss with a divergence term: returns (loss, logp, lse), float32, one a row.
+
+    With ratio = exp(logp - old_logp), logp being the token's log probability under
+    softmax(scale * logits) (ratio 1 where ``old_logp`` is None), and apart = ref_logp - logp:
+    loss = -min(ratio * advantage, clip(ratio, 1 - clip_low, 1 + clip_high) * advantage)
+    + kl * (exp(apart) - apart - 1).  A token outside the row (such as -1) has loss, logp
+    and lse 0, and the row is not read."""
+    if stream is not None:
+        return _on(stream, ew_policy, logits, tokens, advantage, old_logp, ref_logp, clip_low, clip_high, kl, scale)
+    return _C.policy(logits, tokens, advantage, old_logp, ref_logp, clip_low, clip_high, kl, scale)
+
+
+def ew_policy_grad(logits, tokens, advantage, logp, lse, dloss, old_logp=None, ref_logp=None, clip_low=0.2, clip_high=0.2,
+                   kl=0.0, scale=1.0, dlogits=None, stream=None):
+    """Gradient of ew_policy's loss (times dloss, float32, one a row) with respect to the logits, from its logp and lse;
+    returns dlogits, which may be logits.  Where a ratio lies on the border of the clipping, it is not clipped."""
+    if stream is not None:
+        return _on(stream, ew_policy_grad, logits, tokens, advantage, logp, lse, dloss, old_logp, ref_logp, clip_low,
+                   clip_high, kl, scale, dlogits)
+    return _C.policy_grad(logits, tokens, advantage, old_logp, ref_logp, clip_low, clip_high, kl, scale, logp, lse, dloss,
+                          dlogits)
+
+
+def ew_policy_step(logits, tokens, advantage, dloss, old_logp=None, ref_logp=None, clip_low=0.2, clip_high=0.2, kl=0.0,
+                   scale=1.0, dlogits=None, stream=None):
+    """ew_policy and ew_policy_grad in one call, where dloss is known beforehand; returns (loss, logp, lse, dlogits)."""
+    if stream is not None:
+        return _on(stream, ew_policy_step, logits, tokens, advantage, dloss, old_logp, ref_logp, clip_low, clip_high, kl,
+                   scale, dlogits)
+    return _C.policy_step(logits, tokens, advantage, old_logp, ref_logp, clip_low, clip_high, kl, scale, dloss, dlogits)

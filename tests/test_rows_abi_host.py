@@ -274,3 +274,31 @@ def test_expert_rows_refusals():
     assert combine_grad(dy=P + MB) == OVERLAP and combine_grad(dy=P) == OVERLAP and combine_grad(dw=P + 4 * MB) == OVERLAP
     assert combine_grad(dw=None, y=None, dy=P) == OVERLAP
     assert ew.last_launch()["launches"] == 0
+
+
+def policy_step(dt=2, it=1, x=P, s=64, tok=P + MB, adv=P + 2 * MB, old=P + 3 * MB, ref=P + 4 * MB, low=0.2, high=0.2, kl=0.1,
+                scale=1.0, dloss=P + 5 * MB, loss=P + 6 * MB, lp=P + 7 * MB, lse=P + 8 * MB, d=P + 9 * MB, ds=64, rows=4, cols=64):
+    return ew.lib().ew_policy_step(dt, it, x, s, tok, adv, old, ref, low, high, kl, scale, dloss, loss, lp, lse, d, ds, rows,
+                                   cols, None)
+
+
+def test_policy_refusals():
+    assert policy_step(dt=3) == DTYPE and policy_step(it=2) == DTYPE
+    assert policy_step(rows=-1) == INVALID and policy_step(cols=0) == INVALID and policy_step(s=63) == INVALID
+    nan, inf = float("nan"), float("inf")
+    for how in (dict(low=-0.1), dict(low=1.5), dict(low=nan), dict(high=-1e-9), dict(high=nan), dict(kl=-1.0), dict(kl=inf),
+                dict(kl=nan), dict(scale=0.0), dict(scale=2.0 ** 21), dict(scale=nan)):
+        assert policy_step(**how) == INVALID, how
+    for name in ("x", "tok", "adv", "dloss", "loss", "d"):
+        assert policy_step(**{name: None}) == NULLP, name
+    assert policy_step(tok=P + MB + 4) == INVALID and policy_step(lse=P + 2) == INVALID and policy_step(ds=10) == INVALID
+    assert policy_step(d=P + 2) == OVERLAP and policy_step(d=P, ds=128) == OVERLAP and policy_step(loss=P) == OVERLAP
+    assert policy_step(lp=P + 8 * MB) == OVERLAP and policy_step(lse=P + 2 * MB) == OVERLAP
+    assert policy_step(rows=0, x=None, high=inf) == OK
+    L = ew.lib()
+    args = (P, 64, P + MB, P + 2 * MB, None, None, 0.2, 0.2, 0.0, 1.0)
+    assert L.ew_policy(2, 1, *args, None, None, None, 4, 64, None) == NULLP
+    assert L.ew_policy_grad(2, 1, *args, None, P + 3 * MB, P + 4 * MB, P + 5 * MB, 64, 4, 64, None) == NULLP
+    assert L.ew_policy_grad(2, 1, *args, P + 3 * MB, None, P + 4 * MB, P + 5 * MB, 64, 4, 64, None) == NULLP
+    assert L.ew_policy_grad(2, 1, *args, P + 6 * MB, P + 3 * MB, P + 4 * MB, P + 3 * MB, 64, 4, 64, None) == OVERLAP
+    assert ew.last_launch()["launches"] == 0
