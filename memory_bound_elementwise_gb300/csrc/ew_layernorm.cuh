@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && RUNS && KT * ElemOf
 // dy n and dy in registers; each writes them once, to its own row of `partial`,
 // and column_sums_kernel adds those rows in order.
 
-// Matrices whose rows lie apart, element by element.
+// Matrices whose rows lie apart, element by element: slower, for the views that
+// need it.
 template <int DT, int KT> __global__ void __launch_bounds__(512) layernorm_grad_kernel(LayerNormGradArgs a) {
     enter_grid();
     __shared__ float2 part[2][32];
@@ -322,6 +323,266 @@ template <int DT, int KT> __global__ void __launch_bounds__(512) layernorm_grad_
                 out_b[col] = (j & 1) ? db[k][j / 2].y : db[k][j / 2].x;
             }
         }
+}
+
+// Matrices whose rows lie alike, their loads as asynchronous copies of 16 bytes
+// into a ring of `depth` rows in shared memory: rows on their way take no
+// registers.  Each thread copies and reads its own elements alone, waits for its
+// own copies and needs no barrier for them.  P pieces of 16 bytes hold a lane's 8
+// elements of a tile: of binary32 the two are 128 columns apart, so that a copy of
+// the warp takes whole sectors.  Rows that start anywhere: a writer's rows are a
+// multiple of 8 apart and so start at one place between multiples of 16 bytes, and
+// the columns that a thread holds, and sums, stay the same.  A row's first piece
+// begins `past` elements before the row, in the row before it or the gap there, and
+// what it brings along is cleared; only before the first row nothing is read.
+// KT = 4 has no registers left for the weights and reads them for each row.
+template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __grid_constant__ LayerNormGradArgs a, int depth) {
+    enter_grid();
+    using T = typename ElemOf<DT>::type;
+    constexpr int B = ElemOf<DT>::kBytes, P = B / 2, E = 16 / B;
+    constexpr bool kHeld = KT < 4;
+    extern __shared__ uint4 ring[];  // [row][dy, h, dh][tile][piece][thread]
+    __shared__ alignas(16) float2 parts[4][2][16];  // of a row and the next: the warps' sums, zeros beyond
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int threads = blockDim.x * blockDim.y, slot_size = 3 * KT * P * threads;
+    uint4 *const mine = ring + threadIdx.y * blockDim.x + threadIdx.x;
+    const int64_t writer = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    const int64_t writers = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    const int past = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row_of<DT>(a.dy, writer, a.dy_stride)) % 16) / B;
+    auto col = [&](int k, int piece) { return (warp + k * warps) * kTileCols + piece * 128 + lane * E - past; };
+    auto place = [&](int slot, int matrix, int k, int piece) {
+        return mine + slot * slot_size + ((matrix * KT + k) * P + piece) * threads;
+    };
+    // columns of the weight, in the layout of the pieces
+    auto weights = [&](int k, float2 (&w)[4]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = P == 2 ? col(k, j / 4) + j % 4 : col(k, 0) + j;
+            float v = 1.0f;
+            if (a.weight != nullptr) {
+                v = 0.0f;
+                if (c >= 0 && c < a.cols)
+                    v = DT == DT_F32 || a.weight_f32 ? static_cast<const float *>(a.weight)[c]
+                                                     : elem_to_f32<DT>(static_cast<const T *>(a.weight)[c]);
+            }
+            (j & 1 ? w[j / 2].y : w[j / 2].x) = v;
+        }
+    };
+    float2 dw[KT][4], db[KT][4], w[kHeld ? KT : 1][4];
+    int bytes[KT][P];  // that a piece has up to the row's end, 0 to 16; zeros after them
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        if constexpr (kHeld) weights(k, w[k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[k][j] = db[k][j] = both(0.0f);
+#pragma unroll
+        for (int piece = 0; piece < P; ++piece) bytes[k][piece] = max(0, min(16, (a.cols - col(k, piece)) * B));
+    }
+    // pieces outside the row stay zero: nothing is copied there
+    for (int slot = 0; slot < depth; ++slot)
+#pragma unroll
+        for (int matrix = 0; matrix < 3; ++matrix)
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int piece = 0; piece < P; ++piece)
+                    if (bytes[k][piece] == 0 || (matrix == 2 && a.dh == nullptr))
+                        *place(slot, matrix, k, piece) = make_uint4(0u, 0u, 0u, 0u);
+    const int tile_bytes = warps * kTileCols * B;  // from one of a thread's tiles to the next
+    auto copy = [&](const char *from, bool first, uint4 *to) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int piece = 0; piece < P; ++piece) {
+                uint4 *at = to + (k * P + piece) * threads;
+                if (!ALIGNED && k == 0 && piece == 0 && first && col(0, 0) < 0) {  // nothing before this row is the matrix's
+                    const T *elements = reinterpret_cast<const T *>(from);
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        reinterpret_cast<T *>(at)[j] = j >= past && j - past < a.cols ? elements[j] : T(0);
+                } else if (bytes[k][piece] > 0) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                                 :: "r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))),
+                                    "l"(from + k * tile_bytes + piece * 128 * B), "r"(bytes[k][piece]) : "memory");
+                }
+            }
+    };
+    // the next row to be copied, from this thread's first piece on
+    int64_t copy_row = writer;
+    const int64_t first_byte = static_cast<int64_t>(col(0, 0)) * B;
+    const char *from_dy = static_cast<const char *>(row_of<DT>(a.dy, writer, a.dy_stride)) + first_byte;
+    const char *from_h = static_cast<const char *>(row_of<DT>(a.h, writer, a.h_stride)) + first_byte;
+    const char *from_dh = a.dh ? static_cast<const char *>(row_of<DT>(a.dh, writer, a.dh_stride)) + first_byte : nullptr;
+    auto copy_next = [&](int slot) {
+        if (copy_row < a.rows) {
+            uint4 *to = mine + slot * slot_size;
+            copy(from_dy, copy_row * a.dy_stride < past, to);
+            copy(from_h, copy_row * a.h_stride < past, to + KT * P * threads);
+            if (a.dh) copy(from_dh, copy_row * a.dh_stride < past, to + 2 * KT * P * threads);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        copy_row += writers;
+        from_dy += writers * a.dy_stride * B;
+        from_h += writers * a.h_stride * B;
+        if (a.dh) from_dh += writers * a.dh_stride * B;
+    };
+    auto held = [&](int slot, int matrix, int k, float2 (&f)[4]) {
+        Raw8<DT> r;
+#pragma unroll
+        for (int piece = 0; piece < P; ++piece) {
+            const uint4 v = *place(slot, matrix, k, piece);
+            r.w[piece * 4] = v.x;
+            r.w[piece * 4 + 1] = v.y;
+            r.w[piece * 4 + 2] = v.z;
+            r.w[piece * 4 + 3] = v.w;
+        }
+        unpack8<DT>(r, f);
+    };
+    // zeros in what the row's first piece brought along
+    auto clear_first = [&](int slot, int matrix) {
+        uint4 *at = place(slot, matrix, 0, 0);
+        uint4 v = *at;
+        const int words = past * B / 4;
+        const uint32_t half = past * B % 4 ? 0xffff0000u : 0xffffffffu;  // of the word in which the row begins
+        v.x &= words > 0 ? 0u : half;
+        v.y &= words > 1 ? 0u : words == 1 ? half : 0xffffffffu;
+        v.z &= words > 2 ? 0u : words == 2 ? half : 0xffffffffu;
+        v.w &= words == 3 ? half : 0xffffffffu;
+        *at = v;
+    };
+    const float per_col = 1.0f / static_cast<float>(a.cols);
+    // A row's first pass: its columns' sums, and its own two to `sums`.
+    auto add_row = [&](int slot, float mean, float rstd, float2 *sums) {
+        const float2 m = both(-mean), r = both(rstd);
+        if (!ALIGNED && col(0, 0) < 0) {
+            clear_first(slot, 0);
+            clear_first(slot, 1);
+        }
+        float2 c1 = both(0.0f), c2 = both(0.0f);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            float2 g[4], n[4];
+            if constexpr (!kHeld) weights(k, w[0]);
+            held(slot, 0, k, g);
+            held(slot, 1, k, n);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                n[j] = mul2(add2(n[j], m), r);
+                dw[k][j] = fma2(g[j], n[j], dw[k][j]);
+                db[k][j] = add2(g[j], db[k][j]);
+                g[j] = mul2(g[j], w[kHeld ? k : 0][j]);
+                c1 = add2(c1, g[j]);
+                c2 = fma2(g[j], n[j], c2);
+            }
+        }
+        const float2 c = warp_sum2(make_float2(c1.x + c1.y, c2.x + c2.y));
+        if (lane == 0) sums[warp] = c;
+    };
+    // read two rows ahead, and not touched before it is needed
+    auto statistics = [&](int64_t row, float &m, float &r) {
+        if (row < a.rows) m = a.mean[row], r = a.rstd[row];
+    };
+    float2(*const part)[16] = parts[threadIdx.y];
+    if (threadIdx.x < 32) part[threadIdx.x / 16][threadIdx.x % 16] = both(0.0f);
+    __syncthreads();
+#pragma unroll 1
+    for (int q = 0; q < depth; ++q) copy_next(q);
+    float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
+    statistics(writer, mean, rstd);
+    statistics(writer + writers, next_mean, next_rstd);
+    if (depth == 2) copies_left<1>();
+    else if (depth == 3) copies_left<2>();
+    else copies_left<3>();
+    if (writer < a.rows) add_row(0, mean, rstd, part[0]);
+    int turn = 0, slot = 0;
+#pragma unroll 1
+    for (int64_t row = writer; row < a.rows; row += writers, turn ^= 1) {
+        const int next_slot = slot + 1 == depth ? 0 : slot + 1;
+        if (warps > 1) __syncthreads();
+        else __syncwarp();
+        float2 c = both(0.0f);
+        const float4 *all = reinterpret_cast<const float4 *>(part[turn]);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            if (2 * i >= warps) break;
+            const float4 p = all[i], q = all[i + 1];
+            c = add2(add2(c, add2(make_float2(p.x, p.y), make_float2(p.z, p.w))), add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+        }
+        if (depth == 2) copies_left<0>();
+        else if (depth == 3) copies_left<1>();
+        else copies_left<2>();
+        float after_mean = 0.0f, after_rstd = 0.0f;
+        statistics(row + 2 * writers, after_mean, after_rstd);
+        if (row + writers < a.rows) add_row(next_slot, next_mean, next_rstd, part[turn ^ 1]);
+        const float2 m = both(-mean), r = both(rstd);
+        const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * per_col * rstd);
+        T *dx = static_cast<T *>(row_of<DT>(a.dx, row, a.dx_stride));
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            float2 g[4], n[4], d[4];
+            if constexpr (!kHeld) weights(k, w[0]);
+            held(slot, 0, k, g);
+            held(slot, 1, k, n);
+            held(slot, 2, k, d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                d[j] = fma2(r, fma2(g[j], w[kHeld ? k : 0][j], fma2(m2, add2(n[j], m), m1)), d[j]);
+            const Raw8<DT> o = pack8<DT>(d);
+#pragma unroll
+            for (int piece = 0; piece < P; ++piece) {
+                const int c = col(k, piece);
+                if ((ALIGNED || c >= 0) && bytes[k][piece] == 16) {
+                    Vec<16> v;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v.w[i] = o.w[piece * 4 + i];
+                    st<16>(dx + c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < E; ++j)
+                        if ((ALIGNED || c + j >= 0) && c + j < a.cols)
+                            dx[c + j] = static_cast<T>(o.w[piece * 4 + j * B / 4] >> (j * B % 4 * 8));
+                }
+            }
+        }
+        copy_next(slot);
+        slot = next_slot;
+        mean = next_mean, rstd = next_rstd, next_mean = after_mean, next_rstd = after_rstd;
+    }
+    copies_left<0>();
+    if (a.partial == nullptr) return;
+    // The block's sums: of one writer straight from the registers, where whole runs
+    // can be written; otherwise by columns in the ring's place, the writers in order.
+    float *out = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols, *out_b = out + static_cast<int64_t>(gridDim.x) * a.cols;
+    if (ALIGNED && blockDim.y == 1 && a.cols % 4 == 0) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const int c = col(k, P == 2 ? j / 2 : 0) + (P == 2 ? 0 : 2 * j);
+                if (c >= a.cols) continue;
+                *reinterpret_cast<float4 *>(out + c) = make_float4(dw[k][j].x, dw[k][j].y, dw[k][j + 1].x, dw[k][j + 1].y);
+                *reinterpret_cast<float4 *>(out_b + c) = make_float4(db[k][j].x, db[k][j].y, db[k][j + 1].x, db[k][j + 1].y);
+            }
+        return;
+    }
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(ring) + static_cast<int64_t>(threadIdx.y) * 2 * a.cols;
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = P == 2 ? col(k, j / 4) + j % 4 : col(k, 0) + j;
+            if (c < 0 || c >= a.cols) continue;
+            sums[c] = j & 1 ? dw[k][j / 2].y : dw[k][j / 2].x;
+            sums[a.cols + c] = j & 1 ? db[k][j / 2].y : db[k][j / 2].x;
+        }
+    __syncthreads();
+    sums = reinterpret_cast<float *>(ring);
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 2 * a.cols; i += threads) {
+        float sum = sums[i];
+        for (int y = 1; y < static_cast<int>(blockDim.y); ++y) sum += sums[y * 2 * a.cols + i];
+        (i < a.cols ? out[i] : out_b[i - a.cols]) = sum;
+    }
 }
 
 // Rows too wide to hold are read twice, after layernorm_columns_kernel has taken
@@ -414,7 +675,7 @@ cudaError_t layernorm_launch(const LayerNormArgs &a, bool aligned, int sms, cuda
     const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (RUNS && !aligned ? 7 : 0) + kTileCols - 1) / kTileCols);
     const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
     int kt = tiles_per_thread(tiles, kLayerNormWarps, 4);
-    if (many && kt != 0) kt = std::max(kt, tiles == 1 ? 1 : DT != DT_F32 && tiles > 8 ? 4 : 2);
+    if (many && kt != 0) kt = std::max(kt, tiles == 1 ? 1 : 2);
     int warps = 32, per_block = 1;
     if (kt != 0) {
         warps = (tiles + kt - 1) / kt;
@@ -440,31 +701,55 @@ template <int DT> cudaError_t layernorm_dispatch(const LayerNormArgs &a, int sms
                 : layernorm_launch<DT, false>(a, false, sms, s, info);
 }
 
+// Of an SM's shared memory.
+constexpr int kRingBytes = 200 * 1024;
+
 template <int DT>
 cudaError_t layernorm_grad_dispatch(const LayerNormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
                                     int *launches) {
     const bool runs = same_runs<DT>(a.dy, a.dy_stride, a.h, a.h_stride) &&
                       same_runs<DT>(a.dy, a.dy_stride, a.dh, a.dh_stride) && same_runs<DT>(a.dy, a.dy_stride, a.dx, a.dx_stride);
     const bool aligned = runs && wide_rows<DT>(a.dy, a.dy_stride);
-    const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + kTileCols - 1) / kTileCols);
-    const int kt = tiles_per_thread(tiles, kLayerNormWarps, DT == DT_F32 ? 2 : 4);
+    const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (aligned ? 0 : 7) + kTileCols - 1) / kTileCols);
+    const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
+    int kt = tiles_per_thread(tiles, 8, 2);
+    if (DT != DT_F32 && kt == 1 && tiles > 6 && a.rows >= 32 * static_cast<int64_t>(sms)) kt = 2;
+    if (kt == 0) kt = tiles_per_thread(tiles, kLayerNormWarps, DT == DT_F32 ? 2 : 4);
     const bool sums = a.dweight != nullptr || a.dbias != nullptr;
     int64_t writers = 0;
     cudaError_t e = cudaSuccess;
-    info->vec_bytes = ElemOf<DT>::kBytes;
+    info->vec_bytes = runs ? 16 : ElemOf<DT>::kBytes;
     if (a.rows > 0 && kt != 0) {
         const int warps = (tiles + kt - 1) / kt;
-        const int per_block = warps == 1 && a.rows >= 4 * static_cast<int64_t>(sms) ? 4 : 1;
+        // a row for each of 4 warps, where one holds it: their sums leave the block as one
+        const int per_block = runs && warps == 1 && many ? 4 : 1;
         const int resident = std::max(1, 16 / (warps * per_block));  // blocks that make 512 threads an SM
-        const int64_t grid = std::min<int64_t>({(a.rows + per_block - 1) / per_block,
-                                                static_cast<int64_t>(sms) * resident, most_writers / per_block});
-        writers = grid * per_block;
+        int64_t grid = std::min<int64_t>({(a.rows + per_block - 1) / per_block, static_cast<int64_t>(sms) * resident, most_writers});
+        // a writer's rows start alike: a multiple of 8 apart, where it has more than one
+        if (!aligned && grid * per_block < a.rows && grid > 8) grid = grid / 8 * 8;
+        writers = grid;
+        const dim3 block(32 * warps, per_block);
         info->grid = static_cast<int>(grid);
         info->block = 32 * warps * per_block;
-        auto kernel = kt == 1 ? layernorm_grad_kernel<DT, 1> : layernorm_grad_kernel<DT, 2>;
-        if constexpr (DT != DT_F32)
-            if (kt == 4) kernel = layernorm_grad_kernel<DT, 4>;
-        e = launch_rows(kernel, dim3(grid), dim3(32 * warps, per_block), 0, 1, s, a);
+        if (runs && (aligned || grid * per_block % 8 == 0 || grid * per_block >= a.rows)) {
+            auto kernel = aligned ? kt == 1 ? layernorm_grad_ring_kernel<DT, 1, true> : layernorm_grad_ring_kernel<DT, 2, true>
+                                  : kt == 1 ? layernorm_grad_ring_kernel<DT, 1, false> : layernorm_grad_ring_kernel<DT, 2, false>;
+            if constexpr (DT != DT_F32)
+                if (kt == 4) kernel = aligned ? layernorm_grad_ring_kernel<DT, 4, true> : layernorm_grad_ring_kernel<DT, 4, false>;
+            const int row_bytes = 3 * kt * info->block * 8 * ElemOf<DT>::kBytes;  // of a row of each of the block's writers
+            const int depth = std::max(2, std::min(4, kRingBytes / (resident * row_bytes)));
+            static std::atomic<uint64_t> allowed[2][3];
+            e = allow_smem(reinterpret_cast<const void *>(kernel), kRingBytes, &allowed[aligned][kt / 2]);
+            if (e != cudaSuccess) return e;
+            info->smem = depth * row_bytes;
+            e = launch_rows(kernel, dim3(grid), block, depth * row_bytes, 1, s, a, depth);
+        } else {
+            info->vec_bytes = ElemOf<DT>::kBytes;
+            auto kernel = kt == 1 ? layernorm_grad_kernel<DT, 1> : layernorm_grad_kernel<DT, 2>;
+            if constexpr (DT != DT_F32)
+                if (kt == 4) kernel = layernorm_grad_kernel<DT, 4>;
+            e = launch_rows(kernel, dim3(grid), block, 0, 1, s, a);
+        }
         ++*launches;
     } else if (a.rows > 0) {
         if (sums) {
