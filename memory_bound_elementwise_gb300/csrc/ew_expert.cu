@@ -225,6 +225,16 @@ __device__ __forceinline__ float weight_at(const void *w, int wtype, int64_t at)
     return wtype == DT_F16 ? f16_to_f32(v) : bf16_to_f32(v);
 }
 
+// A row of a matrix, and how many elements (up to 16) may be read on both its sides.
+template <int DT> struct RowAt {
+    const void *p;
+    int before, after;
+    __device__ __forceinline__ RowAt(const void *base, int64_t row, int64_t stride, int64_t rows)
+        : p(row_of<DT>(base, row, stride)), before(static_cast<int>(min(row * stride, int64_t(16)))),
+          after(static_cast<int>(min((rows - 1 - row) * stride, int64_t(16)))) {}
+    __device__ __forceinline__ Raw8<DT> load(int c0, int cols) const { return load_at<DT>(p, c0, cols, before, after); }
+};
+
 // ---------------------------------------------------------------- dispatch
 
 // A warp takes U consecutive tiles of a token.  VEC: all rows start at multiples
@@ -242,11 +252,12 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(Expe
     const int64_t token = item / groups;
     if (token >= a.rows) return;
     const int tile0 = static_cast<int>(item - token * groups) * U;
-    const void *x = row_of<DT>(a.x, token, a.x_stride);
+    const RowAt<DT> from(a.x, token, a.x_stride, a.rows);
+    const void *x = from.p;
     Raw8<DT> r[U];
     if constexpr (VEC) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = load_run<DT, true>(x, tile0 + u, 0, a.cols, lane);
+        for (int u = 0; u < U; ++u) r[u] = load_run<DT>(x, tile0 + u, 0, a.cols, lane, false);
     }
     for (int j0 = 0; j0 < a.k; j0 += 32) {
         const int64_t p = position_of(a.positions, token * a.k + j0 + lane, j0 + lane < a.k, a.sorted);
@@ -257,10 +268,10 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(Expe
             const int past = VEC ? 0 : past_of<DT>(out);
             if constexpr (!VEC) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) r[u] = load_at<DT>(x, col_of<true>(tile0 + u, past, lane, 0), a.cols);
+                for (int u = 0; u < U; ++u) r[u] = from.load(col_of<true>(tile0 + u, past, lane, 0), a.cols);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) store_run<DT, true>(out, tile0 + u, past, a.cols, lane, r[u]);
+            for (int u = 0; u < U; ++u) store_run<DT>(out, tile0 + u, past, a.cols, lane, r[u]);
         }
     }
 }
@@ -279,15 +290,15 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_kernel(Exper
     const int tile0 = static_cast<int>(item - token * groups) * U;
     void *out = row_of<DT>(a.out, token, a.out_stride);
     const int past = VEC ? 0 : past_of<DT>(out);
-    auto load = [&](const void *row, int u) {
-        if constexpr (VEC) return load_run<DT, true>(row, tile0 + u, 0, a.cols, lane);
-        else return load_at<DT>(row, col_of<true>(tile0 + u, past, lane, 0), a.cols);
+    auto load = [&](const RowAt<DT> &row, int u) {
+        if constexpr (VEC) return load_run<DT>(row.p, tile0 + u, 0, a.cols, lane, false);
+        else return row.load(col_of<true>(tile0 + u, past, lane, 0), a.cols);
     };
     float2 sum[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         if (a.residual) {
-            unpack8<DT>(load(row_of<DT>(a.residual, token, a.residual_stride), u), sum[u]);
+            unpack8<DT>(load(RowAt<DT>(a.residual, token, a.residual_stride, a.rows), u), sum[u]);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[u][i] = both(0.0f);
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_kernel(Exper
             from[b] = __shfl_sync(kAllLanes, p, b);
             if (from[b] < 0) continue;
 #pragma unroll
-            for (int u = 0; u < U; ++u) r[b][u] = load(row_of<DT>(a.x, from[b], a.x_stride), u);
+            for (int u = 0; u < U; ++u) r[b][u] = load(RowAt<DT>(a.x, from[b], a.x_stride, a.sorted), u);
         }
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
@@ -320,7 +331,7 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_kernel(Exper
         }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) store_run<DT, true>(out, tile0 + u, past, a.cols, lane, pack8<DT>(sum[u]));
+    for (int u = 0; u < U; ++u) store_run<DT>(out, tile0 + u, past, a.cols, lane, pack8<DT>(sum[u]));
 }
 
 // ---------------------------------------------------------------- the gradient of combine
@@ -358,7 +369,8 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_grad_kernel(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp & (split - 1);
     const int64_t token = (static_cast<int64_t>(blockIdx.x - zero_blocks) * kWarpsABlock + warp) / split;
     const bool given = token < a.rows;  // all warps stay for the barriers
-    const void *dout = given ? row_of<DT>(a.residual, token, a.residual_stride) : nullptr;
+    const RowAt<DT> dout_row(a.residual, token, a.residual_stride, a.rows);
+    const void *dout = dout_row.p;  // not looked at unless the token is given
     int turn = 0;
     for (int j0 = 0; j0 < a.k; j0 += KB, turn ^= 1) {
         const bool mine = given && lane < KB && j0 + lane < a.k;
@@ -374,17 +386,17 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_grad_kernel(
         }
         for (int tile = share; given && tile < tiles; tile += split) {
             Raw8<DT> rd[VEC ? 1 : KB], ry[KB];
-            if constexpr (VEC) rd[0] = load_run<DT, true>(dout, tile, 0, a.cols, lane);
+            if constexpr (VEC) rd[0] = load_run<DT>(dout, tile, 0, a.cols, lane, false);
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 if (row[b] < 0) continue;
-                const void *y = a.x ? row_of<DT>(a.x, row[b], a.x_stride) : nullptr;
+                const RowAt<DT> y(a.x, row[b], a.x_stride, a.sorted);
                 if constexpr (VEC) {
-                    if (y) ry[b] = load_run<DT, true>(y, tile, 0, a.cols, lane);
+                    if (a.x) ry[b] = load_run<DT>(y.p, tile, 0, a.cols, lane, false);
                 } else {
                     const int c0 = col_of<true>(tile, past_of<DT>(row_of<DT>(a.out, row[b], a.out_stride)), lane, 0);
-                    rd[b] = load_at<DT>(dout, c0, a.cols);
-                    if (y) ry[b] = load_at<DT>(y, c0, a.cols);
+                    rd[b] = dout_row.load(c0, a.cols);
+                    if (a.x) ry[b] = y.load(c0, a.cols);
                 }
             }
 #pragma unroll
@@ -395,10 +407,15 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_grad_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[i] = mul2(d[i], both(wb[b]));
                 void *out = row_of<DT>(a.out, row[b], a.out_stride);
-                store_run<DT, true>(out, tile, VEC ? 0 : past_of<DT>(out), a.cols, lane, pack8<DT>(o));
+                store_run<DT>(out, tile, VEC ? 0 : past_of<DT>(out), a.cols, lane, pack8<DT>(o));
                 if (a.x) {
                     float2 f[4], s = both(0.0f);
                     unpack8<DT>(ry[b], f);
+                    if constexpr (!VEC) {
+                        const int past = past_of<DT>(out);
+                        clip_columns<true>(tile, past, a.cols, lane, f);
+                        clip_columns<true>(tile, past, a.cols, lane, d);
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s = fma2(f[i], d[i], s);
                     dot[b] += s.x + s.y;

@@ -25,41 +25,46 @@ namespace {
 
 // ---------------------------------------------------------------- columns
 
+// How the rows of a call's matrices lie: all at multiples of 8 elements; all alike,
+// but anywhere; or apart.
+enum Rows : int { kApart = 0, kAligned = 1, kShifted = 2 };
+template <int DT, int ROWS>
+__device__ __forceinline__ Raw8<DT> load_row(const void *row, int tile, int past, int cols, int lane, bool inner) {
+    if constexpr (ROWS == kShifted) return load_run<DT>(row, tile, past, cols, lane, inner);
+    else return load_tile<DT, ROWS == kAligned>(row, tile * kTileCols, cols, lane);
+}
+template <int DT, int ROWS>
+__device__ __forceinline__ void store_row(void *row, int tile, int past, int cols, int lane, const Raw8<DT> &r) {
+    if constexpr (ROWS == kShifted) store_run<DT>(row, tile, past, cols, lane, r);
+    else store_tile<DT, ROWS == kAligned>(row, tile * kTileCols, cols, lane, r);
+}
 // The columns of a vector, in binary32; null stands for `other`, columns
-// outside for zero.  A run of it starts anywhere.
-template <int DT, bool RUNS>
+// outside for zero.  Beside shifted rows a run of it starts anywhere.
+template <int DT, int ROWS>
 __device__ __forceinline__ void load_columns(const void *w, bool f32, float other, int tile, int past, int cols, int lane,
                                              float2 (&f)[4]) {
-    const int c0 = col_of<RUNS>(tile, past, lane, 0);
     if (w == nullptr) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = both(other);
-    } else if (RUNS && (DT == DT_F32 || f32)) {
-        unpack8<DT_F32>(load_at<DT_F32>(w, c0, cols), f);
-    } else if (RUNS) {
-        unpack8<DT>(load_at<DT>(w, c0, cols), f);
+    } else if constexpr (ROWS != kShifted) {
+        load_weight<DT, ROWS == kAligned>(w, f32, tile * kTileCols, cols, lane, f);
     } else {
+        const int c0 = col_of<true>(tile, past, lane, 0);
+        if (c0 >= 8 && c0 + 16 <= cols) {
+            if (DT == DT_F32 || f32) unpack8<DT_F32>(load_at<DT_F32>(w, c0, cols), f);
+            else unpack8<DT>(load_at<DT>(w, c0, cols), f);
+            return;
+        }
+        // at its ends element by element, all under way together
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int col = col_of<false>(tile, past, lane, j);
             float e = 0.0f;
-            if (col < cols) {
-                if (DT == DT_F32 || f32) e = static_cast<const float *>(w)[col];
-                else e = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(w)[col]);
+            if (c0 + j >= 0 && c0 + j < cols) {
+                if (DT == DT_F32 || f32) e = static_cast<const float *>(w)[c0 + j];
+                else e = elem_to_f32<DT>(static_cast<const typename ElemOf<DT>::type *>(w)[c0 + j]);
             }
             (j & 1 ? f[j / 2].y : f[j / 2].x) = e;
         }
-    }
-}
-// Zeros in columns outside the row.
-template <bool RUNS> __device__ __forceinline__ void clip_columns(int tile, int past, int cols, int lane, float2 (&f)[4]) {
-    const int first = tile * kTileCols - (RUNS ? past : 0);
-    if (first >= 0 && first + kTileCols <= cols) return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int a = col_of<RUNS>(tile, past, lane, 2 * j), b = col_of<RUNS>(tile, past, lane, 2 * j + 1);
-        if (a < 0 || a >= cols) f[j].x = 0.0f;
-        if (b < 0 || b >= cols) f[j].y = 0.0f;
     }
 }
 // Columns of the row in tile `tile`.
@@ -89,49 +94,27 @@ __device__ __forceinline__ float2 block_sum2(float2 v, int warps, float2 *part) 
 // One row to a block of `warps` warps, tile t of the row to warp t mod warps;
 // with one warp a row, blockDim.y rows to a block.  HELD: the warps x KT tiles
 // cover the row, which stays in registers.  Each warp takes the mean of its own
-// columns and the squares around that; the parts are joined by
+// columns, beyond one of them, and the squares around that; the parts are joined by
 //     sum (v - m)^2 = sum over warps of (squares + n (mean - m)^2),
 // so that both statistics cost one barrier and no cancellation.  Otherwise the
-// passes read the row again.  Nothing is written before all threads have read
-// the row's first element: h and y may take x's place.
-template <int DT, bool RUNS, int KT, bool HELD>
-__global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && RUNS && KT * ElemOf<DT>::kBytes <= 8 ? 2 : 1)
-    layernorm_kernel(LayerNormArgs a) {
+// passes read the row again.
+//
+// Weights beside shifted rows have to be cut to their phase, which takes as long
+// as all else.  Where a thread has up to two tiles, blocks therefore walk over the
+// rows in steps of a multiple of 8, after which the phase is the same, and cut
+// the weights once.
+template <int DT, int ROWS, int KT, bool HELD, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARPS == 8 ? 3 : KT == 1 || (KT == 2 && ROWS == kAligned) ? 2 : 1)
+    layernorm_kernel(const __grid_constant__ LayerNormArgs a) {
     enter_grid();
-    __shared__ float2 part[32];
+    constexpr bool kWalks = HELD && ROWS == kShifted && KT <= 2;
+    __shared__ float4 parts[2][32];  // of a warp's columns: an element, mean beyond that, squares, number
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= a.rows) return;  // whole warps: blockDim.y > 1 only with one warp a row
-    const void *x = row_of<DT>(a.x, row, a.x_stride);
-    const void *res = a.residual ? row_of<DT>(a.residual, row, a.residual_stride) : nullptr;
-    void *h = a.h ? row_of<DT>(a.h, row, a.h_stride) : nullptr;
-    void *out = row_of<DT>(a.y, row, a.y_stride);
-    const int past = RUNS ? past_of<DT>(x) : 0;
+    const int past = ROWS == kShifted ? past_of<DT>(row_of<DT>(a.x, row, a.x_stride)) : 0;
     const float per_col = a.per_col;
-    auto first_of = [](const void *p) {
-        if constexpr (DT == DT_F32) return __uint_as_float(ld<4>(p).w[0]);
-        else return elem_to_f32<DT>(ld<2>(p).h);
-    };
-    auto sum_of = [&](int tile, float2 (&f)[4]) {
-        unpack8<DT>(load_run<DT, RUNS>(x, tile, past, a.cols, lane), f);
-        if (res) {
-            float2 g[4];
-            unpack8<DT>(load_run<DT, RUNS>(res, tile, past, a.cols, lane), g);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
-        }
-    };
-    // y of one tile from h, the first element `at` and the mean beyond it
-    auto put = [&](int tile, const float2 (&f)[4], float at, float mean, float r) {
-        float2 w[4], b[4], y[4];
-        load_columns<DT, RUNS>(a.weight, a.weight_f32, 1.0f, tile, past, a.cols, lane, w);
-        load_columns<DT, RUNS>(a.bias, a.weight_f32, 0.0f, tile, past, a.cols, lane, b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            y[j] = fma2(mul2(add2(add2(f[j], both(-at)), both(-mean)), both(r)), w[j], b[j]);
-        store_run<DT, RUNS>(out, tile, past, a.cols, lane, pack8<DT>(y));
-    };
-    auto statistics = [&](float at, float mean, float squares) {
+    auto statistics = [&](int64_t row, float at, float mean, float squares) {
         const float r = rsqrtf(fmaf(squares, per_col, a.eps));
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = at + mean;
@@ -139,72 +122,127 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && RUNS && KT * ElemOf
         }
         return r;
     };
+    auto weights = [&](int tile, float2 (&w)[4], float2 (&b)[4]) {
+        load_columns<DT, ROWS>(a.weight, a.weight_f32, 1.0f, tile, past, a.cols, lane, w);
+        load_columns<DT, ROWS>(a.bias, a.weight_f32, 0.0f, tile, past, a.cols, lane, b);
+    };
+    // y of one tile from h, the element `at` and the mean beyond it
+    auto put = [&](void *out, int tile, const float2 (&f)[4], float at, float mean, float r, const float2 (&w)[4], const float2 (&b)[4]) {
+        float2 y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            y[j] = fma2(mul2(add2(add2(f[j], both(-at)), both(-mean)), both(r)), w[j], b[j]);
+        store_row<DT, ROWS>(out, tile, past, a.cols, lane, pack8<DT>(y));
+    };
 
     if constexpr (HELD) {
-        float2 f[KT][4];
-        Raw8<DT> rx[KT], rr[KT];
-#pragma unroll
-        for (int k = 0; k < KT; ++k) rx[k] = load_run<DT, RUNS>(x, warp + k * warps, past, a.cols, lane);
-        if (res) {
-#pragma unroll
-            for (int k = 0; k < KT; ++k) rr[k] = load_run<DT, RUNS>(res, warp + k * warps, past, a.cols, lane);
-        }
-        float at = first_of(x);
-        if (res) at += first_of(res);
-        float2 s2 = both(0.0f);
+        float2 w[kWalks ? KT : 1][4], b[kWalks ? KT : 1][4];
         int n = 0;
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            unpack8<DT>(rx[k], f[k]);
-            if (res) {
-                float2 g[4];
-                unpack8<DT>(rr[k], g);
+        for (int k = 0; k < KT; ++k) n += columns_in(warp + k * warps, past, a.cols);
+        const float per_own = 1.0f / static_cast<float>(max(n, 1));
+        int turn = 0;
+        Raw8<DT> rx[KT], rr[KT];
+        auto load = [&] {
+            const void *x = row_of<DT>(a.x, row, a.x_stride);
+            const bool inner = row > 0 && row + 1 < a.rows;  // strides are at least 8
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f[k][j] = add2(f[k][j], g[j]);
+            for (int k = 0; k < KT; ++k) rx[k] = load_row<DT, ROWS>(x, warp + k * warps, past, a.cols, lane, inner);
+            if (a.residual) {
+                const void *res = row_of<DT>(a.residual, row, a.residual_stride);
+#pragma unroll
+                for (int k = 0; k < KT; ++k) rr[k] = load_row<DT, ROWS>(res, warp + k * warps, past, a.cols, lane, inner);
             }
-            float2 d[4];
+        };
+        load();
+        if constexpr (kWalks) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = add2(f[k][j], both(-at));
-            clip_columns<RUNS>(warp + k * warps, past, a.cols, lane, d);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
-            n += columns_in(warp + k * warps, past, a.cols);
+            for (int k = 0; k < KT; ++k) weights(warp + k * warps, w[k], b[k]);
         }
-        float mean = warp_sum(s2.x + s2.y) / static_cast<float>(max(n, 1));
-        float2 q2 = both(0.0f);
+        do {
+            void *h = a.h ? row_of<DT>(a.h, row, a.h_stride) : nullptr;
+            void *out = row_of<DT>(a.y, row, a.y_stride);
+            const int64_t here = row;
+            float2 f[KT][4];
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            float2 d[4];
+            for (int k = 0; k < KT; ++k) {
+                unpack8<DT>(rx[k], f[k]);
+                if (a.residual) {
+                    float2 g[4];
+                    unpack8<DT>(rr[k], g);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = add2(add2(f[k][j], both(-at)), both(-mean));
-            clip_columns<RUNS>(warp + k * warps, past, a.cols, lane, d);
+                    for (int j = 0; j < 4; ++j) f[k][j] = add2(f[k][j], g[j]);
+                }
+                if (h) store_row<DT, ROWS>(h, warp + k * warps, past, a.cols, lane, pack8<DT>(f[k]));
+            }
+            row += static_cast<int64_t>(gridDim.x) * blockDim.y;
+            if (kWalks && row < a.rows) load();  // on its way while this row is worked on
+            // an element of the warp's first tile that lies in the row, if any does (a row has 8)
+            float at = __shfl_sync(kAllLanes, ROWS == kShifted && warp == 0 ? f[0][3].y : f[0][0].x, 0);
+            float2 s2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
-        }
-        float squares = warp_sum(q2.x + q2.y);
-        if (warps > 1) {
-            if (lane == 0) part[warp] = make_float2(mean, squares);
-            __syncthreads();
-            const float2 v = lane < warps ? part[lane] : both(0.0f);
-            int m = 0;
+            for (int k = 0; k < KT; ++k) {
+                float2 d[4];
 #pragma unroll
-            for (int k = 0; k < KT; ++k) m += lane < warps ? columns_in(lane + k * warps, past, a.cols) : 0;
-            const float count = static_cast<float>(m);
-            mean = warp_sum(m > 0 ? count * v.x : 0.0f) * per_col;
-            const float off = v.x - mean;
-            squares = warp_sum(m > 0 ? fmaf(count * off, off, v.y) : 0.0f);
-        }
-        const float r = statistics(at, mean, squares);
+                for (int j = 0; j < 4; ++j) d[j] = add2(f[k][j], both(-at));
+                clip_columns<ROWS != kApart>(warp + k * warps, past, a.cols, lane, d);
 #pragma unroll
-        for (int k = 0; k < KT; ++k) {
-            const int tile = warp + k * warps;
-            if (tile * kTileCols - past >= a.cols) continue;
-            if (h) store_run<DT, RUNS>(h, tile, past, a.cols, lane, pack8<DT>(f[k]));
-            put(tile, f[k], at, mean, r);
-        }
+                for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
+            }
+            float mean = warp_sum(s2.x + s2.y) * per_own;
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                float2 d[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] = add2(add2(f[k][j], both(-at)), both(-mean));
+                clip_columns<ROWS != kApart>(warp + k * warps, past, a.cols, lane, d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
+            }
+            float squares = warp_sum(q2.x + q2.y);
+            if (warps > 1) {
+                float4 *part = parts[turn];
+                turn ^= 1;  // read by all before it is written again: a barrier lies between
+                if (lane == 0) part[warp] = make_float4(at, mean, squares, static_cast<float>(n));
+                __syncthreads();
+                const float4 v = part[lane < warps ? lane : 0];
+                const float count = lane < warps ? v.w : 0.0f;
+                at = part[0].x;
+                const float apart = v.x - at + v.y;
+                mean = warp_sum(count > 0.0f ? count * apart : 0.0f) * per_col;
+                const float off = apart - mean;
+                squares = warp_sum(count > 0.0f ? fmaf(count * off, off, v.z) : 0.0f);
+            }
+            const float r = statistics(here, at, mean, squares);
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                const int tile = warp + k * warps;
+                if (tile * kTileCols - past >= a.cols) continue;
+                if constexpr (!kWalks) weights(tile, w[0], b[0]);
+                put(out, tile, f[k], at, mean, r, w[kWalks ? k : 0], b[kWalks ? k : 0]);
+            }
+        } while (kWalks && row < a.rows);
     } else {
         __shared__ float sums[2][32];
         const int tiles = (a.cols + past + kTileCols - 1) / kTileCols;
+        const void *x = row_of<DT>(a.x, row, a.x_stride);
+        const void *res = a.residual ? row_of<DT>(a.residual, row, a.residual_stride) : nullptr;
+        void *h = a.h ? row_of<DT>(a.h, row, a.h_stride) : nullptr;
+        const bool inner = row > 0 && row + 1 < a.rows;
+        auto sum_of = [&](int tile, float2 (&f)[4]) {
+            unpack8<DT>(load_row<DT, ROWS>(x, tile, past, a.cols, lane, inner), f);
+            if (res) {
+                float2 g[4];
+                unpack8<DT>(load_row<DT, ROWS>(res, tile, past, a.cols, lane, inner), g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
+            }
+        };
+        // the row's first element: read by all before h or y may take its place
+        auto first_of = [](const void *p) {
+            if constexpr (DT == DT_F32) return __uint_as_float(ld<4>(p).w[0]);
+            else return elem_to_f32<DT>(ld<2>(p).h);
+        };
         float at = first_of(x);
         if (res) at += first_of(res);
         float2 s2 = both(0.0f), q2 = both(0.0f), f[4];
@@ -212,7 +250,7 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && RUNS && KT * ElemOf
             sum_of(t, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = add2(f[j], both(-at));
-            clip_columns<RUNS>(t, past, a.cols, lane, f);
+            clip_columns<ROWS != kApart>(t, past, a.cols, lane, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) s2 = add2(s2, f[j]);
         }
@@ -221,15 +259,17 @@ __global__ void __launch_bounds__(HELD ? 512 : 1024, HELD && RUNS && KT * ElemOf
             sum_of(t, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = add2(add2(f[j], both(-at)), both(-mean));
-            clip_columns<RUNS>(t, past, a.cols, lane, f);
+            clip_columns<ROWS != kApart>(t, past, a.cols, lane, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) q2 = fma2(f[j], f[j], q2);
         }
-        const float r = statistics(at, mean, block_sum(q2.x + q2.y, warps, sums[1]));
+        const float r = statistics(row, at, mean, block_sum(q2.x + q2.y, warps, sums[1]));
         for (int t = warp; t < tiles; t += warps) {
+            float2 w[4], b[4];
             sum_of(t, f);
-            if (h) store_run<DT, RUNS>(h, t, past, a.cols, lane, pack8<DT>(f));
-            put(t, f, at, mean, r);
+            weights(t, w, b);
+            if (h) store_row<DT, ROWS>(h, t, past, a.cols, lane, pack8<DT>(f));
+            put(row_of<DT>(a.y, row, a.y_stride), t, f, at, mean, r, w, b);
         }
     }
 }
@@ -262,13 +302,13 @@ template <int DT, int KT> __global__ void __launch_bounds__(512) layernorm_grad_
         Raw8<DT> cdy[KT], ch[KT];
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            cdy[k] = load_run<DT, false>(dy, warp + k * warps, 0, a.cols, lane);
-            ch[k] = load_run<DT, false>(h, warp + k * warps, 0, a.cols, lane);
+            cdy[k] = load_tile<DT, false>(dy, (warp + k * warps) * kTileCols, a.cols, lane);
+            ch[k] = load_tile<DT, false>(h, (warp + k * warps) * kTileCols, a.cols, lane);
         }
         float2 c1 = both(0.0f), c2 = both(0.0f);
         auto products = [&](int k, float2 (&g)[4], float2 (&n)[4], bool add) {
             float2 w[4];
-            load_columns<DT, false>(a.weight, a.weight_f32, 1.0f, warp + k * warps, 0, a.cols, lane, w);
+            load_columns<DT, kApart>(a.weight, a.weight_f32, 1.0f, warp + k * warps, 0, a.cols, lane, w);
             unpack8<DT>(cdy[k], g);
             unpack8<DT>(ch[k], n);
 #pragma unroll
@@ -301,14 +341,14 @@ template <int DT, int KT> __global__ void __launch_bounds__(512) layernorm_grad_
             float2 g[4], n[4], d[4];
             products(k, g, n, false);
             if (a.dh) {
-                unpack8<DT>(load_run<DT, false>(row_of<DT>(a.dh, row, a.dh_stride), warp + k * warps, 0, a.cols, lane), d);
+                unpack8<DT>(load_tile<DT, false>(row_of<DT>(a.dh, row, a.dh_stride), (warp + k * warps) * kTileCols, a.cols, lane), d);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = both(0.0f);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) d[j] = fma2(r, fma2(m2, n[j], add2(g[j], m1)), d[j]);
-            store_run<DT, false>(dx, warp + k * warps, 0, a.cols, lane, pack8<DT>(d));
+            store_tile<DT, false>(dx, (warp + k * warps) * kTileCols, a.cols, lane, pack8<DT>(d));
         }
     }
     if (a.partial == nullptr) return;
@@ -587,25 +627,27 @@ template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1
 
 // Rows too wide to hold are read twice, after layernorm_columns_kernel has taken
 // the columns' sums (dx may be dy).
-template <int DT, bool RUNS> __global__ void __launch_bounds__(1024) layernorm_grad_wide_kernel(LayerNormGradArgs a) {
+template <int DT, int ROWS> __global__ void __launch_bounds__(1024) layernorm_grad_wide_kernel(LayerNormGradArgs a) {
     enter_grid();
     __shared__ float2 part[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t row = blockIdx.x;
     const void *dy = row_of<DT>(a.dy, row, a.dy_stride), *h = row_of<DT>(a.h, row, a.h_stride);
-    const int past = RUNS ? past_of<DT>(dy) : 0, tiles = (a.cols + past + kTileCols - 1) / kTileCols;
+    const int past = ROWS == kShifted ? past_of<DT>(dy) : 0, tiles = (a.cols + past + kTileCols - 1) / kTileCols;
+    const bool inner = row > 0 && row + 1 < a.rows;
     const float2 m = both(-a.mean[row]), r = both(a.rstd[row]);
     auto products = [&](int tile, float2 (&g)[4], float2 (&n)[4]) {
         float2 w[4];
-        load_columns<DT, RUNS>(a.weight, a.weight_f32, 1.0f, tile, past, a.cols, lane, w);
-        unpack8<DT>(load_run<DT, RUNS>(dy, tile, past, a.cols, lane), g);
-        unpack8<DT>(load_run<DT, RUNS>(h, tile, past, a.cols, lane), n);
+        load_columns<DT, ROWS>(a.weight, a.weight_f32, 1.0f, tile, past, a.cols, lane, w);
+        unpack8<DT>(load_row<DT, ROWS>(dy, tile, past, a.cols, lane, inner), g);
+        unpack8<DT>(load_row<DT, ROWS>(h, tile, past, a.cols, lane, inner), n);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             n[j] = mul2(add2(n[j], m), r);
             g[j] = mul2(g[j], w[j]);
         }
-        clip_columns<RUNS>(tile, past, a.cols, lane, n);
+        clip_columns<ROWS != kApart>(tile, past, a.cols, lane, n);
+        clip_columns<ROWS != kApart>(tile, past, a.cols, lane, g);
     };
     float2 c1 = both(0.0f), c2 = both(0.0f), g[4], n[4];
     for (int t = warp; t < tiles; t += warps) {
@@ -623,10 +665,10 @@ template <int DT, bool RUNS> __global__ void __launch_bounds__(1024) layernorm_g
     for (int t = warp; t < tiles; t += warps) {
         products(t, g, n);
         float2 d[4] = {};
-        if (a.dh) unpack8<DT>(load_run<DT, RUNS>(row_of<DT>(a.dh, row, a.dh_stride), t, past, a.cols, lane), d);
+        if (a.dh) unpack8<DT>(load_row<DT, ROWS>(row_of<DT>(a.dh, row, a.dh_stride), t, past, a.cols, lane, inner), d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = fma2(r, fma2(m2, n[j], add2(g[j], m1)), d[j]);
-        store_run<DT, RUNS>(dx, t, past, a.cols, lane, pack8<DT>(d));
+        store_row<DT, ROWS>(dx, t, past, a.cols, lane, pack8<DT>(d));
     }
 }
 
@@ -664,52 +706,55 @@ template <int DT, bool VEC> __global__ void __launch_bounds__(256) layernorm_col
 // ---------------------------------------------------------------- launches
 
 constexpr int kLayerNormWarps = 16;  // that hold a row
+constexpr int kRingBytes = 200 * 1024;  // of an SM's shared memory
 
 // Whether two matrices have their rows at the same place between multiples of 8 elements.
 template <int DT> bool same_runs(const void *p, int64_t stride, const void *q, int64_t other) {
     return q == nullptr || (past_of<DT>(p) == past_of<DT>(q) && (stride - other) % 8 == 0);
 }
 
-template <int DT, bool RUNS>
-cudaError_t layernorm_launch(const LayerNormArgs &a, bool aligned, int sms, cudaStream_t s, LaunchInfo *info) {
-    const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (RUNS && !aligned ? 7 : 0) + kTileCols - 1) / kTileCols);
+template <int DT, int ROWS> cudaError_t layernorm_launch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
+    const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (ROWS == kShifted ? 7 : 0) + kTileCols - 1) / kTileCols);
     const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
+    info->vec_bytes = ROWS != kApart ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
     int kt = tiles_per_thread(tiles, kLayerNormWarps, 4);
-    if (many && kt != 0) kt = std::max(kt, tiles == 1 ? 1 : 2);
+    if (many && kt != 0 && ROWS != kShifted) kt = std::max(kt, tiles == 1 ? 1 : DT != DT_F32 && tiles > 8 ? 4 : 2);
     int warps = 32, per_block = 1;
     if (kt != 0) {
         warps = (tiles + kt - 1) / kt;
         if (warps == 1 && many) per_block = 8;
     }
-    const int64_t grid = (a.rows + per_block - 1) / per_block;
+    int64_t grid = (a.rows + per_block - 1) / per_block;
+    if (ROWS == kShifted && many && (kt == 1 || kt == 2)) {  // walkers, as many as an SM holds at 64 or 128 registers
+        const int64_t most = static_cast<int64_t>(sms) * std::max(1, 32 / kt / (warps * per_block)) / 8 * 8;
+        if (most > 0) grid = std::min(grid, most);
+    }
     const dim3 block(32 * warps, per_block);
     info->grid = static_cast<int>(grid);
     info->block = 32 * warps * per_block;
-    info->vec_bytes = RUNS ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
-    switch (kt) {
-        case 1: return launch_rows(layernorm_kernel<DT, RUNS, 1, true>, dim3(grid), block, 0, 1, s, a);
-        case 2: return launch_rows(layernorm_kernel<DT, RUNS, 2, true>, dim3(grid), block, 0, 1, s, a);
-        case 4: return launch_rows(layernorm_kernel<DT, RUNS, 4, true>, dim3(grid), block, 0, 1, s, a);
-        default: return launch_rows(layernorm_kernel<DT, RUNS, 1, false>, dim3(grid), block, 0, 1, s, a);
-    }
+    auto kernel = kt == 0   ? layernorm_kernel<DT, ROWS, 1, false, 32>
+                  : kt == 1 ? layernorm_kernel<DT, ROWS, 1, true, 16>
+                  : kt == 2 ? layernorm_kernel<DT, ROWS, 2, true, 16>
+                  : warps <= 8 ? layernorm_kernel<DT, ROWS, 4, true, 8>
+                               : layernorm_kernel<DT, ROWS, 4, true, 16>;
+    return launch_rows(kernel, dim3(grid), block, 0, 1, s, a);
 }
 
 template <int DT> cudaError_t layernorm_dispatch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
-    const bool runs = same_runs<DT>(a.x, a.x_stride, a.residual, a.residual_stride) &&
-                      same_runs<DT>(a.x, a.x_stride, a.y, a.y_stride) && same_runs<DT>(a.x, a.x_stride, a.h, a.h_stride);
-    return runs ? layernorm_launch<DT, true>(a, wide_rows<DT>(a.x, a.x_stride), sms, s, info)
-                : layernorm_launch<DT, false>(a, false, sms, s, info);
+    const bool alike = a.cols >= 8 && same_runs<DT>(a.x, a.x_stride, a.residual, a.residual_stride) &&
+                       same_runs<DT>(a.x, a.x_stride, a.y, a.y_stride) && same_runs<DT>(a.x, a.x_stride, a.h, a.h_stride);
+    if (!alike) return layernorm_launch<DT, kApart>(a, sms, s, info);
+    return wide_rows<DT>(a.x, a.x_stride) && wide_weight<DT>(a.weight, a.weight_f32) && wide_weight<DT>(a.bias, a.weight_f32)
+               ? layernorm_launch<DT, kAligned>(a, sms, s, info)
+               : layernorm_launch<DT, kShifted>(a, sms, s, info);
 }
-
-// Of an SM's shared memory.
-constexpr int kRingBytes = 200 * 1024;
 
 template <int DT>
 cudaError_t layernorm_grad_dispatch(const LayerNormGradArgs &a, int64_t most_writers, int sms, cudaStream_t s, LaunchInfo *info,
                                     int *launches) {
-    const bool runs = same_runs<DT>(a.dy, a.dy_stride, a.h, a.h_stride) &&
+    const bool runs = a.cols >= 8 && same_runs<DT>(a.dy, a.dy_stride, a.h, a.h_stride) &&
                       same_runs<DT>(a.dy, a.dy_stride, a.dh, a.dh_stride) && same_runs<DT>(a.dy, a.dy_stride, a.dx, a.dx_stride);
-    const bool aligned = runs && wide_rows<DT>(a.dy, a.dy_stride);
+    const bool aligned = runs && wide_rows<DT>(a.dy, a.dy_stride) && wide_weight<DT>(a.weight, a.weight_f32);
     const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (aligned ? 0 : 7) + kTileCols - 1) / kTileCols);
     const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
     int kt = tiles_per_thread(tiles, 8, 2);
@@ -760,7 +805,8 @@ cudaError_t layernorm_grad_dispatch(const LayerNormGradArgs &a, int64_t most_wri
             ++*launches;
         }
         if (e == cudaSuccess)
-            e = launch_rows(runs ? layernorm_grad_wide_kernel<DT, true> : layernorm_grad_wide_kernel<DT, false>,
+            e = launch_rows(aligned ? layernorm_grad_wide_kernel<DT, kAligned> : runs ? layernorm_grad_wide_kernel<DT, kShifted>
+                                                                               : layernorm_grad_wide_kernel<DT, kApart>,
                             dim3(static_cast<unsigned>(a.rows)), dim3(1024), 0, 1, s, a);
         ++*launches;
         info->grid = static_cast<int>(a.rows);

@@ -9,6 +9,8 @@
 // that starts at a multiple of its size always lies within one warp.
 #pragma once
 
+#include <type_traits>
+
 #include "ew_device.cuh"
 #include "ew_internal.h"
 
@@ -271,8 +273,10 @@ template <int DT> __device__ __forceinline__ void *row_of(void *base, int64_t ro
 // ---------------------------------------------------------------- runs of 8 elements
 //
 // Rows that start anywhere, in runs of 8 elements that start at multiples of 8
-// in memory: the first begins `past` elements before the row, and what is
-// outside the row is neither read nor written.
+// in memory: the first begins `past` elements before the row.  Nothing outside
+// the row is written.  Reading, a run at a row's end may bring elements of the
+// rows beside it along, whatever they hold, so that all lanes load alike: loads of
+// single elements in a branch are waited for there, one matrix after another.
 
 // Elements of a row's first run that lie before the row.
 template <int DT> __host__ __device__ __forceinline__ int past_of(const void *row) {
@@ -282,66 +286,108 @@ template <int DT> __host__ __device__ __forceinline__ int past_of(const void *ro
 template <bool RUNS> __device__ __forceinline__ int col_of(int tile, int past, int lane, int j) {
     return RUNS ? tile * kTileCols - past + lane * 8 + j : tile * kTileCols + j * 32 + lane;
 }
-// The lane's 8 elements; columns outside the row are zero.
-template <int DT, bool RUNS> __device__ __forceinline__ Raw8<DT> load_run(const void *row, int tile, int past, int cols, int lane) {
-    if constexpr (!RUNS) {
-        return load_tile<DT, false>(row, tile * kTileCols, cols, lane);
-    } else {
-        using T = typename ElemOf<DT>::type;
-        const T *p = static_cast<const T *>(row);
-        const int c0 = col_of<true>(tile, past, lane, 0);
+// Elements c0 .. c0 + 7 one by one, zero outside the row: for a matrix's first and
+// last rows, and so in few registers rather than fast.
+template <int DT> __device__ __forceinline__ Raw8<DT> load_single(const void *row, int c0, int cols) {
+    constexpr int B = ElemOf<DT>::kBytes;
+    const auto *p = static_cast<const typename ElemOf<DT>::type *>(row);
+    Raw8<DT> r;
+#pragma unroll
+    for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = 0u;
+#pragma unroll 1
+    for (int j = max(-c0, 0); j < min(cols - c0, 8); ++j) {
+        const uint32_t v = static_cast<uint32_t>(p[c0 + j]) << (j * B % 4 * 8);
+#pragma unroll
+        for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] |= j * B / 4 == k ? v : 0u;
+    }
+    return r;
+}
+// The lane's run.  `inner`: the 7 elements before the row and after it may be
+// read; otherwise, and in lanes without a column of the row, those outside are zero.
+template <int DT> __device__ __forceinline__ Raw8<DT> load_run(const void *row, int tile, int past, int cols, int lane, bool inner) {
+    const int c0 = col_of<true>(tile, past, lane, 0);
+    if (inner ? c0 > -8 && c0 < cols : c0 >= 0 && c0 + 8 <= cols) {
+        const Vec<8 * ElemOf<DT>::kBytes> v = ld<8 * ElemOf<DT>::kBytes>(static_cast<const typename ElemOf<DT>::type *>(row) + c0);
         Raw8<DT> r;
-        if (c0 >= 0 && c0 + 8 <= cols) {
-            const Vec<8 * ElemOf<DT>::kBytes> v = ld<8 * ElemOf<DT>::kBytes>(p + c0);
 #pragma unroll
-            for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = v.w[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = 0u;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j >= 0 && c0 + j < cols) {
-                    if constexpr (DT == DT_F32) r.w[j] = ld<4>(p + c0 + j).w[0];
-                    else r.w[j / 2] |= static_cast<uint32_t>(ld<2>(p + c0 + j).h) << (16 * (j & 1));
-                }
-        }
+        for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = v.w[k];
         return r;
     }
+    return load_single<DT>(row, c0, cols);
 }
-template <int DT, bool RUNS>
-__device__ __forceinline__ void store_run(void *row, int tile, int past, int cols, int lane, const Raw8<DT> &r) {
-    if constexpr (!RUNS) {
-        store_tile<DT, false>(row, tile * kTileCols, cols, lane, r);
-    } else {
-        using T = typename ElemOf<DT>::type;
-        T *p = static_cast<T *>(row);
-        const int c0 = col_of<true>(tile, past, lane, 0);
-        if (c0 >= 0 && c0 + 8 <= cols) {
-            Vec<8 * ElemOf<DT>::kBytes> v;
-#pragma unroll
-            for (int k = 0; k < ElemOf<DT>::kWords; ++k) v.w[k] = r.w[k];
-            st<8 * ElemOf<DT>::kBytes>(p + c0, v);
+// Elements `from` to 7 of a run, or 0 to `to` - 1, where the row begins or ends in
+// it: one, two and four at a time, as they are aligned.
+template <int DT> __device__ __forceinline__ void store_part(typename ElemOf<DT>::type *run, const Raw8<DT> &r, int from, int to) {
+    constexpr int B = ElemOf<DT>::kBytes;
+    auto put = [&](int at, auto n) {  // elements at .. at + n - 1, `at` a multiple of n
+        constexpr int N = decltype(n)::value, W = N * B / 4;
+        if constexpr (W == 0) {
+            const uint32_t w = at & 4 ? (at & 2 ? r.w[3] : r.w[2]) : (at & 2 ? r.w[1] : r.w[0]);
+            run[at] = static_cast<typename ElemOf<DT>::type>(at & 1 ? w >> 16 : w);
         } else {
+            Vec<N * B> v;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (c0 + j >= 0 && c0 + j < cols) p[c0 + j] = static_cast<T>(r.w[j * ElemOf<DT>::kBytes / 4] >> (j * ElemOf<DT>::kBytes % 4 * 8));
+            for (int i = 0; i < W; ++i) {
+                v.w[i] = r.w[i];
+#pragma unroll
+                for (int k = 1; k < 8 / N; ++k)
+                    if (at == k * N) v.w[i] = r.w[k * W + i];
+            }
+            st<N * B>(run + at, v);
+        }
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Four = std::integral_constant<int, 4>;
+    if (to == 8) {
+        if (from & 1) put(from, One());
+        from += from & 1;
+        if (from & 2) put(from, Two());
+        from += from & 2;
+        if (from & 4) put(4, Four());
+    } else {
+        if (to & 4) put(0, Four());
+        if (to & 2) put(to & 4, Two());
+        if (to & 1) put(to & 6, One());
+    }
+}
+template <int DT> __device__ __forceinline__ void store_run(void *row, int tile, int past, int cols, int lane, const Raw8<DT> &r) {
+    using T = typename ElemOf<DT>::type;
+    const int c0 = col_of<true>(tile, past, lane, 0);
+    T *p = static_cast<T *>(row) + c0;
+    if (c0 >= 0 && c0 + 8 <= cols) {
+        Vec<8 * ElemOf<DT>::kBytes> v;
+#pragma unroll
+        for (int k = 0; k < ElemOf<DT>::kWords; ++k) v.w[k] = r.w[k];
+        st<8 * ElemOf<DT>::kBytes>(p, v);
+    } else if (c0 > -8 && c0 < cols) {
+        if (c0 >= 0 || c0 + 8 <= cols) {
+            store_part<DT>(p, r, max(-c0, 0), min(cols - c0, 8));
+        } else {  // a row within one run
+#pragma unroll 1
+            for (int j = -c0; j < cols - c0; ++j) {
+                uint32_t w = 0;
+#pragma unroll
+                for (int k = 0; k < ElemOf<DT>::kWords; ++k) w |= j * ElemOf<DT>::kBytes / 4 == k ? r.w[k] : 0u;
+                p[j] = static_cast<T>(w >> (j * ElemOf<DT>::kBytes % 4 * 8));
+            }
         }
     }
 }
 
-// The 8 elements from column c0 on, wherever they start; columns outside the row
-// are zero.  They are cut out of the 16-byte pieces around them, which lie
-// within the row but at its ends; the lanes of a warp, which take runs of one
-// row, all cut at the same place.
-template <int DT> __device__ __forceinline__ Raw8<DT> load_at(const void *row, int c0, int cols) {
+// The 8 elements from column c0 on, wherever they start, cut out of the 16-byte
+// pieces around them; the lanes of a warp, which take runs of one row, all cut
+// at the same place.  The pieces may reach `before` and `after` elements out of the
+// row; where that does not do, and in lanes without a column of the row, those
+// outside are zero.
+template <int DT> __device__ __forceinline__ Raw8<DT> load_at(const void *row, int c0, int cols, int before = 0, int after = 0) {
     constexpr int B = ElemOf<DT>::kBytes, W = ElemOf<DT>::kWords;
-    using T = typename ElemOf<DT>::type;
     const char *at = static_cast<const char *>(row) + static_cast<int64_t>(c0) * B;
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
     const int room = shift == 0 ? 0 : 16 / B;
-    Raw8<DT> r;
-    if (c0 >= room && c0 + 8 + room <= cols) {
+    if (c0 > -8 && c0 < cols && c0 - room >= -before && c0 + 8 + room <= cols + after) {
         const uint4 *q = reinterpret_cast<const uint4 *>(at - shift);
+        Raw8<DT> r;
         uint32_t v[W + 4];
 #pragma unroll
         for (int k = 0; k < W / 4; ++k) {
@@ -362,15 +408,20 @@ template <int DT> __device__ __forceinline__ Raw8<DT> load_at(const void *row, i
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) r.w[j] = v[j];
-    } else {
-        const T *p = static_cast<const T *>(row);
-#pragma unroll
-        for (int k = 0; k < W; ++k) r.w[k] = 0u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c0 + j >= 0 && c0 + j < cols) r.w[j * B / 4] |= static_cast<uint32_t>(p[c0 + j]) << (j * B % 4 * 8);
+        return r;
     }
-    return r;
+    return load_single<DT>(row, c0, cols);
+}
+// Zeros in columns outside the row.
+template <bool RUNS> __device__ __forceinline__ void clip_columns(int tile, int past, int cols, int lane, float2 (&f)[4]) {
+    const int first = tile * kTileCols - (RUNS ? past : 0);
+    if (first >= 0 && first + kTileCols <= cols) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int a = col_of<RUNS>(tile, past, lane, 2 * j), b = col_of<RUNS>(tile, past, lane, 2 * j + 1);
+        if (a < 0 || a >= cols) f[j].x = 0.0f;
+        if (b < 0 || b >= cols) f[j].y = 0.0f;
+    }
 }
 
 // One row of zeros, by a warp: whole runs of 8 elements wherever the row starts,
