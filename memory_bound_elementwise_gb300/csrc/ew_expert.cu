@@ -58,6 +58,9 @@ __device__ __forceinline__ void rank_slots(const ExpertSortArgs &a, int bits, in
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t slots = a.rows * a.k, first = static_cast<int64_t>(blockIdx.x) * tiles_each * kTileSlots;
     uint16_t *mine = count + warp * a.n_experts;
+    // a row is of no slot until one is placed there
+    for (int64_t r = blockIdx.x * static_cast<int64_t>(kSortThreads) + threadIdx.x; r < a.capacity; r += static_cast<int64_t>(gridDim.x) * kSortThreads)
+        a.slots[r] = -1;
     for (int e = threadIdx.x; e < a.n_experts; e += kSortThreads) seen[e] = 0u;
     for (int tile = 0; tile < tiles_each; ++tile) {
         const int64_t begin = first + static_cast<int64_t>(tile) * kTileSlots;
@@ -111,8 +114,8 @@ __device__ __forceinline__ void rank_slots(const ExpertSortArgs &a, int bits, in
 }
 
 // Positions from ranks: first[e] is the row of the block's first slot of expert e.
-__device__ __forceinline__ void place_slots(const ExpertSortArgs &a, int tiles_each, int64_t blocks, const uint32_t *first,
-                                            const uint32_t *total, const uint32_t *offset) {
+__device__ __forceinline__ void place_slots(const ExpertSortArgs &a, int tiles_each, const uint32_t *first, const uint32_t *total,
+                                            const uint32_t *offset) {
     const int64_t slots = a.rows * a.k, each = static_cast<int64_t>(tiles_each) * kTileSlots;
     const int64_t begin = blockIdx.x * each, end = min(begin + each, slots);
     for (int64_t s = begin + threadIdx.x; s < end; s += kSortThreads) {
@@ -122,12 +125,6 @@ __device__ __forceinline__ void place_slots(const ExpertSortArgs &a, int tiles_e
         a.positions[s] = at;
         a.slots[at] = static_cast<int32_t>(s);
     }
-    // rows of no slot: what the experts are rounded up by, and what is behind the last
-    for (int e = blockIdx.x; e < a.n_experts; e += static_cast<int>(blocks))
-        for (uint32_t r = offset[e] + total[e] + threadIdx.x; r < offset[e + 1]; r += kSortThreads) a.slots[r] = -1;
-    for (int64_t r = offset[a.n_experts] + blockIdx.x * static_cast<int64_t>(kSortThreads) + threadIdx.x; r < a.capacity;
-         r += blocks * kSortThreads)
-        a.slots[r] = -1;
     if (blockIdx.x == 0) {
         for (int e = threadIdx.x; e < a.n_experts; e += kSortThreads) a.counts[e] = static_cast<int32_t>(total[e]);
         for (int e = threadIdx.x; e <= a.n_experts; e += kSortThreads) a.offsets[e] = static_cast<int32_t>(offset[e]);
@@ -160,7 +157,7 @@ template <bool WHOLE> __global__ void __launch_bounds__(kSortThreads) expert_ran
     rank_slots(a, bits, tiles_each, count, seen);
     if constexpr (WHOLE) {
         experts_offsets(a, seen, offset, scan);
-        place_slots(a, tiles_each, 1, offset, seen, offset);
+        place_slots(a, tiles_each, offset, seen, offset);
     } else {
         for (int e = threadIdx.x; e < a.n_experts; e += kSortThreads) a.partial[static_cast<int64_t>(blockIdx.x) * a.n_experts + e] = seen[e];
     }
@@ -187,7 +184,7 @@ __global__ void __launch_bounds__(kSortThreads) expert_place_kernel(ExpertSortAr
     experts_offsets(a, total, offset, scan);
     for (int e = threadIdx.x; e < a.n_experts; e += kSortThreads) first[e] += offset[e];
     __syncthreads();
-    place_slots(a, tiles_each, blocks, first, total, offset);
+    place_slots(a, tiles_each, first, total, offset);
 }
 
 // ---------------------------------------------------------------- rows of no slot
@@ -225,21 +222,30 @@ __device__ __forceinline__ float weight_at(const void *w, int wtype, int64_t at)
     return wtype == DT_F16 ? f16_to_f32(v) : bf16_to_f32(v);
 }
 
-// A row of a matrix, and how many elements (up to 16) may be read on both its sides.
-template <int DT> struct RowAt {
-    const void *p;
-    int before, after;
-    __device__ __forceinline__ RowAt(const void *base, int64_t row, int64_t stride, int64_t rows)
-        : p(row_of<DT>(base, row, stride)), before(static_cast<int>(min(row * stride, int64_t(16)))),
-          after(static_cast<int>(min((rows - 1 - row) * stride, int64_t(16)))) {}
-    __device__ __forceinline__ Raw8<DT> load(int c0, int cols) const { return load_at<DT>(p, c0, cols, before, after); }
+// How a warp moves 256 columns of a row.  VEC: all rows start at multiples of 8
+// elements; otherwise by pairs, as they lie in the row that is written.
+template <int DT, bool VEC> struct Mover {
+    using Run = std::conditional_t<VEC, Raw8<DT>, Pairs8<DT>>;
+    int cols, lane;
+    __device__ __forceinline__ static int odd(const void *written) { return VEC ? 0 : odd_of<DT>(written); }
+    __device__ __forceinline__ Run load(const void *row, int tile, int odd) const {
+        if constexpr (VEC) return load_tile<DT, true>(row, tile * kTileCols, cols, lane);
+        else return load_pairs<DT>(row, tile, odd, cols, lane);
+    }
+    __device__ __forceinline__ static Raw8<DT> whole(const Run &r) {
+        if constexpr (VEC) return r;
+        else return r.whole();
+    }
+    __device__ __forceinline__ void store(void *row, int tile, int odd, const Raw8<DT> &r) const {
+        if constexpr (VEC) store_tile<DT, true>(row, tile * kTileCols, cols, lane, r);
+        else store_pairs<DT>(row, tile, odd, cols, lane, r);
+    }
 };
 
 // ---------------------------------------------------------------- dispatch
 
-// A warp takes U consecutive tiles of a token.  VEC: all rows start at multiples
-// of 8 elements, and a tile is read once; otherwise it is cut out of the token's
-// row anew for each of the places, whose rows may start anywhere.
+// A warp takes U consecutive tiles of a token.  VEC: a tile is read once;
+// otherwise anew for each of the places, whose rows may start anywhere.
 template <int DT, bool VEC, int U>
 __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(ExpertRowsArgs a, uint32_t zero_blocks, int zero_each, int tiles) {
     enter_grid();
@@ -252,12 +258,12 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(Expe
     const int64_t token = item / groups;
     if (token >= a.rows) return;
     const int tile0 = static_cast<int>(item - token * groups) * U;
-    const RowAt<DT> from(a.x, token, a.x_stride, a.rows);
-    const void *x = from.p;
-    Raw8<DT> r[U];
+    const Mover<DT, VEC> mover = {a.cols, lane};
+    const void *x = row_of<DT>(a.x, token, a.x_stride);
+    typename Mover<DT, VEC>::Run r[U];
     if constexpr (VEC) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = load_run<DT>(x, tile0 + u, 0, a.cols, lane, false);
+        for (int u = 0; u < U; ++u) r[u] = mover.load(x, tile0 + u, 0);
     }
     for (int j0 = 0; j0 < a.k; j0 += 32) {
         const int64_t p = position_of(a.positions, token * a.k + j0 + lane, j0 + lane < a.k, a.sorted);
@@ -265,13 +271,13 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(Expe
             const int64_t to = __shfl_sync(kAllLanes, p, j);
             if (to < 0) continue;
             void *out = row_of<DT>(a.out, to, a.out_stride);
-            const int past = VEC ? 0 : past_of<DT>(out);
+            const int odd = mover.odd(out);
             if constexpr (!VEC) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) r[u] = from.load(col_of<true>(tile0 + u, past, lane, 0), a.cols);
+                for (int u = 0; u < U; ++u) r[u] = mover.load(x, tile0 + u, odd);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) store_run<DT>(out, tile0 + u, past, a.cols, lane, r[u]);
+            for (int u = 0; u < U; ++u) mover.store(out, tile0 + u, odd, mover.whole(r[u]));
         }
     }
 }
@@ -281,41 +287,38 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(Expe
 // A warp takes U consecutive tiles of a token, and of its slots KB at a time, all
 // of whose loads are under way together.
 template <int DT, bool VEC, int KB, int U>
-__global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_kernel(ExpertRowsArgs a, int tiles) {
+__global__ void __launch_bounds__(32 * kWarpsABlock, VEC && DT != DT_F32 ? 3 : 2) expert_combine_kernel(ExpertRowsArgs a, int tiles) {
     enter_grid();
     const int lane = threadIdx.x & 31, groups = (tiles + U - 1) / U;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarpsABlock + (threadIdx.x >> 5);
     const int64_t token = item / groups;
     if (token >= a.rows) return;
     const int tile0 = static_cast<int>(item - token * groups) * U;
+    const Mover<DT, VEC> mover = {a.cols, lane};
+    using Run = typename Mover<DT, VEC>::Run;
     void *out = row_of<DT>(a.out, token, a.out_stride);
-    const int past = VEC ? 0 : past_of<DT>(out);
-    auto load = [&](const RowAt<DT> &row, int u) {
-        if constexpr (VEC) return load_run<DT>(row.p, tile0 + u, 0, a.cols, lane, false);
-        else return row.load(col_of<true>(tile0 + u, past, lane, 0), a.cols);
-    };
-    float2 sum[U][4];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (a.residual) {
-            unpack8<DT>(load(RowAt<DT>(a.residual, token, a.residual_stride, a.rows), u), sum[u]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[u][i] = both(0.0f);
-        }
-    }
+    const int odd = mover.odd(out);
+    float2 sum[U][4] = {};
     for (int j0 = 0; j0 < a.k; j0 += KB) {
         const bool mine = lane < KB && j0 + lane < a.k;
         const int64_t at = token * a.k + j0 + lane, p = position_of(a.positions, at, mine, a.sorted);
         const float w = a.weights && mine ? weight_at(a.weights, a.wtype, at) : 1.0f;
-        Raw8<DT> r[KB][U];
+        Run r[KB][U], first[U];
         int64_t from[KB];
+        if (a.residual && j0 == 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) first[u] = mover.load(row_of<DT>(a.residual, token, a.residual_stride), tile0 + u, odd);
+        }
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
             from[b] = __shfl_sync(kAllLanes, p, b);
             if (from[b] < 0) continue;
 #pragma unroll
-            for (int u = 0; u < U; ++u) r[b][u] = load(RowAt<DT>(a.x, from[b], a.x_stride, a.sorted), u);
+            for (int u = 0; u < U; ++u) r[b][u] = mover.load(row_of<DT>(a.x, from[b], a.x_stride), tile0 + u, odd);
+        }
+        if (a.residual && j0 == 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) unpack8<DT>(mover.whole(first[u]), sum[u]);
         }
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
@@ -324,14 +327,14 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_kernel(Exper
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 float2 f[4];
-                unpack8<DT>(r[b][u], f);
+                unpack8<DT>(mover.whole(r[b][u]), f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum[u][i] = fma2(f[i], wb, sum[u][i]);
             }
         }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) store_run<DT>(out, tile0 + u, past, a.cols, lane, pack8<DT>(sum[u]));
+    for (int u = 0; u < U; ++u) mover.store(out, tile0 + u, odd, pack8<DT>(sum[u]));
 }
 
 // ---------------------------------------------------------------- the gradient of combine
@@ -365,12 +368,14 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_grad_kernel(
         clear_rows<DT>(a.out, a.out_stride, a.slots, a.sorted, a.cols, zero_each);
         return;
     }
+    constexpr int kPlaces = VEC || DT == DT_F32 ? 1 : 2;
     __shared__ float part[2][kWarpsABlock][KB];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp & (split - 1);
     const int64_t token = (static_cast<int64_t>(blockIdx.x - zero_blocks) * kWarpsABlock + warp) / split;
     const bool given = token < a.rows;  // all warps stay for the barriers
-    const RowAt<DT> dout_row(a.residual, token, a.residual_stride, a.rows);
-    const void *dout = dout_row.p;  // not looked at unless the token is given
+    const Mover<DT, VEC> mover = {a.cols, lane};
+    using Run = typename Mover<DT, VEC>::Run;
+    const void *dout = row_of<DT>(a.residual, token, a.residual_stride);  // not read unless the token is given
     int turn = 0;
     for (int j0 = 0; j0 < a.k; j0 += KB, turn ^= 1) {
         const bool mine = given && lane < KB && j0 + lane < a.k;
@@ -385,39 +390,35 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_grad_kernel(
             dot[b] = 0.0f;
         }
         for (int tile = share; given && tile < tiles; tile += split) {
-            Raw8<DT> rd[VEC ? 1 : KB], ry[KB];
-            if constexpr (VEC) rd[0] = load_run<DT>(dout, tile, 0, a.cols, lane, false);
+            // dout as it lies beside rows of either place, where there are two
+            Run rd[kPlaces], ry[KB];
+#pragma unroll
+            for (int o = 0; o < kPlaces; ++o) rd[o] = mover.load(dout, tile, o);
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 if (row[b] < 0) continue;
-                const RowAt<DT> y(a.x, row[b], a.x_stride, a.sorted);
-                if constexpr (VEC) {
-                    if (a.x) ry[b] = load_run<DT>(y.p, tile, 0, a.cols, lane, false);
-                } else {
-                    const int c0 = col_of<true>(tile, past_of<DT>(row_of<DT>(a.out, row[b], a.out_stride)), lane, 0);
-                    rd[b] = dout_row.load(c0, a.cols);
-                    if (a.x) ry[b] = y.load(c0, a.cols);
-                }
+                const int odd = mover.odd(row_of<DT>(a.out, row[b], a.out_stride));
+                if (a.x) ry[b] = mover.load(row_of<DT>(a.x, row[b], a.x_stride), tile, odd);
             }
+            float2 d[kPlaces][4];
+#pragma unroll
+            for (int o = 0; o < kPlaces; ++o) unpack8<DT>(mover.whole(rd[o]), d[o]);
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 if (row[b] < 0) continue;
-                float2 d[4], o[4];
-                unpack8<DT>(rd[VEC ? 0 : b], d);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = mul2(d[i], both(wb[b]));
                 void *out = row_of<DT>(a.out, row[b], a.out_stride);
-                store_run<DT>(out, tile, VEC ? 0 : past_of<DT>(out), a.cols, lane, pack8<DT>(o));
+                const int odd = mover.odd(out);
+                float2 own[4], o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) own[i] = kPlaces == 2 && odd ? d[kPlaces - 1][i] : d[0][i];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[i] = mul2(own[i], both(wb[b]));
+                mover.store(out, tile, odd, pack8<DT>(o));
                 if (a.x) {
                     float2 f[4], s = both(0.0f);
-                    unpack8<DT>(ry[b], f);
-                    if constexpr (!VEC) {
-                        const int past = past_of<DT>(out);
-                        clip_columns<true>(tile, past, a.cols, lane, f);
-                        clip_columns<true>(tile, past, a.cols, lane, d);
-                    }
+                    unpack8<DT>(mover.whole(ry[b]), f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s = fma2(f[i], d[i], s);
+                    for (int i = 0; i < 4; ++i) s = fma2(f[i], own[i], s);
                     dot[b] += s.x + s.y;
                 }
             }
@@ -437,8 +438,13 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_grad_kernel(
 
 // ---------------------------------------------------------------- launches
 
-int tiles_of(int cols, bool vec) { return static_cast<int>((static_cast<int64_t>(cols) + (vec ? 0 : 7) + kTileCols - 1) / kTileCols); }
-int slots_at_once(int k) { return k <= 1 ? 1 : k <= 2 ? 2 : k <= 4 ? 4 : 8; }
+int tiles_of(int cols, bool vec) { return static_cast<int>((static_cast<int64_t>(cols) + (vec ? 0 : 1) + kTileCols - 1) / kTileCols); }
+// Slots whose loads are under way together: as many as registers allow.
+int slots_at_once(int k, int most) {
+    int kb = 1;
+    while (kb < most && kb < k) kb *= 2;
+    return kb;
+}
 
 template <int DT, bool VEC> cudaError_t dispatch_launch(const ExpertRowsArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
     const int tiles = tiles_of(a.cols, VEC);
@@ -449,13 +455,13 @@ template <int DT, bool VEC> cudaError_t dispatch_launch(const ExpertRowsArgs &a,
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     info->grid = static_cast<int>(grid);
     info->block = 32 * kWarpsABlock;
-    info->vec_bytes = 8 * ElemOf<DT>::kBytes;
+    info->vec_bytes = VEC ? 8 * ElemOf<DT>::kBytes : 4;
     auto kernel = many ? expert_dispatch_kernel<DT, VEC, 4> : expert_dispatch_kernel<DT, VEC, 1>;
     return launch_rows(kernel, dim3(grid), dim3(32 * kWarpsABlock), 0, 1, s, a, static_cast<uint32_t>(zeros), each, tiles);
 }
 
 template <int DT, bool VEC, int KB> cudaError_t combine_launch(const ExpertRowsArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
-    constexpr int U = 8 / KB;
+    constexpr int U = KB == 1 ? 4 : KB == 2 || (KB == 4 && VEC && DT != DT_F32) ? 2 : 1;
     const int tiles = tiles_of(a.cols, VEC);
     const bool many = a.rows * tiles >= static_cast<int64_t>(sms) * 64;
     const int u = many ? U : 1;
@@ -463,7 +469,7 @@ template <int DT, bool VEC, int KB> cudaError_t combine_launch(const ExpertRowsA
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     info->grid = static_cast<int>(grid);
     info->block = 32 * kWarpsABlock;
-    info->vec_bytes = 8 * ElemOf<DT>::kBytes;
+    info->vec_bytes = VEC ? 8 * ElemOf<DT>::kBytes : 4;
     auto kernel = many ? expert_combine_kernel<DT, VEC, KB, U> : expert_combine_kernel<DT, VEC, KB, 1>;
     return launch_rows(kernel, dim3(grid), dim3(32 * kWarpsABlock), 0, 1, s, a, tiles);
 }
@@ -477,22 +483,27 @@ template <int DT, bool VEC, int KB> cudaError_t combine_grad_launch(const Expert
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
     info->grid = static_cast<int>(grid);
     info->block = 32 * kWarpsABlock;
-    info->vec_bytes = 8 * ElemOf<DT>::kBytes;
+    info->vec_bytes = VEC ? 8 * ElemOf<DT>::kBytes : 4;
     return launch_rows(expert_combine_grad_kernel<DT, VEC, KB>, dim3(grid), dim3(32 * kWarpsABlock), 0, 1, s, a,
                        static_cast<uint32_t>(zeros), each, tiles, split);
 }
 
 template <int DT, bool VEC> cudaError_t by_slots(int what, const ExpertRowsArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
-    const int kb = slots_at_once(a.k);
-    if (what == EXPERT_COMBINE)
-        return kb == 1   ? combine_launch<DT, VEC, 1>(a, sms, s, info)
-               : kb == 2 ? combine_launch<DT, VEC, 2>(a, sms, s, info)
-               : kb == 4 ? combine_launch<DT, VEC, 4>(a, sms, s, info)
-                         : combine_launch<DT, VEC, 8>(a, sms, s, info);
-    return kb == 1   ? combine_grad_launch<DT, VEC, 1>(a, sms, s, info)
-           : kb == 2 ? combine_grad_launch<DT, VEC, 2>(a, sms, s, info)
-           : kb == 4 ? combine_grad_launch<DT, VEC, 4>(a, sms, s, info)
-                     : combine_grad_launch<DT, VEC, 8>(a, sms, s, info);
+    constexpr int kCombine = VEC || DT != DT_F32 ? 8 : 4, kGrad = VEC ? 8 : DT != DT_F32 ? 4 : 2;
+    if (what == EXPERT_COMBINE) {
+        switch (slots_at_once(a.k, kCombine)) {
+            case 1: return combine_launch<DT, VEC, 1>(a, sms, s, info);
+            case 2: return combine_launch<DT, VEC, 2>(a, sms, s, info);
+            case 4: return combine_launch<DT, VEC, 4>(a, sms, s, info);
+            default: return combine_launch<DT, VEC, kCombine>(a, sms, s, info);
+        }
+    }
+    switch (slots_at_once(a.k, kGrad)) {
+        case 1: return combine_grad_launch<DT, VEC, 1>(a, sms, s, info);
+        case 2: return combine_grad_launch<DT, VEC, 2>(a, sms, s, info);
+        case 4: return combine_grad_launch<DT, VEC, std::min(kGrad, 4)>(a, sms, s, info);
+        default: return combine_grad_launch<DT, VEC, kGrad>(a, sms, s, info);
+    }
 }
 template <int DT> bool all_wide(const ExpertRowsArgs &a) {
     return wide_rows<DT>(a.x, a.x_stride) && wide_rows<DT>(a.residual, a.residual_stride) && wide_rows<DT>(a.out, a.out_stride);

@@ -51,8 +51,8 @@ __device__ __forceinline__ void load_columns(const void *w, bool f32, float othe
     } else {
         const int c0 = col_of<true>(tile, past, lane, 0);
         if (c0 >= 8 && c0 + 16 <= cols) {
-            if (DT == DT_F32 || f32) unpack8<DT_F32>(load_at<DT_F32>(w, c0, cols), f);
-            else unpack8<DT>(load_at<DT>(w, c0, cols), f);
+            if (DT == DT_F32 || f32) unpack8<DT_F32>(cut_run<DT_F32>(w, c0), f);
+            else unpack8<DT>(cut_run<DT>(w, c0), f);
             return;
         }
         // at its ends element by element, all under way together

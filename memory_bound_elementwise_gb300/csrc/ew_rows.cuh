@@ -376,41 +376,27 @@ template <int DT> __device__ __forceinline__ void store_run(void *row, int tile,
 }
 
 // The 8 elements from column c0 on, wherever they start, cut out of the 16-byte
-// pieces around them; the lanes of a warp, which take runs of one row, all cut
-// at the same place.  The pieces may reach `before` and `after` elements out of the
-// row; where that does not do, and in lanes without a column of the row, those
-// outside are zero.
-template <int DT> __device__ __forceinline__ Raw8<DT> load_at(const void *row, int c0, int cols, int before = 0, int after = 0) {
+// pieces around them, which may reach up to 7 elements out of the run.
+template <int DT> __device__ __forceinline__ Raw8<DT> cut_run(const void *row, int c0) {
     constexpr int B = ElemOf<DT>::kBytes, W = ElemOf<DT>::kWords;
     const char *at = static_cast<const char *>(row) + static_cast<int64_t>(c0) * B;
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
-    const int room = shift == 0 ? 0 : 16 / B;
-    if (c0 > -8 && c0 < cols && c0 - room >= -before && c0 + 8 + room <= cols + after) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(at - shift);
-        Raw8<DT> r;
-        uint32_t v[W + 4];
+    const uint4 *q = reinterpret_cast<const uint4 *>(at - shift);
+    uint32_t v[W + 4] = {};
 #pragma unroll
-        for (int k = 0; k < W / 4; ++k) {
+    for (int k = 0; k < W / 4 + 1; ++k)
+        if (k < W / 4 || shift != 0) {
             const uint4 a = q[k];
             v[4 * k] = a.x, v[4 * k + 1] = a.y, v[4 * k + 2] = a.z, v[4 * k + 3] = a.w;
         }
-        if (shift != 0) {
-            const uint4 a = q[W / 4];
-            v[W] = a.x, v[W + 1] = a.y, v[W + 2] = a.z, v[W + 3] = a.w;
 #pragma unroll
-            for (int j = 0; j < W + 2; ++j) v[j] = shift & 8 ? v[j + 2] : v[j];
+    for (int j = 0; j < W + 2; ++j) v[j] = shift & 8 ? v[j + 2] : v[j];
 #pragma unroll
-            for (int j = 0; j < W + 1; ++j) v[j] = shift & 4 ? v[j + 1] : v[j];
-            if constexpr (B == 2) {
+    for (int j = 0; j < W + 1; ++j) v[j] = shift & 4 ? v[j + 1] : v[j];
+    Raw8<DT> r;
 #pragma unroll
-                for (int j = 0; j < W; ++j) v[j] = __funnelshift_r(v[j], v[j + 1], (shift & 3) * 8);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j) r.w[j] = v[j];
-        return r;
-    }
-    return load_single<DT>(row, c0, cols);
+    for (int j = 0; j < W; ++j) r.w[j] = B == 4 ? v[j] : __funnelshift_r(v[j], v[j + 1], (shift & 3) * 8);
+    return r;
 }
 // Zeros in columns outside the row.
 template <bool RUNS> __device__ __forceinline__ void clip_columns(int tile, int past, int cols, int lane, float2 (&f)[4]) {
@@ -421,6 +407,89 @@ template <bool RUNS> __device__ __forceinline__ void clip_columns(int tile, int 
         const int a = col_of<RUNS>(tile, past, lane, 2 * j), b = col_of<RUNS>(tile, past, lane, 2 * j + 1);
         if (a < 0 || a >= cols) f[j].x = 0.0f;
         if (b < 0 || b >= cols) f[j].y = 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------- pairs
+//
+// Rows that lie apart, by what lies at multiples of 4 bytes in the row that is
+// written: lane l of a warp has the pairs of 16-bit elements l, l + 32, .. of its
+// 256 columns, the first pair of a row beginning `odd` elements (0 or 1) before it;
+// of binary32 the elements l, l + 32, ...  A row that is read may lie half a word
+// off: then its elements are read one by one, and put together when they are needed,
+// so that loads of several rows are under way together.
+template <int DT> __host__ __device__ __forceinline__ int odd_of(const void *row) {
+    return DT == DT_F32 ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1 & 1);
+}
+template <int DT> struct Pairs8 {
+    uint32_t a[8];  // words, then what belongs into their upper halves; of binary32 elements
+    __device__ __forceinline__ Raw8<DT> whole() const {
+        Raw8<DT> r;
+#pragma unroll
+        for (int j = 0; j < ElemOf<DT>::kWords; ++j) r.w[j] = DT == DT_F32 ? a[j] : a[j] | a[(j + 4) & 7] << 16;
+        return r;
+    }
+};
+template <int DT> __device__ __forceinline__ Pairs8<DT> load_pairs(const void *row, int tile, int odd, int cols, int lane) {
+    Pairs8<DT> r;
+    const int first = tile * kTileCols - odd;
+    if constexpr (DT == DT_F32) {
+        const uint32_t *p = static_cast<const uint32_t *>(row) + first + lane;
+        if (first + kTileCols <= cols) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r.a[j] = p[j * 32];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r.a[j] = first + j * 32 + lane < cols ? p[j * 32] : 0u;
+        }
+    } else {
+        const int c0 = first + 2 * lane;
+        const uint16_t *p = static_cast<const uint16_t *>(row) + c0;
+        const bool words = (reinterpret_cast<uintptr_t>(p) & 3) == 0;
+        if (words && first >= 0 && first + kTileCols <= cols) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r.a[j] = *reinterpret_cast<const uint32_t *>(p + j * 64);
+#pragma unroll
+            for (int j = 4; j < 8; ++j) r.a[j] = 0u;
+        } else if (first >= 0 && first + kTileCols <= cols) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r.a[j] = p[j * 64];
+                r.a[j + 4] = p[j * 64 + 1];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = c0 + j * 64;
+                r.a[j] = c >= 0 && c < cols ? p[j * 64] : 0u;
+                r.a[j + 4] = c + 1 < cols ? p[j * 64 + 1] : 0u;
+            }
+        }
+    }
+    return r;
+}
+template <int DT> __device__ __forceinline__ void store_pairs(void *row, int tile, int odd, int cols, int lane, const Raw8<DT> &r) {
+    const int first = tile * kTileCols - odd;
+    const bool whole = first >= 0 && first + kTileCols <= cols;
+    if constexpr (DT == DT_F32) {
+        uint32_t *p = static_cast<uint32_t *>(row) + first + lane;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (whole || first + j * 32 + lane < cols) p[j * 32] = r.w[j];
+    } else {
+        const int c0 = first + 2 * lane;
+        uint16_t *p = static_cast<uint16_t *>(row) + c0;
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t *>(p + j * 64) = r.w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = c0 + j * 64;
+                if (c >= 0 && c < cols) p[j * 64] = static_cast<uint16_t>(r.w[j]);
+                if (c + 1 < cols) p[j * 64 + 1] = static_cast<uint16_t>(r.w[j] >> 16);
+            }
+        }
     }
 }
 
