@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(Expe
 // A warp takes U consecutive tiles of a token, and of its slots KB at a time, all
 // of whose loads are under way together.
 template <int DT, bool VEC, int KB, int U>
-__global__ void __launch_bounds__(32 * kWarpsABlock, VEC && DT != DT_F32 ? 3 : 2) expert_combine_kernel(ExpertRowsArgs a, int tiles) {
+__global__ void __launch_bounds__(32 * kWarpsABlock, !VEC && (KB <= 2 || DT == DT_F32) ? 4 : DT != DT_F32 ? 3 : 2) expert_combine_kernel(ExpertRowsArgs a, int tiles) {
     enter_grid();
     const int lane = threadIdx.x & 31, groups = (tiles + U - 1) / U;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarpsABlock + (threadIdx.x >> 5);
@@ -461,7 +461,7 @@ template <int DT, bool VEC> cudaError_t dispatch_launch(const ExpertRowsArgs &a,
 }
 
 template <int DT, bool VEC, int KB> cudaError_t combine_launch(const ExpertRowsArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
-    constexpr int U = KB == 1 ? 4 : KB == 2 || (KB == 4 && VEC && DT != DT_F32) ? 2 : 1;
+    constexpr int U = VEC && DT != DT_F32 ? (KB == 1 ? 4 : KB == 8 ? 1 : 2) : VEC ? (KB == 1 ? 4 : KB == 2 ? 2 : 1) : 1;
     const int tiles = tiles_of(a.cols, VEC);
     const bool many = a.rows * tiles >= static_cast<int64_t>(sms) * 64;
     const int u = many ? U : 1;
@@ -489,7 +489,7 @@ template <int DT, bool VEC, int KB> cudaError_t combine_grad_launch(const Expert
 }
 
 template <int DT, bool VEC> cudaError_t by_slots(int what, const ExpertRowsArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
-    constexpr int kCombine = VEC || DT != DT_F32 ? 8 : 4, kGrad = VEC ? 8 : DT != DT_F32 ? 4 : 2;
+    constexpr int kCombine = VEC ? 8 : 4, kGrad = VEC ? 8 : DT != DT_F32 ? 4 : 2;
     if (what == EXPERT_COMBINE) {
         switch (slots_at_once(a.k, kCombine)) {
             case 1: return combine_launch<DT, VEC, 1>(a, sms, s, info);
