@@ -170,226 +170,297 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) polic
 // row), two of 256 for rows up to 64 KiB, four of 128 up to 32 KiB.  The block's
 // share of a row is `groups` groups of 4 chunks a thread; a ring of kRing groups is
 // filled by asynchronous copies in the order of the stream of groups, row after
-// row, those without a token left out, and a group's place is filled again as soon
-// as the gradient (or, for the loss alone, the sum) has used it.  So kRing - groups
-// groups of rows to come are on their way at any time, through the reductions too.
-// Each thread copies and reads its own chunks only: it waits for its own copies
-// and needs no barrier for them.  A row has one barrier, between its sums and its
-// gradient; its loss and slope are worked out by every thread for itself.
+// row, and a group's place is filled again as soon as the gradient (or, for the
+// loss alone, the sum) has used it.  Of a share of more than kRing groups the first
+// ones give way while the row is summed; they are copied again, from L2, behind
+// the row's last, and their gradient comes last.  That is cheaper than more blocks
+// for a row, whose sums take another barrier and a read across the cluster: 2048
+// rows of 131072 bf16 took 208 us by clusters of two.  Each thread copies and
+// reads its own chunks only: it waits for its own copies and needs no barrier for
+// them.  A row has one barrier, between its sums and its gradient; its loss and
+// slope are worked out by every thread for itself.
+//
+// Rows without a token cost a write and no read, so rows are not dealt out by their
+// numbers: the rows with a token, in their order, go round the blocks (or
+// clusters), and so do those without, from the last block on.  Each block works its
+// list out for itself, from all tokens: 8 bytes a row, where a row has thousands.
+// 2048 rows of 131072 bf16, a quarter of them without a token, took 188 us by
+// numbers and 182 us by lists.
 //
 // Tokens, their numbers and logits are read for 32 of the block's rows at once, one
 // to a lane: what a row needs comes from a register.
 
 constexpr int kGroup = 4;
 constexpr int kRing = 6;
+constexpr int kMostGroups = 8;
 template <int T> struct Stream {  // T threads
     static constexpr int kGroupChunks = kGroup * T;
     static constexpr int kBlocks = 512 / T;  // an SM's
     static constexpr int kSmem = kRing * kGroupChunks * 16;
+    static constexpr int kLooks = 8;         // tokens that a thread looks at together
+    static constexpr int kSlab = kLooks * T;
+    static constexpr int kList = 4 * T;      // rows of a block's list, and rounds of the blocks in a window of rows
 };
 
-template <int DT, bool GRAD, int THREADS>
+// AGAIN: groups of a row that are copied twice; of 1 or more, a row has kRing + AGAIN.
+template <int DT, bool GRAD, int THREADS, int AGAIN>
 __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
     policy_stream_kernel(const __grid_constant__ PolicyArgs a, Split split, int groups) {
     using T = typename ElemOf<DT>::type;
-    constexpr int kGroupChunks = Stream<THREADS>::kGroupChunks, kWarps = THREADS / 32;
+    using S = Stream<THREADS>;
+    constexpr int kGroupChunks = S::kGroupChunks, kWarps = THREADS / 32, kCounts = S::kLooks * kWarps;
+    static_assert(kCounts % 32 == 0, "counts go round the lanes");
     enter_grid();
     extern __shared__ uint4 dynamic[];
     __shared__ Sums part[2][kWarps];
     __shared__ Sums mine[2];
     __shared__ float fpart[32];
+    __shared__ int list[S::kList + 2];  // with a token from the front, without from the back
+    __shared__ int counts[kCounts];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     uint4 *ring = dynamic + tid;
     const uint32_t ring_at = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const int blocks = split.blocks(), block = blockIdx.x & (blocks - 1);
-    const int64_t step = gridDim.x >> split.shift, first_row = blockIdx.x >> split.shift;
+    const unsigned step = gridDim.x >> split.shift, me = blockIdx.x >> split.shift;
+    if (AGAIN > 0) groups = kRing + AGAIN;
     const float ax = a.scale * kLog2e;
     auto share_of = [&](int64_t row) {
         return Share<DT>(row_of<DT>(a.logits, row, a.stride), a.cols, block, split);
     };
     // -1: none
     auto token_of = [&](int64_t row) {
-        if (row >= a.rows) return -1;
         const int64_t token = token_at(a.tokens, a.i64, row);
         return token >= 0 && token < a.cols ? static_cast<int>(token) : -1;
     };
-
-    // Copies: the next group of the stream into the ring; past the last row an empty
-    // one, so that the count holds.
-    int64_t copy_base = first_row - 32 * step, copy_row = a.rows;  // of 32 rows, of which `copy_left` are to come
-    unsigned copy_left = 0;
-    int copy_group = 0, copy_place = 0, copy_count = 0;  // chunks of this thread's row from its next one on
-    const T *copy_from = nullptr;
-    auto next_copy_row = [&] {
-        while (copy_left == 0 && copy_base + 32 * step < a.rows) {
-            copy_base += 32 * step;
-            copy_left = __ballot_sync(kAllLanes, token_of(copy_base + lane * step) >= 0);
-        }
-        copy_count = 0;
-        copy_row = a.rows;
-        if (copy_left == 0) return;
-        copy_row = copy_base + (__ffs(copy_left) - 1) * step;
-        copy_left &= copy_left - 1;
-        const Share<DT> sh = share_of(copy_row);
-        copy_from = sh.row + sh.column(sh.first + tid, 0);
-        copy_count = sh.end - sh.first - tid;
-    };
-    auto copy_next = [&] {
+    int turn = 0;
+#pragma unroll 1
+    for (int64_t base = 0; base < a.rows; base += static_cast<int64_t>(step) * S::kList) {
+        // The block's rows of this window: ranks among those with a token, and without.
+        const int window = static_cast<int>(min(a.rows - base, static_cast<int64_t>(step) * S::kList));
+        unsigned with = 0;
+#pragma unroll 1
+        for (int slab = 0; slab < window; slab += S::kSlab) {
+            unsigned given[S::kLooks];
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
-            if (u * THREADS < copy_count)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                             :: "r"(ring_at + (copy_place * kGroup + u) * THREADS * 16),
-                                "l"(copy_from + u * THREADS * Chunk<DT>::kElems) : "memory");
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        copy_from += kGroupChunks * Chunk<DT>::kElems;
-        copy_count -= kGroupChunks;
-        if (++copy_group == groups) {
-            copy_group = 0;
-            if (copy_row < a.rows) next_copy_row();
+            for (int j = 0; j < S::kLooks; ++j) {
+                const int at = slab + j * THREADS + tid;
+                given[j] = at < window && token_of(base + at) >= 0;
+            }
+#pragma unroll
+            for (int j = 0; j < S::kLooks; ++j) given[j] = __ballot_sync(kAllLanes, given[j] != 0);
+            __syncthreads();  // the counts before, and the list of the window before, have been read
+#pragma unroll
+            for (int j = 0; j < S::kLooks; ++j)
+                if (lane == 0) counts[j * kWarps + warp] = __popc(given[j]);
+            __syncthreads();
+            int some[kCounts / 32], total = 0;
+#pragma unroll
+            for (int i = 0; i < kCounts / 32; ++i) total += some[i] = counts[i * 32 + lane];
+#pragma unroll
+            for (int j = 0; j < S::kLooks; ++j) {
+                const int own = j * kWarps + warp, at = slab + j * THREADS + tid;
+                int earlier = 0;
+#pragma unroll
+                for (int i = 0; i < kCounts / 32; ++i) earlier += i * 32 + lane < own ? some[i] : 0;
+                const unsigned before = with + __reduce_add_sync(kAllLanes, earlier) + __popc(given[j] & ((1u << lane) - 1u));
+                if (at >= window) continue;
+                if (given[j] >> lane & 1) {
+                    if (before % step == me) list[before / step] = at;
+                } else {
+                    const unsigned without = at - before;
+                    if (without % step == step - 1 - me) list[S::kList + 1 - without / step] = at;
+                }
+            }
+            with += __reduce_add_sync(kAllLanes, total);
         }
-        if (++copy_place == kRing) copy_place = 0;
-    };
-    auto held = [&](int place, int u) {
-        const uint4 w = ring[(place * kGroup + u) * THREADS];
-        return Chunk<DT>{{w.x, w.y, w.z, w.w}};
-    };
-    next_copy_row();
-#pragma unroll 1
-    for (int q = 0; q < kRing; ++q) copy_next();
+        const int rows = static_cast<int>((with + step - 1 - me) / step), empty_rows = static_cast<int>((window - with + me) / step);
+        __syncthreads();
 
-    int place0 = 0;  // the ring's place of the row's first group
-    int turn = 0, number = 0;
-    int my_token = -1;  // of 32 rows, this lane's
-    float my_x = 0.0f;
-    PolicyToken my = {};
+        // Copies: the next group of the stream into the ring; past the last row an empty
+        // one, so that the count holds.
+        int copy_number = 0, copy_group = 0, copy_place = 0, copy_count = 0;  // chunks of this thread's row from its next one on
+        const T *copy_from = nullptr;
+        auto start_copies = [&] {
+            copy_count = 0;
+            if (copy_number < rows) {
+                const Share<DT> sh = share_of(base + list[copy_number]);
+                copy_from = sh.row + sh.column(sh.first + tid, 0);
+                copy_count = sh.end - sh.first - tid;
+            }
+        };
+        auto copy_next = [&] {
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u)
+                if (u * THREADS < copy_count)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                 :: "r"(ring_at + (copy_place * kGroup + u) * THREADS * 16),
+                                    "l"(copy_from + u * THREADS * Chunk<DT>::kElems) : "memory");
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            copy_from += kGroupChunks * Chunk<DT>::kElems;
+            copy_count -= kGroupChunks;
+            ++copy_group;
+            if (AGAIN > 0 && copy_group == groups) start_copies();
+            if (copy_group == groups + AGAIN) {
+                copy_group = 0;
+                ++copy_number;
+                start_copies();
+            }
+            if (++copy_place == kRing) copy_place = 0;
+        };
+        auto held = [&](int place, int u) {
+            const uint4 w = ring[(place * kGroup + u) * THREADS];
+            return Chunk<DT>{{w.x, w.y, w.z, w.w}};
+        };
+        start_copies();
 #pragma unroll 1
-    for (int64_t row = first_row; row < a.rows; row += step, ++number) {
-        const int from = number & 31;
-        if (from == 0) {
-            const int64_t own = row + lane * step;
-            my_token = token_of(own);
-            if (my_token >= 0) {
+        for (int q = 0; q < kRing; ++q) copy_next();
+
+#pragma unroll 1
+        for (int i = 0; i < empty_rows; ++i) {
+            const int64_t row = base + list[S::kList + 1 - i];
+            if (block == 0 && tid == 0) write_results(a, row, 0.0f, 0.0f, 0.0f);
+            if (GRAD) write_zeros<DT>(row_of<DT>(a.dlogits, row, a.dstride), a.cols, block, split, THREADS);
+        }
+
+        int next_place = 0;  // the ring's place of the stream's next group
+        auto take_place = [&] {
+            const int place = next_place;
+            if (++next_place == kRing) next_place = 0;
+            return place;
+        };
+        int my_token = -1;  // of 32 rows, this lane's
+        float my_x = 0.0f;
+        PolicyToken my = {};
+#pragma unroll 1
+        for (int number = 0; number < rows; ++number) {
+            const int from = number & 31;
+            const int64_t row = base + list[number];
+            if (from == 0 && number + lane < rows) {
+                const int64_t own = base + list[number + lane];
+                my_token = token_of(own);
                 my = policy_token(a, own, GRAD);
                 my_x = share_of(own).at(my_token);
             }
-        }
-        const int col = __shfl_sync(kAllLanes, my_token, from);
-        if (col < 0) {  // nothing is copied, summed or waited for
-            if (block == 0 && tid == 0) write_results(a, row, 0.0f, 0.0f, 0.0f);
-            if (GRAD) write_zeros<DT>(row_of<DT>(a.dlogits, row, a.dstride), a.cols, block, split, THREADS);
-            continue;
-        }
-        const Share<DT> sh = share_of(row);
-        const bool single = tid < sh.singles;
-        const float one = single ? sh.at(sh.single(tid)) : kNegInf;
+            const int col = __shfl_sync(kAllLanes, my_token, from);
+            const Share<DT> sh = share_of(row);
+            const bool single = tid < sh.singles;
+            const float one = single ? sh.at(sh.single(tid)) : kNegInf;
 
-        PairSums pairs = {kLeastExponent, both(0.0f), both(0.0f)};
-        auto add_group = [&](int g) {
-            int place = place0 + g;
-            if (place >= kRing) place -= kRing;
-            Chunk<DT> r[kGroup];
-            const int c0 = sh.first + g * kGroupChunks;
-            if (c0 + kGroupChunks <= sh.end) {
+            PairSums pairs = {kLeastExponent, both(0.0f), both(0.0f)};
+            int held_from = next_place + AGAIN;  // the place of the first group that stays
+            if (held_from >= kRing) held_from -= kRing;
+            auto add_group = [&](int g) {
+                const int place = take_place();
+                Chunk<DT> r[kGroup];
+                const int c0 = sh.first + g * kGroupChunks;
+                if (c0 + kGroupChunks <= sh.end) {
 #pragma unroll
-                for (int u = 0; u < kGroup; ++u) r[u] = held(place, u);
-            } else {
+                    for (int u = 0; u < kGroup; ++u) r[u] = held(place, u);
+                } else {
 #pragma unroll
-                for (int u = 0; u < kGroup; ++u)
-                    r[u] = c0 + u * THREADS + tid < sh.end ? held(place, u) : masked_chunk<DT>();
+                    for (int u = 0; u < kGroup; ++u)
+                        r[u] = c0 + u * THREADS + tid < sh.end ? held(place, u) : masked_chunk<DT>();
+                }
+                add_chunks<DT, false>(pairs, r, ax);
+                if (!GRAD || g < AGAIN) copy_next();
+            };
+            // A group is complete when only the groups asked for after it are left: kRing - 1
+            // while each group used is one more asked for, one less for each that stays.
+            static_assert(kRing == 6 && kMostGroups == 8, "one wait for each group below");
+            auto left = [](int g) constexpr { return !GRAD || g <= AGAIN ? 5 : g < 5 + AGAIN ? 5 + AGAIN - g : 0; };
+            copies_left<5>();
+            add_group(0);
+            if (groups > 1) { copies_left<left(1)>(); add_group(1); }
+            if (groups > 2) { copies_left<left(2)>(); add_group(2); }
+            if (groups > 3) { copies_left<left(3)>(); add_group(3); }
+            if (groups > 4) { copies_left<left(4)>(); add_group(4); }
+            if (groups > 5) { copies_left<left(5)>(); add_group(5); }
+            if (groups > 6) { copies_left<left(6)>(); add_group(6); }
+            if (groups > 7) { copies_left<left(7)>(); add_group(7); }
+
+            Sums v = warp_sums<32, false>(finished<DT, false>(pairs, single, one, ax));
+            if (lane == 0) part[turn][warp] = v;
+            __syncthreads();
+            v = sums_of_warps<kWarps, false>(part[turn]);
+            if (blocks > 1) {
+                if (tid == 0) mine[turn] = v;
+                cluster_sync();  // the next row's keeps mine[turn] from being written before all have read it
+                v = cluster_sums<false>(&mine[turn], blocks);
             }
-            add_chunks<DT, false>(pairs, r, ax);
-            if (!GRAD) copy_next();
-        };
-        // Group g of the row is complete when only the groups after it are left:
-        // kRing - 1 - g have been asked for since, or, with one more for each
-        // group that the loss alone has used, kRing - 1.
-        static_assert(kRing == 6, "one wait for each group below");
-        copies_left<5>();
-        add_group(0);
-        if (groups > 1) { copies_left<GRAD ? 4 : 5>(); add_group(1); }
-        if (groups > 2) { copies_left<GRAD ? 3 : 5>(); add_group(2); }
-        if (groups > 3) { copies_left<GRAD ? 2 : 5>(); add_group(3); }
-        if (groups > 4) { copies_left<GRAD ? 1 : 5>(); add_group(4); }
-        if (groups > 5) { copies_left<GRAD ? 0 : 5>(); add_group(5); }
-
-        Sums v = warp_sums<32, false>(finished<DT, false>(pairs, single, one, ax));
-        if (lane == 0) part[turn][warp] = v;
-        __syncthreads();
-        v = sums_of_warps<kWarps, false>(part[turn]);
-        if (blocks > 1) {
-            if (tid == 0) mine[turn] = v;
-            cluster_sync();  // the next row's keeps mine[turn] from being written before all have read it
-            v = cluster_sums<false>(&mine[turn], blocks);
-        }
-        turn ^= 1;
-        RowSum r;
-        if (v.s > 0.0f && v.s < 1e37f) {
-            r = {v.c, logf(v.s), 1.0f / v.s, 0.0f, 0.0f, false};
-        } else {
-            // a careful row is read whole by every thread of every block: all are done with it before any writes in place
-            r = careful_row<DT>(sh.row, a.cols, ax, fpart);
-            if (blocks > 1) cluster_sync();
-        }
-        const float x = __shfl_sync(kAllLanes, my_x, from);
-        const PolicyToken t = {__shfl_sync(kAllLanes, my.advantage, from), __shfl_sync(kAllLanes, my.old_logp, from),
-                               __shfl_sync(kAllLanes, my.ref_logp, from), __shfl_sync(kAllLanes, my.dloss, from)};
-        const bool empty = is_empty(r);
-        const float logp = empty ? kNegInf : logp_of(r, x, ax, a.scale);
-        const PolicyTerms terms = policy_terms(a, t, logp);
-        if (block == 0 && tid == 0) write_results(a, row, terms.loss, logp, empty ? kNegInf : lse_of(r, a.scale));
-        if constexpr (GRAD) {
-            T *out = static_cast<T *>(row_of<DT>(a.dlogits, row, a.dstride));
-            const float factor = policy_factor(a, t, terms);
-            const RowGrad rg = row_grad({r.c, r.inv_s, r.top, r.careful}, -factor, 0.0f, 0.0f, 0.0f);
-            const int apart = bytes_apart(out, sh);
-            const ChunkGrad<DT, false> grad(rg, ax);
-            const float at_token = grad_of<false>(rg, x, ax, a.scale) + factor;
+            turn ^= 1;
+            RowSum r;
+            if (v.s > 0.0f && v.s < 1e37f) {
+                r = {v.c, logf(v.s), 1.0f / v.s, 0.0f, 0.0f, false};
+            } else {
+                // a careful row is read whole by every thread of every block: all are done with it before any writes in place
+                r = careful_row<DT>(sh.row, a.cols, ax, fpart);
+                if (blocks > 1) cluster_sync();
+            }
+            const float x = __shfl_sync(kAllLanes, my_x, from);
+            const PolicyToken t = {__shfl_sync(kAllLanes, my.advantage, from), __shfl_sync(kAllLanes, my.old_logp, from),
+                                   __shfl_sync(kAllLanes, my.ref_logp, from), __shfl_sync(kAllLanes, my.dloss, from)};
+            const bool empty = is_empty(r);
+            const float logp = empty ? kNegInf : logp_of(r, x, ax, a.scale);
+            const PolicyTerms terms = policy_terms(a, t, logp);
+            if (block == 0 && tid == 0) write_results(a, row, terms.loss, logp, empty ? kNegInf : lse_of(r, a.scale));
+            if constexpr (GRAD) {
+                T *out = static_cast<T *>(row_of<DT>(a.dlogits, row, a.dstride));
+                const float factor = policy_factor(a, t, terms);
+                const RowGrad rg = row_grad({r.c, r.inv_s, r.top, r.careful}, -factor, 0.0f, 0.0f, 0.0f);
+                const int apart = bytes_apart(out, sh);
+                const ChunkGrad<DT, false> grad(rg, ax);
+                const float at_token = grad_of<false>(rg, x, ax, a.scale) + factor;
+                // first the groups that stayed, then those that were copied again
 #pragma unroll 1
-            for (int g = 0; g < groups; ++g) {
-                int place = place0 + g;
-                if (place >= kRing) place -= kRing;
-                if (!r.careful) {
-                    const int c0 = sh.first + g * kGroupChunks + tid;
-                    T *to = out + sh.column(c0, 0);
-                    if (sh.first + (g + 1) * kGroupChunks <= sh.end) {
-#pragma unroll
-                        for (int u = 0; u < kGroup; ++u)
-                            store_chunk<DT>(to + u * THREADS * Chunk<DT>::kElems, grad(held(place, u)), apart, true);
-                    } else {
-#pragma unroll
-                        for (int u = 0; u < kGroup; ++u)
-                            if (c0 + u * THREADS < sh.end)
-                                store_chunk<DT>(to + u * THREADS * Chunk<DT>::kElems, grad(held(place, u)), apart,
-                                                c0 - lane + 31 + u * THREADS < sh.end);
+                for (int i = 0; i < groups; ++i) {
+                    const bool stayed = AGAIN == 0 || i < kRing;
+                    const int g = stayed ? AGAIN + i : i - kRing;
+                    int place = held_from + i;
+                    if (place >= kRing) place -= kRing;
+                    if (!stayed) {
+                        copies_left<kRing - 1>();
+                        place = take_place();
                     }
+                    if (!r.careful) {
+                        const int c0 = sh.first + g * kGroupChunks + tid;
+                        T *to = out + sh.column(c0, 0);
+                        if (sh.first + (g + 1) * kGroupChunks <= sh.end) {
+#pragma unroll
+                            for (int u = 0; u < kGroup; ++u)
+                                store_chunk<DT>(to + u * THREADS * Chunk<DT>::kElems, grad(held(place, u)), apart, true);
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < kGroup; ++u)
+                                if (c0 + u * THREADS < sh.end)
+                                    store_chunk<DT>(to + u * THREADS * Chunk<DT>::kElems, grad(held(place, u)), apart,
+                                                    c0 - lane + 31 + u * THREADS < sh.end);
+                        }
+                    }
+                    copy_next();  // into this group's place
                 }
-                copy_next();  // into this group's place
-            }
-            if (!r.careful) {
-                if (single) store_one<DT>(out, sh.single(tid), grad_of<false>(rg, one, ax, a.scale));
-                // The token's column, over what the warp that has its chunk has stored (the
-                // whole chunk, where rows lie apart by the lanes before or after, too), or
-                // the thread that has the single element.
-                if (sh.holds(col)) {
-                    const bool in_chunk = col >= sh.head && col < sh.tail0;
-                    const int owner = in_chunk ? ((col - sh.head) / Chunk<DT>::kElems - sh.first) % THREADS
-                                               : col < sh.head ? col : sh.n_head + col - sh.tail0;
-                    __syncwarp();
-                    if (tid == owner) store_one<DT>(out, col, at_token);
+                if (!r.careful) {
+                    if (single) store_one<DT>(out, sh.single(tid), grad_of<false>(rg, one, ax, a.scale));
+                    // The token's column, over what the warp that has its chunk has stored (the
+                    // whole chunk, where rows lie apart by the lanes before or after, too), or
+                    // the thread that has the single element.
+                    if (sh.holds(col)) {
+                        const bool in_chunk = col >= sh.head && col < sh.tail0;
+                        const int owner = in_chunk ? ((col - sh.head) / Chunk<DT>::kElems - sh.first) % THREADS
+                                                   : col < sh.head ? col : sh.n_head + col - sh.tail0;
+                        __syncwarp();
+                        if (tid == owner) store_one<DT>(out, col, at_token);
+                    }
+                } else if (empty) {
+                    write_zeros<DT>(out, a.cols, block, split, THREADS);
+                } else {
+                    write_grad_slowly<DT, false>(sh, out, rg, ax, a.scale, THREADS);
+                    __syncthreads();
+                    if (tid == 0 && sh.holds(col)) store_one<DT>(out, col, at_token);
                 }
-            } else if (empty) {
-                write_zeros<DT>(out, a.cols, block, split, THREADS);
-            } else {
-                write_grad_slowly<DT, false>(sh, out, rg, ax, a.scale, THREADS);
-                __syncthreads();
-                if (tid == 0 && sh.holds(col)) store_one<DT>(out, col, at_token);
             }
         }
-        place0 += groups;
-        if (place0 >= kRing) place0 -= kRing;
+        copies_left<0>();
     }
-    copies_left<0>();
     if (blocks > 1) cluster_sync();  // no block leaves while its sums are read
 }
 
@@ -436,10 +507,15 @@ template <int DT, int THREADS> int groups_of(int cols, int shift) {
 template <int DT, int THREADS>
 cudaError_t policy_stream(const PolicyArgs &a, bool grad, int shift, int sms, cudaStream_t s, LaunchInfo *info) {
     const Split split = split_of<DT>(a.cols, shift);
-    auto kernel = grad ? policy_stream_kernel<DT, true, THREADS> : policy_stream_kernel<DT, false, THREADS>;
-    static std::atomic<uint64_t> allowed[2];
+    const int groups = groups_of<DT, THREADS>(a.cols, shift), again = grad ? std::max(0, groups - kRing) : 0;
+    auto kernel = grad ? policy_stream_kernel<DT, true, THREADS, 0> : policy_stream_kernel<DT, false, THREADS, 0>;
+    if constexpr (THREADS == 512) {
+        if (again == 1) kernel = policy_stream_kernel<DT, true, THREADS, 1>;
+        if (again == 2) kernel = policy_stream_kernel<DT, true, THREADS, 2>;
+    }
+    static std::atomic<uint64_t> allowed[4];
     int at_once = 0;
-    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), Stream<THREADS>::kSmem, &allowed[grad]);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), Stream<THREADS>::kSmem, &allowed[grad ? 1 + again : 0]);
     if (e == cudaSuccess) e = rows_at_once<THREADS>(kernel, shift, sms, &at_once);
     if (e != cudaSuccess) return e;
     const int64_t grid = std::min<int64_t>(a.rows, at_once) << shift;
@@ -447,8 +523,7 @@ cudaError_t policy_stream(const PolicyArgs &a, bool grad, int shift, int sms, cu
     info->block = THREADS;
     info->vec_bytes = 16;
     info->smem = Stream<THREADS>::kSmem;
-    return launch_rows(kernel, dim3(grid), dim3(THREADS), Stream<THREADS>::kSmem, split.blocks(), s, a, split,
-                       groups_of<DT, THREADS>(a.cols, shift));
+    return launch_rows(kernel, dim3(grid), dim3(THREADS), Stream<THREADS>::kSmem, split.blocks(), s, a, split, groups);
 }
 
 template <int DT> cudaError_t policy_launch(const PolicyArgs &a, bool sums, bool grad, int sms, cudaStream_t s, LaunchInfo *info) {
@@ -461,11 +536,10 @@ template <int DT> cudaError_t policy_launch(const PolicyArgs &a, bool sums, bool
     if (sums && bytes > (few ? 16 : 32) * kKiB && bytes <= (few ? 32 : 64) * kKiB)
         return policy_stream<DT, 256>(a, grad, 0, sms, s, info);
     if (sums && bytes > (few ? 32 : 64) * kKiB) {
-        // at most 4 groups a row, so that 2 are on their way
         int shift = 0;
-        while (shift < 3 && groups_of<DT, 512>(a.cols, shift) > 4) ++shift;
+        while (shift < 3 && groups_of<DT, 512>(a.cols, shift) > kMostGroups) ++shift;
         while (shift < 3 && a.rows << (shift + 1) <= sms && a.cols >> (shift + 1) >= 4096) ++shift;
-        if (groups_of<DT, 512>(a.cols, shift) <= kRing) return policy_stream<DT, 512>(a, grad, shift, sms, s, info);
+        if (groups_of<DT, 512>(a.cols, shift) <= kMostGroups) return policy_stream<DT, 512>(a, grad, shift, sms, s, info);
     }
     if (!few && bytes <= 32 * kKiB) return policy_twice<DT, kNarrow>(a, sums, grad, 0, s, info);
     return policy_twice<DT, kThreads>(a, sums, grad, split_shift(a.rows, a.cols, sms), s, info);

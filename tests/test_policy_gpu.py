@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 # of every size at which another kernel, block size or split is chosen
 SHAPES = [(1, 1, 0, 0), (3, 5, 0, 1), (2, 8, 0, 0), (5, 100, 0, 0), (3, 1000, 24, 8), (4, 4097, 0, 0), (5, 8192, 0, 0),
           (3, 16387, 0, 3), (6, 50001, 0, 0), (1, 131072, 0, 0), (3, 150001, 0, 0), (400, 3001, 0, 0), (700, 12000, 8, 0),
-          (330, 20001, 0, 0), (170, 33333, 0, 0), (165, 65536, 0, 0), (160, 100003, 5, 1), (2, 400001, 0, 0)]
+          (330, 20001, 0, 0), (170, 33333, 0, 0), (165, 65536, 0, 0), (160, 100003, 5, 1), (320, 131071, 0, 0), (2, 400001, 0, 0)]
 HOW = dict(clip_low=0.2, clip_high=0.3, kl=0.1)
 
 
@@ -145,7 +145,8 @@ def test_without_an_old_policy_or_a_reference(dtype, rows, cols, old, ref):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,cols", [(4, 4097), (3, 20001), (400, 3001), (330, 20001), (165, 65536), (3, 150001), (2, 400001)])
+@pytest.mark.parametrize("rows,cols", [(4, 4097), (3, 20001), (400, 3001), (330, 20001), (165, 65536), (160, 131072), (3, 150001),
+                                       (2, 400001)])
 def test_in_place_and_repeated(dtype, rows, cols):
     c = Case(rows, cols, dtype, 0, 0, 4)
     how = dict(old_logp=c.old, ref_logp=c.ref, **HOW)
@@ -172,7 +173,7 @@ def test_outputs_whose_rows_lie_apart(dtype, cols, rows):
         assert out.intact() and c.x.intact()
 
 
-@pytest.mark.parametrize("rows,cols", [(200, 20000), (600, 70000), (1000, 4000), (9, 70000)])
+@pytest.mark.parametrize("rows,cols", [(200, 20000), (600, 70000), (1000, 4000), (9, 70000), (500, 131072)])
 @pytest.mark.parametrize("how", ["none", "all but one", "prompts", "all"])
 def test_rows_without_a_token_are_not_read(rows, cols, how):
     """Runs of rows without a token, longer than what is read ahead; NaN in them changes nothing."""
@@ -353,6 +354,34 @@ def test_more_than_2_to_the_31_elements():
         off = adv[part].double().abs()[:, None] * want.p * (want.bound[:, None] + 16 * EPS32) + 8 * EPS32 * g.abs()
         assert_within(d[part], g, UNIT["bf16"] * g.abs() + 2 * off + TINY["bf16"], "dlogits")
     assert torch.isfinite(loss).all()
+
+
+def test_more_rows_than_a_blocks_list_holds():
+    """Rows of 24 KiB and more, 512 of them from each block at a time: three rounds of lists, rows without a token among
+    them, whole lists of either kind."""
+    rows, cols = 700000, 12300
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=generator(19))
+    tokens = torch.randint(0, cols, (rows,), generator=generator(20), device="cuda", dtype=torch.int32)
+    tokens[torch.rand(rows, generator=generator(21), device="cuda") < 0.5] = -1
+    tokens[:300] = -1
+    tokens[320000:330000] = 7
+    adv, one = randn((rows,), 22), torch.ones(rows, device="cuda")
+    given = tokens >= 0
+    picked = torch.cat([torch.nonzero(given)[:3, 0], torch.nonzero(given)[-3:, 0], torch.tensor([320000, 329999], device="cuda")])
+    before = x[picked].clone()
+    loss, logp, lse, d = ew.ew_policy_step(x, tokens, adv, one, dlogits=x)
+    assert not loss[~given].any() and not logp[~given].any() and not lse[~given].any()
+    assert_within(loss[given], -adv[given].double(), 4 * EPS32 * adv[given].double().abs(), "loss")
+    assert float(lse[given].min()) > 9.0 and float(lse[given].max()) < 11.0  # log(12300) + 1/2, give or take 0.02
+    for part in torch.arange(rows, device="cuda").split(100000):  # a gradient's row adds up to nothing, and holds something
+        sums, largest = d[part].float().sum(1), d[part].abs().amax(1).float()
+        assert not largest[~given[part]].any() and (largest[given[part]] > 0.9 * adv[part][given[part]].abs()).all()
+        assert (sums.abs() <= 2 * UNIT["bf16"] * 2 * adv[part].abs()).all()
+    want = Want(before, 1.0)
+    at = tokens[picked].long()[:, None]
+    g = -adv[picked].double()[:, None] * (torch.zeros_like(want.p).scatter_(1, at, 1.0) - want.p)
+    off = adv[picked].double().abs()[:, None] * want.p * (want.bound[:, None] + 16 * EPS32) + 8 * EPS32 * g.abs()
+    assert_within(d[picked], g, UNIT["bf16"] * g.abs() + 2 * off + TINY["bf16"], "dlogits")
 
 
 def test_no_rows():
