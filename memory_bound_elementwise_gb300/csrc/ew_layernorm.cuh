@@ -9,10 +9,10 @@
 // a multiple, `past` elements before the row, and the runs at its two ends are
 // moved element by element (RUNS).  Other matrices are moved an element at a time.
 //
-// The mean of a row far from zero is subtracted in two steps: first the row's
-// first element, an exact difference where the row's elements are within a factor
-// of two of each other, then the mean of what is left.  So y does not lose what
-// the rounding of m to binary32 would cost it.
+// The mean of a row far from zero is subtracted in two steps: first one of the
+// row's elements, an exact difference where they are within a factor of two of
+// each other, then the mean of what is left.  So y does not lose what the rounding
+// of m to binary32 would cost it.
 #pragma once
 
 #include <algorithm>
@@ -90,6 +90,15 @@ __device__ __forceinline__ float2 block_sum2(float2 v, int warps, float2 *part) 
 }
 
 // ---------------------------------------------------------------- forward
+
+// What the elements are compared with: lane 0's of the warp's samples (`mine`, where
+// `given`) where all have one sign, and so may lie far from zero, else zero.  Zero
+// leaves the mean of a row around it as precise as a plain sum does.
+__device__ __forceinline__ float landmark(float mine, bool given) {
+    const unsigned all = __ballot_sync(kAllLanes, given), negative = __ballot_sync(kAllLanes, given && mine < 0.0f);
+    const float first = __shfl_sync(kAllLanes, mine, 0);
+    return negative == 0 || negative == all ? first : 0.0f;
+}
 
 // One row to a block of `warps` warps, tile t of the row to warp t mod warps;
 // with one warp a row, blockDim.y rows to a block.  HELD: the warps x KT tiles
@@ -177,8 +186,9 @@ __global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARP
             }
             row += static_cast<int64_t>(gridDim.x) * blockDim.y;
             if (kWalks && row < a.rows) load();  // on its way while this row is worked on
-            // an element of the warp's first tile that lies in the row, if any does (a row has 8)
-            float at = __shfl_sync(kAllLanes, ROWS == kShifted && warp == 0 ? f[0][3].y : f[0][0].x, 0);
+            // lane 0's lies in the row, if any of the warp's first tile does (a shifted row has 8)
+            const int j = ROWS == kShifted && warp == 0 ? 7 : 0;
+            float at = landmark(j == 0 ? f[0][0].x : f[0][3].y, col_of<ROWS != kApart>(warp, past, lane, j) < a.cols);
             float2 s2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
@@ -238,13 +248,12 @@ __global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARP
                 for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
             }
         };
-        // the row's first element: read by all before h or y may take its place
-        auto first_of = [](const void *p) {
-            if constexpr (DT == DT_F32) return __uint_as_float(ld<4>(p).w[0]);
-            else return elem_to_f32<DT>(ld<2>(p).h);
+        // the row's first 32 elements, to every warp: read before h or y may take their place
+        auto element = [&](const void *p) {
+            using T = typename ElemOf<DT>::type;
+            return elem_to_f32<DT>(static_cast<const T *>(p)[min(lane, a.cols - 1)]);
         };
-        float at = first_of(x);
-        if (res) at += first_of(res);
+        const float at = landmark(res ? element(x) + element(res) : element(x), lane < a.cols);
         float2 s2 = both(0.0f), q2 = both(0.0f), f[4];
         for (int t = warp; t < tiles; t += warps) {
             sum_of(t, f);

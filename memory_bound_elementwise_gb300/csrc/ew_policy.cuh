@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) polic
 // numbers: the rows with a token, in their order, go round the blocks (or
 // clusters), and so do those without, from the last block on.  Each block works its
 // list out for itself, from all tokens: 8 bytes a row, where a row has thousands.
-// 2048 rows of 131072 bf16, a quarter of them without a token, took 188 us by
+// 2048 rows of 131072 bf16, a quarter of them without a token, took 178 us by
 // numbers and 182 us by lists.
 //
 // Tokens, their numbers and logits are read for 32 of the block's rows at once, one
@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
         const int64_t token = token_at(a.tokens, a.i64, row);
         return token >= 0 && token < a.cols ? static_cast<int>(token) : -1;
     };
+    const float per_step = 1.0f / static_cast<float>(step);
     int turn = 0;
 #pragma unroll 1
     for (int64_t base = 0; base < a.rows; base += static_cast<int64_t>(step) * S::kList) {
@@ -241,37 +242,55 @@ __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
 #pragma unroll 1
         for (int slab = 0; slab < window; slab += S::kSlab) {
             unsigned given[S::kLooks];
+            int64_t token[S::kLooks];  // read together: past the window its last one again
+            if (a.i64) {
+                const int64_t *from = static_cast<const int64_t *>(a.tokens) + base;
 #pragma unroll
-            for (int j = 0; j < S::kLooks; ++j) {
-                const int at = slab + j * THREADS + tid;
-                given[j] = at < window && token_of(base + at) >= 0;
+                for (int j = 0; j < S::kLooks; ++j) token[j] = from[min(slab + j * THREADS + tid, window - 1)];
+            } else {
+                const int32_t *from = static_cast<const int32_t *>(a.tokens) + base;
+#pragma unroll
+                for (int j = 0; j < S::kLooks; ++j) token[j] = from[min(slab + j * THREADS + tid, window - 1)];
             }
 #pragma unroll
-            for (int j = 0; j < S::kLooks; ++j) given[j] = __ballot_sync(kAllLanes, given[j] != 0);
+            for (int j = 0; j < S::kLooks; ++j)
+                given[j] = __ballot_sync(kAllLanes, slab + j * THREADS + tid < window && token[j] >= 0 && token[j] < a.cols);
             __syncthreads();  // the counts before, and the list of the window before, have been read
 #pragma unroll
             for (int j = 0; j < S::kLooks; ++j)
                 if (lane == 0) counts[j * kWarps + warp] = __popc(given[j]);
             __syncthreads();
-            int some[kCounts / 32], total = 0;
+            // a lane has kOwn counts in a row, and those before them in `upto`
+            constexpr int kOwn = kCounts / 32;
+            int upto[kOwn + 1] = {};
 #pragma unroll
-            for (int i = 0; i < kCounts / 32; ++i) total += some[i] = counts[i * 32 + lane];
+            for (int i = 0; i < kOwn; ++i) upto[i + 1] = upto[i] + counts[lane * kOwn + i];
+            int scan = upto[kOwn];
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int below = __shfl_up_sync(kAllLanes, scan, d);
+                if (lane >= d) scan += below;
+            }
+            const int before_lane = scan - upto[kOwn];
 #pragma unroll
             for (int j = 0; j < S::kLooks; ++j) {
                 const int own = j * kWarps + warp, at = slab + j * THREADS + tid;
-                int earlier = 0;
+                if (slab + j * THREADS >= window) break;
+                int earlier = before_lane;
 #pragma unroll
-                for (int i = 0; i < kCounts / 32; ++i) earlier += i * 32 + lane < own ? some[i] : 0;
-                const unsigned before = with + __reduce_add_sync(kAllLanes, earlier) + __popc(given[j] & ((1u << lane) - 1u));
-                if (at >= window) continue;
-                if (given[j] >> lane & 1) {
-                    if (before % step == me) list[before / step] = at;
-                } else {
-                    const unsigned without = at - before;
-                    if (without % step == step - 1 - me) list[S::kList + 1 - without / step] = at;
-                }
+                for (int i = 1; i < kOwn; ++i) earlier = own % kOwn == i ? before_lane + upto[i] : earlier;
+                earlier = __shfl_sync(kAllLanes, earlier, own / kOwn);
+                const bool one = given[j] >> lane & 1;
+                // its rank among those with a token, or without: a number below 2^24, so that its
+                // quotient by the blocks is off by one at most
+                const unsigned before = with + earlier + __popc(given[j] & ((1u << lane) - 1u)), rank = one ? before : at - before;
+                unsigned round = static_cast<unsigned>(static_cast<float>(rank) * per_step);
+                if (round * step > rank) --round;
+                if ((round + 1) * step <= rank) ++round;
+                const unsigned whose = rank - round * step;
+                if (at < window && whose == (one ? me : step - 1 - me)) list[one ? round : S::kList + 1 - round] = at;
             }
-            with += __reduce_add_sync(kAllLanes, total);
+            with += __shfl_sync(kAllLanes, scan, 31);
         }
         const int rows = static_cast<int>((with + step - 1 - me) / step), empty_rows = static_cast<int>((window - with + me) / step);
         __syncthreads();
