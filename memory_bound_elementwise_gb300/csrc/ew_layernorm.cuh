@@ -384,44 +384,48 @@ template <int DT, int KT> __global__ void __launch_bounds__(512) layernorm_grad_
 // the columns that a thread holds, and sums, stay the same.  A row's first piece
 // begins `past` elements before the row, in the row before it or the gap there, and
 // what it brings along is cleared; only before the first row nothing is read.
-// KT = 4 has no registers left for the weights and reads them for each row.
-template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __grid_constant__ LayerNormGradArgs a, int depth) {
+//
+// PAIR: rows of more than 16 warps x 2 tiles go to clusters of two blocks, a half of
+// the warps' tiles each.  The barrier between a row's two passes is the cluster's
+// then; what its wait takes passes while the row before is finished.
+template <int DT, int KT, bool ALIGNED, bool PAIR>
+__global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __grid_constant__ LayerNormGradArgs a, int depth) {
     enter_grid();
     using T = typename ElemOf<DT>::type;
     constexpr int B = ElemOf<DT>::kBytes, P = B / 2, E = 16 / B;
-    constexpr bool kHeld = KT < 4;
     extern __shared__ uint4 ring[];  // [row][dy, h, dh][tile][piece][thread]
     __shared__ alignas(16) float2 parts[4][2][16];  // of a row and the next: the warps' sums, zeros beyond
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int threads = blockDim.x * blockDim.y, slot_size = 3 * KT * P * threads;
     uint4 *const mine = ring + threadIdx.y * blockDim.x + threadIdx.x;
-    const int64_t writer = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    const int64_t writers = static_cast<int64_t>(gridDim.x) * blockDim.y;
+    // the row's warps, of this block and its neighbour
+    const int half = PAIR ? blockIdx.x & 1 : 0, row_warps = PAIR ? 2 * warps : warps, row_warp = half * warps + warp;
+    const int64_t team = PAIR ? blockIdx.x >> 1 : blockIdx.x, teams = PAIR ? gridDim.x >> 1 : gridDim.x;
+    const int64_t writer = team * blockDim.y + threadIdx.y, writers = teams * blockDim.y;
     const int past = ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row_of<DT>(a.dy, writer, a.dy_stride)) % 16) / B;
-    auto col = [&](int k, int piece) { return (warp + k * warps) * kTileCols + piece * 128 + lane * E - past; };
+    auto col = [&](int k, int piece) { return (row_warp + k * row_warps) * kTileCols + piece * 128 + lane * E - past; };
     auto place = [&](int slot, int matrix, int k, int piece) {
         return mine + slot * slot_size + ((matrix * KT + k) * P + piece) * threads;
     };
     // columns of the weight, in the layout of the pieces
     auto weights = [&](int k, float2 (&w)[4]) {
+        if constexpr (P == 1) {
+            load_columns<DT, ALIGNED ? kAligned : kShifted>(a.weight, a.weight_f32, 1.0f, row_warp + k * row_warps, past, a.cols, lane, w);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = P == 2 ? col(k, j / 4) + j % 4 : col(k, 0) + j;
-            float v = 1.0f;
-            if (a.weight != nullptr) {
-                v = 0.0f;
-                if (c >= 0 && c < a.cols)
-                    v = DT == DT_F32 || a.weight_f32 ? static_cast<const float *>(a.weight)[c]
-                                                     : elem_to_f32<DT>(static_cast<const T *>(a.weight)[c]);
+            for (int j = 0; j < 8; ++j) {
+                const int c = col(k, j / 4) + j % 4;
+                float v = a.weight == nullptr ? 1.0f : 0.0f;
+                if (a.weight != nullptr && c >= 0 && c < a.cols) v = static_cast<const float *>(a.weight)[c];
+                (j & 1 ? w[j / 2].y : w[j / 2].x) = v;
             }
-            (j & 1 ? w[j / 2].y : w[j / 2].x) = v;
         }
     };
-    float2 dw[KT][4], db[KT][4], w[kHeld ? KT : 1][4];
+    float2 dw[KT][4], db[KT][4], w[KT][4];
     int bytes[KT][P];  // that a piece has up to the row's end, 0 to 16; zeros after them
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
-        if constexpr (kHeld) weights(k, w[k]);
+        weights(k, w[k]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) dw[k][j] = db[k][j] = both(0.0f);
 #pragma unroll
@@ -437,7 +441,7 @@ template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1
                 for (int piece = 0; piece < P; ++piece)
                     if (bytes[k][piece] == 0 || (matrix == 2 && a.dh == nullptr))
                         *place(slot, matrix, k, piece) = make_uint4(0u, 0u, 0u, 0u);
-    const int tile_bytes = warps * kTileCols * B;  // from one of a thread's tiles to the next
+    const int tile_bytes = row_warps * kTileCols * B;  // from one of a thread's tiles to the next
     auto copy = [&](const char *from, bool first, uint4 *to) {
 #pragma unroll
         for (int k = 0; k < KT; ++k)
@@ -511,7 +515,6 @@ template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             float2 g[4], n[4];
-            if constexpr (!kHeld) weights(k, w[0]);
             held(slot, 0, k, g);
             held(slot, 1, k, n);
 #pragma unroll
@@ -519,7 +522,7 @@ template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1
                 n[j] = mul2(add2(n[j], m), r);
                 dw[k][j] = fma2(g[j], n[j], dw[k][j]);
                 db[k][j] = add2(g[j], db[k][j]);
-                g[j] = mul2(g[j], w[kHeld ? k : 0][j]);
+                g[j] = mul2(g[j], w[k][j]);
                 c1 = add2(c1, g[j]);
                 c2 = fma2(g[j], n[j], c2);
             }
@@ -543,19 +546,25 @@ template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1
     else if (depth == 3) copies_left<2>();
     else copies_left<3>();
     if (writer < a.rows) add_row(0, mean, rstd, part[0]);
+    if (PAIR) cluster_arrive();
     int turn = 0, slot = 0;
 #pragma unroll 1
     for (int64_t row = writer; row < a.rows; row += writers, turn ^= 1) {
         const int next_slot = slot + 1 == depth ? 0 : slot + 1;
-        if (warps > 1) __syncthreads();
-        else __syncwarp();
         float2 c = both(0.0f);
-        const float4 *all = reinterpret_cast<const float4 *>(part[turn]);
+        if constexpr (PAIR) {
+            cluster_wait();
+            c = warp_sum2(*in_block(&part[turn][lane & 15], lane >> 4));
+        } else {
+            if (warps > 1) __syncthreads();
+            else __syncwarp();
+            const float4 *all = reinterpret_cast<const float4 *>(part[turn]);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            if (2 * i >= warps) break;
-            const float4 p = all[i], q = all[i + 1];
-            c = add2(add2(c, add2(make_float2(p.x, p.y), make_float2(p.z, p.w))), add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+            for (int i = 0; i < 8; i += 2) {
+                if (2 * i >= warps) break;
+                const float4 p = all[i], q = all[i + 1];
+                c = add2(add2(c, add2(make_float2(p.x, p.y), make_float2(p.z, p.w))), add2(make_float2(q.x, q.y), make_float2(q.z, q.w)));
+            }
         }
         if (depth == 2) copies_left<0>();
         else if (depth == 3) copies_left<1>();
@@ -563,19 +572,19 @@ template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1
         float after_mean = 0.0f, after_rstd = 0.0f;
         statistics(row + 2 * writers, after_mean, after_rstd);
         if (row + writers < a.rows) add_row(next_slot, next_mean, next_rstd, part[turn ^ 1]);
+        if (PAIR) cluster_arrive();
         const float2 m = both(-mean), r = both(rstd);
         const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * per_col * rstd);
         T *dx = static_cast<T *>(row_of<DT>(a.dx, row, a.dx_stride));
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             float2 g[4], n[4], d[4];
-            if constexpr (!kHeld) weights(k, w[0]);
             held(slot, 0, k, g);
             held(slot, 1, k, n);
             held(slot, 2, k, d);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                d[j] = fma2(r, fma2(g[j], w[kHeld ? k : 0][j], fma2(m2, add2(n[j], m), m1)), d[j]);
+                d[j] = fma2(r, fma2(g[j], w[k][j], fma2(m2, add2(n[j], m), m1)), d[j]);
             const Raw8<DT> o = pack8<DT>(d);
 #pragma unroll
             for (int piece = 0; piece < P; ++piece) {
@@ -598,10 +607,11 @@ template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1
         mean = next_mean, rstd = next_rstd, next_mean = after_mean, next_rstd = after_rstd;
     }
     copies_left<0>();
+    if (PAIR) cluster_wait();  // the neighbour has read this block's sums
     if (a.partial == nullptr) return;
     // The block's sums: of one writer straight from the registers, where whole runs
-    // can be written; otherwise by columns in the ring's place, the writers in order.
-    float *out = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols, *out_b = out + static_cast<int64_t>(gridDim.x) * a.cols;
+    // can be written; otherwise by columns through the ring's place, the writers' in order.
+    float *out = a.partial + team * a.cols, *out_b = out + teams * a.cols;
     if (ALIGNED && blockDim.y == 1 && a.cols % 4 == 0) {
 #pragma unroll
         for (int k = 0; k < KT; ++k)
@@ -625,12 +635,26 @@ template <int DT, int KT, bool ALIGNED> __global__ void __launch_bounds__(512, 1
             sums[c] = j & 1 ? dw[k][j / 2].y : dw[k][j / 2].x;
             sums[a.cols + c] = j & 1 ? db[k][j / 2].y : db[k][j / 2].x;
         }
+    if (blockDim.y == 1) {  // a warp's own columns
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = (row_warp + k * row_warps) * kTileCols - past + j * 32 + lane;
+                if (c < 0 || c >= a.cols) continue;
+                out[c] = sums[c];
+                out_b[c] = sums[a.cols + c];
+            }
+        return;
+    }
     __syncthreads();
     sums = reinterpret_cast<float *>(ring);
     for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 2 * a.cols; i += threads) {
         float sum = sums[i];
         for (int y = 1; y < static_cast<int>(blockDim.y); ++y) sum += sums[y * 2 * a.cols + i];
-        (i < a.cols ? out[i] : out_b[i - a.cols]) = sum;
+        if (i < a.cols) out[i] = sum;
+        else out_b[i - a.cols] = sum;
     }
 }
 
@@ -767,42 +791,45 @@ cudaError_t layernorm_grad_dispatch(const LayerNormGradArgs &a, int64_t most_wri
     const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (aligned ? 0 : 7) + kTileCols - 1) / kTileCols);
     const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
     int kt = tiles_per_thread(tiles, 8, 2);
+    // One tile a thread spreads a row over more warps; two save the barrier of rows of
+    // two tiles, and instructions of wide 16-bit rows, where there are many.  16384 rows
+    // of 2048 bf16: 50 us with two, 57 with one; 3000 rows: 17 and 16 us.
+    if (kt == 1 && many && tiles == 2) kt = 2;
     if (DT != DT_F32 && kt == 1 && tiles > 6 && a.rows >= 32 * static_cast<int64_t>(sms)) kt = 2;
-    if (kt == 0) kt = tiles_per_thread(tiles, kLayerNormWarps, DT == DT_F32 ? 2 : 4);
+    if (kt == 0) kt = tiles_per_thread(tiles, kLayerNormWarps, 2);
+    const bool pair = kt == 0 && runs && tiles <= 4 * kLayerNormWarps && (aligned || sms >= 16);  // 8 pairs of blocks
+    if (pair) kt = 2;
     const bool sums = a.dweight != nullptr || a.dbias != nullptr;
     int64_t writers = 0;
     cudaError_t e = cudaSuccess;
     info->vec_bytes = runs ? 16 : ElemOf<DT>::kBytes;
     if (a.rows > 0 && kt != 0) {
-        const int warps = (tiles + kt - 1) / kt;
+        const int blocks = pair ? 2 : 1, warps = (tiles + kt * blocks - 1) / (kt * blocks);
         // a row for each of 4 warps, where one holds it: their sums leave the block as one
         const int per_block = runs && warps == 1 && many ? 4 : 1;
         const int resident = std::max(1, 16 / (warps * per_block));  // blocks that make 512 threads an SM
-        int64_t grid = std::min<int64_t>({(a.rows + per_block - 1) / per_block, static_cast<int64_t>(sms) * resident, most_writers});
+        int64_t grid = std::min<int64_t>({(a.rows + per_block - 1) / per_block, static_cast<int64_t>(sms) * resident / blocks, most_writers});
         // a writer's rows start alike: a multiple of 8 apart, where it has more than one
         if (!aligned && grid * per_block < a.rows && grid > 8) grid = grid / 8 * 8;
+        grid = std::max<int64_t>(grid, 1);
         writers = grid;
         const dim3 block(32 * warps, per_block);
-        info->grid = static_cast<int>(grid);
+        info->grid = static_cast<int>(grid * blocks);
         info->block = 32 * warps * per_block;
         if (runs && (aligned || grid * per_block % 8 == 0 || grid * per_block >= a.rows)) {
-            auto kernel = aligned ? kt == 1 ? layernorm_grad_ring_kernel<DT, 1, true> : layernorm_grad_ring_kernel<DT, 2, true>
-                                  : kt == 1 ? layernorm_grad_ring_kernel<DT, 1, false> : layernorm_grad_ring_kernel<DT, 2, false>;
-            if constexpr (DT != DT_F32)
-                if (kt == 4) kernel = aligned ? layernorm_grad_ring_kernel<DT, 4, true> : layernorm_grad_ring_kernel<DT, 4, false>;
+            auto kernel = aligned ? kt == 1 ? layernorm_grad_ring_kernel<DT, 1, true, false> : layernorm_grad_ring_kernel<DT, 2, true, false>
+                                  : kt == 1 ? layernorm_grad_ring_kernel<DT, 1, false, false> : layernorm_grad_ring_kernel<DT, 2, false, false>;
+            if (pair) kernel = aligned ? layernorm_grad_ring_kernel<DT, 2, true, true> : layernorm_grad_ring_kernel<DT, 2, false, true>;
             const int row_bytes = 3 * kt * info->block * 8 * ElemOf<DT>::kBytes;  // of a row of each of the block's writers
             const int depth = std::max(2, std::min(4, kRingBytes / (resident * row_bytes)));
             static std::atomic<uint64_t> allowed[2][3];
-            e = allow_smem(reinterpret_cast<const void *>(kernel), kRingBytes, &allowed[aligned][kt / 2]);
+            e = allow_smem(reinterpret_cast<const void *>(kernel), kRingBytes, &allowed[aligned][pair ? 2 : kt - 1]);
             if (e != cudaSuccess) return e;
             info->smem = depth * row_bytes;
-            e = launch_rows(kernel, dim3(grid), block, depth * row_bytes, 1, s, a, depth);
+            e = launch_rows(kernel, dim3(grid * blocks), block, depth * row_bytes, blocks, s, a, depth);
         } else {
             info->vec_bytes = ElemOf<DT>::kBytes;
-            auto kernel = kt == 1 ? layernorm_grad_kernel<DT, 1> : layernorm_grad_kernel<DT, 2>;
-            if constexpr (DT != DT_F32)
-                if (kt == 4) kernel = layernorm_grad_kernel<DT, 4>;
-            e = launch_rows(kernel, dim3(grid), block, 0, 1, s, a);
+            e = launch_rows(kt == 1 ? layernorm_grad_kernel<DT, 1> : layernorm_grad_kernel<DT, 2>, dim3(grid), block, 0, 1, s, a);
         }
         ++*launches;
     } else if (a.rows > 0) {
