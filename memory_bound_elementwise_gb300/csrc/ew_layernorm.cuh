@@ -109,23 +109,37 @@ __device__ __forceinline__ float landmark(float mine, bool given) {
 // passes read the row again.
 //
 // Weights beside shifted rows have to be cut to their phase, which takes as long
-// as all else.  Where a thread has up to two tiles, blocks therefore walk over the
-// rows in steps of a multiple of 8, after which the phase is the same, and cut
-// the weights once.
-template <int DT, int ROWS, int KT, bool HELD, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARPS == 8 ? 3 : KT == 1 || (KT == 2 && ROWS == kAligned) ? 2 : 1)
+// as all else, and those of rows of more than 32 tiles of 16 bits are read from the
+// L2 as often as the rows.  Blocks therefore walk over such rows, in steps of a
+// multiple of 8, after which the phase is the same: each thread keeps its weights in
+// shared memory, and the next row is on its way while one is worked on.
+//
+// PAIR: the row goes to a cluster of two blocks, which read each other's parts.
+__host__ __device__ constexpr bool layernorm_walks(int dt, int rows, int kt, int warps) {
+    return rows == kShifted || (rows == kAligned && dt != DT_F32 && kt == 4 && warps == 16);
+}
+__host__ __device__ constexpr int layernorm_resident(int dt, int rows, int kt, bool held, int warps) {  // blocks to an SM
+    if (!held || rows == kApart) return 1;
+    if (warps == 8) return 3;
+    return kt == 1 || (rows == kAligned && kt == 2) ? 2 : 1;
+}
+template <int DT, int ROWS, int KT, bool HELD, int WARPS, bool PAIR>
+__global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, HELD, WARPS))
     layernorm_kernel(const __grid_constant__ LayerNormArgs a) {
     enter_grid();
-    constexpr bool kWalks = HELD && ROWS == kShifted && KT <= 2;
+    constexpr bool kWalks = HELD && layernorm_walks(DT, ROWS, KT, WARPS);
+    extern __shared__ float4 cut[];  // of walkers, [tile][weight's 4 and 4, bias' 4 and 4][thread]
     __shared__ float4 parts[2][32];  // of a warp's columns: an element, mean beyond that, squares, number
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    // the row's warps, of this block and its neighbour
+    const int half = PAIR ? blockIdx.x & 1 : 0, row_warps = PAIR ? 2 * warps : warps, row_warp = half * warps + warp;
+    int64_t row = static_cast<int64_t>(PAIR ? blockIdx.x >> 1 : blockIdx.x) * blockDim.y + threadIdx.y;
     if (row >= a.rows) return;  // whole warps: blockDim.y > 1 only with one warp a row
     const int past = ROWS == kShifted ? past_of<DT>(row_of<DT>(a.x, row, a.x_stride)) : 0;
     const float per_col = a.per_col;
     auto statistics = [&](int64_t row, float at, float mean, float squares) {
         const float r = rsqrtf(fmaf(squares, per_col, a.eps));
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 && half == 0) {
             if (a.mean) a.mean[row] = at + mean;
             if (a.rstd) a.rstd[row] = r;
         }
@@ -145,28 +159,37 @@ __global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARP
     };
 
     if constexpr (HELD) {
-        float2 w[kWalks ? KT : 1][4], b[kWalks ? KT : 1][4];
         int n = 0;
 #pragma unroll
-        for (int k = 0; k < KT; ++k) n += columns_in(warp + k * warps, past, a.cols);
+        for (int k = 0; k < KT; ++k) n += columns_in(row_warp + k * row_warps, past, a.cols);
         const float per_own = 1.0f / static_cast<float>(max(n, 1));
+        const int threads = blockDim.x * blockDim.y;
+        float4 *const mine = cut + threadIdx.y * blockDim.x + threadIdx.x;
         int turn = 0;
         Raw8<DT> rx[KT], rr[KT];
         auto load = [&] {
             const void *x = row_of<DT>(a.x, row, a.x_stride);
             const bool inner = row > 0 && row + 1 < a.rows;  // strides are at least 8
 #pragma unroll
-            for (int k = 0; k < KT; ++k) rx[k] = load_row<DT, ROWS>(x, warp + k * warps, past, a.cols, lane, inner);
+            for (int k = 0; k < KT; ++k) rx[k] = load_row<DT, ROWS>(x, row_warp + k * row_warps, past, a.cols, lane, inner);
             if (a.residual) {
                 const void *res = row_of<DT>(a.residual, row, a.residual_stride);
 #pragma unroll
-                for (int k = 0; k < KT; ++k) rr[k] = load_row<DT, ROWS>(res, warp + k * warps, past, a.cols, lane, inner);
+                for (int k = 0; k < KT; ++k) rr[k] = load_row<DT, ROWS>(res, row_warp + k * row_warps, past, a.cols, lane, inner);
             }
         };
         load();
         if constexpr (kWalks) {
 #pragma unroll
-            for (int k = 0; k < KT; ++k) weights(warp + k * warps, w[k], b[k]);
+            for (int k = 0; k < KT; ++k) {
+                float2 w[4], b[4];
+                weights(row_warp + k * row_warps, w, b);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mine[(4 * k + i) * threads] = make_float4(w[2 * i].x, w[2 * i].y, w[2 * i + 1].x, w[2 * i + 1].y);
+                    mine[(4 * k + 2 + i) * threads] = make_float4(b[2 * i].x, b[2 * i].y, b[2 * i + 1].x, b[2 * i + 1].y);
+                }
+            }
         }
         do {
             void *h = a.h ? row_of<DT>(a.h, row, a.h_stride) : nullptr;
@@ -182,20 +205,20 @@ __global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARP
 #pragma unroll
                     for (int j = 0; j < 4; ++j) f[k][j] = add2(f[k][j], g[j]);
                 }
-                if (h) store_row<DT, ROWS>(h, warp + k * warps, past, a.cols, lane, pack8<DT>(f[k]));
+                if (h) store_row<DT, ROWS>(h, row_warp + k * row_warps, past, a.cols, lane, pack8<DT>(f[k]));
             }
-            row += static_cast<int64_t>(gridDim.x) * blockDim.y;
+            row += static_cast<int64_t>(PAIR ? gridDim.x >> 1 : gridDim.x) * blockDim.y;
             if (kWalks && row < a.rows) load();  // on its way while this row is worked on
             // lane 0's lies in the row, if any of the warp's first tile does (a shifted row has 8)
-            const int j = ROWS == kShifted && warp == 0 ? 7 : 0;
-            float at = landmark(j == 0 ? f[0][0].x : f[0][3].y, col_of<ROWS != kApart>(warp, past, lane, j) < a.cols);
+            const int j = ROWS == kShifted && row_warp == 0 ? 7 : 0;
+            float at = landmark(j == 0 ? f[0][0].x : f[0][3].y, col_of<ROWS != kApart>(row_warp, past, lane, j) < a.cols);
             float2 s2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
                 float2 d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = add2(f[k][j], both(-at));
-                clip_columns<ROWS != kApart>(warp + k * warps, past, a.cols, lane, d);
+                clip_columns<ROWS != kApart>(row_warp + k * row_warps, past, a.cols, lane, d);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
             }
@@ -205,7 +228,7 @@ __global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARP
                 float2 d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[j] = add2(add2(f[k][j], both(-at)), both(-mean));
-                clip_columns<ROWS != kApart>(warp + k * warps, past, a.cols, lane, d);
+                clip_columns<ROWS != kApart>(row_warp + k * row_warps, past, a.cols, lane, d);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
             }
@@ -214,10 +237,12 @@ __global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARP
                 float4 *part = parts[turn];
                 turn ^= 1;  // read by all before it is written again: a barrier lies between
                 if (lane == 0) part[warp] = make_float4(at, mean, squares, static_cast<float>(n));
-                __syncthreads();
-                const float4 v = part[lane < warps ? lane : 0];
-                const float count = lane < warps ? v.w : 0.0f;
-                at = part[0].x;
+                if (PAIR) cluster_sync();
+                else __syncthreads();
+                const int other = lane < row_warps ? lane : 0;
+                const float4 v = PAIR ? *in_block(&part[other % warps], other / warps) : part[other];
+                const float count = lane < row_warps ? v.w : 0.0f;
+                at = __shfl_sync(kAllLanes, v.x, 0);
                 const float apart = v.x - at + v.y;
                 mean = warp_sum(count > 0.0f ? count * apart : 0.0f) * per_col;
                 const float off = apart - mean;
@@ -226,12 +251,23 @@ __global__ void __launch_bounds__(WARPS * 32, !HELD || ROWS == kApart ? 1 : WARP
             const float r = statistics(here, at, mean, squares);
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
-                const int tile = warp + k * warps;
+                const int tile = row_warp + k * row_warps;
                 if (tile * kTileCols - past >= a.cols) continue;
-                if constexpr (!kWalks) weights(tile, w[0], b[0]);
-                put(out, tile, f[k], at, mean, r, w[kWalks ? k : 0], b[kWalks ? k : 0]);
+                float2 w[4], b[4];
+                if constexpr (kWalks) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 u = mine[(4 * k + i) * threads], v = mine[(4 * k + 2 + i) * threads];
+                        w[2 * i] = make_float2(u.x, u.y), w[2 * i + 1] = make_float2(u.z, u.w);
+                        b[2 * i] = make_float2(v.x, v.y), b[2 * i + 1] = make_float2(v.z, v.w);
+                    }
+                } else {
+                    weights(tile, w, b);
+                }
+                put(out, tile, f[k], at, mean, r, w, b);
             }
         } while (kWalks && row < a.rows);
+        if (PAIR) cluster_sync();  // the neighbour has read this block's parts
     } else {
         __shared__ float sums[2][32];
         const int tiles = (a.cols + past + kTileCols - 1) / kTileCols;
@@ -746,31 +782,59 @@ template <int DT> bool same_runs(const void *p, int64_t stride, const void *q, i
     return q == nullptr || (past_of<DT>(p) == past_of<DT>(q) && (stride - other) % 8 == 0);
 }
 
+// Tiles a thread: as few as hold the row in 16 warps, which is the shortest way for
+// few rows.  Where there are many, two keep more loads on their way, and four pay for
+// the statistics of wide 16-bit rows: 16384 rows of 4096 bf16 take 88 us with four,
+// 16384 of 4001 96 us with four and 115 with one; 2048 binary32 93 us with one, 89
+// with two.  Rows of more than 32 tiles: few go to clusters of two blocks (30 of 12480
+// bf16 4.3 us, by one block of four tiles a thread 5.9).  Many go to one block: 8192
+// of 16384 bf16 166 us by walkers, 224 by a block a row, 303 by clusters; 4096 of
+// 16384 binary32 167 us by a block a row, 218 by walkers, 188 by clusters; but shifted
+// rows of binary32, for which the registers do not suffice, to clusters, 230 and 256 us.
 template <int DT, int ROWS> cudaError_t layernorm_launch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
+    constexpr bool kNarrow = DT != DT_F32;
     const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (ROWS == kShifted ? 7 : 0) + kTileCols - 1) / kTileCols);
     const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
     info->vec_bytes = ROWS != kApart ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
     int kt = tiles_per_thread(tiles, kLayerNormWarps, 4);
-    if (many && kt != 0 && ROWS != kShifted) kt = std::max(kt, tiles == 1 ? 1 : DT != DT_F32 && tiles > 8 ? 4 : 2);
+    const bool pair = ROWS != kApart && kt == 4 && (!many || (ROWS == kShifted && !kNarrow));
+    if (pair) kt = 2;
+    else if (many && kt != 0) kt = std::max(kt, tiles == 1 ? 1 : kNarrow && tiles > (ROWS == kShifted ? 6 : 8) ? 4 : 2);
+    const int blocks = pair ? 2 : 1;  // to a row
     int warps = 32, per_block = 1;
     if (kt != 0) {
-        warps = (tiles + kt - 1) / kt;
+        warps = (tiles + blocks * kt - 1) / (blocks * kt);
         if (warps == 1 && many) per_block = 8;
     }
-    int64_t grid = (a.rows + per_block - 1) / per_block;
-    if (ROWS == kShifted && many && (kt == 1 || kt == 2)) {  // walkers, as many as an SM holds at 64 or 128 registers
-        const int64_t most = static_cast<int64_t>(sms) * std::max(1, 32 / kt / (warps * per_block)) / 8 * 8;
-        if (most > 0) grid = std::min(grid, most);
+    const bool small = kNarrow && ROWS != kShifted && kt == 4 && warps <= 8;
+    int64_t teams = (a.rows + per_block - 1) / per_block;
+    size_t smem = 0;
+    if (kt != 0 && layernorm_walks(DT, ROWS, kt, small ? 8 : 16)) {
+        smem = static_cast<size_t>(kt) * warps * per_block * 32 * 4 * sizeof(float4);
+        if (many) {  // as many walkers as an SM holds at 64 or 128 registers
+            const int resident = std::max(1, (kt == 1 ? 32 : 16) / (warps * per_block));
+            const int64_t most = static_cast<int64_t>(sms) * resident / (8 * blocks) * 8;
+            if (most > 0) teams = std::min(teams, most);
+        }
     }
-    const dim3 block(32 * warps, per_block);
-    info->grid = static_cast<int>(grid);
+    info->grid = static_cast<int>(blocks * teams);
     info->block = 32 * warps * per_block;
-    auto kernel = kt == 0   ? layernorm_kernel<DT, ROWS, 1, false, 32>
-                  : kt == 1 ? layernorm_kernel<DT, ROWS, 1, true, 16>
-                  : kt == 2 ? layernorm_kernel<DT, ROWS, 2, true, 16>
-                  : warps <= 8 ? layernorm_kernel<DT, ROWS, 4, true, 8>
-                               : layernorm_kernel<DT, ROWS, 4, true, 16>;
-    return launch_rows(kernel, dim3(grid), block, 0, 1, s, a);
+    auto kernel = kt == 0   ? layernorm_kernel<DT, ROWS, 1, false, 32, false>
+                  : kt == 1 ? layernorm_kernel<DT, ROWS, 1, true, 16, false>
+                            : layernorm_kernel<DT, ROWS, 2, true, 16, false>;
+    if constexpr (kNarrow || ROWS != kShifted)
+        if (kt == 4) kernel = layernorm_kernel<DT, ROWS, 4, true, 16, false>;
+    if constexpr (kNarrow && ROWS != kShifted)
+        if (small) kernel = layernorm_kernel<DT, ROWS, 4, true, 8, false>;
+    if constexpr (ROWS != kApart)
+        if (pair) kernel = layernorm_kernel<DT, ROWS, 2, true, 16, true>;
+    if (smem > 32 * 1024) {  // up to 48 KiB less the kernel's own variables go without asking
+        static std::atomic<uint64_t> ready[5];
+        constexpr int kMost = 4 * kLayerNormWarps * 32 * 4 * sizeof(float4);
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), kMost, &ready[pair ? 3 : kt]);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_rows(kernel, dim3(info->grid), dim3(32 * warps, per_block), smem, blocks, s, a);
 }
 
 template <int DT> cudaError_t layernorm_dispatch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {

@@ -19,7 +19,9 @@ STEPS = 64 * EPS32
 SHAPES = [(1, 1, 0, 0), (3, 7, 0, 0), (9, 3, 0, 5), (2, 8, 0, 0), (5, 255, 0, 0), (4, 256, 8, 0), (4, 257, 0, 0),
           (17, 256, 3, 7), (3, 1000, 0, 1), (2, 1001, 7, 3), (7, 5120, 0, 0), (2, 8192, 64, 8), (2, 8199, 0, 0),
           (3, 4096, 1, 2), (1, 16384, 0, 0), (2, 16390, 0, 0), (5, 16380, 3, 6), (700, 64, 0, 0), (701, 300, 4, 0),
-          (700, 61, 0, 3), (650, 2048, 0, 0), (620, 4096, 0, 0), (613, 5001, 0, 0), (1, 40003, 0, 0), (3, 33001, 0, 3)]
+          (700, 61, 0, 3), (650, 2048, 0, 0), (620, 4096, 0, 0), (613, 5001, 0, 0), (1, 40003, 0, 0), (3, 33001, 0, 3),
+          (640, 1801, 0, 0), (3, 12480, 0, 0), (700, 9001, 0, 0), (613, 9344, 0, 0), (611, 12288, 8, 0), (700, 16384, 0, 0),
+          (620, 16377, 0, 3)]
 
 
 def make(rows, cols, dtype, pad, offset, seed, spread=1.0, at=0.0):
@@ -95,7 +97,7 @@ def test_no_residual(dtype, cols, given):
     check_forward(got, x.t, None, w, b, 0.0, dtype)
 
 
-@pytest.mark.parametrize("cols", [64, 1003, 4096, 20001])
+@pytest.mark.parametrize("cols", [64, 1003, 4096, 12000, 12001, 20001])
 @pytest.mark.parametrize("at", [1e3, -1e6])
 def test_mean_far_from_zero(cols, at):
     """Rows of spread 1 around a mean of up to 1e6: the elements hold the spread to 2^-5, and y loses no more."""
@@ -107,7 +109,7 @@ def test_mean_far_from_zero(cols, at):
     assert float((got[0].double() - want.y).abs().max()) < 200 * EPS32 * float(want.y.abs().max() + 4)
 
 
-@pytest.mark.parametrize("cols", [64, 1003, 20001])
+@pytest.mark.parametrize("cols", [64, 1003, 12000, 12001, 20001])
 def test_constant_and_outlying_rows(cols):
     x = torch.full((4, cols), 1234.567, device="cuda")
     x[1] = 0.0
@@ -122,7 +124,7 @@ def test_constant_and_outlying_rows(cols):
     check_forward(got, x, None, None, b, 1e-5, "f32")
 
 
-@pytest.mark.parametrize("cols", [320, 321, 20001])
+@pytest.mark.parametrize("cols", [320, 321, 12000, 12001, 20001])
 def test_nan_and_infinity(cols):
     x = randn((4, cols), 16)
     x[0, 5], x[1, 0], x[2, cols - 1] = math.nan, math.inf, -math.inf
@@ -132,7 +134,7 @@ def test_nan_and_infinity(cols):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
-@pytest.mark.parametrize("rows,cols", [(5, 512), (5, 1003), (700, 40), (5, 33000), (3, 33001)])
+@pytest.mark.parametrize("rows,cols", [(5, 512), (5, 1003), (700, 40), (5, 33000), (3, 33001), (700, 9001), (700, 16000)])
 @pytest.mark.parametrize("form", ["y=x,h=residual", "y=residual,h=x", "h=x", "y=x"])
 def test_in_place(dtype, rows, cols, form):
     x, r = make(rows, cols, dtype, 0, 0, 17), make(rows, cols, dtype, 0, 0, 18)
