@@ -540,7 +540,9 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
         *at = v;
     };
     const float per_col = 1.0f / static_cast<float>(a.cols);
-    // A row's first pass: its columns' sums, and its own two to `sums`.
+    // A row's first pass: its columns' sums, and its own two to `sums`.  The second is of
+    // g (h - m), whose r comes later: columns outside the row have g 0 and h 0, and -m r
+    // might be infinite.
     auto add_row = [&](int slot, float mean, float rstd, float2 *sums) {
         const float2 m = both(-mean), r = both(rstd);
         if (!ALIGNED && col(0, 0) < 0) {
@@ -555,8 +557,8 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
             held(slot, 1, k, n);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                n[j] = mul2(add2(n[j], m), r);
-                dw[k][j] = fma2(g[j], n[j], dw[k][j]);
+                n[j] = add2(n[j], m);
+                dw[k][j] = fma2(g[j], mul2(n[j], r), dw[k][j]);
                 db[k][j] = add2(g[j], db[k][j]);
                 g[j] = mul2(g[j], w[k][j]);
                 c1 = add2(c1, g[j]);
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
         if (row + writers < a.rows) add_row(next_slot, next_mean, next_rstd, part[turn ^ 1]);
         if (PAIR) cluster_arrive();
         const float2 m = both(-mean), r = both(rstd);
-        const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * per_col * rstd);
+        const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * rstd * per_col * rstd);
         T *dx = static_cast<T *>(row_of<DT>(a.dx, row, a.dx_stride));
 #pragma unroll
         for (int k = 0; k < KT; ++k) {

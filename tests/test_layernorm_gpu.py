@@ -210,6 +210,18 @@ def test_backward_of_matrices_whose_rows_lie_apart(dtype, rows, cols, places):
     assert all(m.intact() for m in (dy, h, dh, dx, w))
 
 
+@pytest.mark.parametrize("cols", [64, 203, 1003, 9000, 9001, 20001])
+def test_backward_of_constant_rows_far_out(cols):
+    """m r is past binary32, and no column of the row has it: dx = r (g - mean(g)), dweight = 0."""
+    m, r = 2e36, 316.0
+    h, dy = torch.full((5, cols), m, device="cuda"), randn((5, cols), 31)
+    mean, rstd = (torch.full((5,), v, device="cuda") for v in (m, r))
+    mean.copy_(h[:, 0])
+    got = ew.ew_layernorm_grad(dy, h, None, mean, rstd)
+    check_backward(got, dy, h, None, mean, rstd, None, "f32")
+    assert not got[1].any()
+
+
 @pytest.mark.parametrize("rows,cols", [(9, 64), (9, 1003), (1300, 1003), (9, 8192), (200, 9001), (90, 16000), (9, 33001)])
 @pytest.mark.parametrize("place", ["dy", "dh"])
 def test_backward_in_place(rows, cols, place):
