@@ -788,20 +788,34 @@ template <int DT> bool same_runs(const void *p, int64_t stride, const void *q, i
 // few rows.  Where there are many, two keep more loads on their way, and four pay for
 // the statistics of wide 16-bit rows: 16384 rows of 4096 bf16 take 88 us with four,
 // 16384 of 4001 96 us with four and 115 with one; 2048 binary32 93 us with one, 89
-// with two.  Rows of more than 32 tiles: few go to clusters of two blocks (30 of 12480
-// bf16 4.3 us, by one block of four tiles a thread 5.9).  Many go to one block: 8192
-// of 16384 bf16 166 us by walkers, 224 by a block a row, 303 by clusters; 4096 of
-// 16384 binary32 167 us by a block a row, 218 by walkers, 188 by clusters; but shifted
-// rows of binary32, for which the registers do not suffice, to clusters, 230 and 256 us.
+// with two.  But walkers hold weights as well, fewer of them fit, and what matters is
+// how many columns an SM works on: 6392 rows of 2135 bf16 take 34 us with four (45 of
+// 64 tiles), 29 with one (27 of 32); of less than 8 tiles the barrier is short and one
+// is as good or better (7897 x 777 f16 17.0 us, 18.0 with four).
+//
+// Rows of more than 32 tiles: up to a row an SM go to clusters of two blocks (30 of 12480
+// bf16 4.3 us, by one block of four tiles a thread 5.9; 600 of 16384 22.5 and 16.0 us),
+// of shifted rows half as many.  More go to one block each: 8192 of 16384 bf16 166 us by
+// walkers, 224 by a block a row, 303 by clusters; 4096 of 16384 binary32 167 us by a
+// block a row, 218 by walkers, 188 by clusters; but shifted rows of binary32, for which
+// the registers do not suffice, to clusters, 230 and 256 us.
 template <int DT, int ROWS> cudaError_t layernorm_launch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
     constexpr bool kNarrow = DT != DT_F32;
     const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (ROWS == kShifted ? 7 : 0) + kTileCols - 1) / kTileCols);
     const bool many = a.rows >= 4 * static_cast<int64_t>(sms);
     info->vec_bytes = ROWS != kApart ? 8 * ElemOf<DT>::kBytes : ElemOf<DT>::kBytes;
     int kt = tiles_per_thread(tiles, kLayerNormWarps, 4);
-    const bool pair = ROWS != kApart && kt == 4 && (!many || (ROWS == kShifted && !kNarrow));
-    if (pair) kt = 2;
-    else if (many && kt != 0) kt = std::max(kt, tiles == 1 ? 1 : kNarrow && tiles > (ROWS == kShifted ? 6 : 8) ? 4 : 2);
+    const bool pair = ROWS != kApart && kt == 4 && (a.rows <= (ROWS == kShifted ? sms / 2 : sms) || (ROWS == kShifted && !kNarrow));
+    if (pair) {
+        kt = 2;
+    } else if (ROWS == kShifted && kNarrow && tiles >= 8) {
+        // tiles of the rows that an SM holds, of 32 by ones and of 64 by fours
+        const int one = kt == 1 ? tiles * (32 / tiles) : 0, four = tiles * (16 / ((tiles + 3) / 4));
+        if (many ? 4 * four >= 7 * one : kt == 2 && a.rows > sms) kt = 4;
+    } else if (kt != 0 && many) {
+        const bool spread = ROWS == kShifted && tiles > 2 && (kNarrow || a.rows < 32 * static_cast<int64_t>(sms));
+        kt = std::max(kt, tiles == 1 || spread ? 1 : kNarrow && tiles > 8 ? 4 : 2);
+    }
     const int blocks = pair ? 2 : 1;  // to a row
     int warps = 32, per_block = 1;
     if (kt != 0) {
@@ -813,11 +827,10 @@ template <int DT, int ROWS> cudaError_t layernorm_launch(const LayerNormArgs &a,
     size_t smem = 0;
     if (kt != 0 && layernorm_walks(DT, ROWS, kt, small ? 8 : 16)) {
         smem = static_cast<size_t>(kt) * warps * per_block * 32 * 4 * sizeof(float4);
-        if (many) {  // as many walkers as an SM holds at 64 or 128 registers
-            const int resident = std::max(1, (kt == 1 ? 32 : 16) / (warps * per_block));
-            const int64_t most = static_cast<int64_t>(sms) * resident / (8 * blocks) * 8;
-            if (most > 0) teams = std::min(teams, most);
-        }
+        // as many walkers as an SM holds at 64 or 128 registers
+        const int resident = std::max(1, (kt == 1 ? 32 : 16) / (warps * per_block));
+        const int64_t most = static_cast<int64_t>(sms) * resident / (8 * blocks) * 8;
+        if (most > 0) teams = std::min(teams, most);
     }
     info->grid = static_cast<int>(blocks * teams);
     info->block = 32 * warps * per_block;
