@@ -566,15 +566,20 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
             }
         }
         const float2 c = warp_sum2(make_float2(c1.x + c1.y, c2.x + c2.y));
-        if (lane == 0) sums[warp] = c;
+        if (lane == 0) {
+            sums[PAIR ? half * 16 + warp : warp] = c;
+            if (PAIR) *const_cast<float2 *>(in_block(&sums[half * 16 + warp], half ^ 1)) = c;
+        }
     };
     // read two rows ahead, and not touched before it is needed
     auto statistics = [&](int64_t row, float &m, float &r) {
         if (row < a.rows) m = a.mean[row], r = a.rstd[row];
     };
-    float2(*const part)[16] = parts[threadIdx.y];
-    if (threadIdx.x < 32) part[threadIdx.x / 16][threadIdx.x % 16] = both(0.0f);
-    __syncthreads();
+    constexpr int kParts = PAIR ? 32 : 16;  // of a row
+    float2 *const part = &parts[threadIdx.y][0][0];
+    for (int i = threadIdx.x; i < 2 * kParts; i += blockDim.x) part[i] = both(0.0f);
+    if (PAIR) cluster_sync();  // before the neighbour writes here
+    else __syncthreads();
 #pragma unroll 1
     for (int q = 0; q < depth; ++q) copy_next(q);
     float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
@@ -583,7 +588,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
     if (depth == 2) copies_left<1>();
     else if (depth == 3) copies_left<2>();
     else copies_left<3>();
-    if (writer < a.rows) add_row(0, mean, rstd, part[0]);
+    if (writer < a.rows) add_row(0, mean, rstd, part);
     if (PAIR) cluster_arrive();
     int turn = 0, slot = 0;
 #pragma unroll 1
@@ -592,11 +597,11 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
         float2 c = both(0.0f);
         if constexpr (PAIR) {
             cluster_wait();
-            c = warp_sum2(*in_block(&part[turn][lane & 15], lane >> 4));
+            c = warp_sum2(part[turn * kParts + lane]);
         } else {
             if (warps > 1) __syncthreads();
             else __syncwarp();
-            const float4 *all = reinterpret_cast<const float4 *>(part[turn]);
+            const float4 *all = reinterpret_cast<const float4 *>(part + turn * kParts);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 if (2 * i >= warps) break;
@@ -609,7 +614,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
         else copies_left<2>();
         float after_mean = 0.0f, after_rstd = 0.0f;
         statistics(row + 2 * writers, after_mean, after_rstd);
-        if (row + writers < a.rows) add_row(next_slot, next_mean, next_rstd, part[turn ^ 1]);
+        if (row + writers < a.rows) add_row(next_slot, next_mean, next_rstd, part + (turn ^ 1) * kParts);
         if (PAIR) cluster_arrive();
         const float2 m = both(-mean), r = both(rstd);
         const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * rstd * per_col * rstd);
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
         mean = next_mean, rstd = next_rstd, next_mean = after_mean, next_rstd = after_rstd;
     }
     copies_left<0>();
-    if (PAIR) cluster_wait();  // the neighbour has read this block's sums
+    if (PAIR) cluster_wait();  // the neighbour has written its last sums here
     if (a.partial == nullptr) return;
     // The block's sums: of one writer straight from the registers, where whole runs
     // can be written; otherwise by columns through the ring's place, the writers' in order.
@@ -874,7 +879,7 @@ cudaError_t layernorm_grad_dispatch(const LayerNormGradArgs &a, int64_t most_wri
     // two tiles, and instructions of wide 16-bit rows, where there are many.  16384 rows
     // of 2048 bf16: 50 us with two, 57 with one; 3000 rows: 17 and 16 us.
     if (kt == 1 && many && tiles == 2) kt = 2;
-    if (DT != DT_F32 && kt == 1 && tiles > 6 && a.rows >= 32 * static_cast<int64_t>(sms)) kt = 2;
+    if (DT != DT_F32 && kt == 1 && tiles > 5 && a.rows >= 32 * static_cast<int64_t>(sms)) kt = 2;
     if (kt == 0) kt = tiles_per_thread(tiles, kLayerNormWarps, 2);
     const bool pair = kt == 0 && runs && tiles <= 4 * kLayerNormWarps && (aligned || sms >= 16);  // 8 pairs of blocks
     if (pair) kt = 2;

@@ -13,7 +13,9 @@
 // The gradient needs the row's sums, so a row is worked over twice.  At the floor
 // it crosses DRAM once: policy_stream_kernel keeps it in shared memory in between.
 // policy_kernel reads it again, mostly from L2: for rows too short to be worth a
-// ring, rows too long, and the gradient from a given lse.
+// ring, rows too long, the gradient from a given lse, and where there is no more than
+// a row an SM, for which the lists below come late (loss and gradient of 7 rows of
+// 79525 bf16 5.9 us, with a ring 7.4; of 100 of 123400 binary32 24 and 32 us).
 #pragma once
 
 #include "ew_logits.cuh"
@@ -184,8 +186,8 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) polic
 // numbers: the rows with a token, in their order, go round the blocks (or
 // clusters), and so do those without, from the last block on.  Each block works its
 // list out for itself, from all tokens: 8 bytes a row, where a row has thousands.
-// 2048 rows of 131072 bf16, a quarter of them without a token, took 178 us by
-// numbers and 182 us by lists.
+// 2048 rows of 131072 bf16, a quarter of them without a token, took 188 us by
+// numbers and 182 us by lists, both by clusters of two; a block a row takes 157 us.
 //
 // Tokens, their numbers and logits are read for 32 of the block's rows at once, one
 // to a lane: what a row needs comes from a register.
@@ -551,13 +553,11 @@ template <int DT> cudaError_t policy_launch(const PolicyArgs &a, bool sums, bool
     constexpr int64_t kKiB = 1024;
     const int64_t bytes = static_cast<int64_t>(a.cols) * ElemOf<DT>::kBytes;
     const bool few = a.rows <= sms;
-    if (sums && !few && bytes > 24 * kKiB && bytes <= 32 * kKiB) return policy_stream<DT, 128>(a, grad, 0, sms, s, info);
-    if (sums && bytes > (few ? 16 : 32) * kKiB && bytes <= (few ? 32 : 64) * kKiB)
-        return policy_stream<DT, 256>(a, grad, 0, sms, s, info);
-    if (sums && bytes > (few ? 32 : 64) * kKiB) {
+    if (sums && !few && bytes > 24 * kKiB) {
+        if (bytes <= 32 * kKiB) return policy_stream<DT, 128>(a, grad, 0, sms, s, info);
+        if (bytes <= 64 * kKiB) return policy_stream<DT, 256>(a, grad, 0, sms, s, info);
         int shift = 0;
         while (shift < 3 && groups_of<DT, 512>(a.cols, shift) > kMostGroups) ++shift;
-        while (shift < 3 && a.rows << (shift + 1) <= sms && a.cols >> (shift + 1) >= 4096) ++shift;
         if (groups_of<DT, 512>(a.cols, shift) <= kMostGroups) return policy_stream<DT, 512>(a, grad, shift, sms, s, info);
     }
     if (!few && bytes <= 32 * kKiB) return policy_twice<DT, kNarrow>(a, sums, grad, 0, s, info);
