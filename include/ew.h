@@ -364,7 +364,8 @@ EW_API int64_t ew_rmsnorm_grad_workspace(int64_t rows, int64_t cols);
  * mean costs it nothing; mean_out is rounded.  y may be x or residual, and h_out may be x
  * or residual (the same base and stride), but y is not h_out.  eps >= 0.  A NaN or
  * an infinity makes y's whole row and rstd NaN.  Where the variance is past binary32
- * rstd is 0; where it and eps are 0 rstd is infinite and y NaN. */
+ * rstd is 0; where it and eps are 0 rstd is infinite and y NaN.  Elements whose sum is
+ * past binary32 may make y NaN. */
 EW_API ew_status ew_layernorm(ew_dtype dtype, const void *x, int64_t x_stride, const void *residual,
                               int64_t residual_stride, ew_dtype wtype, const void *weight, const void *bias, float eps,
                               void *y, int64_t y_stride, void *h_out, int64_t h_stride, float *mean_out,
@@ -514,8 +515,8 @@ EW_API ew_status ew_distill_step(ew_dtype dtype, ew_index itype, const void *log
  * advantage, old_logp, ref_logp, dloss: binary32, one a row.  ref_logp may be NULL; with
  * it NULL or kl 0 the terms with apart are left out.  0 <= clip_low <= 1, clip_high >= 0
  * (infinity: not clipped above), 0 <= kl < infinity, 2^-20 <= scale <= 2^20.  An
- * advantage of 0 has gain and slope 0, a dloss of 0 gradient 0.  A row without a token has loss, logp and lse 0
- * and gradient 0, and its logits are not read.  Masked logits have p = 0; a token
+ * advantage of 0 has gain and slope 0, a dloss of 0 gradient 0.  A row without a token
+ * has loss, logp and lse 0 and gradient 0, and its logits are not read.  Masked logits have p = 0; a token
  * there has logp -inf, and with kl an infinite loss.  A row of -inf alone has lse
  * and logp -inf and gradient 0, a row with NaN or +inf NaN in all its results.
  * ew_policy computes loss, logp and lse (the last two may be NULL), ew_policy_grad

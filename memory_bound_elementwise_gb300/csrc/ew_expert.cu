@@ -28,7 +28,9 @@ namespace {
 // ballots, and a count for each warp and expert says how many came before.  Up to
 // kTileSlots slots, one block does all of it in one launch; more take two, the
 // first leaving each slot's rank within its block in `positions` and the blocks'
-// counts in the workspace.
+// counts in the workspace.  Latency bounds it: 512 slots of 128 experts take 3.8 us,
+// 4000 6.3, 131072 9.0 in a graph.  Rows of no slot are marked before anything else;
+// marked at the end, expert by expert, they took 10 to 37 us.
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -245,7 +247,10 @@ template <int DT, bool VEC> struct Mover {
 // ---------------------------------------------------------------- dispatch
 
 // A warp takes U consecutive tiles of a token.  VEC: a tile is read once;
-// otherwise anew for each of the places, whose rows may start anywhere.
+// otherwise anew for each of the places, whose rows may start anywhere.  Bounded by
+// what it writes: 16384 tokens of 4096 bf16 to 8 experts 199 us at a floor of 202 with
+// the sort (0.96 of a plain copy's rate); of 2001 columns 108 us at 89.  Few
+// tokens take a warp for each tile, so that all SMs have one.
 template <int DT, bool VEC, int U>
 __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(ExpertRowsArgs a, uint32_t zero_blocks, int zero_each, int tiles) {
     enter_grid();
@@ -285,7 +290,9 @@ __global__ void __launch_bounds__(32 * kWarpsABlock) expert_dispatch_kernel(Expe
 // ---------------------------------------------------------------- combine
 
 // A warp takes U consecutive tiles of a token, and of its slots KB at a time, all
-// of whose loads are under way together.
+// of whose loads are under way together: in registers, so KB x U is what fits 80 of
+// them.  Bounded by what it reads: 16384 tokens of 4096 bf16 from 8 experts each 206
+// us at a floor of 202; of 2001 columns 150 us at 99, by 4-byte and 2-byte loads.
 template <int DT, bool VEC, int KB, int U>
 __global__ void __launch_bounds__(32 * kWarpsABlock, !VEC && (KB <= 2 || DT == DT_F32) ? 4 : DT != DT_F32 ? 3 : 2) expert_combine_kernel(ExpertRowsArgs a, int tiles) {
     enter_grid();
@@ -359,7 +366,10 @@ template <int N> __device__ __forceinline__ float warp_sums_of(float (&v)[N]) {
 }
 
 // `split` warps of a block (1, 2, 4 or 8) take a token, tile t warp t mod split, KB
-// of its slots at a time.
+// of its slots at a time: a tile of dout is read once and both used for the slots'
+// rows and multiplied with theirs.  Bounded by memory: 16384 tokens of 4096 bf16 to 8
+// experts 355 us at a floor of 343; 5003 of 1001 binary32 to 2 16.7 at 15.1; of 2001
+// bf16 242 at 168, where dout is kept for rows at either half of a word.
 template <int DT, bool VEC, int KB>
 __global__ void __launch_bounds__(32 * kWarpsABlock) expert_combine_grad_kernel(ExpertRowsArgs a, uint32_t zero_blocks, int zero_each,
                                                                                int tiles, int split) {
