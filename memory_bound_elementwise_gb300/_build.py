@@ -125,7 +125,7 @@ def _link_binding(obj, torch_lib):
     tmp = BINDING + ".tmp.%d" % os.getpid()
     # by name: the library has no soname, and by path its place would be written down
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-lc10",
-           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
+           "-lc10_cuda", "-ltorch_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if r.returncode != 0:
         raise RuntimeError("link of the torch binding failed:\n%s" % r.stdout)

@@ -14,7 +14,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -60,8 +60,10 @@ int64_t integer(PyObject *o) {
 
 struct Device {
     c10::DeviceIndex index;
-    at::TensorOptions options(at::ScalarType t) const {
-        return at::TensorOptions().dtype(t).device(c10::Device(c10::kCUDA, index));
+    // From the caching allocator without a way through the dispatcher, which takes 0.7 us a
+    // tensor: a layer norm's call with its four outputs 6.0 us of host time, 8.4 by at::empty.
+    Tensor empty(at::IntArrayRef sizes, at::ScalarType t) const {
+        return at::detail::empty_cuda(sizes, t, c10::Device(c10::kCUDA, index), std::nullopt);
     }
     ew_stream_t stream() const {
         return reinterpret_cast<ew_stream_t>(c10::cuda::getCurrentCUDAStream(index).stream());
@@ -152,7 +154,7 @@ struct Output {
         o = given;
     }
     void *make(at::IntArrayRef sizes, at::ScalarType type, Device d) {
-        Tensor t = at::empty(sizes, d.options(type));
+        Tensor t = d.empty(sizes, type);
         void *p = t.data_ptr();
         o = THPVariable_Wrap(std::move(t));
         if (o == nullptr) throw Raised{};
@@ -194,9 +196,9 @@ struct Workspace {
     int64_t bytes;
     Workspace(int64_t need, const char *what, Device d) : bytes(need) {
         if (need < 0) REFUSE(PyExc_ValueError, "%s: sizes out of range", what);
-        t = at::empty({need}, d.options(at::kByte));
+        if (need > 0) t = d.empty({need}, at::kByte);
     }
-    void *p() const { return t.data_ptr(); }
+    void *p() const { return t.defined() ? t.data_ptr() : nullptr; }
 };
 
 // ---------------------------------------------------------------- embedding
@@ -668,7 +670,8 @@ PyObject *set_check(PyObject *, PyObject *fn) {
 PyMethodDef g_methods[] = {
     ENTRY(embed, 4), ENTRY(embed_grad, 6), ENTRY(rmsnorm, 7), ENTRY(rmsnorm_quant, 10), ENTRY(rmsnorm_grad, 7),
     ENTRY(layernorm, 9), ENTRY(layernorm_grad, 9), ENTRY(expert_sort, 3), ENTRY(expert_dispatch, 3),
-    ENTRY(expert_combine, 5), ENTRY(expert_combine_grad, 6), ENTRY(logprob, 4), ENTRY(logprob_grad, 8), ENTRY(distill, 4), ENTRY(distill_grad, 7), ENTRY(distill_step, 6),
+    ENTRY(expert_combine, 5), ENTRY(expert_combine_grad, 6), ENTRY(logprob, 4), ENTRY(logprob_grad, 8), ENTRY(distill, 4),
+    ENTRY(distill_grad, 7), ENTRY(distill_step, 6),
     ENTRY(policy, 9), ENTRY(policy_grad, 13), ENTRY(policy_step, 11),
     {"set_check", set_check, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 
