@@ -169,7 +169,9 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) polic
 // ---------------------------------------------------------------- rows held in shared memory
 //
 // A block walks over rows; one of 512 threads an SM (or a cluster of up to 8 for a
-// row), two of 256 for rows up to 64 KiB, four of 128 up to 32 KiB.  The block's
+// row), two of 256 for rows up to 96 KiB, which their rings hold (4096 rows of 40000
+// bf16 104 us, by one block an SM 115; of 65536, which they do not hold, 190 and 176),
+// four of 128 up to 32 KiB.  The block's
 // share of a row is `groups` groups of 4 chunks a thread; a ring of kRing groups is
 // filled by asynchronous copies in the order of the stream of groups, row after
 // row, and a group's place is filled again as soon as the gradient (or, for the
@@ -555,7 +557,7 @@ template <int DT> cudaError_t policy_launch(const PolicyArgs &a, bool sums, bool
     const bool few = a.rows <= sms;
     if (sums && !few && bytes > 24 * kKiB) {
         if (bytes <= 32 * kKiB) return policy_stream<DT, 128>(a, grad, 0, sms, s, info);
-        if (bytes <= 64 * kKiB) return policy_stream<DT, 256>(a, grad, 0, sms, s, info);
+        if (bytes <= 96 * kKiB) return policy_stream<DT, 256>(a, grad, 0, sms, s, info);
         int shift = 0;
         while (shift < 3 && groups_of<DT, 512>(a.cols, shift) > kMostGroups) ++shift;
         if (groups_of<DT, 512>(a.cols, shift) <= kMostGroups) return policy_stream<DT, 512>(a, grad, shift, sms, s, info);
