@@ -172,7 +172,9 @@ __global__ void __launch_bounds__(THREADS, kResident * kThreads / THREADS) polic
 // row), two of 256 for rows up to 96 KiB, which their rings hold (4096 rows of 40000
 // bf16 104 us, by one block an SM 115; of 65536, which they do not hold, 190 and 176),
 // four of 128 up to 32 KiB.  The block's
-// share of a row is `groups` groups of 4 chunks a thread; a ring of kRing groups is
+// share of a row, from the line in which it begins on, so that a warp's 512 bytes are
+// whole lines wherever the row starts (8192 rows of 50257 bf16 336 us, 353 from the
+// first chunk on), is `groups` groups of 4 chunks a thread; a ring of kRing groups is
 // filled by asynchronous copies in the order of the stream of groups, row after
 // row, and a group's place is filled again as soon as the gradient (or, for the
 // loss alone, the sum) has used it.  Of a share of more than kRing groups the first
@@ -230,6 +232,10 @@ __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
     const float ax = a.scale * kLog2e;
     auto share_of = [&](int64_t row) {
         return Share<DT>(row_of<DT>(a.logits, row, a.stride), a.cols, block, split);
+    };
+    // the chunk, at or before the share's first, from which a warp's chunks are whole lines
+    auto begin_of = [&](const Share<DT> &sh) {
+        return sh.first - static_cast<int>(reinterpret_cast<uintptr_t>(sh.row + sh.column(sh.first, 0)) / 16 % 8);
     };
     // -1: none
     auto token_of = [&](int64_t row) {
@@ -302,25 +308,29 @@ __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
         // Copies: the next group of the stream into the ring; past the last row an empty
         // one, so that the count holds.
         int copy_number = 0, copy_group = 0, copy_place = 0, copy_count = 0;  // chunks of this thread's row from its next one on
+        bool copy_before = false;                                             // its next one is before the share's first
         const T *copy_from = nullptr;
         auto start_copies = [&] {
             copy_count = 0;
             if (copy_number < rows) {
                 const Share<DT> sh = share_of(base + list[copy_number]);
-                copy_from = sh.row + sh.column(sh.first + tid, 0);
-                copy_count = sh.end - sh.first - tid;
+                const int c = begin_of(sh) + tid;
+                copy_from = sh.row + sh.column(c, 0);
+                copy_count = sh.end - c;
+                copy_before = c < sh.first;
             }
         };
         auto copy_next = [&] {
 #pragma unroll
             for (int u = 0; u < kGroup; ++u)
-                if (u * THREADS < copy_count)
+                if (u * THREADS < copy_count && !(u == 0 && copy_before))
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
                                  :: "r"(ring_at + (copy_place * kGroup + u) * THREADS * 16),
                                     "l"(copy_from + u * THREADS * Chunk<DT>::kElems) : "memory");
             asm volatile("cp.async.commit_group;" ::: "memory");
             copy_from += kGroupChunks * Chunk<DT>::kElems;
             copy_count -= kGroupChunks;
+            copy_before = false;
             ++copy_group;
             if (AGAIN > 0 && copy_group == groups) start_copies();
             if (copy_group == groups + AGAIN) {
@@ -366,6 +376,7 @@ __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
             }
             const int col = __shfl_sync(kAllLanes, my_token, from);
             const Share<DT> sh = share_of(row);
+            const int begin = begin_of(sh);
             const bool single = tid < sh.singles;
             const float one = single ? sh.at(sh.single(tid)) : kNegInf;
 
@@ -375,14 +386,16 @@ __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
             auto add_group = [&](int g) {
                 const int place = take_place();
                 Chunk<DT> r[kGroup];
-                const int c0 = sh.first + g * kGroupChunks;
-                if (c0 + kGroupChunks <= sh.end) {
+                const int c0 = begin + g * kGroupChunks;
+                if (c0 >= sh.first && c0 + kGroupChunks <= sh.end) {
 #pragma unroll
                     for (int u = 0; u < kGroup; ++u) r[u] = held(place, u);
                 } else {
 #pragma unroll
-                    for (int u = 0; u < kGroup; ++u)
-                        r[u] = c0 + u * THREADS + tid < sh.end ? held(place, u) : masked_chunk<DT>();
+                    for (int u = 0; u < kGroup; ++u) {
+                        const int c = c0 + u * THREADS + tid;
+                        r[u] = c >= sh.first && c < sh.end ? held(place, u) : masked_chunk<DT>();
+                    }
                 }
                 add_chunks<DT, false>(pairs, r, ax);
                 if (!GRAD || g < AGAIN) copy_next();
@@ -445,18 +458,20 @@ __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
                         place = take_place();
                     }
                     if (!r.careful) {
-                        const int c0 = sh.first + g * kGroupChunks + tid;
+                        const int c0 = begin + g * kGroupChunks + tid;
                         T *to = out + sh.column(c0, 0);
-                        if (sh.first + (g + 1) * kGroupChunks <= sh.end) {
+                        if (c0 - tid >= sh.first && c0 - tid + kGroupChunks <= sh.end) {
 #pragma unroll
                             for (int u = 0; u < kGroup; ++u)
                                 store_chunk<DT>(to + u * THREADS * Chunk<DT>::kElems, grad(held(place, u)), apart, true);
                         } else {
 #pragma unroll
-                            for (int u = 0; u < kGroup; ++u)
-                                if (c0 + u * THREADS < sh.end)
+                            for (int u = 0; u < kGroup; ++u) {
+                                const int c = c0 + u * THREADS;
+                                if (c >= sh.first && c < sh.end)
                                     store_chunk<DT>(to + u * THREADS * Chunk<DT>::kElems, grad(held(place, u)), apart,
-                                                    c0 - lane + 31 + u * THREADS < sh.end);
+                                                    c - lane >= sh.first && c - lane + 31 < sh.end);
+                            }
                         }
                     }
                     copy_next();  // into this group's place
@@ -468,7 +483,7 @@ __global__ void __launch_bounds__(THREADS, Stream<THREADS>::kBlocks)
                     // the thread that has the single element.
                     if (sh.holds(col)) {
                         const bool in_chunk = col >= sh.head && col < sh.tail0;
-                        const int owner = in_chunk ? ((col - sh.head) / Chunk<DT>::kElems - sh.first) % THREADS
+                        const int owner = in_chunk ? ((col - sh.head) / Chunk<DT>::kElems - begin) % THREADS
                                                    : col < sh.head ? col : sh.n_head + col - sh.tail0;
                         __syncwarp();
                         if (tid == owner) store_one<DT>(out, col, at_token);
@@ -523,14 +538,19 @@ template <int THREADS, typename Kernel> cudaError_t rows_at_once(Kernel kernel, 
     if (e == cudaSuccess) known[shift].store(*rows = std::max(1, *rows), std::memory_order_relaxed);
     return e;
 }
-// Groups that a row's share takes when 2^shift blocks of THREADS split it.
-template <int DT, int THREADS> int groups_of(int cols, int shift) {
-    return std::max(1, (split_of<DT>(cols, shift).each + Stream<THREADS>::kGroupChunks - 1) / Stream<THREADS>::kGroupChunks);
+// Groups that a row's share takes when 2^shift blocks of THREADS split it, up to 7
+// chunks more where a share may begin within a line.
+template <int DT, int THREADS> int groups_of(const PolicyArgs &a, int shift) {
+    const int64_t each = split_of<DT>(a.cols, shift).each;
+    const bool lines = reinterpret_cast<uintptr_t>(a.logits) % 128 == 0 && a.stride * ElemOf<DT>::kBytes % 128 == 0 &&
+                       (shift == 0 || each % 8 == 0);
+    constexpr int kChunks = Stream<THREADS>::kGroupChunks;
+    return static_cast<int>(std::max<int64_t>(1, (each + (lines ? 0 : 7) + kChunks - 1) / kChunks));
 }
 template <int DT, int THREADS>
 cudaError_t policy_stream(const PolicyArgs &a, bool grad, int shift, int sms, cudaStream_t s, LaunchInfo *info) {
     const Split split = split_of<DT>(a.cols, shift);
-    const int groups = groups_of<DT, THREADS>(a.cols, shift), again = grad ? std::max(0, groups - kRing) : 0;
+    const int groups = groups_of<DT, THREADS>(a, shift), again = grad ? std::max(0, groups - kRing) : 0;
     auto kernel = grad ? policy_stream_kernel<DT, true, THREADS, 0> : policy_stream_kernel<DT, false, THREADS, 0>;
     if constexpr (THREADS == 512) {
         if (again == 1) kernel = policy_stream_kernel<DT, true, THREADS, 1>;
@@ -557,10 +577,10 @@ template <int DT> cudaError_t policy_launch(const PolicyArgs &a, bool sums, bool
     const bool few = a.rows <= sms;
     if (sums && !few && bytes > 24 * kKiB) {
         if (bytes <= 32 * kKiB) return policy_stream<DT, 128>(a, grad, 0, sms, s, info);
-        if (bytes <= 96 * kKiB) return policy_stream<DT, 256>(a, grad, 0, sms, s, info);
+        if (groups_of<DT, 256>(a, 0) <= kRing) return policy_stream<DT, 256>(a, grad, 0, sms, s, info);
         int shift = 0;
-        while (shift < 3 && groups_of<DT, 512>(a.cols, shift) > kMostGroups) ++shift;
-        if (groups_of<DT, 512>(a.cols, shift) <= kMostGroups) return policy_stream<DT, 512>(a, grad, shift, sms, s, info);
+        while (shift < 3 && groups_of<DT, 512>(a, shift) > kMostGroups) ++shift;
+        if (groups_of<DT, 512>(a, shift) <= kMostGroups) return policy_stream<DT, 512>(a, grad, shift, sms, s, info);
     }
     if (!few && bytes <= 32 * kKiB) return policy_twice<DT, kNarrow>(a, sums, grad, 0, s, info);
     return policy_twice<DT, kThreads>(a, sums, grad, split_shift(a.rows, a.cols, sms), s, info);
