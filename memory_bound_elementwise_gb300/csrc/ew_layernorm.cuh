@@ -321,6 +321,90 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
     }
 }
 
+// Aligned rows of up to 128 columns, such as the heads of a query: LANES lanes (8 or
+// 16) to a row, 8 elements each, so that the steps of the reductions are shared by 4 or
+// 2 rows of a warp.  131072 rows of 64 bf16 take 12 us (floor 10; a warp a row 60),
+// 65536 of 128 12 us (10; 31), of 128 binary32 22 us (20; 33).  TURNS rows of a lane
+// are under way together: two where there are many rows of 16 bits (262144 of 128 bf16
+// 46 us, 52 with one), one otherwise (2464 of 64 1.7 us, 2.2 with two; 65536 of 128
+// binary32 22 and 24).  Many 16-bit rows of up to 256 columns go this way, too, a
+// warp to two rows: 65536 of 192 23 us (33), of 256 24 us (26).
+constexpr int kNarrowWarps = 8;
+template <int DT, int LANES, int TURNS>
+__global__ void __launch_bounds__(32 * kNarrowWarps) layernorm_narrow_kernel(const __grid_constant__ LayerNormArgs a) {
+    enter_grid();
+    constexpr int kRows = 32 / LANES;  // of a warp at a time
+    const int lane = threadIdx.x & (LANES - 1), group = (threadIdx.x & 31) / LANES;
+    const unsigned peers = (kAllLanes >> (32 - LANES)) << (group * LANES);
+    const int64_t warp = static_cast<int64_t>(blockIdx.x) * kNarrowWarps + (threadIdx.x >> 5);
+    const int64_t first = warp * kRows * TURNS + group;
+    auto sum = [](float v) {
+#pragma unroll
+        for (int d = LANES / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kAllLanes, v, d);
+        return v;
+    };
+    Raw8<DT> rx[TURNS], rr[TURNS];
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t) {
+        const int64_t row = min(first + t * kRows, a.rows - 1);  // behind the last one it again
+        rx[t] = load_tile<DT, true>(row_of<DT>(a.x, row, a.x_stride), 0, a.cols, lane);
+        if (a.residual) rr[t] = load_tile<DT, true>(row_of<DT>(a.residual, row, a.residual_stride), 0, a.cols, lane);
+    }
+    float2 w[4], b[4];
+    load_columns<DT, kAligned>(a.weight, a.weight_f32, 1.0f, 0, 0, a.cols, lane, w);
+    load_columns<DT, kAligned>(a.bias, a.weight_f32, 0.0f, 0, 0, a.cols, lane, b);
+#pragma unroll
+    for (int t = 0; t < TURNS; ++t) {
+        const int64_t row = first + t * kRows;
+        const bool given = row < a.rows;
+        float2 f[4], d[4];
+        unpack8<DT>(rx[t], f);
+        if (a.residual) {
+            float2 g[4];
+            unpack8<DT>(rr[t], g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
+        }
+        // lane 0 of a row has its first element
+        const unsigned held = __ballot_sync(kAllLanes, lane * 8 < a.cols) & peers;
+        const unsigned negative = __ballot_sync(kAllLanes, lane * 8 < a.cols && f[0].x < 0.0f) & peers;
+        const float one = __shfl_sync(kAllLanes, f[0].x, group * LANES);
+        const float at = negative == 0 || negative == held ? one : 0.0f;
+        float2 s2 = both(0.0f), q2 = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = add2(f[j], both(-at));
+        clip_columns<true>(0, 0, a.cols, lane, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
+        const float mean = sum(s2.x + s2.y) * a.per_col;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = d[j] = add2(add2(f[j], both(-at)), both(-mean));
+        clip_columns<true>(0, 0, a.cols, lane, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
+        const float r = rsqrtf(fmaf(sum(q2.x + q2.y), a.per_col, a.eps));
+        if (!given) continue;
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = at + mean;
+            if (a.rstd) a.rstd[row] = r;
+        }
+        if (a.h) {
+            float2 h[4];
+            unpack8<DT>(rx[t], h);
+            if (a.residual) {
+                float2 g[4];
+                unpack8<DT>(rr[t], g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = add2(h[j], g[j]);
+            }
+            store_tile<DT, true>(row_of<DT>(a.h, row, a.h_stride), 0, a.cols, lane, pack8<DT>(h));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(f[j], both(r)), w[j], b[j]);
+        store_tile<DT, true>(row_of<DT>(a.y, row, a.y_stride), 0, a.cols, lane, pack8<DT>(f));
+    }
+}
+
 // ---------------------------------------------------------------- backward
 //
 // With n = (h - m) r and g = dy w:  dx = r (g - mean(g) - n mean(g n)) + dh.
@@ -866,13 +950,29 @@ template <int DT, int ROWS> cudaError_t layernorm_launch(const LayerNormArgs &a,
     return launch_rows(kernel, dim3(info->grid), dim3(32 * warps, per_block), smem, blocks, s, a);
 }
 
+template <int DT, int LANES, int TURNS> cudaError_t layernorm_narrow(const LayerNormArgs &a, cudaStream_t s, LaunchInfo *info) {
+    constexpr int kRows = kNarrowWarps * 32 / LANES * TURNS;
+    info->grid = static_cast<int>((a.rows + kRows - 1) / kRows);
+    info->block = 32 * kNarrowWarps;
+    info->vec_bytes = 8 * ElemOf<DT>::kBytes;
+    return launch_rows(layernorm_narrow_kernel<DT, LANES, TURNS>, dim3(info->grid), dim3(info->block), 0, 1, s, a);
+}
+
 template <int DT> cudaError_t layernorm_dispatch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
     const bool alike = a.cols >= 8 && same_runs<DT>(a.x, a.x_stride, a.residual, a.residual_stride) &&
                        same_runs<DT>(a.x, a.x_stride, a.y, a.y_stride) && same_runs<DT>(a.x, a.x_stride, a.h, a.h_stride);
     if (!alike) return layernorm_launch<DT, kApart>(a, sms, s, info);
-    return wide_rows<DT>(a.x, a.x_stride) && wide_weight<DT>(a.weight, a.weight_f32) && wide_weight<DT>(a.bias, a.weight_f32)
-               ? layernorm_launch<DT, kAligned>(a, sms, s, info)
-               : layernorm_launch<DT, kShifted>(a, sms, s, info);
+    if (!wide_rows<DT>(a.x, a.x_stride) || !wide_weight<DT>(a.weight, a.weight_f32) || !wide_weight<DT>(a.bias, a.weight_f32))
+        return layernorm_launch<DT, kShifted>(a, sms, s, info);
+    const bool two = DT != DT_F32 && a.rows >= 64 * static_cast<int64_t>(sms);
+    if constexpr (DT != DT_F32) {
+        if (two && a.cols <= 64) return layernorm_narrow<DT, 8, 2>(a, s, info);
+        if (two && a.cols <= 128) return layernorm_narrow<DT, 16, 2>(a, s, info);
+        if (two && a.cols <= 256) return layernorm_narrow<DT, 32, 2>(a, s, info);
+    }
+    if (a.cols <= 64) return layernorm_narrow<DT, 8, 1>(a, s, info);
+    if (a.cols <= 128) return layernorm_narrow<DT, 16, 1>(a, s, info);
+    return layernorm_launch<DT, kAligned>(a, sms, s, info);
 }
 
 template <int DT>

@@ -21,7 +21,8 @@ SHAPES = [(1, 1, 0, 0), (3, 7, 0, 0), (9, 3, 0, 5), (2, 8, 0, 0), (5, 255, 0, 0)
           (3, 4096, 1, 2), (1, 16384, 0, 0), (2, 16390, 0, 0), (5, 16380, 3, 6), (700, 64, 0, 0), (701, 300, 4, 0),
           (700, 61, 0, 3), (650, 2048, 0, 0), (620, 4096, 0, 0), (613, 5001, 0, 0), (1, 40003, 0, 0), (3, 33001, 0, 3),
           (640, 1801, 0, 0), (3, 12480, 0, 0), (700, 9001, 0, 0), (613, 9344, 0, 0), (611, 12288, 8, 0), (700, 16384, 0, 0),
-          (620, 16377, 0, 3)]
+          (620, 16377, 0, 3), (3, 128, 0, 0), (1003, 64, 64, 0), (9999, 56, 0, 0), (9999, 100, 4, 0), (10001, 128, 0, 8),
+          (9999, 250, 6, 0), (10000, 136, 0, 0)]
 
 
 def make(rows, cols, dtype, pad, offset, seed, spread=1.0, at=0.0):
@@ -134,7 +135,7 @@ def test_nan_and_infinity(cols):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
-@pytest.mark.parametrize("rows,cols", [(5, 512), (5, 1003), (700, 40), (5, 33000), (3, 33001), (700, 9001), (700, 16000)])
+@pytest.mark.parametrize("rows,cols", [(5, 512), (5, 1003), (700, 40), (5, 33000), (3, 33001), (700, 9001), (700, 16000), (10003, 128), (10003, 192)])
 @pytest.mark.parametrize("form", ["y=x,h=residual", "y=residual,h=x", "h=x", "y=x"])
 def test_in_place(dtype, rows, cols, form):
     x, r = make(rows, cols, dtype, 0, 0, 17), make(rows, cols, dtype, 0, 0, 18)
