@@ -794,6 +794,95 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
     }
 }
 
+// Aligned narrow rows, several to a warp as in layernorm_narrow_kernel: each lane holds
+// its 8 columns' sums over its rows, and the next row is on its way, in registers, while
+// one is worked on.  131072 rows of 64 bf16 16 us (floor 10; by the ring 50), 65536 of
+// 128 16 us (10; 29), of 256 24 us (20; 32), of 128 binary32 24 us (20; 31).  As many
+// blocks as an SM holds at once: two, with three at fewer registers 17 us for 65536 of
+// 128 bf16; three where a row takes a warp, with two 28 us for 256 columns.
+__host__ __device__ constexpr int narrow_resident(int dt, int lanes) { return dt != DT_F32 && lanes == 32 ? 3 : 2; }
+template <int DT, int LANES>
+__global__ void __launch_bounds__(32 * kNarrowWarps, narrow_resident(DT, LANES)) layernorm_grad_narrow_kernel(const __grid_constant__ LayerNormGradArgs a) {
+    enter_grid();
+    constexpr int kRows = 32 / LANES;  // of a warp at a time
+    __shared__ alignas(8) float sums[kNarrowWarps][2][8 * LANES];
+    const int lane = threadIdx.x & (LANES - 1), group = (threadIdx.x & 31) / LANES, warp = threadIdx.x >> 5;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kNarrowWarps * kRows;
+    int64_t base = (static_cast<int64_t>(blockIdx.x) * kNarrowWarps + warp) * kRows;  // of the warp's rows the first
+    const float per_col = 1.0f / static_cast<float>(a.cols);
+    float2 w[4], dw[4], db[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[j] = db[j] = both(0.0f);
+    Raw8<DT> rdy, rh, rdh;
+    float mean = 0.0f, rstd = 0.0f;
+    auto load = [&] {
+        const int64_t row = min(base + group, a.rows - 1);  // behind the last one it again
+        rdy = load_tile<DT, true>(row_of<DT>(a.dy, row, a.dy_stride), 0, a.cols, lane);
+        rh = load_tile<DT, true>(row_of<DT>(a.h, row, a.h_stride), 0, a.cols, lane);
+        if (a.dh) rdh = load_tile<DT, true>(row_of<DT>(a.dh, row, a.dh_stride), 0, a.cols, lane);
+        mean = a.mean[row], rstd = a.rstd[row];
+    };
+    if (base < a.rows) load();
+    load_columns<DT, kAligned>(a.weight, a.weight_f32, 1.0f, 0, 0, a.cols, lane, w);
+    while (base < a.rows) {
+        const int64_t row = base + group;
+        const bool given = row < a.rows;
+        float2 g[4], n[4], d[4];
+        unpack8<DT>(rdy, g);
+        unpack8<DT>(rh, n);
+        if (a.dh) unpack8<DT>(rdh, d);
+        const float2 m = both(-mean), r = both(rstd);
+        base += step;
+        if (base < a.rows) load();
+        float2 c = both(0.0f), c2 = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!given) g[j] = both(0.0f);
+            if (!a.dh) d[j] = both(0.0f);
+            n[j] = add2(n[j], m);
+            if (given) dw[j] = fma2(g[j], mul2(n[j], r), dw[j]);
+            db[j] = add2(g[j], db[j]);
+            g[j] = mul2(g[j], w[j]);
+            c = add2(c, g[j]);
+            c2 = fma2(g[j], n[j], c2);
+        }
+        c = make_float2(c.x + c.y, c2.x + c2.y);
+#pragma unroll
+        for (int i = LANES / 2; i > 0; i >>= 1)
+            c = add2(c, make_float2(__shfl_xor_sync(kAllLanes, c.x, i), __shfl_xor_sync(kAllLanes, c.y, i)));
+        if (!given) continue;
+        const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * r.x * per_col * r.x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = fma2(r, add2(g[j], fma2(m2, n[j], m1)), d[j]);
+        store_tile<DT, true>(row_of<DT>(a.dx, row, a.dx_stride), 0, a.cols, lane, pack8<DT>(d));
+    }
+    if (a.partial == nullptr) return;
+    // the warp's rows, then the block's warps in order
+#pragma unroll
+    for (int i = LANES; i < 32; i *= 2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            dw[j] = add2(dw[j], make_float2(__shfl_xor_sync(kAllLanes, dw[j].x, i), __shfl_xor_sync(kAllLanes, dw[j].y, i)));
+            db[j] = add2(db[j], make_float2(__shfl_xor_sync(kAllLanes, db[j].x, i), __shfl_xor_sync(kAllLanes, db[j].y, i)));
+        }
+    if (group == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<float2 *>(&sums[warp][0][lane * 8 + 2 * j]) = dw[j];
+            *reinterpret_cast<float2 *>(&sums[warp][1][lane * 8 + 2 * j]) = db[j];
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * 8 * LANES; i += 32 * kNarrowWarps) {
+        const int which = i / (8 * LANES), col = i % (8 * LANES);
+        if (col >= a.cols) continue;
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kNarrowWarps; ++v) sum += sums[v][which][col];
+        a.partial[(which * static_cast<int64_t>(gridDim.x) + blockIdx.x) * a.cols + col] = sum;
+    }
+}
+
 // Rows too wide to hold are read twice, a block of 32 warps a row, after
 // layernorm_columns_kernel has taken the columns' sums (dx may be dy).
 template <int DT, int ROWS> __global__ void __launch_bounds__(1024) layernorm_grad_wide_kernel(LayerNormGradArgs a) {
@@ -996,7 +1085,19 @@ cudaError_t layernorm_grad_dispatch(const LayerNormGradArgs &a, int64_t most_wri
     int64_t writers = 0;
     cudaError_t e = cudaSuccess;
     info->vec_bytes = runs ? 16 : ElemOf<DT>::kBytes;
-    if (a.rows > 0 && kt != 0) {
+    if (a.rows > 0 && aligned && a.cols <= 256) {
+        const int rows = kNarrowWarps * (a.cols <= 64 ? 4 : a.cols <= 128 ? 2 : 1);  // of a block at a time
+        const int resident = narrow_resident(DT, a.cols <= 128 ? 16 : 32);
+        writers = std::min<int64_t>({(a.rows + rows - 1) / rows, static_cast<int64_t>(sms) * resident, most_writers});
+        info->grid = static_cast<int>(writers);
+        info->block = 32 * kNarrowWarps;
+        info->vec_bytes = 8 * ElemOf<DT>::kBytes;
+        e = launch_rows(a.cols <= 64    ? layernorm_grad_narrow_kernel<DT, 8>
+                        : a.cols <= 128 ? layernorm_grad_narrow_kernel<DT, 16>
+                                        : layernorm_grad_narrow_kernel<DT, 32>,
+                        dim3(info->grid), dim3(info->block), 0, 1, s, a);
+        ++*launches;
+    } else if (a.rows > 0 && kt != 0) {
         const int blocks = pair ? 2 : 1, warps = (tiles + kt * blocks - 1) / (kt * blocks);
         // a row for each of 4 warps, where one holds it: their sums leave the block as one
         const int per_block = runs && warps == 1 && many ? 4 : 1;

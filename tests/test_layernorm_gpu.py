@@ -186,7 +186,8 @@ def check_backward(got, dy, h, w, mean, rstd, dh, dtype):
 @pytest.mark.parametrize("rows,cols,pad,offset", SHAPES + [(3000, 96, 0, 0), (1300, 1000, 0, 0), (3001, 97, 0, 5),
                                                            (1301, 1003, 2, 1), (1400, 2049, 0, 0), (400, 8187, 0, 0),
                                                            (170, 12001, 0, 3), (400, 10240, 0, 0), (200, 16384, 8, 8),
-                                                           (700, 400, 0, 0), (701, 509, 0, 0), (5000, 2041, 0, 0)])
+                                                           (700, 400, 0, 0), (701, 509, 0, 0), (5000, 2041, 0, 0),
+                                                           (10927, 248, 8, 0), (20003, 32, 0, 8), (9, 192, 0, 0)])
 def test_backward(dtype, rows, cols, pad, offset):
     dy, h, dh = (make(rows, cols, dtype, pad, offset, k, s, m) for k, s, m in ((21, 1.0, 0.0), (22, 2.0, 0.7), (23, 0.5, 0.0)))
     w = randn((cols,), 24, TORCH[dtype] if rows % 2 else torch.float32)
@@ -211,7 +212,7 @@ def test_backward_of_matrices_whose_rows_lie_apart(dtype, rows, cols, places):
     assert all(m.intact() for m in (dy, h, dh, dx, w))
 
 
-@pytest.mark.parametrize("cols", [64, 203, 1003, 9000, 9001, 20001])
+@pytest.mark.parametrize("cols", [56, 64, 203, 300, 1003, 9000, 9001, 20001])
 def test_backward_of_constant_rows_far_out(cols):
     """m r is past binary32, and no column of the row has it: dx = r (g - mean(g)), dweight = 0."""
     m, r = 2e36, 316.0
@@ -223,7 +224,7 @@ def test_backward_of_constant_rows_far_out(cols):
     assert not got[1].any()
 
 
-@pytest.mark.parametrize("rows,cols", [(9, 64), (9, 1003), (1300, 1003), (9, 8192), (200, 9001), (90, 16000), (9, 33001)])
+@pytest.mark.parametrize("rows,cols", [(9, 64), (10003, 120), (5003, 256), (9, 1003), (1300, 1003), (9, 8192), (200, 9001), (90, 16000), (9, 33001)])
 @pytest.mark.parametrize("place", ["dy", "dh"])
 def test_backward_in_place(rows, cols, place):
     dy, h, dh = (make(rows, cols, "bf16", 0, 0, k) for k in (29, 30, 31))
