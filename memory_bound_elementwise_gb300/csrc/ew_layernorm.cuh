@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
 // binary32 22 and 24).  Many 16-bit rows of up to 256 columns go this way, too, a
 // warp to two rows: 65536 of 192 23 us (33), of 256 24 us (26).
 constexpr int kNarrowWarps = 8;
+constexpr int kNarrowWalkers = 3;  // blocks to an SM
 template <int DT, int LANES, int TURNS>
 __global__ void __launch_bounds__(32 * kNarrowWarps) layernorm_narrow_kernel(const __grid_constant__ LayerNormArgs a) {
     enter_grid();
@@ -402,6 +403,80 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) layernorm_narrow_kernel(con
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(f[j], both(r)), w[j], b[j]);
         store_tile<DT, true>(row_of<DT>(a.y, row, a.y_stride), 0, a.cols, lane, pack8<DT>(f));
+    }
+}
+
+// Shifted narrow rows, which share a warp in the same way.  A lane's rows are a multiple of
+// 8 apart, so that its weights, cut once, stay in registers; the next row is on its way
+// while one is worked on.  65536 rows of 101 bf16 take 21 us (floor 8; a warp a row 37),
+// 131072 of 51 21 us (8; 70), 65536 of 201, a warp each, 35 us (16; 37), of 51 binary32
+// 14 us (8; 36).  Four blocks an SM have to spill: 22 us for 101 bf16.
+template <int DT, int LANES>
+__global__ void __launch_bounds__(32 * kNarrowWarps, kNarrowWalkers) layernorm_narrow_walk_kernel(const __grid_constant__ LayerNormArgs a) {
+    enter_grid();
+    constexpr int kRows = 32 / LANES;  // of a warp at a time
+    const int lane = threadIdx.x & (LANES - 1), group = (threadIdx.x & 31) / LANES;
+    const unsigned peers = (kAllLanes >> (32 - LANES)) << (group * LANES);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kNarrowWarps * kRows;  // a multiple of 8
+    int64_t base = (static_cast<int64_t>(blockIdx.x) * kNarrowWarps + (threadIdx.x >> 5)) * kRows;  // of the warp's rows the first
+    const int past = past_of<DT>(row_of<DT>(a.x, base + group, a.x_stride));
+    auto sum = [](float v) {
+#pragma unroll
+        for (int d = LANES / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kAllLanes, v, d);
+        return v;
+    };
+    Raw8<DT> rx, rr;
+    auto load = [&] {
+        const int64_t row = base + group;
+        const bool inner = row > 0 && row + 1 < a.rows;  // strides are at least 8
+        const int cols = row < a.rows ? a.cols : 0;      // nothing behind the last row
+        rx = load_run<DT>(row_of<DT>(a.x, row, a.x_stride), 0, past, cols, lane, inner);
+        if (a.residual) rr = load_run<DT>(row_of<DT>(a.residual, row, a.residual_stride), 0, past, cols, lane, inner);
+    };
+    if (base < a.rows) load();
+    float2 w[4], b[4];
+    load_columns<DT, kShifted>(a.weight, a.weight_f32, 1.0f, 0, past, a.cols, lane, w);
+    load_columns<DT, kShifted>(a.bias, a.weight_f32, 0.0f, 0, past, a.cols, lane, b);
+    while (base < a.rows) {
+        const int64_t row = base + group;
+        float2 f[4], d[4];
+        unpack8<DT>(rx, f);
+        if (a.residual) {
+            float2 g[4];
+            unpack8<DT>(rr, g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
+        }
+        base += step;
+        if (base < a.rows) load();
+        if (a.h && row < a.rows) store_run<DT>(row_of<DT>(a.h, row, a.h_stride), 0, past, a.cols, lane, pack8<DT>(f));
+        // element 7 of lane 0, element 0 of the others, where the row has it
+        const bool held = lane == 0 || lane * 8 - past < a.cols;
+        const float mine = lane == 0 ? f[3].y : f[0].x;
+        const unsigned all = __ballot_sync(kAllLanes, held) & peers, negative = __ballot_sync(kAllLanes, held && mine < 0.0f) & peers;
+        const float one = __shfl_sync(kAllLanes, mine, group * LANES);
+        const float at = negative == 0 || negative == all ? one : 0.0f;
+        float2 s2 = both(0.0f), q2 = both(0.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = add2(f[j], both(-at));
+        clip_columns<true>(0, past, a.cols, lane, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
+        const float mean = sum(s2.x + s2.y) * a.per_col;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = d[j] = add2(add2(f[j], both(-at)), both(-mean));
+        clip_columns<true>(0, past, a.cols, lane, d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
+        const float r = rsqrtf(fmaf(sum(q2.x + q2.y), a.per_col, a.eps));
+        if (row >= a.rows) continue;
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = at + mean;
+            if (a.rstd) a.rstd[row] = r;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(f[j], both(r)), w[j], b[j]);
+        store_run<DT>(row_of<DT>(a.y, row, a.y_stride), 0, past, a.cols, lane, pack8<DT>(f));
     }
 }
 
@@ -1047,12 +1122,24 @@ template <int DT, int LANES, int TURNS> cudaError_t layernorm_narrow(const Layer
     return launch_rows(layernorm_narrow_kernel<DT, LANES, TURNS>, dim3(info->grid), dim3(info->block), 0, 1, s, a);
 }
 
+template <int DT, int LANES> cudaError_t layernorm_narrow_walk(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
+    constexpr int kRows = kNarrowWarps * 32 / LANES;
+    info->grid = static_cast<int>(std::min<int64_t>((a.rows + kRows - 1) / kRows, static_cast<int64_t>(sms) * kNarrowWalkers));
+    info->block = 32 * kNarrowWarps;
+    info->vec_bytes = 8 * ElemOf<DT>::kBytes;
+    return launch_rows(layernorm_narrow_walk_kernel<DT, LANES>, dim3(info->grid), dim3(info->block), 0, 1, s, a);
+}
+
 template <int DT> cudaError_t layernorm_dispatch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
     const bool alike = a.cols >= 8 && same_runs<DT>(a.x, a.x_stride, a.residual, a.residual_stride) &&
                        same_runs<DT>(a.x, a.x_stride, a.y, a.y_stride) && same_runs<DT>(a.x, a.x_stride, a.h, a.h_stride);
     if (!alike) return layernorm_launch<DT, kApart>(a, sms, s, info);
-    if (!wide_rows<DT>(a.x, a.x_stride) || !wide_weight<DT>(a.weight, a.weight_f32) || !wide_weight<DT>(a.bias, a.weight_f32))
+    if (!wide_rows<DT>(a.x, a.x_stride) || !wide_weight<DT>(a.weight, a.weight_f32) || !wide_weight<DT>(a.bias, a.weight_f32)) {
+        if (a.cols + 7 <= 64) return layernorm_narrow_walk<DT, 8>(a, sms, s, info);
+        if (a.cols + 7 <= 128) return layernorm_narrow_walk<DT, 16>(a, sms, s, info);
+        if (a.cols + 7 <= 256) return layernorm_narrow_walk<DT, 32>(a, sms, s, info);
         return layernorm_launch<DT, kShifted>(a, sms, s, info);
+    }
     const bool two = DT != DT_F32 && a.rows >= 64 * static_cast<int64_t>(sms);
     if constexpr (DT != DT_F32) {
         if (two && a.cols <= 64) return layernorm_narrow<DT, 8, 2>(a, s, info);

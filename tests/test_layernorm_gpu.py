@@ -22,7 +22,8 @@ SHAPES = [(1, 1, 0, 0), (3, 7, 0, 0), (9, 3, 0, 5), (2, 8, 0, 0), (5, 255, 0, 0)
           (700, 61, 0, 3), (650, 2048, 0, 0), (620, 4096, 0, 0), (613, 5001, 0, 0), (1, 40003, 0, 0), (3, 33001, 0, 3),
           (640, 1801, 0, 0), (3, 12480, 0, 0), (700, 9001, 0, 0), (613, 9344, 0, 0), (611, 12288, 8, 0), (700, 16384, 0, 0),
           (620, 16377, 0, 3), (3, 128, 0, 0), (1003, 64, 64, 0), (9999, 56, 0, 0), (9999, 100, 4, 0), (10001, 128, 0, 8),
-          (9999, 250, 6, 0), (10000, 136, 0, 0)]
+          (9999, 250, 6, 0), (10000, 136, 0, 0), (5, 8, 0, 3), (9999, 57, 0, 0), (20001, 121, 0, 1), (10001, 101, 2, 0),
+          (9999, 249, 0, 3)]
 
 
 def make(rows, cols, dtype, pad, offset, seed, spread=1.0, at=0.0):
@@ -98,7 +99,7 @@ def test_no_residual(dtype, cols, given):
     check_forward(got, x.t, None, w, b, 0.0, dtype)
 
 
-@pytest.mark.parametrize("cols", [64, 1003, 4096, 12000, 12001, 20001])
+@pytest.mark.parametrize("cols", [61, 64, 201, 1003, 4096, 12000, 12001, 20001])
 @pytest.mark.parametrize("at", [1e3, -1e6])
 def test_mean_far_from_zero(cols, at):
     """Rows of spread 1 around a mean of up to 1e6: the elements hold the spread to 2^-5, and y loses no more."""
@@ -110,7 +111,7 @@ def test_mean_far_from_zero(cols, at):
     assert float((got[0].double() - want.y).abs().max()) < 200 * EPS32 * float(want.y.abs().max() + 4)
 
 
-@pytest.mark.parametrize("cols", [64, 1003, 12000, 12001, 20001])
+@pytest.mark.parametrize("cols", [61, 64, 201, 1003, 12000, 12001, 20001])
 def test_constant_and_outlying_rows(cols):
     x = torch.full((4, cols), 1234.567, device="cuda")
     x[1] = 0.0
@@ -125,7 +126,7 @@ def test_constant_and_outlying_rows(cols):
     check_forward(got, x, None, None, b, 1e-5, "f32")
 
 
-@pytest.mark.parametrize("cols", [320, 321, 12000, 12001, 20001])
+@pytest.mark.parametrize("cols", [57, 64, 121, 249, 320, 321, 12000, 12001, 20001])
 def test_nan_and_infinity(cols):
     x = randn((4, cols), 16)
     x[0, 5], x[1, 0], x[2, cols - 1] = math.nan, math.inf, -math.inf
@@ -135,7 +136,7 @@ def test_nan_and_infinity(cols):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16"])
-@pytest.mark.parametrize("rows,cols", [(5, 512), (5, 1003), (700, 40), (5, 33000), (3, 33001), (700, 9001), (700, 16000), (10003, 128), (10003, 192)])
+@pytest.mark.parametrize("rows,cols", [(5, 512), (5, 1003), (700, 40), (5, 33000), (3, 33001), (700, 9001), (700, 16000), (10003, 128), (10003, 192), (20003, 101), (30003, 50)])
 @pytest.mark.parametrize("form", ["y=x,h=residual", "y=residual,h=x", "h=x", "y=x"])
 def test_in_place(dtype, rows, cols, form):
     x, r = make(rows, cols, dtype, 0, 0, 17), make(rows, cols, dtype, 0, 0, 18)
