@@ -869,21 +869,28 @@ __global__ void __launch_bounds__(512, 1) layernorm_grad_ring_kernel(const __gri
     }
 }
 
-// Aligned narrow rows, several to a warp as in layernorm_narrow_kernel: each lane holds
-// its 8 columns' sums over its rows, and the next row is on its way, in registers, while
-// one is worked on.  131072 rows of 64 bf16 16 us (floor 10; by the ring 50), 65536 of
-// 128 16 us (10; 29), of 256 24 us (20; 32), of 128 binary32 24 us (20; 31).  As many
-// blocks as an SM holds at once: two, with three at fewer registers 17 us for 65536 of
-// 128 bf16; three where a row takes a warp, with two 28 us for 256 columns.
-__host__ __device__ constexpr int narrow_resident(int dt, int lanes) { return dt != DT_F32 && lanes == 32 ? 3 : 2; }
-template <int DT, int LANES>
-__global__ void __launch_bounds__(32 * kNarrowWarps, narrow_resident(DT, LANES)) layernorm_grad_narrow_kernel(const __grid_constant__ LayerNormGradArgs a) {
+// Narrow rows, several to a warp as in layernorm_narrow_kernel: each lane holds its 8
+// columns' sums over its rows, which are a multiple of 8 apart, and the next row is on its
+// way, in registers, while one is worked on.  131072 rows of 64 bf16 16 us (floor 10; by
+// the ring 50), 65536 of 128 16 us (10; 29), of 256 24 us (20; 32), of 128 binary32 24 us
+// (20; 31); shifted ones, where there are many, 131072 of 51 bf16 21 us (8; 70), 65536 of
+// 101 22 us (8; 39), of 201 36 us (16; 41).  As many blocks as an SM holds at once: two,
+// with three at fewer registers 17 us for 65536 of 128 bf16; three where an aligned row
+// takes a warp, with two 28 us for 256 columns.
+__host__ __device__ constexpr int narrow_resident(int dt, int rows, int lanes) {
+    return dt != DT_F32 && rows == kAligned && lanes == 32 ? 3 : 2;
+}
+template <int DT, int ROWS, int LANES>
+__global__ void __launch_bounds__(32 * kNarrowWarps, narrow_resident(DT, ROWS, LANES)) layernorm_grad_narrow_kernel(const __grid_constant__ LayerNormGradArgs a) {
     enter_grid();
     constexpr int kRows = 32 / LANES;  // of a warp at a time
-    __shared__ alignas(8) float sums[kNarrowWarps][2][8 * LANES];
+    // sums of a warp, or of each of its groups, whose columns lie apart by `past`
+    constexpr int kSums = kNarrowWarps * (ROWS == kShifted ? kRows : 1);
+    __shared__ alignas(8) float sums[kSums][2][8 * LANES];
     const int lane = threadIdx.x & (LANES - 1), group = (threadIdx.x & 31) / LANES, warp = threadIdx.x >> 5;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kNarrowWarps * kRows;
     int64_t base = (static_cast<int64_t>(blockIdx.x) * kNarrowWarps + warp) * kRows;  // of the warp's rows the first
+    const int past = ROWS == kShifted ? past_of<DT>(row_of<DT>(a.dy, base + group, a.dy_stride)) : 0;
     const float per_col = 1.0f / static_cast<float>(a.cols);
     float2 w[4], dw[4], db[4];
 #pragma unroll
@@ -891,14 +898,18 @@ __global__ void __launch_bounds__(32 * kNarrowWarps, narrow_resident(DT, LANES))
     Raw8<DT> rdy, rh, rdh;
     float mean = 0.0f, rstd = 0.0f;
     auto load = [&] {
-        const int64_t row = min(base + group, a.rows - 1);  // behind the last one it again
-        rdy = load_tile<DT, true>(row_of<DT>(a.dy, row, a.dy_stride), 0, a.cols, lane);
-        rh = load_tile<DT, true>(row_of<DT>(a.h, row, a.h_stride), 0, a.cols, lane);
-        if (a.dh) rdh = load_tile<DT, true>(row_of<DT>(a.dh, row, a.dh_stride), 0, a.cols, lane);
-        mean = a.mean[row], rstd = a.rstd[row];
+        // behind the last row: of aligned ones it again, of shifted ones nothing
+        const int64_t row = ROWS == kAligned ? min(base + group, a.rows - 1) : base + group;
+        const bool inner = row > 0 && row + 1 < a.rows;
+        const int cols = ROWS == kAligned || row < a.rows ? a.cols : 0;
+        rdy = load_row<DT, ROWS>(row_of<DT>(a.dy, row, a.dy_stride), 0, past, cols, lane, inner);
+        rh = load_row<DT, ROWS>(row_of<DT>(a.h, row, a.h_stride), 0, past, cols, lane, inner);
+        if (a.dh) rdh = load_row<DT, ROWS>(row_of<DT>(a.dh, row, a.dh_stride), 0, past, cols, lane, inner);
+        const int64_t at = ROWS == kAligned ? row : min(row, a.rows - 1);
+        mean = a.mean[at], rstd = a.rstd[at];
     };
     if (base < a.rows) load();
-    load_columns<DT, kAligned>(a.weight, a.weight_f32, 1.0f, 0, 0, a.cols, lane, w);
+    load_columns<DT, ROWS>(a.weight, a.weight_f32, 1.0f, 0, past, a.cols, lane, w);
     while (base < a.rows) {
         const int64_t row = base + group;
         const bool given = row < a.rows;
@@ -911,10 +922,15 @@ __global__ void __launch_bounds__(32 * kNarrowWarps, narrow_resident(DT, LANES))
         if (base < a.rows) load();
         float2 c = both(0.0f), c2 = both(0.0f);
 #pragma unroll
+        for (int j = 0; j < 4; ++j) n[j] = add2(n[j], m);
+        if constexpr (ROWS == kShifted) {  // what runs have of the rows beside
+            clip_columns<true>(0, past, a.cols, lane, g);
+            clip_columns<true>(0, past, a.cols, lane, n);
+        }
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (!given) g[j] = both(0.0f);
             if (!a.dh) d[j] = both(0.0f);
-            n[j] = add2(n[j], m);
             if (given) dw[j] = fma2(g[j], mul2(n[j], r), dw[j]);
             db[j] = add2(g[j], db[j]);
             g[j] = mul2(g[j], w[j]);
@@ -925,26 +941,35 @@ __global__ void __launch_bounds__(32 * kNarrowWarps, narrow_resident(DT, LANES))
 #pragma unroll
         for (int i = LANES / 2; i > 0; i >>= 1)
             c = add2(c, make_float2(__shfl_xor_sync(kAllLanes, c.x, i), __shfl_xor_sync(kAllLanes, c.y, i)));
-        if (!given) continue;
+        if (row >= a.rows) continue;
         const float2 m1 = both(-c.x * per_col), m2 = both(-c.y * r.x * per_col * r.x);
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = fma2(r, add2(g[j], fma2(m2, n[j], m1)), d[j]);
-        store_tile<DT, true>(row_of<DT>(a.dx, row, a.dx_stride), 0, a.cols, lane, pack8<DT>(d));
+        store_row<DT, ROWS>(row_of<DT>(a.dx, row, a.dx_stride), 0, past, a.cols, lane, pack8<DT>(d));
     }
     if (a.partial == nullptr) return;
-    // the warp's rows, then the block's warps in order
+    if constexpr (ROWS == kAligned) {
 #pragma unroll
-    for (int i = LANES; i < 32; i *= 2)
+        for (int i = LANES; i < 32; i *= 2)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            dw[j] = add2(dw[j], make_float2(__shfl_xor_sync(kAllLanes, dw[j].x, i), __shfl_xor_sync(kAllLanes, dw[j].y, i)));
-            db[j] = add2(db[j], make_float2(__shfl_xor_sync(kAllLanes, db[j].x, i), __shfl_xor_sync(kAllLanes, db[j].y, i)));
+            for (int j = 0; j < 4; ++j) {
+                dw[j] = add2(dw[j], make_float2(__shfl_xor_sync(kAllLanes, dw[j].x, i), __shfl_xor_sync(kAllLanes, dw[j].y, i)));
+                db[j] = add2(db[j], make_float2(__shfl_xor_sync(kAllLanes, db[j].x, i), __shfl_xor_sync(kAllLanes, db[j].y, i)));
+            }
+        if (group == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                *reinterpret_cast<float2 *>(&sums[warp][0][lane * 8 + 2 * j]) = dw[j];
+                *reinterpret_cast<float2 *>(&sums[warp][1][lane * 8 + 2 * j]) = db[j];
+            }
         }
-    if (group == 0) {
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            *reinterpret_cast<float2 *>(&sums[warp][0][lane * 8 + 2 * j]) = dw[j];
-            *reinterpret_cast<float2 *>(&sums[warp][1][lane * 8 + 2 * j]) = db[j];
+        for (int j = 0; j < 8; ++j) {
+            const int col = lane * 8 + j - past;
+            if (col < 0 || col >= a.cols) continue;
+            sums[warp * kRows + group][0][col] = j & 1 ? dw[j / 2].y : dw[j / 2].x;
+            sums[warp * kRows + group][1][col] = j & 1 ? db[j / 2].y : db[j / 2].x;
         }
     }
     __syncthreads();
@@ -953,7 +978,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps, narrow_resident(DT, LANES))
         if (col >= a.cols) continue;
         float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < kNarrowWarps; ++v) sum += sums[v][which][col];
+        for (int v = 0; v < kSums; ++v) sum += sums[v][which][col];
         a.partial[(which * static_cast<int64_t>(gridDim.x) + blockIdx.x) * a.cols + col] = sum;
     }
 }
@@ -1172,17 +1197,22 @@ cudaError_t layernorm_grad_dispatch(const LayerNormGradArgs &a, int64_t most_wri
     int64_t writers = 0;
     cudaError_t e = cudaSuccess;
     info->vec_bytes = runs ? 16 : ElemOf<DT>::kBytes;
-    if (a.rows > 0 && aligned && a.cols <= 256) {
-        const int rows = kNarrowWarps * (a.cols <= 64 ? 4 : a.cols <= 128 ? 2 : 1);  // of a block at a time
-        const int resident = narrow_resident(DT, a.cols <= 128 ? 16 : 32);
+    if (a.rows > 0 && tiles == 1 && (aligned || (runs && many))) {
+        const int width = a.cols + (aligned ? 0 : 7), lanes = width <= 64 ? 8 : width <= 128 ? 16 : 32;
+        const int rows = kNarrowWarps * 32 / lanes;  // of a block at a time
+        const int resident = narrow_resident(DT, aligned ? kAligned : kShifted, lanes);
         writers = std::min<int64_t>({(a.rows + rows - 1) / rows, static_cast<int64_t>(sms) * resident, most_writers});
         info->grid = static_cast<int>(writers);
         info->block = 32 * kNarrowWarps;
         info->vec_bytes = 8 * ElemOf<DT>::kBytes;
-        e = launch_rows(a.cols <= 64    ? layernorm_grad_narrow_kernel<DT, 8>
-                        : a.cols <= 128 ? layernorm_grad_narrow_kernel<DT, 16>
-                                        : layernorm_grad_narrow_kernel<DT, 32>,
-                        dim3(info->grid), dim3(info->block), 0, 1, s, a);
+        auto kernel = lanes == 8    ? layernorm_grad_narrow_kernel<DT, kAligned, 8>
+                      : lanes == 16 ? layernorm_grad_narrow_kernel<DT, kAligned, 16>
+                                    : layernorm_grad_narrow_kernel<DT, kAligned, 32>;
+        if (!aligned)
+            kernel = lanes == 8    ? layernorm_grad_narrow_kernel<DT, kShifted, 8>
+                     : lanes == 16 ? layernorm_grad_narrow_kernel<DT, kShifted, 16>
+                                   : layernorm_grad_narrow_kernel<DT, kShifted, 32>;
+        e = launch_rows(kernel, dim3(info->grid), dim3(info->block), 0, 1, s, a);
         ++*launches;
     } else if (a.rows > 0 && kt != 0) {
         const int blocks = pair ? 2 : 1, warps = (tiles + kt * blocks - 1) / (kt * blocks);

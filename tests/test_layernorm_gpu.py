@@ -225,7 +225,7 @@ def test_backward_of_constant_rows_far_out(cols):
     assert not got[1].any()
 
 
-@pytest.mark.parametrize("rows,cols", [(9, 64), (10003, 120), (5003, 256), (9, 1003), (1300, 1003), (9, 8192), (200, 9001), (90, 16000), (9, 33001)])
+@pytest.mark.parametrize("rows,cols", [(9, 64), (10003, 120), (10003, 101), (5003, 256), (9, 1003), (1300, 1003), (9, 8192), (200, 9001), (90, 16000), (9, 33001)])
 @pytest.mark.parametrize("place", ["dy", "dh"])
 def test_backward_in_place(rows, cols, place):
     dy, h, dh = (make(rows, cols, "bf16", 0, 0, k) for k in (29, 30, 31))
