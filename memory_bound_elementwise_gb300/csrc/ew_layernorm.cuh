@@ -107,7 +107,7 @@ __device__ __forceinline__ float landmark(float mine, bool given) {
 //     sum (v - m)^2 = sum over warps of (squares + n (mean - m)^2),
 // so that both statistics cost one barrier and no cancellation.  Otherwise the
 // passes read the row again.  Bounded by memory: 16384 rows of 8192 bf16 with a residual
-// 175 us at a floor of 161; by latency where there are few rows (9 of 5120 3.0 us) and
+// 168 us at a floor of 161; by latency where there are few rows (9 of 5120 3.0 us) and
 // by the issue rate where rows are narrow (65536 of 201 bf16 36 us at 16).
 //
 // Weights beside shifted rows have to be cut to their phase, which takes as long
@@ -1073,9 +1073,9 @@ template <int DT> bool same_runs(const void *p, int64_t stride, const void *q, i
 
 // Tiles a thread: as few as hold the row in 16 warps, which is the shortest way for
 // few rows.  Where there are many, two keep more loads on their way, and four pay for
-// the statistics of wide 16-bit rows: 16384 rows of 4096 bf16 take 88 us with four,
-// 16384 of 4001 96 us with four and 115 with one; 2048 binary32 93 us with one, 89
-// with two.  But walkers hold weights as well, fewer of them fit, and what matters is
+// the statistics of wide 16-bit rows: 16384 rows of 4096 bf16 take 81 us with four,
+// 16384 of 4001 96 us with four and 115 with one; of 2001 binary32 93 us with one,
+// 89 with two.  But walkers hold weights as well, fewer of them fit, and what matters is
 // how many columns an SM works on: 6392 rows of 2135 bf16 take 34 us with four (45 of
 // 64 tiles), 29 with one (27 of 32); of less than 8 tiles the barrier is short and one
 // is as good or better (7897 x 777 f16 17.0 us, 18.0 with four).

@@ -117,7 +117,9 @@ __device__ __forceinline__ Raw8<DT> load_tile(const void *row, int base, int col
     } else {
 #pragma unroll
         for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = 0u;
-        if (c0 >= cols) return r;  // a lane without a column
+        // A lane without a column.  Not of binary32, where four tiles a thread would then be
+        // waited for one by one (4096 rows of 12288: layer norm 192 us, 130 without).
+        if (DT != DT_F32 && c0 >= cols) return r;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = tile_col<VEC>(base, lane, j);
