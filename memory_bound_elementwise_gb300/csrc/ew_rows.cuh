@@ -118,8 +118,10 @@ __device__ __forceinline__ Raw8<DT> load_tile(const void *row, int base, int col
 #pragma unroll
         for (int k = 0; k < ElemOf<DT>::kWords; ++k) r.w[k] = 0u;
         // A lane without a column.  Not of binary32, where four tiles a thread would then be
-        // waited for one by one (4096 rows of 12288: layer norm 192 us, 130 without).
-        if (DT != DT_F32 && c0 >= cols) return r;
+        // waited for one by one (4096 rows of 12288: layer norm 192 us, 130 without), nor of
+        // single elements, for the same reason (the norm's backward of 33520 x 1001 bf16 79 us
+        // and 66).
+        if (VEC && DT != DT_F32 && c0 >= cols) return r;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = tile_col<VEC>(base, lane, j);
@@ -141,7 +143,7 @@ __device__ __forceinline__ void store_tile(void *row, int base, int cols, int la
 #pragma unroll
         for (int k = 0; k < ElemOf<DT>::kWords; ++k) v.w[k] = r.w[k];
         st<8 * ElemOf<DT>::kBytes>(p + c0, v);
-    } else if (c0 < cols) {
+    } else if (!VEC || c0 < cols) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = tile_col<VEC>(base, lane, j);
