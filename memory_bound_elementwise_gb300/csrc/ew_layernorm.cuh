@@ -1095,7 +1095,7 @@ template <int DT, int ROWS> cudaError_t layernorm_launch(const LayerNormArgs &a,
     const bool pair = ROWS != kApart && kt == 4 && (a.rows <= (ROWS == kShifted ? sms / 2 : sms) || (ROWS == kShifted && !kNarrow));
     if (pair) {
         kt = 2;
-    } else if (ROWS == kShifted && kNarrow && tiles >= 8) {
+    } else if (kt != 0 && ROWS == kShifted && kNarrow && tiles >= 8) {
         // tiles of the rows that an SM holds, of 32 by ones and of 64 by fours
         const int one = kt == 1 ? tiles * (32 / tiles) : 0, four = tiles * (16 / ((tiles + 3) / 4));
         if (many ? 4 * four >= 7 * one : kt == 2 && a.rows > sms) kt = 4;
