@@ -360,12 +360,12 @@ EW_API int64_t ew_rmsnorm_grad_workspace(int64_t rows, int64_t cols);
  * rstd_out (binary32, rows) may be NULL where they are not wanted; the backward call
  * needs all three (h is x where there is no residual, unless y has taken its place).
  * The norm is taken of the binary32 sum; only what is stored in h_out is rounded.
- * y of a row far from zero is formed from differences to one of its elements, so its
- * mean costs it nothing; mean_out is rounded.  y may be x or residual, and h_out may be x
- * or residual (the same base and stride), but y is not h_out.  eps >= 0.  A NaN or
- * an infinity makes y's whole row and rstd NaN.  Where the variance is past binary32
- * rstd is 0; where it and eps are 0 rstd is infinite and y NaN.  Elements whose sum is
- * past binary32 may make y NaN. */
+ * y is formed from differences to a number near the row's mean, so neither a mean far from
+ * zero nor elements that stand out of the row cost the others' y its digits; mean_out is
+ * rounded.  y may be x or residual, and h_out may be x or residual (the same base and
+ * stride), but y is not h_out.  eps >= 0.  A NaN or an infinity makes y's whole row and
+ * rstd NaN.  Where the variance is past binary32 rstd is 0; where it and eps are 0 rstd is
+ * infinite and y NaN.  Elements whose sum is past binary32 may make y NaN. */
 EW_API ew_status ew_layernorm(ew_dtype dtype, const void *x, int64_t x_stride, const void *residual,
                               int64_t residual_stride, ew_dtype wtype, const void *weight, const void *bias, float eps,
                               void *y, int64_t y_stride, void *h_out, int64_t h_stride, float *mean_out,

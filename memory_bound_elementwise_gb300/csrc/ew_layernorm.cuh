@@ -9,10 +9,16 @@
 // a multiple, `past` elements before the row, and the runs at its two ends are
 // moved element by element (RUNS).  Other matrices are moved an element at a time.
 //
-// The mean of a row far from zero is subtracted in two steps: first one of the
-// row's elements, an exact difference where they are within a factor of two of
-// each other, then the mean of what is left.  So y does not lose what the rounding
-// of m to binary32 would cost it.
+// The mean is subtracted in two steps, so that y does not lose what its rounding to
+// binary32 would cost.  First a number L near the mean: one of the row's elements where it
+// is within a factor of two of the mean, which makes the differences of elements near it
+// exact and those of a row of one value 0; otherwise the mean as a plain sum gives it.  Then
+// the mean d of the differences.  With those, v = h - L - d, the squares are summed, and the
+// v, whose mean e is what rounding took from d:
+//     m = L + (d + e),  sum (h - m)^2 = sum v^2 - n e^2,
+// where e^2 is next to nothing beside the squares.  Rows that share a warp, whose time is
+// that of instructions, take zero for L where their elements have both signs, and e only
+// where L is a mean (65536 x 201 bf16 35.2 us; always 36.1).
 #pragma once
 
 #include <algorithm>
@@ -73,13 +79,20 @@ __device__ __forceinline__ int columns_in(int tile, int past, int cols) {
     return max(end - first, 0);
 }
 
-// Two sums over a block of `warps` warps at once; `part` as in block_sum.
-__device__ __forceinline__ float2 warp_sum2(float2 v) {
+// Sums over the LANES lanes around this one.
+template <int LANES> __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
+    for (int d = LANES / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kAllLanes, v, d);
+    return v;
+}
+template <int LANES> __device__ __forceinline__ float2 lanes_sum(float2 v) {
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1)
         v = add2(v, make_float2(__shfl_xor_sync(kAllLanes, v.x, d), __shfl_xor_sync(kAllLanes, v.y, d)));
     return v;
 }
+// Two sums over a block of `warps` warps at once; `part` as in block_sum.
+__device__ __forceinline__ float2 warp_sum2(float2 v) { return lanes_sum<32>(v); }
 __device__ __forceinline__ float2 block_sum2(float2 v, int warps, float2 *part) {
     v = warp_sum2(v);
     if (warps == 1) return v;
@@ -91,13 +104,36 @@ __device__ __forceinline__ float2 block_sum2(float2 v, int warps, float2 *part) 
 
 // ---------------------------------------------------------------- forward
 
-// What the elements are compared with: lane 0's of the warp's samples (`mine`, where
-// `given`) where all have one sign, and so may lie far from zero, else zero.  Zero
-// leaves the mean of a row around it as precise as a plain sum does.
-__device__ __forceinline__ float landmark(float mine, bool given) {
-    const unsigned all = __ballot_sync(kAllLanes, given), negative = __ballot_sync(kAllLanes, given && mine < 0.0f);
-    const float first = __shfl_sync(kAllLanes, mine, 0);
+// What the elements are first compared with: of samples (`mine`, where `given`), one to
+// each of the LANES lanes that share a row, the first where all have one sign, and so may lie
+// far from zero, else zero.
+template <int LANES = 32> __device__ __forceinline__ float landmark(float mine, bool given) {
+    unsigned all = __ballot_sync(kAllLanes, given), negative = __ballot_sync(kAllLanes, given && mine < 0.0f);
+    const int from = threadIdx.x & 31 & ~(LANES - 1);
+    if constexpr (LANES < 32) {
+        const unsigned peers = (kAllLanes >> (32 - LANES)) << from;
+        all &= peers, negative &= peers;
+    }
+    const float first = __shfl_sync(kAllLanes, mine, from);
     return negative == 0 || negative == all ? first : 0.0f;
+}
+// The landmark and the mean `beyond` it, where they lie apart, as where the landmark stands
+// out of its row: differences to it hold fewer of the elements' bits then, and the mean
+// takes its place.  Apart: more than the mean's size over `times`; with 1, zero never is.
+__device__ __forceinline__ bool to_mean(float &at, float &beyond, float times) {
+    const float mean = at + beyond;
+    const bool apart = times * fabsf(beyond) > fabsf(mean);
+    at = apart ? mean : at;
+    beyond = apart ? 0.0f : beyond;
+    return apart;
+}
+// What `beyond` lacks, from the sum of what n elements have beyond it; the squares become
+// those around the mean.  Squares past binary32 stay.
+__device__ __forceinline__ void finish_mean(float &beyond, float &squares, float sum, float n, float per) {
+    const bool finite = squares < __int_as_float(0x7f800000);
+    const float e = finite ? sum * per : 0.0f;
+    squares = finite ? fmaxf(fmaf(-n * e, e, squares), 0.0f) : squares;
+    beyond += e;
 }
 
 // One row to a block of `warps` warps, tile t of the row to warp t mod warps;
@@ -107,7 +143,7 @@ __device__ __forceinline__ float landmark(float mine, bool given) {
 //     sum (v - m)^2 = sum over warps of (squares + n (mean - m)^2),
 // so that both statistics cost one barrier and no cancellation.  Otherwise the
 // passes read the row again.  Bounded by memory: 16384 rows of 8192 bf16 with a residual
-// 168 us at a floor of 161; by latency where there are few rows (9 of 5120 3.0 us) and
+// 171 us at a floor of 161; by latency where there are few rows (9 of 5120 3.0 us) and
 // by the issue rate where rows are narrow (65536 of 201 bf16 36 us at 16).
 //
 // Weights beside shifted rows have to be cut to their phase, which takes as long
@@ -156,7 +192,7 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
         float2 y[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            y[j] = fma2(mul2(add2(add2(f[j], both(-at)), both(-mean)), both(r)), w[j], b[j]);
+            y[j] = fma2(fma2(add2(f[j], both(-at)), both(r), both(-mean * r)), w[j], b[j]);
         store_row<DT, ROWS>(out, tile, past, a.cols, lane, pack8<DT>(y));
     };
 
@@ -214,7 +250,7 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
             // lane 0's lies in the row, if any of the warp's first tile does (a shifted row has 8)
             const int j = ROWS == kShifted && row_warp == 0 ? 7 : 0;
             float at = landmark(j == 0 ? f[0][0].x : f[0][3].y, col_of<ROWS != kApart>(row_warp, past, lane, j) < a.cols);
-            float2 s2 = both(0.0f), q2 = both(0.0f);
+            float2 s2 = both(0.0f), e2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
                 float2 d[4];
@@ -225,6 +261,7 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
                 for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
             }
             float mean = warp_sum(s2.x + s2.y) * per_own;
+            to_mean(at, mean, 2.0f);
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
                 float2 d[4];
@@ -232,23 +269,33 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
                 for (int j = 0; j < 4; ++j) d[j] = add2(add2(f[k][j], both(-at)), both(-mean));
                 clip_columns<ROWS != kApart>(row_warp + k * row_warps, past, a.cols, lane, d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
+                for (int j = 0; j < 4; ++j) {
+                    e2 = add2(e2, d[j]);
+                    q2 = fma2(d[j], d[j], q2);
+                }
             }
             float squares = warp_sum(q2.x + q2.y);
+            finish_mean(mean, squares, warp_sum(e2.x + e2.y), static_cast<float>(n), per_own);
             if (warps > 1) {
                 float4 *part = parts[turn];
                 turn ^= 1;  // read by all before it is written again: a barrier lies between
                 if (lane == 0) part[warp] = make_float4(at, mean, squares, static_cast<float>(n));
                 if (PAIR) cluster_sync();
                 else __syncthreads();
-                const int other = lane < row_warps ? lane : 0;
+                // a part to each lane, twice where half the warp has enough
+                constexpr int kLanes = PAIR ? 32 : 16;
+                static_assert(WARPS <= 16, "a lane for each part");
+                const int peer = lane % kLanes, other = peer < row_warps ? peer : 0;
                 const float4 v = PAIR ? *in_block(&part[other % warps], other / warps) : part[other];
-                const float count = lane < row_warps ? v.w : 0.0f;
+                const float count = peer < row_warps ? v.w : 0.0f;
                 at = __shfl_sync(kAllLanes, v.x, 0);
-                const float apart = v.x - at + v.y;
-                mean = warp_sum(count > 0.0f ? count * apart : 0.0f) * per_col;
-                const float off = apart - mean;
-                squares = warp_sum(count > 0.0f ? fmaf(count * off, off, v.z) : 0.0f);
+                mean = lanes_sum<kLanes>(count > 0.0f ? count * (v.x - at + v.y) : 0.0f) * per_col;
+                to_mean(at, mean, 2.0f);
+                const float off = v.x - at + v.y - mean;
+                // together: one after the other, 16384 shifted rows of 2001 binary32 take 58 us, not 52
+                const float2 sums = lanes_sum<kLanes>(count > 0.0f ? make_float2(count * off, fmaf(count * off, off, v.z)) : both(0.0f));
+                squares = sums.y;
+                finish_mean(mean, squares, sums.x, static_cast<float>(a.cols), per_col);
             }
             const float r = statistics(here, at, mean, squares);
 #pragma unroll
@@ -271,7 +318,8 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
         } while (kWalks && row < a.rows);
         if (PAIR) cluster_sync();  // the neighbour has read this block's parts
     } else {
-        __shared__ float sums[2][32];
+        __shared__ float part[32];
+        __shared__ float2 part2[32];
         const int tiles = (a.cols + past + kTileCols - 1) / kTileCols;
         const void *x = row_of<DT>(a.x, row, a.x_stride);
         const void *res = a.residual ? row_of<DT>(a.residual, row, a.residual_stride) : nullptr;
@@ -291,8 +339,8 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
             using T = typename ElemOf<DT>::type;
             return elem_to_f32<DT>(static_cast<const T *>(p)[min(lane, a.cols - 1)]);
         };
-        const float at = landmark(res ? element(x) + element(res) : element(x), lane < a.cols);
-        float2 s2 = both(0.0f), q2 = both(0.0f), f[4];
+        float at = landmark(res ? element(x) + element(res) : element(x), lane < a.cols);
+        float2 s2 = both(0.0f), e2 = both(0.0f), q2 = both(0.0f), f[4];
         for (int t = warp; t < tiles; t += warps) {
             sum_of(t, f);
 #pragma unroll
@@ -301,16 +349,22 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
 #pragma unroll
             for (int j = 0; j < 4; ++j) s2 = add2(s2, f[j]);
         }
-        const float mean = block_sum(s2.x + s2.y, warps, sums[0]) * per_col;
+        float mean = block_sum(s2.x + s2.y, warps, part) * per_col;
+        to_mean(at, mean, 2.0f);
         for (int t = warp; t < tiles; t += warps) {
             sum_of(t, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = add2(add2(f[j], both(-at)), both(-mean));
             clip_columns<ROWS != kApart>(t, past, a.cols, lane, f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q2 = fma2(f[j], f[j], q2);
+            for (int j = 0; j < 4; ++j) {
+                e2 = add2(e2, f[j]);
+                q2 = fma2(f[j], f[j], q2);
+            }
         }
-        const float r = statistics(row, at, mean, block_sum(q2.x + q2.y, warps, sums[1]));
+        float2 sums = block_sum2(make_float2(e2.x + e2.y, q2.x + q2.y), warps, part2);
+        finish_mean(mean, sums.y, sums.x, static_cast<float>(a.cols), per_col);
+        const float r = statistics(row, at, mean, sums.y);
         for (int t = warp; t < tiles; t += warps) {
             float2 w[4], b[4];
             sum_of(t, f);
@@ -332,18 +386,12 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
 constexpr int kNarrowWarps = 8;
 constexpr int kNarrowWalkers = 3;  // blocks to an SM
 template <int DT, int LANES, int TURNS>
-__global__ void __launch_bounds__(32 * kNarrowWarps) layernorm_narrow_kernel(const __grid_constant__ LayerNormArgs a) {
+__global__ void __launch_bounds__(32 * kNarrowWarps, 4) layernorm_narrow_kernel(const __grid_constant__ LayerNormArgs a) {
     enter_grid();
     constexpr int kRows = 32 / LANES;  // of a warp at a time
     const int lane = threadIdx.x & (LANES - 1), group = (threadIdx.x & 31) / LANES;
-    const unsigned peers = (kAllLanes >> (32 - LANES)) << (group * LANES);
     const int64_t warp = static_cast<int64_t>(blockIdx.x) * kNarrowWarps + (threadIdx.x >> 5);
     const int64_t first = warp * kRows * TURNS + group;
-    auto sum = [](float v) {
-#pragma unroll
-        for (int d = LANES / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kAllLanes, v, d);
-        return v;
-    };
     Raw8<DT> rx[TURNS], rr[TURNS];
 #pragma unroll
     for (int t = 0; t < TURNS; ++t) {
@@ -367,23 +415,30 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) layernorm_narrow_kernel(con
             for (int j = 0; j < 4; ++j) f[j] = add2(f[j], g[j]);
         }
         // lane 0 of a row has its first element
-        const unsigned held = __ballot_sync(kAllLanes, lane * 8 < a.cols) & peers;
-        const unsigned negative = __ballot_sync(kAllLanes, lane * 8 < a.cols && f[0].x < 0.0f) & peers;
-        const float one = __shfl_sync(kAllLanes, f[0].x, group * LANES);
-        const float at = negative == 0 || negative == held ? one : 0.0f;
+        float at = landmark<LANES>(f[0].x, lane * 8 < a.cols);
         float2 s2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = add2(f[j], both(-at));
         clip_columns<true>(0, 0, a.cols, lane, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
-        const float mean = sum(s2.x + s2.y) * a.per_col;
+        float mean = lanes_sum<LANES>(s2.x + s2.y) * a.per_col;
+        const bool moved = to_mean(at, mean, 1.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = d[j] = add2(add2(f[j], both(-at)), both(-mean));
         clip_columns<true>(0, 0, a.cols, lane, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
-        const float r = rsqrtf(fmaf(sum(q2.x + q2.y), a.per_col, a.eps));
+        float squares = lanes_sum<LANES>(q2.x + q2.y), off = 0.0f;  // off: what f has beyond the mean
+        if (__any_sync(kAllLanes, moved)) {
+            float2 e2 = both(0.0f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e2 = add2(e2, d[j]);
+            const float lacks = lanes_sum<LANES>(e2.x + e2.y);  // not of the rows beside: each has its own bits
+            finish_mean(off, squares, moved ? lacks : 0.0f, static_cast<float>(a.cols), a.per_col);
+            mean += off;
+        }
+        const float r = rsqrtf(fmaf(squares, a.per_col, a.eps));
         if (!given) continue;
         if (lane == 0) {
             if (a.mean) a.mean[row] = at + mean;
@@ -401,7 +456,7 @@ __global__ void __launch_bounds__(32 * kNarrowWarps) layernorm_narrow_kernel(con
             store_tile<DT, true>(row_of<DT>(a.h, row, a.h_stride), 0, a.cols, lane, pack8<DT>(h));
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(f[j], both(r)), w[j], b[j]);
+        for (int j = 0; j < 4; ++j) f[j] = fma2(fma2(f[j], both(r), both(-off * r)), w[j], b[j]);
         store_tile<DT, true>(row_of<DT>(a.y, row, a.y_stride), 0, a.cols, lane, pack8<DT>(f));
     }
 }
@@ -416,15 +471,9 @@ __global__ void __launch_bounds__(32 * kNarrowWarps, kNarrowWalkers) layernorm_n
     enter_grid();
     constexpr int kRows = 32 / LANES;  // of a warp at a time
     const int lane = threadIdx.x & (LANES - 1), group = (threadIdx.x & 31) / LANES;
-    const unsigned peers = (kAllLanes >> (32 - LANES)) << (group * LANES);
     const int64_t step = static_cast<int64_t>(gridDim.x) * kNarrowWarps * kRows;  // a multiple of 8
     int64_t base = (static_cast<int64_t>(blockIdx.x) * kNarrowWarps + (threadIdx.x >> 5)) * kRows;  // of the warp's rows the first
     const int past = past_of<DT>(row_of<DT>(a.x, base + group, a.x_stride));
-    auto sum = [](float v) {
-#pragma unroll
-        for (int d = LANES / 2; d > 0; d >>= 1) v += __shfl_xor_sync(kAllLanes, v, d);
-        return v;
-    };
     Raw8<DT> rx, rr;
     auto load = [&] {
         const int64_t row = base + group;
@@ -451,31 +500,37 @@ __global__ void __launch_bounds__(32 * kNarrowWarps, kNarrowWalkers) layernorm_n
         if (base < a.rows) load();
         if (a.h && row < a.rows) store_run<DT>(row_of<DT>(a.h, row, a.h_stride), 0, past, a.cols, lane, pack8<DT>(f));
         // element 7 of lane 0, element 0 of the others, where the row has it
-        const bool held = lane == 0 || lane * 8 - past < a.cols;
-        const float mine = lane == 0 ? f[3].y : f[0].x;
-        const unsigned all = __ballot_sync(kAllLanes, held) & peers, negative = __ballot_sync(kAllLanes, held && mine < 0.0f) & peers;
-        const float one = __shfl_sync(kAllLanes, mine, group * LANES);
-        const float at = negative == 0 || negative == all ? one : 0.0f;
+        float at = landmark<LANES>(lane == 0 ? f[3].y : f[0].x, lane == 0 || lane * 8 - past < a.cols);
         float2 s2 = both(0.0f), q2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[j] = add2(f[j], both(-at));
         clip_columns<true>(0, past, a.cols, lane, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) s2 = add2(s2, d[j]);
-        const float mean = sum(s2.x + s2.y) * a.per_col;
+        float mean = lanes_sum<LANES>(s2.x + s2.y) * a.per_col;
+        const bool moved = to_mean(at, mean, 1.0f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[j] = d[j] = add2(add2(f[j], both(-at)), both(-mean));
         clip_columns<true>(0, past, a.cols, lane, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) q2 = fma2(d[j], d[j], q2);
-        const float r = rsqrtf(fmaf(sum(q2.x + q2.y), a.per_col, a.eps));
+        float squares = lanes_sum<LANES>(q2.x + q2.y), off = 0.0f;  // off: what f has beyond the mean
+        if (__any_sync(kAllLanes, moved)) {
+            float2 e2 = both(0.0f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e2 = add2(e2, d[j]);
+            const float lacks = lanes_sum<LANES>(e2.x + e2.y);  // not of the rows beside: each has its own bits
+            finish_mean(off, squares, moved ? lacks : 0.0f, static_cast<float>(a.cols), a.per_col);
+            mean += off;
+        }
+        const float r = rsqrtf(fmaf(squares, a.per_col, a.eps));
         if (row >= a.rows) continue;
         if (lane == 0) {
             if (a.mean) a.mean[row] = at + mean;
             if (a.rstd) a.rstd[row] = r;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = fma2(mul2(f[j], both(r)), w[j], b[j]);
+        for (int j = 0; j < 4; ++j) f[j] = fma2(fma2(f[j], both(r), both(-off * r)), w[j], b[j]);
         store_run<DT>(row_of<DT>(a.y, row, a.y_stride), 0, past, a.cols, lane, pack8<DT>(f));
     }
 }
