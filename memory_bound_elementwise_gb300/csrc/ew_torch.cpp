@@ -435,7 +435,18 @@ struct Plan {
         slots = static_cast<const int32_t *>(vector(s, "slots", capacity, at::kInt, d));
     }
 };
+// A number for each slot: in the tokens' order, as tokens x k or flat.  Of as many
+// elements in other shapes, such as k x tokens, the order would be another.
+void check_slots(PyObject *o, const char *what, const Plan &plan) {
+    if (o == Py_None || plan.k == 1) return;
+    int64_t dims = 0, last = 1;  // of those above 1
+    for (int64_t size : tensor(o, what).sizes())
+        if (size != 1) ++dims, last = size;
+    if (dims > 1 && last != plan.k)
+        REFUSE(PyExc_ValueError, "%s: expected %lld x %lld", what, static_cast<long long>(plan.rows), static_cast<long long>(plan.k));
+}
 Weight weights_of(PyObject *o, const Plan &plan, ew_dtype code, at::ScalarType type, Device d) {
+    check_slots(o, "weights", plan);
     return weight_of(o, plan.rows * plan.k, code, type, d, "weights");
 }
 
@@ -490,6 +501,7 @@ PyObject *expert_combine_grad(PyObject *const *a) {  // dout, y, plan, weights, 
     const Matrix o = dy.matrix(a[4], "dy", {plan.capacity, m.cols}, plan.capacity, m.cols, type, d);
     float *dw;
     if (a[5] != Py_None) {
+        check_slots(a[5], "dweights", plan);
         dw = dweights.floats(a[5], "dweights", plan.rows * plan.k, d);
     } else {
         dw = static_cast<float *>(dweights.make({plan.rows, plan.k}, at::kFloat, d));

@@ -158,8 +158,8 @@ def ew_expert_dispatch(x, plan, out=None, stream=None):
 def ew_expert_combine(y, plan, weights=None, residual=None, out=None, stream=None):
     """out[t] = residual[t] + sum over j of weights[t, j] * y[plan.positions[t, j]]; returns out.
 
-    ``weights`` has y's dtype or float32 (None: ones).  Without a residual the sum begins at zero;
-    out may be residual."""
+    ``weights``, tokens x k, has y's dtype or float32 (None: ones).  Without a residual the sum
+    begins at zero; out may be residual."""
     if stream is not None:
         return _on(stream, ew_expert_combine, y, plan, weights, residual, out)
     return _C.expert_combine(y, plan, weights, residual, out)
