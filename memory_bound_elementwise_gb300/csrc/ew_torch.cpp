@@ -191,35 +191,6 @@ template <typename... O> PyObject *tuple_of(O &...outs) {
     return t;
 }
 
-// New outputs of 4-byte elements that belong together lie in one allocation, each from a
-// multiple of 256 bytes on: the allocator and the storage are half of the host time that
-// an output takes (a sort's four 5.7 us one by one, 4.3 together).
-struct Together {
-    c10::Storage storage;
-    int64_t next = 0;
-    Device d;
-    static int64_t room(int64_t n) { return (4 * n + 255) / 256 * 256; }
-    template <size_t N> Together(const int64_t (&numbers)[N], Device d_) : d(d_) {
-        int64_t bytes = 0;
-        for (int64_t n : numbers) bytes += room(n);
-        const Tensor all = d.empty({bytes}, at::kByte);
-        storage = all.storage();
-    }
-    void *make(Output &out, at::IntArrayRef sizes, at::ScalarType type) {
-        Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
-                                                            c10::scalarTypeToTypeMeta(type));
-        c10::SmallVector<int64_t, 2> strides(sizes.size(), 1);
-        int64_t n = 1;
-        for (size_t i = sizes.size(); i-- > 0; n *= sizes[i]) strides[i] = n;
-        t.unsafeGetTensorImpl()->set_sizes_and_strides(sizes, strides, next / 4);
-        next += room(n);
-        void *p = t.data_ptr();
-        out.o = THPVariable_Wrap(std::move(t));
-        if (out.o == nullptr) throw Raised{};
-        return p;
-    }
-};
-
 // A workspace: lives to the end of the call, on the call's stream.
 struct Workspace {
     Tensor t;
@@ -409,9 +380,7 @@ PyObject *expert_sort(PyObject *const *a) {  // experts, n_experts, align
     if (capacity < 0 || need < 0) check_status(EW_ERR_INVALID_VALUE, "ew_expert_sort");
     const Workspace work(need, "ew_expert_sort", d);
     Output positions, offsets, counts, slots;
-    const int64_t numbers[] = {m.rows * m.cols, n_experts + 1, n_experts, capacity};
-    Together all(numbers, d);
-    auto make = [&](Output &o, at::IntArrayRef sizes) { return static_cast<int32_t *>(all.make(o, sizes, at::kInt)); };
+    auto make = [&](Output &o, at::IntArrayRef sizes) { return static_cast<int32_t *>(o.make(sizes, at::kInt, d)); };
     int32_t *p = make(positions, {m.rows, m.cols}), *o = make(offsets, {n_experts + 1}), *c = make(counts, {n_experts});
     int32_t *s = make(slots, {capacity});
     check_status(ew_expert_sort(type, m.p, m.stride, n_experts, align, p, o, c, s, capacity, m.rows, m.cols, work.p(),
@@ -647,11 +616,9 @@ struct PolicyCall {
 
 // loss, logp and lse, new ones
 std::array<float *, 3> policy_rows(Output &loss, Output &logp, Output &lse, const PolicyCall &c) {
-    const int64_t n = c.m.rows, numbers[] = {n, n, n};
-    Together all(numbers, c.d);
-    auto make = [&](Output &o) { return static_cast<float *>(all.make(o, {n}, at::kFloat)); };
-    float *loss_p = make(loss), *logp_p = make(logp);
-    return {loss_p, logp_p, make(lse)};
+    auto make = [&](Output &o, const char *what) { return o.floats(Py_None, what, c.m.rows, c.d); };
+    float *loss_p = make(loss, "loss"), *logp_p = make(logp, "logp");
+    return {loss_p, logp_p, make(lse, "lse")};
 }
 
 PyObject *policy(PyObject *const *a) {  // what PolicyCall takes

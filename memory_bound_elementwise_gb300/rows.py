@@ -4,9 +4,9 @@ Matrices are CUDA tensors whose last dimension is contiguous.  Two-dimensional
 ones may have any row stride; others are contiguous and count as rows of their
 last dimension.  Outputs that are not given are allocated; calls are enqueued
 on ``stream`` (default: torch's current stream) and do not synchronise.  What is
-allocated belongs to that stream, and the small outputs of a call may share an
-allocation.  Arguments that do not fit raise ``ValueError``
-or ``TypeError``, and ``EwError`` carries the library's status.
+allocated belongs to that stream; it comes straight from torch's caching allocator,
+where dispatch modes do not see it.  Arguments that do not fit raise ``ValueError`` or
+``TypeError``, and ``EwError`` carries the library's status.
 
 Gradients are calls of their own (``ew_*_grad``, ``ew_distill_step``): autograd does
 not see these functions.  Results require no gradient whatever the inputs do, and
