@@ -518,12 +518,16 @@ cudaError_t policy_twice(const PolicyArgs &a, bool sums, bool grad, int shift, c
 
 // Rows that are worked on at once: an SM's blocks, or as many clusters of a row's
 // blocks as fit the device (a cluster lies within one of its partitions); asked
-// once for each size of block and of cluster, on the first device that calls.
+// once for each size of block and of cluster on a device (past 15, every time).
 template <int THREADS, typename Kernel> cudaError_t rows_at_once(Kernel kernel, int shift, int sms, int *rows) {
     *rows = sms * Stream<THREADS>::kBlocks;
     if (shift == 0) return cudaSuccess;
-    static std::atomic<int> known[4];  // the loss, and the loss with its gradient, have the same block and memory
-    if ((*rows = known[shift].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    constexpr int kKnown = 16;
+    static std::atomic<int> known[kKnown][4];  // the loss, and the loss with its gradient, have the same block and memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kKnown && (*rows = known[dev][shift].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sms >> shift << shift);
     cfg.blockDim = dim3(THREADS);
@@ -534,8 +538,9 @@ template <int THREADS, typename Kernel> cudaError_t rows_at_once(Kernel kernel, 
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(rows, kernel, &cfg);
-    if (e == cudaSuccess) known[shift].store(*rows = std::max(1, *rows), std::memory_order_relaxed);
+    e = cudaOccupancyMaxActiveClusters(rows, kernel, &cfg);
+    *rows = std::max(1, *rows);
+    if (e == cudaSuccess && dev < kKnown) known[dev][shift].store(*rows, std::memory_order_relaxed);
     return e;
 }
 // Groups that a row's share takes when 2^shift blocks of THREADS split it, up to 7
