@@ -281,8 +281,9 @@ ew_status expert_rows_call(int what, ew_dtype dt, const Operand &by_token, const
     return EW_OK;
 }
 
-// Rows of partial sums that the norm's backward may use: one for each row up to
-// 1280, which is more than its blocks.
+// Rows of partial sums that the norms' backward calls may use: one for each row up to
+// 1280.  That is more than their blocks, but for layer norm's of matrices whose rows lie
+// apart and take a warp each: without it those would be 16 an SM.
 constexpr int64_t kNormPartials = 1280;
 
 }  // namespace
