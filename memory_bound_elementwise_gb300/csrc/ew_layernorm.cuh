@@ -164,7 +164,7 @@ __device__ __forceinline__ void finish_mean(float &beyond, float &squares, float
 // so that both statistics cost one barrier and no cancellation.  Otherwise the
 // passes read the row again.  Bounded by memory: 16384 rows of 8192 bf16 with a residual
 // 171 us at a floor of 161; by latency where there are few rows (9 of 5120 3.0 us) and
-// by the issue rate where rows are narrow (65536 of 201 bf16 36 us at 16).
+// by the issue rate where rows are narrow (65536 of 201 bf16 35 us at 16).
 //
 // Weights beside shifted rows have to be cut to their phase, which takes as long
 // as all else, and those of rows of more than 32 tiles of 16 bits are read from the
@@ -398,11 +398,11 @@ __global__ void __launch_bounds__(WARPS * 32, layernorm_resident(DT, ROWS, KT, H
 // Aligned rows of up to 128 columns, such as the heads of a query: LANES lanes (8 or
 // 16) to a row, 8 elements each, so that the steps of the reductions are shared by 4 or
 // 2 rows of a warp.  131072 rows of 64 bf16 take 12 us (floor 10; a warp a row 60),
-// 65536 of 128 12 us (10; 31), of 128 binary32 22 us (20; 33).  TURNS rows of a lane
+// 65536 of 128 12 us (10; 31), of 128 binary32 21 us (20; 33).  TURNS rows of a lane
 // are under way together: two where there are many rows of 16 bits (262144 of 128 bf16
-// 46 us, 52 with one), one otherwise (2464 of 64 1.7 us, 2.2 with two; 65536 of 128
+// 47 us, 52 with one), one otherwise (2464 of 64 1.7 us, 2.2 with two; 65536 of 128
 // binary32 22 and 24).  Many 16-bit rows of up to 256 columns go this way, too, a
-// warp to two rows: 65536 of 192 23 us (33), of 256 24 us (26).
+// warp to two rows: 65536 of 192 24 us (33), of 256 23 us (26).
 constexpr int kNarrowWarps = 8;
 constexpr int kNarrowWalkers = 3;  // blocks to an SM
 template <int DT, int LANES, int TURNS>
@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(32 * kNarrowWarps, 4) layernorm_narrow_kernel(
 
 // Shifted narrow rows, which share a warp in the same way.  A lane's rows are a multiple of
 // 8 apart, so that its weights, cut once, stay in registers; the next row is on its way
-// while one is worked on.  65536 rows of 101 bf16 take 21 us (floor 8; a warp a row 37),
-// 131072 of 51 21 us (8; 70), 65536 of 201, a warp each, 35 us (16; 37), of 51 binary32
+// while one is worked on.  65536 rows of 101 bf16 take 22 us (floor 8; a warp a row 37),
+// 131072 of 51 22 us (8; 70), 65536 of 201, a warp each, 35 us (16; 37), of 51 binary32
 // 14 us (8; 36).  Four blocks an SM have to spill: 22 us for 101 bf16.
 template <int DT, int LANES>
 __global__ void __launch_bounds__(32 * kNarrowWarps, kNarrowWalkers) layernorm_narrow_walk_kernel(const __grid_constant__ LayerNormArgs a) {
@@ -1148,19 +1148,19 @@ template <int DT> bool same_runs(const void *p, int64_t stride, const void *q, i
 
 // Tiles a thread: as few as hold the row in 16 warps, which is the shortest way for
 // few rows.  Where there are many, two keep more loads on their way, and four pay for
-// the statistics of wide 16-bit rows: 16384 rows of 4096 bf16 take 81 us with four,
-// 16384 of 4001 96 us with four and 115 with one; of 2001 binary32 93 us with one,
-// 89 with two.  But walkers hold weights as well, fewer of them fit, and what matters is
-// how many columns an SM works on: 6392 rows of 2135 bf16 take 34 us with four (45 of
-// 64 tiles), 29 with one (27 of 32); of less than 8 tiles the barrier is short and one
-// is as good or better (7897 x 777 f16 17.0 us, 18.0 with four).
+// the statistics of wide 16-bit rows: 16384 rows of 4096 bf16 take 83 us with four, 94 with
+// two, 16384 of 4001 94 us with four and 119 with one; of 2001 binary32 93 us with one,
+// 90 with two.  But walkers hold weights as well, fewer of them fit, and what matters is
+// how many columns an SM works on: 6392 rows of 2135 bf16 take 35 us with four (45 of
+// 64 tiles), 30 with one (27 of 32); of less than 8 tiles the barrier is short and one
+// is as good or better (7897 x 777 f16 17.5 us, 18.7 with four).
 //
 // Rows of more than 32 tiles: up to a row an SM go to clusters of two blocks (30 of 12480
-// bf16 4.3 us, by one block of four tiles a thread 5.9; 600 of 16384 22.5 and 16.0 us),
-// of shifted rows half as many.  More go to one block each: 8192 of 16384 bf16 166 us by
-// walkers, 224 by a block a row, 303 by clusters; 4096 of 16384 binary32 167 us by a
-// block a row, 218 by walkers, 188 by clusters; but shifted rows of binary32, for which
-// the registers do not suffice, to clusters, 230 and 256 us.
+// bf16 4.4 us, by one block of four tiles a thread 5.3; 600 of 16384 22.8 and 14.7 us),
+// of shifted rows half as many.  More go to one block each: 8192 of 16384 bf16 163 us by
+// walkers, 224 by a block a row, 288 by clusters; 4096 of 16384 binary32 169 us by a
+// block a row, 218 by walkers, 190 by clusters; but shifted rows of binary32, for which
+// the registers do not suffice, to clusters, 231 and 256 us.
 template <int DT, int ROWS> cudaError_t layernorm_launch(const LayerNormArgs &a, int sms, cudaStream_t s, LaunchInfo *info) {
     constexpr bool kNarrow = DT != DT_F32;
     const int tiles = static_cast<int>((static_cast<int64_t>(a.cols) + (ROWS == kShifted ? 7 : 0) + kTileCols - 1) / kTileCols);
